@@ -10,6 +10,8 @@ raises if the compiled library is missing.
 from .binding import (  # noqa: F401
     TG_EPILOGUE_NONE,
     TG_EPILOGUE_RELU,
+    TG_HEAD_VOCAB_MAJOR,
+    TG_HEAD_WIDTH_MAJOR,
     TgError,
     gemm_relu,
     gemm_relu_host,
@@ -23,3 +25,10 @@ from .binding import (  # noqa: F401
     tg_release_workspace,
     tg_status_string,
 )
+from .head import (  # noqa: F401
+    linear_cross_entropy,
+    linear_cross_entropy_step,
+    linear_distillation,
+    linear_distillation_step,
+)
+from .norm import layer_norm, layer_norm_backward  # noqa: F401

@@ -41,6 +41,17 @@ class tg_epilogue(ctypes.Structure):
 
 TG_ACT_NONE, TG_ACT_RELU, TG_ACT_GELU, TG_ACT_GELU_TANH = 0, 1, 2, 3
 
+TG_TYPE_F16, TG_TYPE_F32 = 0, 1
+TG_NORM_MAX_WIDTH = 32768
+TG_HEAD_VOCAB_MAJOR, TG_HEAD_WIDTH_MAJOR = 0, 1
+TG_HEAD_MAX_TOP = 1024
+
+
+class tg_head_options(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("debug_flags", ctypes.c_int),
+                ("timeout_ms", ctypes.c_int), ("reserved", ctypes.c_int),
+                ("piece_rows", ctypes.c_int64)]
+
 
 class tg_plan(ctypes.Structure):
     _fields_ = [
@@ -102,6 +113,13 @@ def load_library() -> ctypes.CDLL:
         L.tg_gemm_w4a16_f16.argtypes = [vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, ci,
                                         ctypes.POINTER(tg_epilogue), ctypes.POINTER(tg_options), vp]
         L.tg_gemm_nf4a16_f16.argtypes = L.tg_gemm_w4a16_f16.argtypes
+        cf, hp = ctypes.c_float, ctypes.POINTER(tg_head_options)
+        L.tg_layernorm_f16.argtypes = [vp] * 6 + [i64] * 4 + [cf, ci, vp]
+        L.tg_layernorm_backward_f16.argtypes = [vp] * 8 + [i64] * 5 + [ci, vp]
+        L.tg_linear_cross_entropy_f16.argtypes = ([vp, vp, vp, i64, cf] + [vp] * 5 + [i64] * 7 +
+                                                  [hp, vp])
+        L.tg_linear_distill_f16.argtypes = ([vp] * 4 + [ci, ci, i64, cf] + [vp] * 5 + [i64] * 7 +
+                                            [hp, vp])
         L.tg_plan_query.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64, ci,
                                     ctypes.POINTER(tg_options), ctypes.POINTER(tg_plan)]
         L.tg_device_error_check.argtypes = [ctypes.POINTER(ctypes.c_uint), ci]
@@ -113,7 +131,8 @@ def load_library() -> ctypes.CDLL:
         for name in ("tg_gemm_relu_f16", "tg_gemm_relu_f16_ex", "tg_gemm_relu_f16_host",
                      "tg_gemm_relu_f16_splitk_noalloc", "tg_gemm_f16_epilogue",
                      "tg_gemm_f16_t", "tg_relu_backward_f16", "tg_gemm_w4a16_f16",
-                     "tg_gemm_nf4a16_f16",
+                     "tg_gemm_nf4a16_f16", "tg_layernorm_f16", "tg_layernorm_backward_f16",
+                     "tg_linear_cross_entropy_f16", "tg_linear_distill_f16",
                      "tg_plan_query", "tg_device_error_check", "tg_last_cuda_error",
                      "tg_release_workspace", "tg_version"):
             getattr(L, name).restype = ci
@@ -191,6 +210,55 @@ def tg_gemm_nf4a16_f16(A: int, Wq: int, scales: int, C: int, M: int, N: int, K: 
 def tg_relu_backward_f16(dC: int, C: int, dZ: int, M: int, N: int, lddc: int, ldc: int,
                          lddz: int, stream: int = 0) -> int:
     return load_library().tg_relu_backward_f16(dC, C, dZ, M, N, lddc, ldc, lddz, stream or None)
+
+
+def tg_layernorm_f16(X: int, gamma: int, beta: int, Y: int, mean: int, rstd: int, M: int, N: int,
+                     ldx: int, ldy: int, eps: float, param_type: int = TG_TYPE_F16,
+                     stream: int = 0) -> int:
+    return load_library().tg_layernorm_f16(X, gamma or None, beta or None, Y, mean or None,
+                                           rstd or None, M, N, ldx, ldy, eps, param_type,
+                                           stream or None)
+
+
+def tg_layernorm_backward_f16(dY: int, X: int, gamma: int, mean: int, rstd: int, dX: int,
+                              dgamma: int, dbeta: int, M: int, N: int, lddy: int, ldx: int,
+                              lddx: int, param_type: int = TG_TYPE_F16, stream: int = 0) -> int:
+    return load_library().tg_layernorm_backward_f16(dY, X, gamma or None, mean, rstd, dX or None,
+                                                    dgamma or None, dbeta or None, M, N, lddy,
+                                                    ldx, lddx, param_type, stream or None)
+
+
+def _head_opts(options) -> ctypes.POINTER(tg_head_options) | None:
+    if options is None:
+        return None
+    if isinstance(options, tg_head_options):
+        return ctypes.pointer(options)
+    o = tg_head_options()
+    for k, v in dict(options).items():
+        if not hasattr(o, k):
+            raise KeyError(f"unknown option {k!r}")
+        setattr(o, k, int(v))
+    return ctypes.pointer(o)
+
+
+def tg_linear_cross_entropy_f16(X: int, W: int, target: int, ignore_index: int,
+                                logit_scale: float, dloss: int, loss: int, lse: int, dX: int,
+                                dW: int, T: int, V: int, D: int, ldx: int, ldw: int, lddx: int = 0,
+                                lddw: int = 0, options=None, stream: int = 0) -> int:
+    return load_library().tg_linear_cross_entropy_f16(
+        X, W, target, ignore_index, logit_scale, dloss or None, loss or None, lse or None,
+        dX or None, dW or None, T, V, D, ldx, ldw, lddx, lddw, _head_opts(options), stream or None)
+
+
+def tg_linear_distill_f16(X: int, W: int, teacher_index: int, teacher_logits: int,
+                          teacher_type: int, top: int, ldt: int, temperature: float, dloss: int,
+                          loss: int, lse: int, dX: int, dW: int, T: int, V: int, D: int, ldx: int,
+                          ldw: int, lddx: int = 0, lddw: int = 0, options=None,
+                          stream: int = 0) -> int:
+    return load_library().tg_linear_distill_f16(
+        X, W, teacher_index, teacher_logits, teacher_type, top, ldt, temperature, dloss or None,
+        loss or None, lse or None, dX or None, dW or None, T, V, D, ldx, ldw, lddx, lddw,
+        _head_opts(options), stream or None)
 
 
 def tg_gemm_relu_f16_host(hA: int, hB: int, hC: int, M: int, N: int, K: int, lda: int,

@@ -777,7 +777,13 @@ tg_status validate_epilogue(const tg_epilogue& e, const void* C, int64_t N, int6
 
 tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
                    int64_t lda, int64_t ldb, int64_t ldc, const tg_epilogue& epi,
-                   const tg_options* opt, cudaStream_t stream, int ta = 0, int tb = 0) {
+                   const tg_options* opt, cudaStream_t stream, int ta = 0, int tb = 0,
+                   const tg::GemmExtra* extra = nullptr) {
+  float* const out32 = extra ? extra->out32 : nullptr;
+  if (out32) {  // validated and planned like a C that goes through the float32 workspace
+    C = out32;
+    ldc = N;
+  }
   tg_status st = validate(A, B, C, M, N, K, lda, ldb, ldc, TG_EPILOGUE_NONE, ta, tb);
   if (st != TG_OK) return st;
   if ((st = validate_epilogue(epi, C, N, ldc)) != TG_OK) return st;
@@ -804,11 +810,25 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     e = cudaGetLastError();
     return e == cudaSuccess ? TG_OK : cuda_fail(e);
   }
+  tg_options out32_opt;
+  if (out32) {
+    std::memset(&out32_opt, 0, sizeof(out32_opt));
+    if (opt) out32_opt = *opt;
+    out32_opt.split_k = 1;
+    out32_opt.force_workspace = 1;
+    if (extra->add) out32_opt.pair = 1;
+    opt = &out32_opt;
+  }
   Plan pl;
   st = make_plan(reinterpret_cast<uintptr_t>(A), reinterpret_cast<uintptr_t>(B),
                  reinterpret_cast<uintptr_t>(C), M, N, K, lda, ldb, ldc, ds->sm_count,
                  ds->pair_clusters, opt, &pl, ta, tb);
   if (st != TG_OK) return st;
+  if (out32) {  // the workspace is the caller's
+    pl.ldw = extra->ld32;
+    pl.pub.workspace_bytes = pl.off_w;
+    if (extra->block_n) *extra->block_n = pl.pub.block_n;
+  }
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   if ((st = encode_fn(&enc)) != TG_OK) return st;
   const tg_plan& P = pl.pub;
@@ -920,7 +940,9 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
                         uint64_t(ldb_e) * 2, tg::kBK, P.cta_pair ? 128u : uint32_t(P.block_n))
             : encode_2d(enc, &L.b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Be, uint64_t(N), uint64_t(K),
                         uint64_t(ldb_e) * 2, 64, mn_box_k);
-  float* ws = P.workspace_epilogue ? reinterpret_cast<float*>(scratch + pl.off_w) : nullptr;
+  float* ws = out32                  ? out32
+              : P.workspace_epilogue ? reinterpret_cast<float*>(scratch + pl.off_w)
+                                     : nullptr;
   if (cr == CUDA_SUCCESS) {
     if (ws)
       cr = encode_ws_3d(enc, &L.out, ws, uint64_t(N), uint64_t(ws_rows), uint64_t(P.split_k),
@@ -947,6 +969,11 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   gp.bias = static_cast<const __half*>(epi.bias);
   gp.residual = static_cast<const __half*>(epi.residual);
   gp.ldr = epi.residual ? epi.ldr : 0;
+  if (extra) {
+    gp.alpha = extra->alpha;
+    gp.stats = extra->stats;
+    gp.stat_c = extra->stat_c;
+  }
   gp.a_mn = ta;
   gp.b_k = tb;
   if (P.tail_tiles) {
@@ -975,6 +1002,9 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   L.grid = P.grid;
   L.stream = stream;
   auto launch = [&](const tg::GemmLaunch& l) -> cudaError_t {
+    if (out32)
+      return extra->add ? tg::launch_head_add(l)
+                        : tg::launch_head_logits(l, P.cta_pair ? 0 : P.block_n);
     if (P.a_row_classes) return tg::launch_gemm_pair_cls(cls, l);
     if (P.cta_pair) return tg::launch_gemm_pair(l, ws != nullptr);
     switch (P.block_n) {
@@ -1027,7 +1057,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     if (ce != cudaSuccess) return fail(cuda_fail(ce));
   }
 
-  if (ws) {
+  if (ws && !out32) {
     tg_splitk_reduce_kernel<<<reduce_grid(M, N), kReduceThreads, 0, stream>>>(
         ws, pl.ldw, ws_rows * pl.ldw, P.split_k, static_cast<__half*>(C), ldc, reduce_params,
         P.a_row_classes ? pl.cls_rows : 0);
@@ -1125,6 +1155,20 @@ tg_status scratch_alloc(size_t bytes, cudaStream_t stream, void** out) {
 
 cudaError_t error_word_address(unsigned int** out) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_tg_error_word);
+}
+
+tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
+                     int64_t K, int64_t lda, int64_t ldb, int64_t ldc, const GemmExtra& x,
+                     const tg_options* opt, cudaStream_t stream) {
+  return run_gemm(A, B, C, M, N, K, lda, ldb, ldc, epilogue_from_flag(TG_EPILOGUE_NONE), opt,
+                  stream, ta, tb, &x);
+}
+
+cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst,
+                             int64_t rows, int64_t cols, int num_sms, cudaStream_t stream) {
+  launch_pack(static_cast<const uint16_t*>(src), ld_src, static_cast<uint16_t*>(dst), ld_dst, rows,
+              cols, num_sms, 8, true, stream);
+  return cudaGetLastError();
 }
 
 bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) { return encode_fn(fn) == TG_OK; }

@@ -82,6 +82,12 @@ struct GemmParams {
   const __half* bias;
   const __half* residual;
   long long ldr;
+  // fp16 output only: device float32 that the sum is multiplied by before the bias (nullptr: 1)
+  const float* alpha;
+  // kModeLogits: [tiles_n][M] softmax statistics of each row of an output tile (row_stats_chunk),
+  // of the sums times stat_c
+  float2* stats;
+  float stat_c;
   // A read by row classes (CTA-pair kernel, float32 output; see AClassMaps): M tile m holds
   // rows 16 j + r of class r = m / cls_tiles, j from (m % cls_tiles) * 256; class r's rows
   // start cls_shift[r] elements past a 32-byte boundary, so its K windows (and the matching B
@@ -89,6 +95,11 @@ struct GemmParams {
   int cls_tiles;
   unsigned char cls_shift[kARowClasses];
 };
+
+// What the epilogue of a float32 output does with a tile, beside storing it (kModePlain):
+// kModeLogits adds the rows' softmax statistics; kModeAdd adds the tile to the output instead of
+// overwriting it (each element is added to once a launch, so the result does not depend on order).
+enum : int { kModePlain = 0, kModeLogits = 1, kModeAdd = 2 };
 
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3 };
 
@@ -108,8 +119,9 @@ __device__ __forceinline__ float activation(float x, int act) {
   }
 }
 
-// Full epilogue of one float32 sum at (row, col): (sum + bias) -> activation -> + residual.
+// Full epilogue of one float32 sum at (row, col): (alpha sum + bias) -> activation -> + residual.
 __device__ __forceinline__ float epilogue_value(float x, int row, int col, const GemmParams& p) {
+  if (p.alpha) x *= __ldg(p.alpha);
   if (p.bias) x += __half2float(p.bias[col]);
   x = activation(x, p.act);
   if (p.residual) x += __half2float(p.residual[static_cast<long long>(row) * p.ldr + col]);
@@ -199,6 +211,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
                                              int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(m)),
+      "r"(src), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int c0, int c1,
+                                           int c2) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
           reinterpret_cast<uint64_t>(m)),
       "r"(src), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
@@ -557,13 +578,18 @@ __device__ __forceinline__ void load_half32(const __half* src, int col, int n, f
   }
 }
 
-// General fused epilogue of 32 consecutive columns of one row: x = acc + bias, activation,
+// General fused epilogue of 32 consecutive columns of one row: x = alpha acc + bias, activation,
 // + residual, then fp16 pairs into pk[0..15].
 __device__ __forceinline__ void epilogue_general_32(const uint32_t (&acc)[32], int row, int col,
                                                     const GemmParams& p, uint32_t* pk) {
   float x[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(acc[i]);
+  if (p.alpha) {
+    const float a = __ldg(p.alpha);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] *= a;
+  }
   if (p.bias) {
     float b[32];
     load_half32(p.bias, col, p.N, b);  // the same 64 bytes for every lane: broadcast
@@ -607,7 +633,7 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
                                                 const uint32_t (&r1)[32], int row0, int col0,
                                                 uint8_t* stg, int& sb, int lane) {
   uint32_t pk[32];
-  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu) {
+  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu && p.alpha == nullptr) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       pk[i] = relu_pack_h2(r0[2 * i], r0[2 * i + 1], p.act);
@@ -669,7 +695,35 @@ __device__ __forceinline__ void unperm8(uint32_t (&r)[32]) {
   }
 }
 
-template <int BN, bool OUT_F32, bool PERM8 = false>
+// Softmax statistics of one row, 32 columns at a time (r: float32 bits of the sums; cnt: how many
+// are columns of the matrix): m = the largest of the scaled sums so far, s = the sum of
+// 2^(scaled sum - m), with log2(e) in the scale c.  A row's statistics over several tiles combine
+// as 2^(m - M) s.  An infinite m (every sum -inf, or none) adds nothing but a NaN among the sums.
+__device__ __forceinline__ void row_stats_chunk(const uint32_t (&r)[32], int cnt, float c, float& m,
+                                                float& s) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < cnt) top = fmaxf(top, __uint_as_float(r[i]));
+  const float m1 = fmaxf(m, top * c);
+  float add = 0.0f;
+  if (m1 == -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float x = __uint_as_float(r[i]);
+      if (i < cnt && x != x) add = x;
+    }
+    s += add;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < cnt) add += exp2f(fmaf(__uint_as_float(r[i]), c, -m1));
+  s = s * exp2f(m - m1) + add;
+  m = m1;
+}
+
+template <int BN, bool OUT_F32, bool PERM8 = false, int MODE = kModePlain>
 __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const GemmParams& p,
                                               uint32_t tl, int row0, int col_base, int split,
                                               uint8_t* stg, int& sb, uint32_t release_bar,
@@ -688,6 +742,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
     release();
     return;
   }
+  static_assert(OUT_F32 || MODE == kModePlain, "modes are of the float32 output");
   if constexpr (!OUT_F32) {
 #pragma unroll 1
     for (int c = 0; c < BN / 64; ++c) {
@@ -704,12 +759,14 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
       store_chunk_f16(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
     }
   } else {
+    float m = -INFINITY, s = 0.0f;  // kModeLogits
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
       uint32_t r[32];
       tmem_ld_x32(tl + c * 32, r);
       tmem_wait_ld(r);
       if (c == BN / 32 - 1) release();
+      if constexpr (MODE == kModeLogits) row_stats_chunk(r, p.N - col_base - c * 32, p.stat_c, m, s);
       uint8_t* st = stg + sb * kStagingBuf;
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
@@ -721,10 +778,17 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        tma_store_3d(tmOut, smem_u32(st), col_base + c * 32, row0, split);
+        if constexpr (MODE == kModeAdd)
+          tma_add_3d(tmOut, smem_u32(st), col_base + c * 32, row0, split);
+        else
+          tma_store_3d(tmOut, smem_u32(st), col_base + c * 32, row0, split);
         bulk_commit();
       }
       sb ^= 1;
+    }
+    if constexpr (MODE == kModeLogits) {
+      if (row0 + lane < p.M)
+        p.stats[static_cast<long long>(col_base / BN) * p.M + row0 + lane] = make_float2(m, s);
     }
   }
 }
@@ -741,7 +805,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
 // 0); the single producer and MMA threads then build descriptors and TMA boxes from constants,
 // which keeps their per-k-block instruction count inside the MMA time.  GENERAL == true reads
 // the layouts from p.a_mn and p.b_k (the transposed-operand GEMMs of the backward pass).
-template <int BN, bool OUT_F32, bool GENERAL>
+template <int BN, bool OUT_F32, bool GENERAL, int MODE = kModePlain>
 __global__ void __launch_bounds__(kThreads, 1)
     tg_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -902,8 +966,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
-      epilogue_tile<BN, OUT_F32>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN, w.split,
-                                 stg, sb, smem_u32(&tempty[buf]), false, lane);
+      epilogue_tile<BN, OUT_F32, false, MODE>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN, w.split,
+                                              stg, sb, smem_u32(&tempty[buf]), false, lane);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
@@ -1032,7 +1096,7 @@ struct AClassMaps {
 // K-major ones as one {64 K, 128} box per 64-k block.  tiles_m/tiles_n in p count 256 x 256
 // pair tiles.  With A_CLS (float32 output, forward layout) A comes through `cls` (tmA unused)
 // and M tiles index class-major rows.
-template <bool OUT_F32, bool A_MN, bool B_K, bool A_CLS>
+template <bool OUT_F32, bool A_MN, bool B_K, bool A_CLS, int MODE = kModePlain>
 __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                const CUtensorMap& tmOut, const GemmParams& p,
                                                const AClassMaps* cls) {
@@ -1241,8 +1305,8 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
         epilogue_tail<Cfg::kBN>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot, w.split,
                                 static_cast<int>(rank) * 4 + q, stg, sb, release_bar, lane);
       else
-        epilogue_tile<Cfg::kBN, OUT_F32>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.split, stg,
-                                         sb, release_bar, true, lane);
+        epilogue_tile<Cfg::kBN, OUT_F32, false, MODE>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN,
+                                                      w.split, stg, sb, release_bar, true, lane);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
@@ -1261,13 +1325,13 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
   }
 }
 
-template <bool OUT_F32, bool A_MN, bool B_K>
+template <bool OUT_F32, bool A_MN, bool B_K, int MODE = kModePlain>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tg_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmOut,
                         const __grid_constant__ GemmParams p) {
-  pair_gemm_body<OUT_F32, A_MN, B_K, false>(tmA, tmB, tmOut, p, nullptr);
+  pair_gemm_body<OUT_F32, A_MN, B_K, false, MODE>(tmA, tmB, tmOut, p, nullptr);
 }
 
 // The CTA-pair kernel with A read through row classes (float32 partials, forward layout).

@@ -32,6 +32,10 @@ cudaError_t launch_gemm_pair(const GemmLaunch& l, bool out_f32);
 // The CTA-pair kernel with A read in place through row classes (float32 output only; l.a is
 // unused, l.p.cls_* describe the classes).
 cudaError_t launch_gemm_pair_cls(const AClassMaps& cls, const GemmLaunch& l);
+// Float32 logits of a head (kModeLogits; block_n 0: CTA pairs), A row-major, B in either layout.
+cudaError_t launch_head_logits(const GemmLaunch& l, int block_n);
+// The CTA-pair kernel that adds A^T B to its float32 output (kModeAdd; A stored K x M).
+cudaError_t launch_head_add(const GemmLaunch& l);
 // Clusters of two that can be resident at once on the current device.
 cudaError_t gemm_pair_max_clusters(int* out);
 
@@ -55,6 +59,25 @@ tg_status scratch_alloc(size_t bytes, cudaStream_t stream, void** out);
 
 // cuTensorMapEncodeTiled from the driver (false if the driver does not provide it).
 bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
+
+// The GEMM behind every entry point, with what the head's passes need beside the public ones.
+// With out32 (no K splits, no fp16 output) C is not used.
+struct GemmExtra {
+  const float* alpha;  // device factor of an fp16 output (nullptr: 1)
+  float* out32;        // float32 output, M rows of ld32 (a multiple of 32) floats
+  int64_t ld32;
+  bool add;            // add to out32 (A stored K x M, B stored K x N) instead of writing logits
+  float2* stats;       // logits: [ceil(N / *block_n)][M] row statistics of stat_c times the logits
+  float stat_c;
+  int* block_n;        // out: the width of the tiles that stats are of (128, 192 or 256)
+};
+tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
+                     int64_t K, int64_t lda, int64_t ldb, int64_t ldc, const GemmExtra& x,
+                     const tg_options* opt, cudaStream_t stream);
+
+// dst (rows x ld_dst, 16-byte aligned rows, columns up to a multiple of 8 written as zero) <- src.
+cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst,
+                             int64_t rows, int64_t cols, int num_sms, cudaStream_t stream);
 
 // Deterministic split-K reduction: C = fp16(epi(sum_s W[s])) (see tg_splitk_reduce_kernel).
 // p supplies the epilogue (act, bias, residual, ldr) and the shape (M, N).

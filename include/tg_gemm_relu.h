@@ -319,6 +319,103 @@ tg_status tg_gemm_relu_f16_splitk_noalloc(const void* A, const void* B, void* C,
                                           int64_t ldc, int epilogue_flag, int split_k,
                                           tg_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * The end of a language model: layer normalisation, and losses of a linear head.
+ *
+ * Conventions as above (leading dimensions in elements, errors found on the host before anything
+ * is launched, asynchronous on `stream`, scratch from the library's pool, capturable), and:
+ *  - Activations, head weights and their gradients are fp16 with any 2-byte alignment and leading
+ *    dimension; float32 arrays are 4-byte, int64 arrays 8-byte aligned (TG_ERR_MISALIGNED).
+ *  - Sums, statistics and losses are float32; every fp16 output is rounded once.  Results are
+ *    bitwise reproducible run to run.
+ *  - Outputs must not overlap inputs, except where said.
+ * ---------------------------------------------------------------------------------------
+ */
+
+/* Types of layer norm's parameters and of a teacher's logits. */
+enum { TG_TYPE_F16 = 0, TG_TYPE_F32 = 1 };
+
+#define TG_NORM_MAX_WIDTH 32768 /* a row is held in one thread block's registers */
+
+/*
+ * Layer normalisation of each row of X (M x N, N in 1..TG_NORM_MAX_WIDTH):
+ *     Y[i][j] = fp16( (X[i][j] - mean_i) * rstd_i * gamma[j] + beta[j] )
+ *     mean_i = sum_j X[i][j] / N,  rstd_i = 1 / sqrt( sum_j (X[i][j] - mean_i)^2 / N + eps )
+ * gamma, beta: N values of param_type, or NULL for 1 and 0.  mean, rstd: NULL, or float32[M] that
+ * get the statistics (the backward pass needs them).  eps >= 0.  Y may be X (with ldy == ldx).
+ */
+tg_status tg_layernorm_f16(const void* X, const void* gamma, const void* beta, void* Y,
+                           float* mean, float* rstd, int64_t M, int64_t N, int64_t ldx,
+                           int64_t ldy, float eps, int param_type, tg_stream_t stream);
+
+/*
+ * Backward of tg_layernorm_f16, with h = (X - mean) * rstd and g = dY * gamma:
+ *     dX[i][j] = fp16( rstd_i * (g[i][j] - sum_k g[i][k] / N - h[i][j] * sum_k g[i][k] h[i][k] / N) )
+ *     dgamma[j] = sum_i dY[i][j] h[i][j],   dbeta[j] = sum_i dY[i][j]     (of param_type)
+ * dX, dgamma, dbeta: each may be NULL (not computed).  dX may be dY or X (with the same leading
+ * dimension).  M == 0 writes zeros to dgamma and dbeta.
+ */
+tg_status tg_layernorm_backward_f16(const void* dY, const void* X, const void* gamma,
+                                    const float* mean, const float* rstd, void* dX, void* dgamma,
+                                    void* dbeta, int64_t M, int64_t N, int64_t lddy, int64_t ldx,
+                                    int64_t lddx, int param_type, tg_stream_t stream);
+
+/* Storage of a head's weight and of its gradient: V x D (as an embedding), or D x V (as the right
+ * operand of tg_gemm_relu_f16). */
+enum { TG_HEAD_VOCAB_MAJOR = 0, TG_HEAD_WIDTH_MAJOR = 1 };
+
+#define TG_HEAD_MAX_TOP 1024 /* teacher entries of a row */
+
+/* Options of the head's losses.  Zero-initialise; zero fields choose. */
+typedef struct {
+  int layout;         /* TG_HEAD_* */
+  int debug_flags;    /* TG_DEBUG_*, for the error-path test */
+  int timeout_ms;     /* as tg_options.timeout_ms */
+  int reserved;
+  int64_t piece_rows; /* 0, or the number of tokens whose logits are in scratch at a time */
+} tg_head_options;
+
+/*
+ * Softmax cross entropy of the linear head z = logit_scale * X W^T (X T x D; z T x V, float32):
+ *     lse[t]  = log sum_v exp z[t][v]                                  (NULL: not wanted)
+ *     loss[t] = lse[t] - z[t][target[t]]                               (NULL: not wanted)
+ *     dX = d/dX sum_t dloss[t] loss[t]  (T x D),   dW = d/dW of the same   (NULL: not wanted)
+ * target: int64[T].  A row whose target is ignore_index has loss 0 and no gradient; any other
+ * target outside [0, V) makes the row's loss and the gradients NaN.  dloss: float32[T], needed for
+ * a gradient.  V, D >= 1; T == 0 writes only dW = 0.  logit_scale > 0.
+ * Scratch: the logits (float32) and their gradient (fp16) of a piece of the tokens, 2^29 of them
+ * or 256 tokens' by default; with several pieces, dW in float32; copies of X and W when they are not
+ * 16-byte aligned with leading dimensions that are multiples of 8.
+ * The gradient of the logits is rounded to fp16 relative to the largest |dloss|: a row whose
+ * |dloss| is below 2^-15 of that keeps fewer than 11 bits of its small probabilities.
+ */
+tg_status tg_linear_cross_entropy_f16(const void* X, const void* W, const int64_t* target,
+                                      int64_t ignore_index, float logit_scale, const float* dloss,
+                                      float* loss, float* lse, void* dX, void* dW, int64_t T,
+                                      int64_t V, int64_t D, int64_t ldx, int64_t ldw, int64_t lddx,
+                                      int64_t lddw, const tg_head_options* opt,
+                                      tg_stream_t stream);
+
+/*
+ * Distillation of the head from a teacher's `top` (1..TG_HEAD_MAX_TOP) kept logits of each row:
+ *     q = softmax over the row's entries e of teacher_logits[t][e] / temperature
+ *     z = X W^T / temperature,   lse[t] = log sum_v exp z[t][v]
+ *     loss[t] = sum_e q_e (log q_e - (z[t][teacher_index[t][e]] - lse[t]))
+ * (the divergence of the student from the teacher's distribution over its kept tokens; 0 log 0 is
+ * 0).  teacher_index: int64, teacher_logits: teacher_type, rows of ldt >= top entries each.  An
+ * entry with a negative index is not there; entries may be in any order, and entries of the same
+ * token add up.  A row with no entry, or with all of them at -inf, has loss 0 and no gradient.  An
+ * index >= V, or a teacher's logit of NaN or +inf, makes the row's loss and the gradients NaN.
+ * Everything else as tg_linear_cross_entropy_f16.
+ */
+tg_status tg_linear_distill_f16(const void* X, const void* W, const int64_t* teacher_index,
+                                const void* teacher_logits, int teacher_type, int top, int64_t ldt,
+                                float temperature, const float* dloss, float* loss, float* lse,
+                                void* dX, void* dW, int64_t T, int64_t V, int64_t D, int64_t ldx,
+                                int64_t ldw, int64_t lddx, int64_t lddw,
+                                const tg_head_options* opt, tg_stream_t stream);
+
 /* Library version as major*10000 + minor*100 + patch.  300: tg_options gained dequant_first
  * (callers must be built against this header). */
 int tg_version(void);
