@@ -17,7 +17,7 @@ import torch
 
 from . import binding
 from .binding import TG_HEAD_VOCAB_MAJOR
-from .tensors import call, param_type, rows, stream_of
+from .tensors import check, here, library, on, param_type, ptr, rows, stream_handle, vector
 
 _LAYOUTS = {}
 
@@ -45,13 +45,6 @@ def _sizes(x, weight, layout):
     return T, V, D, ldx, ldw
 
 
-def _vector(t, T, dtype, device, name):
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.shape != (T,) or t.device != device or (T > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous ({T},) tensor on x's device")
-
-
 def _teacher(index, logits, T, device):
     if index.dtype != torch.int64:
         raise TypeError("teacher_index must be torch.int64")
@@ -68,37 +61,62 @@ def _teacher(index, logits, T, device):
     return top, kind
 
 
-def _run(x, weight, layout, piece_rows, stream, dloss, need_dx, need_dw, want_lse, inputs, make):
-    """One call: allocates the outputs and hands make(...)'s leading arguments on."""
-    T, V, D, ldx, ldw = _sizes(x, weight, layout)
+def _outputs(x, weight, T, D, need_dx, need_dw, want_lse):
     dev = x.device
+    return (torch.empty(T, dtype=torch.float32, device=dev),
+            torch.empty(T, dtype=torch.float32, device=dev) if want_lse else None,
+            torch.empty((T, D), dtype=torch.float16, device=dev) if need_dx else None,
+            torch.empty(weight.shape, dtype=torch.float16, device=dev) if need_dw else None)
+
+
+def _weights(dloss, T, device):
     if dloss is not None:
-        _vector(dloss, T, torch.float32, dev, "dloss")
-    with stream_of(dev, stream, x, weight, dloss, *inputs) as handle:
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-        lse = torch.empty(T, dtype=torch.float32, device=dev) if want_lse else None
-        dx = torch.empty((T, D), dtype=torch.float16, device=dev) if need_dx else None
-        dw = torch.empty(weight.shape, dtype=torch.float16, device=dev) if need_dw else None
-        name, lead = make
-        call(name, x, weight, *lead, dloss, loss, lse, dx, dw, T, V, D, ldx, ldw, D,
-             weight.shape[1], _options(layout, piece_rows), handle)
-    return loss, lse, dx, dw
+        if dloss.dtype is not torch.float32:
+            raise TypeError("dloss must be torch.float32")
+        vector(dloss, T, device, "dloss")
 
 
 def _cross_entropy(x, weight, target, dloss, need_dx, need_dw, want_lse, ignore_index, logit_scale,
                    layout, piece_rows, stream):
-    _vector(target, x.shape[0], torch.int64, x.device, "target")
-    return _run(x, weight, layout, piece_rows, stream, dloss, need_dx, need_dw, want_lse, (target,),
-                ("tg_linear_cross_entropy_f16", (target, ignore_index, logit_scale)))
+    """(loss, lse, dx, dweight), None for what is not wanted."""
+    T, V, D, ldx, ldw = _sizes(x, weight, layout)
+    dev = x.device
+    if not here(dev, stream):
+        with on(dev, stream, x, weight, target, dloss):
+            return _cross_entropy(x, weight, target, dloss, need_dx, need_dw, want_lse,
+                                  ignore_index, logit_scale, layout, piece_rows, None)
+    if target.dtype is not torch.int64:
+        raise TypeError("target must be torch.int64")
+    vector(target, T, dev, "target")
+    _weights(dloss, T, dev)
+    out = _outputs(x, weight, T, D, need_dx, need_dw, want_lse)
+    loss, lse, dx, dw = out
+    check(library().tg_linear_cross_entropy_f16(
+        x.data_ptr(), weight.data_ptr(), target.data_ptr(), ignore_index, logit_scale, ptr(dloss),
+        loss.data_ptr(), ptr(lse), ptr(dx), ptr(dw), T, V, D, ldx, ldw, D, weight.shape[1],
+        _options(layout, piece_rows), stream_handle(dev.index)), "tg_linear_cross_entropy_f16")
+    return out
 
 
 def _distillation(x, weight, teacher_index, teacher_logits, dloss, need_dx, need_dw, want_lse,
                   temperature, layout, piece_rows, stream):
-    top, kind = _teacher(teacher_index, teacher_logits, x.shape[0], x.device)
-    return _run(x, weight, layout, piece_rows, stream, dloss, need_dx, need_dw, want_lse,
-                (teacher_index, teacher_logits),
-                ("tg_linear_distill_f16",
-                 (teacher_index, teacher_logits, kind, top, top, temperature)))
+    """(loss, lse, dx, dweight), None for what is not wanted."""
+    T, V, D, ldx, ldw = _sizes(x, weight, layout)
+    dev = x.device
+    if not here(dev, stream):
+        with on(dev, stream, x, weight, teacher_index, teacher_logits, dloss):
+            return _distillation(x, weight, teacher_index, teacher_logits, dloss, need_dx, need_dw,
+                                 want_lse, temperature, layout, piece_rows, None)
+    top, kind = _teacher(teacher_index, teacher_logits, T, dev)
+    _weights(dloss, T, dev)
+    out = _outputs(x, weight, T, D, need_dx, need_dw, want_lse)
+    loss, lse, dx, dw = out
+    check(library().tg_linear_distill_f16(
+        x.data_ptr(), weight.data_ptr(), teacher_index.data_ptr(), teacher_logits.data_ptr(), kind,
+        top, top, temperature, ptr(dloss), loss.data_ptr(), ptr(lse), ptr(dx), ptr(dw), T, V, D,
+        ldx, ldw, D, weight.shape[1], _options(layout, piece_rows), stream_handle(dev.index)),
+        "tg_linear_distill_f16")
+    return out
 
 
 def linear_cross_entropy(x, weight, target, ignore_index: int = -100, logit_scale: float = 1.0,

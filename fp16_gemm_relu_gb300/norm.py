@@ -12,20 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import binding
-from .tensors import call, param_type, rows, stream_of
-
-
-def _params(gamma, beta, n, device):
-    kind = binding.TG_TYPE_F16
-    for p, name in ((gamma, "gamma"), (beta, "beta")):
-        if p is None:
-            continue
-        if p.shape != (n,) or not p.is_contiguous() or p.device != device:
-            raise ValueError(f"{name} must be a contiguous ({n},) tensor on x's device")
-        kind = param_type(p, name)
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise TypeError("gamma and beta must have one type")
-    return kind
+from .tensors import check, here, library, on, param_type, ptr, rows, stream_handle, vector
 
 
 def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False, out=None,
@@ -38,20 +25,34 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False,
     Runs on ``stream`` (default: torch's current stream) and returns without synchronising.
     """
     ldx = rows(x, "x")
+    dev = x.device
+    if not here(dev, stream):
+        with on(dev, stream, x, gamma, beta, out):
+            return layer_norm(x, gamma, beta, eps, stats, out)
     M, N = x.shape
-    kind = _params(gamma, beta, N, x.device)
-    with stream_of(x.device, stream, x, gamma, beta, out) as handle:
-        if out is None:
-            out = torch.empty((M, N), dtype=torch.float16, device=x.device)
-            ldy = N
-        else:
-            if out.shape != x.shape or out.device != x.device:
-                raise ValueError("out must be an (M, N) tensor on x's device")
-            ldy = rows(out, "out")
-        mean = rstd = None
-        if stats:
-            mean, rstd = torch.empty((2, M), dtype=torch.float32, device=x.device).unbind(0)
-        call("tg_layernorm_f16", x, gamma, beta, out, mean, rstd, M, N, ldx, ldy, eps, kind, handle)
+    kind = binding.TG_TYPE_F16
+    if gamma is not None:
+        kind = param_type(gamma, "gamma")
+        vector(gamma, N, dev, "gamma")
+    if beta is not None:
+        kind = param_type(beta, "beta")
+        vector(beta, N, dev, "beta")
+        if gamma is not None and gamma.dtype is not beta.dtype:
+            raise TypeError("gamma and beta must have one type")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        ldy = N
+    else:
+        if out.shape != x.shape or out.device != dev:
+            raise ValueError("out must be an (M, N) tensor on x's device")
+        ldy = rows(out, "out")
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(M, dtype=torch.float32, device=dev)
+        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    check(library().tg_layernorm_f16(x.data_ptr(), ptr(gamma), ptr(beta), out.data_ptr(), ptr(mean),
+                                     ptr(rstd), M, N, ldx, ldy, eps, kind,
+                                     stream_handle(dev.index)), "tg_layernorm_f16")
     return (out, mean, rstd) if stats else out
 
 
@@ -62,21 +63,28 @@ def layer_norm_backward(dy, x, mean, rstd, gamma=None, param_grads: bool = True,
     are None and not computed.
     """
     lddy, ldx = rows(dy, "dy"), rows(x, "x")
+    dev = x.device
+    if not here(dev, stream):
+        with on(dev, stream, dy, x, mean, rstd, gamma):
+            return layer_norm_backward(dy, x, mean, rstd, gamma, param_grads)
     M, N = x.shape
-    if dy.shape != x.shape or dy.device != x.device:
+    if dy.shape != x.shape or dy.device != dev:
         raise ValueError("dy must have x's shape and device")
-    for s, name in ((mean, "mean"), (rstd, "rstd")):
-        if s.shape != (M,) or s.dtype != torch.float32 or s.device != x.device or (
-                M > 1 and s.stride(0) != 1):
-            raise ValueError(f"{name} must be a contiguous float32 (M,) tensor on x's device")
-    kind = _params(gamma, None, N, x.device) if gamma is not None else binding.TG_TYPE_F32
-    with stream_of(x.device, stream, dy, x, mean, rstd, gamma) as handle:
-        dx = torch.empty((M, N), dtype=torch.float16, device=x.device)
-        dgamma = dbeta = None
-        if param_grads:
-            dtype = torch.float32 if gamma is None else gamma.dtype
-            dgamma = torch.empty(N, dtype=dtype, device=x.device)
-            dbeta = torch.empty(N, dtype=dtype, device=x.device)
-        call("tg_layernorm_backward_f16", dy, x, gamma, mean, rstd, dx, dgamma, dbeta, M, N, lddy,
-             ldx, max(N, 1), kind, handle)
+    vector(mean, M, dev, "mean")
+    vector(rstd, M, dev, "rstd")
+    if mean.dtype is not torch.float32 or rstd.dtype is not torch.float32:
+        raise TypeError("mean and rstd must be torch.float32")
+    kind, dtype = binding.TG_TYPE_F32, torch.float32
+    if gamma is not None:
+        kind, dtype = param_type(gamma, "gamma"), gamma.dtype
+        vector(gamma, N, dev, "gamma")
+    dx = torch.empty((M, N), dtype=torch.float16, device=dev)
+    dgamma = dbeta = None
+    if param_grads:
+        dgamma = torch.empty(N, dtype=dtype, device=dev)
+        dbeta = torch.empty(N, dtype=dtype, device=dev)
+    check(library().tg_layernorm_backward_f16(
+        dy.data_ptr(), x.data_ptr(), ptr(gamma), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
+        ptr(dgamma), ptr(dbeta), M, N, lddy, ldx, N, kind, stream_handle(dev.index)),
+        "tg_layernorm_backward_f16")
     return dx, dgamma, dbeta

@@ -1,4 +1,8 @@
-"""What the operators' torch entry points share: argument checks, streams, and the C call."""
+"""What the operators' torch entry points share: argument checks, streams, and the C call.
+
+The smallest calls take a few microseconds on the GPU, so the common case (tensors of the current
+device, torch's current stream) goes without context managers and temporary objects.
+"""
 
 from __future__ import annotations
 
@@ -8,75 +12,81 @@ import torch
 
 from . import binding
 
+_F16, _F32 = torch.float16, torch.float32
+
 
 def rows(t: torch.Tensor, name: str) -> int:
     """The leading dimension of a 2-D CUDA fp16 tensor of rows with unit column stride."""
-    if t.dtype != torch.float16:
+    if t.dtype is not _F16:
         raise TypeError(f"{name} must be torch.float16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    n = t.shape[1]
-    if n > 1 and t.stride(1) != 1:
+    m, n = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and n > 1:
         raise ValueError(f"{name} must be row-major (unit stride along columns)")
-    if t.shape[0] <= 1:
-        return max(n, 1)
-    ld = t.stride(0)
-    if ld < max(n, 1):
+    if m <= 1:
+        return n or 1
+    if ld < n or ld < 1:
         raise ValueError(f"{name}'s rows overlap")
     return ld
 
 
 def param_type(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.float16:
+    if t.dtype is _F16:
         return binding.TG_TYPE_F16
-    if t.dtype == torch.float32:
+    if t.dtype is _F32:
         return binding.TG_TYPE_F32
     raise TypeError(f"{name} must be torch.float16 or torch.float32")
 
 
+def vector(t: torch.Tensor, n: int, device: torch.device, name: str) -> None:
+    """A dense vector of n values on `device`."""
+    if t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous ({n},) tensor on x's device")
+
+
+def here(device: torch.device, stream) -> bool:
+    """Whether a call goes to torch's current stream of the current device."""
+    return stream is None and device.index == torch.cuda.current_device()
+
+
 @contextlib.contextmanager
-def _other_stream(device, stream, tensors):
+def on(device: torch.device, stream, *tensors):
+    """Makes ``device`` and ``stream`` (a torch stream or a handle; None: torch's current one on that
+    device) current.  On a stream of the caller's, outputs are allocated there, and the inputs are
+    kept until its work is done."""
     with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
         if not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
-            yield stream.cuda_stream
+            yield
 
 
-class _Here:
-    """The current stream of the current device: nothing to enter."""
-
-    __slots__ = ("handle",)
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        return False
+def _torch_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def stream_of(device: torch.device, stream, *tensors):
-    """Context that gives the handle of ``stream`` (None: torch's current one on ``device``), with
-    ``device`` current.  On a stream of the caller's, outputs are allocated there and the inputs are
-    kept until its work is done."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _Here(torch.cuda.current_stream(device).cuda_stream)
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return _other_stream(device, stream, tensors)
+#: Handle of torch's current stream on a device: without the Stream object where torch offers that.
+stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", _torch_stream)
 
 
-def call(name: str, *args) -> None:
-    """The C function ``name``: tensors go as pointers, None as NULL, a zero stream as NULL."""
-    lib = binding._lib or binding.load_library()
-    st = getattr(lib, name)(*[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args])
-    if st != binding.TG_OK:
-        raise binding.TgError(st, name)
+def ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def library():
+    return binding._lib or binding.load_library()
+
+
+def check(status: int, name: str) -> None:
+    if status != binding.TG_OK:
+        raise binding.TgError(status, name)
