@@ -195,23 +195,6 @@ __device__ __forceinline__ void load_param(const P* p, int c, int n, float none,
   for (int i = 0; i < 4; ++i) f[i] = pair(g[2 * i], g[2 * i + 1]);
 }
 
-// Sum of v over a row's threads: a warp, or (BLOCK) the whole block, which then calls it together.
-// slots: 32 floats, not in use by the call before (callers alternate).
-template <bool BLOCK>
-__device__ __forceinline__ float row_sum(float v, float* slots) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if constexpr (BLOCK) {
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) slots[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = lane < static_cast<int>(blockDim.x >> 5) ? slots[lane] : 0.0f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  }
-  return v;
-}
-
 // 1 for the columns 8c .. 8c + 7 that a row of n has, 0 for the others (VEC: all or none).
 template <bool VEC>
 __device__ __forceinline__ f32x2 there(int c, int n, int i) {
@@ -220,183 +203,388 @@ __device__ __forceinline__ f32x2 there(int c, int n, int i) {
   return pair(e0 + 2 * i < n ? 1.0f : 0.0f, e0 + 2 * i + 1 < n ? 1.0f : 0.0f);
 }
 
-// Forward: a row a warp (BLOCK false) or a row a block, CH chunks of eight a thread, THREADS at
-// most a block.  Warps or blocks walk the rows in steps of the grid, so with CH <= 2 gamma and
-// beta stay in registers, and the next row is loaded before the current one is reduced: its
-// latency passes under the current row's arithmetic and barriers.
-template <int CH, bool BLOCK, bool VEC, int THREADS, typename P>
-__global__ void __launch_bounds__(THREADS)
+// ---------------------------------------------------------------------------------------
+// Rows through shared memory.  A group of threads (a warp, or several) works on one row at a time;
+// its first thread fetches rows ahead into a ring of slots with bulk copies, so the next rows'
+// latency passes under the current one's arithmetic without holding registers, and a row costs
+// one copy instruction instead of a load and its addresses a thread.
+// ---------------------------------------------------------------------------------------
+
+// 16-byte blocks that hold elements of a matrix's rows, from `lo` on and before `hi`: blocks in
+// between may hold other elements of the same rows' buffer, never anything outside it.
+struct Span {
+  uintptr_t lo, hi;
+};
+__device__ __forceinline__ Span span_of(const uint16_t* p, int64_t ld, int64_t rows, int n) {
+  return {(reinterpret_cast<uintptr_t>(p) + 15) & ~uintptr_t{15},
+          reinterpret_cast<uintptr_t>(p + (rows - 1) * ld + n) & ~uintptr_t{15}};
+}
+
+// What one thread copies of a row into a slot (the row starts (row mod 16) bytes in): its aligned
+// blocks [from, to), which the barrier is told of; elements of the matrix's first and last block,
+// where those are not whole, one by one.
+struct Fetch {
+  uintptr_t from, to, start;
+};
+template <bool VEC>
+__device__ __forceinline__ Fetch plan_fetch(const uint16_t* row, int n, const Span& sp) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(row), z = reinterpret_cast<uintptr_t>(row + n);
+  if constexpr (VEC) return {a, z, a};
+  const uintptr_t start = a & ~uintptr_t{15}, end = (z + 15) & ~uintptr_t{15};
+  const uintptr_t from = start > sp.lo ? start : sp.lo, to = end < sp.hi ? end : sp.hi;
+  return {from, to > from ? to : from, start};
+}
+// The elements that no whole block has; before the barrier's arrive, which releases them.
+template <bool VEC>
+__device__ __forceinline__ void fetch_edges(const Fetch& f, uint8_t* slot, const uint16_t* row, int n) {
+  if constexpr (!VEC) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row), z = reinterpret_cast<uintptr_t>(row + n);
+    for (uintptr_t p = a; p < z && p < f.from; p += 2)
+      *reinterpret_cast<uint16_t*>(slot + (p - f.start)) = *reinterpret_cast<const uint16_t*>(p);
+    for (uintptr_t p = f.to > a ? f.to : a; p < z; p += 2)
+      *reinterpret_cast<uint16_t*>(slot + (p - f.start)) = *reinterpret_cast<const uint16_t*>(p);
+  }
+}
+__device__ __forceinline__ void fetch_blocks(const Fetch& f, uint8_t* slot, uint32_t bar) {
+  if (f.to == f.from) return;
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          tg::smem_u32(slot + (f.from - f.start))),
+      "l"(f.from), "r"(static_cast<uint32_t>(f.to - f.from)), "r"(bar)
+      : "memory");
+}
+
+// Waits for a slot.  A wait that runs out (2 s) is recorded as a timeout and ends all later
+// waits of the block, which then runs to its end on what is there.
+__device__ __forceinline__ void slot_wait(uint32_t bar, uint32_t parity, volatile int* late,
+                                          unsigned* err) {
+  if (tg::mbar_try_wait(bar, parity)) return;
+  const unsigned long long t0 = tg::global_timer_ns();
+  for (uint32_t it = 1; !tg::mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) != 0) continue;
+    if (*late) return;
+    if (tg::global_timer_ns() - t0 > 2000000000ull) {
+      *late = 1;
+      atomicOr(err, 1u | (tg::kRoleProducer << 8));
+      return;
+    }
+  }
+}
+
+// Elements [8c, 8c + 8) of the row in a slot, zeros from n on; b: bytes from the slot's start to the
+// row's.
+template <bool VEC>
+__device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int c, int n) {
+  const int e0 = c << 3;
+  if (e0 >= n) return make_uint4(0, 0, 0, 0);
+  const uint4* blk = reinterpret_cast<const uint4*>(slot) + c;
+  if (VEC) return *blk;
+  const uint4 lo = blk[0], hi = blk[1];
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const uint32_t q = b >> 2;
+  uint32_t t[7], u[5], o[4];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) t[i] = (q & 1u) ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) u[i] = (q & 2u) ? t[i + 2] : t[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (b & 2u) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+  if (e0 + 8 > n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e0 + 2 * i >= n) o[i] = 0u;
+      else if (e0 + 2 * i + 1 >= n) o[i] &= 0xFFFFu;
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// The threads of a group meet (id: the group's number in the block).
+__device__ __forceinline__ void group_sync(int tpr, int id) {
+  if (tpr == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(tpr) : "memory");
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// Sum over a group; slots: a float for each of its warps, not in use by the call before.
+__device__ __forceinline__ float group_sum(float v, int tpr, int id, float* slots) {
+  v = warp_sum(v);
+  if (tpr == 32) {
+    __syncwarp();
+    return v;
+  }
+  const int wpr = tpr >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) slots[(threadIdx.x >> 5) - id * wpr] = v;
+  group_sync(tpr, id);
+  return warp_sum(lane < wpr ? slots[lane] : 0.0f);
+}
+
+// gamma (or beta) as float32 in shared memory, `chunks` of eight columns, `none` where there is no
+// value: the chunks' first halves, then their second halves, so that a warp's 16-byte reads of
+// either are contiguous (side by side they would meet in the same banks two by two).
+template <bool VEC, typename P>
+__device__ __forceinline__ void stage_param(float* dst, const P* p, int n, int chunks, float none) {
+  ulonglong2* q = reinterpret_cast<ulonglong2*>(dst);
+#pragma unroll 4
+  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+    f32x2 f[4];
+    load_param<VEC>(p, c, n, none, f);
+    q[c] = make_ulonglong2(f[0], f[1]);
+    q[chunks + c] = make_ulonglong2(f[2], f[3]);
+  }
+}
+__device__ __forceinline__ void staged(const float* src, int c, int chunks, f32x2 (&f)[4]) {
+  const ulonglong2* q = reinterpret_cast<const ulonglong2*>(src);
+  const ulonglong2 a = q[c], b = q[chunks + c];
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+
+// Bytes by which a row's start misses a 16-byte boundary.
+__device__ __forceinline__ uint32_t row_shift(const uint16_t* p, int64_t ld, int64_t row) {
+  return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) +
+          2u * static_cast<uint32_t>(ld) * static_cast<uint32_t>(row)) & 15u;
+}
+
+constexpr int kFwdChunks = 4, kFwdSlots = 2;
+
+// Forward, kFwdChunks chunks a thread: 32 elements share the reductions' and the loop's cost.
+template <bool VEC, typename P>
+__global__ void __launch_bounds__(512)
     tg_layernorm_kernel(const uint16_t* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
                         const P* __restrict__ beta, uint16_t* __restrict__ y, int64_t ldy,
                         float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int n,
-                        float eps) {
-  __shared__ float slots[2][32];
-  constexpr bool kKeep = CH <= 2;
-  const int tpr = BLOCK ? blockDim.x : 32;  // threads of a row
-  const int lane = threadIdx.x & 31, t = BLOCK ? threadIdx.x : lane;
-  const int64_t step = BLOCK ? gridDim.x : int64_t(gridDim.x) * (blockDim.x >> 5);
-  int64_t r = BLOCK ? blockIdx.x : blockIdx.x * int64_t(blockDim.x >> 5) + (threadIdx.x >> 5);
-  const float inv_n = 1.0f / static_cast<float>(n);
-  uint4 next[CH];
-  auto load = [&](int64_t row) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) next[i] = load_chunk<VEC>(x + row * ldx, i * tpr + t, n);
+                        float eps, int tpr, int slot_bytes, unsigned* err) {
+  constexpr int CH = kFwdChunks, S = kFwdSlots;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t bars[8][S];
+  __shared__ float sums[8][2][16];
+  __shared__ volatile int late;
+  const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, lane = threadIdx.x & 31;
+  const int per_block = blockDim.x / tpr, chunks = CH * tpr;
+  float* sg = reinterpret_cast<float*>(smem);
+  float* so = sg + chunks * 8;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(so + chunks * 8) + int64_t(group) * S * slot_bytes;
+  const Span sp = span_of(x, ldx, rows, n);
+  const int64_t step = int64_t(gridDim.x) * per_block;
+  int64_t r = blockIdx.x * int64_t(per_block) + group;
+  auto fetch = [&](int64_t row, int s) {
+    const uint16_t* src = x + row * ldx;
+    const uint32_t bar = tg::smem_u32(&bars[group][s]);
+    const Fetch f = plan_fetch<VEC>(src, n, sp);
+    uint8_t* slot = ring + s * slot_bytes;
+    fetch_edges<VEC>(f, slot, src, n);
+    tg::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(f.to - f.from));
+    fetch_blocks(f, slot, bar);
   };
-  if (r < rows) load(r);
-  f32x2 g[kKeep ? CH : 1][4], o[kKeep ? CH : 1][4];
-  if constexpr (kKeep) {
+  if (threadIdx.x == 0) late = 0;
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) tg::mbar_init(tg::smem_u32(&bars[group][s]), 1);
+    tg::fence_mbar_init();
+    for (int s = 0; s < S; ++s)
+      if (r + s * step < rows) fetch(r + s * step, s);
+  }
+  stage_param<VEC>(sg, gamma, n, chunks, 1.0f);
+  stage_param<VEC>(so, beta, n, chunks, 0.0f);
+  __syncthreads();
+  const float inv_n = 1.0f / static_cast<float>(n);
+  for (int k = 0; r < rows; r += step, ++k) {
+    const int s = k & 1;
+    slot_wait(tg::smem_u32(&bars[group][s]), (k >> 1) & 1, &late, err);
+    const uint32_t b = VEC ? 0u : row_shift(x, ldx, r);
+    f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      load_param<VEC>(gamma, i * tpr + t, n, 1.0f, g[i]);
-      load_param<VEC>(beta, i * tpr + t, n, 0.0f, o[i]);
+      unpack8(slot_chunk<VEC>(ring + s * slot_bytes, b, i * tpr + t, n), v[i]);
+      acc = add2(acc, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
     }
-  }
-  for (; r < rows; r += step) {
-    f32x2 v[CH][4];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) unpack8(next[i], v[i]);
-    if (kKeep && r + step < rows) load(r + step);
-    f32x2 s = pair(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-      s = add2(s, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
-    const float mu = row_sum<BLOCK>(sum2(s), slots[0]) * inv_n;
+    const float mu = group_sum(sum2(acc), tpr, group, sums[group][0]) * inv_n;
+    if (t == 0 && r + S * step < rows) fetch(r + S * step, s);  // everyone has read this slot
     const f32x2 less = pair(-mu, -mu);
     f32x2 q = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+      const int c = i * tpr + t;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        v[i][j] = mul2(add2(v[i][j], less), there<VEC>(i * tpr + t, n, j));
-        q = fma2(v[i][j], v[i][j], q);
+        v[i][j] = add2(v[i][j], less);
+        if (VEC) {
+          if (c * 8 < n) q = fma2(v[i][j], v[i][j], q);
+        } else {
+          const f32x2 d = mul2(v[i][j], there<VEC>(c, n, j));
+          q = fma2(d, d, q);
+        }
       }
     }
-    const float rs = 1.0f / sqrtf(row_sum<BLOCK>(sum2(q), slots[1]) * inv_n + eps);
+    const float rs = rsqrtf(group_sum(sum2(q), tpr, group, sums[group][1]) * inv_n + eps);
     if (t == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
     }
     const f32x2 times = pair(rs, rs);
+    uint16_t* yr = y + r * ldy;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = i * tpr + t, k = kKeep ? i : 0;
-      if constexpr (!kKeep) {
-        load_param<VEC>(gamma, c, n, 1.0f, g[0]);
-        load_param<VEC>(beta, c, n, 0.0f, o[0]);
-      }
-      f32x2 out[4];
+      const int c = i * tpr + t;
+      f32x2 g[4], o[4];
+      staged(sg, c, chunks, g);
+      staged(so, c, chunks, o);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) out[j] = fma2(mul2(v[i][j], times), g[k][j], o[k][j]);
-      store_chunk<VEC>(y + r * ldy, c, n, pack8(out), lane);
+      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], times), g[j], o[j]);
+      store_chunk<VEC>(yr, c, n, pack8(o), lane);
     }
-    if (!kKeep && r + step < rows) load(r + step);
   }
 }
 
-// Backward, a row a warp or a row a block as above.  A thread keeps the same columns for all of
-// its rows, so its part of dgamma and dbeta stays in registers, and each block writes one partial
-// row of both (of np floats): part[0][block], part[1][block].  With CH <= 2 the row (as h and g)
-// and the next one stay in registers; a longer row is read a second time for dx, from L2.
-template <int CH, bool BLOCK, bool VEC, int THREADS, typename P>
-__global__ void __launch_bounds__(THREADS)
+// Backward, CH chunks a thread.  A thread keeps the same columns for all of its rows, so its part
+// of dgamma and dbeta stays in registers, and each block writes one partial row of both (of np
+// floats): part[0][block], part[1][block].  The row's two sums are needed before its dx, so the
+// loop works on two rows: it sums row i + 1 while it writes dx of row i, and meets once a row.
+template <int CH, int S, bool VEC, typename P>
+__global__ void __launch_bounds__(512)
     tg_layernorm_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                  const uint16_t* __restrict__ x, int64_t ldx,
                                  const P* __restrict__ gamma, const float* __restrict__ mean,
                                  const float* __restrict__ rstd, uint16_t* __restrict__ dx,
                                  int64_t lddx, float* __restrict__ part, int64_t np, int64_t rows,
-                                 int n) {
-  extern __shared__ float groups[];  // a row a warp: [warps][2][np]
-  __shared__ float slots[2][2][32];
-  constexpr bool kKeep = CH <= 2;
-  constexpr int kHold = kKeep ? CH : 1;
-  const int tpr = BLOCK ? blockDim.x : 32;
-  const int lane = threadIdx.x & 31, t = BLOCK ? threadIdx.x : lane;
-  const int64_t step = BLOCK ? gridDim.x : int64_t(gridDim.x) * (blockDim.x >> 5);
-  int64_t r = BLOCK ? blockIdx.x : blockIdx.x * int64_t(blockDim.x >> 5) + (threadIdx.x >> 5);
+                                 int n, int tpr, int slot_bytes, unsigned* err) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ uint64_t bars[8][S];
+  __shared__ float2 sums[8][2][16];
+  __shared__ volatile int late;
+  const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, lane = threadIdx.x & 31;
+  const int per_block = blockDim.x / tpr, chunks = CH * tpr, wpr = tpr >> 5;
+  float* sg = reinterpret_cast<float*>(smem);
+  uint8_t* ring = reinterpret_cast<uint8_t*>(sg + chunks * 8) + int64_t(group) * S * 2 * slot_bytes;
+  const Span sx = span_of(x, ldx, rows, n), sd = span_of(dy, lddy, rows, n);
+  const int64_t step = int64_t(gridDim.x) * per_block;
+  const int64_t first = blockIdx.x * int64_t(per_block) + group;
+  auto fetch = [&](int64_t row, int s) {
+    const uint32_t bar = tg::smem_u32(&bars[group][s]);
+    const uint16_t *px = x + row * ldx, *pd = dy + row * lddy;
+    const Fetch fx = plan_fetch<VEC>(px, n, sx), fd = plan_fetch<VEC>(pd, n, sd);
+    uint8_t* slot = ring + s * 2 * slot_bytes;
+    fetch_edges<VEC>(fx, slot, px, n);
+    fetch_edges<VEC>(fd, slot + slot_bytes, pd, n);
+    tg::mbar_arrive_expect_tx(bar, static_cast<uint32_t>((fx.to - fx.from) + (fd.to - fd.from)));
+    fetch_blocks(fx, slot, bar);
+    fetch_blocks(fd, slot + slot_bytes, bar);
+  };
+  if (threadIdx.x == 0) late = 0;
+  if (t == 0) {
+    for (int s = 0; s < S; ++s) tg::mbar_init(tg::smem_u32(&bars[group][s]), 1);
+    tg::fence_mbar_init();
+    for (int s = 0; s < S; ++s)
+      if (first + s * step < rows) fetch(first + s * step, s);
+  }
+  stage_param<VEC>(sg, gamma, n, chunks, 1.0f);
+  __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
   f32x2 dg[CH][4], db[CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
-  uint4 next_x[kHold], next_dy[kHold];
-  float next_mu = 0.0f, next_rs = 0.0f;
-  auto load = [&](int64_t row) {
-    if constexpr (kKeep) {
+  // u = x - mean, d = dy and gamma of chunk i of the row in slot s; past the row's end d is 0
+  auto terms = [&](int s, int64_t row, int i, float mu, f32x2(&u)[4], f32x2(&d)[4], f32x2(&g)[4]) {
+    const uint8_t* slot = ring + s * 2 * slot_bytes;
+    const int c = i * tpr + t;
+    const uint32_t bx = VEC ? 0u : row_shift(x, ldx, row), bd = VEC ? 0u : row_shift(dy, lddy, row);
+    unpack8(slot_chunk<VEC>(slot, bx, c, n), u);
+    unpack8(slot_chunk<VEC>(slot + slot_bytes, bd, c, n), d);
+    staged(sg, c, chunks, g);
+    const f32x2 less = pair(-mu, -mu);
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        next_x[i] = load_chunk<VEC>(x + row * ldx, i * tpr + t, n);
-        next_dy[i] = load_chunk<VEC>(dy + row * lddy, i * tpr + t, n);
-      }
-    }
-    next_mu = __ldg(mean + row);
-    next_rs = __ldg(rstd + row);
+    for (int j = 0; j < 4; ++j) u[j] = add2(u[j], less);
   };
-  if (r < rows) load(r);
-  f32x2 gm[kHold][4];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) load_param<VEC>(gamma, i * tpr + t, n, 1.0f, gm[i]);
-  }
-  // h and g of chunk i of a row; past the row's end dy, and with it g, is 0
-  auto terms = [&](int64_t row, int i, f32x2 less, f32x2 times, f32x2(&h)[4], f32x2(&d)[4],
-                   f32x2(&g)[4]) {
-    const int c = i * tpr + t, k = kKeep ? i : 0;
-    if constexpr (!kKeep) {
-      next_x[0] = load_chunk<VEC>(x + row * ldx, c, n);
-      next_dy[0] = load_chunk<VEC>(dy + row * lddy, c, n);
-      load_param<VEC>(gamma, c, n, 1.0f, gm[0]);
-    }
-    unpack8(next_x[k], h);
-    unpack8(next_dy[k], d);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = mul2(add2(h[j], less), times);
-      g[j] = mul2(d[j], gm[k][j]);
-    }
-  };
-  for (int turn = 0; r < rows; r += step, turn ^= 1) {
-    const float rs = next_rs;
-    const f32x2 less = pair(-next_mu, -next_mu), times = pair(rs, rs);
-    f32x2 h[kHold][4], g[kHold][4], a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
+  // With h = u rstd and g = d gamma: the sums of g and of g u (= g h / rstd) of row `row`, the k-th
+  // of this group, into sums[k & 1], and the row's part of dgamma (d u, times rstd) and dbeta
+  auto sum_row = [&](int k, int64_t row, float mu, float rs) {
+    const int s = k % S;
+    slot_wait(tg::smem_u32(&bars[group][s]), (k / S) & 1, &late, err);
+    const f32x2 times = pair(rs, rs);
+    f32x2 a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int k = kKeep ? i : 0;
-      f32x2 d[4];
-      terms(r, i, less, times, h[k], d, g[k]);
+      f32x2 u[4], d[4], g[4];
+      terms(s, row, i, mu, u, d, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a2 = add2(a2, g[k][j]);
-        b2 = fma2(g[k][j], h[k][j], b2);
-        dg[i][j] = fma2(d[j], h[k][j], dg[i][j]);
+        const f32x2 du = mul2(d[j], u[j]);
+        a2 = fma2(d[j], g[j], a2);
+        b2 = fma2(du, g[j], b2);
+        dg[i][j] = fma2(du, times, dg[i][j]);
         db[i][j] = add2(db[i][j], d[j]);
       }
     }
-    if (r + step < rows) load(r + step);
+    float a = sum2(a2), b = sum2(b2);
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, w);
+      b += __shfl_xor_sync(0xffffffffu, b, w);
+    }
+    if (lane == 0) sums[group][k & 1][(threadIdx.x >> 5) - group * wpr] = make_float2(a, b);
+  };
+  float mu = 0.0f, rs = 0.0f, mu1 = 0.0f, rs1 = 0.0f;
+  if (first < rows) {
+    mu = __ldg(mean + first);
+    rs = __ldg(rstd + first);
+    if (first + step < rows) {
+      mu1 = __ldg(mean + first + step);
+      rs1 = __ldg(rstd + first + step);
+    }
+    sum_row(0, first, mu, rs);
+  }
+  group_sync(tpr, group);
+  int64_t r = first;
+  uint16_t* dxr = dx + first * lddx;
+  for (int k = 0; r < rows; r += step, ++k) {
+    float mu2 = 0.0f, rs2 = 0.0f;
+    if (r + 2 * step < rows) {
+      mu2 = __ldg(mean + r + 2 * step);
+      rs2 = __ldg(rstd + r + 2 * step);
+    }
+    if (r + step < rows) sum_row(k + 1, r + step, mu1, rs1);
     if (dx != nullptr) {
-      const float a = row_sum<BLOCK>(sum2(a2), slots[turn][0]) * inv_n;
-      const float b = row_sum<BLOCK>(sum2(b2), slots[turn][1]) * inv_n;
-      const f32x2 less_a = pair(-a, -a), less_b = pair(-b, -b);
+      // dx = rstd (g - mean(g) - h mean(g h)) = d (gamma rstd) + u (-rstd^3 mean(g u)) - rstd mean(g)
+      float2 p = lane < wpr ? sums[group][k & 1][lane] : make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) {
+        p.x += __shfl_xor_sync(0xffffffffu, p.x, w);
+        p.y += __shfl_xor_sync(0xffffffffu, p.y, w);
+      }
+      p.x = __shfl_sync(0xffffffffu, p.x, 0);
+      p.y = __shfl_sync(0xffffffffu, p.y, 0);
+      const float c1 = -rs * rs * rs * (p.y * inv_n), c0 = -rs * (p.x * inv_n);
+      const f32x2 of_u = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int k = kKeep ? i : 0;
-        if constexpr (!kKeep) {
-          f32x2 d[4];
-          terms(r, i, less, times, h[0], d, g[0]);
-        }
-        f32x2 out[4];
+        f32x2 u[4], d[4], g[4];
+        terms(k % S, r, i, mu, u, d, g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          out[j] = mul2(times, fma2(h[k][j], less_b, add2(g[k][j], less_a)));
-        store_chunk<VEC>(dx + r * lddx, i * tpr + t, n, pack8(out), lane);
+        for (int j = 0; j < 4; ++j) g[j] = fma2(d[j], mul2(g[j], times), fma2(u[j], of_u, plus));
+        store_chunk<VEC>(dxr, i * tpr + t, n, pack8(g), lane);
       }
     }
+    dxr += step * lddx;
+    mu = mu1, rs = rs1, mu1 = mu2, rs1 = rs2;
+    group_sync(tpr, group);  // slot k % S and sums[k & 1] are free, sums[(k + 1) & 1] is written
+    if (t == 0 && r + S * step < rows) fetch(r + S * step, k % S);
   }
   if (part == nullptr) return;
+  // the block's groups are added in their order; the ring is empty by now
+  __syncthreads();
+  float* groups = sg + chunks * 8;  // [groups][2][np], over the ring
   float* out_g = part + int64_t(blockIdx.x) * np;
   float* out_b = part + (int64_t(gridDim.x) + blockIdx.x) * np;
-  float* to_g = BLOCK ? out_g : groups + int64_t(threadIdx.x >> 5) * 2 * np;
-  float* to_b = BLOCK ? out_b : to_g + np;
+  float* to_g = per_block == 1 ? out_g : groups + int64_t(group) * 2 * np;
+  float* to_b = per_block == 1 ? out_b : to_g + np;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int e0 = (i * tpr + t) << 3;
@@ -407,16 +595,148 @@ __global__ void __launch_bounds__(THREADS)
       if (e0 + 2 * j + 1 < n) to_g[e0 + 2 * j + 1] = fg.y, to_b[e0 + 2 * j + 1] = fb.y;
     }
   }
-  if constexpr (!BLOCK) {  // the block's warps are added in their order
-    __syncthreads();
-    for (int e = threadIdx.x; e < n; e += blockDim.x) {
-      float sg = 0.0f, sb = 0.0f;
-      for (int k = 0; k < static_cast<int>(blockDim.x >> 5); ++k) {
-        sg += groups[int64_t(k) * 2 * np + e];
-        sb += groups[(int64_t(k) * 2 + 1) * np + e];
+  if (per_block == 1) return;
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+    float g = 0.0f, b = 0.0f;
+    for (int k = 0; k < per_block; ++k) {
+      g += groups[int64_t(k) * 2 * np + e];
+      b += groups[(int64_t(k) * 2 + 1) * np + e];
+    }
+    out_g[e] = g;
+    out_b[e] = b;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// Rows of more than 16384 columns, whose ring would not fit in shared memory: a row a block,
+// straight from global memory.
+// ---------------------------------------------------------------------------------------
+constexpr int kLongThreads = 1024, kLongChunks = 4;
+
+template <bool VEC, typename P>
+__global__ void __launch_bounds__(kLongThreads)
+    tg_layernorm_long_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                             const P* __restrict__ gamma, const P* __restrict__ beta,
+                             uint16_t* __restrict__ y, int64_t ldy, float* __restrict__ mean,
+                             float* __restrict__ rstd, int64_t rows, int n, float eps) {
+  constexpr int CH = kLongChunks;
+  __shared__ float slots[2][32];
+  const int t = threadIdx.x, lane = t & 31;
+  const float inv_n = 1.0f / static_cast<float>(n);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    uint4 v[CH];
+    f32x2 s = pair(0.0f, 0.0f), q = s;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = load_chunk<VEC>(x + r * ldx, i * kLongThreads + t, n);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 f[4];
+      unpack8(v[i], f);
+      s = add2(s, add2(add2(f[0], f[1]), add2(f[2], f[3])));
+    }
+    const float mu = group_sum(sum2(s), kLongThreads, 0, slots[0]) * inv_n;
+    const f32x2 less = pair(-mu, -mu);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 f[4];
+      unpack8(v[i], f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 d = mul2(add2(f[j], less), there<VEC>(i * kLongThreads + t, n, j));
+        q = fma2(d, d, q);
       }
-      out_g[e] = sg;
-      out_b[e] = sb;
+    }
+    const float rs = rsqrtf(group_sum(sum2(q), kLongThreads, 0, slots[1]) * inv_n + eps);
+    if (t == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
+    const f32x2 times = pair(rs, rs);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = i * kLongThreads + t;
+      f32x2 f[4], g[4], o[4];
+      unpack8(v[i], f);
+      load_param<VEC>(gamma, c, n, 1.0f, g);
+      load_param<VEC>(beta, c, n, 0.0f, o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(add2(f[j], less), times), g[j], o[j]);
+      store_chunk<VEC>(y + r * ldy, c, n, pack8(o), lane);
+    }
+  }
+}
+
+// The row is read a second time for dx, from L2.
+template <bool VEC, typename P>
+__global__ void __launch_bounds__(kLongThreads)
+    tg_layernorm_backward_long_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
+                                      const uint16_t* __restrict__ x, int64_t ldx,
+                                      const P* __restrict__ gamma, const float* __restrict__ mean,
+                                      const float* __restrict__ rstd, uint16_t* __restrict__ dx,
+                                      int64_t lddx, float* __restrict__ part, int64_t np,
+                                      int64_t rows, int n) {
+  constexpr int CH = kLongChunks;
+  __shared__ float slots[2][2][32];
+  const int t = threadIdx.x, lane = t & 31;
+  const float inv_n = 1.0f / static_cast<float>(n);
+  f32x2 dg[CH][4], db[CH][4];
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
+    const float rs = __ldg(rstd + r), mu = __ldg(mean + r);
+    const f32x2 less = pair(-mu, -mu), times = pair(rs, rs);
+    auto terms = [&](int c, f32x2(&h)[4], f32x2(&d)[4], f32x2(&g)[4]) {
+      unpack8(load_chunk<VEC>(x + r * ldx, c, n), h);
+      unpack8(load_chunk<VEC>(dy + r * lddy, c, n), d);
+      load_param<VEC>(gamma, c, n, 1.0f, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = mul2(add2(h[j], less), times);
+        g[j] = mul2(d[j], g[j]);
+      }
+    };
+    f32x2 a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 h[4], d[4], g[4];
+      terms(i * kLongThreads + t, h, d, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a2 = add2(a2, g[j]);
+        b2 = fma2(g[j], h[j], b2);
+        dg[i][j] = fma2(d[j], h[j], dg[i][j]);
+        db[i][j] = add2(db[i][j], d[j]);
+      }
+    }
+    if (dx == nullptr) continue;
+    const float a = group_sum(sum2(a2), kLongThreads, 0, slots[turn][0]) * inv_n;
+    const float b = group_sum(sum2(b2), kLongThreads, 0, slots[turn][1]) * inv_n;
+    const f32x2 less_a = pair(-a, -a), less_b = pair(-b, -b);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = i * kLongThreads + t;
+      f32x2 h[4], d[4], g[4];
+      terms(c, h, d, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = mul2(times, fma2(h[j], less_b, add2(g[j], less_a)));
+      store_chunk<VEC>(dx + r * lddx, c, n, pack8(g), lane);
+    }
+  }
+  if (part == nullptr) return;
+  float* out_g = part + int64_t(blockIdx.x) * np;
+  float* out_b = part + (int64_t(gridDim.x) + blockIdx.x) * np;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int e0 = (i * kLongThreads + t) << 3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 fg = halves(dg[i][j]), fb = halves(db[i][j]);
+      if (e0 + 2 * j < n) out_g[e0 + 2 * j] = fg.x, out_b[e0 + 2 * j] = fb.x;
+      if (e0 + 2 * j + 1 < n) out_g[e0 + 2 * j + 1] = fg.y, out_b[e0 + 2 * j + 1] = fb.y;
     }
   }
 }
@@ -466,76 +786,102 @@ int64_t round_up4(int64_t n) { return (n + 3) & ~int64_t{3}; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kWarpThreads = 256;  // of a block whose warps have a row each
+constexpr int64_t kRingWidth = 16384;  // longer rows go without the ring
 
-// Threads of a block that has a row of n columns, CH chunks of eight a thread.
-int block_threads(int64_t n, int ch) {
-  return static_cast<int>(cdiv(cdiv(n, 8 * ch), 32) * 32);
+// Threads of a group, groups of a block, shared memory and blocks for n columns: ch chunks a
+// thread, `slots` slots of `arrays` rows a group, `params` parameters staged.
+struct Shape {
+  int tpr, threads, slot_bytes, blocks;
+  size_t smem;
+};
+Shape ring_shape(int64_t rows, int64_t n, int ch, int slots, int arrays, int params, int regs,
+                 bool vec, int sms) {
+  Shape s;
+  const int64_t chunks = cdiv(n, 8);
+  s.tpr = static_cast<int>(cdiv(chunks, 32 * ch) * 32);
+  const int groups = std::max(1, 256 / s.tpr);  // at most 8
+  s.threads = groups * s.tpr;
+  s.slot_bytes = static_cast<int>((chunks + (vec ? 0 : 1)) * 16);
+  s.smem = size_t(params) * ch * s.tpr * 8 * 4 + size_t(groups) * slots * arrays * s.slot_bytes;
+  const int by_smem = static_cast<int>(size_t(tg::kSmemLimit) / (s.smem + 2048));
+  const int per_sm = std::max(1, std::min(by_smem, 65536 / (regs * s.threads)));
+  s.blocks = static_cast<int>(std::min<int64_t>(cdiv(rows, groups), int64_t(sms) * per_sm));
+  return s;
+}
+
+Shape forward_shape(int64_t rows, int64_t n, bool vec, int sms) {
+  return ring_shape(rows, n, kFwdChunks, kFwdSlots, 1, 2, vec ? 80 : 128, vec, sms);
+}
+// Two chunks and three slots where they fit; past 8192 columns a block has threads for four
+// chunks and shared memory for two slots.
+Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
+  if (n > kRingWidth) {
+    Shape s = {};
+    s.blocks = static_cast<int>(std::min<int64_t>(rows, sms));
+    return s;
+  }
+  return n <= 8192 ? ring_shape(rows, n, 2, 3, 2, 1, vec ? 104 : 120, vec, sms)
+                   : ring_shape(rows, n, 4, 2, 2, 1, 128, vec, sms);
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;  // beside the kernels' static shared memory
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(bytes));
 }
 
 template <bool VEC, typename P>
 cudaError_t forward(const void* x, const void* gamma, const void* beta, void* y, float* mean,
                     float* rstd, int64_t rows, int64_t n, int64_t ldx, int64_t ldy, float eps,
-                    int sms, cudaStream_t st) {
-  auto go = [&](auto kern, int threads, int64_t blocks) {
-    kern<<<static_cast<unsigned>(blocks), threads, 0, st>>>(
-        static_cast<const uint16_t*>(x), ldx, static_cast<const P*>(gamma),
-        static_cast<const P*>(beta), static_cast<uint16_t*>(y), ldy, mean, rstd, rows,
-        static_cast<int>(n), eps);
+                    int sms, unsigned* err, cudaStream_t st) {
+  const uint16_t* px = static_cast<const uint16_t*>(x);
+  const P *g = static_cast<const P*>(gamma), *b = static_cast<const P*>(beta);
+  uint16_t* py = static_cast<uint16_t*>(y);
+  if (n > kRingWidth) {
+    tg_layernorm_long_kernel<VEC, P><<<static_cast<unsigned>(std::min<int64_t>(rows, sms)),
+                                       kLongThreads, 0, st>>>(px, ldx, g, b, py, ldy, mean, rstd,
+                                                              rows, static_cast<int>(n), eps);
     return cudaGetLastError();
-  };
-  constexpr int kT = kWarpThreads;
-  if (n <= 512) {
-    const int64_t blocks = std::min<int64_t>(cdiv(rows, kT / 32), int64_t(sms) * 4);
-    return n <= 256 ? go(tg_layernorm_kernel<1, false, VEC, kT, P>, kT, blocks)
-                    : go(tg_layernorm_kernel<2, false, VEC, kT, P>, kT, blocks);
   }
-  if (n <= 8192) {
-    const int threads = block_threads(n, 2);
-    return go(tg_layernorm_kernel<2, true, VEC, 512, P>, threads,
-              std::min<int64_t>(rows, int64_t(sms) * std::min(16, 1024 / threads)));
-  }
-  const int threads = block_threads(n, n <= 16384 ? 4 : 8);
-  return go(n <= 16384 ? tg_layernorm_kernel<4, true, VEC, 512, P>
-                       : tg_layernorm_kernel<8, true, VEC, 512, P>,
-            threads, std::min<int64_t>(rows, int64_t(sms) * 2));
-}
-
-// Threads of a block, and blocks, of the backward pass.
-struct BackwardShape {
-  int threads, blocks;
-};
-BackwardShape backward_shape(int64_t rows, int64_t n, int sms) {
-  if (n <= 512)  // a row a warp
-    return {kWarpThreads,
-            static_cast<int>(std::min<int64_t>(cdiv(rows, kWarpThreads / 32), int64_t(sms) * 2))};
-  const int threads = block_threads(n, n <= 8192 ? 2 : 4);
-  const int per_sm = std::min(8, std::max(1, 512 / threads));
-  return {threads, static_cast<int>(std::min<int64_t>(rows, int64_t(sms) * per_sm))};
+  const Shape s = forward_shape(rows, n, VEC, sms);
+  auto kern = tg_layernorm_kernel<VEC, P>;
+  const cudaError_t e = allow_smem(kern, s.smem);
+  if (e != cudaSuccess) return e;
+  kern<<<s.blocks, s.threads, s.smem, st>>>(px, ldx, g, b, py, ldy, mean, rstd, rows,
+                                            static_cast<int>(n), eps, s.tpr, s.slot_bytes, err);
+  return cudaGetLastError();
 }
 
 template <bool VEC, typename P>
 cudaError_t backward(const void* dy, const void* x, const void* gamma, const float* mean,
                      const float* rstd, void* dx, void* dgamma, void* dbeta, float* part,
                      int64_t rows, int64_t n, int64_t lddy, int64_t ldx, int64_t lddx,
-                     const BackwardShape& s, cudaStream_t st) {
-  auto go = [&](auto kern, size_t smem) {
-    kern<<<s.blocks, s.threads, smem, st>>>(
-        static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(x), ldx,
-        static_cast<const P*>(gamma), mean, rstd, static_cast<uint16_t*>(dx), lddx, part,
-        round_up4(n), rows, static_cast<int>(n));
-    return cudaGetLastError();
-  };
-  const size_t groups = part ? size_t(kWarpThreads / 32) * 2 * round_up4(n) * 4 : 0;  // <= 32 KB
+                     const Shape& s, unsigned* err, cudaStream_t st) {
+  const uint16_t *pd = static_cast<const uint16_t*>(dy), *px = static_cast<const uint16_t*>(x);
+  const P* g = static_cast<const P*>(gamma);
+  uint16_t* out = static_cast<uint16_t*>(dx);
+  const int width = static_cast<int>(n);
+  const int64_t np = round_up4(n);
   cudaError_t e;
-  if (n <= 256) e = go(tg_layernorm_backward_kernel<1, false, VEC, kWarpThreads, P>, groups);
-  else if (n <= 512) e = go(tg_layernorm_backward_kernel<2, false, VEC, kWarpThreads, P>, groups);
-  else if (n <= 8192) e = go(tg_layernorm_backward_kernel<2, true, VEC, 512, P>, 0);
-  else if (n <= 16384) e = go(tg_layernorm_backward_kernel<4, true, VEC, 512, P>, 0);
-  else e = go(tg_layernorm_backward_kernel<4, true, VEC, 1024, P>, 0);
+  if (n > kRingWidth) {
+    tg_layernorm_backward_long_kernel<VEC, P><<<s.blocks, kLongThreads, 0, st>>>(
+        pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, rows, width);
+    e = cudaGetLastError();
+  } else {
+    auto go = [&](auto kern) {
+      const cudaError_t a = allow_smem(kern, s.smem);
+      if (a != cudaSuccess) return a;
+      kern<<<s.blocks, s.threads, s.smem, st>>>(pd, lddy, px, ldx, g, mean, rstd, out, lddx, part,
+                                                np, rows, width, s.tpr, s.slot_bytes, err);
+      return cudaGetLastError();
+    };
+    e = n <= 8192 ? go(tg_layernorm_backward_kernel<2, 3, VEC, P>)
+                  : go(tg_layernorm_backward_kernel<4, 2, VEC, P>);
+  }
   if (e != cudaSuccess || part == nullptr) return e;
   tg_layernorm_params_kernel<P><<<static_cast<unsigned>(cdiv(n, 32)), dim3(8, kPartRows), 0, st>>>(
-      part, s.blocks, round_up4(n), static_cast<int>(n), static_cast<P*>(dgamma), static_cast<P*>(dbeta));
+      part, s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
   return cudaGetLastError();
 }
 
@@ -570,7 +916,7 @@ tg_status tg_layernorm_f16(const void* X, const void* gamma, const void* beta, v
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool vec = aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
                    ldx % 8 == 0 && ldy % 8 == 0 && N % 8 == 0;
-  auto run = [&](auto f) { return f(X, gamma, beta, Y, mean, rstd, M, N, ldx, ldy, eps, sms, s); };
+  auto run = [&](auto f) { return f(X, gamma, beta, Y, mean, rstd, M, N, ldx, ldy, eps, sms, err, s); };
   const cudaError_t e = param_type == TG_TYPE_F16
                             ? (vec ? run(forward<true, __half>) : run(forward<false, __half>))
                             : (vec ? run(forward<true, float>) : run(forward<false, float>));
@@ -603,16 +949,16 @@ tg_status tg_layernorm_backward_f16(const void* dY, const void* X, const void* g
         return tg::record_cuda_error(e);
     return TG_OK;
   }
-  const BackwardShape shape = backward_shape(M, N, sms);
+  const bool vec = aligned16(dY) && aligned16(X) && aligned16(dX) && aligned16(gamma) &&
+                   lddy % 8 == 0 && ldx % 8 == 0 && (!dX || lddx % 8 == 0) && N % 8 == 0;
+  const Shape shape = backward_shape(M, N, vec, sms);
   float* part = nullptr;
   if (dgamma || dbeta) {
     st = tg::scratch_alloc(size_t(2) * shape.blocks * round_up4(N) * 4, s, reinterpret_cast<void**>(&part));
     if (st != TG_OK) return st;
   }
-  const bool vec = aligned16(dY) && aligned16(X) && aligned16(dX) && aligned16(gamma) &&
-                   lddy % 8 == 0 && ldx % 8 == 0 && (!dX || lddx % 8 == 0) && N % 8 == 0;
   auto run = [&](auto f) {
-    return f(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, part, M, N, lddy, ldx, lddx, shape, s);
+    return f(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, part, M, N, lddy, ldx, lddx, shape, err, s);
   };
   e = param_type == TG_TYPE_F16 ? (vec ? run(backward<true, __half>) : run(backward<false, __half>))
                                 : (vec ? run(backward<true, float>) : run(backward<false, float>));
