@@ -195,14 +195,6 @@ __device__ __forceinline__ void load_param(const P* p, int c, int n, float none,
   for (int i = 0; i < 4; ++i) f[i] = pair(g[2 * i], g[2 * i + 1]);
 }
 
-// 1 for the columns 8c .. 8c + 7 that a row of n has, 0 for the others (VEC: all or none).
-template <bool VEC>
-__device__ __forceinline__ f32x2 there(int c, int n, int i) {
-  const int e0 = c << 3;
-  if constexpr (VEC) return e0 < n ? pair(1.0f, 1.0f) : pair(0.0f, 0.0f);
-  return pair(e0 + 2 * i < n ? 1.0f : 0.0f, e0 + 2 * i + 1 < n ? 1.0f : 0.0f);
-}
-
 // ---------------------------------------------------------------------------------------
 // Rows through shared memory.  A group of threads (a warp, or several) works on one row at a time;
 // its first thread fetches rows ahead into a ring of slots with bulk copies, so the next rows'
@@ -271,40 +263,52 @@ __device__ __forceinline__ void slot_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
-// Elements [8c, 8c + 8) of the row in a slot, zeros from n on; b: bytes from the slot's start to the
-// row's.
-template <bool VEC>
-__device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int c, int n) {
-  const int e0 = c << 3;
-  if (e0 >= n) return make_uint4(0, 0, 0, 0);
-  const uint4* blk = reinterpret_cast<const uint4*>(slot) + c;
-  if (VEC) return *blk;
-  const uint4 lo = blk[0], hi = blk[1];
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const uint32_t q = b >> 2;
-  uint32_t t[7], u[5], o[4];
-#pragma unroll
-  for (int i = 0; i < 7; ++i) t[i] = (q & 1u) ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) u[i] = (q & 2u) ? t[i + 2] : t[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (b & 2u) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
-  if (e0 + 8 > n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (e0 + 2 * i >= n) o[i] = 0u;
-      else if (e0 + 2 * i + 1 >= n) o[i] &= 0xFFFFu;
-    }
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+// 1 for the columns `col` and `col` + 1 that a row of n has, 0 for the others.
+__device__ __forceinline__ f32x2 there(int col, int n) {
+  return pair(col < n ? 1.0f : 0.0f, col + 1 < n ? 1.0f : 0.0f);
 }
 
-// The threads of a group meet (id: the group's number in the block).
+// Elements [8c, 8c + 8) of the row in a slot, zeros from n on; b: bytes from the slot's start to the
+// row's (0 with VEC).  Otherwise the two blocks that hold them are shifted together: with 4-byte
+// reads at the row's own offset, a warp's pairs contiguous, 8192 x 4096 forward took 63 us, not 37.
+template <bool VEC>
+__device__ __forceinline__ void slot_chunk(const uint8_t* slot, uint32_t b, int c, int n,
+                                           f32x2 (&f)[4]) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  const int e0 = c << 3;
+  if (e0 < n) {
+    const uint4* blk = reinterpret_cast<const uint4*>(slot) + c;
+    v = blk[0];
+    if constexpr (!VEC) {
+      const uint4 hi = blk[1];
+      const uint32_t w[8] = {v.x, v.y, v.z, v.w, hi.x, hi.y, hi.z, hi.w};
+      const uint32_t q = b >> 2;
+      uint32_t t[7], u[5], o[4];
+#pragma unroll
+      for (int i = 0; i < 7; ++i) t[i] = (q & 1u) ? w[i + 1] : w[i];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) u[i] = (q & 2u) ? t[i + 2] : t[i];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = (b & 2u) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+      if (e0 + 8 > n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (e0 + 2 * i >= n) o[i] = 0u;
+          else if (e0 + 2 * i + 1 >= n) o[i] &= 0xFFFFu;
+        }
+      }
+      v = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  unpack8(v, f);
+}
+
+// The threads of a group meet (id: the group's number in the block).  barrier.sync, not bar.sync:
+// the latter counts a whole warp each time that any of its threads comes by, and a warp's threads
+// may come apart (waits, row ends, the first lane's fetch).
 __device__ __forceinline__ void group_sync(int tpr, int id) {
-  if (tpr == 32)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(tpr) : "memory");
+  __syncwarp();
+  if (tpr > 32) asm volatile("barrier.sync %0, %1;" ::"r"(id + 1), "r"(tpr) : "memory");
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -316,10 +320,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Sum over a group; slots: a float for each of its warps, not in use by the call before.
 __device__ __forceinline__ float group_sum(float v, int tpr, int id, float* slots) {
   v = warp_sum(v);
-  if (tpr == 32) {
-    __syncwarp();
-    return v;
-  }
+  if (tpr == 32) return v;
   const int wpr = tpr >> 5, lane = threadIdx.x & 31;
   if (lane == 0) slots[(threadIdx.x >> 5) - id * wpr] = v;
   group_sync(tpr, id);
@@ -341,8 +342,8 @@ __device__ __forceinline__ void stage_param(float* dst, const P* p, int n, int c
   }
 }
 __device__ __forceinline__ void staged(const float* src, int c, int chunks, f32x2 (&f)[4]) {
-  const ulonglong2* q = reinterpret_cast<const ulonglong2*>(src);
-  const ulonglong2 a = q[c], b = q[chunks + c];
+  const ulonglong2* q = reinterpret_cast<const ulonglong2*>(src) + c;
+  const ulonglong2 a = q[0], b = q[chunks];
   f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 
@@ -355,11 +356,13 @@ __device__ __forceinline__ uint32_t row_shift(const uint16_t* p, int64_t ld, int
 constexpr int kFwdChunks = 4, kFwdSlots = 2;
 
 // Forward, kFwdChunks chunks a thread: 32 elements share the reductions' and the loop's cost.
-template <bool VEC, typename P>
-__global__ void __launch_bounds__(512)
+// 16384 x 4096 took 45 us, 0.88 of the copy rate (a row a warp in registers 59, two chunks a thread
+// from global memory 59).
+template <int THREADS, int BLOCKS, bool VEC, typename P>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
     tg_layernorm_kernel(const uint16_t* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
                         const P* __restrict__ beta, uint16_t* __restrict__ y, int64_t ldy,
-                        float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int n,
+                        float* __restrict__ mean, float* __restrict__ rstd, int rows, int n,
                         float eps, int tpr, int slot_bytes, unsigned* err) {
   constexpr int CH = kFwdChunks, S = kFwdSlots;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -370,12 +373,12 @@ __global__ void __launch_bounds__(512)
   const int per_block = blockDim.x / tpr, chunks = CH * tpr;
   float* sg = reinterpret_cast<float*>(smem);
   float* so = sg + chunks * 8;
-  uint8_t* ring = reinterpret_cast<uint8_t*>(so + chunks * 8) + int64_t(group) * S * slot_bytes;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(so + chunks * 8) + group * S * slot_bytes;
   const Span sp = span_of(x, ldx, rows, n);
-  const int64_t step = int64_t(gridDim.x) * per_block;
-  int64_t r = blockIdx.x * int64_t(per_block) + group;
-  auto fetch = [&](int64_t row, int s) {
-    const uint16_t* src = x + row * ldx;
+  const int step = gridDim.x * per_block, first = blockIdx.x * per_block + group;
+  const int count = first < rows ? (rows - 1 - first) / step + 1 : 0;  // rows of this group
+  auto fetch = [&](int k, int s) {
+    const uint16_t* src = x + (first + int64_t(k) * step) * ldx;
     const uint32_t bar = tg::smem_u32(&bars[group][s]);
     const Fetch f = plan_fetch<VEC>(src, n, sp);
     uint8_t* slot = ring + s * slot_bytes;
@@ -387,37 +390,39 @@ __global__ void __launch_bounds__(512)
   if (t == 0) {
     for (int s = 0; s < S; ++s) tg::mbar_init(tg::smem_u32(&bars[group][s]), 1);
     tg::fence_mbar_init();
-    for (int s = 0; s < S; ++s)
-      if (r + s * step < rows) fetch(r + s * step, s);
+    for (int s = 0; s < S && s < count; ++s) fetch(s, s);
   }
   stage_param<VEC>(sg, gamma, n, chunks, 1.0f);
   stage_param<VEC>(so, beta, n, chunks, 0.0f);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
-  for (int k = 0; r < rows; r += step, ++k) {
+  const int64_t y_step = int64_t(step) * ldy;
+  uint16_t* yr = y + first * ldy;
+  unsigned r = first;
+  for (int k = 0; k < count; ++k, r += step, yr += y_step) {
     const int s = k & 1;
     slot_wait(tg::smem_u32(&bars[group][s]), (k >> 1) & 1, &late, err);
     const uint32_t b = VEC ? 0u : row_shift(x, ldx, r);
     f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      unpack8(slot_chunk<VEC>(ring + s * slot_bytes, b, i * tpr + t, n), v[i]);
+      slot_chunk<VEC>(ring + s * slot_bytes, b, i * tpr + t, n, v[i]);
       acc = add2(acc, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
     }
     const float mu = group_sum(sum2(acc), tpr, group, sums[group][0]) * inv_n;
-    if (t == 0 && r + S * step < rows) fetch(r + S * step, s);  // everyone has read this slot
+    if (t == 0 && k + S < count) fetch(k + S, s);  // everyone has read this slot
     const f32x2 less = pair(-mu, -mu);
     f32x2 q = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = i * tpr + t;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const int col = ((i * tpr + t) << 3) + 2 * j;
         v[i][j] = add2(v[i][j], less);
-        if (VEC) {
-          if (c * 8 < n) q = fma2(v[i][j], v[i][j], q);
+        if (VEC || col + 1 < n) {
+          if (col < n) q = fma2(v[i][j], v[i][j], q);
         } else {
-          const f32x2 d = mul2(v[i][j], there<VEC>(c, n, j));
+          const f32x2 d = mul2(v[i][j], there(col, n));
           q = fma2(d, d, q);
         }
       }
@@ -428,44 +433,52 @@ __global__ void __launch_bounds__(512)
       if (rstd) rstd[r] = rs;
     }
     const f32x2 times = pair(rs, rs);
-    uint16_t* yr = y + r * ldy;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = i * tpr + t;
       f32x2 g[4], o[4];
-      staged(sg, c, chunks, g);
-      staged(so, c, chunks, o);
+      staged(sg, i * tpr + t, chunks, g);
+      staged(so, i * tpr + t, chunks, o);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], times), g[j], o[j]);
-      store_chunk<VEC>(yr, c, n, pack8(o), lane);
+      store_chunk<VEC>(yr, i * tpr + t, n, pack8(o), lane);
     }
   }
+}
+
+// Sums of two values over a warp: the first ends in the lower 16 lanes, the second in the upper.
+__device__ __forceinline__ float warp_sum_two(float a, float b, int lane) {
+  const bool up = lane & 16;
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
 }
 
 // Backward, CH chunks a thread.  A thread keeps the same columns for all of its rows, so its part
 // of dgamma and dbeta stays in registers, and each block writes one partial row of both (of np
 // floats): part[0][block], part[1][block].  The row's two sums are needed before its dx, so the
-// loop works on two rows: it sums row i + 1 while it writes dx of row i, and meets once a row.
+// loop works on two rows: it sums row k + 1 while it writes dx of row k, and meets once a row.
 template <int CH, int S, bool VEC, typename P>
 __global__ void __launch_bounds__(512)
     tg_layernorm_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                  const uint16_t* __restrict__ x, int64_t ldx,
                                  const P* __restrict__ gamma, const float* __restrict__ mean,
                                  const float* __restrict__ rstd, uint16_t* __restrict__ dx,
-                                 int64_t lddx, float* __restrict__ part, int64_t np, int64_t rows,
+                                 int64_t lddx, float* __restrict__ part, int64_t np, int rows,
                                  int n, int tpr, int slot_bytes, unsigned* err) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
-  __shared__ float2 sums[8][2][16];
+  __shared__ float sums[8][2][32];  // [group][row's turn][of g: 16 warps, of g u: 16 warps]
   __shared__ volatile int late;
   const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, lane = threadIdx.x & 31;
   const int per_block = blockDim.x / tpr, chunks = CH * tpr, wpr = tpr >> 5;
   float* sg = reinterpret_cast<float*>(smem);
-  uint8_t* ring = reinterpret_cast<uint8_t*>(sg + chunks * 8) + int64_t(group) * S * 2 * slot_bytes;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(sg + chunks * 8) + group * S * 2 * slot_bytes;
   const Span sx = span_of(x, ldx, rows, n), sd = span_of(dy, lddy, rows, n);
-  const int64_t step = int64_t(gridDim.x) * per_block;
-  const int64_t first = blockIdx.x * int64_t(per_block) + group;
-  auto fetch = [&](int64_t row, int s) {
+  const int step = gridDim.x * per_block, first = blockIdx.x * per_block + group;
+  const int count = first < rows ? (rows - 1 - first) / step + 1 : 0;  // rows of this group
+  auto fetch = [&](int k, int s) {
+    const int64_t row = first + int64_t(k) * step;
     const uint32_t bar = tg::smem_u32(&bars[group][s]);
     const uint16_t *px = x + row * ldx, *pd = dy + row * lddy;
     const Fetch fx = plan_fetch<VEC>(px, n, sx), fd = plan_fetch<VEC>(pd, n, sd);
@@ -480,8 +493,7 @@ __global__ void __launch_bounds__(512)
   if (t == 0) {
     for (int s = 0; s < S; ++s) tg::mbar_init(tg::smem_u32(&bars[group][s]), 1);
     tg::fence_mbar_init();
-    for (int s = 0; s < S; ++s)
-      if (first + s * step < rows) fetch(first + s * step, s);
+    for (int s = 0; s < S && s < count; ++s) fetch(s, s);
   }
   stage_param<VEC>(sg, gamma, n, chunks, 1.0f);
   __syncthreads();
@@ -491,91 +503,92 @@ __global__ void __launch_bounds__(512)
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
-  // u = x - mean, d = dy and gamma of chunk i of the row in slot s; past the row's end d is 0
-  auto terms = [&](int s, int64_t row, int i, float mu, f32x2(&u)[4], f32x2(&d)[4], f32x2(&g)[4]) {
-    const uint8_t* slot = ring + s * 2 * slot_bytes;
+  // x, d = dy and gamma of the row in a slot; past the row's end d is 0
+  auto terms = [&](const uint8_t* slot, unsigned row, int i, f32x2(&v)[4], f32x2(&d)[4],
+                   f32x2(&g)[4]) {
     const int c = i * tpr + t;
-    const uint32_t bx = VEC ? 0u : row_shift(x, ldx, row), bd = VEC ? 0u : row_shift(dy, lddy, row);
-    unpack8(slot_chunk<VEC>(slot, bx, c, n), u);
-    unpack8(slot_chunk<VEC>(slot + slot_bytes, bd, c, n), d);
+    slot_chunk<VEC>(slot, VEC ? 0u : row_shift(x, ldx, row), c, n, v);
+    slot_chunk<VEC>(slot + slot_bytes, VEC ? 0u : row_shift(dy, lddy, row), c, n, d);
     staged(sg, c, chunks, g);
-    const f32x2 less = pair(-mu, -mu);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = add2(u[j], less);
   };
-  // With h = u rstd and g = d gamma: the sums of g and of g u (= g h / rstd) of row `row`, the k-th
-  // of this group, into sums[k & 1], and the row's part of dgamma (d u, times rstd) and dbeta
-  auto sum_row = [&](int k, int64_t row, float mu, float rs) {
-    const int s = k % S;
-    slot_wait(tg::smem_u32(&bars[group][s]), (k / S) & 1, &late, err);
-    const f32x2 times = pair(rs, rs);
+  // With u = x - mean, h = u rstd and g = d gamma: this thread's part of the sums of g and of g u (= g h / rstd)
+  // of a row, into sums[turn], and the row's part of dgamma (d u, times rstd) and dbeta
+  auto sum_row = [&](const uint8_t* slot, unsigned row, float mu, float rs, int turn) {
+    const f32x2 less = pair(-mu, -mu), times = pair(rs, rs);
     f32x2 a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      f32x2 u[4], d[4], g[4];
-      terms(s, row, i, mu, u, d, g);
+      f32x2 v[4], d[4], g[4];
+      terms(slot, row, i, v, d, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x2 du = mul2(d[j], u[j]);
+        const f32x2 du = mul2(d[j], add2(v[j], less));
         a2 = fma2(d[j], g[j], a2);
         b2 = fma2(du, g[j], b2);
         dg[i][j] = fma2(du, times, dg[i][j]);
         db[i][j] = add2(db[i][j], d[j]);
       }
     }
-    float a = sum2(a2), b = sum2(b2);
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, w);
-      b += __shfl_xor_sync(0xffffffffu, b, w);
-    }
-    if (lane == 0) sums[group][k & 1][(threadIdx.x >> 5) - group * wpr] = make_float2(a, b);
+    const float v = warp_sum_two(sum2(a2), sum2(b2), lane);
+    if ((lane & 15) == 0) sums[group][turn][(lane & 16) + (t >> 5)] = v;
   };
+  const float *pm = mean + first, *pr = rstd + first;
   float mu = 0.0f, rs = 0.0f, mu1 = 0.0f, rs1 = 0.0f;
-  if (first < rows) {
-    mu = __ldg(mean + first);
-    rs = __ldg(rstd + first);
-    if (first + step < rows) {
-      mu1 = __ldg(mean + first + step);
-      rs1 = __ldg(rstd + first + step);
+  if (count > 0) {
+    mu = __ldg(pm);
+    rs = __ldg(pr);
+    if (count > 1) {
+      mu1 = __ldg(pm + step);
+      rs1 = __ldg(pr + step);
     }
-    sum_row(0, first, mu, rs);
+    slot_wait(tg::smem_u32(&bars[group][0]), 0, &late, err);
+    sum_row(ring, first, mu, rs, 0);
   }
   group_sync(tpr, group);
-  int64_t r = first;
+  const int64_t dx_step = int64_t(step) * lddx;
   uint16_t* dxr = dx + first * lddx;
-  for (int k = 0; r < rows; r += step, ++k) {
+  int s = 0, s1 = 1;     // the slots of rows k and k + 1
+  uint32_t phase1 = 0;   // of slot s1
+  unsigned r = first;
+  for (int k = 0; k < count; ++k, r += step, dxr += dx_step) {
+    pm += step;
+    pr += step;
     float mu2 = 0.0f, rs2 = 0.0f;
-    if (r + 2 * step < rows) {
-      mu2 = __ldg(mean + r + 2 * step);
-      rs2 = __ldg(rstd + r + 2 * step);
+    if (k + 2 < count) {
+      mu2 = __ldg(pm + step);
+      rs2 = __ldg(pr + step);
     }
-    if (r + step < rows) sum_row(k + 1, r + step, mu1, rs1);
+    if (k + 1 < count) {
+      slot_wait(tg::smem_u32(&bars[group][s1]), phase1, &late, err);
+      sum_row(ring + s1 * 2 * slot_bytes, r + step, mu1, rs1, (k + 1) & 1);
+    }
     if (dx != nullptr) {
-      // dx = rstd (g - mean(g) - h mean(g h)) = d (gamma rstd) + u (-rstd^3 mean(g u)) - rstd mean(g)
-      float2 p = lane < wpr ? sums[group][k & 1][lane] : make_float2(0.0f, 0.0f);
+      // dx = rstd (g - mean(g) - h mean(g h)) = d (gamma rstd) + x c1 + c0 with
+      // c1 = -rstd^3 mean(g u) and c0 = -rstd mean(g) - mean c1.  (Left uncentred, x c1 + c0 is off
+      // by 2^-24 |mean| / spread of its size, far below dx's rounding to fp16.)
+      float v = (lane & 15) < wpr ? sums[group][k & 1][lane] : 0.0f;
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) {
-        p.x += __shfl_xor_sync(0xffffffffu, p.x, w);
-        p.y += __shfl_xor_sync(0xffffffffu, p.y, w);
-      }
-      p.x = __shfl_sync(0xffffffffu, p.x, 0);
-      p.y = __shfl_sync(0xffffffffu, p.y, 0);
-      const float c1 = -rs * rs * rs * (p.y * inv_n), c0 = -rs * (p.x * inv_n);
-      const f32x2 of_u = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
+      for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      const float a = __shfl_sync(0xffffffffu, v, 0), b = __shfl_sync(0xffffffffu, v, 16);
+      const float c1 = -rs * rs * rs * (b * inv_n), c0 = fmaf(-mu, c1, -rs * (a * inv_n));
+      const f32x2 of_x = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        f32x2 u[4], d[4], g[4];
-        terms(k % S, r, i, mu, u, d, g);
+        f32x2 v[4], d[4], g[4];
+        terms(ring + s * 2 * slot_bytes, r, i, v, d, g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = fma2(d[j], mul2(g[j], times), fma2(u[j], of_u, plus));
+        for (int j = 0; j < 4; ++j) g[j] = fma2(d[j], mul2(g[j], times), fma2(v[j], of_x, plus));
         store_chunk<VEC>(dxr, i * tpr + t, n, pack8(g), lane);
       }
     }
-    dxr += step * lddx;
     mu = mu1, rs = rs1, mu1 = mu2, rs1 = rs2;
-    group_sync(tpr, group);  // slot k % S and sums[k & 1] are free, sums[(k + 1) & 1] is written
-    if (t == 0 && r + S * step < rows) fetch(r + S * step, k % S);
+    group_sync(tpr, group);  // slot s and sums[k & 1] are free, sums[(k + 1) & 1] is written
+    if (t == 0 && k + S < count) fetch(k + S, s);
+    s = s1;
+    if (++s1 == S) {
+      s1 = 0;
+      phase1 ^= 1;
+    }
   }
   if (part == nullptr) return;
   // the block's groups are added in their order; the ring is empty by now
@@ -587,12 +600,12 @@ __global__ void __launch_bounds__(512)
   float* to_b = per_block == 1 ? out_b : to_g + np;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int e0 = (i * tpr + t) << 3;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      const int e = ((i * tpr + t) << 3) + 2 * j;
       const float2 fg = halves(dg[i][j]), fb = halves(db[i][j]);
-      if (e0 + 2 * j < n) to_g[e0 + 2 * j] = fg.x, to_b[e0 + 2 * j] = fb.x;
-      if (e0 + 2 * j + 1 < n) to_g[e0 + 2 * j + 1] = fg.y, to_b[e0 + 2 * j + 1] = fb.y;
+      if (e < n) to_g[e] = fg.x, to_b[e] = fb.x;
+      if (e + 1 < n) to_g[e + 1] = fg.y, to_b[e + 1] = fb.y;
     }
   }
   if (per_block == 1) return;
@@ -609,45 +622,67 @@ __global__ void __launch_bounds__(512)
 }
 
 // ---------------------------------------------------------------------------------------
-// Rows of more than 16384 columns, whose ring would not fit in shared memory: a row a block,
-// straight from global memory.
+// Rows straight from global memory, where the ring does not pay or does not fit: up to 512 columns
+// a row a warp (the ring's waits and copies cost more than so short a row: 100000 x 128 forward 63
+// against 20 us, 32768 x 512 backward 36 against 32 us), more than 16384 a row a block of 1024.
+// With CH <= 2 chunks a thread the next row is loaded before the current one is worked on, and the
+// parameters stay in registers; a longer row is read a second time for dx, from L2.
 // ---------------------------------------------------------------------------------------
-constexpr int kLongThreads = 1024, kLongChunks = 4;
+constexpr int kNarrowThreads = 256, kLongThreads = 1024, kLongChunks = 4;
 
-template <bool VEC, typename P>
-__global__ void __launch_bounds__(kLongThreads)
-    tg_layernorm_long_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                             const P* __restrict__ gamma, const P* __restrict__ beta,
-                             uint16_t* __restrict__ y, int64_t ldy, float* __restrict__ mean,
-                             float* __restrict__ rstd, int64_t rows, int n, float eps) {
-  constexpr int CH = kLongChunks;
+template <int CH, bool BLOCK, bool VEC, int THREADS, typename P>
+__global__ void __launch_bounds__(THREADS)
+    tg_layernorm_direct_kernel(const uint16_t* __restrict__ x, int64_t ldx,
+                               const P* __restrict__ gamma, const P* __restrict__ beta,
+                               uint16_t* __restrict__ y, int64_t ldy, float* __restrict__ mean,
+                               float* __restrict__ rstd, int64_t rows, int n, float eps) {
   __shared__ float slots[2][32];
-  const int t = threadIdx.x, lane = t & 31;
+  constexpr bool kKeep = CH <= 2;
+  constexpr int tpr = BLOCK ? THREADS : 32;  // threads of a row
+  const int lane = threadIdx.x & 31, t = BLOCK ? threadIdx.x : lane;
+  const int64_t step = BLOCK ? gridDim.x : int64_t(gridDim.x) * (THREADS >> 5);
+  int64_t r = BLOCK ? blockIdx.x : blockIdx.x * int64_t(THREADS >> 5) + (threadIdx.x >> 5);
   const float inv_n = 1.0f / static_cast<float>(n);
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    uint4 v[CH];
-    f32x2 s = pair(0.0f, 0.0f), q = s;
+  uint4 next[CH];
+  auto load = [&](int64_t row) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) v[i] = load_chunk<VEC>(x + r * ldx, i * kLongThreads + t, n);
+    for (int i = 0; i < CH; ++i) next[i] = load_chunk<VEC>(x + row * ldx, i * tpr + t, n);
+  };
+  if (kKeep && r < rows) load(r);
+  f32x2 g[kKeep ? CH : 1][4], o[kKeep ? CH : 1][4];
+  if constexpr (kKeep) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      f32x2 f[4];
-      unpack8(v[i], f);
-      s = add2(s, add2(add2(f[0], f[1]), add2(f[2], f[3])));
+      load_param<VEC>(gamma, i * tpr + t, n, 1.0f, g[i]);
+      load_param<VEC>(beta, i * tpr + t, n, 0.0f, o[i]);
     }
-    const float mu = group_sum(sum2(s), kLongThreads, 0, slots[0]) * inv_n;
+  }
+  for (; r < rows; r += step) {
+    uint4 now[CH];
+    if constexpr (!kKeep) load(r);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) now[i] = next[i];
+    if (kKeep && r + step < rows) load(r + step);
+    f32x2 s = pair(0.0f, 0.0f), q = s;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 v[4];
+      unpack8(now[i], v);
+      s = add2(s, add2(add2(v[0], v[1]), add2(v[2], v[3])));
+    }
+    const float mu = group_sum(sum2(s), tpr, 0, slots[0]) * inv_n;
     const f32x2 less = pair(-mu, -mu);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      f32x2 f[4];
-      unpack8(v[i], f);
+      f32x2 v[4];
+      unpack8(now[i], v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x2 d = mul2(add2(f[j], less), there<VEC>(i * kLongThreads + t, n, j));
+        const f32x2 d = mul2(add2(v[j], less), there(((i * tpr + t) << 3) + 2 * j, n));
         q = fma2(d, d, q);
       }
     }
-    const float rs = rsqrtf(group_sum(sum2(q), kLongThreads, 0, slots[1]) * inv_n + eps);
+    const float rs = rsqrtf(group_sum(sum2(q), tpr, 0, slots[1]) * inv_n + eps);
     if (t == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
@@ -655,88 +690,141 @@ __global__ void __launch_bounds__(kLongThreads)
     const f32x2 times = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = i * kLongThreads + t;
-      f32x2 f[4], g[4], o[4];
-      unpack8(v[i], f);
-      load_param<VEC>(gamma, c, n, 1.0f, g);
-      load_param<VEC>(beta, c, n, 0.0f, o);
+      const int c = i * tpr + t, k = kKeep ? i : 0;
+      if constexpr (!kKeep) {
+        load_param<VEC>(gamma, c, n, 1.0f, g[0]);
+        load_param<VEC>(beta, c, n, 0.0f, o[0]);
+      }
+      f32x2 v[4];
+      unpack8(now[i], v);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(add2(f[j], less), times), g[j], o[j]);
-      store_chunk<VEC>(y + r * ldy, c, n, pack8(o), lane);
+      for (int j = 0; j < 4; ++j) v[j] = fma2(mul2(add2(v[j], less), times), g[k][j], o[k][j]);
+      store_chunk<VEC>(y + r * ldy, c, n, pack8(v), lane);
     }
   }
 }
 
-// The row is read a second time for dx, from L2.
-template <bool VEC, typename P>
-__global__ void __launch_bounds__(kLongThreads)
-    tg_layernorm_backward_long_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
-                                      const uint16_t* __restrict__ x, int64_t ldx,
-                                      const P* __restrict__ gamma, const float* __restrict__ mean,
-                                      const float* __restrict__ rstd, uint16_t* __restrict__ dx,
-                                      int64_t lddx, float* __restrict__ part, int64_t np,
-                                      int64_t rows, int n) {
-  constexpr int CH = kLongChunks;
+template <int CH, bool BLOCK, bool VEC, int THREADS, typename P>
+__global__ void __launch_bounds__(THREADS)
+    tg_layernorm_backward_direct_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
+                                        const uint16_t* __restrict__ x, int64_t ldx,
+                                        const P* __restrict__ gamma,
+                                        const float* __restrict__ mean,
+                                        const float* __restrict__ rstd, uint16_t* __restrict__ dx,
+                                        int64_t lddx, float* __restrict__ part, int64_t np,
+                                        int64_t rows, int n) {
+  extern __shared__ float groups[];  // a row a warp: [warps][2][np]
   __shared__ float slots[2][2][32];
-  const int t = threadIdx.x, lane = t & 31;
+  constexpr bool kKeep = CH <= 2;
+  constexpr int kHold = kKeep ? CH : 1;
+  constexpr int tpr = BLOCK ? THREADS : 32;
+  const int lane = threadIdx.x & 31, t = BLOCK ? threadIdx.x : lane;
+  const int64_t step = BLOCK ? gridDim.x : int64_t(gridDim.x) * (THREADS >> 5);
+  int64_t r = BLOCK ? blockIdx.x : blockIdx.x * int64_t(THREADS >> 5) + (threadIdx.x >> 5);
   const float inv_n = 1.0f / static_cast<float>(n);
   f32x2 dg[CH][4], db[CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
-  int turn = 0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
-    const float rs = __ldg(rstd + r), mu = __ldg(mean + r);
-    const f32x2 less = pair(-mu, -mu), times = pair(rs, rs);
-    auto terms = [&](int c, f32x2(&h)[4], f32x2(&d)[4], f32x2(&g)[4]) {
-      unpack8(load_chunk<VEC>(x + r * ldx, c, n), h);
-      unpack8(load_chunk<VEC>(dy + r * lddy, c, n), d);
-      load_param<VEC>(gamma, c, n, 1.0f, g);
+  uint4 next_x[kHold], next_dy[kHold];
+  float next_mu = 0.0f, next_rs = 0.0f;
+  auto load = [&](int64_t row) {
+    if constexpr (kKeep) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = mul2(add2(h[j], less), times);
-        g[j] = mul2(d[j], g[j]);
+      for (int i = 0; i < CH; ++i) {
+        next_x[i] = load_chunk<VEC>(x + row * ldx, i * tpr + t, n);
+        next_dy[i] = load_chunk<VEC>(dy + row * lddy, i * tpr + t, n);
       }
-    };
-    f32x2 a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
+    }
+    next_mu = __ldg(mean + row);
+    next_rs = __ldg(rstd + row);
+  };
+  if (r < rows) load(r);
+  f32x2 gm[kHold][4];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) load_param<VEC>(gamma, i * tpr + t, n, 1.0f, gm[i]);
+  }
+  // h, d = dy and g = d gamma of chunk i of a row; past the row's end d, and with it g, is 0
+  auto terms = [&](int64_t row, int i, f32x2 less, f32x2 times, f32x2(&h)[4], f32x2(&d)[4],
+                   f32x2(&g)[4]) {
+    const int c = i * tpr + t, k = kKeep ? i : 0;
+    if constexpr (!kKeep) {
+      next_x[0] = load_chunk<VEC>(x + row * ldx, c, n);
+      next_dy[0] = load_chunk<VEC>(dy + row * lddy, c, n);
+      load_param<VEC>(gamma, c, n, 1.0f, gm[0]);
+    }
+    unpack8(next_x[k], h);
+    unpack8(next_dy[k], d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = mul2(add2(h[j], less), times);
+      g[j] = mul2(d[j], gm[k][j]);
+    }
+  };
+  for (int turn = 0; r < rows; r += step, turn ^= 1) {
+    const float rs = next_rs;
+    const f32x2 less = pair(-next_mu, -next_mu), times = pair(rs, rs);
+    f32x2 h[kHold][4], g[kHold][4], a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      f32x2 h[4], d[4], g[4];
-      terms(i * kLongThreads + t, h, d, g);
+      const int k = kKeep ? i : 0;
+      f32x2 d[4];
+      terms(r, i, less, times, h[k], d, g[k]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a2 = add2(a2, g[j]);
-        b2 = fma2(g[j], h[j], b2);
-        dg[i][j] = fma2(d[j], h[j], dg[i][j]);
+        a2 = add2(a2, g[k][j]);
+        b2 = fma2(g[k][j], h[k][j], b2);
+        dg[i][j] = fma2(d[j], h[k][j], dg[i][j]);
         db[i][j] = add2(db[i][j], d[j]);
       }
     }
-    if (dx == nullptr) continue;
-    const float a = group_sum(sum2(a2), kLongThreads, 0, slots[turn][0]) * inv_n;
-    const float b = group_sum(sum2(b2), kLongThreads, 0, slots[turn][1]) * inv_n;
-    const f32x2 less_a = pair(-a, -a), less_b = pair(-b, -b);
+    if (r + step < rows) load(r + step);
+    if (dx != nullptr) {
+      const float a = group_sum(sum2(a2), tpr, 0, slots[turn][0]) * inv_n;
+      const float b = group_sum(sum2(b2), tpr, 0, slots[turn][1]) * inv_n;
+      const f32x2 less_a = pair(-a, -a), less_b = pair(-b, -b);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = i * kLongThreads + t;
-      f32x2 h[4], d[4], g[4];
-      terms(c, h, d, g);
+      for (int i = 0; i < CH; ++i) {
+        const int k = kKeep ? i : 0;
+        if constexpr (!kKeep) {
+          f32x2 d[4];
+          terms(r, i, less, times, h[0], d, g[0]);
+        }
+        f32x2 out[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = mul2(times, fma2(h[j], less_b, add2(g[j], less_a)));
-      store_chunk<VEC>(dx + r * lddx, c, n, pack8(g), lane);
+        for (int j = 0; j < 4; ++j)
+          out[j] = mul2(times, fma2(h[k][j], less_b, add2(g[k][j], less_a)));
+        store_chunk<VEC>(dx + r * lddx, i * tpr + t, n, pack8(out), lane);
+      }
     }
   }
   if (part == nullptr) return;
   float* out_g = part + int64_t(blockIdx.x) * np;
   float* out_b = part + (int64_t(gridDim.x) + blockIdx.x) * np;
+  float* to_g = BLOCK ? out_g : groups + int64_t(threadIdx.x >> 5) * 2 * np;
+  float* to_b = BLOCK ? out_b : to_g + np;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int e0 = (i * kLongThreads + t) << 3;
+    const int e0 = (i * tpr + t) << 3;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 fg = halves(dg[i][j]), fb = halves(db[i][j]);
-      if (e0 + 2 * j < n) out_g[e0 + 2 * j] = fg.x, out_b[e0 + 2 * j] = fb.x;
-      if (e0 + 2 * j + 1 < n) out_g[e0 + 2 * j + 1] = fg.y, out_b[e0 + 2 * j + 1] = fb.y;
+      if (e0 + 2 * j < n) to_g[e0 + 2 * j] = fg.x, to_b[e0 + 2 * j] = fb.x;
+      if (e0 + 2 * j + 1 < n) to_g[e0 + 2 * j + 1] = fg.y, to_b[e0 + 2 * j + 1] = fb.y;
+    }
+  }
+  if constexpr (!BLOCK) {  // the block's warps are added in their order
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += THREADS) {
+      float sg = 0.0f, sb = 0.0f;
+      for (int k = 0; k < (THREADS >> 5); ++k) {
+        sg += groups[int64_t(k) * 2 * np + e];
+        sb += groups[(int64_t(k) * 2 + 1) * np + e];
+      }
+      out_g[e] = sg;
+      out_b[e] = sb;
     }
   }
 }
@@ -786,7 +874,7 @@ int64_t round_up4(int64_t n) { return (n + 3) & ~int64_t{3}; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int64_t kRingWidth = 16384;  // longer rows go without the ring
+constexpr int64_t kNarrowWidth = 512, kRingWidth = 16384;  // the ring's rows lie between
 
 // Threads of a group, groups of a block, shared memory and blocks for n columns: ch chunks a
 // thread, `slots` slots of `arrays` rows a group, `params` parameters staged.
@@ -810,13 +898,17 @@ Shape ring_shape(int64_t rows, int64_t n, int ch, int slots, int arrays, int par
 }
 
 Shape forward_shape(int64_t rows, int64_t n, bool vec, int sms) {
-  return ring_shape(rows, n, kFwdChunks, kFwdSlots, 1, 2, vec ? 80 : 128, vec, sms);
+  return ring_shape(rows, n, kFwdChunks, kFwdSlots, 1, 2, vec && n <= 8192 ? 80 : 128, vec, sms);
 }
 // Two chunks and three slots where they fit; past 8192 columns a block has threads for four
 // chunks and shared memory for two slots.
 Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
+  Shape s = {};
+  if (n <= kNarrowWidth) {
+    s.blocks = static_cast<int>(std::min<int64_t>(cdiv(rows, kNarrowThreads / 32), 2 * sms));
+    return s;
+  }
   if (n > kRingWidth) {
-    Shape s = {};
     s.blocks = static_cast<int>(std::min<int64_t>(rows, sms));
     return s;
   }
@@ -838,19 +930,32 @@ cudaError_t forward(const void* x, const void* gamma, const void* beta, void* y,
   const uint16_t* px = static_cast<const uint16_t*>(x);
   const P *g = static_cast<const P*>(gamma), *b = static_cast<const P*>(beta);
   uint16_t* py = static_cast<uint16_t*>(y);
-  if (n > kRingWidth) {
-    tg_layernorm_long_kernel<VEC, P><<<static_cast<unsigned>(std::min<int64_t>(rows, sms)),
-                                       kLongThreads, 0, st>>>(px, ldx, g, b, py, ldy, mean, rstd,
-                                                              rows, static_cast<int>(n), eps);
+  auto direct = [&](auto kern, int threads, int64_t blocks) {
+    kern<<<static_cast<unsigned>(blocks), threads, 0, st>>>(px, ldx, g, b, py, ldy, mean, rstd, rows,
+                                                            static_cast<int>(n), eps);
     return cudaGetLastError();
+  };
+  if (n <= kNarrowWidth) {
+    constexpr int kT = kNarrowThreads;
+    const int64_t blocks = std::min<int64_t>(cdiv(rows, kT / 32), int64_t(sms) * 4);
+    return n <= 256 ? direct(tg_layernorm_direct_kernel<1, false, VEC, kT, P>, kT, blocks)
+                    : direct(tg_layernorm_direct_kernel<2, false, VEC, kT, P>, kT, blocks);
   }
+  if (n > kRingWidth)
+    return direct(tg_layernorm_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>, kLongThreads,
+                  std::min<int64_t>(rows, sms));
   const Shape s = forward_shape(rows, n, VEC, sms);
-  auto kern = tg_layernorm_kernel<VEC, P>;
-  const cudaError_t e = allow_smem(kern, s.smem);
-  if (e != cudaSuccess) return e;
-  kern<<<s.blocks, s.threads, s.smem, st>>>(px, ldx, g, b, py, ldy, mean, rstd, rows,
-                                            static_cast<int>(n), eps, s.tpr, s.slot_bytes, err);
-  return cudaGetLastError();
+  auto ring = [&](auto kern) {
+    const cudaError_t e = allow_smem(kern, s.smem);
+    if (e != cudaSuccess) return e;
+    kern<<<s.blocks, s.threads, s.smem, st>>>(px, ldx, g, b, py, ldy, mean, rstd,
+                                              static_cast<int>(rows), static_cast<int>(n), eps,
+                                              s.tpr, s.slot_bytes, err);
+    return cudaGetLastError();
+  };
+  // up to 8192 columns a block has 256 threads at most: three of them an SM where registers allow
+  return n <= 8192 ? ring(tg_layernorm_kernel<256, VEC ? 3 : 2, VEC, P>)
+                   : ring(tg_layernorm_kernel<512, 1, VEC, P>);
 }
 
 template <bool VEC, typename P>
@@ -864,16 +969,25 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
   const int width = static_cast<int>(n);
   const int64_t np = round_up4(n);
   cudaError_t e;
-  if (n > kRingWidth) {
-    tg_layernorm_backward_long_kernel<VEC, P><<<s.blocks, kLongThreads, 0, st>>>(
-        pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, rows, width);
-    e = cudaGetLastError();
+  auto direct = [&](auto kern, int threads, size_t smem) {
+    kern<<<s.blocks, threads, smem, st>>>(pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, rows,
+                                          width);
+    return cudaGetLastError();
+  };
+  if (n <= kNarrowWidth) {
+    constexpr int kT = kNarrowThreads;
+    const size_t smem = part ? size_t(kT / 32) * 2 * np * 4 : 0;  // at most 32 KB
+    e = n <= 256 ? direct(tg_layernorm_backward_direct_kernel<1, false, VEC, kT, P>, kT, smem)
+                 : direct(tg_layernorm_backward_direct_kernel<2, false, VEC, kT, P>, kT, smem);
+  } else if (n > kRingWidth) {
+    e = direct(tg_layernorm_backward_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>,
+               kLongThreads, 0);
   } else {
     auto go = [&](auto kern) {
       const cudaError_t a = allow_smem(kern, s.smem);
       if (a != cudaSuccess) return a;
       kern<<<s.blocks, s.threads, s.smem, st>>>(pd, lddy, px, ldx, g, mean, rstd, out, lddx, part,
-                                                np, rows, width, s.tpr, s.slot_bytes, err);
+                                                np, static_cast<int>(rows), width, s.tpr, s.slot_bytes, err);
       return cudaGetLastError();
     };
     e = n <= 8192 ? go(tg_layernorm_backward_kernel<2, 3, VEC, P>)

@@ -83,8 +83,8 @@ def test_forward(M, N, pad, offset):
     assert y is out
     check_forward(x, gamma, beta, y, mean, rstd)
     assert (buf[:, :offset] == 7).all() and (buf[:, offset + N:] == 7).all()
-    y2 = tg.layer_norm(x, gamma, beta, eps=EPS)
-    assert torch.equal(y2, y)
+    # an output at another alignment may go by another order of the sums
+    check_forward(x, gamma, beta, tg.layer_norm(x, gamma, beta, eps=EPS), mean, rstd)
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
@@ -128,7 +128,8 @@ def test_forward_large_offset_and_extremes():
 def test_forward_in_place():
     for pad in (0, 3):
         x = make(50, 1003, pad, seed=13)
-        want = tg.layer_norm(x, eps=EPS)
+        want = tg.layer_norm(x, eps=EPS, out=torch.empty_strided(
+            x.shape, x.stride(), dtype=x.dtype, device="cuda"))
         got = tg.layer_norm(x, eps=EPS, out=x)
         assert got is x and torch.equal(x, want)
 
