@@ -779,9 +779,11 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
                    int64_t lda, int64_t ldb, int64_t ldc, const tg_epilogue& epi,
                    const tg_options* opt, cudaStream_t stream, int ta = 0, int tb = 0,
                    const tg::GemmExtra* extra = nullptr) {
-  float* const out32 = extra ? extra->out32 : nullptr;
-  if (out32) {  // validated and planned like a C that goes through the float32 workspace
-    C = out32;
+  const tg::LogitsExtra* const logits = extra ? extra->logits : nullptr;
+  float* const out32 = logits ? logits->z : extra ? extra->out32 : nullptr;
+  const bool f32 = logits || out32;  // no fp16 output
+  if (f32) {  // validated and planned like a C that goes through the float32 workspace
+    C = const_cast<void*>(A);  // only its presence and alignment are looked at
     ldc = N;
   }
   tg_status st = validate(A, B, C, M, N, K, lda, ldb, ldc, TG_EPILOGUE_NONE, ta, tb);
@@ -810,24 +812,24 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     e = cudaGetLastError();
     return e == cudaSuccess ? TG_OK : cuda_fail(e);
   }
-  tg_options out32_opt;
-  if (out32) {
-    std::memset(&out32_opt, 0, sizeof(out32_opt));
-    if (opt) out32_opt = *opt;
-    out32_opt.split_k = 1;
-    out32_opt.force_workspace = 1;
-    if (extra->add) out32_opt.pair = 1;
-    opt = &out32_opt;
+  tg_options f32_opt;
+  if (f32) {
+    std::memset(&f32_opt, 0, sizeof(f32_opt));
+    if (opt) f32_opt = *opt;
+    f32_opt.split_k = 1;
+    f32_opt.force_workspace = 1;
+    if (!logits && extra->add) f32_opt.pair = 1;
+    opt = &f32_opt;
   }
   Plan pl;
   st = make_plan(reinterpret_cast<uintptr_t>(A), reinterpret_cast<uintptr_t>(B),
                  reinterpret_cast<uintptr_t>(C), M, N, K, lda, ldb, ldc, ds->sm_count,
                  ds->pair_clusters, opt, &pl, ta, tb);
   if (st != TG_OK) return st;
-  if (out32) {  // the workspace is the caller's
-    pl.ldw = extra->ld32;
+  if (f32) {  // the workspace is the caller's, or there is none
+    pl.ldw = logits ? logits->ldz : extra->ld32;
     pl.pub.workspace_bytes = pl.off_w;
-    if (extra->block_n) *extra->block_n = pl.pub.block_n;
+    if (logits) *logits->block_n = pl.pub.block_n;
   }
   PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
   if ((st = encode_fn(&enc)) != TG_OK) return st;
@@ -940,10 +942,10 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
                         uint64_t(ldb_e) * 2, tg::kBK, P.cta_pair ? 128u : uint32_t(P.block_n))
             : encode_2d(enc, &L.b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Be, uint64_t(N), uint64_t(K),
                         uint64_t(ldb_e) * 2, 64, mn_box_k);
-  float* ws = out32                  ? out32
+  float* ws = f32                    ? out32
               : P.workspace_epilogue ? reinterpret_cast<float*>(scratch + pl.off_w)
                                      : nullptr;
-  if (cr == CUDA_SUCCESS) {
+  if (cr == CUDA_SUCCESS && (ws || !f32)) {
     if (ws)
       cr = encode_ws_3d(enc, &L.out, ws, uint64_t(N), uint64_t(ws_rows), uint64_t(P.split_k),
                         uint64_t(pl.ldw));
@@ -971,8 +973,8 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   gp.ldr = epi.residual ? epi.ldr : 0;
   if (extra) {
     gp.alpha = extra->alpha;
-    gp.stats = extra->stats;
-    gp.stat_c = extra->stat_c;
+    gp.addend = extra->addend;
+    gp.ld_addend = extra->ld32;
   }
   gp.a_mn = ta;
   gp.b_k = tb;
@@ -1002,9 +1004,8 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   L.grid = P.grid;
   L.stream = stream;
   auto launch = [&](const tg::GemmLaunch& l) -> cudaError_t {
-    if (out32)
-      return extra->add ? tg::launch_head_add(l)
-                        : tg::launch_head_logits(l, P.cta_pair ? 0 : P.block_n);
+    if (logits) return tg::launch_head_logits(l, *logits, P.cta_pair ? 0 : P.block_n);
+    if (out32 && extra->add) return tg::launch_head_add(l);
     if (P.a_row_classes) return tg::launch_gemm_pair_cls(cls, l);
     if (P.cta_pair) return tg::launch_gemm_pair(l, ws != nullptr);
     switch (P.block_n) {
@@ -1057,7 +1058,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     if (ce != cudaSuccess) return fail(cuda_fail(ce));
   }
 
-  if (ws && !out32) {
+  if (ws && !f32) {
     tg_splitk_reduce_kernel<<<reduce_grid(M, N), kReduceThreads, 0, stream>>>(
         ws, pl.ldw, ws_rows * pl.ldw, P.split_k, static_cast<__half*>(C), ldc, reduce_params,
         P.a_row_classes ? pl.cls_rows : 0);

@@ -82,12 +82,11 @@ struct GemmParams {
   const __half* bias;
   const __half* residual;
   long long ldr;
-  // fp16 output only: device float32 that the sum is multiplied by before the bias (nullptr: 1)
+  // fp16 output only: (sum + addend[i*ld_addend + j]) * *alpha goes on to the bias (device
+  // float32; nullptr: 0 and 1)
   const float* alpha;
-  // kModeLogits: [tiles_n][M] softmax statistics of each row of an output tile (row_stats_chunk),
-  // of the sums times stat_c
-  float2* stats;
-  float stat_c;
+  const float* addend;
+  long long ld_addend;
   // A read by row classes (CTA-pair kernel, float32 output; see AClassMaps): M tile m holds
   // rows 16 j + r of class r = m / cls_tiles, j from (m % cls_tiles) * 256; class r's rows
   // start cls_shift[r] elements past a 32-byte boundary, so its K windows (and the matching B
@@ -96,10 +95,9 @@ struct GemmParams {
   unsigned char cls_shift[kARowClasses];
 };
 
-// What the epilogue of a float32 output does with a tile, beside storing it (kModePlain):
-// kModeLogits adds the rows' softmax statistics; kModeAdd adds the tile to the output instead of
-// overwriting it (each element is added to once a launch, so the result does not depend on order).
-enum : int { kModePlain = 0, kModeLogits = 1, kModeAdd = 2 };
+// What the epilogue of a float32 output does with a tile: stores it, or adds it to the output
+// (each element is added to once a launch, so the result does not depend on order).
+enum : int { kModePlain = 0, kModeAdd = 1 };
 
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3 };
 
@@ -119,8 +117,10 @@ __device__ __forceinline__ float activation(float x, int act) {
   }
 }
 
-// Full epilogue of one float32 sum at (row, col): (alpha sum + bias) -> activation -> + residual.
+// Full epilogue of one float32 sum at (row, col): (alpha (sum + addend) + bias) -> activation ->
+// + residual.
 __device__ __forceinline__ float epilogue_value(float x, int row, int col, const GemmParams& p) {
+  if (p.addend) x += p.addend[static_cast<long long>(row) * p.ld_addend + col];
   if (p.alpha) x *= __ldg(p.alpha);
   if (p.bias) x += __half2float(p.bias[col]);
   x = activation(x, p.act);
@@ -400,6 +400,27 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------------------
 // Descriptors (PTX ISA, tcgen05 "matrix descriptor" and "instruction descriptor")
 // ---------------------------------------------------------------------------------------
@@ -578,13 +599,30 @@ __device__ __forceinline__ void load_half32(const __half* src, int col, int n, f
   }
 }
 
-// General fused epilogue of 32 consecutive columns of one row: x = alpha acc + bias, activation,
-// + residual, then fp16 pairs into pk[0..15].
+// General fused epilogue of 32 consecutive columns of one row: x = alpha (acc + addend) + bias,
+// activation, + residual, then fp16 pairs into pk[0..15].
 __device__ __forceinline__ void epilogue_general_32(const uint32_t (&acc)[32], int row, int col,
                                                     const GemmParams& p, uint32_t* pk) {
   float x[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(acc[i]);
+  if (p.addend && row < p.M) {  // ld_addend is a multiple of 32, its rows 128-byte aligned
+    const float* w = p.addend + static_cast<long long>(row) * p.ld_addend + col;
+    if (col + 32 <= p.N) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(w) + i);
+        x[4 * i] += v.x;
+        x[4 * i + 1] += v.y;
+        x[4 * i + 2] += v.z;
+        x[4 * i + 3] += v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (col + i < p.N) x[i] += w[i];
+    }
+  }
   if (p.alpha) {
     const float a = __ldg(p.alpha);
 #pragma unroll
@@ -633,7 +671,8 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
                                                 const uint32_t (&r1)[32], int row0, int col0,
                                                 uint8_t* stg, int& sb, int lane) {
   uint32_t pk[32];
-  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu && p.alpha == nullptr) {
+  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu &&
+      p.alpha == nullptr && p.addend == nullptr) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       pk[i] = relu_pack_h2(r0[2 * i], r0[2 * i + 1], p.act);
@@ -695,34 +734,6 @@ __device__ __forceinline__ void unperm8(uint32_t (&r)[32]) {
   }
 }
 
-// Softmax statistics of one row, 32 columns at a time (r: float32 bits of the sums; cnt: how many
-// are columns of the matrix): m = the largest of the scaled sums so far, s = the sum of
-// 2^(scaled sum - m), with log2(e) in the scale c.  A row's statistics over several tiles combine
-// as 2^(m - M) s.  An infinite m (every sum -inf, or none) adds nothing but a NaN among the sums.
-__device__ __forceinline__ void row_stats_chunk(const uint32_t (&r)[32], int cnt, float c, float& m,
-                                                float& s) {
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < cnt) top = fmaxf(top, __uint_as_float(r[i]));
-  const float m1 = fmaxf(m, top * c);
-  float add = 0.0f;
-  if (m1 == -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float x = __uint_as_float(r[i]);
-      if (i < cnt && x != x) add = x;
-    }
-    s += add;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < cnt) add += exp2f(fmaf(__uint_as_float(r[i]), c, -m1));
-  s = s * exp2f(m - m1) + add;
-  m = m1;
-}
-
 template <int BN, bool OUT_F32, bool PERM8 = false, int MODE = kModePlain>
 __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const GemmParams& p,
                                               uint32_t tl, int row0, int col_base, int split,
@@ -759,14 +770,12 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
       store_chunk_f16(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
     }
   } else {
-    float m = -INFINITY, s = 0.0f;  // kModeLogits
 #pragma unroll 1
     for (int c = 0; c < BN / 32; ++c) {
       uint32_t r[32];
       tmem_ld_x32(tl + c * 32, r);
       tmem_wait_ld(r);
       if (c == BN / 32 - 1) release();
-      if constexpr (MODE == kModeLogits) row_stats_chunk(r, p.N - col_base - c * 32, p.stat_c, m, s);
       uint8_t* st = stg + sb * kStagingBuf;
       if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
@@ -786,10 +795,6 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
       }
       sb ^= 1;
     }
-    if constexpr (MODE == kModeLogits) {
-      if (row0 + lane < p.M)
-        p.stats[static_cast<long long>(col_base / BN) * p.M + row0 + lane] = make_float2(m, s);
-    }
   }
 }
 
@@ -805,7 +810,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
 // 0); the single producer and MMA threads then build descriptors and TMA boxes from constants,
 // which keeps their per-k-block instruction count inside the MMA time.  GENERAL == true reads
 // the layouts from p.a_mn and p.b_k (the transposed-operand GEMMs of the backward pass).
-template <int BN, bool OUT_F32, bool GENERAL, int MODE = kModePlain>
+template <int BN, bool OUT_F32, bool GENERAL>
 __global__ void __launch_bounds__(kThreads, 1)
     tg_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -966,8 +971,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
-      epilogue_tile<BN, OUT_F32, false, MODE>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN, w.split,
-                                              stg, sb, smem_u32(&tempty[buf]), false, lane);
+      epilogue_tile<BN, OUT_F32>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN, w.split,
+                                 stg, sb, smem_u32(&tempty[buf]), false, lane);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();

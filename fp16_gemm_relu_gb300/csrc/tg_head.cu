@@ -11,10 +11,10 @@
 //     dX = alpha G W,  dW = alpha G^T X
 //
 // The three products are the work (2 T V D each), so they run on the tensor cores: the logits
-// through the GEMM kernels' float32 output, whose epilogue also leaves each tile's row maximum and
-// sum of exponentials (so lse needs no pass over the logits); dX and dW through the ordinary
-// GEMMs on G.  Tokens go in pieces that bound the logits' scratch; dW is summed over the pieces
-// in float32.
+// through tg_head_kernel.cuh, whose epilogue also leaves each tile's row maximum and sum of
+// exponentials (so lse needs no pass over the logits, and cross entropy alone does not store
+// them); dX and dW through the ordinary GEMMs on G.  Tokens go in pieces that bound the logits'
+// scratch; dW is summed over the pieces in float32.
 //
 // G is rounded to fp16 once, the operand type of the products.  So that the many small
 // probabilities stay normal fp16 numbers, G carries the factor 2^15 / max|w| (|p - q| <= 1, so
@@ -75,12 +75,14 @@ __device__ __forceinline__ float row_factor(float w, float wmax) {
   return (wmax > 0.0f ? w / wmax : 0.0f * w) * kGScale;  // 0 * w keeps a NaN
 }
 
-// lse of 32 rows a block from their tiles' statistics; cross entropy's loss and RowInfo too.
+// lse of 32 rows a block from their tiles' statistics; cross entropy's loss and RowInfo too (the
+// targets' logits from z, or picked where z is not stored).
 // alpha (one float): s max|w| / 2^15, written by the first block.
 constexpr int kRowLanes = 16;
 __global__ void __launch_bounds__(32 * kRowLanes)
     tg_head_rows_kernel(const float2* __restrict__ stats, int tiles, int64_t rows,
-                        const float* __restrict__ z, int64_t ldz, float scale, int64_t vocab,
+                        const float* __restrict__ z, int64_t ldz,
+                        const float* __restrict__ picked, float scale, int64_t vocab,
                         const int64_t* __restrict__ target, int64_t ignore,
                         const float* __restrict__ dloss, const unsigned* __restrict__ wmax,
                         float* loss, float* lse, RowInfo* info, float* alpha) {
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(32 * kRowLanes)
     float l = 0.0f;
     if (kind == RowKind::kCounts) {
       ri.target = static_cast<int>(y);
-      l = lse2 * kLn2 - scale * z[r * ldz + y];
+      l = lse2 * kLn2 - scale * (z ? z[r * ldz + y] : picked[r]);
       if (dloss) ri.gs = row_factor(dloss[r], w);
     } else if (kind == RowKind::kBad) {
       l = ri.gs = NAN;
@@ -258,6 +260,8 @@ constexpr int64_t kMaxLd = int64_t{1} << 36;
 // Logits of a piece by default: 2 GiB of float32, 1 GiB of G.  Fewer, longer pieces cost less: a
 // piece adds one pass of reads and writes over dW in float32.
 constexpr int64_t kPieceLogits = int64_t{1} << 29;
+// Without logits a token's scratch is its statistics: 1 GiB of them.
+constexpr int64_t kPieceStats = int64_t{1} << 27;
 
 // One call's arguments beside the sizes; `top` > 0 makes it distillation.
 struct Head {
@@ -324,10 +328,13 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     return e == cudaSuccess ? TG_OK : tg::record_cuda_error(e);
   }
   const bool grad = h.dX || h.dW;
+  const bool store = grad || h.top > 0;  // the logits are needed again
   const int64_t ldz = round_up(h.V, 32), ldg = round_up(h.V, 64);
+  const int64_t tiles = 2 * cdiv(h.V, 128);  // statistics of a row, at most
+  const int64_t per_row = store ? ldz : tiles, budget = store ? kPieceLogits : kPieceStats;
   int64_t piece = h.o.piece_rows ? std::min(h.o.piece_rows, h.T) : h.T;
-  if (!h.o.piece_rows && h.T * ldz > kPieceLogits) {
-    const int64_t most = std::max<int64_t>(kPieceLogits / ldz / 256 * 256, 256);
+  if (!h.o.piece_rows && h.T > budget / per_row) {
+    const int64_t most = std::max<int64_t>(budget / per_row / 256 * 256, 256);
     piece = std::min(h.T, round_up(cdiv(h.T, cdiv(h.T, most)), 256));
   }
   const bool sum_w = h.dW && piece < h.T;  // dW is summed over pieces in float32
@@ -337,8 +344,9 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const bool copy_x = misaligned(h.X, 16) || h.ldx % 8 != 0;
   const bool copy_w = misaligned(h.W, 16) || h.ldw % 8 != 0;
   const int64_t ldxp = round_up(h.D, 64), ldwp = round_up(w_cols, 64), ldw32 = round_up(w_cols, 32);
-  const int64_t at_z = lay.add(piece * ldz * 4);
-  const int64_t at_stats = lay.add(cdiv(h.V, 128) * piece * int64_t(sizeof(float2)));
+  const int64_t at_z = lay.add(store ? piece * ldz * 4 : 0);
+  const int64_t at_stats = lay.add(tiles * piece * int64_t(sizeof(float2)));
+  const int64_t at_picked = lay.add(store ? 0 : piece * 4);
   const int64_t at_info = lay.add(piece * int64_t(sizeof(RowInfo)));
   const int64_t at_small = lay.add(2 * 4);
   const int64_t at_g = lay.add(grad ? piece * ldg * 2 : 0);
@@ -353,7 +361,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     const cudaError_t fe = cudaFreeAsync(mem, stream);
     return s == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : s;
   };
-  float* z = reinterpret_cast<float*>(mem + at_z);
+  float* z = store ? reinterpret_cast<float*>(mem + at_z) : nullptr;
+  float* picked = reinterpret_cast<float*>(mem + at_picked);
   float2* stats = reinterpret_cast<float2*>(mem + at_stats);
   RowInfo* info = reinterpret_cast<RowInfo*>(mem + at_info);
   unsigned* wmax = grad ? reinterpret_cast<unsigned*>(mem + at_small) : nullptr;
@@ -386,8 +395,6 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
                             stream>>>(h.dloss, h.index, h.ldt, h.top, h.ignore, h.T, wmax);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
   }
-  if (sum_w && (e = cudaMemsetAsync(w32, 0, size_t(w_rows) * ldw32 * 4, stream)) != cudaSuccess)
-    return done(tg::record_cuda_error(e));
 
   tg_options opt;
   std::memset(&opt, 0, sizeof(opt));
@@ -404,17 +411,21 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     const float* dloss = grad ? h.dloss + t0 : nullptr;
     float* loss = h.loss ? h.loss + t0 : nullptr;
     int block_n = 0;
+    tg::LogitsExtra lx;
+    lx.z = z;
+    lx.ldz = ldz;
+    lx.stats = stats;
+    lx.stat_c = c;
+    lx.target = store ? nullptr : reinterpret_cast<const long long*>(index);
+    lx.picked = picked;
+    lx.block_n = &block_n;
     tg::GemmExtra ex;
     std::memset(&ex, 0, sizeof(ex));
-    ex.out32 = z;
-    ex.ld32 = ldz;
-    ex.stats = stats;
-    ex.stat_c = c;
-    ex.block_n = &block_n;
+    ex.logits = &lx;
     st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &opt, stream);
     if (st != TG_OK) return done(st);
     tg_head_rows_kernel<<<static_cast<unsigned>(cdiv(n, 32)), dim3(32, kRowLanes), 0, stream>>>(
-        stats, static_cast<int>(cdiv(h.V, block_n)), n, z, ldz, h.scale, h.V,
+        stats, static_cast<int>(2 * cdiv(h.V, block_n)), n, z, ldz, picked, h.scale, h.V,
         h.top ? nullptr : index, h.ignore, dloss, wmax, loss, h.lse ? h.lse + t0 : nullptr, info,
         alpha);
     if (h.top)
@@ -440,25 +451,19 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     if (h.dW) {  // G^T X (V x D), or X^T G (D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
-      if (sum_w) {
-        ex.out32 = w32;
+      if (sum_w) {  // the first piece writes the sums, the last takes them into its epilogue
         ex.ld32 = ldw32;
-        ex.add = true;
+        if (t0 + piece < h.T) {
+          ex.out32 = w32;
+          ex.add = t0 > 0;
+        } else {
+          ex.addend = w32;
+        }
       }
       st = by_vocab ? tg::gemm_extra(1, 0, g, x, h.dW, h.V, h.D, n, ldg, ldx, h.lddw, ex, &opt, stream)
                     : tg::gemm_extra(1, 0, x, g, h.dW, h.D, h.V, n, ldx, ldg, h.lddw, ex, &opt, stream);
       if (st != TG_OK) return done(st);
     }
-  }
-  if (sum_w) {  // one rounding to fp16 after the last piece
-    tg::GemmParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.alpha = alpha;
-    p.M = static_cast<int>(w_rows);
-    p.N = static_cast<int>(w_cols);
-    if ((e = tg::launch_splitk_reduce(w32, ldw32, 0, 1, h.dW, h.lddw, p, sms, stream)) !=
-        cudaSuccess)
-      return done(tg::record_cuda_error(e));
   }
   return done(TG_OK);
 }

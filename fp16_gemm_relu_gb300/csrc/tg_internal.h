@@ -32,8 +32,18 @@ cudaError_t launch_gemm_pair(const GemmLaunch& l, bool out_f32);
 // The CTA-pair kernel with A read in place through row classes (float32 output only; l.a is
 // unused, l.p.cls_* describe the classes).
 cudaError_t launch_gemm_pair_cls(const AClassMaps& cls, const GemmLaunch& l);
-// Float32 logits of a head (kModeLogits; block_n 0: CTA pairs), A row-major, B in either layout.
-cudaError_t launch_head_logits(const GemmLaunch& l, int block_n);
+// What the head's logits pass gives beside, or instead of, the logits.
+struct LogitsExtra {
+  float* z;                 // float32 logits, rows of ldz (a multiple of 32); NULL: not stored
+  int64_t ldz;
+  float2* stats;            // [2 ceil(N / *block_n)][M]: each row's softmax statistics over
+  float stat_c;             // *block_n / 2 columns, of stat_c times the logits
+  const long long* target;  // without z: [M], and the targets' logits [M]
+  float* picked;
+  int* block_n;             // out: the tiles' width
+};
+// Logits kernel (block_n 0: CTA pairs), X row-major, W in either layout (l.p.b_k).
+cudaError_t launch_head_logits(const GemmLaunch& l, const LogitsExtra& x, int block_n);
 // The CTA-pair kernel that adds A^T B to its float32 output (kModeAdd; A stored K x M).
 cudaError_t launch_head_add(const GemmLaunch& l);
 // Clusters of two that can be resident at once on the current device.
@@ -61,15 +71,14 @@ tg_status scratch_alloc(size_t bytes, cudaStream_t stream, void** out);
 bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 
 // The GEMM behind every entry point, with what the head's passes need beside the public ones.
-// With out32 (no K splits, no fp16 output) C is not used.
+// With `logits` or out32 there are no K splits and no fp16 output (C is not used).
 struct GemmExtra {
-  const float* alpha;  // device factor of an fp16 output (nullptr: 1)
-  float* out32;        // float32 output, M rows of ld32 (a multiple of 32) floats
+  const LogitsExtra* logits;
+  const float* alpha;   // fp16 output: C = fp16(alpha (A B + addend)), both device float32
+  const float* addend;  // (NULL: 1 and 0), rows of ld32
+  float* out32;         // float32 output, rows of ld32 floats (a multiple of 32)
   int64_t ld32;
-  bool add;            // add to out32 (A stored K x M, B stored K x N) instead of writing logits
-  float2* stats;       // logits: [ceil(N / *block_n)][M] row statistics of stat_c times the logits
-  float stat_c;
-  int* block_n;        // out: the width of the tiles that stats are of (128, 192 or 256)
+  bool add;             // add to out32 (A stored K x M, B stored K x N) instead of writing it
 };
 tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
                      int64_t K, int64_t lda, int64_t ldb, int64_t ldc, const GemmExtra& x,
