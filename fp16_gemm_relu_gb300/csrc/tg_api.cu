@@ -626,11 +626,62 @@ __global__ void __launch_bounds__(kReduceThreads)
   }
 }
 
+// The same sums (the same order, the same bits) for a small output: one row a thread, so that there
+// are four times as many threads, and kReduceAhead splits' loads in flight at a time.  128 x 1024
+// from 13 splits took 15 us as above, where 64 blocks waited for one split after the other.
+constexpr int kReduceAhead = 8;
+__global__ void __launch_bounds__(kReduceThreads)
+    tg_splitk_reduce_small_kernel(const float* __restrict__ ws, int64_t ldw, int64_t split_stride,
+                                  int splits, __half* C, int64_t ldc, const tg::GemmParams p) {
+  const int64_t g = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;  // group of 4 columns
+  const int64_t N = p.N, r = blockIdx.y, c0 = g << 2;
+  if (c0 >= N) return;
+  const float* w = ws + r * ldw + c0;
+  float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < splits; s0 += kReduceAhead) {
+    float4 v[kReduceAhead];
+#pragma unroll
+    for (int i = 0; i < kReduceAhead; ++i)
+      if (s0 + i < splits)
+        v[i] = __ldg(reinterpret_cast<const float4*>(w + (s0 + i) * split_stride));
+#pragma unroll
+    for (int i = 0; i < kReduceAhead; ++i) {
+      if (s0 + i >= splits) break;
+      if (s0 + i == 0) {
+        a[0] = v[0].x, a[1] = v[0].y, a[2] = v[0].z, a[3] = v[0].w;
+      } else {
+        a[0] += v[i].x, a[1] += v[i].y, a[2] += v[i].z, a[3] += v[i].w;
+      }
+    }
+  }
+  __half* d = C + r * ldc + c0;
+  for (int e = 0; e < 4 && c0 + e < N; ++e)
+    d[e] = __float2half_rn(tg::epilogue_value(a[e], int(r), int(c0 + e), p));
+}
+
 // Grid of the reduction: x over the groups of 4 columns, y over chunks of kReduceRows rows.
 dim3 reduce_grid(int64_t M, int64_t N) {
   return dim3(static_cast<unsigned>(cdiv(cdiv(std::max<int64_t>(N, 1), 4), kReduceThreads)),
               static_cast<unsigned>(std::min<int64_t>(cdiv(std::max<int64_t>(M, 1), kReduceRows),
                                                       65535)));
+}
+
+// Small: kReduceRows rows a thread would leave SMs without a block.
+bool reduce_small(int64_t M, int64_t N, int num_sms) {
+  const dim3 grid = reduce_grid(M, N);
+  return int64_t(grid.x) * grid.y < 2 * int64_t(num_sms) && M <= 65535;
+}
+
+void launch_reduce(const float* ws, int64_t ldw, int64_t split_stride, int splits, __half* C,
+                   int64_t ldc, const tg::GemmParams& p, int64_t cls_rows, int num_sms,
+                   cudaStream_t stream) {
+  if (cls_rows == 0 && splits > 1 && reduce_small(p.M, p.N, num_sms))
+    tg_splitk_reduce_small_kernel<<<dim3(reduce_grid(p.M, p.N).x, static_cast<unsigned>(p.M)),
+                                    kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C,
+                                                                 ldc, p);
+  else
+    tg_splitk_reduce_kernel<<<reduce_grid(p.M, p.N), kReduceThreads, 0, stream>>>(
+        ws, ldw, split_stride, splits, C, ldc, p, cls_rows);
 }
 
 // dZ[i, j] = C[i, j] > 0 ? dC[i, j] : +0 (the relu derivative taken on the forward output C;
@@ -1059,9 +1110,8 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   }
 
   if (ws && !f32) {
-    tg_splitk_reduce_kernel<<<reduce_grid(M, N), kReduceThreads, 0, stream>>>(
-        ws, pl.ldw, ws_rows * pl.ldw, P.split_k, static_cast<__half*>(C), ldc, reduce_params,
-        P.a_row_classes ? pl.cls_rows : 0);
+    launch_reduce(ws, pl.ldw, ws_rows * pl.ldw, P.split_k, static_cast<__half*>(C), ldc,
+                  reduce_params, P.a_row_classes ? pl.cls_rows : 0, ds->sm_count, stream);
     if ((e = cudaGetLastError()) != cudaSuccess) return fail(cuda_fail(e));
   }
   if (scratch && (e = cudaFreeAsync(scratch, stream)) != cudaSuccess) return cuda_fail(e);
@@ -1177,8 +1227,7 @@ bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) { return encode_f
 cudaError_t launch_splitk_reduce(const float* ws, int64_t ldw, int64_t split_stride, int splits,
                                  void* C, int64_t ldc, const GemmParams& p, int num_sms,
                                  cudaStream_t stream) {
-  tg_splitk_reduce_kernel<<<reduce_grid(p.M, p.N), kReduceThreads, 0, stream>>>(
-      ws, ldw, split_stride, splits, static_cast<__half*>(C), ldc, p, 0);
+  launch_reduce(ws, ldw, split_stride, splits, static_cast<__half*>(C), ldc, p, 0, num_sms, stream);
   return cudaGetLastError();
 }
 

@@ -53,12 +53,35 @@ __device__ __forceinline__ RowKind target_kind(int64_t y, int64_t vocab, int64_t
   return y >= 0 && y < vocab ? RowKind::kCounts : RowKind::kBad;
 }
 
-// max |w_t| over the rows that count, as the bits of a non-negative float (the maximum does not
-// depend on the order of the atomics).  top == 0: cross entropy; else a row counts when one of
-// its `top` entries does.
-__global__ void tg_head_weight_kernel(const float* __restrict__ dloss,
-                                      const int64_t* __restrict__ index, int64_t ld, int top,
-                                      int64_t ignore, int64_t rows, unsigned* wmax) {
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+// Elements [k, k + 8) of a 16-byte aligned row of n, zeros from n on.
+__device__ __forceinline__ void load8(const uint16_t* row, int k, int n, float (&f)[8]) {
+  if (k + 8 <= n) {
+    unpack8(__ldg(reinterpret_cast<const uint4*>(row + k)), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      f[i] = k + i < n ? __half2float(__ushort_as_half(row[k + i])) : 0.0f;
+  }
+}
+
+// max |w_t| over the rows that count, as the bits of a non-negative float.  top == 0: cross
+// entropy; else a row counts when one of its `top` entries does.  One block writes the maximum; with
+// several it is zero before and the largest of theirs wins (the order of the atomics does not
+// matter).
+__global__ void __launch_bounds__(1024)
+    tg_head_weight_kernel(const float* __restrict__ dloss, const int64_t* __restrict__ index,
+                          int64_t ld, int top, int64_t ignore, int64_t rows, unsigned* wmax) {
+  __shared__ float part[32];
   float m = 0.0f;
   for (int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; r < rows;
        r += int64_t(gridDim.x) * blockDim.x) {
@@ -68,134 +91,187 @@ __global__ void tg_head_weight_kernel(const float* __restrict__ dloss,
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((threadIdx.x & 31) == 0 && m > 0.0f) atomicMax(wmax, __float_as_uint(m));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) m = fmaxf(m, part[w]);
+  if (gridDim.x == 1)
+    *wmax = __float_as_uint(m);
+  else if (m > 0.0f)
+    atomicMax(wmax, __float_as_uint(m));
 }
 
 __device__ __forceinline__ float row_factor(float w, float wmax) {
   return (wmax > 0.0f ? w / wmax : 0.0f * w) * kGScale;  // 0 * w keeps a NaN
 }
 
-// lse of 32 rows a block from their tiles' statistics; cross entropy's loss and RowInfo too (the
-// targets' logits from z, or picked where z is not stored).
-// alpha (one float): s max|w| / 2^15, written by the first block.
-constexpr int kRowLanes = 16;
-__global__ void __launch_bounds__(32 * kRowLanes)
-    tg_head_rows_kernel(const float2* __restrict__ stats, int tiles, int64_t rows,
-                        const float* __restrict__ z, int64_t ldz,
-                        const float* __restrict__ picked, float scale, int64_t vocab,
-                        const int64_t* __restrict__ target, int64_t ignore,
-                        const float* __restrict__ dloss, const unsigned* __restrict__ wmax,
-                        float* loss, float* lse, RowInfo* info, float* alpha) {
-  __shared__ float2 part[kRowLanes][32];
-  const int64_t r = blockIdx.x * int64_t(32) + threadIdx.x;
-  float m = -INFINITY, s = 0.0f;
-  if (r < rows) {
-    for (int t = threadIdx.y; t < tiles; t += kRowLanes) {
-      const float2 v = stats[t * rows + r];
-      const float m1 = fmaxf(m, v.x);
-      if (m1 == -INFINITY) {
-        s += v.y;  // zero or NaN
-      } else {
-        s = s * exp2f(m - m1) + v.y * exp2f(v.x - m1);
-        m = m1;
-      }
-    }
-  }
-  part[threadIdx.y][threadIdx.x] = make_float2(m, s);
-  __syncthreads();
-  const float w = wmax ? __uint_as_float(*wmax) : 0.0f;
-  if (alpha && blockIdx.x == 0 && threadIdx.x == 0 && threadIdx.y == 0) *alpha = scale * w / kGScale;
-  if (threadIdx.y != 0 || r >= rows) return;
-  m = -INFINITY;
-  for (int y = 0; y < kRowLanes; ++y) m = fmaxf(m, part[y][threadIdx.x].x);
-  s = 0.0f;
-  for (int y = 0; y < kRowLanes; ++y) {
-    const float2 v = part[y][threadIdx.x];
-    s += m == -INFINITY ? v.y : v.y * exp2f(v.x - m);
-  }
-  const float lse2 = m + log2f(s);
-  if (lse) lse[r] = lse2 * kLn2;
-  RowInfo ri;
-  ri.lse2 = lse2;
-  ri.gs = 0.0f;
-  ri.target = -1;
-  ri.pad = 0;
-  if (target) {
-    const int64_t y = target[r];
-    const RowKind kind = target_kind(y, vocab, ignore);
-    float l = 0.0f;
-    if (kind == RowKind::kCounts) {
-      ri.target = static_cast<int>(y);
-      l = lse2 * kLn2 - scale * (z ? z[r * ldz + y] : picked[r]);
-      if (dloss) ri.gs = row_factor(dloss[r], w);
-    } else if (kind == RowKind::kBad) {
-      l = ri.gs = NAN;
-    }
-    if (loss) loss[r] = l;
-  }
-  info[r] = ri;
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
 }
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+constexpr int kRowThreads = 128;  // of a row in tg_head_rows_kernel
+
+// Maximum and sum over the block; slots is used again only after the next meeting of the block.
+__device__ __forceinline__ float block_max(float v, float* slots) {
+  v = warp_max(v);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(slots[0], slots[1]), fmaxf(slots[2], slots[3]));
+}
+__device__ __forceinline__ float block_sum(float v, float* slots) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return (slots[0] + slots[1]) + (slots[2] + slots[3]);
+}
+
+// Where the logits of a row's targets are: in z, or (z NULL) in picked, [rows] or [rows][top].
+struct Logits {
+  const float* z;
+  int64_t ldz;
+  const float* picked;
+};
 
 // Entry e's teacher logit.
 __device__ __forceinline__ float teacher_at(const void* t, int64_t at, int is_f32) {
   return is_f32 ? static_cast<const float*>(t)[at] : __half2float(static_cast<const __half*>(t)[at]);
 }
 
-// Distillation: a warp a row.  Entries with a negative index are not there; q is the softmax of
-// the others (one at -inf has q = 0).  A row without entries, or whose entries are all -inf, has
-// no teacher: loss 0 and no gradient.  q (float32, 0 for what is not there) is kept for the
-// gradient when `q` is given.
-__global__ void tg_head_distil_rows_kernel(const int64_t* __restrict__ index,
-                                           const void* __restrict__ teacher, int teacher_f32,
-                                           int64_t ldt, int top, int64_t rows,
-                                           const float* __restrict__ z, int64_t ldz, float scale,
-                                           int64_t vocab, const float* __restrict__ dloss,
-                                           const unsigned* __restrict__ wmax, float* loss,
-                                           RowInfo* info, float* q) {
-  const int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (r >= rows) return;
-  const float c = scale * kLog2e;
-  float m = -INFINITY;
-  bool bad = false;
-  for (int e = lane; e < top; e += 32) {
-    const int64_t i = index[r * ldt + e];
-    if (i < 0) continue;
-    bad |= i >= vocab;
-    const float u = teacher_at(teacher, r * ldt + e, teacher_f32);
-    bad |= !(u < INFINITY);  // NaN or +inf
-    m = fmaxf(m, u * c);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  bad = __any_sync(0xffffffffu, bad);
-  float s = 0.0f;
-  for (int e = lane; e < top && m > -INFINITY; e += 32)
-    if (index[r * ldt + e] >= 0)
-      s += exp2f(fmaf(teacher_at(teacher, r * ldt + e, teacher_f32), c, -m));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  const float lq = m + log2f(s), lse = info[r].lse2 * kLn2;
-  float l = 0.0f;
-  for (int e = lane; e < top; e += 32) {
-    float qe = 0.0f;
-    const int64_t i = index[r * ldt + e];
-    if (i >= 0 && m > -INFINITY) {
-      const float t2 = fmaf(teacher_at(teacher, r * ldt + e, teacher_f32), c, -lq);
-      qe = exp2f(t2);
-      if (qe > 0.0f && i < vocab) l += qe * (t2 * kLn2 - (scale * z[r * ldz + i] - lse));
+// A block a row: lse from the row's statistics, then its loss and what the gradient needs of it.
+// Distillation (top > 0): entries with a negative index are not there; q is the softmax of the
+// others (one at -inf has q = 0), kept for the gradient when `q` is given (0 for what is not
+// there).  A row without entries, or whose entries are all at -inf, has no teacher: loss 0 and no
+// gradient.  alpha (one float): s max|w| / 2^15, written by the first block.
+__global__ void __launch_bounds__(kRowThreads)
+    tg_head_rows_kernel(const float2* __restrict__ stats, int tiles, Logits lg, float scale,
+                        int64_t vocab, const int64_t* __restrict__ index, int64_t ignore,
+                        const void* __restrict__ teacher, int teacher_f32, int64_t ldt, int top,
+                        const float* __restrict__ dloss, const unsigned* __restrict__ wmax,
+                        float* loss, float* lse, RowInfo* info, float* q, float* alpha) {
+  __shared__ float slots[5][4];
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x;
+  const float w = wmax ? __uint_as_float(*wmax) : 0.0f;
+  if (alpha && r == 0 && tid == 0) *alpha = scale * w / kGScale;
+  float m = -INFINITY, s = 0.0f;
+#pragma unroll 4
+  for (int t = tid; t < tiles; t += kRowThreads) {
+    const float2 v = stats[r * tiles + t];
+    const float m1 = fmaxf(m, v.x);
+    if (m1 == -INFINITY) {
+      s += v.y;  // zero or NaN
+    } else {
+      s = s * exp2f(m - m1) + v.y * exp2f(v.x - m1);
+      m = m1;
     }
-    if (q) q[r * top + e] = qe;
   }
+  const float row_m = block_max(m, slots[0]);
+  if (row_m > -INFINITY) s *= exp2f(m - row_m);
+  const float lse2 = row_m + log2f(block_sum(s, slots[1])), lse_r = lse2 * kLn2;
+  RowInfo ri;
+  ri.lse2 = lse2;
+  ri.gs = 0.0f;
+  ri.target = -1;
+  ri.pad = 0;
+  float l = 0.0f;
+  if (top == 0) {
+    const int64_t y = index[r];
+    const RowKind kind = target_kind(y, vocab, ignore);
+    if (kind == RowKind::kCounts) {
+      ri.target = static_cast<int>(y);
+      l = lse_r - scale * (lg.z ? lg.z[r * lg.ldz + y] : lg.picked[r]);
+      if (dloss) ri.gs = row_factor(dloss[r], w);
+    } else if (kind == RowKind::kBad) {
+      l = ri.gs = NAN;
+    }
+  } else {
+    const float c = scale * kLog2e;
+    float mt = -INFINITY;
+    bool bad = false;
+    for (int e = tid; e < top; e += kRowThreads) {
+      const int64_t i = index[r * ldt + e];
+      if (i < 0) continue;
+      const float u = teacher_at(teacher, r * ldt + e, teacher_f32);
+      bad |= i >= vocab || !(u < INFINITY);  // NaN or +inf
+      mt = fmaxf(mt, u * c);
+    }
+    mt = block_max(mt, slots[2]);
+    bad = __syncthreads_or(bad);
+    float st = 0.0f;
+    for (int e = tid; e < top && mt > -INFINITY; e += kRowThreads)
+      if (index[r * ldt + e] >= 0)
+        st += exp2f(fmaf(teacher_at(teacher, r * ldt + e, teacher_f32), c, -mt));
+    const float lq = mt + log2f(block_sum(st, slots[3]));
+    for (int e = tid; e < top; e += kRowThreads) {
+      float qe = 0.0f;
+      const int64_t i = index[r * ldt + e];
+      if (i >= 0 && mt > -INFINITY) {
+        const float t2 = fmaf(teacher_at(teacher, r * ldt + e, teacher_f32), c, -lq);
+        qe = exp2f(t2);
+        if (qe > 0.0f && i < vocab) {
+          const float z = lg.z ? lg.z[r * lg.ldz + i] : lg.picked[r * top + e];
+          l += qe * (t2 * kLn2 - (scale * z - lse_r));
+        }
+      }
+      if (q) q[r * top + e] = qe;
+    }
+    l = block_sum(l, slots[4]);
+    if (bad) l = ri.gs = NAN;
+    else if (dloss && mt > -INFINITY) ri.gs = row_factor(dloss[r], w);
+  }
+  if (tid != 0) return;
+  if (loss) loss[r] = l;
+  if (lse) lse[r] = lse_r;
+  info[r] = ri;
+}
+
+// The logits of a row's entries without the logits' matrix: one dot product of X and a row of W
+// (V x D, 16-byte aligned rows) an entry, in float32.  A warp takes kPickRows entries at a time, whose
+// loads go out together: bound by the latency of rows all over W.
+constexpr int kPickRows = 4;
+__global__ void __launch_bounds__(256)
+    tg_head_pick_kernel(const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ w,
+                        int64_t ldw, const int64_t* __restrict__ index, int64_t ldt, int top,
+                        int64_t rows, int64_t vocab, int width, float* __restrict__ picked) {
+  const int lane = threadIdx.x & 31;
+  const int64_t groups = (top + kPickRows - 1) / kPickRows;
+  const int64_t step = int64_t(gridDim.x) * (blockDim.x >> 5);
+  for (int64_t it = blockIdx.x * int64_t(blockDim.x >> 5) + (threadIdx.x >> 5); it < rows * groups;
+       it += step) {
+    const int64_t r = it / groups;
+    const int e0 = static_cast<int>(it - r * groups) * kPickRows;
+    const uint16_t* xr = x + r * ldx;
+    const uint16_t* wr[kPickRows];
+    float s[kPickRows];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if (lane == 0) {
-    if (bad) l = NAN;
-    if (loss) loss[r] = l;
-    float gs = 0.0f;
-    if (bad) gs = NAN;
-    else if (dloss && m > -INFINITY) gs = row_factor(dloss[r], __uint_as_float(*wmax));
-    info[r].gs = gs;
+    for (int j = 0; j < kPickRows; ++j) {  // an entry that is not there reads W's first row
+      const int64_t i = e0 + j < top ? index[r * ldt + e0 + j] : 0;
+      wr[j] = w + (i >= 0 && i < vocab ? i : 0) * ldw;
+      s[j] = 0.0f;
+    }
+#pragma unroll 2
+    for (int k = lane * 8; k < width; k += 256) {
+      float a[8], b[kPickRows][8];
+      load8(xr, k, width, a);
+#pragma unroll
+      for (int j = 0; j < kPickRows; ++j) load8(wr[j], k, width, b[j]);
+#pragma unroll
+      for (int j = 0; j < kPickRows; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j] = fmaf(a[i], b[j][i], s[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kPickRows; ++j) {
+      const float v = warp_sum(s[j]);
+      if (lane == 0 && e0 + j < top) picked[r * top + e0 + j] = v;
+    }
   }
 }
 
@@ -204,48 +280,46 @@ __device__ __forceinline__ float grad_value(float z, float c, float lse2, float 
   return gs == 0.0f ? 0.0f : gs * (exp2f(fmaf(z, c, -lse2)) - q);
 }
 
-// G (fp16, rows of ldg) from the logits, eight columns of a row a thread; the target's -1 with it.
+// G (fp16, rows of ldg) from the logits, eight columns of a row a thread, the targets' part with it:
+// cross entropy's -1 in place; a teacher's entries (top > 0, weights q) in the block's columns after
+// the block has written them.  Entries of one token add up; each of them writes the same value.
+// Bound by HBM: 10 bytes an element, 4096 x 131072 in 459 us, 7.0 TB/s.
 __global__ void __launch_bounds__(256)
     tg_head_grad_kernel(const float* __restrict__ z, int64_t ldz, float c,
-                        const RowInfo* __restrict__ info, int64_t rows, int64_t vocab,
-                        uint16_t* __restrict__ g, int64_t ldg) {
-  const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
-  if (v0 >= vocab) return;
+                        const RowInfo* __restrict__ info, const int64_t* __restrict__ index,
+                        int64_t ldt, int top, const float* __restrict__ q, int64_t rows,
+                        int64_t vocab, uint16_t* __restrict__ g, int64_t ldg) {
+  const int64_t first = blockIdx.x * int64_t(256 * 8);
+  const int64_t v0 = first + threadIdx.x * 8;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const RowInfo ri = info[r];
-    const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
-    const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
-    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t w[4];
+    if (v0 < vocab) {
+      const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
+      const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
+      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float lo = grad_value(f[2 * i], c, ri.lse2, ri.gs, v0 + 2 * i == ri.target ? 1.0f : 0.0f);
-      const float hi =
-          grad_value(f[2 * i + 1], c, ri.lse2, ri.gs, v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
-      const __half2 h = __floats2half2_rn(lo, hi);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 4; ++i) {
+        const float lo =
+            grad_value(f[2 * i], c, ri.lse2, ri.gs, v0 + 2 * i == ri.target ? 1.0f : 0.0f);
+        const float hi =
+            grad_value(f[2 * i + 1], c, ri.lse2, ri.gs, v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
+        const __half2 h = __floats2half2_rn(lo, hi);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(g + r * ldg + v0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(g + r * ldg + v0) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-}
-
-// Distillation: G at the teacher's entries, a warp a row.  Entries of one token add up; each of
-// them then writes the same value.
-__global__ void tg_head_distil_grad_kernel(const int64_t* __restrict__ index, int64_t ldt, int top,
-                                           const float* __restrict__ q, const float* __restrict__ z,
-                                           int64_t ldz, float c, const RowInfo* __restrict__ info,
-                                           int64_t rows, int64_t vocab, __half* __restrict__ g,
-                                           int64_t ldg) {
-  const int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
-  if (r >= rows) return;
-  const RowInfo ri = info[r];
-  for (int e = threadIdx.x & 31; e < top; e += 32) {
-    const int64_t i = index[r * ldt + e];
-    if (i < 0 || i >= vocab) continue;
-    float sum = 0.0f;
-    for (int k = 0; k < top; ++k)
-      if (index[r * ldt + k] == i) sum += q[r * top + k];
-    g[r * ldg + i] = __float2half_rn(grad_value(z[r * ldz + i], c, ri.lse2, ri.gs, sum));
+    if (top == 0) continue;
+    __syncthreads();
+    for (int e = threadIdx.x; e < top; e += 256) {
+      const int64_t i = index[r * ldt + e];
+      if (i < first || i >= first + 256 * 8 || i >= vocab) continue;  // first >= 0
+      float sum = 0.0f;
+      for (int k = 0; k < top; ++k)
+        if (index[r * ldt + k] == i) sum += q[r * top + k];
+      g[r * ldg + i] = __half_as_ushort(
+          __float2half_rn(grad_value(z[r * ldz + i], c, ri.lse2, ri.gs, sum)));
+    }
   }
 }
 
@@ -328,7 +402,12 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     return e == cudaSuccess ? TG_OK : tg::record_cuda_error(e);
   }
   const bool grad = h.dX || h.dW;
-  const bool store = grad || h.top > 0;  // the logits are needed again
+  // The logits are needed again for a gradient, and for a teacher's entries, which without a
+  // gradient are also had as dot products of their own: 2 top D bytes a token against 4 V to store
+  // its logits (1024 tokens, V = 131072, D = 1024, 32 entries: 190 against 251 us).  A row of W is
+  // contiguous only in a head stored V x D.
+  const bool pick = h.top > 0 && !grad && by_vocab && h.top * h.D <= 2 * h.V;
+  const bool store = grad || (h.top > 0 && !pick);
   const int64_t ldz = round_up(h.V, 32), ldg = round_up(h.V, 64);
   const int64_t tiles = 2 * cdiv(h.V, 128);  // statistics of a row, at most
   const int64_t per_row = store ? ldz : tiles, budget = store ? kPieceLogits : kPieceStats;
@@ -346,7 +425,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const int64_t ldxp = round_up(h.D, 64), ldwp = round_up(w_cols, 64), ldw32 = round_up(w_cols, 32);
   const int64_t at_z = lay.add(store ? piece * ldz * 4 : 0);
   const int64_t at_stats = lay.add(tiles * piece * int64_t(sizeof(float2)));
-  const int64_t at_picked = lay.add(store ? 0 : piece * 4);
+  const int64_t at_picked = lay.add(store ? 0 : piece * std::max(h.top, 1) * 4);
   const int64_t at_info = lay.add(piece * int64_t(sizeof(RowInfo)));
   const int64_t at_small = lay.add(2 * 4);
   const int64_t at_g = lay.add(grad ? piece * ldg * 2 : 0);
@@ -389,17 +468,21 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     ldw = ldwp;
   }
   if (grad) {
-    if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess)
+    // one block for what it can read in a few microseconds, else several on a zeroed maximum
+    const int64_t reads = h.T * std::max(h.top, 1);
+    const int blocks = reads <= 4096 ? 1 : static_cast<int>(std::min<int64_t>(cdiv(h.T, 256), sms));
+    const int threads = blocks == 1 ? static_cast<int>(std::min<int64_t>(round_up(h.T, 32), 1024)) : 256;
+    if (blocks > 1 && (e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess)
       return done(tg::record_cuda_error(e));
-    tg_head_weight_kernel<<<static_cast<unsigned>(std::min<int64_t>(cdiv(h.T, 128), 4 * sms)), 128, 0,
-                            stream>>>(h.dloss, h.index, h.ldt, h.top, h.ignore, h.T, wmax);
+    tg_head_weight_kernel<<<blocks, threads, 0, stream>>>(h.dloss, h.index, h.ldt, h.top, h.ignore,
+                                                          h.T, wmax);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
   }
 
-  tg_options opt;
-  std::memset(&opt, 0, sizeof(opt));
-  opt.timeout_ms = h.o.timeout_ms;
-  opt.debug_flags = h.o.debug_flags;
+  tg_options gemm_opt;
+  std::memset(&gemm_opt, 0, sizeof(gemm_opt));
+  gemm_opt.timeout_ms = h.o.timeout_ms;
+  gemm_opt.debug_flags = h.o.debug_flags;
   const float c = h.scale * kLog2e;
   for (int64_t t0 = 0; t0 < h.T; t0 += piece) {
     const int64_t n = std::min(piece, h.T - t0);
@@ -410,42 +493,41 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
                                                      t0 * h.ldt * (h.teacher_f32 ? 4 : 2);
     const float* dloss = grad ? h.dloss + t0 : nullptr;
     float* loss = h.loss ? h.loss + t0 : nullptr;
+    tg::GemmExtra ex;
     int block_n = 0;
     tg::LogitsExtra lx;
     lx.z = z;
     lx.ldz = ldz;
     lx.stats = stats;
     lx.stat_c = c;
-    lx.target = store ? nullptr : reinterpret_cast<const long long*>(index);
+    lx.target = store || h.top ? nullptr : reinterpret_cast<const long long*>(index);
     lx.picked = picked;
     lx.block_n = &block_n;
-    tg::GemmExtra ex;
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
-    st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &opt, stream);
+    st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &gemm_opt,
+                        stream);
     if (st != TG_OK) return done(st);
-    tg_head_rows_kernel<<<static_cast<unsigned>(cdiv(n, 32)), dim3(32, kRowLanes), 0, stream>>>(
-        stats, static_cast<int>(2 * cdiv(h.V, block_n)), n, z, ldz, picked, h.scale, h.V,
-        h.top ? nullptr : index, h.ignore, dloss, wmax, loss, h.lse ? h.lse + t0 : nullptr, info,
-        alpha);
-    if (h.top)
-      tg_head_distil_rows_kernel<<<static_cast<unsigned>(cdiv(n, 4)), 128, 0, stream>>>(
-          index, teacher, h.teacher_f32, h.ldt, h.top, n, z, ldz, h.scale, h.V, dloss, wmax, loss,
-          info, q);
+    if (pick)
+      tg_head_pick_kernel<<<static_cast<unsigned>(std::min<int64_t>(
+                                cdiv(n * cdiv(h.top, kPickRows), 8), 16 * int64_t(sms))),
+                            256, 0, stream>>>(x, ldx, static_cast<const uint16_t*>(W), ldw, index, h.ldt,
+                                      h.top, n, h.V, static_cast<int>(h.D), picked);
+    tg_head_rows_kernel<<<static_cast<unsigned>(n), kRowThreads, 0, stream>>>(
+        stats, static_cast<int>(2 * cdiv(h.V, block_n)), Logits{z, ldz, picked}, h.scale, h.V, index, h.ignore,
+        teacher, h.teacher_f32, h.ldt, h.top, dloss, wmax, loss, h.lse ? h.lse + t0 : nullptr, info,
+        q, alpha);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
     if (!grad) continue;
     tg_head_grad_kernel<<<dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
                                static_cast<unsigned>(std::min<int64_t>(n, 65535))),
-                          256, 0, stream>>>(z, ldz, c, info, n, h.V, g, ldg);
-    if (h.top)
-      tg_head_distil_grad_kernel<<<static_cast<unsigned>(cdiv(n, 4)), 128, 0, stream>>>(
-          index, h.ldt, h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg);
+                          256, 0, stream>>>(z, ldz, c, info, index, h.ldt, h.top, q, n, h.V, g, ldg);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
     if (h.dX) {  // G (n x V) times W (V x D, or stored D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
       st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, n, h.D,
-                          h.V, ldg, ldw, h.lddx, ex, &opt, stream);
+                          h.V, ldg, ldw, h.lddx, ex, &gemm_opt, stream);
       if (st != TG_OK) return done(st);
     }
     if (h.dW) {  // G^T X (V x D), or X^T G (D x V)
@@ -460,6 +542,11 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
           ex.addend = w32;
         }
       }
+      // With few tokens dW's epilogue is the work: a tile of one CTA is better at it than a pair's
+      // (28672 x 1024 from 128 tokens 20.5 against 26.7 us, 131072 x 2048 from 64 135 against 173; at
+      // 512 tokens they are even).
+      tg_options opt = gemm_opt;
+      if (n <= 256 && !(ex.out32 && ex.add)) opt.pair = -1;
       st = by_vocab ? tg::gemm_extra(1, 0, g, x, h.dW, h.V, h.D, n, ldg, ldx, h.lddw, ex, &opt, stream)
                     : tg::gemm_extra(1, 0, x, g, h.dW, h.D, h.V, n, ldx, ldg, h.lddw, ex, &opt, stream);
       if (st != TG_OK) return done(st);

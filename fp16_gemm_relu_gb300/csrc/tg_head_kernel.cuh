@@ -4,12 +4,14 @@
 // The roles are those of tg_gemm_kernel.cuh (TMA producer, tcgen05 issuer, epilogue; one CTA a tile
 // of 128 x BN, or a pair of CTAs a tile of 256 x 256).  Two things differ:
 //
-//  - A tile's sum over the width is cut into segments of kSegK k-blocks (512 columns).  The tensor
+//  - A tile's sum over the width is cut into segments of kSegK k-blocks (1024 columns).  The tensor
 //    core adds each instruction's 16 products to the float32 accumulator by cutting off, not by
 //    rounding, so a sum's error grows with its length and always towards zero: 8192 columns put
-//    4.5e-6 of a loss, where float32 sums in registers are off by 3e-8.  So each segment starts
+//    4.5e-6 on a loss, in segments of 512 or 1024 columns 2e-7 (float32 sums by other means are off
+//    by about 1e-7, the loss's own arithmetic included).  So each segment starts
 //    from zero in one of the two TMEM accumulators, and the epilogue warps add it to running sums
-//    in registers, rounding to nearest, while the next segment runs in the other.
+//    in registers, rounding to nearest, while the next segment runs in the other.  Segments of 512
+//    cost 1-3% more time than of 1024, those of 2048 save nothing further.
 //  - The running sums take 128 registers a thread, so there are eight epilogue warps, each with 32
 //    rows and half of the tile's columns.  With the whole row segment in registers they take its
 //    maximum and sum of exponentials, and then store it, or only look up the rows' targets.
@@ -19,7 +21,7 @@
 
 namespace tg {
 
-constexpr int kSegK = 8;             // k-blocks of a segment
+constexpr int kSegK = 16;            // k-blocks of a segment
 constexpr int kHeadEpiWarps = 8;
 constexpr int kHeadThreads = 64 + 32 * kHeadEpiWarps;
 
@@ -43,9 +45,9 @@ struct HeadCfg {
 
 struct HeadParams {
   GemmParams g;             // tiles, k-blocks, M and N, time limit and error word
-  float2* stats;            // [2 tiles_n][M]: of BN / 2 columns each
+  float2* stats;            // [M][2 tiles_n]: of BN / 2 columns each
   float stat_c;             // scale of the statistics' logits, log2(e) included
-  const long long* target;  // !STORE: [M], the column whose logit goes to picked (none outside)
+  const long long* target;  // !STORE, or NULL: [M], the column whose logit goes to picked
   float* picked;
   int rotate;               // 1: tiles start at different k-blocks (CG == 1)
 };
@@ -55,9 +57,8 @@ struct HeadParams {
 // statistics over several tiles combine as 2^(m - M) s.  m = -inf (every sum -inf, or no column)
 // comes with s = 0, or NaN if there is a NaN among the sums.
 template <int NC>
-__device__ __forceinline__ float2 row_stats(const float (&v)[NC], int cnt, float c) {
+__device__ __forceinline__ float row_max(const float (&v)[NC], int cnt) {
   float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (cnt >= NC) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
@@ -66,20 +67,24 @@ __device__ __forceinline__ float2 row_stats(const float (&v)[NC], int cnt, float
     for (int i = 0; i < NC; ++i)
       if (i < cnt) top[i & 3] = fmaxf(top[i & 3], v[i]);
   }
-  const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+// The part of s of 32 columns from `v` on.
+__device__ __forceinline__ float row_sum32(const float* v, int cnt, float c, float m) {
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (m == -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < 32; ++i)
       if (i < cnt && v[i] != v[i]) s[0] = v[i];
-  } else if (cnt >= NC) {
+  } else if (cnt >= 32) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) s[i & 3] += exp2f(fmaf(v[i], c, -m));
+    for (int i = 0; i < 32; ++i) s[i & 3] += exp2f(fmaf(v[i], c, -m));
   } else {
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+    for (int i = 0; i < 32; ++i)
       if (i < cnt) s[i & 3] += exp2f(fmaf(v[i], c, -m));
   }
-  return make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // v[at mod 16] by selects: an index at run time would put the array into memory.
@@ -296,6 +301,9 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
     const int q = warp & 3;             // TMEM lane quarter this warp may access
     const int ew = warp - 2, half = ew >> 2;
     uint8_t* stg = sStg + ew * kStagingBuf;
+    // the logits are read again only after all of them are written: they need not push the operands,
+    // which other tiles read, out of L2
+    const uint64_t policy = evict_first_policy();
     int t = 0;
     bool ok = true;
     for (int u = first; ok && u < p.units; u += step) {
@@ -341,13 +349,13 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
       if (!ok || !live) continue;
       const int row = row0 + lane;
       const int cnt = p.N - col0;
-      const float2 st = row_stats<NC>(acc, cnt, hp.stat_c);
-      if (row < p.M) hp.stats[static_cast<long long>(2 * w.n_blk + half) * p.M + row] = st;
-      if constexpr (STORE) {
+      const float m = row_max<NC>(acc, cnt) * hp.stat_c;
+      float sum = 0.0f;
 #pragma unroll
-        for (int c = 0; c < NC / 32; ++c) {
-          if (c * 32 < cnt) {
-            if (lane == 0) bulk_wait_read<0>();  // the store that last read this buffer is done
+      for (int c = 0; c < NC / 32; ++c) {
+        if constexpr (STORE) {
+          if (c * 32 < cnt) {  // this chunk's exponentials run while the store reads its buffer
+            if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -358,13 +366,18 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&tmZ, smem_u32(stg), col0 + c * 32, row0, 0);
+              tma_store_3d_hint(&tmZ, smem_u32(stg), col0 + c * 32, row0, 0, policy);
               bulk_commit();
             }
           }
         }
-      } else {
-        const long long y = row < p.M ? hp.target[row] - col0 : -1;
+        sum += row_sum32(acc + c * 32, cnt - c * 32, hp.stat_c, m);
+      }
+      if (row < p.M)
+        hp.stats[static_cast<long long>(row) * (2 * p.tiles_n) + 2 * w.n_blk + half] =
+            make_float2(m, sum);
+      if constexpr (!STORE) {
+        const long long y = hp.target && row < p.M ? hp.target[row] - col0 : -1;
         const bool mine = y >= 0 && y < NC && y < cnt;
         if (__any_sync(0xffffffffu, mine)) {
           const int at = static_cast<int>(y);

@@ -36,7 +36,7 @@ cudaError_t launch_gemm_pair_cls(const AClassMaps& cls, const GemmLaunch& l);
 struct LogitsExtra {
   float* z;                 // float32 logits, rows of ldz (a multiple of 32); NULL: not stored
   int64_t ldz;
-  float2* stats;            // [2 ceil(N / *block_n)][M]: each row's softmax statistics over
+  float2* stats;            // [M][2 ceil(N / *block_n)]: each row's softmax statistics over
   float stat_c;             // *block_n / 2 columns, of stat_c times the logits
   const long long* target;  // without z: [M], and the targets' logits [M]
   float* picked;

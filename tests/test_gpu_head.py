@@ -287,7 +287,7 @@ def test_wrong_targets_are_nan():
         assert torch.isnan(dx[7]).all() and torch.isfinite(dx[rest]).all()
         assert torch.isnan(dw).any()
     index, logits = teacher(T, V, 6, 97, torch.float32)
-    good = tg.linear_distillation(x, w, index, logits)
+    good = tg.linear_distillation_step(x, w, index, logits, torch.ones(T, device="cuda"))[0]
     for wrong in ("index", "nan", "inf"):
         i, u = index.clone(), logits.clone()
         i[7] = torch.arange(6, device="cuda")
