@@ -686,12 +686,22 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
                                                 const uint32_t (&r1)[32], int row0, int col0,
                                                 uint8_t* stg, int& sb, int lane) {
   uint32_t pk[32];
-  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu &&
-      p.alpha == nullptr && p.addend == nullptr) {
+  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu && p.addend == nullptr) {
+    if (p.alpha) {
+      const float a = __ldg(p.alpha);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        pk[i] = relu_pack_h2(__float_as_uint(__uint_as_float(r0[2 * i]) * a),
+                             __float_as_uint(__uint_as_float(r0[2 * i + 1]) * a), p.act);
+        pk[16 + i] = relu_pack_h2(__float_as_uint(__uint_as_float(r1[2 * i]) * a),
+                                  __float_as_uint(__uint_as_float(r1[2 * i + 1]) * a), p.act);
+      }
+    } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       pk[i] = relu_pack_h2(r0[2 * i], r0[2 * i + 1], p.act);
       pk[16 + i] = relu_pack_h2(r1[2 * i], r1[2 * i + 1], p.act);
+    }
     }
   } else {
     // general fused epilogue, 32 columns at a time; columns past N and rows past M are

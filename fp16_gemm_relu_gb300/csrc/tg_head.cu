@@ -293,6 +293,9 @@ __global__ void __launch_bounds__(256)
   const int64_t v0 = first + threadIdx.x * 8;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const RowInfo ri = info[r];
+    // entries are read ahead of the columns: after them their latency stood alone (4096 x 65537 with
+    // 64 entries: 324 us, cross entropy 235)
+    const int64_t ahead = threadIdx.x < top ? index[r * ldt + threadIdx.x] : -1;
     if (v0 < vocab) {
       const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
       const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(256)
     if (top == 0) continue;
     __syncthreads();
     for (int e = threadIdx.x; e < top; e += 256) {
-      const int64_t i = index[r * ldt + e];
+      const int64_t i = e < 256 ? ahead : index[r * ldt + e];
       if (i < first || i >= first + 256 * 8 || i >= vocab) continue;  // first >= 0
       float sum = 0.0f;
       for (int k = 0; k < top; ++k)

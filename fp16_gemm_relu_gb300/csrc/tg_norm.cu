@@ -24,6 +24,31 @@
 
 namespace {
 
+// 16 bytes of the 32 in (lo, hi), from byte s on (even, below 16).  s is the same for a row's
+// threads, so this branches on it, where selects by its bits would be 20 instructions.
+template <int WORD, bool HALF>
+__device__ __forceinline__ uint4 shifted(const uint32_t (&w)[8]) {
+  if constexpr (HALF)
+    return make_uint4(__funnelshift_r(w[WORD], w[WORD + 1], 16),
+                      __funnelshift_r(w[WORD + 1], w[WORD + 2], 16),
+                      __funnelshift_r(w[WORD + 2], w[WORD + 3], 16),
+                      __funnelshift_r(w[WORD + 3], w[WORD + 4], 16));
+  return make_uint4(w[WORD], w[WORD + 1], w[WORD + 2], w[WORD + 3]);
+}
+__device__ __forceinline__ uint4 shift16(const uint4& lo, const uint4& hi, uint32_t s) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  switch (s) {
+    case 0: return lo;
+    case 2: return shifted<0, true>(w);
+    case 4: return shifted<1, false>(w);
+    case 6: return shifted<1, true>(w);
+    case 8: return shifted<2, false>(w);
+    case 10: return shifted<2, true>(w);
+    case 12: return shifted<3, false>(w);
+    default: return shifted<3, true>(w);
+  }
+}
+
 // Eight fp16 values of a row: elements [8c, 8c + 8), zeros from n on.  b: the bytes by which the
 // row's start misses a 16-byte boundary (even).  With b == 0 a whole chunk is one 16-byte load.
 // Otherwise it lies in two aligned blocks, which are loaded and shifted together where both lie
@@ -38,17 +63,7 @@ __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int c, int n) {
   if (b == 0 && e0 + 8 <= n) return __ldg(reinterpret_cast<const uint4*>(row + e0));
   if (b != 0 && c > 0 && e0 + 16 - static_cast<int>(b >> 1) <= n) {
     const uint4* blk = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(row) - b) + c;
-    const uint4 lo = __ldg(blk), hi = __ldg(blk + 1);
-    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    const uint32_t q = b >> 2;
-    uint32_t t[7], u[5], o[4];
-#pragma unroll
-    for (int i = 0; i < 7; ++i) t[i] = (q & 1u) ? w[i + 1] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) u[i] = (q & 2u) ? t[i + 2] : t[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (b & 2u) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    return shift16(__ldg(blk), __ldg(blk + 1), b);
   }
   uint32_t o[4];
 #pragma unroll
@@ -85,31 +100,21 @@ __device__ __forceinline__ void store_chunk(uint16_t* row, int c, int n, uint4 v
     return;
   }
   const int own = 8 - static_cast<int>(b >> 1);  // elements of this chunk in its aligned block
-  uint32_t w[8];
-  w[4] = v.x;
-  w[5] = v.y;
-  w[6] = v.z;
-  w[7] = v.w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, w[4 + i], 1);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint4 before;
+  before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
+  before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
+  before.z = __shfl_up_sync(0xffffffffu, v.z, 1);
+  before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
   const bool whole = lane > 0 && e0 + own <= n;
   const bool next_whole = lane < 31 && e0 + 8 + own <= n;
-  if (whole) {  // 16 bytes of w, starting 16 - b bytes in
-    const uint32_t s = 16u - b, q = s >> 2;
-    uint32_t t[7], u[5], o[4];
-#pragma unroll
-    for (int i = 0; i < 7; ++i) t[i] = (q & 1u) ? w[i + 1] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) u[i] = (q & 2u) ? t[i + 2] : t[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (s & 2u) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
-    *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(row + e0) - b) =
-        make_uint4(o[0], o[1], o[2], o[3]);
-  }
+  const uint4 o = shift16(before, v, 16u - b);
+  if (whole) *reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(row + e0) - b) = o;
+  if (whole && next_whole) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const bool covered = i < own ? whole : next_whole;
-    if (!covered && e0 + i < n) row[e0 + i] = static_cast<uint16_t>(w[4 + (i >> 1)] >> ((i & 1) << 4));
+    if (!covered && e0 + i < n) row[e0 + i] = static_cast<uint16_t>(w[i >> 1] >> ((i & 1) << 4));
   }
 }
 
@@ -280,24 +285,16 @@ __device__ __forceinline__ void slot_chunk(const uint8_t* slot, uint32_t b, int 
     const uint4* blk = reinterpret_cast<const uint4*>(slot) + c;
     v = blk[0];
     if constexpr (!VEC) {
-      const uint4 hi = blk[1];
-      const uint32_t w[8] = {v.x, v.y, v.z, v.w, hi.x, hi.y, hi.z, hi.w};
-      const uint32_t q = b >> 2;
-      uint32_t t[7], u[5], o[4];
-#pragma unroll
-      for (int i = 0; i < 7; ++i) t[i] = (q & 1u) ? w[i + 1] : w[i];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) u[i] = (q & 2u) ? t[i + 2] : t[i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = (b & 2u) ? __funnelshift_r(u[i], u[i + 1], 16) : u[i];
+      v = shift16(v, blk[1], b);
       if (e0 + 8 > n) {
+        uint32_t o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (e0 + 2 * i >= n) o[i] = 0u;
           else if (e0 + 2 * i + 1 >= n) o[i] &= 0xFFFFu;
         }
+        v = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      v = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
   unpack8(v, f);
@@ -829,44 +826,39 @@ __global__ void __launch_bounds__(THREADS)
   }
 }
 
-// dgamma and dbeta from the blocks' partial rows, in a fixed order: 32 columns a block, four a
-// thread; each of the 32 thread rows adds every 32nd partial row, four loads in flight, then the
-// thread rows are added in order.  Bound by the latency of its few loads: 304 partial rows of 8192
-// columns (20 MB, in L2) took 9.5 us with one load in flight and 16 thread rows.
+// dgamma (blockIdx.y 0) or dbeta (1) from the blocks' partial rows, in a fixed order: 32 columns a
+// block, four a thread; each of the 32 thread rows adds every 32nd partial row, eight loads in
+// flight, then the thread rows are added in order.  The partial rows (304 of 4096 columns: 10 MB)
+// are in L2; the latency of the few loads bounds it.
 constexpr int kPartRows = 32;
 template <typename P>
 __global__ void __launch_bounds__(8 * kPartRows)
     tg_layernorm_params_kernel(const float* __restrict__ part, int parts, int64_t np, int n,
                                P* dgamma, P* dbeta) {
-  __shared__ float4 sum[2][kPartRows][8];
+  __shared__ float4 sum[kPartRows][8];
+  P* out = blockIdx.y == 0 ? dgamma : dbeta;
+  if (out == nullptr) return;
   const int j = blockIdx.x * 32 + threadIdx.x * 4;  // np is a multiple of 4
-  float4 acc[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    acc[w] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (j >= n) continue;
-    const float* src = part + int64_t(w) * parts * np + j;
-#pragma unroll 4
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (j < n) {
+    const float* src = part + int64_t(blockIdx.y) * parts * np + j;
+#pragma unroll 8
     for (int p = threadIdx.y; p < parts; p += kPartRows) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(src + p * np));
-      acc[w].x += v.x;
-      acc[w].y += v.y;
-      acc[w].z += v.z;
-      acc[w].w += v.w;
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
     }
   }
-  sum[0][threadIdx.y][threadIdx.x] = acc[0];
-  sum[1][threadIdx.y][threadIdx.x] = acc[1];
+  sum[threadIdx.y][threadIdx.x] = acc;
   __syncthreads();
-  const int e = threadIdx.y * 8 + threadIdx.x;  // 32 columns of both
-  if (e >= 64 || blockIdx.x * 32 + (e & 31) >= n) return;
-  P* out = e < 32 ? dgamma : dbeta;
-  if (out == nullptr) return;
+  const int e = threadIdx.y * 8 + threadIdx.x;
+  if (e >= 32 || blockIdx.x * 32 + e >= n) return;
   float s = 0.0f;
 #pragma unroll
-  for (int p = 0; p < kPartRows; ++p)
-    s += reinterpret_cast<const float*>(&sum[e >> 5][p][0])[e & 31];
-  put(out + blockIdx.x * 32 + (e & 31), s);
+  for (int p = 0; p < kPartRows; ++p) s += reinterpret_cast<const float*>(&sum[p][0])[e];
+  put(out + blockIdx.x * 32 + e, s);
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -994,8 +986,8 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
                   : go(tg_layernorm_backward_kernel<4, 2, VEC, P>);
   }
   if (e != cudaSuccess || part == nullptr) return e;
-  tg_layernorm_params_kernel<P><<<static_cast<unsigned>(cdiv(n, 32)), dim3(8, kPartRows), 0, st>>>(
-      part, s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
+  tg_layernorm_params_kernel<P><<<dim3(static_cast<unsigned>(cdiv(n, 32)), 2), dim3(8, kPartRows), 0,
+                                  st>>>(part, s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
   return cudaGetLastError();
 }
 

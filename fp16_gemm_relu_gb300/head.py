@@ -40,18 +40,18 @@ def _sizes(x, weight, layout):
     V, wd = weight.shape if layout == TG_HEAD_VOCAB_MAJOR else weight.shape[::-1]
     if wd != D:
         raise ValueError(f"x has width {D}, weight {wd}")
-    if weight.device != x.device:
+    if weight.get_device() != x.get_device():
         raise ValueError("weight must be on x's device")
     return T, V, D, ldx, ldw
 
 
-def _teacher(index, logits, T, device):
+def _teacher(index, logits, T, dev):
     if index.dtype != torch.int64:
         raise TypeError("teacher_index must be torch.int64")
     kind = param_type(logits, "teacher_logits")
     if index.dim() != 2 or index.shape[0] != T or logits.shape != index.shape:
         raise ValueError(f"teacher_index and teacher_logits must be ({T}, top)")
-    if index.device != device or logits.device != device:
+    if index.get_device() != dev or logits.get_device() != dev:
         raise ValueError("the teacher's entries must be on x's device")
     top = index.shape[1]
     if not 1 <= top <= binding.TG_HEAD_MAX_TOP:
@@ -69,20 +69,20 @@ def _outputs(x, weight, T, D, need_dx, need_dw, want_lse):
             torch.empty(weight.shape, dtype=torch.float16, device=dev) if need_dw else None)
 
 
-def _weights(dloss, T, device):
+def _weights(dloss, T, dev):
     if dloss is not None:
         if dloss.dtype is not torch.float32:
             raise TypeError("dloss must be torch.float32")
-        vector(dloss, T, device, "dloss")
+        vector(dloss, T, dev, "dloss")
 
 
 def _cross_entropy(x, weight, target, dloss, need_dx, need_dw, want_lse, ignore_index, logit_scale,
                    layout, piece_rows, stream):
     """(loss, lse, dx, dweight), None for what is not wanted."""
     T, V, D, ldx, ldw = _sizes(x, weight, layout)
-    dev = x.device
+    dev = x.get_device()
     if not here(dev, stream):
-        with on(dev, stream, x, weight, target, dloss):
+        with on(x.device, stream, x, weight, target, dloss):
             return _cross_entropy(x, weight, target, dloss, need_dx, need_dw, want_lse,
                                   ignore_index, logit_scale, layout, piece_rows, None)
     if target.dtype is not torch.int64:
@@ -94,7 +94,7 @@ def _cross_entropy(x, weight, target, dloss, need_dx, need_dw, want_lse, ignore_
     check(library().tg_linear_cross_entropy_f16(
         x.data_ptr(), weight.data_ptr(), target.data_ptr(), ignore_index, logit_scale, ptr(dloss),
         loss.data_ptr(), ptr(lse), ptr(dx), ptr(dw), T, V, D, ldx, ldw, D, weight.shape[1],
-        _options(layout, piece_rows), stream_handle(dev.index)), "tg_linear_cross_entropy_f16")
+        _options(layout, piece_rows), stream_handle(dev)), "tg_linear_cross_entropy_f16")
     return out
 
 
@@ -102,9 +102,9 @@ def _distillation(x, weight, teacher_index, teacher_logits, dloss, need_dx, need
                   temperature, layout, piece_rows, stream):
     """(loss, lse, dx, dweight), None for what is not wanted."""
     T, V, D, ldx, ldw = _sizes(x, weight, layout)
-    dev = x.device
+    dev = x.get_device()
     if not here(dev, stream):
-        with on(dev, stream, x, weight, teacher_index, teacher_logits, dloss):
+        with on(x.device, stream, x, weight, teacher_index, teacher_logits, dloss):
             return _distillation(x, weight, teacher_index, teacher_logits, dloss, need_dx, need_dw,
                                  want_lse, temperature, layout, piece_rows, None)
     top, kind = _teacher(teacher_index, teacher_logits, T, dev)
@@ -114,7 +114,7 @@ def _distillation(x, weight, teacher_index, teacher_logits, dloss, need_dx, need
     check(library().tg_linear_distill_f16(
         x.data_ptr(), weight.data_ptr(), teacher_index.data_ptr(), teacher_logits.data_ptr(), kind,
         top, top, temperature, ptr(dloss), loss.data_ptr(), ptr(lse), ptr(dx), ptr(dw), T, V, D,
-        ldx, ldw, D, weight.shape[1], _options(layout, piece_rows), stream_handle(dev.index)),
+        ldx, ldw, D, weight.shape[1], _options(layout, piece_rows), stream_handle(dev)),
         "tg_linear_distill_f16")
     return out
 

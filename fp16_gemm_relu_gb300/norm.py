@@ -25,9 +25,9 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False,
     Runs on ``stream`` (default: torch's current stream) and returns without synchronising.
     """
     ldx = rows(x, "x")
-    dev = x.device
+    dev = x.get_device()
     if not here(dev, stream):
-        with on(dev, stream, x, gamma, beta, out):
+        with on(x.device, stream, x, gamma, beta, out):
             return layer_norm(x, gamma, beta, eps, stats, out)
     M, N = x.shape
     kind = binding.TG_TYPE_F16
@@ -40,19 +40,19 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False,
         if gamma is not None and gamma.dtype is not beta.dtype:
             raise TypeError("gamma and beta must have one type")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.float16, device=dev)
+        out = torch.empty((M, N), dtype=torch.float16, device=x.device)
         ldy = N
     else:
-        if out.shape != x.shape or out.device != dev:
+        if out.shape != x.shape or out.get_device() != dev:
             raise ValueError("out must be an (M, N) tensor on x's device")
         ldy = rows(out, "out")
     mean = rstd = None
     if stats:
-        mean = torch.empty(M, dtype=torch.float32, device=dev)
-        rstd = torch.empty(M, dtype=torch.float32, device=dev)
+        mean = torch.empty(M, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
     check(library().tg_layernorm_f16(x.data_ptr(), ptr(gamma), ptr(beta), out.data_ptr(), ptr(mean),
                                      ptr(rstd), M, N, ldx, ldy, eps, kind,
-                                     stream_handle(dev.index)), "tg_layernorm_f16")
+                                     stream_handle(dev)), "tg_layernorm_f16")
     return (out, mean, rstd) if stats else out
 
 
@@ -63,12 +63,12 @@ def layer_norm_backward(dy, x, mean, rstd, gamma=None, param_grads: bool = True,
     are None and not computed.
     """
     lddy, ldx = rows(dy, "dy"), rows(x, "x")
-    dev = x.device
+    dev = x.get_device()
     if not here(dev, stream):
-        with on(dev, stream, dy, x, mean, rstd, gamma):
+        with on(x.device, stream, dy, x, mean, rstd, gamma):
             return layer_norm_backward(dy, x, mean, rstd, gamma, param_grads)
     M, N = x.shape
-    if dy.shape != x.shape or dy.device != dev:
+    if dy.shape != x.shape or dy.get_device() != dev:
         raise ValueError("dy must have x's shape and device")
     vector(mean, M, dev, "mean")
     vector(rstd, M, dev, "rstd")
@@ -78,13 +78,14 @@ def layer_norm_backward(dy, x, mean, rstd, gamma=None, param_grads: bool = True,
     if gamma is not None:
         kind, dtype = param_type(gamma, "gamma"), gamma.dtype
         vector(gamma, N, dev, "gamma")
-    dx = torch.empty((M, N), dtype=torch.float16, device=dev)
+    device = x.device
+    dx = torch.empty((M, N), dtype=torch.float16, device=device)
     dgamma = dbeta = None
     if param_grads:
-        dgamma = torch.empty(N, dtype=dtype, device=dev)
-        dbeta = torch.empty(N, dtype=dtype, device=dev)
+        dgamma = torch.empty(N, dtype=dtype, device=device)
+        dbeta = torch.empty(N, dtype=dtype, device=device)
     check(library().tg_layernorm_backward_f16(
         dy.data_ptr(), x.data_ptr(), ptr(gamma), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(),
-        ptr(dgamma), ptr(dbeta), M, N, lddy, ldx, N, kind, stream_handle(dev.index)),
+        ptr(dgamma), ptr(dbeta), M, N, lddy, ldx, N, kind, stream_handle(dev)),
         "tg_layernorm_backward_f16")
     return dx, dgamma, dbeta

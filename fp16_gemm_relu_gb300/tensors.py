@@ -42,15 +42,18 @@ def param_type(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name} must be torch.float16 or torch.float32")
 
 
-def vector(t: torch.Tensor, n: int, device: torch.device, name: str) -> None:
-    """A dense vector of n values on `device`."""
-    if t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
+def vector(t: torch.Tensor, n: int, index: int, name: str) -> None:
+    """A dense vector of n values on the CUDA device `index`."""
+    if t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous ({n},) tensor on x's device")
 
 
-def here(device: torch.device, stream) -> bool:
+def here(index: int, stream) -> bool:
     """Whether a call goes to torch's current stream of the current device."""
-    return stream is None and device.index == torch.cuda.current_device()
+    return stream is None and index == _current_device()
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 @contextlib.contextmanager
