@@ -284,6 +284,7 @@ __device__ __forceinline__ float grad_value(float z, float c, float lse2, float 
 // cross entropy's -1 in place; a teacher's entries (top > 0, weights q) in the block's columns after
 // the block has written them.  Entries of one token add up; each of them writes the same value.
 // Bound by HBM: 10 bytes an element, 4096 x 131072 in 459 us, 7.0 TB/s.
+template <bool TEACHER>
 __global__ void __launch_bounds__(256)
     tg_head_grad_kernel(const float* __restrict__ z, int64_t ldz, float c,
                         const RowInfo* __restrict__ info, const int64_t* __restrict__ index,
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(256)
     const RowInfo ri = info[r];
     // entries are read ahead of the columns: after them their latency stood alone (4096 x 65537 with
     // 64 entries: 324 us, cross entropy 235)
-    const int64_t ahead = threadIdx.x < top ? index[r * ldt + threadIdx.x] : -1;
+    const int64_t ahead = TEACHER && threadIdx.x < top ? index[r * ldt + threadIdx.x] : -1;
     if (v0 < vocab) {
       const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
       const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
@@ -304,15 +305,17 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float lo =
-            grad_value(f[2 * i], c, ri.lse2, ri.gs, v0 + 2 * i == ri.target ? 1.0f : 0.0f);
+            grad_value(f[2 * i], c, ri.lse2, ri.gs,
+                       !TEACHER && v0 + 2 * i == ri.target ? 1.0f : 0.0f);
         const float hi =
-            grad_value(f[2 * i + 1], c, ri.lse2, ri.gs, v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
+            grad_value(f[2 * i + 1], c, ri.lse2, ri.gs,
+                       !TEACHER && v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
         const __half2 h = __floats2half2_rn(lo, hi);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       *reinterpret_cast<uint4*>(g + r * ldg + v0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (top == 0) continue;
+    if constexpr (!TEACHER) continue;
     __syncthreads();
     for (int e = threadIdx.x; e < top; e += 256) {
       const int64_t i = e < 256 ? ahead : index[r * ldt + e];
@@ -522,9 +525,14 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
         q, alpha);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
     if (!grad) continue;
-    tg_head_grad_kernel<<<dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
-                               static_cast<unsigned>(std::min<int64_t>(n, 65535))),
-                          256, 0, stream>>>(z, ldz, c, info, index, h.ldt, h.top, q, n, h.V, g, ldg);
+    const dim3 cells(static_cast<unsigned>(cdiv(h.V, 2048)),
+                     static_cast<unsigned>(std::min<int64_t>(n, 65535)));
+    if (h.top)
+      tg_head_grad_kernel<true><<<cells, 256, 0, stream>>>(z, ldz, c, info, index, h.ldt, h.top, q,
+                                                           n, h.V, g, ldg);
+    else
+      tg_head_grad_kernel<false><<<cells, 256, 0, stream>>>(z, ldz, c, info, index, h.ldt, h.top, q,
+                                                            n, h.V, g, ldg);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
     if (h.dX) {  // G (n x V) times W (V x D, or stored D x V)
       std::memset(&ex, 0, sizeof(ex));

@@ -200,6 +200,27 @@ __device__ __forceinline__ void load_param(const P* p, int c, int n, float none,
   for (int i = 0; i < 4; ++i) f[i] = pair(g[2 * i], g[2 * i + 1]);
 }
 
+// Eight columns from e0 on of a partial row of dgamma and dbeta (16-byte aligned rows).
+__device__ __forceinline__ void put_part(float* to_g, float* to_b, int e0, int n, const f32x2 (&g)[4],
+                                         const f32x2 (&b)[4]) {
+  if (e0 + 8 <= n) {
+    ulonglong2* pg = reinterpret_cast<ulonglong2*>(to_g + e0);
+    ulonglong2* pb = reinterpret_cast<ulonglong2*>(to_b + e0);
+    pg[0] = make_ulonglong2(g[0], g[1]);
+    pg[1] = make_ulonglong2(g[2], g[3]);
+    pb[0] = make_ulonglong2(b[0], b[1]);
+    pb[1] = make_ulonglong2(b[2], b[3]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = e0 + 2 * j;
+    const float2 fg = halves(g[j]), fb = halves(b[j]);
+    if (e < n) to_g[e] = fg.x, to_b[e] = fb.x;
+    if (e + 1 < n) to_g[e + 1] = fg.y, to_b[e + 1] = fb.y;
+  }
+}
+
 // ---------------------------------------------------------------------------------------
 // Rows through shared memory.  A group of threads (a warp, or several) works on one row at a time;
 // its first thread fetches rows ahead into a ring of slots with bulk copies, so the next rows'
@@ -277,8 +298,7 @@ __device__ __forceinline__ f32x2 there(int col, int n) {
 // row's (0 with VEC).  Otherwise the two blocks that hold them are shifted together: with 4-byte
 // reads at the row's own offset, a warp's pairs contiguous, 8192 x 4096 forward took 63 us, not 37.
 template <bool VEC>
-__device__ __forceinline__ void slot_chunk(const uint8_t* slot, uint32_t b, int c, int n,
-                                           f32x2 (&f)[4]) {
+__device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int c, int n) {
   uint4 v = make_uint4(0, 0, 0, 0);
   const int e0 = c << 3;
   if (e0 < n) {
@@ -297,7 +317,7 @@ __device__ __forceinline__ void slot_chunk(const uint8_t* slot, uint32_t b, int 
       }
     }
   }
-  unpack8(v, f);
+  return v;
 }
 
 // The threads of a group meet (id: the group's number in the block).  barrier.sync, not bar.sync:
@@ -403,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      slot_chunk<VEC>(ring + s * slot_bytes, b, i * tpr + t, n, v[i]);
+      unpack8(slot_chunk<VEC>(ring + s * slot_bytes, b, i * tpr + t, n), v[i]);
       acc = add2(acc, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
     }
     const float mu = group_sum(sum2(acc), tpr, group, sums[group][0]) * inv_n;
@@ -500,23 +520,31 @@ __global__ void __launch_bounds__(512)
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
-  // x, d = dy and gamma of the row in a slot; past the row's end d is 0
-  auto terms = [&](const uint8_t* slot, unsigned row, int i, f32x2(&v)[4], f32x2(&d)[4],
-                   f32x2(&g)[4]) {
+  // x and dy of chunk i of the row in a slot; past the row's end both are 0
+  auto read = [&](const uint8_t* slot, unsigned row, int i, uint4& xv, uint4& dv) {
     const int c = i * tpr + t;
-    slot_chunk<VEC>(slot, VEC ? 0u : row_shift(x, ldx, row), c, n, v);
-    slot_chunk<VEC>(slot + slot_bytes, VEC ? 0u : row_shift(dy, lddy, row), c, n, d);
-    staged(sg, c, chunks, g);
+    xv = slot_chunk<VEC>(slot, VEC ? 0u : row_shift(x, ldx, row), c, n);
+    dv = slot_chunk<VEC>(slot + slot_bytes, VEC ? 0u : row_shift(dy, lddy, row), c, n);
   };
-  // With u = x - mean, h = u rstd and g = d gamma: this thread's part of the sums of g and of g u (= g h / rstd)
-  // of a row, into sums[turn], and the row's part of dgamma (d u, times rstd) and dbeta
+  // With two chunks a thread a row stays in registers from its sums to its dx; with four it is read
+  // from its slot again.
+  constexpr bool kCarry = CH <= 2;
+  uint4 cx[kCarry ? CH : 1], cd[kCarry ? CH : 1];    // of row k
+  uint4 nx[kCarry ? CH : 1], nd[kCarry ? CH : 1];    // of row k + 1
+  // With u = x - mean, h = u rstd and g = d gamma: this thread's part of the sums of g and of g u
+  // (= g h / rstd) of a row, into sums[turn], and the row's part of dgamma (d u, times rstd) and
+  // dbeta
   auto sum_row = [&](const uint8_t* slot, unsigned row, float mu, float rs, int turn) {
     const f32x2 less = pair(-mu, -mu), times = pair(rs, rs);
     f32x2 a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+      const int k = kCarry ? i : 0;
       f32x2 v[4], d[4], g[4];
-      terms(slot, row, i, v, d, g);
+      read(slot, row, i, nx[k], nd[k]);
+      unpack8(nx[k], v);
+      unpack8(nd[k], d);
+      staged(sg, i * tpr + t, chunks, g);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const f32x2 du = mul2(d[j], add2(v[j], less));
@@ -541,6 +569,14 @@ __global__ void __launch_bounds__(512)
     slot_wait(tg::smem_u32(&bars[group][0]), 0, &late, err);
     sum_row(ring, first, mu, rs, 0);
   }
+  auto carry = [&]() {
+#pragma unroll
+    for (int i = 0; i < (kCarry ? CH : 0); ++i) {
+      cx[i] = nx[i];
+      cd[i] = nd[i];
+    }
+  };
+  carry();
   group_sync(tpr, group);
   const int64_t dx_step = int64_t(step) * lddx;
   uint16_t* dxr = dx + first * lddx;
@@ -571,14 +607,19 @@ __global__ void __launch_bounds__(512)
       const f32x2 of_x = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
+        const int c = kCarry ? i : 0;
         f32x2 v[4], d[4], g[4];
-        terms(ring + s * 2 * slot_bytes, r, i, v, d, g);
+        if constexpr (!kCarry) read(ring + s * 2 * slot_bytes, r, i, cx[0], cd[0]);
+        unpack8(cx[c], v);
+        unpack8(cd[c], d);
+        staged(sg, i * tpr + t, chunks, g);
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[j] = fma2(d[j], mul2(g[j], times), fma2(v[j], of_x, plus));
         store_chunk<VEC>(dxr, i * tpr + t, n, pack8(g), lane);
       }
     }
     mu = mu1, rs = rs1, mu1 = mu2, rs1 = rs2;
+    carry();
     group_sync(tpr, group);  // slot s and sums[k & 1] are free, sums[(k + 1) & 1] is written
     if (t == 0 && k + S < count) fetch(k + S, s);
     s = s1;
@@ -596,15 +637,7 @@ __global__ void __launch_bounds__(512)
   float* to_g = per_block == 1 ? out_g : groups + int64_t(group) * 2 * np;
   float* to_b = per_block == 1 ? out_b : to_g + np;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = ((i * tpr + t) << 3) + 2 * j;
-      const float2 fg = halves(dg[i][j]), fb = halves(db[i][j]);
-      if (e < n) to_g[e] = fg.x, to_b[e] = fb.x;
-      if (e + 1 < n) to_g[e + 1] = fg.y, to_b[e + 1] = fb.y;
-    }
-  }
+  for (int i = 0; i < CH; ++i) put_part(to_g, to_b, (i * tpr + t) << 3, n, dg[i], db[i]);
   if (per_block == 1) return;
   __syncthreads();
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
@@ -803,15 +836,7 @@ __global__ void __launch_bounds__(THREADS)
   float* to_g = BLOCK ? out_g : groups + int64_t(threadIdx.x >> 5) * 2 * np;
   float* to_b = BLOCK ? out_b : to_g + np;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int e0 = (i * tpr + t) << 3;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 fg = halves(dg[i][j]), fb = halves(db[i][j]);
-      if (e0 + 2 * j < n) to_g[e0 + 2 * j] = fg.x, to_b[e0 + 2 * j] = fb.x;
-      if (e0 + 2 * j + 1 < n) to_g[e0 + 2 * j + 1] = fg.y, to_b[e0 + 2 * j + 1] = fb.y;
-    }
-  }
+  for (int i = 0; i < CH; ++i) put_part(to_g, to_b, (i * tpr + t) << 3, n, dg[i], db[i]);
   if constexpr (!BLOCK) {  // the block's warps are added in their order
     __syncthreads();
     for (int e = threadIdx.x; e < n; e += THREADS) {
