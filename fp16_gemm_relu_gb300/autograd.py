@@ -6,13 +6,20 @@ Forward:  C = fp16(relu(A·B))                         tg_gemm_relu_f16
 Backward: dZ = C > 0 ? dC : +0                        tg_relu_backward_f16
           dA = dZ·B^T  (fp32 accumulate, fp16 out)    tg_gemm_f16_t(trans_b = 1)
           dB = A^T·dZ                                  tg_gemm_f16_t(trans_a = 1)
+
+Likewise layer normalisation and the losses of a linear head: layer_norm, linear_cross_entropy and
+linear_distillation.  The losses' forward pass is the loss alone and their backward pass the whole
+step (the logits are computed again, not kept); head.linear_cross_entropy_step and
+head.linear_distillation_step give loss and gradients in one call where the upstream gradient is
+known beforehand, a quarter of the products fewer.
 """
 
 from __future__ import annotations
 
 import torch
 
-from . import binding
+from . import binding, head, norm
+from .binding import TG_HEAD_VOCAB_MAJOR
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -66,3 +73,92 @@ class ReluMatmul(torch.autograd.Function):
 def relu_matmul(A: torch.Tensor, B: torch.Tensor) -> torch.Tensor:
     """Differentiable C = relu(A·B) for CUDA fp16 tensors."""
     return ReluMatmul.apply(A, B)
+
+
+class LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps):
+        y, mean, rstd = norm.layer_norm(x, gamma, beta, eps, stats=True)
+        ctx.save_for_backward(x, gamma, mean, rstd)
+        ctx.beta_dtype = None if beta is None else beta.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, gamma, mean, rstd = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        dx, dgamma, dbeta = norm.layer_norm_backward(dy.to(torch.float16).contiguous(), x, mean,
+                                                     rstd, gamma, param_grads=want[1] or want[2])
+        if want[2] and dbeta.dtype != ctx.beta_dtype:  # a beta without a gamma
+            dbeta = dbeta.to(ctx.beta_dtype)
+        return (dx if want[0] else None, dgamma if want[1] else None, dbeta if want[2] else None,
+                None)
+
+
+def layer_norm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-5) -> torch.Tensor:
+    """Differentiable layer normalisation of the rows of a CUDA fp16 (M, N) tensor."""
+    return LayerNorm.apply(x, gamma, beta, eps)
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, target, ignore_index, logit_scale, layout):
+        ctx.save_for_backward(x, weight, target)
+        ctx.args = (ignore_index, logit_scale, layout)
+        return head.linear_cross_entropy(x, weight, target, ignore_index, logit_scale, layout)
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x, weight, target = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        _, _, dx, dw = head._cross_entropy(x, weight, target, dloss.contiguous(), want[0], want[1],
+                                           False, *ctx.args, 0, None)
+        return dx, dw, None, None, None, None
+
+
+class LinearDistillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, teacher_index, teacher_logits, temperature, layout):
+        ctx.save_for_backward(x, weight, teacher_index, teacher_logits)
+        ctx.args = (temperature, layout)
+        return head.linear_distillation(x, weight, teacher_index, teacher_logits, temperature,
+                                        layout)
+
+    @staticmethod
+    def backward(ctx, dloss):
+        x, weight, teacher_index, teacher_logits = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        _, _, dx, dw = head._distillation(x, weight, teacher_index, teacher_logits,
+                                          dloss.contiguous(), want[0], want[1], False, *ctx.args,
+                                          0, None)
+        return dx, dw, None, None, None, None
+
+
+def _reduce(loss, count, reduction):
+    if reduction == "none":
+        return loss
+    if reduction == "sum":
+        return loss.sum()
+    if reduction == "mean":
+        return loss.sum() / count().clamp_min(1)
+    raise ValueError("reduction must be none, sum or mean")
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
+                         ignore_index: int = -100, reduction: str = "mean",
+                         logit_scale: float = 1.0,
+                         layout: int = TG_HEAD_VOCAB_MAJOR) -> torch.Tensor:
+    """Differentiable cross entropy of x @ weight.T (see head.linear_cross_entropy); "mean" is over the
+    rows whose target is not ignore_index."""
+    loss = LinearCrossEntropy.apply(x, weight, target, ignore_index, logit_scale, layout)
+    return _reduce(loss, lambda: (target != ignore_index).sum(), reduction)
+
+
+def linear_distillation(x: torch.Tensor, weight: torch.Tensor, teacher_index: torch.Tensor,
+                        teacher_logits: torch.Tensor, temperature: float = 1.0,
+                        reduction: str = "mean",
+                        layout: int = TG_HEAD_VOCAB_MAJOR) -> torch.Tensor:
+    """Differentiable distillation from a teacher's top logits (see head.linear_distillation); "mean" is
+    over the rows that have an entry.  Not multiplied by temperature squared."""
+    loss = LinearDistillation.apply(x, weight, teacher_index, teacher_logits, temperature, layout)
+    return _reduce(loss, lambda: (teacher_index >= 0).any(1).sum(), reduction)

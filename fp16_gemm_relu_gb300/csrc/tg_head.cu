@@ -280,52 +280,50 @@ __device__ __forceinline__ float grad_value(float z, float c, float lse2, float 
   return gs == 0.0f ? 0.0f : gs * (exp2f(fmaf(z, c, -lse2)) - q);
 }
 
-// G (fp16, rows of ldg) from the logits, eight columns of a row a thread, the targets' part with it:
-// cross entropy's -1 in place; a teacher's entries (top > 0, weights q) in the block's columns after
-// the block has written them.  Entries of one token add up; each of them writes the same value.
-// Bound by HBM: 10 bytes an element, 4096 x 131072 in 459 us, 7.0 TB/s.
-template <bool TEACHER>
+// G (fp16, rows of ldg) from the logits, eight columns of a row a thread; cross entropy's target with
+// it.  Bound by HBM: 6 bytes an element, 4096 x 131072 in 456 us, 7.0 TB/s.
 __global__ void __launch_bounds__(256)
     tg_head_grad_kernel(const float* __restrict__ z, int64_t ldz, float c,
-                        const RowInfo* __restrict__ info, const int64_t* __restrict__ index,
-                        int64_t ldt, int top, const float* __restrict__ q, int64_t rows,
-                        int64_t vocab, uint16_t* __restrict__ g, int64_t ldg) {
-  const int64_t first = blockIdx.x * int64_t(256 * 8);
-  const int64_t v0 = first + threadIdx.x * 8;
+                        const RowInfo* __restrict__ info, int64_t rows, int64_t vocab,
+                        uint16_t* __restrict__ g, int64_t ldg) {
+  const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
+  if (v0 >= vocab) return;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const RowInfo ri = info[r];
-    // entries are read ahead of the columns: after them their latency stood alone (4096 x 65537 with
-    // 64 entries: 324 us, cross entropy 235)
-    const int64_t ahead = TEACHER && threadIdx.x < top ? index[r * ldt + threadIdx.x] : -1;
-    if (v0 < vocab) {
-      const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
-      const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
-      const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      uint32_t w[4];
+    const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
+    const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
+    const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo =
-            grad_value(f[2 * i], c, ri.lse2, ri.gs,
-                       !TEACHER && v0 + 2 * i == ri.target ? 1.0f : 0.0f);
-        const float hi =
-            grad_value(f[2 * i + 1], c, ri.lse2, ri.gs,
-                       !TEACHER && v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
-        const __half2 h = __floats2half2_rn(lo, hi);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(g + r * ldg + v0) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+      const float lo = grad_value(f[2 * i], c, ri.lse2, ri.gs, v0 + 2 * i == ri.target ? 1.0f : 0.0f);
+      const float hi =
+          grad_value(f[2 * i + 1], c, ri.lse2, ri.gs, v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
+      const __half2 h = __floats2half2_rn(lo, hi);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    if constexpr (!TEACHER) continue;
-    __syncthreads();
-    for (int e = threadIdx.x; e < top; e += 256) {
-      const int64_t i = e < 256 ? ahead : index[r * ldt + e];
-      if (i < first || i >= first + 256 * 8 || i >= vocab) continue;  // first >= 0
-      float sum = 0.0f;
-      for (int k = 0; k < top; ++k)
-        if (index[r * ldt + k] == i) sum += q[r * top + k];
-      g[r * ldg + i] = __half_as_ushort(
-          __float2half_rn(grad_value(z[r * ldz + i], c, ri.lse2, ri.gs, sum)));
-    }
+    *reinterpret_cast<uint4*>(g + r * ldg + v0) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Distillation: G again at the teacher's entries, a warp a row.  Entries of one token add up; each of
+// them then writes the same value.  Within the pass above the entries' reads would be on every
+// block's way: 4096 x 65537 with 64 entries took 325 to 380 us so, 235 and 17 apart.
+__global__ void __launch_bounds__(128)
+    tg_head_teacher_grad_kernel(const int64_t* __restrict__ index, int64_t ldt, int top,
+                                const float* __restrict__ q, const float* __restrict__ z,
+                                int64_t ldz, float c, const RowInfo* __restrict__ info,
+                                int64_t rows, int64_t vocab, __half* __restrict__ g, int64_t ldg) {
+  const int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
+  if (r >= rows) return;
+  const RowInfo ri = info[r];
+  for (int e = threadIdx.x & 31; e < top; e += 32) {
+    const int64_t i = index[r * ldt + e];
+    if (i < 0 || i >= vocab) continue;
+    float sum = 0.0f;
+    for (int k = 0; k < top; ++k)
+      if (index[r * ldt + k] == i) sum += q[r * top + k];
+    g[r * ldg + i] = __float2half_rn(grad_value(z[r * ldz + i], c, ri.lse2, ri.gs, sum));
   }
 }
 
@@ -525,14 +523,12 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
         q, alpha);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
     if (!grad) continue;
-    const dim3 cells(static_cast<unsigned>(cdiv(h.V, 2048)),
-                     static_cast<unsigned>(std::min<int64_t>(n, 65535)));
+    tg_head_grad_kernel<<<dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
+                               static_cast<unsigned>(std::min<int64_t>(n, 65535))),
+                          256, 0, stream>>>(z, ldz, c, info, n, h.V, g, ldg);
     if (h.top)
-      tg_head_grad_kernel<true><<<cells, 256, 0, stream>>>(z, ldz, c, info, index, h.ldt, h.top, q,
-                                                           n, h.V, g, ldg);
-    else
-      tg_head_grad_kernel<false><<<cells, 256, 0, stream>>>(z, ldz, c, info, index, h.ldt, h.top, q,
-                                                            n, h.V, g, ldg);
+      tg_head_teacher_grad_kernel<<<static_cast<unsigned>(cdiv(n, 4)), 128, 0, stream>>>(
+          index, h.ldt, h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg);
     if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
     if (h.dX) {  // G (n x V) times W (V x D, or stored D x V)
       std::memset(&ex, 0, sizeof(ex));
