@@ -982,12 +982,13 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   // A: K-major box {64 K, 128 rows} or, stored K x M, two MN-major boxes {64 M, 64 K};
   // B: MN-major boxes {64 N, 64 K} or, stored N x K, one K-major box {64 K, BN (or 128) rows}
   // the CTA-pair kernel stages 128 k: its MN-major boxes are {64, 128 K}
+  const int64_t a_rows = extra && extra->a_rows > M && Ae == A ? extra->a_rows : M;
   const uint32_t mn_box_k = P.cta_pair ? uint32_t(tg::PairCfgFwd::kKB * tg::kBK) : tg::kBK;
   CUresult cr = P.a_row_classes ? CUDA_SUCCESS  // A comes through cls
                 : ta ? encode_2d(enc, &L.a, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Ae, uint64_t(M),
                                  uint64_t(K), uint64_t(lda_e) * 2, 64, mn_box_k)
                      : encode_2d(enc, &L.a, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Ae, uint64_t(K),
-                                 uint64_t(M), uint64_t(lda_e) * 2, tg::kBK, tg::kBM);
+                                 uint64_t(a_rows), uint64_t(lda_e) * 2, tg::kBK, tg::kBM);
   if (cr == CUDA_SUCCESS)
     cr = tb ? encode_2d(enc, &L.b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Be, uint64_t(K), uint64_t(N),
                         uint64_t(ldb_e) * 2, tg::kBK, P.cta_pair ? 128u : uint32_t(P.block_n))

@@ -338,6 +338,11 @@ constexpr int64_t kMaxLd = int64_t{1} << 36;
 // Logits of a piece by default: 2 GiB of float32, 1 GiB of G.  Fewer, longer pieces cost less: a
 // piece adds one pass of reads and writes over dW in float32.
 constexpr int64_t kPieceLogits = int64_t{1} << 29;
+// A TMA box of 128 rows of a matrix of fewer than eight (the rows of a swizzle atom) takes longer at
+// some addresses: one token against 28672 x 8192, memory-bound, took 87 or 112 us by where the token
+// lay, and never more than 88 from eight rows on.  So small operands lie in scratch of that many
+// rows; what the others hold does not matter, an MMA's rows have nothing to do with each other.
+constexpr int64_t kLeastRows = 8;
 // Without logits a token's scratch is its statistics: 1 GiB of them.
 constexpr int64_t kPieceStats = int64_t{1} << 27;
 
@@ -423,8 +428,9 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const bool sum_w = h.dW && piece < h.T;  // dW is summed over pieces in float32
 
   Layout lay;
-  // rows that TMA cannot read in place are copied once for all pieces and products
-  const bool copy_x = misaligned(h.X, 16) || h.ldx % 8 != 0;
+  // Rows that TMA cannot read in place are copied once for all pieces and products, and so are the
+  // tokens where there are fewer than kLeastRows.
+  const bool copy_x = misaligned(h.X, 16) || h.ldx % 8 != 0 || h.T < kLeastRows;
   const bool copy_w = misaligned(h.W, 16) || h.ldw % 8 != 0;
   const int64_t ldxp = round_up(h.D, 64), ldwp = round_up(w_cols, 64), ldw32 = round_up(w_cols, 32);
   const int64_t at_z = lay.add(store ? piece * ldz * 4 : 0);
@@ -432,9 +438,9 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const int64_t at_picked = lay.add(store ? 0 : piece * std::max(h.top, 1) * 4);
   const int64_t at_info = lay.add(piece * int64_t(sizeof(RowInfo)));
   const int64_t at_small = lay.add(2 * 4);
-  const int64_t at_g = lay.add(grad ? piece * ldg * 2 : 0);
+  const int64_t at_g = lay.add(grad ? std::max(piece, kLeastRows) * ldg * 2 : 0);
   const int64_t at_q = lay.add(grad && h.top ? piece * h.top * 4 : 0);
-  const int64_t at_x = lay.add(copy_x ? h.T * ldxp * 2 : 0);
+  const int64_t at_x = lay.add(copy_x ? std::max(h.T, kLeastRows) * ldxp * 2 : 0);
   const int64_t at_w = lay.add(copy_w ? w_rows * ldwp * 2 : 0);
   const int64_t at_w32 = lay.add(sum_w ? w_rows * ldw32 * 4 : 0);
   uint8_t* mem = nullptr;
@@ -509,6 +515,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     lx.block_n = &block_n;
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
+    if (h.T < kLeastRows) ex.a_rows = kLeastRows - t0;
     st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &gemm_opt,
                         stream);
     if (st != TG_OK) return done(st);
@@ -533,6 +540,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     if (h.dX) {  // G (n x V) times W (V x D, or stored D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
+      ex.a_rows = std::max(n, kLeastRows);
       st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, n, h.D,
                           h.V, ldg, ldw, h.lddx, ex, &gemm_opt, stream);
       if (st != TG_OK) return done(st);

@@ -79,6 +79,7 @@ struct GemmExtra {
   float* out32;         // float32 output, rows of ld32 floats (a multiple of 32)
   int64_t ld32;
   bool add;             // add to out32 (A stored K x M, B stored K x N) instead of writing it
+  int64_t a_rows;       // 0, or the rows (>= M) that A, stored M x K and not copied, has in memory
 };
 tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
                      int64_t K, int64_t lda, int64_t ldb, int64_t ldc, const GemmExtra& x,
