@@ -160,6 +160,14 @@ __global__ void __launch_bounds__(kRowThreads)
   const int tid = threadIdx.x;
   const float w = wmax ? __uint_as_float(*wmax) : 0.0f;
   if (alpha && r == 0 && tid == 0) *alpha = scale * w / kGScale;
+  // the first entries and their logits are on their way while the statistics are reduced
+  int64_t i0 = -1;
+  float u0 = 0.0f, z0 = 0.0f;
+  if (tid < top) {
+    i0 = index[r * ldt + tid];
+    u0 = teacher_at(teacher, r * ldt + tid, teacher_f32);
+    if (i0 >= 0 && i0 < vocab) z0 = lg.z ? lg.z[r * lg.ldz + i0] : lg.picked[r * top + tid];
+  }
   float m = -INFINITY, s = 0.0f;
 #pragma unroll 4
   for (int t = tid; t < tiles; t += kRowThreads) {
@@ -182,6 +190,7 @@ __global__ void __launch_bounds__(kRowThreads)
   ri.pad = 0;
   float l = 0.0f;
   if (top == 0) {
+    if (tid != 0) return;
     const int64_t y = index[r];
     const RowKind kind = target_kind(y, vocab, ignore);
     if (kind == RowKind::kCounts) {
@@ -196,9 +205,9 @@ __global__ void __launch_bounds__(kRowThreads)
     float mt = -INFINITY;
     bool bad = false;
     for (int e = tid; e < top; e += kRowThreads) {
-      const int64_t i = index[r * ldt + e];
+      const int64_t i = e == tid ? i0 : index[r * ldt + e];
       if (i < 0) continue;
-      const float u = teacher_at(teacher, r * ldt + e, teacher_f32);
+      const float u = e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32);
       bad |= i >= vocab || !(u < INFINITY);  // NaN or +inf
       mt = fmaxf(mt, u * c);
     }
@@ -206,17 +215,18 @@ __global__ void __launch_bounds__(kRowThreads)
     bad = __syncthreads_or(bad);
     float st = 0.0f;
     for (int e = tid; e < top && mt > -INFINITY; e += kRowThreads)
-      if (index[r * ldt + e] >= 0)
-        st += exp2f(fmaf(teacher_at(teacher, r * ldt + e, teacher_f32), c, -mt));
+      if ((e == tid ? i0 : index[r * ldt + e]) >= 0)
+        st += exp2f(fmaf(e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32), c, -mt));
     const float lq = mt + log2f(block_sum(st, slots[3]));
     for (int e = tid; e < top; e += kRowThreads) {
       float qe = 0.0f;
-      const int64_t i = index[r * ldt + e];
+      const int64_t i = e == tid ? i0 : index[r * ldt + e];
       if (i >= 0 && mt > -INFINITY) {
-        const float t2 = fmaf(teacher_at(teacher, r * ldt + e, teacher_f32), c, -lq);
+        const float u = e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32);
+        const float t2 = fmaf(u, c, -lq);
         qe = exp2f(t2);
         if (qe > 0.0f && i < vocab) {
-          const float z = lg.z ? lg.z[r * lg.ldz + i] : lg.picked[r * top + e];
+          const float z = e == tid ? z0 : lg.z ? lg.z[r * lg.ldz + i] : lg.picked[r * top + e];
           l += qe * (t2 * kLn2 - (scale * z - lse_r));
         }
       }
@@ -335,6 +345,7 @@ bool misaligned(const void* p, unsigned bytes) {
 
 constexpr int64_t kMaxRows = (int64_t{1} << 31) - 1024;
 constexpr int64_t kMaxLd = int64_t{1} << 36;
+constexpr int64_t kMaxElements = int64_t{1} << 44;
 // Logits of a piece by default: 2 GiB of float32, 1 GiB of G.  Fewer, longer pieces cost less: a
 // piece adds one pass of reads and writes over dW in float32.
 constexpr int64_t kPieceLogits = int64_t{1} << 29;
@@ -377,6 +388,8 @@ tg_status check(const Head& h) {
     return TG_ERR_INVALID_ARG;
   if (h.o.layout != TG_HEAD_VOCAB_MAJOR && h.o.layout != TG_HEAD_WIDTH_MAJOR)
     return TG_ERR_INVALID_ARG;
+  // sizes whose products leave 64 bits could only come with pointers to nothing
+  if (h.T > kMaxElements / h.D || h.V > kMaxElements / h.D) return TG_ERR_INVALID_ARG;
   if (h.o.piece_rows < 0 || h.o.timeout_ms < 0) return TG_ERR_INVALID_ARG;
   if (!(h.scale > 0.0f) || !(h.scale <= 3.0e38f)) return TG_ERR_INVALID_ARG;
   const int64_t w_cols = h.o.layout == TG_HEAD_VOCAB_MAJOR ? h.D : h.V;
@@ -420,8 +433,10 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const int64_t ldz = round_up(h.V, 32), ldg = round_up(h.V, 64);
   const int64_t tiles = 2 * cdiv(h.V, 128);  // statistics of a row, at most
   const int64_t per_row = store ? ldz : tiles, budget = store ? kPieceLogits : kPieceStats;
-  int64_t piece = h.o.piece_rows ? std::min(h.o.piece_rows, h.T) : h.T;
-  if (!h.o.piece_rows && h.T > budget / per_row) {
+  int64_t piece = h.T;
+  if (h.o.piece_rows) {
+    piece = std::min({h.o.piece_rows, h.T, std::max<int64_t>(kMaxElements / per_row, 1)});
+  } else if (h.T > budget / per_row) {
     const int64_t most = std::max<int64_t>(budget / per_row / 256 * 256, 256);
     piece = std::min(h.T, round_up(cdiv(h.T, cdiv(h.T, most)), 256));
   }

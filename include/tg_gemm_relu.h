@@ -330,6 +330,11 @@ tg_status tg_gemm_relu_f16_splitk_noalloc(const void* A, const void* B, void* C,
  *  - Sums, statistics and losses are float32; every fp16 output is rounded once.  Results are
  *    bitwise reproducible run to run.
  *  - Outputs must not overlap inputs, except where said.
+ *  - Invalid arguments are found before anything is launched; TG_ERR_NO_WORKSPACE and TG_ERR_CUDA
+ *    of the head's losses may come after part of a call is queued (its outputs are then undefined).
+ *  - Rows are independent: a NaN or an infinity in a row of activations shows in that row's results
+ *    (and in sums over the rows), not in another's.  A logit of +inf makes its row's lse, loss and
+ *    gradient NaN.
  * ---------------------------------------------------------------------------------------
  */
 

@@ -317,6 +317,64 @@ def test_not_finite_rows_stay_in_their_rows():
     assert torch.isnan(dx[3]).all() and (dx[5] == 0).all() and torch.isfinite(dx[rest]).all()
 
 
+def test_infinite_logits():
+    # fp16 values whose products leave float32's range do not exist; infinities come with the operands
+    T, V, D = 20, 300, 64
+    x, w = operands(T, V, D, 0, 126)
+    w = w.clone()
+    x = x.abs().contiguous()
+    target = torch.full((T,), 5, dtype=torch.int64, device="cuda")
+    good = tg.linear_cross_entropy(x, w, target)
+    w[250] = -math.inf  # a token that cannot be: its logit is -inf, its probability 0
+    wz = w.clone()
+    wz[250] = 0
+    loss, lse = tg.linear_cross_entropy(x, w, target, return_lse=True)
+    z = (x.double() @ wz.double().t())
+    z[:, 250] = -math.inf
+    want = torch.logsumexp(z, 1)
+    assert ((lse.double() - want).abs() <= 1e-5 * (want.abs() + 1)).all()
+    assert ((loss.double() - (want - z[:, 5])).abs() <= 1e-5 * (want.abs() + 1)).all()
+    assert not torch.equal(loss, good) and torch.isfinite(loss).all()
+    target[3] = 250
+    assert torch.isposinf(tg.linear_cross_entropy(x, w, target)[3])
+    w[250] = math.inf
+    loss, lse = tg.linear_cross_entropy(x, w, target, return_lse=True)
+    assert torch.isnan(lse).all() and torch.isnan(loss).all()
+    w[:] = -math.inf  # no token can be
+    loss, lse = tg.linear_cross_entropy(x, w, target, return_lse=True)
+    assert torch.isneginf(lse).all() and torch.isnan(loss).all()
+
+
+@pytest.mark.parametrize("V", [1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257, 383, 385, 511,
+                               513])
+@pytest.mark.parametrize("T", [1, 7, 8, 127, 129])
+def test_tile_edges(T, V):
+    D = 72
+    x, w = operands(T, V, D, 0, 127 + V)
+    target = targets(T, V, 128, 0.0)
+    target[-1] = V - 1  # the last column
+    dloss = torch.ones(T, device="cuda")
+    q, live = one_hot(target, V)
+    zero = torch.zeros(T, dtype=D64, device="cuda")
+    loss, lse = tg.linear_cross_entropy(x, w, target, return_lse=True)
+    check(x, w, 0, 1.0, q, live, zero, None, loss, lse, None, None)
+    step = tg.linear_cross_entropy_step(x, w, target, dloss)
+    check(x, w, 0, 1.0, q, live, zero, dloss, step[0], None, step[1], step[2])
+
+
+@pytest.mark.parametrize("D", [1, 63, 64, 65, 1023, 1024, 1025, 1088, 2048, 2112, 3000])
+@pytest.mark.parametrize("T,V", [(5, 300), (300, 600)])
+def test_widths_around_the_segments(T, V, D):
+    x, w = operands(T, V, D, 0, 129 + D)
+    target = targets(T, V, 130)
+    q, live = one_hot(target, V)
+    zero = torch.zeros(T, dtype=D64, device="cuda")
+    loss, lse = tg.linear_cross_entropy(x, w, target, return_lse=True)
+    check(x, w, 0, 1.0, q, live, zero, None, loss, lse, None, None)
+    step = tg.linear_cross_entropy_step(x, w, target, torch.ones(T, device="cuda"))
+    check(x, w, 0, 1.0, q, live, zero, torch.ones(T, device="cuda"), step[0], None, step[1], step[2])
+
+
 def test_same_token_twice():
     T, V, D = 33, 200, 48
     x, w = operands(T, V, D, 0, 100)

@@ -187,6 +187,45 @@ def test_backward_parameter_types(dtype):
     assert none1 is None and none2 is None and torch.equal(dx, got[0])
 
 
+@pytest.mark.parametrize("M,N", [(700, 60), (40, 500), (300, 1000), (50, 4097), (9, 9000), (5, 20000)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (3, 1)])
+@pytest.mark.parametrize("over", ["dy", "x"])
+def test_backward_in_place(M, N, pad, offset, over):
+    # the C entry may write dX over dY or X; N in every range of the kernels
+    x, dy = make(M, N, pad, offset, 32, 1.5, 0.3), make(M, N, pad, offset, 33)
+    gamma = make(1, N, seed=34)[0].contiguous()
+    _, mean, rstd = tg.layer_norm(x, gamma, eps=EPS, stats=True)
+    keep_x, keep_dy = x.clone(), dy.clone()
+    dg, db = torch.empty_like(gamma), torch.empty_like(gamma)
+    out = dy if over == "dy" else x
+    st = binding.tg_layernorm_backward_f16(
+        dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        out.data_ptr(), dg.data_ptr(), db.data_ptr(), M, N, dy.stride(0), x.stride(0),
+        out.stride(0), binding.TG_TYPE_F16, torch.cuda.current_stream().cuda_stream)
+    assert st == binding.TG_OK
+    check_backward(keep_dy, keep_x, gamma, mean, rstd, out, dg, db)
+    # each output alone, and none of the others touched
+    alone = torch.empty_like(gamma)
+    st = binding.tg_layernorm_backward_f16(
+        keep_dy.data_ptr(), keep_x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        0, 0, alone.data_ptr(), M, N, keep_dy.stride(0), keep_x.stride(0), 0, binding.TG_TYPE_F16,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == binding.TG_OK
+    _, _, dbr, _, _ = backward_reference(keep_dy, keep_x, gamma, mean, rstd)
+    tol = dbr.abs() * 2 ** -11 + 2 ** -25 + keep_dy.double().abs().sum(0) * (M / 16 + 64) * 2 ** -24
+    assert ((alone.double() - dbr).abs() <= tol).all()
+
+
+def test_many_short_rows():
+    # more rows than one wave of warps, widths at the edges of the kernels' ranges
+    for N in (1, 8, 256, 257, 512, 513):
+        x, dy = make(6000, N, 0, 0, 35), make(6000, N, 0, 0, 36)
+        gamma = make(1, N, seed=37)[0].contiguous()
+        y, mean, rstd = tg.layer_norm(x, gamma, eps=EPS, stats=True)
+        check_forward(x, gamma, None, y, mean, rstd)
+        check_backward(dy, x, gamma, mean, rstd, *tg.layer_norm_backward(dy, x, mean, rstd, gamma))
+
+
 def test_backward_against_differences():
     d = torch.float64
     x, dy = make(6, 200, seed=26), make(6, 200, seed=27)

@@ -80,6 +80,7 @@ def test_norm_nothing_to_do():
 
 BAD_HEAD = [
     dict(T=-1), dict(V=0), dict(D=0), dict(T=2 ** 31), dict(V=2 ** 31), dict(ldx=15),
+    dict(T=2 ** 30, V=2 ** 30, D=2 ** 30, ldx=2 ** 30, ldw=2 ** 30, lddx=2 ** 30, lddw=2 ** 30),
     dict(ldw=15), dict(lddx=15), dict(lddw=15), dict(X=0), dict(W=0), dict(dloss=0),
     dict(options={"layout": 2}), dict(options={"layout": 1}),  # width-major: ldw >= V
     dict(options={"piece_rows": -1}), dict(options={"timeout_ms": -1})]
