@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "tg_gemm_relu.h"
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     tg_layernorm_kernel(const uint16_t* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
                         const P* __restrict__ beta, uint16_t* __restrict__ y, int64_t ldy,
                         float* __restrict__ mean, float* __restrict__ rstd, int rows, int n,
-                        float eps, int tpr, int slot_bytes, unsigned* err) {
+                        float eps, unsigned* err, int tpr, int slot_bytes) {
   constexpr int CH = kFwdChunks, S = kFwdSlots;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
@@ -482,7 +483,7 @@ __global__ void __launch_bounds__(512)
                                  const P* __restrict__ gamma, const float* __restrict__ mean,
                                  const float* __restrict__ rstd, uint16_t* __restrict__ dx,
                                  int64_t lddx, float* __restrict__ part, int64_t np, int rows,
-                                 int n, int tpr, int slot_bytes, unsigned* err) {
+                                 int n, unsigned* err, int tpr, int slot_bytes) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
   __shared__ float sums[8][2][32];  // [group][row's turn][of g: 16 warps, of g u: 16 warps]
@@ -933,11 +934,23 @@ Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
                    : ring_shape(rows, n, 4, 2, 2, 1, 128, vec, sms);
 }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-  if (bytes <= 40 * 1024) return cudaSuccess;  // beside the kernels' static shared memory
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
+// Launches a ring kernel.  That it may have more than 48 KB of shared memory is said once for each
+// device: said again at every launch it is a fifth of a small call's time.
+constexpr int kRingSmem = tg::kSmemLimit - 4096;  // beside the kernels' static shared memory
+template <auto KERNEL, typename... Args>
+cudaError_t launch_ring(const Shape& s, cudaStream_t st, Args... args) {
+  static std::atomic<uint64_t> told{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t{1} << (dev & 63);  // device_info has refused devices past 63
+  if ((told.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+    if (e != cudaSuccess) return e;
+    told.fetch_or(bit, std::memory_order_relaxed);
+  }
+  KERNEL<<<s.blocks, s.threads, s.smem, st>>>(args..., s.tpr, s.slot_bytes);
+  return cudaGetLastError();
 }
 
 template <bool VEC, typename P>
@@ -962,17 +975,13 @@ cudaError_t forward(const void* x, const void* gamma, const void* beta, void* y,
     return direct(tg_layernorm_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>, kLongThreads,
                   std::min<int64_t>(rows, sms));
   const Shape s = forward_shape(rows, n, VEC, sms);
-  auto ring = [&](auto kern) {
-    const cudaError_t e = allow_smem(kern, s.smem);
-    if (e != cudaSuccess) return e;
-    kern<<<s.blocks, s.threads, s.smem, st>>>(px, ldx, g, b, py, ldy, mean, rstd,
-                                              static_cast<int>(rows), static_cast<int>(n), eps,
-                                              s.tpr, s.slot_bytes, err);
-    return cudaGetLastError();
-  };
+  const int width = static_cast<int>(n), count = static_cast<int>(rows);
   // up to 8192 columns a block has 256 threads at most: three of them an SM where registers allow
-  return n <= 8192 ? ring(tg_layernorm_kernel<256, VEC ? 3 : 2, VEC, P>)
-                   : ring(tg_layernorm_kernel<512, 1, VEC, P>);
+  if (n <= 8192)
+    return launch_ring<tg_layernorm_kernel<256, VEC ? 3 : 2, VEC, P>>(
+        s, st, px, ldx, g, b, py, ldy, mean, rstd, count, width, eps, err);
+  return launch_ring<tg_layernorm_kernel<512, 1, VEC, P>>(s, st, px, ldx, g, b, py, ldy, mean, rstd,
+                                                          count, width, eps, err);
 }
 
 template <bool VEC, typename P>
@@ -1000,15 +1009,11 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
     e = direct(tg_layernorm_backward_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>,
                kLongThreads, 0);
   } else {
-    auto go = [&](auto kern) {
-      const cudaError_t a = allow_smem(kern, s.smem);
-      if (a != cudaSuccess) return a;
-      kern<<<s.blocks, s.threads, s.smem, st>>>(pd, lddy, px, ldx, g, mean, rstd, out, lddx, part,
-                                                np, static_cast<int>(rows), width, s.tpr, s.slot_bytes, err);
-      return cudaGetLastError();
-    };
-    e = n <= 8192 ? go(tg_layernorm_backward_kernel<2, 3, VEC, P>)
-                  : go(tg_layernorm_backward_kernel<4, 2, VEC, P>);
+    const int count = static_cast<int>(rows);
+    e = n <= 8192 ? launch_ring<tg_layernorm_backward_kernel<2, 3, VEC, P>>(
+                        s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, count, width, err)
+                  : launch_ring<tg_layernorm_backward_kernel<4, 2, VEC, P>>(
+                        s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, count, width, err);
   }
   if (e != cudaSuccess || part == nullptr) return e;
   tg_layernorm_params_kernel<P><<<dim3(static_cast<unsigned>(cdiv(n, 32)), 2), dim3(8, kPartRows), 0,
