@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(256)
       wr[j] = w + (i >= 0 && i < vocab ? i : 0) * ldw;
       s[j] = 0.0f;
     }
-#pragma unroll 2
+#pragma unroll 4
     for (int k = lane * 8; k < width; k += 256) {
       float a[8], b[kPickRows][8];
       load8(xr, k, width, a);

@@ -463,20 +463,32 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   }
 }
 
-// Sums of two values over a warp: the first ends in the lower 16 lanes, the second in the upper.
-__device__ __forceinline__ float warp_sum_two(float a, float b, int lane) {
+// Sums over a warp of R rows' pairs of values, all at once: each halving of the lanes also halves the
+// values that a lane has left.  Value (which, row) ends in the lanes [16 which + 16 / R row, + 16 / R).
+template <int R>
+__device__ __forceinline__ float warp_sums(const float (&a)[R], const float (&b)[R], int lane) {
   const bool up = lane & 16;
-  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+  float v[R];
 #pragma unroll
-  for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
+  for (int j = 0; j < R; ++j)
+    v[j] = (up ? b[j] : a[j]) + __shfl_xor_sync(0xffffffffu, up ? a[j] : b[j], 16);
+  float r = v[0];
+  if constexpr (R == 2) {
+    const bool second = lane & 8;
+    r = (second ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, second ? v[0] : v[1], 8);
+  }
+#pragma unroll
+  for (int d = 8 / R; d > 0; d >>= 1) r += __shfl_xor_sync(0xffffffffu, r, d);
+  return r;
 }
 
-// Backward, CH chunks a thread.  A thread keeps the same columns for all of its rows, so its part
-// of dgamma and dbeta stays in registers, and each block writes one partial row of both (of np
-// floats): part[0][block], part[1][block].  The row's two sums are needed before its dx, so the
-// loop works on two rows: it sums row k + 1 while it writes dx of row k, and meets once a row.
-template <int CH, int S, bool VEC, typename P>
+// Backward, CH chunks a thread, R adjacent rows at a time.  A thread keeps the same columns for all
+// of its rows, so its part of dgamma and dbeta stays in registers, and each block writes one partial
+// row of both (of np floats): part[0][block], part[1][block].  A row's two sums are needed before
+// its dx, so the loop works on two turns: it sums the rows of turn k + 1 while it writes dx of turn
+// k, and meets once a turn.  CARRY: rows stay in registers in between; otherwise they are read
+// from their slots again.
+template <int CH, int R, int S, bool CARRY, bool VEC, typename P>
 __global__ void __launch_bounds__(512)
     tg_layernorm_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                  const uint16_t* __restrict__ x, int64_t ldx,
@@ -484,28 +496,46 @@ __global__ void __launch_bounds__(512)
                                  const float* __restrict__ rstd, uint16_t* __restrict__ dx,
                                  int64_t lddx, float* __restrict__ part, int64_t np, int rows,
                                  int n, unsigned* err, int tpr, int slot_bytes) {
+  static_assert(R == 1 || R == 2, "one row or two");
+  constexpr int V = 2 * R;             // sums of a turn
+  constexpr int kLanes = 32 / V;       // lanes that read one of them back
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
-  __shared__ float sums[8][2][32];  // [group][row's turn][of g: 16 warps, of g u: 16 warps]
+  __shared__ float sums[2][V][16];  // [turn mod 2][(which, row)][warp of the block]
   __shared__ volatile int late;
   const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, lane = threadIdx.x & 31;
   const int per_block = blockDim.x / tpr, chunks = CH * tpr, wpr = tpr >> 5;
   float* sg = reinterpret_cast<float*>(smem);
-  uint8_t* ring = reinterpret_cast<uint8_t*>(sg + chunks * 8) + group * S * 2 * slot_bytes;
+  const int stage_bytes = 2 * R * slot_bytes;  // x and dy of each row in turn
+  uint8_t* ring = reinterpret_cast<uint8_t*>(sg + chunks * 8) + group * S * stage_bytes;
   const Span sx = span_of(x, ldx, rows, n), sd = span_of(dy, lddy, rows, n);
+  const int turns = (rows - 1) / R + 1;
   const int step = gridDim.x * per_block, first = blockIdx.x * per_block + group;
-  const int count = first < rows ? (rows - 1 - first) / step + 1 : 0;  // rows of this group
+  const int count = first < turns ? (turns - 1 - first) / step + 1 : 0;  // turns of this group
+  auto row_of = [&](int k) { return (first + int64_t(k) * step) * R; };
   auto fetch = [&](int k, int s) {
-    const int64_t row = first + int64_t(k) * step;
     const uint32_t bar = tg::smem_u32(&bars[group][s]);
-    const uint16_t *px = x + row * ldx, *pd = dy + row * lddy;
-    const Fetch fx = plan_fetch<VEC>(px, n, sx), fd = plan_fetch<VEC>(pd, n, sd);
-    uint8_t* slot = ring + s * 2 * slot_bytes;
-    fetch_edges<VEC>(fx, slot, px, n);
-    fetch_edges<VEC>(fd, slot + slot_bytes, pd, n);
-    tg::mbar_arrive_expect_tx(bar, static_cast<uint32_t>((fx.to - fx.from) + (fd.to - fd.from)));
-    fetch_blocks(fx, slot, bar);
-    fetch_blocks(fd, slot + slot_bytes, bar);
+    Fetch fx[R], fd[R];
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = row_of(k) + j;
+      fx[j] = fd[j] = Fetch{0, 0, 0};
+      if (row >= rows) continue;
+      uint8_t* slot = ring + s * stage_bytes + 2 * j * slot_bytes;
+      fx[j] = plan_fetch<VEC>(x + row * ldx, n, sx);
+      fd[j] = plan_fetch<VEC>(dy + row * lddy, n, sd);
+      fetch_edges<VEC>(fx[j], slot, x + row * ldx, n);
+      fetch_edges<VEC>(fd[j], slot + slot_bytes, dy + row * lddy, n);
+      bytes += static_cast<uint32_t>((fx[j].to - fx[j].from) + (fd[j].to - fd[j].from));
+    }
+    tg::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      uint8_t* slot = ring + s * stage_bytes + 2 * j * slot_bytes;
+      fetch_blocks(fx[j], slot, bar);
+      fetch_blocks(fd[j], slot + slot_bytes, bar);
+    }
   };
   if (threadIdx.x == 0) late = 0;
   if (t == 0) {
@@ -521,107 +551,140 @@ __global__ void __launch_bounds__(512)
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
-  // x and dy of chunk i of the row in a slot; past the row's end both are 0
-  auto read = [&](const uint8_t* slot, unsigned row, int i, uint4& xv, uint4& dv) {
-    const int c = i * tpr + t;
-    xv = slot_chunk<VEC>(slot, VEC ? 0u : row_shift(x, ldx, row), c, n);
-    dv = slot_chunk<VEC>(slot + slot_bytes, VEC ? 0u : row_shift(dy, lddy, row), c, n);
+  struct Stats {  // of a turn's rows; 0 for a row past the last, whose x and dy count as 0 too
+    float mu[R], rs[R];
   };
-  // With two chunks a thread a row stays in registers from its sums to its dx; with four it is read
-  // from its slot again.
-  constexpr bool kCarry = CH <= 2;
-  uint4 cx[kCarry ? CH : 1], cd[kCarry ? CH : 1];    // of row k
-  uint4 nx[kCarry ? CH : 1], nd[kCarry ? CH : 1];    // of row k + 1
+  auto stats_of = [&](int k) {
+    Stats st;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = row_of(k) + j;
+      const bool live = k < count && row < rows;
+      st.mu[j] = live ? __ldg(mean + row) : 0.0f;
+      st.rs[j] = live ? __ldg(rstd + row) : 0.0f;
+    }
+    return st;
+  };
+  // x and dy of chunk i of a row in its slot; past the row's end, and the last row, 0
+  auto read = [&](int s, int64_t row, int j, int i, uint4& xv, uint4& dv) {
+    const uint8_t* slot = ring + s * stage_bytes + 2 * j * slot_bytes;
+    const int c = i * tpr + t, width = R == 1 || row < rows ? n : 0;
+    xv = slot_chunk<VEC>(slot, VEC ? 0u : row_shift(x, ldx, row), c, width);
+    dv = slot_chunk<VEC>(slot + slot_bytes, VEC ? 0u : row_shift(dy, lddy, row), c, width);
+  };
+  constexpr int kHold = CARRY ? CH : 1;
+  uint4 cx[R][kHold], cd[R][kHold];  // of turn k
+  uint4 nx[R][kHold], nd[R][kHold];  // of turn k + 1
   // With u = x - mean, h = u rstd and g = d gamma: this thread's part of the sums of g and of g u
-  // (= g h / rstd) of a row, into sums[turn], and the row's part of dgamma (d u, times rstd) and
-  // dbeta
-  auto sum_row = [&](const uint8_t* slot, unsigned row, float mu, float rs, int turn) {
-    const f32x2 less = pair(-mu, -mu), times = pair(rs, rs);
-    f32x2 a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
+  // (= g h / rstd) of a turn's rows, and the rows' part of dgamma (d u, times rstd) and dbeta
+  auto sum_rows = [&](int k, int s, const Stats& st) {
+    f32x2 a2[R], b2[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) a2[j] = b2[j] = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int k = kCarry ? i : 0;
-      f32x2 v[4], d[4], g[4];
-      read(slot, row, i, nx[k], nd[k]);
-      unpack8(nx[k], v);
-      unpack8(nd[k], d);
+      f32x2 g[4];
       staged(sg, i * tpr + t, chunks, g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x2 du = mul2(d[j], add2(v[j], less));
-        a2 = fma2(d[j], g[j], a2);
-        b2 = fma2(du, g[j], b2);
-        dg[i][j] = fma2(du, times, dg[i][j]);
-        db[i][j] = add2(db[i][j], d[j]);
+      for (int j = 0; j < R; ++j) {
+        const int h = CARRY ? i : 0;
+        const f32x2 less = pair(-st.mu[j], -st.mu[j]), times = pair(st.rs[j], st.rs[j]);
+        f32x2 v[4], d[4];
+        read(s, row_of(k) + j, j, i, nx[j][h], nd[j][h]);
+        unpack8(nx[j][h], v);
+        unpack8(nd[j][h], d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f32x2 du = mul2(d[e], add2(v[e], less));
+          a2[j] = fma2(d[e], g[e], a2[j]);
+          b2[j] = fma2(du, g[e], b2[j]);
+          dg[i][e] = fma2(du, times, dg[i][e]);
+          db[i][e] = add2(db[i][e], d[e]);
+        }
       }
     }
-    const float v = warp_sum_two(sum2(a2), sum2(b2), lane);
-    if ((lane & 15) == 0) sums[group][turn][(lane & 16) + (t >> 5)] = v;
-  };
-  const float *pm = mean + first, *pr = rstd + first;
-  float mu = 0.0f, rs = 0.0f, mu1 = 0.0f, rs1 = 0.0f;
-  if (count > 0) {
-    mu = __ldg(pm);
-    rs = __ldg(pr);
-    if (count > 1) {
-      mu1 = __ldg(pm + step);
-      rs1 = __ldg(pr + step);
-    }
-    slot_wait(tg::smem_u32(&bars[group][0]), 0, &late, err);
-    sum_row(ring, first, mu, rs, 0);
-  }
-  auto carry = [&]() {
+    float a[R], b[R];
 #pragma unroll
-    for (int i = 0; i < (kCarry ? CH : 0); ++i) {
-      cx[i] = nx[i];
-      cd[i] = nd[i];
+    for (int j = 0; j < R; ++j) {
+      a[j] = sum2(a2[j]);
+      b[j] = sum2(b2[j]);
+    }
+    const float v = warp_sums<R>(a, b, lane);
+    if (lane % kLanes == 0) sums[k & 1][lane / kLanes][threadIdx.x >> 5] = v;
+  };
+  auto carry = [&]() {
+    if constexpr (CARRY) {
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          cx[j][i] = nx[j][i];
+          cd[j][i] = nd[j][i];
+        }
     }
   };
+  // where this lane reads its value's parts: of one warp, or (R == 2) of two, eight apart
+  const int first_warp = lane % kLanes;
+  const float* mine = &sums[0][0][0] + lane / kLanes * 16 + group * wpr + first_warp;
+  Stats now = stats_of(0), next = stats_of(1);
+  if (count > 0) {
+    slot_wait(tg::smem_u32(&bars[group][0]), 0, &late, err);
+    sum_rows(0, 0, now);
+  }
   carry();
   group_sync(tpr, group);
-  const int64_t dx_step = int64_t(step) * lddx;
-  uint16_t* dxr = dx + first * lddx;
-  int s = 0, s1 = 1;     // the slots of rows k and k + 1
-  uint32_t phase1 = 0;   // of slot s1
-  unsigned r = first;
-  for (int k = 0; k < count; ++k, r += step, dxr += dx_step) {
-    pm += step;
-    pr += step;
-    float mu2 = 0.0f, rs2 = 0.0f;
-    if (k + 2 < count) {
-      mu2 = __ldg(pm + step);
-      rs2 = __ldg(pr + step);
-    }
+  int s = 0, s1 = 1;     // the stages of turns k and k + 1
+  uint32_t phase1 = 0;   // of stage s1
+  for (int k = 0; k < count; ++k) {
+    const Stats ahead = stats_of(k + 2);
     if (k + 1 < count) {
       slot_wait(tg::smem_u32(&bars[group][s1]), phase1, &late, err);
-      sum_row(ring + s1 * 2 * slot_bytes, r + step, mu1, rs1, (k + 1) & 1);
+      sum_rows(k + 1, s1, next);
     }
     if (dx != nullptr) {
       // dx = rstd (g - mean(g) - h mean(g h)) = d (gamma rstd) + x c1 + c0 with
       // c1 = -rstd^3 mean(g u) and c0 = -rstd mean(g) - mean c1.  (Left uncentred, x c1 + c0 is off
       // by 2^-24 |mean| / spread of its size, far below dx's rounding to fp16.)
-      float v = (lane & 15) < wpr ? sums[group][k & 1][lane] : 0.0f;
+      const float* from = mine + (k & 1) * (V * 16);
+      float v = first_warp < wpr ? from[0] : 0.0f;
+      if (R == 2 && first_warp + 8 < wpr) v += from[8];
 #pragma unroll
-      for (int d = 8; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      const float a = __shfl_sync(0xffffffffu, v, 0), b = __shfl_sync(0xffffffffu, v, 16);
-      const float c1 = -rs * rs * rs * (b * inv_n), c0 = fmaf(-mu, c1, -rs * (a * inv_n));
-      const f32x2 of_x = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
+      for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      f32x2 of_x[R], plus[R], times[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float a = __shfl_sync(0xffffffffu, v, j * kLanes);
+        const float b = __shfl_sync(0xffffffffu, v, 16 + j * kLanes);
+        const float rs = now.rs[j], c1 = -rs * rs * rs * (b * inv_n);
+        const float c0 = fmaf(-now.mu[j], c1, -rs * (a * inv_n));
+        of_x[j] = pair(c1, c1);
+        plus[j] = pair(c0, c0);
+        times[j] = pair(rs, rs);
+      }
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = kCarry ? i : 0;
-        f32x2 v[4], d[4], g[4];
-        if constexpr (!kCarry) read(ring + s * 2 * slot_bytes, r, i, cx[0], cd[0]);
-        unpack8(cx[c], v);
-        unpack8(cd[c], d);
+        f32x2 g[4];
         staged(sg, i * tpr + t, chunks, g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = fma2(d[j], mul2(g[j], times), fma2(v[j], of_x, plus));
-        store_chunk<VEC>(dxr, i * tpr + t, n, pack8(g), lane);
+        for (int j = 0; j < R; ++j) {
+          const int64_t row = row_of(k) + j;
+          if (R > 1 && row >= rows) continue;  // the same for the whole group
+          const int h = CARRY ? i : 0;
+          if constexpr (!CARRY) read(s, row, j, i, cx[j][0], cd[j][0]);
+          f32x2 w[4], d[4], o[4];
+          unpack8(cx[j][h], w);
+          unpack8(cd[j][h], d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            o[e] = fma2(d[e], mul2(g[e], times[j]), fma2(w[e], of_x[j], plus[j]));
+          store_chunk<VEC>(dx + row * lddx, i * tpr + t, n, pack8(o), lane);
+        }
       }
     }
-    mu = mu1, rs = rs1, mu1 = mu2, rs1 = rs2;
+    now = next;
+    next = ahead;
     carry();
-    group_sync(tpr, group);  // slot s and sums[k & 1] are free, sums[(k + 1) & 1] is written
+    group_sync(tpr, group);  // stage s and sums[k & 1] are free, sums[(k + 1) & 1] is written
     if (t == 0 && k + S < count) fetch(k + S, s);
     s = s1;
     if (++s1 == S) {
@@ -918,8 +981,12 @@ Shape ring_shape(int64_t rows, int64_t n, int ch, int slots, int arrays, int par
 Shape forward_shape(int64_t rows, int64_t n, bool vec, int sms) {
   return ring_shape(rows, n, kFwdChunks, kFwdSlots, 1, 2, vec && n <= 8192 ? 80 : 128, vec, sms);
 }
-// Two chunks and three slots where they fit; past 8192 columns a block has threads for four
-// chunks and shared memory for two slots.
+// Which backward kernel.  Up to 8192 columns two chunks a thread and three stages; beyond, a block
+// has threads for four chunks and shared memory for two stages.  Two rows a turn halve the meetings
+// and the reductions' latency where one block fills an SM (8192 x 8192 82 us, one row a turn 90); with
+// blocks to spare (16384 x 4096 97 against 86 us), or rows to shift (4095 x 3073 62 against 49), one
+// row that stays in registers is better.
+bool two_rows(int64_t n, bool vec) { return vec && n > 4096 && n <= 8192; }
 Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
   Shape s = {};
   if (n <= kNarrowWidth) {
@@ -930,13 +997,19 @@ Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
     s.blocks = static_cast<int>(std::min<int64_t>(rows, sms));
     return s;
   }
-  return n <= 8192 ? ring_shape(rows, n, 2, 3, 2, 1, vec ? 104 : 120, vec, sms)
+  if (two_rows(n, vec)) return ring_shape((rows - 1) / 2 + 1, n, 2, 3, 4, 1, 128, vec, sms);
+  return n <= 8192 ? ring_shape(rows, n, 2, 3, 2, 1, 120, vec, sms)
                    : ring_shape(rows, n, 4, 2, 2, 1, 128, vec, sms);
 }
 
+template <auto KERNEL>
+struct Kernel {
+  static constexpr auto value = KERNEL;
+};
+
 // Launches a ring kernel.  That it may have more than 48 KB of shared memory is said once for each
 // device: said again at every launch it is a fifth of a small call's time.
-constexpr int kRingSmem = tg::kSmemLimit - 4096;  // beside the kernels' static shared memory
+constexpr int kRingSmem = tg::kSmemLimit - 1280;  // beside the kernels' static shared memory
 template <auto KERNEL, typename... Args>
 cudaError_t launch_ring(const Shape& s, cudaStream_t st, Args... args) {
   static std::atomic<uint64_t> told{0};
@@ -1010,10 +1083,16 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
                kLongThreads, 0);
   } else {
     const int count = static_cast<int>(rows);
-    e = n <= 8192 ? launch_ring<tg_layernorm_backward_kernel<2, 3, VEC, P>>(
-                        s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, count, width, err)
-                  : launch_ring<tg_layernorm_backward_kernel<4, 2, VEC, P>>(
-                        s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, count, width, err);
+    auto go = [&](auto which) {
+      return launch_ring<which.value>(s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np,
+                                      count, width, err);
+    };
+    if (n > 8192)
+      e = go(Kernel<tg_layernorm_backward_kernel<4, 1, 2, false, VEC, P>>{});
+    else if (!two_rows(n, VEC))
+      e = go(Kernel<tg_layernorm_backward_kernel<2, 1, 3, true, VEC, P>>{});
+    else
+      e = go(Kernel<tg_layernorm_backward_kernel<2, 2, 3, false, true, P>>{});
   }
   if (e != cudaSuccess || part == nullptr) return e;
   tg_layernorm_params_kernel<P><<<dim3(static_cast<unsigned>(cdiv(n, 32)), 2), dim3(8, kPartRows), 0,
