@@ -414,11 +414,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   stage_param<VEC>(so, beta, n, chunks, 0.0f);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
-  const int64_t y_step = int64_t(step) * ldy;
-  uint16_t* yr = y + first * ldy;
-  unsigned r = first;
-  for (int k = 0; k < count; ++k, r += step, yr += y_step) {
+  for (int k = 0; k < count; ++k) {
     const int s = k & 1;
+    const int64_t r = first + int64_t(k) * step;
     slot_wait(tg::smem_u32(&bars[group][s]), (k >> 1) & 1, &late, err);
     const uint32_t b = VEC ? 0u : row_shift(x, ldx, r);
     f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
@@ -458,7 +456,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
       staged(so, i * tpr + t, chunks, o);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], times), g[j], o[j]);
-      store_chunk<VEC>(yr, i * tpr + t, n, pack8(o), lane);
+      store_chunk<VEC>(y + r * ldy, i * tpr + t, n, pack8(o), lane);
     }
   }
 }
