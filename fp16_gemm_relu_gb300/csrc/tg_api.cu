@@ -565,6 +565,11 @@ __global__ void tg_first_window_kernel(const uint16_t* __restrict__ A, int64_t l
 // (a flat index split by a 64-bit division per item, one row at a time, ran at 0.67 of HBM).
 constexpr int kReduceRows = 4;
 constexpr int kReduceThreads = 128;
+template <bool SCALED>  // the scaled sum (p.alpha) in place of the epilogue
+__device__ __forceinline__ float reduced_value(float x, int row, int col, const tg::GemmParams& p) {
+  return SCALED ? tg::scaled_value(x, row, col, p) : tg::epilogue_value(x, row, col, p);
+}
+template <bool SCALED>
 __global__ void __launch_bounds__(kReduceThreads)
     tg_splitk_reduce_kernel(const float* __restrict__ ws, int64_t ldw, int64_t split_stride,
                             int splits, __half* C, int64_t ldc, const tg::GemmParams p,
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(kReduceThreads)
       __half h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        h[e] = __float2half_rn(c0 + e < N ? tg::epilogue_value(a[e], int(r), int(c0 + e), p)
+        h[e] = __float2half_rn(c0 + e < N ? reduced_value<SCALED>(a[e], int(r), int(c0 + e), p)
                                           : 0.0f);
       __half* d = C + r * ldc + c0;
       if (c0 + 4 <= N && (reinterpret_cast<uintptr_t>(d) & 7u) == 0) {
@@ -630,6 +635,7 @@ __global__ void __launch_bounds__(kReduceThreads)
 // are four times as many threads, and kReduceAhead splits' loads in flight at a time.  128 x 1024
 // from 13 splits took 15 us as above, where 64 blocks waited for one split after the other.
 constexpr int kReduceAhead = 8;
+template <bool SCALED>
 __global__ void __launch_bounds__(kReduceThreads)
     tg_splitk_reduce_small_kernel(const float* __restrict__ ws, int64_t ldw, int64_t split_stride,
                                   int splits, __half* C, int64_t ldc, const tg::GemmParams p) {
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(kReduceThreads)
   }
   __half* d = C + r * ldc + c0;
   for (int e = 0; e < 4 && c0 + e < N; ++e)
-    d[e] = __float2half_rn(tg::epilogue_value(a[e], int(r), int(c0 + e), p));
+    d[e] = __float2half_rn(reduced_value<SCALED>(a[e], int(r), int(c0 + e), p));
 }
 
 // Grid of the reduction: x over the groups of 4 columns, y over chunks of kReduceRows rows.
@@ -675,13 +681,15 @@ bool reduce_small(int64_t M, int64_t N, int num_sms) {
 void launch_reduce(const float* ws, int64_t ldw, int64_t split_stride, int splits, __half* C,
                    int64_t ldc, const tg::GemmParams& p, int64_t cls_rows, int num_sms,
                    cudaStream_t stream) {
-  if (cls_rows == 0 && splits > 1 && reduce_small(p.M, p.N, num_sms))
-    tg_splitk_reduce_small_kernel<<<dim3(reduce_grid(p.M, p.N).x, static_cast<unsigned>(p.M)),
-                                    kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C,
-                                                                 ldc, p);
-  else
-    tg_splitk_reduce_kernel<<<reduce_grid(p.M, p.N), kReduceThreads, 0, stream>>>(
-        ws, ldw, split_stride, splits, C, ldc, p, cls_rows);
+  if (cls_rows == 0 && splits > 1 && reduce_small(p.M, p.N, num_sms)) {
+    const dim3 grid(reduce_grid(p.M, p.N).x, static_cast<unsigned>(p.M));
+    auto kern = p.alpha ? tg_splitk_reduce_small_kernel<true> : tg_splitk_reduce_small_kernel<false>;
+    kern<<<grid, kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C, ldc, p);
+  } else {
+    auto kern = p.alpha ? tg_splitk_reduce_kernel<true> : tg_splitk_reduce_kernel<false>;
+    kern<<<reduce_grid(p.M, p.N), kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C, ldc,
+                                                               p, cls_rows);
+  }
 }
 
 // dZ[i, j] = C[i, j] > 0 ? dC[i, j] : +0 (the relu derivative taken on the forward output C;
@@ -858,7 +866,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     gp.ldr = epi.residual ? epi.ldr : 0;
     gp.M = static_cast<int>(M);
     gp.N = static_cast<int>(N);
-    tg_splitk_reduce_kernel<<<reduce_grid(M, N), kReduceThreads, 0, stream>>>(
+    tg_splitk_reduce_kernel<false><<<reduce_grid(M, N), kReduceThreads, 0, stream>>>(
         nullptr, 0, 0, 0, static_cast<__half*>(C), ldc, gp, 0);
     e = cudaGetLastError();
     return e == cudaSuccess ? TG_OK : cuda_fail(e);

@@ -82,8 +82,8 @@ struct GemmParams {
   const __half* bias;
   const __half* residual;
   long long ldr;
-  // fp16 output only: (sum + addend[i*ld_addend + j]) * *alpha goes on to the bias (device
-  // float32; nullptr: 0 and 1)
+  // fp16 output only, alpha not nullptr: C = fp16((sum + addend[i*ld_addend + j]) * *alpha) in place of
+  // the epilogue above (device float32; addend nullptr: 0)
   const float* alpha;
   const float* addend;
   long long ld_addend;
@@ -117,11 +117,14 @@ __device__ __forceinline__ float activation(float x, int act) {
   }
 }
 
-// Full epilogue of one float32 sum at (row, col): (alpha (sum + addend) + bias) -> activation ->
-// + residual.
-__device__ __forceinline__ float epilogue_value(float x, int row, int col, const GemmParams& p) {
+// The scaled sum in place of it (p.alpha).
+__device__ __forceinline__ float scaled_value(float x, int row, int col, const GemmParams& p) {
   if (p.addend) x += p.addend[static_cast<long long>(row) * p.ld_addend + col];
-  if (p.alpha) x *= __ldg(p.alpha);
+  return x * __ldg(p.alpha);
+}
+
+// Full epilogue of one float32 sum at (row, col): (sum + bias) -> activation -> + residual.
+__device__ __forceinline__ float epilogue_value(float x, int row, int col, const GemmParams& p) {
   if (p.bias) x += __half2float(p.bias[col]);
   x = activation(x, p.act);
   if (p.residual) x += __half2float(p.residual[static_cast<long long>(row) * p.ldr + col]);
@@ -614,35 +617,41 @@ __device__ __forceinline__ void load_half32(const __half* src, int col, int n, f
   }
 }
 
-// General fused epilogue of 32 consecutive columns of one row: x = alpha (acc + addend) + bias,
-// activation, + residual, then fp16 pairs into pk[0..15].
+// 32 consecutive columns of one row scaled: fp16 pairs of alpha (acc + addend) into pk[0..15].
+__device__ __forceinline__ void epilogue_scaled_32(const uint32_t (&acc)[32], int row, int col,
+                                                   const GemmParams& p, uint32_t* pk) {
+  const float a = __ldg(p.alpha);
+  if (p.addend == nullptr || row >= p.M) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const __half2 h = __floats2half2_rn(__uint_as_float(acc[2 * i]) * a,
+                                          __uint_as_float(acc[2 * i + 1]) * a);
+      pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return;
+  }
+  // ld_addend is a multiple of 32, its rows 128-byte aligned and that long
+  const float4* w = reinterpret_cast<const float4*>(
+      p.addend + static_cast<long long>(row) * p.ld_addend + col);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 v = col + 4 * i < p.N ? __ldcs(w + i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const __half2 lo = __floats2half2_rn((__uint_as_float(acc[4 * i]) + v.x) * a,
+                                         (__uint_as_float(acc[4 * i + 1]) + v.y) * a);
+    const __half2 hi = __floats2half2_rn((__uint_as_float(acc[4 * i + 2]) + v.z) * a,
+                                         (__uint_as_float(acc[4 * i + 3]) + v.w) * a);
+    pk[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
+    pk[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+  }
+}
+
+// General fused epilogue of 32 consecutive columns of one row: x = acc + bias, activation,
+// + residual, then fp16 pairs into pk[0..15].
 __device__ __forceinline__ void epilogue_general_32(const uint32_t (&acc)[32], int row, int col,
                                                     const GemmParams& p, uint32_t* pk) {
   float x[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(acc[i]);
-  if (p.addend && row < p.M) {  // ld_addend is a multiple of 32, its rows 128-byte aligned
-    const float* w = p.addend + static_cast<long long>(row) * p.ld_addend + col;
-    if (col + 32 <= p.N) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(w) + i);
-        x[4 * i] += v.x;
-        x[4 * i + 1] += v.y;
-        x[4 * i + 2] += v.z;
-        x[4 * i + 3] += v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (col + i < p.N) x[i] += w[i];
-    }
-  }
-  if (p.alpha) {
-    const float a = __ldg(p.alpha);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] *= a;
-  }
   if (p.bias) {
     float b[32];
     load_half32(p.bias, col, p.N, b);  // the same 64 bytes for every lane: broadcast
@@ -686,22 +695,14 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
                                                 const uint32_t (&r1)[32], int row0, int col0,
                                                 uint8_t* stg, int& sb, int lane) {
   uint32_t pk[32];
-  if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu && p.addend == nullptr) {
-    if (p.alpha) {
-      const float a = __ldg(p.alpha);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        pk[i] = relu_pack_h2(__float_as_uint(__uint_as_float(r0[2 * i]) * a),
-                             __float_as_uint(__uint_as_float(r0[2 * i + 1]) * a), p.act);
-        pk[16 + i] = relu_pack_h2(__float_as_uint(__uint_as_float(r1[2 * i]) * a),
-                                  __float_as_uint(__uint_as_float(r1[2 * i + 1]) * a), p.act);
-      }
-    } else {
+  if (p.alpha) {
+    epilogue_scaled_32(r0, row0 + lane, col0, p, pk);
+    epilogue_scaled_32(r1, row0 + lane, col0 + 32, p, pk + 16);
+  } else if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       pk[i] = relu_pack_h2(r0[2 * i], r0[2 * i + 1], p.act);
       pk[16 + i] = relu_pack_h2(r1[2 * i], r1[2 * i + 1], p.act);
-    }
     }
   } else {
     // general fused epilogue, 32 columns at a time; columns past N and rows past M are
