@@ -21,7 +21,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libtg_gemm_relu.so")
 
 SOURCES = ["tg_api.cu", "tg_gemm_bn256.cu", "tg_gemm_bn192.cu", "tg_gemm_bn128.cu",
-           "tg_gemm_pair.cu", "tg_gemm_w4.cu", "tg_no_alloc.cu", "tg_head_gemm.cu",
+           "tg_gemm_pair.cu", "tg_gemm_w4.cu", "tg_no_alloc.cu", "tg_head_gemm.cu", "tg_head_scaled.cu",
            "tg_head.cu", "tg_norm.cu"]
 HEADERS = ["tg_gemm_kernel.cuh", "tg_gemm_w4.cuh", "tg_head_kernel.cuh", "tg_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1066,6 +1066,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   auto launch = [&](const tg::GemmLaunch& l) -> cudaError_t {
     if (logits) return tg::launch_head_logits(l, *logits, P.cta_pair ? 0 : P.block_n);
     if (out32 && extra->add) return tg::launch_head_add(l);
+    if (l.p.alpha && !ws) return tg::launch_gemm_scaled(l, P.cta_pair ? 0 : P.block_n);
     if (P.a_row_classes) return tg::launch_gemm_pair_cls(cls, l);
     if (P.cta_pair) return tg::launch_gemm_pair(l, ws != nullptr);
     switch (P.block_n) {

@@ -82,8 +82,8 @@ struct GemmParams {
   const __half* bias;
   const __half* residual;
   long long ldr;
-  // fp16 output only, alpha not nullptr: C = fp16((sum + addend[i*ld_addend + j]) * *alpha) in place of
-  // the epilogue above (device float32; addend nullptr: 0)
+  // kModeScaled: C = fp16((sum + addend[i*ld_addend + j]) * *alpha) in place of the epilogue above
+  // (device float32; addend nullptr: 0)
   const float* alpha;
   const float* addend;
   long long ld_addend;
@@ -95,9 +95,11 @@ struct GemmParams {
   unsigned char cls_shift[kARowClasses];
 };
 
-// What the epilogue of a float32 output does with a tile: stores it, or adds it to the output
-// (each element is added to once a launch, so the result does not depend on order).
-enum : int { kModePlain = 0, kModeAdd = 1 };
+// What the epilogue does with a tile.  Plain: the fused epilogue (fp16 output) or a store
+// (float32).  Add: a float32 tile is added to the output (each element is added to once a
+// launch, so the result does not depend on order).  Scaled: fp16(alpha (sum + addend)).  A mode
+// of the kernel and not a branch in it, so that the plain kernels carry none of the others.
+enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2 };
 
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3 };
 
@@ -690,12 +692,13 @@ __device__ __forceinline__ void epilogue_general_32(const uint32_t (&acc)[32], i
 // 64 columns of one row per lane (float32 bits in r0 = columns 0..31, r1 = 32..63): epilogue,
 // fp16 pack, 128B-swizzled staging and TMA store of the warp's 32 x 64 block; columns in
 // [n_tma, N) are written with plain stores.
+template <int MODE = kModePlain>
 __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const GemmParams& p,
                                                 const uint32_t (&r0)[32],
                                                 const uint32_t (&r1)[32], int row0, int col0,
                                                 uint8_t* stg, int& sb, int lane) {
   uint32_t pk[32];
-  if (p.alpha) {
+  if constexpr (MODE == kModeScaled) {
     epilogue_scaled_32(r0, row0 + lane, col0, p, pk);
     epilogue_scaled_32(r1, row0 + lane, col0 + 32, p, pk + 16);
   } else if (p.bias == nullptr && p.residual == nullptr && p.act <= kActRelu) {
@@ -779,7 +782,8 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
     release();
     return;
   }
-  static_assert(OUT_F32 || MODE == kModePlain, "modes are of the float32 output");
+  static_assert(MODE == kModePlain || (OUT_F32 ? MODE == kModeAdd : MODE == kModeScaled),
+                "the sum is added in float32 and scaled in fp16");
   if constexpr (!OUT_F32) {
 #pragma unroll 1
     for (int c = 0; c < BN / 64; ++c) {
@@ -793,7 +797,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
         unperm8(r0);
         unperm8(r1);
       }
-      store_chunk_f16(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
+      store_chunk_f16<MODE>(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
     }
   } else {
 #pragma unroll 1
@@ -836,7 +840,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
 // 0); the single producer and MMA threads then build descriptors and TMA boxes from constants,
 // which keeps their per-k-block instruction count inside the MMA time.  GENERAL == true reads
 // the layouts from p.a_mn and p.b_k (the transposed-operand GEMMs of the backward pass).
-template <int BN, bool OUT_F32, bool GENERAL>
+template <int BN, bool OUT_F32, bool GENERAL, int MODE = kModePlain>
 __global__ void __launch_bounds__(kThreads, 1)
     tg_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -997,8 +1001,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
-      epilogue_tile<BN, OUT_F32>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN, w.split,
-                                 stg, sb, smem_u32(&tempty[buf]), false, lane);
+      epilogue_tile<BN, OUT_F32, false, MODE>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN,
+                                              w.split, stg, sb, smem_u32(&tempty[buf]), false,
+                                              lane);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
@@ -1018,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // counter.  The warp that arrives second adds the two halves (a + b == b + a in IEEE
 // arithmetic, so the sum does not depend on which half finished last), runs the normal
 // epilogue and resets the counter.  No warp waits for another CTA.
-template <int BN>
+template <int BN, int MODE>
 __device__ __forceinline__ void epilogue_tail(const CUtensorMap* tmOut, const GemmParams& p,
                                               uint32_t tl, int row0, int col_base, int slot,
                                               int half, int part, uint8_t* stg, int& sb,
@@ -1065,7 +1070,7 @@ __device__ __forceinline__ void epilogue_tail(const CUtensorMap* tmOut, const Ge
       r1[j] = __float_as_uint(mine[(c * 64 + 32 + j) * 32] +
                               __ldcg(other + (c * 64 + 32 + j) * 32));
     }
-    store_chunk_f16(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
+    store_chunk_f16<MODE>(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
   }
   if (lane == 0) p.tail_cnt[slot * 8 + part] = 0;  // ready for the next launch
 }
@@ -1333,8 +1338,9 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
       const int row0 = w.m_blk * 2 * kBM + static_cast<int>(rank) * kBM + q * 32;
       const uint32_t release_bar = mapa_shared(smem_u32(&tempty[buf]), 0);
       if (!OUT_F32 && w.tail_slot >= 0)
-        epilogue_tail<Cfg::kBN>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot, w.split,
-                                static_cast<int>(rank) * 4 + q, stg, sb, release_bar, lane);
+        epilogue_tail<Cfg::kBN, MODE>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot,
+                                      w.split, static_cast<int>(rank) * 4 + q, stg, sb,
+                                      release_bar, lane);
       else
         epilogue_tile<Cfg::kBN, OUT_F32, false, MODE>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN,
                                                       w.split, stg, sb, release_bar, true, lane);

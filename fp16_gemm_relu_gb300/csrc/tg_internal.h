@@ -46,6 +46,9 @@ struct LogitsExtra {
 cudaError_t launch_head_logits(const GemmLaunch& l, const LogitsExtra& x, int block_n);
 // The CTA-pair kernel that adds A^T B to its float32 output (kModeAdd; A stored K x M).
 cudaError_t launch_head_add(const GemmLaunch& l);
+// The fp16-output kernels whose epilogue is the scaled sum (kModeScaled; block_n 0: CTA pairs).
+// A^T B^T is not among the head's products and not a launch.
+cudaError_t launch_gemm_scaled(const GemmLaunch& l, int block_n);
 // Clusters of two that can be resident at once on the current device.
 cudaError_t gemm_pair_max_clusters(int* out);
 
@@ -74,8 +77,8 @@ bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 // With `logits` or out32 there are no K splits and no fp16 output (C is not used).
 struct GemmExtra {
   const LogitsExtra* logits;
-  const float* alpha;   // fp16 output: C = fp16(alpha (A B + addend)), both device float32
-  const float* addend;  // (NULL: 1 and 0), rows of ld32
+  const float* alpha;   // fp16 output, device float32: C = fp16(alpha (A B + addend)) (NULL: the
+  const float* addend;  // plain product); addend, device float32, rows of ld32 (NULL: 0)
   float* out32;         // float32 output, rows of ld32 floats (a multiple of 32)
   int64_t ld32;
   bool add;             // add to out32 (A stored K x M, B stored K x N) instead of writing it
