@@ -556,8 +556,22 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
       ex.a_rows = std::max(n, kLeastRows);
+      // One row of tiles reads W once at the memory's rate, if the splits of V make one wave of
+      // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
+      // products' costs and for 128 tokens 20.4 against 20.7, 131072 x 4096 166 against 203, 28672 x
+      // 8192 for one token 77 against 119; two rows of tiles gain at some widths and lose at others).
+      // Narrow W: narrow tiles.
+      tg_options opt = gemm_opt;
+      const int64_t width = h.D <= 2048 ? 128 : 256;
+      const int64_t splits =
+          std::min({sms / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)});
+      if (n <= 128 && splits > 1) {
+        opt.pair = -1;
+        opt.block_n = static_cast<int>(width);
+        opt.split_k = static_cast<int>(splits);
+      }
       st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, n, h.D,
-                          h.V, ldg, ldw, h.lddx, ex, &gemm_opt, stream);
+                          h.V, ldg, ldw, h.lddx, ex, &opt, stream);
       if (st != TG_OK) return done(st);
     }
     if (h.dW) {  // G^T X (V x D), or X^T G (D x V)
