@@ -578,6 +578,10 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int64_t g = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;  // group of 4 columns
   if (g >= (N + 3) >> 2) return;
   const int64_t c0 = g << 2;
+  if constexpr (SCALED) {
+    tg::chain_wait();
+    tg::chain_release();
+  }
   for (int64_t r0 = int64_t(blockIdx.y) * kReduceRows; r0 < M;
        r0 += int64_t(gridDim.y) * kReduceRows) {
     // rows past M read row M - 1 (in bounds) and are never stored
@@ -642,6 +646,10 @@ __global__ void __launch_bounds__(kReduceThreads)
   const int64_t g = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;  // group of 4 columns
   const int64_t N = p.N, r = blockIdx.y, c0 = g << 2;
   if (c0 >= N) return;
+  if constexpr (SCALED) {
+    tg::chain_wait();
+    tg::chain_release();
+  }
   const float* w = ws + r * ldw + c0;
   float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int s0 = 0; s0 < splits; s0 += kReduceAhead) {
@@ -683,12 +691,18 @@ void launch_reduce(const float* ws, int64_t ldw, int64_t split_stride, int split
                    cudaStream_t stream) {
   if (cls_rows == 0 && splits > 1 && reduce_small(p.M, p.N, num_sms)) {
     const dim3 grid(reduce_grid(p.M, p.N).x, static_cast<unsigned>(p.M));
-    auto kern = p.alpha ? tg_splitk_reduce_small_kernel<true> : tg_splitk_reduce_small_kernel<false>;
-    kern<<<grid, kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C, ldc, p);
+    if (p.alpha)
+      tg::launch_chained(tg_splitk_reduce_small_kernel<true>, true, grid, kReduceThreads, 0, stream, ws,
+                         ldw, split_stride, splits, C, ldc, p);
+    else
+      tg_splitk_reduce_small_kernel<false>
+          <<<grid, kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C, ldc, p);
+  } else if (p.alpha) {
+    tg::launch_chained(tg_splitk_reduce_kernel<true>, true, reduce_grid(p.M, p.N), kReduceThreads, 0,
+                       stream, ws, ldw, split_stride, splits, C, ldc, p, cls_rows);
   } else {
-    auto kern = p.alpha ? tg_splitk_reduce_kernel<true> : tg_splitk_reduce_kernel<false>;
-    kern<<<reduce_grid(p.M, p.N), kReduceThreads, 0, stream>>>(ws, ldw, split_stride, splits, C, ldc,
-                                                               p, cls_rows);
+    tg_splitk_reduce_kernel<false><<<reduce_grid(p.M, p.N), kReduceThreads, 0, stream>>>(
+        ws, ldw, split_stride, splits, C, ldc, p, cls_rows);
   }
 }
 
@@ -1032,6 +1046,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   gp.residual = static_cast<const __half*>(epi.residual);
   gp.ldr = epi.residual ? epi.ldr : 0;
   if (extra) {
+    L.chained = extra->chained && !P.repack_a && !P.repack_b && !P.tail_tiles;
     gp.alpha = extra->alpha;
     gp.addend = extra->addend;
     gp.ld_addend = extra->ld32;

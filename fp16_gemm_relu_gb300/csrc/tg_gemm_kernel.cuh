@@ -101,6 +101,12 @@ struct GemmParams {
 // of the kernel and not a branch in it, so that the plain kernels carry none of the others.
 enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2 };
 
+// Kernels that are launched chained.  chain_wait: nothing that the kernel before has written is read,
+// and nothing that it reads is written, before this.  chain_release, after it: the next kernel's
+// blocks may take what room this one leaves.
+__device__ __forceinline__ void chain_wait() { cudaGridDependencySynchronize(); }
+__device__ __forceinline__ void chain_release() { cudaTriggerProgrammaticLaunchCompletion(); }
+
 enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3 };
 
 // The activations of the fused epilogue, in float32:
@@ -894,6 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  if constexpr (MODE == kModeScaled) {
+    chain_wait();
+    chain_release();
+  }
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
@@ -1192,6 +1202,10 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  if constexpr (MODE == kModeScaled) {
+    chain_wait();
+    chain_release();
+  }
 
   if (warp == 0) {
     // ------------------------------ TMA producer (both CTAs) ------------------------------

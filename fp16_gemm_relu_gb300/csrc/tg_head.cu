@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(1024)
     tg_head_weight_kernel(const float* __restrict__ dloss, const int64_t* __restrict__ index,
                           int64_t ld, int top, int64_t ignore, int64_t rows, unsigned* wmax) {
   __shared__ float part[32];
+  tg::chain_release();
   float m = 0.0f;
   for (int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; r < rows;
        r += int64_t(gridDim.x) * blockDim.x) {
@@ -158,6 +159,8 @@ __global__ void __launch_bounds__(kRowThreads)
   __shared__ float slots[5][4];
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x;
+  tg::chain_wait();
+  tg::chain_release();
   const float w = wmax ? __uint_as_float(*wmax) : 0.0f;
   if (alpha && r == 0 && tid == 0) *alpha = scale * w / kGScale;
   // the first entries and their logits are on their way while the statistics are reduced
@@ -251,6 +254,8 @@ __global__ void __launch_bounds__(256)
                         int64_t ldw, const int64_t* __restrict__ index, int64_t ldt, int top,
                         int64_t rows, int64_t vocab, int width, float* __restrict__ picked) {
   const int lane = threadIdx.x & 31;
+  tg::chain_wait();
+  tg::chain_release();
   const int64_t groups = (top + kPickRows - 1) / kPickRows;
   const int64_t step = int64_t(gridDim.x) * (blockDim.x >> 5);
   for (int64_t it = blockIdx.x * int64_t(blockDim.x >> 5) + (threadIdx.x >> 5); it < rows * groups;
@@ -298,6 +303,8 @@ __global__ void __launch_bounds__(256)
                         uint16_t* __restrict__ g, int64_t ldg) {
   const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   if (v0 >= vocab) return;
+  tg::chain_wait();
+  tg::chain_release();
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const RowInfo ri = info[r];
     const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
@@ -326,6 +333,8 @@ __global__ void __launch_bounds__(128)
                                 int64_t rows, int64_t vocab, __half* __restrict__ g, int64_t ldg) {
   const int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
   if (r >= rows) return;
+  tg::chain_wait();
+  tg::chain_release();
   const RowInfo ri = info[r];
   for (int e = threadIdx.x & 31; e < top; e += 32) {
     const int64_t i = index[r * ldt + e];
@@ -509,6 +518,12 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   gemm_opt.timeout_ms = h.o.timeout_ms;
   gemm_opt.debug_flags = h.o.debug_flags;
   const float c = h.scale * kLog2e;
+  // the kernels between the products, each chained to the launch before it; the first error stays
+  e = cudaSuccess;
+  auto chain = [&](auto kern, dim3 grid, int threads, const auto&... args) {
+    const cudaError_t le = tg::launch_chained(kern, true, grid, threads, 0, stream, args...);
+    if (e == cudaSuccess) e = le;
+  };
   for (int64_t t0 = 0; t0 < h.T; t0 += piece) {
     const int64_t n = std::min(piece, h.T - t0);
     const uint16_t* x = X + t0 * ldx;
@@ -531,30 +546,34 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
     if (h.T < kLeastRows) ex.a_rows = kLeastRows - t0;
+    ex.chained = grad || copy_x || copy_w || t0 > 0;
     st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &gemm_opt,
                         stream);
     if (st != TG_OK) return done(st);
     if (pick)
-      tg_head_pick_kernel<<<static_cast<unsigned>(std::min<int64_t>(
-                                cdiv(n * cdiv(h.top, kPickRows), 8), 16 * int64_t(sms))),
-                            256, 0, stream>>>(x, ldx, static_cast<const uint16_t*>(W), ldw, index, h.ldt,
-                                      h.top, n, h.V, static_cast<int>(h.D), picked);
-    tg_head_rows_kernel<<<static_cast<unsigned>(n), kRowThreads, 0, stream>>>(
+      chain(tg_head_pick_kernel,
+            dim3(static_cast<unsigned>(
+                std::min<int64_t>(cdiv(n * cdiv(h.top, kPickRows), 8), 16 * int64_t(sms)))),
+            256, x, ldx, static_cast<const uint16_t*>(W), ldw, index, h.ldt, h.top, n, h.V,
+            static_cast<int>(h.D), picked);
+    chain(tg_head_rows_kernel, dim3(static_cast<unsigned>(n)), kRowThreads,
         stats, static_cast<int>(2 * cdiv(h.V, block_n)), Logits{z, ldz, picked}, h.scale, h.V, index, h.ignore,
         teacher, h.teacher_f32, h.ldt, h.top, dloss, wmax, loss, h.lse ? h.lse + t0 : nullptr, info,
         q, alpha);
-    if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
+    if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     if (!grad) continue;
-    tg_head_grad_kernel<<<dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
-                               static_cast<unsigned>(std::min<int64_t>(n, 65535))),
-                          256, 0, stream>>>(z, ldz, c, info, n, h.V, g, ldg);
+    chain(tg_head_grad_kernel,
+          dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
+               static_cast<unsigned>(std::min<int64_t>(n, 65535))),
+          256, z, ldz, c, info, n, h.V, g, ldg);
     if (h.top)
-      tg_head_teacher_grad_kernel<<<static_cast<unsigned>(cdiv(n, 4)), 128, 0, stream>>>(
-          index, h.ldt, h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg);
-    if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
+      chain(tg_head_teacher_grad_kernel, dim3(static_cast<unsigned>(cdiv(n, 4))), 128, index, h.ldt,
+            h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg);
+    if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     if (h.dX) {  // G (n x V) times W (V x D, or stored D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
+      ex.chained = true;
       ex.a_rows = std::max(n, kLeastRows);
       // One row of tiles reads W once at the memory's rate, if the splits of V make one wave of
       // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
@@ -577,6 +596,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     if (h.dW) {  // G^T X (V x D), or X^T G (D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
+      ex.chained = true;
       if (sum_w) {  // the first piece writes the sums, the last takes them into its epilogue
         ex.ld32 = ldw32;
         if (t0 + piece < h.T) {

@@ -11,8 +11,8 @@ cudaError_t launch(K kern, int threads, int smem, const GemmLaunch& l, const P& 
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<l.grid, threads, smem, l.stream>>>(l.a, l.b, l.out, p);
-  return cudaGetLastError();
+  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), threads, smem, l.stream,
+                        l.a, l.b, l.out, p);
 }
 
 template <bool B_K, bool STORE>
@@ -50,8 +50,13 @@ cudaError_t launch_head_logits(const GemmLaunch& l, const LogitsExtra& x, int bl
 
 cudaError_t launch_head_add(const GemmLaunch& l) {
   if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
-  return launch(tg_gemm_pair_kernel<true, true, false, kModeAdd>, kThreads, PairCfgFwd::kSmemBytes,
-                l, l.p);
+  auto kern = tg_gemm_pair_kernel<true, true, false, kModeAdd>;
+  constexpr int smem = PairCfgFwd::kSmemBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.out, l.p);
+  return cudaGetLastError();
 }
 
 }  // namespace tg

@@ -166,6 +166,8 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
     __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  chain_wait();
+  chain_release();
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------

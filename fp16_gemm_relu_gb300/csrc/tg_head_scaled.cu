@@ -9,8 +9,8 @@ cudaError_t launch(K kern, int smem, const GemmLaunch& l) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.out, l.p);
-  return cudaGetLastError();
+  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), kThreads, smem, l.stream,
+                        l.a, l.b, l.out, l.p);
 }
 
 template <int BN>

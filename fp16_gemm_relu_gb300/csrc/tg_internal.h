@@ -16,7 +16,27 @@ struct GemmLaunch {
   GemmParams p;
   int grid;
   cudaStream_t stream;
+  bool chained;  // logits and scaled kernels: the launch before it on the stream is the library's
 };
+
+// A launch that may begin while the kernel before it on the stream still runs: its blocks are made
+// and set up early, and chain_wait (tg_gemm_kernel.cuh) in the kernel holds each thread until all
+// of the kernel before has finished and its writes are visible.
+template <typename... P, typename... Q>
+cudaError_t launch_chained(void (*kern)(P...), bool chained, dim3 grid, int threads, size_t smem,
+                           cudaStream_t stream, const Q&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 
 // Shared-memory bytes and stage count of the kernel for a tile width.
 int gemm_smem_bytes(int block_n);
@@ -82,6 +102,7 @@ struct GemmExtra {
   float* out32;         // float32 output, rows of ld32 floats (a multiple of 32)
   int64_t ld32;
   bool add;             // add to out32 (A stored K x M, B stored K x N) instead of writing it
+  bool chained;         // logits or alpha: see GemmLaunch
   int64_t a_rows;       // 0, or the rows (>= M) that A, stored M x K and not copied, has in memory
 };
 tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
