@@ -25,6 +25,17 @@
 
 namespace {
 
+// How a matrix's rows lie.  Whole: every row starts on a 16-byte boundary and its width is a multiple
+// of 8 elements.  Alike: a call's matrices miss the boundaries by the same bytes, row by row
+// (contiguous rows of any width do).  Any: each matrix in its own way.
+//
+// Alike rows r and r + 8 start equally far from a boundary (8 rows are a multiple of 16 bytes
+// apart), so a block that takes every eighth row can work on aligned 16-byte blocks, `off` elements to
+// the left of the row's own chunks of eight, and keeps the same columns for all of them: nothing is
+// shifted, and only a row's first and last block need care.  4095 x 3073 forward 20.5 us, shifted 31.8,
+// backward 41 and 47; 4096 x 12287 61 and 100, 143 and 199.
+enum : int { kRowsAny = 0, kRowsAlike = 1, kRowsWhole = 2 };
+
 // 16 bytes of the 32 in (lo, hi), from byte s on (even, below 16).  s is the same for a row's
 // threads, so this branches on it, where selects by its bits would be 20 instructions.
 template <int WORD, bool HALF>
@@ -119,6 +130,24 @@ __device__ __forceinline__ void store_chunk(uint16_t* row, int c, int n, uint4 v
   }
 }
 
+// The same in a ring kernel.  Alike rows: chunk c begins off elements before 8c, on a 16-byte boundary.
+template <int A>
+__device__ __forceinline__ void store_row_chunk(uint16_t* row, int c, int off, int n, uint4 v, int lane) {
+  if constexpr (A != kRowsAlike) {
+    store_chunk<A == kRowsWhole>(row, c, n, v, lane);
+    return;
+  }
+  const int e0 = (c << 3) - off;
+  if (e0 >= 0 && e0 + 8 <= n) {
+    *reinterpret_cast<uint4*>(row + e0) = v;
+  } else if (e0 < n) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e0 + i >= 0 && e0 + i < n) row[e0 + i] = static_cast<uint16_t>(w[i >> 1] >> ((i & 1) << 4));
+  }
+}
+
 // Two float32 values in a 64-bit register pair, and the arithmetic on such pairs (one instruction
 // for both, each rounded as usual): the kernels below spend most of their issue slots on it.
 using f32x2 = unsigned long long;
@@ -178,11 +207,12 @@ __device__ __forceinline__ float as_float(const float* p) { return *p; }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-// Eight parameters from column 8c on (`none` where there are none: a null pointer or past n).
-// VEC: the pointer is 16-byte aligned and n a multiple of 8.
+// Eight parameters from column 8c - off on (`none` where there are none: a null pointer, before 0 or
+// past n).  VEC: the pointer is 16-byte aligned, n a multiple of 8 and off 0.
 template <bool VEC, typename P>
-__device__ __forceinline__ void load_param(const P* p, int c, int n, float none, f32x2 (&f)[4]) {
-  const int e0 = c << 3;
+__device__ __forceinline__ void load_param(const P* p, int c, int n, float none, f32x2 (&f)[4],
+                                           int off = 0) {
+  const int e0 = VEC ? c << 3 : (c << 3) - off;
   if (VEC && p != nullptr && e0 < n) {
     if constexpr (sizeof(P) == 2) {
       unpack8(__ldg(reinterpret_cast<const uint4*>(p + e0)), f);
@@ -196,15 +226,17 @@ __device__ __forceinline__ void load_param(const P* p, int c, int n, float none,
   float g[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    g[i] = (!VEC && p != nullptr && e0 + i < n) ? as_float(p + e0 + i) : none;
+    g[i] = (!VEC && p != nullptr && e0 + i >= 0 && e0 + i < n) ? as_float(p + e0 + i) : none;
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = pair(g[2 * i], g[2 * i + 1]);
 }
 
-// Eight columns from e0 on of a partial row of dgamma and dbeta (16-byte aligned rows).
+// Eight columns from e0 on of a partial row of dgamma and dbeta (16-byte aligned rows; WHOLE: e0 is a
+// multiple of 8).
+template <bool WHOLE>
 __device__ __forceinline__ void put_part(float* to_g, float* to_b, int e0, int n, const f32x2 (&g)[4],
                                          const f32x2 (&b)[4]) {
-  if (e0 + 8 <= n) {
+  if (WHOLE && e0 + 8 <= n) {
     ulonglong2* pg = reinterpret_cast<ulonglong2*>(to_g + e0);
     ulonglong2* pb = reinterpret_cast<ulonglong2*>(to_b + e0);
     pg[0] = make_ulonglong2(g[0], g[1]);
@@ -217,8 +249,8 @@ __device__ __forceinline__ void put_part(float* to_g, float* to_b, int e0, int n
   for (int j = 0; j < 4; ++j) {
     const int e = e0 + 2 * j;
     const float2 fg = halves(g[j]), fb = halves(b[j]);
-    if (e < n) to_g[e] = fg.x, to_b[e] = fb.x;
-    if (e + 1 < n) to_g[e + 1] = fg.y, to_b[e + 1] = fb.y;
+    if (e >= 0 && e < n) to_g[e] = fg.x, to_b[e] = fb.x;
+    if (e + 1 >= 0 && e + 1 < n) to_g[e + 1] = fg.y, to_b[e + 1] = fb.y;
   }
 }
 
@@ -292,30 +324,32 @@ __device__ __forceinline__ void slot_wait(uint32_t bar, uint32_t parity, volatil
 
 // 1 for the columns `col` and `col` + 1 that a row of n has, 0 for the others.
 __device__ __forceinline__ f32x2 there(int col, int n) {
-  return pair(col < n ? 1.0f : 0.0f, col + 1 < n ? 1.0f : 0.0f);
+  return pair(col >= 0 && col < n ? 1.0f : 0.0f, col + 1 >= 0 && col + 1 < n ? 1.0f : 0.0f);
 }
 
-// Elements [8c, 8c + 8) of the row in a slot, zeros from n on; b: bytes from the slot's start to the
-// row's (0 with VEC).  Otherwise the two blocks that hold them are shifted together: with 4-byte
-// reads at the row's own offset, a warp's pairs contiguous, 8192 x 4096 forward took 63 us, not 37.
-template <bool VEC>
+// Chunk c of the row in a slot, zeros where the row has no element; b: bytes from the slot's start to
+// the row's.  Whole and alike rows: block c of the slot, of which an alike row may have only a part (b
+// is 2 off then).  Else elements [8c, 8c + 8), shifted together from the two blocks that hold them: with
+// 4-byte reads at the row's own offset, a warp's pairs contiguous, 8192 x 4096 forward took 63 us, not 37.
+template <int A>
 __device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int c, int n) {
   uint4 v = make_uint4(0, 0, 0, 0);
-  const int e0 = c << 3;
+  const int e0 = (c << 3) - (A == kRowsAlike ? static_cast<int>(b >> 1) : 0);
   if (e0 < n) {
     const uint4* blk = reinterpret_cast<const uint4*>(slot) + c;
     v = blk[0];
-    if constexpr (!VEC) {
-      v = shift16(v, blk[1], b);
-      if (e0 + 8 > n) {
-        uint32_t o[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (A == kRowsAny) v = shift16(v, blk[1], b);
+    if (A != kRowsWhole && ((A == kRowsAlike && e0 < 0) || e0 + 8 > n)) {
+      uint32_t o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (e0 + 2 * i >= n) o[i] = 0u;
-          else if (e0 + 2 * i + 1 >= n) o[i] &= 0xFFFFu;
-        }
-        v = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + 2 * i;
+        if (e >= n) o[i] = 0u;
+        else if (e + 1 >= n) o[i] &= 0xFFFFu;
+        if (A == kRowsAlike && e + 1 < 0) o[i] = 0u;
+        else if (A == kRowsAlike && e < 0) o[i] &= 0xFFFF0000u;
       }
+      v = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
   return v;
@@ -349,12 +383,13 @@ __device__ __forceinline__ float group_sum(float v, int tpr, int id, float* slot
 // value: the chunks' first halves, then their second halves, so that a warp's 16-byte reads of
 // either are contiguous (side by side they would meet in the same banks two by two).
 template <bool VEC, typename P>
-__device__ __forceinline__ void stage_param(float* dst, const P* p, int n, int chunks, float none) {
+__device__ __forceinline__ void stage_param(float* dst, const P* p, int n, int chunks, float none,
+                                            int off) {
   ulonglong2* q = reinterpret_cast<ulonglong2*>(dst);
 #pragma unroll 4
   for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
     f32x2 f[4];
-    load_param<VEC>(p, c, n, none, f);
+    load_param<VEC>(p, c, n, none, f, off);
     q[c] = make_ulonglong2(f[0], f[1]);
     q[chunks + c] = make_ulonglong2(f[2], f[3]);
   }
@@ -371,18 +406,28 @@ __device__ __forceinline__ uint32_t row_shift(const uint16_t* p, int64_t ld, int
           2u * static_cast<uint32_t>(ld) * static_cast<uint32_t>(row)) & 15u;
 }
 
+// The first row of a group; its others follow in steps of the grid's groups.  Alike rows: a block's
+// rows are all in the class blockIdx.x mod 8 (the grid is a multiple of 8).
+template <int A>
+__device__ __forceinline__ int first_row(int per_block, int group) {
+  if constexpr (A == kRowsAlike)
+    return (blockIdx.x & 7) + 8 * ((blockIdx.x >> 3) * per_block + group);
+  return blockIdx.x * per_block + group;
+}
+
 constexpr int kFwdChunks = 4, kFwdSlots = 2;
 
 // Forward, kFwdChunks chunks a thread: 32 elements share the reductions' and the loop's cost.
-// 16384 x 4096 took 45 us, 0.88 of the copy rate (a row a warp in registers 59, two chunks a thread
+// 16384 x 4096 takes 46 us, 0.86 of the copy rate (a row a warp in registers 59, two chunks a thread
 // from global memory 59).
-template <int THREADS, int BLOCKS, bool VEC, typename P>
+template <int THREADS, int BLOCKS, int A, typename P>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
     tg_layernorm_kernel(const uint16_t* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
                         const P* __restrict__ beta, uint16_t* __restrict__ y, int64_t ldy,
                         float* __restrict__ mean, float* __restrict__ rstd, int rows, int n,
                         float eps, unsigned* err, int tpr, int slot_bytes) {
   constexpr int CH = kFwdChunks, S = kFwdSlots;
+  constexpr bool VEC = A == kRowsWhole;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
   __shared__ float sums[8][2][16];
@@ -393,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   float* so = sg + chunks * 8;
   uint8_t* ring = reinterpret_cast<uint8_t*>(so + chunks * 8) + group * S * slot_bytes;
   const Span sp = span_of(x, ldx, rows, n);
-  const int step = gridDim.x * per_block, first = blockIdx.x * per_block + group;
+  const int step = gridDim.x * per_block, first = first_row<A>(per_block, group);
   const int count = first < rows ? (rows - 1 - first) / step + 1 : 0;  // rows of this group
   auto fetch = [&](int k, int s) {
     const uint16_t* src = x + (first + int64_t(k) * step) * ldx;
@@ -410,19 +455,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     tg::fence_mbar_init();
     for (int s = 0; s < S && s < count; ++s) fetch(s, s);
   }
-  stage_param<VEC>(sg, gamma, n, chunks, 1.0f);
-  stage_param<VEC>(so, beta, n, chunks, 0.0f);
+  const uint32_t shift = A == kRowsAlike ? row_shift(x, ldx, first) : 0u;  // of all the group's rows
+  const int off = static_cast<int>(shift >> 1);
+  stage_param<VEC>(sg, gamma, n, chunks, 1.0f, off);
+  stage_param<VEC>(so, beta, n, chunks, 0.0f, off);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
   for (int k = 0; k < count; ++k) {
     const int s = k & 1;
     const int64_t r = first + int64_t(k) * step;
     slot_wait(tg::smem_u32(&bars[group][s]), (k >> 1) & 1, &late, err);
-    const uint32_t b = VEC ? 0u : row_shift(x, ldx, r);
+    const uint32_t b = A == kRowsAny ? row_shift(x, ldx, r) : shift;
     f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      unpack8(slot_chunk<VEC>(ring + s * slot_bytes, b, i * tpr + t, n), v[i]);
+      unpack8(slot_chunk<A>(ring + s * slot_bytes, b, i * tpr + t, n), v[i]);
       acc = add2(acc, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
     }
     const float mu = group_sum(sum2(acc), tpr, group, sums[group][0]) * inv_n;
@@ -431,14 +478,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     f32x2 q = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+      const int e0 = ((i * tpr + t) << 3) - off;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = ((i * tpr + t) << 3) + 2 * j;
-        v[i][j] = add2(v[i][j], less);
-        if (VEC || col + 1 < n) {
-          if (col < n) q = fma2(v[i][j], v[i][j], q);
-        } else {
-          const f32x2 d = mul2(v[i][j], there(col, n));
+      for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], less);
+      if (VEC ? e0 < n : e0 >= 0 && e0 + 8 <= n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q = fma2(v[i][j], v[i][j], q);
+      } else if (!VEC && e0 < n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x2 d = mul2(v[i][j], there(e0 + 2 * j, n));
           q = fma2(d, d, q);
         }
       }
@@ -456,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
       staged(so, i * tpr + t, chunks, o);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = fma2(mul2(v[i][j], times), g[j], o[j]);
-      store_chunk<VEC>(y + r * ldy, i * tpr + t, n, pack8(o), lane);
+      store_row_chunk<A>(y + r * ldy, i * tpr + t, off, n, pack8(o), lane);
     }
   }
 }
@@ -486,7 +535,7 @@ __device__ __forceinline__ float warp_sums(const float (&a)[R], const float (&b)
 // its dx, so the loop works on two turns: it sums the rows of turn k + 1 while it writes dx of turn
 // k, and meets once a turn.  CARRY: rows stay in registers in between; otherwise they are read
 // from their slots again.
-template <int CH, int R, int S, bool CARRY, bool VEC, typename P>
+template <int CH, int R, int S, bool CARRY, int A, typename P>
 __global__ void __launch_bounds__(512)
     tg_layernorm_backward_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                  const uint16_t* __restrict__ x, int64_t ldx,
@@ -494,7 +543,8 @@ __global__ void __launch_bounds__(512)
                                  const float* __restrict__ rstd, uint16_t* __restrict__ dx,
                                  int64_t lddx, float* __restrict__ part, int64_t np, int rows,
                                  int n, unsigned* err, int tpr, int slot_bytes) {
-  static_assert(R == 1 || R == 2, "one row or two");
+  static_assert(R == 1 || (R == 2 && A == kRowsWhole), "one row, or two whole ones");
+  constexpr bool VEC = A == kRowsWhole;
   constexpr int V = 2 * R;             // sums of a turn
   constexpr int kLanes = 32 / V;       // lanes that read one of them back
   extern __shared__ __align__(16) uint8_t smem[];
@@ -508,7 +558,7 @@ __global__ void __launch_bounds__(512)
   uint8_t* ring = reinterpret_cast<uint8_t*>(sg + chunks * 8) + group * S * stage_bytes;
   const Span sx = span_of(x, ldx, rows, n), sd = span_of(dy, lddy, rows, n);
   const int turns = (rows - 1) / R + 1;
-  const int step = gridDim.x * per_block, first = blockIdx.x * per_block + group;
+  const int step = gridDim.x * per_block, first = first_row<A>(per_block, group);
   const int count = first < turns ? (turns - 1 - first) / step + 1 : 0;  // turns of this group
   auto row_of = [&](int k) { return (first + int64_t(k) * step) * R; };
   auto fetch = [&](int k, int s) {
@@ -541,7 +591,9 @@ __global__ void __launch_bounds__(512)
     tg::fence_mbar_init();
     for (int s = 0; s < S && s < count; ++s) fetch(s, s);
   }
-  stage_param<VEC>(sg, gamma, n, chunks, 1.0f);
+  const uint32_t shift = A == kRowsAlike ? row_shift(x, ldx, first) : 0u;  // of all the group's rows
+  const int off = static_cast<int>(shift >> 1);
+  stage_param<VEC>(sg, gamma, n, chunks, 1.0f, off);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
   f32x2 dg[CH][4], db[CH][4];
@@ -567,8 +619,8 @@ __global__ void __launch_bounds__(512)
   auto read = [&](int s, int64_t row, int j, int i, uint4& xv, uint4& dv) {
     const uint8_t* slot = ring + s * stage_bytes + 2 * j * slot_bytes;
     const int c = i * tpr + t, width = R == 1 || row < rows ? n : 0;
-    xv = slot_chunk<VEC>(slot, VEC ? 0u : row_shift(x, ldx, row), c, width);
-    dv = slot_chunk<VEC>(slot + slot_bytes, VEC ? 0u : row_shift(dy, lddy, row), c, width);
+    xv = slot_chunk<A>(slot, A == kRowsAny ? row_shift(x, ldx, row) : shift, c, width);
+    dv = slot_chunk<A>(slot + slot_bytes, A == kRowsAny ? row_shift(dy, lddy, row) : shift, c, width);
   };
   constexpr int kHold = CARRY ? CH : 1;
   uint4 cx[R][kHold], cd[R][kHold];  // of turn k
@@ -675,7 +727,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             o[e] = fma2(d[e], mul2(g[e], times[j]), fma2(w[e], of_x[j], plus[j]));
-          store_chunk<VEC>(dx + row * lddx, i * tpr + t, n, pack8(o), lane);
+          store_row_chunk<A>(dx + row * lddx, i * tpr + t, off, n, pack8(o), lane);
         }
       }
     }
@@ -691,6 +743,7 @@ __global__ void __launch_bounds__(512)
     }
   }
   if (part == nullptr) return;
+  tg::chain_release();
   // the block's groups are added in their order; the ring is empty by now
   __syncthreads();
   float* groups = sg + chunks * 8;  // [groups][2][np], over the ring
@@ -699,7 +752,8 @@ __global__ void __launch_bounds__(512)
   float* to_g = per_block == 1 ? out_g : groups + int64_t(group) * 2 * np;
   float* to_b = per_block == 1 ? out_b : to_g + np;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) put_part(to_g, to_b, (i * tpr + t) << 3, n, dg[i], db[i]);
+  for (int i = 0; i < CH; ++i) 
+    put_part<A != kRowsAlike>(to_g, to_b, ((i * tpr + t) << 3) - off, n, dg[i], db[i]);
   if (per_block == 1) return;
   __syncthreads();
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
@@ -893,12 +947,14 @@ __global__ void __launch_bounds__(THREADS)
     }
   }
   if (part == nullptr) return;
+  tg::chain_release();
   float* out_g = part + int64_t(blockIdx.x) * np;
   float* out_b = part + (int64_t(gridDim.x) + blockIdx.x) * np;
   float* to_g = BLOCK ? out_g : groups + int64_t(threadIdx.x >> 5) * 2 * np;
   float* to_b = BLOCK ? out_b : to_g + np;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) put_part(to_g, to_b, (i * tpr + t) << 3, n, dg[i], db[i]);
+  for (int i = 0; i < CH; ++i) 
+    put_part<true>(to_g, to_b, (i * tpr + t) << 3, n, dg[i], db[i]);
   if constexpr (!BLOCK) {  // the block's warps are added in their order
     __syncthreads();
     for (int e = threadIdx.x; e < n; e += THREADS) {
@@ -925,12 +981,14 @@ __global__ void __launch_bounds__(8 * kPartRows)
   __shared__ float4 sum[kPartRows][8];
   P* out = blockIdx.y == 0 ? dgamma : dbeta;
   if (out == nullptr) return;
-  const int j = blockIdx.x * 32 + threadIdx.x * 4;  // np is a multiple of 4
+  tg::chain_wait();
+  const int row = threadIdx.x >> 3, quad = threadIdx.x & 7;
+  const int j = blockIdx.x * 32 + quad * 4;  // np is a multiple of 4
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (j < n) {
     const float* src = part + int64_t(blockIdx.y) * parts * np + j;
 #pragma unroll 8
-    for (int p = threadIdx.y; p < parts; p += kPartRows) {
+    for (int p = row; p < parts; p += kPartRows) {
       const float4 v = __ldg(reinterpret_cast<const float4*>(src + p * np));
       acc.x += v.x;
       acc.y += v.y;
@@ -938,9 +996,9 @@ __global__ void __launch_bounds__(8 * kPartRows)
       acc.w += v.w;
     }
   }
-  sum[threadIdx.y][threadIdx.x] = acc;
+  sum[row][quad] = acc;
   __syncthreads();
-  const int e = threadIdx.y * 8 + threadIdx.x;
+  const int e = threadIdx.x;
   if (e >= 32 || blockIdx.x * 32 + e >= n) return;
   float s = 0.0f;
 #pragma unroll
@@ -955,37 +1013,58 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 constexpr int64_t kNarrowWidth = 512, kRingWidth = 16384;  // the ring's rows lie between
 
+// Columns that a group's threads have to have.
+int64_t room(int64_t n, int align) { return align == kRowsAlike ? n + 7 : n; }
+
+// `same`: the same pitch and the same base address but for multiples of 16 bytes.  For the ring, and
+// unless a power of two lies between the row and its seven more columns: there the warp more that
+// they take costs resident warps or does not fit (8192 x 4095 backward 102 against 87 us).
+int rows_lie(bool whole, bool same, int64_t n) {
+  if (whole) return kRowsWhole;
+  const bool fits = n > kNarrowWidth && n <= kRingWidth && ((n - 1) ^ (n + 6)) < n - 1;
+  return same && fits ? kRowsAlike : kRowsAny;
+}
+bool same_pitch(const void* p, int64_t ldp, const void* q, int64_t ldq) {
+  return ((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) & 15u) == 0 &&
+         (ldp - ldq) % 8 == 0;
+}
+
 // Threads of a group, groups of a block, shared memory and blocks for n columns: ch chunks a
-// thread, `slots` slots of `arrays` rows a group, `params` parameters staged.
+// thread, `slots` slots of `arrays` rows a group, `params` parameters staged.  An alike row may take
+// seven columns more, and its grid is a multiple of 8.
 struct Shape {
   int tpr, threads, slot_bytes, blocks;
   size_t smem;
 };
 Shape ring_shape(int64_t rows, int64_t n, int ch, int slots, int arrays, int params, int regs,
-                 bool vec, int sms) {
+                 int align, int sms) {
   Shape s;
-  const int64_t chunks = cdiv(n, 8);
+  const int64_t chunks = cdiv(room(n, align), 8);
   s.tpr = static_cast<int>(cdiv(chunks, 32 * ch) * 32);
   const int groups = std::max(1, 256 / s.tpr);  // at most 8
   s.threads = groups * s.tpr;
-  s.slot_bytes = static_cast<int>((chunks + (vec ? 0 : 1)) * 16);
+  s.slot_bytes = static_cast<int>((chunks + (align == kRowsAny ? 1 : 0)) * 16);
   s.smem = size_t(params) * ch * s.tpr * 8 * 4 + size_t(groups) * slots * arrays * s.slot_bytes;
   const int by_smem = static_cast<int>(size_t(tg::kSmemLimit) / (s.smem + 2048));
   const int per_sm = std::max(1, std::min(by_smem, 65536 / (regs * s.threads)));
   s.blocks = static_cast<int>(std::min<int64_t>(cdiv(rows, groups), int64_t(sms) * per_sm));
+  if (align == kRowsAlike)
+    s.blocks = static_cast<int>(std::min<int64_t>(cdiv(s.blocks, 8), std::max(1, sms * per_sm / 8)) * 8);
   return s;
 }
 
-Shape forward_shape(int64_t rows, int64_t n, bool vec, int sms) {
-  return ring_shape(rows, n, kFwdChunks, kFwdSlots, 1, 2, vec && n <= 8192 ? 80 : 128, vec, sms);
+Shape forward_shape(int64_t rows, int64_t n, int align, int sms) {
+  return ring_shape(rows, n, kFwdChunks, kFwdSlots, 1, 2,
+                    align != kRowsAny && n <= 8192 ? 80 : 128, align, sms);
 }
 // Which backward kernel.  Up to 8192 columns two chunks a thread and three stages; beyond, a block
 // has threads for four chunks and shared memory for two stages.  Two rows a turn halve the meetings
 // and the reductions' latency where one block fills an SM (8192 x 8192 82 us, one row a turn 90); with
 // blocks to spare (16384 x 4096 97 against 86 us), or rows to shift (4095 x 3073 62 against 49), one
 // row that stays in registers is better.
-bool two_rows(int64_t n, bool vec) { return vec && n > 4096 && n <= 8192; }
-Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
+int backward_chunks(int64_t n) { return n <= 8192 ? 2 : 4; }
+bool two_rows(int64_t n, int align) { return align == kRowsWhole && n > 4096 && n <= 8192; }
+Shape backward_shape(int64_t rows, int64_t n, int align, int sms) {
   Shape s = {};
   if (n <= kNarrowWidth) {
     s.blocks = static_cast<int>(std::min<int64_t>(cdiv(rows, kNarrowThreads / 32), 2 * sms));
@@ -995,9 +1074,10 @@ Shape backward_shape(int64_t rows, int64_t n, bool vec, int sms) {
     s.blocks = static_cast<int>(std::min<int64_t>(rows, sms));
     return s;
   }
-  if (two_rows(n, vec)) return ring_shape((rows - 1) / 2 + 1, n, 2, 3, 4, 1, 128, vec, sms);
-  return n <= 8192 ? ring_shape(rows, n, 2, 3, 2, 1, 120, vec, sms)
-                   : ring_shape(rows, n, 4, 2, 2, 1, 128, vec, sms);
+  if (two_rows(n, align)) return ring_shape((rows - 1) / 2 + 1, n, 2, 3, 4, 1, 128, align, sms);
+  const int ch = backward_chunks(n);
+  return ch == 2 ? ring_shape(rows, n, ch, 3, 2, 1, 120, align, sms)
+                 : ring_shape(rows, n, ch, 2, 2, 1, 128, align, sms);
 }
 
 template <auto KERNEL>
@@ -1024,10 +1104,11 @@ cudaError_t launch_ring(const Shape& s, cudaStream_t st, Args... args) {
   return cudaGetLastError();
 }
 
-template <bool VEC, typename P>
+template <int A, typename P>
 cudaError_t forward(const void* x, const void* gamma, const void* beta, void* y, float* mean,
                     float* rstd, int64_t rows, int64_t n, int64_t ldx, int64_t ldy, float eps,
                     int sms, unsigned* err, cudaStream_t st) {
+  constexpr bool VEC = A == kRowsWhole;
   const uint16_t* px = static_cast<const uint16_t*>(x);
   const P *g = static_cast<const P*>(gamma), *b = static_cast<const P*>(beta);
   uint16_t* py = static_cast<uint16_t*>(y);
@@ -1036,30 +1117,33 @@ cudaError_t forward(const void* x, const void* gamma, const void* beta, void* y,
                                                             static_cast<int>(n), eps);
     return cudaGetLastError();
   };
-  if (n <= kNarrowWidth) {
-    constexpr int kT = kNarrowThreads;
-    const int64_t blocks = std::min<int64_t>(cdiv(rows, kT / 32), int64_t(sms) * 4);
-    return n <= 256 ? direct(tg_layernorm_direct_kernel<1, false, VEC, kT, P>, kT, blocks)
-                    : direct(tg_layernorm_direct_kernel<2, false, VEC, kT, P>, kT, blocks);
+  if constexpr (A != kRowsAlike) {
+    if (n <= kNarrowWidth) {
+      constexpr int kT = kNarrowThreads;
+      const int64_t blocks = std::min<int64_t>(cdiv(rows, kT / 32), int64_t(sms) * 4);
+      return n <= 256 ? direct(tg_layernorm_direct_kernel<1, false, VEC, kT, P>, kT, blocks)
+                      : direct(tg_layernorm_direct_kernel<2, false, VEC, kT, P>, kT, blocks);
+    }
+    if (n > kRingWidth)
+      return direct(tg_layernorm_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>, kLongThreads,
+                    std::min<int64_t>(rows, sms));
   }
-  if (n > kRingWidth)
-    return direct(tg_layernorm_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>, kLongThreads,
-                  std::min<int64_t>(rows, sms));
-  const Shape s = forward_shape(rows, n, VEC, sms);
+  const Shape s = forward_shape(rows, n, A, sms);
   const int width = static_cast<int>(n), count = static_cast<int>(rows);
   // up to 8192 columns a block has 256 threads at most: three of them an SM where registers allow
   if (n <= 8192)
-    return launch_ring<tg_layernorm_kernel<256, VEC ? 3 : 2, VEC, P>>(
+    return launch_ring<tg_layernorm_kernel<256, A == kRowsAny ? 2 : 3, A, P>>(
         s, st, px, ldx, g, b, py, ldy, mean, rstd, count, width, eps, err);
-  return launch_ring<tg_layernorm_kernel<512, 1, VEC, P>>(s, st, px, ldx, g, b, py, ldy, mean, rstd,
+  return launch_ring<tg_layernorm_kernel<512, 1, A, P>>(s, st, px, ldx, g, b, py, ldy, mean, rstd,
                                                           count, width, eps, err);
 }
 
-template <bool VEC, typename P>
+template <int A, typename P>
 cudaError_t backward(const void* dy, const void* x, const void* gamma, const float* mean,
                      const float* rstd, void* dx, void* dgamma, void* dbeta, float* part,
                      int64_t rows, int64_t n, int64_t lddy, int64_t ldx, int64_t lddx,
                      const Shape& s, unsigned* err, cudaStream_t st) {
+  constexpr bool VEC = A == kRowsWhole;
   const uint16_t *pd = static_cast<const uint16_t*>(dy), *px = static_cast<const uint16_t*>(x);
   const P* g = static_cast<const P*>(gamma);
   uint16_t* out = static_cast<uint16_t*>(dx);
@@ -1071,7 +1155,18 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
                                           width);
     return cudaGetLastError();
   };
-  if (n <= kNarrowWidth) {
+  auto ring = [&]() {
+    auto go = [&](auto which) {
+      return launch_ring<which.value>(s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np,
+                                      static_cast<int>(rows), width, err);
+    };
+    if (n > 8192) return go(Kernel<tg_layernorm_backward_kernel<4, 1, 2, false, A, P>>{});
+    if (!two_rows(n, A)) return go(Kernel<tg_layernorm_backward_kernel<2, 1, 3, true, A, P>>{});
+    return go(Kernel<tg_layernorm_backward_kernel<2, 2, 3, false, kRowsWhole, P>>{});
+  };
+  if constexpr (A == kRowsAlike) {
+    e = ring();
+  } else if (n <= kNarrowWidth) {
     constexpr int kT = kNarrowThreads;
     const size_t smem = part ? size_t(kT / 32) * 2 * np * 4 : 0;  // at most 32 KB
     e = n <= 256 ? direct(tg_layernorm_backward_direct_kernel<1, false, VEC, kT, P>, kT, smem)
@@ -1080,22 +1175,12 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
     e = direct(tg_layernorm_backward_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>,
                kLongThreads, 0);
   } else {
-    const int count = static_cast<int>(rows);
-    auto go = [&](auto which) {
-      return launch_ring<which.value>(s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np,
-                                      count, width, err);
-    };
-    if (n > 8192)
-      e = go(Kernel<tg_layernorm_backward_kernel<4, 1, 2, false, VEC, P>>{});
-    else if (!two_rows(n, VEC))
-      e = go(Kernel<tg_layernorm_backward_kernel<2, 1, 3, true, VEC, P>>{});
-    else
-      e = go(Kernel<tg_layernorm_backward_kernel<2, 2, 3, false, true, P>>{});
+    e = ring();
   }
   if (e != cudaSuccess || part == nullptr) return e;
-  tg_layernorm_params_kernel<P><<<dim3(static_cast<unsigned>(cdiv(n, 32)), 2), dim3(8, kPartRows), 0,
-                                  st>>>(part, s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
-  return cudaGetLastError();
+  return tg::launch_chained(tg_layernorm_params_kernel<P>, true,
+                            dim3(static_cast<unsigned>(cdiv(n, 32)), 2), 8 * kPartRows, 0, st, part,
+                            s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
 }
 
 bool misaligned(const void* p, unsigned bytes) {
@@ -1127,12 +1212,17 @@ tg_status tg_layernorm_f16(const void* X, const void* gamma, const void* beta, v
   const tg_status st = tg::device_info(&sms, &err);
   if (st != TG_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool vec = aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
-                   ldx % 8 == 0 && ldy % 8 == 0 && N % 8 == 0;
+  const bool whole = aligned16(X) && aligned16(Y) && aligned16(gamma) && aligned16(beta) &&
+                     ldx % 8 == 0 && ldy % 8 == 0 && N % 8 == 0;
+  const int align = rows_lie(whole, same_pitch(X, ldx, Y, ldy), N);
   auto run = [&](auto f) { return f(X, gamma, beta, Y, mean, rstd, M, N, ldx, ldy, eps, sms, err, s); };
-  const cudaError_t e = param_type == TG_TYPE_F16
-                            ? (vec ? run(forward<true, __half>) : run(forward<false, __half>))
-                            : (vec ? run(forward<true, float>) : run(forward<false, float>));
+  auto with = [&](auto type) {
+    using P = decltype(type);
+    return align == kRowsWhole   ? run(forward<kRowsWhole, P>)
+           : align == kRowsAlike ? run(forward<kRowsAlike, P>)
+                                 : run(forward<kRowsAny, P>);
+  };
+  const cudaError_t e = param_type == TG_TYPE_F16 ? with(__half()) : with(0.0f);
   return e == cudaSuccess ? TG_OK : tg::record_cuda_error(e);
 }
 
@@ -1162,9 +1252,11 @@ tg_status tg_layernorm_backward_f16(const void* dY, const void* X, const void* g
         return tg::record_cuda_error(e);
     return TG_OK;
   }
-  const bool vec = aligned16(dY) && aligned16(X) && aligned16(dX) && aligned16(gamma) &&
-                   lddy % 8 == 0 && ldx % 8 == 0 && (!dX || lddx % 8 == 0) && N % 8 == 0;
-  const Shape shape = backward_shape(M, N, vec, sms);
+  const bool whole = aligned16(dY) && aligned16(X) && aligned16(dX) && aligned16(gamma) &&
+                     lddy % 8 == 0 && ldx % 8 == 0 && (!dX || lddx % 8 == 0) && N % 8 == 0;
+  const bool same = same_pitch(X, ldx, dY, lddy) && (!dX || same_pitch(X, ldx, dX, lddx));
+  const int align = rows_lie(whole, same, N);
+  const Shape shape = backward_shape(M, N, align, sms);
   float* part = nullptr;
   if (dgamma || dbeta) {
     st = tg::scratch_alloc(size_t(2) * shape.blocks * round_up4(N) * 4, s, reinterpret_cast<void**>(&part));
@@ -1173,8 +1265,13 @@ tg_status tg_layernorm_backward_f16(const void* dY, const void* X, const void* g
   auto run = [&](auto f) {
     return f(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, part, M, N, lddy, ldx, lddx, shape, err, s);
   };
-  e = param_type == TG_TYPE_F16 ? (vec ? run(backward<true, __half>) : run(backward<false, __half>))
-                                : (vec ? run(backward<true, float>) : run(backward<false, float>));
+  auto with = [&](auto type) {
+    using P = decltype(type);
+    return align == kRowsWhole   ? run(backward<kRowsWhole, P>)
+           : align == kRowsAlike ? run(backward<kRowsAlike, P>)
+                                 : run(backward<kRowsAny, P>);
+  };
+  e = param_type == TG_TYPE_F16 ? with(__half()) : with(0.0f);
   if (part) {
     const cudaError_t fe = cudaFreeAsync(part, s);
     if (e == cudaSuccess) e = fe;

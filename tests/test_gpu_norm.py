@@ -216,6 +216,36 @@ def test_backward_in_place(M, N, pad, offset, over):
     assert ((alone.double() - dbr).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("M,N", [(1, 600), (7, 513), (61, 1017), (61, 1018), (30, 2041), (30, 2042),
+                                 (700, 1537), (1300, 3073), (40, 4090), (17, 8185), (17, 8186),
+                                 (9, 12001), (9, 16377), (9, 16378), (11, 5000)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (1, 3), (5, 6), (8, 7), (3, 0)])
+def test_matrices_that_lie_alike(M, N, pad, offset):
+    """Rows that miss a 16-byte boundary, all matrices by the same bytes: NaN around x and dy must
+    not enter, and what is around y and dx must stay."""
+    def room():
+        buf = torch.full((offset + M * (N + pad) + 8,), 7.0, dtype=torch.float16, device="cuda")
+        return buf, buf[offset:offset + M * (N + pad)].view(M, N + pad)
+
+    x, dy = make(M, N, pad, offset, 40, 1.5, 0.3), make(M, N, pad, offset, 41)
+    gamma, beta = make(1, N, seed=42)[0].contiguous(), make(1, N, seed=43)[0].contiguous()
+    buf, y = room()
+    _, mean, rstd = tg.layer_norm(x, gamma, beta, eps=EPS, stats=True, out=y[:, :N])
+    check_forward(x, gamma, beta, y[:, :N], mean, rstd)
+    y[:, :N] = 7.0
+    assert (buf == 7).all()
+    buf, dx = room()
+    dgamma, dbeta = torch.empty(2, N, dtype=torch.float16, device="cuda")
+    st = binding.tg_layernorm_backward_f16(
+        dy.data_ptr(), x.data_ptr(), gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), M, N, N + pad, N + pad, N + pad,
+        binding.TG_TYPE_F16, torch.cuda.current_stream().cuda_stream)
+    assert st == binding.TG_OK
+    check_backward(dy, x, gamma, mean, rstd, dx[:, :N], dgamma, dbeta)
+    dx[:, :N] = 7.0
+    assert (buf == 7).all()
+
+
 def test_many_short_rows():
     # more rows than one wave of warps, widths at the edges of the kernels' ranges
     for N in (1, 8, 256, 257, 512, 513):
