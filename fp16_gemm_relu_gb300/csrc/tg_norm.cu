@@ -768,47 +768,39 @@ __global__ void __launch_bounds__(512)
 }
 
 // ---------------------------------------------------------------------------------------
-// Rows straight from global memory, where the ring does not pay or does not fit: up to 512 columns
-// a row a warp (the ring's waits and copies cost more than so short a row: 100000 x 128 forward 63
-// against 20 us, 32768 x 512 backward 36 against 32 us), more than 16384 a row a block of 1024.
-// With CH <= 2 chunks a thread the next row is loaded before the current one is worked on, and the
-// parameters stay in registers; a longer row is read a second time for dx, from L2.
+// Up to 512 columns: a row a warp, straight from global memory (the ring's waits and copies cost more
+// than so short a row: 100000 x 128 forward 63 against 20 us, 32768 x 512 backward 36 against 32).
+// The next row is loaded before the current one is worked on; the parameters stay in registers.
 // ---------------------------------------------------------------------------------------
-constexpr int kNarrowThreads = 256, kLongThreads = 1024, kLongChunks = 4;
+constexpr int kNarrowThreads = 256;
 
-template <int CH, bool BLOCK, bool VEC, int THREADS, typename P>
+template <int CH, bool VEC, int THREADS, typename P>
 __global__ void __launch_bounds__(THREADS)
     tg_layernorm_direct_kernel(const uint16_t* __restrict__ x, int64_t ldx,
                                const P* __restrict__ gamma, const P* __restrict__ beta,
                                uint16_t* __restrict__ y, int64_t ldy, float* __restrict__ mean,
                                float* __restrict__ rstd, int64_t rows, int n, float eps) {
-  __shared__ float slots[2][32];
-  constexpr bool kKeep = CH <= 2;
-  constexpr int tpr = BLOCK ? THREADS : 32;  // threads of a row
-  const int lane = threadIdx.x & 31, t = BLOCK ? threadIdx.x : lane;
-  const int64_t step = BLOCK ? gridDim.x : int64_t(gridDim.x) * (THREADS >> 5);
-  int64_t r = BLOCK ? blockIdx.x : blockIdx.x * int64_t(THREADS >> 5) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t step = int64_t(gridDim.x) * (THREADS >> 5);
+  int64_t r = blockIdx.x * int64_t(THREADS >> 5) + (threadIdx.x >> 5);
   const float inv_n = 1.0f / static_cast<float>(n);
   uint4 next[CH];
   auto load = [&](int64_t row) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) next[i] = load_chunk<VEC>(x + row * ldx, i * tpr + t, n);
+    for (int i = 0; i < CH; ++i) next[i] = load_chunk<VEC>(x + row * ldx, i * 32 + lane, n);
   };
-  if (kKeep && r < rows) load(r);
-  f32x2 g[kKeep ? CH : 1][4], o[kKeep ? CH : 1][4];
-  if constexpr (kKeep) {
+  if (r < rows) load(r);
+  f32x2 g[CH][4], o[CH][4];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      load_param<VEC>(gamma, i * tpr + t, n, 1.0f, g[i]);
-      load_param<VEC>(beta, i * tpr + t, n, 0.0f, o[i]);
-    }
+  for (int i = 0; i < CH; ++i) {
+    load_param<VEC>(gamma, i * 32 + lane, n, 1.0f, g[i]);
+    load_param<VEC>(beta, i * 32 + lane, n, 0.0f, o[i]);
   }
   for (; r < rows; r += step) {
     uint4 now[CH];
-    if constexpr (!kKeep) load(r);
 #pragma unroll
     for (int i = 0; i < CH; ++i) now[i] = next[i];
-    if (kKeep && r + step < rows) load(r + step);
+    if (r + step < rows) load(r + step);
     f32x2 s = pair(0.0f, 0.0f), q = s;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -816,7 +808,7 @@ __global__ void __launch_bounds__(THREADS)
       unpack8(now[i], v);
       s = add2(s, add2(add2(v[0], v[1]), add2(v[2], v[3])));
     }
-    const float mu = group_sum(sum2(s), tpr, 0, slots[0]) * inv_n;
+    const float mu = warp_sum(sum2(s)) * inv_n;
     const f32x2 less = pair(-mu, -mu);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -824,33 +816,29 @@ __global__ void __launch_bounds__(THREADS)
       unpack8(now[i], v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x2 d = mul2(add2(v[j], less), there(((i * tpr + t) << 3) + 2 * j, n));
+        const f32x2 d = mul2(add2(v[j], less), there(((i * 32 + lane) << 3) + 2 * j, n));
         q = fma2(d, d, q);
       }
     }
-    const float rs = rsqrtf(group_sum(sum2(q), tpr, 0, slots[1]) * inv_n + eps);
-    if (t == 0) {
+    const float rs = rsqrtf(warp_sum(sum2(q)) * inv_n + eps);
+    if (lane == 0) {
       if (mean) mean[r] = mu;
       if (rstd) rstd[r] = rs;
     }
     const f32x2 times = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int c = i * tpr + t, k = kKeep ? i : 0;
-      if constexpr (!kKeep) {
-        load_param<VEC>(gamma, c, n, 1.0f, g[0]);
-        load_param<VEC>(beta, c, n, 0.0f, o[0]);
-      }
       f32x2 v[4];
       unpack8(now[i], v);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = fma2(mul2(add2(v[j], less), times), g[k][j], o[k][j]);
-      store_chunk<VEC>(y + r * ldy, c, n, pack8(v), lane);
+      for (int j = 0; j < 4; ++j) v[j] = fma2(mul2(add2(v[j], less), times), g[i][j], o[i][j]);
+      store_chunk<VEC>(y + r * ldy, i * 32 + lane, n, pack8(v), lane);
     }
   }
 }
 
-template <int CH, bool BLOCK, bool VEC, int THREADS, typename P>
+// Backward, up to 512 columns.
+template <int CH, bool VEC, int THREADS, typename P>
 __global__ void __launch_bounds__(THREADS)
     tg_layernorm_backward_direct_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
                                         const uint16_t* __restrict__ x, int64_t ldx,
@@ -859,112 +847,269 @@ __global__ void __launch_bounds__(THREADS)
                                         const float* __restrict__ rstd, uint16_t* __restrict__ dx,
                                         int64_t lddx, float* __restrict__ part, int64_t np,
                                         int64_t rows, int n) {
-  extern __shared__ float groups[];  // a row a warp: [warps][2][np]
-  __shared__ float slots[2][2][32];
-  constexpr bool kKeep = CH <= 2;
-  constexpr int kHold = kKeep ? CH : 1;
-  constexpr int tpr = BLOCK ? THREADS : 32;
-  const int lane = threadIdx.x & 31, t = BLOCK ? threadIdx.x : lane;
-  const int64_t step = BLOCK ? gridDim.x : int64_t(gridDim.x) * (THREADS >> 5);
-  int64_t r = BLOCK ? blockIdx.x : blockIdx.x * int64_t(THREADS >> 5) + (threadIdx.x >> 5);
+  extern __shared__ float groups[];  // [warps][2][np]
+  const int lane = threadIdx.x & 31;
+  const int64_t step = int64_t(gridDim.x) * (THREADS >> 5);
+  int64_t r = blockIdx.x * int64_t(THREADS >> 5) + (threadIdx.x >> 5);
   const float inv_n = 1.0f / static_cast<float>(n);
   f32x2 dg[CH][4], db[CH][4];
 #pragma unroll
   for (int i = 0; i < CH; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = pair(0.0f, 0.0f);
-  uint4 next_x[kHold], next_dy[kHold];
+  uint4 next_x[CH], next_dy[CH];
   float next_mu = 0.0f, next_rs = 0.0f;
   auto load = [&](int64_t row) {
-    if constexpr (kKeep) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        next_x[i] = load_chunk<VEC>(x + row * ldx, i * tpr + t, n);
-        next_dy[i] = load_chunk<VEC>(dy + row * lddy, i * tpr + t, n);
-      }
+    for (int i = 0; i < CH; ++i) {
+      next_x[i] = load_chunk<VEC>(x + row * ldx, i * 32 + lane, n);
+      next_dy[i] = load_chunk<VEC>(dy + row * lddy, i * 32 + lane, n);
     }
     next_mu = __ldg(mean + row);
     next_rs = __ldg(rstd + row);
   };
   if (r < rows) load(r);
-  f32x2 gm[kHold][4];
-  if constexpr (kKeep) {
+  f32x2 gm[CH][4];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) load_param<VEC>(gamma, i * tpr + t, n, 1.0f, gm[i]);
-  }
-  // h, d = dy and g = d gamma of chunk i of a row; past the row's end d, and with it g, is 0
-  auto terms = [&](int64_t row, int i, f32x2 less, f32x2 times, f32x2(&h)[4], f32x2(&d)[4],
-                   f32x2(&g)[4]) {
-    const int c = i * tpr + t, k = kKeep ? i : 0;
-    if constexpr (!kKeep) {
-      next_x[0] = load_chunk<VEC>(x + row * ldx, c, n);
-      next_dy[0] = load_chunk<VEC>(dy + row * lddy, c, n);
-      load_param<VEC>(gamma, c, n, 1.0f, gm[0]);
-    }
-    unpack8(next_x[k], h);
-    unpack8(next_dy[k], d);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = mul2(add2(h[j], less), times);
-      g[j] = mul2(d[j], gm[k][j]);
-    }
-  };
-  for (int turn = 0; r < rows; r += step, turn ^= 1) {
+  for (int i = 0; i < CH; ++i) load_param<VEC>(gamma, i * 32 + lane, n, 1.0f, gm[i]);
+  for (; r < rows; r += step) {
     const float rs = next_rs;
     const f32x2 less = pair(-next_mu, -next_mu), times = pair(rs, rs);
-    f32x2 h[kHold][4], g[kHold][4], a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
+    f32x2 h[CH][4], g[CH][4], a2 = pair(0.0f, 0.0f), b2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int k = kKeep ? i : 0;
-      f32x2 d[4];
-      terms(r, i, less, times, h[k], d, g[k]);
+      f32x2 d[4];  // past the row's end d, and with it g, is 0
+      unpack8(next_x[i], h[i]);
+      unpack8(next_dy[i], d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        a2 = add2(a2, g[k][j]);
-        b2 = fma2(g[k][j], h[k][j], b2);
-        dg[i][j] = fma2(d[j], h[k][j], dg[i][j]);
+        h[i][j] = mul2(add2(h[i][j], less), times);
+        g[i][j] = mul2(d[j], gm[i][j]);
+        a2 = add2(a2, g[i][j]);
+        b2 = fma2(g[i][j], h[i][j], b2);
+        dg[i][j] = fma2(d[j], h[i][j], dg[i][j]);
         db[i][j] = add2(db[i][j], d[j]);
       }
     }
     if (r + step < rows) load(r + step);
     if (dx != nullptr) {
-      const float a = group_sum(sum2(a2), tpr, 0, slots[turn][0]) * inv_n;
-      const float b = group_sum(sum2(b2), tpr, 0, slots[turn][1]) * inv_n;
+      const float a = warp_sum(sum2(a2)) * inv_n, b = warp_sum(sum2(b2)) * inv_n;
       const f32x2 less_a = pair(-a, -a), less_b = pair(-b, -b);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int k = kKeep ? i : 0;
-        if constexpr (!kKeep) {
-          f32x2 d[4];
-          terms(r, i, less, times, h[0], d, g[0]);
-        }
         f32x2 out[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          out[j] = mul2(times, fma2(h[k][j], less_b, add2(g[k][j], less_a)));
-        store_chunk<VEC>(dx + r * lddx, i * tpr + t, n, pack8(out), lane);
+          out[j] = mul2(times, fma2(h[i][j], less_b, add2(g[i][j], less_a)));
+        store_chunk<VEC>(dx + r * lddx, i * 32 + lane, n, pack8(out), lane);
       }
     }
   }
   if (part == nullptr) return;
   tg::chain_release();
-  float* out_g = part + int64_t(blockIdx.x) * np;
-  float* out_b = part + (int64_t(gridDim.x) + blockIdx.x) * np;
-  float* to_g = BLOCK ? out_g : groups + int64_t(threadIdx.x >> 5) * 2 * np;
-  float* to_b = BLOCK ? out_b : to_g + np;
+  float* mine = groups + int64_t(threadIdx.x >> 5) * 2 * np;
 #pragma unroll
-  for (int i = 0; i < CH; ++i) 
-    put_part<true>(to_g, to_b, (i * tpr + t) << 3, n, dg[i], db[i]);
-  if constexpr (!BLOCK) {  // the block's warps are added in their order
-    __syncthreads();
-    for (int e = threadIdx.x; e < n; e += THREADS) {
-      float sg = 0.0f, sb = 0.0f;
-      for (int k = 0; k < (THREADS >> 5); ++k) {
-        sg += groups[int64_t(k) * 2 * np + e];
-        sb += groups[(int64_t(k) * 2 + 1) * np + e];
+  for (int i = 0; i < CH; ++i) put_part<true>(mine, mine + np, (i * 32 + lane) << 3, n, dg[i], db[i]);
+  __syncthreads();  // the block's warps are added in their order
+  for (int e = threadIdx.x; e < n; e += THREADS) {
+    float sg = 0.0f, sb = 0.0f;
+    for (int k = 0; k < (THREADS >> 5); ++k) {
+      sg += groups[int64_t(k) * 2 * np + e];
+      sb += groups[(int64_t(k) * 2 + 1) * np + e];
+    }
+    part[int64_t(blockIdx.x) * np + e] = sg;
+    part[(int64_t(gridDim.x) + blockIdx.x) * np + e] = sb;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// More than 16384 columns: a row a block of T threads, as fp16 in registers between the passes over
+// it.  A thread's i-th eight elements: whole rows, chunk i T + t.  Others, the columns 8 i T + t,
+// T further and so on, each read and written alone: a warp's accesses are contiguous at any alignment,
+// and nothing is shifted (4096 x 20001 forward 221 against 247 us with shifted chunks; 4096 x 20000 128).
+// ---------------------------------------------------------------------------------------
+template <bool VEC, int T>
+__device__ __forceinline__ int long_column(int i, int e) {
+  return VEC ? ((i * T + static_cast<int>(threadIdx.x)) << 3) + e
+             : (8 * i + e) * T + static_cast<int>(threadIdx.x);
+}
+template <bool VEC, int T>
+__device__ __forceinline__ uint4 long_load(const uint16_t* row, int i, int n) {
+  if constexpr (VEC) return load_chunk<true>(row, i * T + threadIdx.x, n);
+  uint32_t o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int col = long_column<VEC, T>(i, e);
+    o[e] = col < n ? __ldg(row + col) : 0u;
+  }
+  return make_uint4(o[0] | (o[1] << 16), o[2] | (o[3] << 16), o[4] | (o[5] << 16), o[6] | (o[7] << 16));
+}
+template <bool VEC, int T>
+__device__ __forceinline__ void long_store(uint16_t* row, int i, int n, uint4 v) {
+  if constexpr (VEC) {
+    store_chunk<true>(row, i * T + threadIdx.x, n, v, 0);
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int col = long_column<VEC, T>(i, e);
+    if (col < n) row[col] = static_cast<uint16_t>(w[e >> 1] >> ((e & 1) << 4));
+  }
+}
+template <bool VEC, int T, typename P>
+__device__ __forceinline__ void long_param(const P* p, int i, int n, float none, f32x2 (&f)[4]) {
+  if constexpr (VEC) {
+    load_param<true>(p, i * T + threadIdx.x, n, none, f);
+    return;
+  }
+  float g[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int col = long_column<VEC, T>(i, e);
+    g[e] = p != nullptr && col < n ? as_float(p + col) : none;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = pair(g[2 * j], g[2 * j + 1]);
+}
+
+constexpr int kLongThreads = 1024, kLongChunks = 4;
+template <bool VEC, typename P>
+__global__ void __launch_bounds__(kLongThreads)
+    tg_layernorm_long_kernel(const uint16_t* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
+                             const P* __restrict__ beta, uint16_t* __restrict__ y, int64_t ldy,
+                             float* __restrict__ mean, float* __restrict__ rstd, int64_t rows, int n,
+                             float eps) {
+  constexpr int CH = kLongChunks, T = kLongThreads;
+  __shared__ float slots[2][32];
+  const float inv_n = 1.0f / static_cast<float>(n);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    uint4 now[CH];
+    f32x2 s = pair(0.0f, 0.0f), q = s;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) now[i] = long_load<VEC, T>(x + r * ldx, i, n);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 v[4];
+      unpack8(now[i], v);
+      s = add2(s, add2(add2(v[0], v[1]), add2(v[2], v[3])));
+    }
+    const float mu = group_sum(sum2(s), T, 0, slots[0]) * inv_n;
+    const f32x2 less = pair(-mu, -mu);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 v[4];
+      unpack8(now[i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x2 in = pair(long_column<VEC, T>(i, 2 * j) < n ? 1.0f : 0.0f,
+                              long_column<VEC, T>(i, 2 * j + 1) < n ? 1.0f : 0.0f);
+        const f32x2 d = mul2(add2(v[j], less), in);
+        q = fma2(d, d, q);
       }
-      out_g[e] = sg;
-      out_b[e] = sb;
+    }
+    const float rs = rsqrtf(group_sum(sum2(q), T, 0, slots[1]) * inv_n + eps);
+    if (threadIdx.x == 0) {
+      if (mean) mean[r] = mu;
+      if (rstd) rstd[r] = rs;
+    }
+    const f32x2 times = pair(rs, rs);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 v[4], g[4], o[4];
+      long_param<VEC, T>(gamma, i, n, 1.0f, g);
+      long_param<VEC, T>(beta, i, n, 0.0f, o);
+      unpack8(now[i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fma2(mul2(add2(v[j], less), times), g[j], o[j]);
+      long_store<VEC, T>(y + r * ldy, i, n, pack8(v));
+    }
+  }
+}
+
+// Backward: a thread's part of dgamma and dbeta beside its elements does not fit its registers
+// (4096 x 20000 took 630 us so, spilling, against 190), and so these two have a pass of their own.
+// A chunk of eight columns a thread (shifted where rows are not whole: element by element 315 us
+// against 106 for 4096 x 20001), a split of the rows a block; each split writes one partial row of
+// both.  It reads what the pass for dx also reads: 10 bytes an element in all, not 6.
+constexpr int kColumnThreads = 128;
+template <bool VEC>
+__global__ void __launch_bounds__(kColumnThreads)
+    tg_layernorm_columns_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
+                                const uint16_t* __restrict__ x, int64_t ldx,
+                                const float* __restrict__ mean, const float* __restrict__ rstd,
+                                float* __restrict__ part, int64_t np, int64_t rows, int n) {
+  const int c = blockIdx.x * kColumnThreads + threadIdx.x;
+  const int64_t per = (rows + gridDim.y - 1) / gridDim.y;
+  const int64_t from = blockIdx.y * per, to = from + per < rows ? from + per : rows;
+  f32x2 dg[4], db[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dg[j] = db[j] = pair(0.0f, 0.0f);
+#pragma unroll(VEC ? 4 : 2)
+  for (int64_t r = from; r < to; ++r) {
+    const float mu = __ldg(mean + r), rs = __ldg(rstd + r);
+    const f32x2 less = pair(-mu, -mu), times = pair(rs, rs);
+    f32x2 h[4], d[4];
+    unpack8(load_chunk<VEC>(x + r * ldx, c, n), h);
+    unpack8(load_chunk<VEC>(dy + r * lddy, c, n), d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      dg[j] = fma2(d[j], mul2(add2(h[j], less), times), dg[j]);
+      db[j] = add2(db[j], d[j]);
+    }
+  }
+  put_part<true>(part + blockIdx.y * np, part + (int64_t(gridDim.y) + blockIdx.y) * np, c << 3, n, dg,
+                 db);
+}
+
+constexpr int kLongDxThreads = 512, kLongDxChunks = 8;
+template <bool VEC, typename P>
+__global__ void __launch_bounds__(kLongDxThreads)
+    tg_layernorm_long_dx_kernel(const uint16_t* __restrict__ dy, int64_t lddy,
+                                const uint16_t* __restrict__ x, int64_t ldx,
+                                const P* __restrict__ gamma, const float* __restrict__ mean,
+                                const float* __restrict__ rstd, uint16_t* __restrict__ dx,
+                                int64_t lddx, int64_t rows, int n) {
+  constexpr int CH = kLongDxChunks, T = kLongDxThreads;
+  __shared__ float slots[2][2][32];
+  const float inv_n = 1.0f / static_cast<float>(n);
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
+    const float mu = __ldg(mean + r), rs = __ldg(rstd + r);
+    uint4 xv[CH], dv[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      xv[i] = long_load<VEC, T>(x + r * ldx, i, n);
+      dv[i] = long_load<VEC, T>(dy + r * lddy, i, n);
+    }
+    const f32x2 less = pair(-mu, -mu);
+    f32x2 a2 = pair(0.0f, 0.0f), b2 = a2;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 w[4], d[4], g[4];
+      long_param<VEC, T>(gamma, i, n, 1.0f, g);
+      unpack8(xv[i], w);
+      unpack8(dv[i], d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a2 = fma2(d[j], g[j], a2);
+        b2 = fma2(mul2(d[j], add2(w[j], less)), g[j], b2);
+      }
+    }
+    const float a = group_sum(sum2(a2), T, 0, slots[turn][0]);
+    const float b = group_sum(sum2(b2), T, 0, slots[turn][1]);
+    // as in the ring's kernel: dx = d (gamma rstd) + x c1 + c0
+    const float c1 = -rs * rs * rs * (b * inv_n), c0 = fmaf(-mu, c1, -rs * (a * inv_n));
+    const f32x2 of_x = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      f32x2 w[4], d[4], g[4];
+      long_param<VEC, T>(gamma, i, n, 1.0f, g);
+      unpack8(xv[i], w);
+      unpack8(dv[i], d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = fma2(d[j], mul2(g[j], times), fma2(w[j], of_x, plus));
+      long_store<VEC, T>(dx + r * lddx, i, n, pack8(w));
     }
   }
 }
@@ -1070,8 +1215,9 @@ Shape backward_shape(int64_t rows, int64_t n, int align, int sms) {
     s.blocks = static_cast<int>(std::min<int64_t>(cdiv(rows, kNarrowThreads / 32), 2 * sms));
     return s;
   }
-  if (n > kRingWidth) {
-    s.blocks = static_cast<int>(std::min<int64_t>(rows, sms));
+  if (n > kRingWidth) {  // the splits of the columns' pass: eight blocks an SM, eight rows each
+    const int64_t most = 8 * int64_t(sms) / cdiv(n, 8 * kColumnThreads);
+    s.blocks = static_cast<int>(std::max<int64_t>(1, std::min(most, cdiv(rows, 8))));
     return s;
   }
   if (two_rows(n, align)) return ring_shape((rows - 1) / 2 + 1, n, 2, 3, 4, 1, 128, align, sms);
@@ -1121,11 +1267,11 @@ cudaError_t forward(const void* x, const void* gamma, const void* beta, void* y,
     if (n <= kNarrowWidth) {
       constexpr int kT = kNarrowThreads;
       const int64_t blocks = std::min<int64_t>(cdiv(rows, kT / 32), int64_t(sms) * 4);
-      return n <= 256 ? direct(tg_layernorm_direct_kernel<1, false, VEC, kT, P>, kT, blocks)
-                      : direct(tg_layernorm_direct_kernel<2, false, VEC, kT, P>, kT, blocks);
+      return n <= 256 ? direct(tg_layernorm_direct_kernel<1, VEC, kT, P>, kT, blocks)
+                      : direct(tg_layernorm_direct_kernel<2, VEC, kT, P>, kT, blocks);
     }
     if (n > kRingWidth)
-      return direct(tg_layernorm_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>, kLongThreads,
+      return direct(tg_layernorm_long_kernel<VEC, P>, kLongThreads,
                     std::min<int64_t>(rows, sms));
   }
   const Shape s = forward_shape(rows, n, A, sms);
@@ -1142,7 +1288,7 @@ template <int A, typename P>
 cudaError_t backward(const void* dy, const void* x, const void* gamma, const float* mean,
                      const float* rstd, void* dx, void* dgamma, void* dbeta, float* part,
                      int64_t rows, int64_t n, int64_t lddy, int64_t ldx, int64_t lddx,
-                     const Shape& s, unsigned* err, cudaStream_t st) {
+                     const Shape& s, int sms, unsigned* err, cudaStream_t st) {
   constexpr bool VEC = A == kRowsWhole;
   const uint16_t *pd = static_cast<const uint16_t*>(dy), *px = static_cast<const uint16_t*>(x);
   const P* g = static_cast<const P*>(gamma);
@@ -1150,11 +1296,6 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
   const int width = static_cast<int>(n);
   const int64_t np = round_up4(n);
   cudaError_t e;
-  auto direct = [&](auto kern, int threads, size_t smem) {
-    kern<<<s.blocks, threads, smem, st>>>(pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, rows,
-                                          width);
-    return cudaGetLastError();
-  };
   auto ring = [&]() {
     auto go = [&](auto which) {
       return launch_ring<which.value>(s, st, pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np,
@@ -1164,23 +1305,39 @@ cudaError_t backward(const void* dy, const void* x, const void* gamma, const flo
     if (!two_rows(n, A)) return go(Kernel<tg_layernorm_backward_kernel<2, 1, 3, true, A, P>>{});
     return go(Kernel<tg_layernorm_backward_kernel<2, 2, 3, false, kRowsWhole, P>>{});
   };
+  auto params = [&]() {
+    return tg::launch_chained(tg_layernorm_params_kernel<P>, true,
+                              dim3(static_cast<unsigned>(cdiv(n, 32)), 2), 8 * kPartRows, 0, st, part,
+                              s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
+  };
   if constexpr (A == kRowsAlike) {
     e = ring();
   } else if (n <= kNarrowWidth) {
     constexpr int kT = kNarrowThreads;
     const size_t smem = part ? size_t(kT / 32) * 2 * np * 4 : 0;  // at most 32 KB
-    e = n <= 256 ? direct(tg_layernorm_backward_direct_kernel<1, false, VEC, kT, P>, kT, smem)
-                 : direct(tg_layernorm_backward_direct_kernel<2, false, VEC, kT, P>, kT, smem);
+    auto direct = [&](auto kern) {
+      kern<<<s.blocks, kT, smem, st>>>(pd, lddy, px, ldx, g, mean, rstd, out, lddx, part, np, rows, width);
+      return cudaGetLastError();
+    };
+    e = n <= 256 ? direct(tg_layernorm_backward_direct_kernel<1, VEC, kT, P>)
+                 : direct(tg_layernorm_backward_direct_kernel<2, VEC, kT, P>);
   } else if (n > kRingWidth) {
-    e = direct(tg_layernorm_backward_direct_kernel<kLongChunks, true, VEC, kLongThreads, P>,
-               kLongThreads, 0);
+    if (part != nullptr) {  // before dx, which may take dy's or x's place
+      tg_layernorm_columns_kernel<VEC>
+          <<<dim3(static_cast<unsigned>(cdiv(n, 8 * kColumnThreads)), static_cast<unsigned>(s.blocks)),
+             kColumnThreads, 0, st>>>(pd, lddy, px, ldx, mean, rstd, part, np, rows, width);
+      if ((e = cudaGetLastError()) != cudaSuccess || (e = params()) != cudaSuccess) return e;
+    }
+    if (out == nullptr) return cudaSuccess;
+    tg_layernorm_long_dx_kernel<VEC, P>
+        <<<static_cast<unsigned>(std::min<int64_t>(rows, sms)), kLongDxThreads, 0, st>>>(
+            pd, lddy, px, ldx, g, mean, rstd, out, lddx, rows, width);
+    return cudaGetLastError();
   } else {
     e = ring();
   }
   if (e != cudaSuccess || part == nullptr) return e;
-  return tg::launch_chained(tg_layernorm_params_kernel<P>, true,
-                            dim3(static_cast<unsigned>(cdiv(n, 32)), 2), 8 * kPartRows, 0, st, part,
-                            s.blocks, np, width, static_cast<P*>(dgamma), static_cast<P*>(dbeta));
+  return params();
 }
 
 bool misaligned(const void* p, unsigned bytes) {
@@ -1263,7 +1420,7 @@ tg_status tg_layernorm_backward_f16(const void* dY, const void* X, const void* g
     if (st != TG_OK) return st;
   }
   auto run = [&](auto f) {
-    return f(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, part, M, N, lddy, ldx, lddx, shape, err, s);
+    return f(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, part, M, N, lddy, ldx, lddx, shape, sms, err, s);
   };
   auto with = [&](auto type) {
     using P = decltype(type);
