@@ -32,8 +32,8 @@ namespace {
 // Alike rows r and r + 8 start equally far from a boundary (8 rows are a multiple of 16 bytes
 // apart), so a block that takes every eighth row can work on aligned 16-byte blocks, `off` elements to
 // the left of the row's own chunks of eight, and keeps the same columns for all of them: nothing is
-// shifted, and only a row's first and last block need care.  4095 x 3073 forward 20.5 us, shifted 31.8,
-// backward 41 and 47; 4096 x 12287 61 and 100, 143 and 199.
+// shifted, and only a row's first and last block need care.  4095 x 3073 forward 20 us, shifted 32,
+// backward 39 and 47; 4096 x 12287 59 and 100, 134 and 199.
 enum : int { kRowsAny = 0, kRowsAlike = 1, kRowsWhole = 2 };
 
 // 16 bytes of the 32 in (lo, hi), from byte s on (even, below 16).  s is the same for a row's
@@ -327,12 +327,30 @@ __device__ __forceinline__ f32x2 there(int col, int n) {
   return pair(col >= 0 && col < n ? 1.0f : 0.0f, col + 1 >= 0 && col + 1 < n ? 1.0f : 0.0f);
 }
 
+// A row's first and last chunk may have elements that are not the row's: which of the eight are, as
+// bits for them as fp16 and as factors for them as pairs.  In shared memory, the same for all rows of
+// a block (8192 x 5001 backward 98 us; worked out at each read 106).
+struct Edges {
+  uint4 bits[2];
+  f32x2 in[2][4];
+};
+__device__ __forceinline__ void set_edges(Edges* e, int off, int n) {
+  const int i = threadIdx.x;
+  if (i >= 16) return;
+  const int last = ((n + off - 1) & ~7) - off;  // the last chunk's first column
+  const int which = i >> 3, col = (which == 0 ? -off : last) + (i & 7);
+  const bool in = col >= 0 && col < n;
+  reinterpret_cast<uint16_t*>(&e->bits[which])[i & 7] = in ? 0xFFFFu : 0u;
+  reinterpret_cast<float*>(&e->in[which][0])[i & 7] = in ? 1.0f : 0.0f;
+}
+
 // Chunk c of the row in a slot, zeros where the row has no element; b: bytes from the slot's start to
 // the row's.  Whole and alike rows: block c of the slot, of which an alike row may have only a part (b
 // is 2 off then).  Else elements [8c, 8c + 8), shifted together from the two blocks that hold them: with
 // 4-byte reads at the row's own offset, a warp's pairs contiguous, 8192 x 4096 forward took 63 us, not 37.
 template <int A>
-__device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int c, int n) {
+__device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int c, int n,
+                                            const Edges& edges) {
   uint4 v = make_uint4(0, 0, 0, 0);
   const int e0 = (c << 3) - (A == kRowsAlike ? static_cast<int>(b >> 1) : 0);
   if (e0 < n) {
@@ -340,16 +358,8 @@ __device__ __forceinline__ uint4 slot_chunk(const uint8_t* slot, uint32_t b, int
     v = blk[0];
     if constexpr (A == kRowsAny) v = shift16(v, blk[1], b);
     if (A != kRowsWhole && ((A == kRowsAlike && e0 < 0) || e0 + 8 > n)) {
-      uint32_t o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = e0 + 2 * i;
-        if (e >= n) o[i] = 0u;
-        else if (e + 1 >= n) o[i] &= 0xFFFFu;
-        if (A == kRowsAlike && e + 1 < 0) o[i] = 0u;
-        else if (A == kRowsAlike && e < 0) o[i] &= 0xFFFF0000u;
-      }
-      v = make_uint4(o[0], o[1], o[2], o[3]);
+      const uint4 m = edges.bits[A == kRowsAlike && e0 < 0 ? 0 : 1];
+      v = make_uint4(v.x & m.x, v.y & m.y, v.z & m.z, v.w & m.w);
     }
   }
   return v;
@@ -431,6 +441,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
   __shared__ float sums[8][2][16];
+  __shared__ __align__(16) Edges edges;
   __shared__ volatile int late;
   const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, lane = threadIdx.x & 31;
   const int per_block = blockDim.x / tpr, chunks = CH * tpr;
@@ -459,6 +470,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   const int off = static_cast<int>(shift >> 1);
   stage_param<VEC>(sg, gamma, n, chunks, 1.0f, off);
   stage_param<VEC>(so, beta, n, chunks, 0.0f, off);
+  if constexpr (!VEC) set_edges(&edges, off, n);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
   for (int k = 0; k < count; ++k) {
@@ -469,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      unpack8(slot_chunk<A>(ring + s * slot_bytes, b, i * tpr + t, n), v[i]);
+      unpack8(slot_chunk<A>(ring + s * slot_bytes, b, i * tpr + t, n, edges), v[i]);
       acc = add2(acc, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
     }
     const float mu = group_sum(sum2(acc), tpr, group, sums[group][0]) * inv_n;
@@ -487,7 +499,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
       } else if (!VEC && e0 < n) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const f32x2 d = mul2(v[i][j], there(e0 + 2 * j, n));
+          const f32x2 d = mul2(v[i][j], edges.in[A == kRowsAlike && e0 < 0 ? 0 : 1][j]);
           q = fma2(d, d, q);
         }
       }
@@ -549,6 +561,7 @@ __global__ void __launch_bounds__(512)
   constexpr int kLanes = 32 / V;       // lanes that read one of them back
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint64_t bars[8][S];
+  __shared__ __align__(16) Edges edges;
   __shared__ float sums[2][V][16];  // [turn mod 2][(which, row)][warp of the block]
   __shared__ volatile int late;
   const int group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, lane = threadIdx.x & 31;
@@ -594,6 +607,7 @@ __global__ void __launch_bounds__(512)
   const uint32_t shift = A == kRowsAlike ? row_shift(x, ldx, first) : 0u;  // of all the group's rows
   const int off = static_cast<int>(shift >> 1);
   stage_param<VEC>(sg, gamma, n, chunks, 1.0f, off);
+  if constexpr (!VEC) set_edges(&edges, off, n);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
   f32x2 dg[CH][4], db[CH][4];
@@ -619,8 +633,8 @@ __global__ void __launch_bounds__(512)
   auto read = [&](int s, int64_t row, int j, int i, uint4& xv, uint4& dv) {
     const uint8_t* slot = ring + s * stage_bytes + 2 * j * slot_bytes;
     const int c = i * tpr + t, width = R == 1 || row < rows ? n : 0;
-    xv = slot_chunk<A>(slot, A == kRowsAny ? row_shift(x, ldx, row) : shift, c, width);
-    dv = slot_chunk<A>(slot + slot_bytes, A == kRowsAny ? row_shift(dy, lddy, row) : shift, c, width);
+    xv = slot_chunk<A>(slot, A == kRowsAny ? row_shift(x, ldx, row) : shift, c, width, edges);
+    dv = slot_chunk<A>(slot + slot_bytes, A == kRowsAny ? row_shift(dy, lddy, row) : shift, c, width, edges);
   };
   constexpr int kHold = CARRY ? CH : 1;
   uint4 cx[R][kHold], cd[R][kHold];  // of turn k
