@@ -15,6 +15,10 @@
 //  - The running sums take 128 registers a thread, so there are eight epilogue warps, each with 32
 //    rows and half of the tile's columns.  With the whole row segment in registers they take its
 //    maximum and sum of exponentials, and then store it, or only look up the rows' targets.
+//
+// Bound by the tensor cores: 4096 tokens, 65537 classes of 2048 alone 605 us, 1817 TFLOP/s, 0.94 of
+// the rate measured with large bf16 products, 674 with the logits stored; in a long run the power
+// limit lowers the clock (695 us).  One token, 28672 classes of 8192: bound by HBM, 78 us, 6.0 TB/s.
 #pragma once
 
 #include "tg_gemm_kernel.cuh"
