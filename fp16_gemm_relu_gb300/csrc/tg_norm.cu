@@ -1218,9 +1218,9 @@ Shape forward_shape(int64_t rows, int64_t n, int align, int sms) {
 }
 // Which backward kernel.  Up to 8192 columns two chunks a thread and three stages; beyond, a block
 // has threads for four chunks and shared memory for two stages.  Two rows a turn halve the meetings
-// and the reductions' latency where one block fills an SM (8192 x 8192 82 us, one row a turn 90); with
-// blocks to spare (16384 x 4096 97 against 86 us), or rows to shift (4095 x 3073 62 against 49), one
-// row that stays in registers is better.
+// and the reductions' latency where one block fills an SM (8192 x 8192 80 us, one row a turn 90; 8192 x
+// 5000 62 and 74); with blocks to spare (16384 x 4096 97 against 86 us), rows to shift (4095 x 3073 62
+// against 49) or their end chunks (8192 x 5001 102 against 98), one row that stays in registers is better.
 int backward_chunks(int64_t n) { return n <= 8192 ? 2 : 4; }
 bool two_rows(int64_t n, int align) { return align == kRowsWhole && n > 4096 && n <= 8192; }
 Shape backward_shape(int64_t rows, int64_t n, int align, int sms) {

@@ -512,6 +512,36 @@ def test_other_stream_and_threads():
         assert all(torch.equal(a, b) for a, b in zip(g, want))
 
 
+def test_calls_back_to_back():
+    """Calls that share scratch and follow one another without a wait give what they give alone."""
+    calls = []
+    for k, (T, V, D, layout) in enumerate([
+            (1, 5000, 256, tg.TG_HEAD_VOCAB_MAJOR), (130, 3000, 136, tg.TG_HEAD_WIDTH_MAJOR),
+            (600, 2000, 64, tg.TG_HEAD_VOCAB_MAJOR), (16, 40000, 1024, tg.TG_HEAD_VOCAB_MAJOR),
+            (300, 1001, 77, tg.TG_HEAD_VOCAB_MAJOR)]):
+        x, w = operands(T, V, D, layout, 130 + k)
+        target, (index, logits) = targets(T, V, 140 + k), teacher(T, V, 9, 150 + k, torch.float16)
+        dloss = torch.rand(T, generator=gen(160 + k), device="cuda")
+        piece = 256 if T > 256 else 0
+        calls += [lambda x=x, w=w, t=target, n=layout: [tg.linear_cross_entropy(x, w, t, layout=n)],
+                  lambda x=x, w=w, t=target, d=dloss, n=layout, p=piece:
+                      tg.linear_cross_entropy_step(x, w, t, d, layout=n, piece_rows=p),
+                  lambda x=x, w=w, i=index, u=logits, n=layout:
+                      [tg.linear_distillation(x, w, i, u, 2.0, layout=n)],
+                  lambda x=x, w=w, i=index, u=logits, d=dloss, n=layout, p=piece:
+                      tg.linear_distillation_step(x, w, i, u, d, 2.0, layout=n, piece_rows=p)]
+    want = []
+    for c in calls:
+        torch.cuda.synchronize()
+        want.append(c())
+    torch.cuda.synchronize()
+    got = [[c() for c in calls] for _ in range(20)]
+    torch.cuda.synchronize()
+    for run in got:
+        for g, e in zip(run, want):
+            assert all(torch.equal(a, b) for a, b in zip(g, e))
+
+
 def test_graph_capture():
     T, V, D = 130, 2000, 136
     x, w = operands(T, V, D, 0, 118)

@@ -218,7 +218,8 @@ def test_backward_in_place(M, N, pad, offset, over):
 
 @pytest.mark.parametrize("M,N", [(1, 600), (7, 513), (61, 1017), (61, 1018), (30, 2041), (30, 2042),
                                  (700, 1537), (1300, 3073), (40, 4090), (17, 8185), (17, 8186),
-                                 (9, 12001), (9, 16377), (9, 16378), (11, 5000)])
+                                 (9, 12001), (9, 16377), (9, 16378), (11, 5000), (8, 5001),
+                                 (9, 5001), (1201, 5001), (2450, 4097)])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (0, 1), (1, 3), (5, 6), (8, 7), (3, 0)])
 def test_matrices_that_lie_alike(M, N, pad, offset):
     """Rows that miss a 16-byte boundary, all matrices by the same bytes: NaN around x and dy must
@@ -244,6 +245,25 @@ def test_matrices_that_lie_alike(M, N, pad, offset):
     check_backward(dy, x, gamma, mean, rstd, dx[:, :N], dgamma, dbeta)
     dx[:, :N] = 7.0
     assert (buf == 7).all()
+
+
+def test_calls_back_to_back():
+    """Calls that share scratch and follow one another without a wait give what they give alone."""
+    cases = []
+    for k, (M, N, pad) in enumerate([(300, 4096, 0), (5, 700, 3), (1000, 512, 0), (64, 5001, 0),
+                                     (2, 20000, 0), (700, 3073, 0), (1, 8192, 0)]):
+        x, dy = make(M, N, pad, 0, 50 + k), make(M, N, pad, 0, 60 + k)
+        gamma = make(1, N, seed=70 + k)[0].contiguous()
+        _, mean, rstd = tg.layer_norm(x, gamma, eps=EPS, stats=True)
+        torch.cuda.synchronize()
+        want = tg.layer_norm_backward(dy, x, mean, rstd, gamma)
+        torch.cuda.synchronize()
+        cases.append((dy, x, mean, rstd, gamma, want))
+    got = [[tg.layer_norm_backward(*c[:5]) for c in cases] for _ in range(20)]
+    torch.cuda.synchronize()
+    for run in got:
+        for g, c in zip(run, cases):
+            assert all(torch.equal(a, b) for a, b in zip(g, c[5]))
 
 
 def test_many_short_rows():
