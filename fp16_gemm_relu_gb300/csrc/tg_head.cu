@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "tg_gemm_relu.h"
 #include "tg_internal.h"
@@ -368,6 +369,42 @@ constexpr int64_t kLeastRows = 8;
 // Without logits a token's scratch is its statistics: 1 GiB of them.
 constexpr int64_t kPieceStats = int64_t{1} << 27;
 
+// A stream beside the caller's, one a device, and the events that fork to it and join from it; held by
+// one call at a time while that enqueues.
+struct Side {
+  bool ready = false;
+  cudaStream_t stream = nullptr;
+  cudaEvent_t start = nullptr, done = nullptr;
+  std::mutex mu;
+};
+cudaError_t side_stream(Side** out) {
+  static Side sides[64];  // device_info has refused devices past 63
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  Side& s = sides[dev & 63];
+  std::lock_guard<std::mutex> lock(s.mu);
+  if (!s.ready) {
+    if ((e = cudaStreamCreateWithFlags(&s.stream, cudaStreamNonBlocking)) != cudaSuccess ||
+        (e = cudaEventCreateWithFlags(&s.start, cudaEventDisableTiming)) != cudaSuccess ||
+        (e = cudaEventCreateWithFlags(&s.done, cudaEventDisableTiming)) != cudaSuccess)
+      return e;
+    s.ready = true;
+  }
+  *out = &s;
+  return cudaSuccess;
+}
+
+bool capturing(cudaStream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusActive;
+  if (cudaStreamIsCapturing(stream, &status) == cudaSuccess)
+    return status != cudaStreamCaptureStatusNone;
+  cudaGetLastError();  // the legacy stream while another one is captured
+  return true;
+}
+// Elements of W from which dX and dW run side by side.
+constexpr int64_t kSideWork = int64_t{12} << 20;
+
 // One call's arguments beside the sizes; `top` > 0 makes it distillation.
 struct Head {
   const void* X;
@@ -572,33 +609,31 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       chain(tg_head_teacher_grad_kernel, dim3(static_cast<unsigned>(cdiv(n, 4))), 128, index, h.ldt,
             h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
-    if (h.dX) {  // G (n x V) times W (V x D, or stored D x V)
-      std::memset(&ex, 0, sizeof(ex));
-      ex.alpha = alpha;
-      ex.chained = true;
-      ex.a_rows = std::max(n, kLeastRows);
-      // One row of tiles reads W once at the memory's rate, if the splits of V make one wave of
-      // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
-      // products' costs and for 128 tokens 20.4 against 20.7, 131072 x 4096 166 against 203, 28672 x
-      // 8192 for one token 77 against 119; two rows of tiles gain at some widths and lose at others).
-      // Narrow W: narrow tiles.
-      tg_options opt = gemm_opt;
-      const int64_t width = h.D <= 2048 ? 128 : 256;
-      const int64_t splits =
-          std::min({sms / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)});
-      if (n <= 128 && splits > 1) {
-        opt.pair = -1;
-        opt.block_n = static_cast<int>(width);
-        opt.split_k = static_cast<int>(splits);
-      }
-      st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, n, h.D,
-                          h.V, ldg, ldw, h.lddx, ex, &opt, stream);
-      if (st != TG_OK) return done(st);
+    // Few tokens: dX reads W and dW writes as much, each bound by HBM, where writes alone run at 3.9 TB/s
+    // and reads and writes together at up to 6.8.  So the two run side by side, dX on a third of the
+    // SMs (28672 x 4096, 16 tokens: the step 149 us, one after the other 160; dX on 64 SMs 159, on 80
+    // 179), where the work is worth a second stream (32000 x 512 47 against 53 us, 33000 x 256 43.4
+    // against 42.7).  Not into a graph that is being captured: the stream would belong to it until its
+    // end.  (Other shares are other splits of V, so dX may differ from that in its last bit.)
+    const bool both = h.dX && h.dW && n == h.T && n <= 128 && h.V * h.D >= kSideWork &&
+                      !capturing(stream);
+    const int sms_x = both ? sms / 3 : sms;
+    Side* side = nullptr;
+    std::unique_lock<std::mutex> lock;
+    cudaStream_t stream_w = stream;
+    if (both) {
+      if ((e = side_stream(&side)) != cudaSuccess) return done(tg::record_cuda_error(e));
+      lock = std::unique_lock<std::mutex>(side->mu);
+      if ((e = cudaEventRecord(side->start, stream)) != cudaSuccess ||
+          (e = cudaStreamWaitEvent(side->stream, side->start, 0)) != cudaSuccess)
+        return done(tg::record_cuda_error(e));
+      stream_w = side->stream;
     }
+    st = TG_OK;
     if (h.dW) {  // G^T X (V x D), or X^T G (D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
-      ex.chained = true;
+      ex.chained = !both;
       if (sum_w) {  // the first piece writes the sums, the last takes them into its epilogue
         ex.ld32 = ldw32;
         if (t0 + piece < h.T) {
@@ -613,10 +648,43 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       // 512 tokens they are even).
       tg_options opt = gemm_opt;
       if (n <= 256 && !(ex.out32 && ex.add)) opt.pair = -1;
-      st = by_vocab ? tg::gemm_extra(1, 0, g, x, h.dW, h.V, h.D, n, ldg, ldx, h.lddw, ex, &opt, stream)
-                    : tg::gemm_extra(1, 0, x, g, h.dW, h.D, h.V, n, ldx, ldg, h.lddw, ex, &opt, stream);
-      if (st != TG_OK) return done(st);
+      if (both) opt.max_ctas = sms - sms_x;
+      st = by_vocab
+               ? tg::gemm_extra(1, 0, g, x, h.dW, h.V, h.D, n, ldg, ldx, h.lddw, ex, &opt, stream_w)
+               : tg::gemm_extra(1, 0, x, g, h.dW, h.D, h.V, n, ldx, ldg, h.lddw, ex, &opt, stream_w);
     }
+    if (h.dX && st == TG_OK) {  // G (n x V) times W (V x D, or stored D x V)
+      std::memset(&ex, 0, sizeof(ex));
+      ex.alpha = alpha;
+      ex.chained = !both;
+      ex.a_rows = std::max(n, kLeastRows);
+      // One row of tiles reads W once at the memory's rate, if the splits of V make one wave of
+      // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
+      // products' costs and for 128 tokens 20.4 against 20.7, 131072 x 4096 166 against 203, 28672 x
+      // 8192 for one token 77 against 119; two rows of tiles gain at some widths and lose at others).
+      // Narrow W: narrow tiles.
+      tg_options opt = gemm_opt;
+      const int64_t width = h.D <= 2048 ? 128 : 256;
+      const int64_t splits =
+          std::min({sms_x / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)});
+      if (n <= 128 && splits > 1) {
+        opt.pair = -1;
+        opt.block_n = static_cast<int>(width);
+        opt.split_k = static_cast<int>(splits);
+      }
+      if (both) opt.max_ctas = sms_x;
+      st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, n, h.D,
+                          h.V, ldg, ldw, h.lddx, ex, &opt, stream);
+    }
+    if (both) {  // joined on success and on error alike: the scratch is freed on `stream`
+      if ((e = cudaEventRecord(side->done, side->stream)) == cudaSuccess)
+        e = cudaStreamWaitEvent(stream, side->done, 0);
+      if (e != cudaSuccess) {
+        cudaStreamSynchronize(side->stream);
+        if (st == TG_OK) st = tg::record_cuda_error(e);
+      }
+    }
+    if (st != TG_OK) return done(st);
   }
   return done(TG_OK);
 }

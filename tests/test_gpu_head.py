@@ -542,6 +542,48 @@ def test_calls_back_to_back():
             assert all(torch.equal(a, b) for a, b in zip(g, e))
 
 
+def test_few_tokens_over_a_large_head():
+    """Sizes at which dX and dW run side by side: against the definition, alone, from several threads
+    on streams of their own, and captured."""
+    import threading
+
+    T, V, D = 9, 26000, 520
+    layout = tg.TG_HEAD_VOCAB_MAJOR
+    x, w = operands(T, V, D, layout, 170)
+    target = targets(T, V, 171)
+    dloss = torch.rand(T, generator=gen(172), device="cuda") + 0.5
+    want = tg.linear_cross_entropy_step(x, w, target, dloss)
+    q, live = one_hot(target, V)
+    zero = torch.zeros(T, dtype=D64, device="cuda")
+    check(x, w, layout, 1.0, q, live, zero, dloss, want[0], None, *want[1:])
+    for layout2 in (layout, tg.TG_HEAD_WIDTH_MAJOR):
+        w2 = w if layout2 == layout else rows(w.t())
+        got = tg.linear_cross_entropy_step(x, w2, target, dloss, layout=layout2)
+        check(x, w2, layout2, 1.0, q, live, zero, dloss, got[0], None, *got[1:])
+    torch.cuda.synchronize()
+    got = {}
+
+    def work(k):
+        s = torch.cuda.Stream()
+        for _ in range(5):
+            got[k] = tg.linear_cross_entropy_step(x, w, target, dloss, stream=s)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 4
+    for g in got.values():
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        inside = tg.linear_cross_entropy_step(x, w, target, dloss)
+    graph.replay()
+    check(x, w, layout, 1.0, q, live, zero, dloss, inside[0], None, *inside[1:])
+
+
 def test_graph_capture():
     T, V, D = 130, 2000, 136
     x, w = operands(T, V, D, 0, 118)
