@@ -392,6 +392,9 @@ typedef struct {
  * Scratch: the logits (float32) and their gradient (fp16) of a piece of the tokens, 2^29 of them
  * or 256 tokens' by default; with several pieces, dW in float32; copies of X and W when they are not
  * 16-byte aligned with leading dimensions that are multiples of 8.
+ * Up to 128 tokens, with both gradients of a large head, dW runs on a library stream beside dX and
+ * joins `stream`; a call made under stream capture runs one after the other (dX may differ in its
+ * last bit: its sum over V is split another way).
  * The gradient of the logits is rounded to fp16 relative to the largest |dloss|: a row whose
  * |dloss| is below 2^-15 of that keeps fewer than 11 bits of its small probabilities.
  */
