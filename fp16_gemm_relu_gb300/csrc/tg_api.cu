@@ -1135,8 +1135,15 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   }
 
   if (ws && !f32) {
-    launch_reduce(ws, pl.ldw, ws_rows * pl.ldw, P.split_k, static_cast<__half*>(C), ldc,
-                  reduce_params, P.a_row_classes ? pl.cls_rows : 0, ds->sm_count, stream);
+    tg::GemmParams rp = reduce_params;
+    int64_t rows = ws_rows;
+    int splits = P.split_k;
+    if (extra && extra->fold) {  // the second half of a split's rows is one more split of the first
+      rp.M = static_cast<int>(rows /= 2);
+      splits *= 2;
+    }
+    launch_reduce(ws, pl.ldw, rows * pl.ldw, splits, static_cast<__half*>(C), ldc, rp,
+                  P.a_row_classes ? pl.cls_rows : 0, ds->sm_count, stream);
     if ((e = cudaGetLastError()) != cudaSuccess) return fail(cuda_fail(e));
   }
   if (scratch && (e = cudaFreeAsync(scratch, stream)) != cudaSuccess) return cuda_fail(e);

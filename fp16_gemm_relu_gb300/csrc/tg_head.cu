@@ -16,7 +16,7 @@
 // them); dX and dW through the ordinary GEMMs on G.  Tokens go in pieces that bound the logits'
 // scratch; dW is summed over the pieces in float32.
 //
-// G is rounded to fp16 once, the operand type of the products.  So that the many small
+// G is rounded to fp16 once, the operand type of the products (kFineTokens: twice as fine).  So that the many small
 // probabilities stay normal fp16 numbers, G carries the factor 2^15 / max|w| (|p - q| <= 1, so
 // nothing overflows) and alpha = s max|w| / 2^15 is applied to the float32 sums: a row of the
 // largest weight keeps 11 bits of every p above 2^-29.
@@ -300,29 +300,52 @@ __device__ __forceinline__ float grad_value(float z, float c, float lse2, float 
 
 // G (fp16, rows of ldg) from the logits, eight columns of a row a thread; cross entropy's target with
 // it.  Bound by HBM: 6 bytes an element, 4096 x 131072 in 456 us, 7.0 TB/s.
+// FINE (few tokens): each value in two parts, G and `lo` elements further what its rounding left; and
+// X's rows (16-byte aligned, of `width`) twice over, for the product with both parts.
+template <bool FINE>
 __global__ void __launch_bounds__(256)
     tg_head_grad_kernel(const float* __restrict__ z, int64_t ldz, float c,
                         const RowInfo* __restrict__ info, int64_t rows, int64_t vocab,
-                        uint16_t* __restrict__ g, int64_t ldg) {
+                        uint16_t* __restrict__ g, int64_t ldg, int64_t lo,
+                        const uint16_t* __restrict__ x, int64_t ldx, uint16_t* __restrict__ x2,
+                        int64_t ldx2, int width) {
   const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
-  if (v0 >= vocab) return;
   tg::chain_wait();
   tg::chain_release();
+  if (FINE && x2 != nullptr && blockIdx.x == 0) {
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+      const uint16_t* from = x + r * ldx;
+      uint16_t *to = x2 + r * ldx2, *again = x2 + (r + rows) * ldx2;
+      const int whole = width & ~7;
+      for (int k = threadIdx.x * 8; k < whole; k += blockDim.x * 8)
+        *reinterpret_cast<uint4*>(to + k) = *reinterpret_cast<uint4*>(again + k) =
+            __ldg(reinterpret_cast<const uint4*>(from + k));
+      for (int k = whole + threadIdx.x; k < width; k += blockDim.x) to[k] = again[k] = from[k];
+    }
+  }
+  if (v0 >= vocab) return;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const RowInfo ri = info[r];
     const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
     const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
     const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t w[4];
+    uint32_t w[4], u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float lo = grad_value(f[2 * i], c, ri.lse2, ri.gs, v0 + 2 * i == ri.target ? 1.0f : 0.0f);
-      const float hi =
+      const float p0 = grad_value(f[2 * i], c, ri.lse2, ri.gs, v0 + 2 * i == ri.target ? 1.0f : 0.0f);
+      const float p1 =
           grad_value(f[2 * i + 1], c, ri.lse2, ri.gs, v0 + 2 * i + 1 == ri.target ? 1.0f : 0.0f);
-      const __half2 h = __floats2half2_rn(lo, hi);
+      const __half2 h = __floats2half2_rn(p0, p1);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      if constexpr (FINE) {
+        const float2 back = __half22float2(h);
+        const __half2 rest = __floats2half2_rn(p0 - back.x, p1 - back.y);
+        u[i] = *reinterpret_cast<const uint32_t*>(&rest);
+      }
     }
     *reinterpret_cast<uint4*>(g + r * ldg + v0) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (FINE)
+      *reinterpret_cast<uint4*>(g + lo + r * ldg + v0) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -333,7 +356,8 @@ __global__ void __launch_bounds__(128)
     tg_head_teacher_grad_kernel(const int64_t* __restrict__ index, int64_t ldt, int top,
                                 const float* __restrict__ q, const float* __restrict__ z,
                                 int64_t ldz, float c, const RowInfo* __restrict__ info,
-                                int64_t rows, int64_t vocab, __half* __restrict__ g, int64_t ldg) {
+                                int64_t rows, int64_t vocab, __half* __restrict__ g, int64_t ldg,
+                                int64_t lo) {
   const int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
   if (r >= rows) return;
   tg::chain_wait();
@@ -345,7 +369,10 @@ __global__ void __launch_bounds__(128)
     float sum = 0.0f;
     for (int k = 0; k < top; ++k)
       if (index[r * ldt + k] == i) sum += q[r * top + k];
-    g[r * ldg + i] = __float2half_rn(grad_value(z[r * ldz + i], c, ri.lse2, ri.gs, sum));
+    const float v = grad_value(z[r * ldz + i], c, ri.lse2, ri.gs, sum);
+    const __half h = __float2half_rn(v);
+    g[r * ldg + i] = h;
+    if (lo) g[lo + r * ldg + i] = __float2half_rn(v - __half2float(h));
   }
 }
 
@@ -366,6 +393,12 @@ constexpr int64_t kPieceLogits = int64_t{1} << 29;
 // lay, and never more than 88 from eight rows on.  So small operands lie in scratch of that many
 // rows; what the others hold does not matter, an MMA's rows have nothing to do with each other.
 constexpr int64_t kLeastRows = 8;
+// Up to so many tokens the products are bound by W's and dW's bytes, not by the tensor cores, and G is
+// kept in two fp16 parts (22 bits), as twice the rows of one product: with few rows its largest entries
+// may all round badly (the gradients' error 0.00032 of their size, with two parts 0.00021, which is
+// their own rounding to fp16; more tokens average to 0.0003).  It costs 1 to 3% of a step (64 tokens,
+// 28672 classes of 4096: 155 against 152 us).
+constexpr int64_t kFineTokens = 64;
 // Without logits a token's scratch is its statistics: 1 GiB of them.
 constexpr int64_t kPieceStats = int64_t{1} << 27;
 
@@ -489,6 +522,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     piece = std::min(h.T, round_up(cdiv(h.T, cdiv(h.T, most)), 256));
   }
   const bool sum_w = h.dW && piece < h.T;  // dW is summed over pieces in float32
+  const bool fine = grad && h.T <= kFineTokens && piece == h.T;
+  const int64_t parts = fine ? 2 : 1;  // of G
 
   Layout lay;
   // Rows that TMA cannot read in place are copied once for all pieces and products, and so are the
@@ -501,7 +536,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const int64_t at_picked = lay.add(store ? 0 : piece * std::max(h.top, 1) * 4);
   const int64_t at_info = lay.add(piece * int64_t(sizeof(RowInfo)));
   const int64_t at_small = lay.add(2 * 4);
-  const int64_t at_g = lay.add(grad ? std::max(piece, kLeastRows) * ldg * 2 : 0);
+  const int64_t at_g = lay.add(grad ? std::max(parts * piece, kLeastRows) * ldg * 2 : 0);
+  const int64_t at_x2 = lay.add(fine && h.dW ? 2 * h.T * ldxp * 2 : 0);
   const int64_t at_q = lay.add(grad && h.top ? piece * h.top * 4 : 0);
   const int64_t at_x = lay.add(copy_x ? std::max(h.T, kLeastRows) * ldxp * 2 : 0);
   const int64_t at_w = lay.add(copy_w ? w_rows * ldwp * 2 : 0);
@@ -601,13 +637,15 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
         q, alpha);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     if (!grad) continue;
-    chain(tg_head_grad_kernel,
+    const int64_t lo = fine ? n * ldg : 0;
+    uint16_t* x2 = fine && h.dW ? reinterpret_cast<uint16_t*>(mem + at_x2) : nullptr;
+    chain(fine ? tg_head_grad_kernel<true> : tg_head_grad_kernel<false>,
           dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
                static_cast<unsigned>(std::min<int64_t>(n, 65535))),
-          256, z, ldz, c, info, n, h.V, g, ldg);
+          256, z, ldz, c, info, n, h.V, g, ldg, lo, x, ldx, x2, ldxp, static_cast<int>(h.D));
     if (h.top)
       chain(tg_head_teacher_grad_kernel, dim3(static_cast<unsigned>(cdiv(n, 4))), 128, index, h.ldt,
-            h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg);
+            h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg, lo);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     // Few tokens: dX reads W and dW writes as much, each bound by HBM, where writes alone run at 3.9 TB/s
     // and reads and writes together at up to 6.8.  So the two run side by side, dX on a third of the
@@ -647,17 +685,22 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       // (28672 x 1024 from 128 tokens 20.5 against 26.7 us, 131072 x 2048 from 64 135 against 173; at
       // 512 tokens they are even).
       tg_options opt = gemm_opt;
+      const uint16_t* xs = fine ? x2 : x;
+      const int64_t ldxs = fine ? ldxp : ldx;
       if (n <= 256 && !(ex.out32 && ex.add)) opt.pair = -1;
       if (both) opt.max_ctas = sms - sms_x;
       st = by_vocab
-               ? tg::gemm_extra(1, 0, g, x, h.dW, h.V, h.D, n, ldg, ldx, h.lddw, ex, &opt, stream_w)
-               : tg::gemm_extra(1, 0, x, g, h.dW, h.D, h.V, n, ldx, ldg, h.lddw, ex, &opt, stream_w);
+               ? tg::gemm_extra(1, 0, g, xs, h.dW, h.V, h.D, parts * n, ldg, ldxs, h.lddw, ex, &opt,
+                                stream_w)
+               : tg::gemm_extra(1, 0, xs, g, h.dW, h.D, h.V, parts * n, ldxs, ldg, h.lddw, ex, &opt,
+                                stream_w);
     }
     if (h.dX && st == TG_OK) {  // G (n x V) times W (V x D, or stored D x V)
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
       ex.chained = !both;
-      ex.a_rows = std::max(n, kLeastRows);
+      ex.a_rows = std::max(parts * n, kLeastRows);
+      ex.fold = fine;
       // One row of tiles reads W once at the memory's rate, if the splits of V make one wave of
       // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
       // products' costs and for 128 tokens 20.4 against 20.7, 131072 x 4096 166 against 203, 28672 x
@@ -673,8 +716,9 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
         opt.split_k = static_cast<int>(splits);
       }
       if (both) opt.max_ctas = sms_x;
-      st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, n, h.D,
-                          h.V, ldg, ldw, h.lddx, ex, &opt, stream);
+      opt.force_workspace = fine ? 1 : 0;  // the sum of the parts is taken there
+      st = tg::gemm_extra(0, !by_vocab, g, W, static_cast<uint16_t*>(h.dX) + t0 * h.lddx, parts * n,
+                          h.D, h.V, ldg, ldw, h.lddx, ex, &opt, stream);
     }
     if (both) {  // joined on success and on error alike: the scratch is freed on `stream`
       if ((e = cudaEventRecord(side->done, side->stream)) == cudaSuccess)

@@ -396,7 +396,8 @@ typedef struct {
  * joins `stream`; a call made under stream capture runs one after the other (dX may differ in its
  * last bit: its sum over V is split another way).
  * The gradient of the logits is rounded to fp16 relative to the largest |dloss|: a row whose
- * |dloss| is below 2^-15 of that keeps fewer than 11 bits of its small probabilities.
+ * |dloss| is below 2^-15 of that keeps fewer than 11 bits of its small probabilities.  Up to 64
+ * tokens in one piece it is kept in two fp16 parts, with twice the bits.
  */
 tg_status tg_linear_cross_entropy_f16(const void* X, const void* W, const int64_t* target,
                                       int64_t ignore_index, float logit_scale, const float* dloss,
