@@ -565,13 +565,19 @@ __global__ void tg_first_window_kernel(const uint16_t* __restrict__ A, int64_t l
 // (a flat index split by a 64-bit division per item, one row at a time, ran at 0.67 of HBM).
 constexpr int kReduceRows = 4;
 constexpr int kReduceThreads = 128;
+// Four partial sums.  The scaled reduction is chained to the GEMM that writes them (chain_wait).
+template <bool SCALED>
+__device__ __forceinline__ float4 partial4(const float* p) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+  return SCALED ? __ldcg(q) : __ldg(q);
+}
 template <bool SCALED>  // the scaled sum (p.alpha) in place of the epilogue
 __device__ __forceinline__ float reduced_value(float x, int row, int col, const tg::GemmParams& p) {
   return SCALED ? tg::scaled_value(x, row, col, p) : tg::epilogue_value(x, row, col, p);
 }
 template <bool SCALED>
 __global__ void __launch_bounds__(kReduceThreads)
-    tg_splitk_reduce_kernel(const float* __restrict__ ws, int64_t ldw, int64_t split_stride,
+    tg_splitk_reduce_kernel(const float* ws, int64_t ldw, int64_t split_stride,
                             int splits, __half* C, int64_t ldc, const tg::GemmParams p,
                             int64_t cls_rows) {
   const int64_t M = p.M, N = p.N;
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kReduceThreads)
       float4 v[kReduceRows];
 #pragma unroll
       for (int i = 0; i < kReduceRows; ++i)
-        v[i] = __ldg(reinterpret_cast<const float4*>(w[i] + s * split_stride));
+        v[i] = partial4<SCALED>(w[i] + s * split_stride);
 #pragma unroll
       for (int i = 0; i < kReduceRows; ++i) {
         if (s == 0) {
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(kReduceThreads)
 constexpr int kReduceAhead = 8;
 template <bool SCALED>
 __global__ void __launch_bounds__(kReduceThreads)
-    tg_splitk_reduce_small_kernel(const float* __restrict__ ws, int64_t ldw, int64_t split_stride,
+    tg_splitk_reduce_small_kernel(const float* ws, int64_t ldw, int64_t split_stride,
                                   int splits, __half* C, int64_t ldc, const tg::GemmParams p) {
   const int64_t g = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;  // group of 4 columns
   const int64_t N = p.N, r = blockIdx.y, c0 = g << 2;
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(kReduceThreads)
 #pragma unroll
     for (int i = 0; i < kReduceAhead; ++i)
       if (s0 + i < splits)
-        v[i] = __ldg(reinterpret_cast<const float4*>(w + (s0 + i) * split_stride));
+        v[i] = partial4<SCALED>(w + (s0 + i) * split_stride);
 #pragma unroll
     for (int i = 0; i < kReduceAhead; ++i) {
       if (s0 + i >= splits) break;

@@ -103,7 +103,11 @@ enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2 };
 
 // Kernels that are launched chained.  chain_wait: nothing that the kernel before has written is read,
 // and nothing that it reads is written, before this.  chain_release, after it: the next kernel's
-// blocks may take what room this one leaves.
+// blocks may take what room this one leaves.  A chained kernel is resident while the one before it
+// writes, so what that one writes is not read-only for its life: it is read by ordinary loads or
+// __ldcg, after chain_wait, and never by __ldg or through a const __restrict__ pointer (which the
+// compiler may read by the non-coherent path, and early).  Those are for the caller's own inputs, and
+// for copies of them that were finished before the kernel before began.
 __device__ __forceinline__ void chain_wait() { cudaGridDependencySynchronize(); }
 __device__ __forceinline__ void chain_release() { cudaTriggerProgrammaticLaunchCompletion(); }
 
@@ -128,7 +132,7 @@ __device__ __forceinline__ float activation(float x, int act) {
 // The scaled sum in place of it (p.alpha).
 __device__ __forceinline__ float scaled_value(float x, int row, int col, const GemmParams& p) {
   if (p.addend) x += p.addend[static_cast<long long>(row) * p.ld_addend + col];
-  return x * __ldg(p.alpha);
+  return x * *p.alpha;
 }
 
 // Full epilogue of one float32 sum at (row, col): (sum + bias) -> activation -> + residual.
@@ -628,7 +632,7 @@ __device__ __forceinline__ void load_half32(const __half* src, int col, int n, f
 // 32 consecutive columns of one row scaled: fp16 pairs of alpha (acc + addend) into pk[0..15].
 __device__ __forceinline__ void epilogue_scaled_32(const uint32_t (&acc)[32], int row, int col,
                                                    const GemmParams& p, uint32_t* pk) {
-  const float a = __ldg(p.alpha);
+  const float a = *p.alpha;
   if (p.addend == nullptr || row >= p.M) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

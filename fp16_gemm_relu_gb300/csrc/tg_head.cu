@@ -38,7 +38,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kGScale = 32768.0f;
 
 // What the passes after the logits know of a row.
-struct RowInfo {
+struct alignas(16) RowInfo {
   float lse2;    // log2 of the sum of 2^(c logit), c = s log2(e)
   float gs;      // factor of the row of G: w_t 2^15 / max|w|, 0 for a row that does not count
   int target;    // cross entropy: the row's target in [0, V); -1 otherwise
@@ -153,10 +153,10 @@ __device__ __forceinline__ float teacher_at(const void* t, int64_t at, int is_f3
 // gradient.  alpha (one float): s max|w| / 2^15, written by the first block.  Bound by latency: 4096
 // rows of 65537 classes (2 KB of statistics each) and 64 entries 18 us, one row 5 us.
 __global__ void __launch_bounds__(kRowThreads)
-    tg_head_rows_kernel(const float2* __restrict__ stats, int tiles, Logits lg, float scale,
+    tg_head_rows_kernel(const float2* stats, int tiles, Logits lg, float scale,
                         int64_t vocab, const int64_t* __restrict__ index, int64_t ignore,
                         const void* __restrict__ teacher, int teacher_f32, int64_t ldt, int top,
-                        const float* __restrict__ dloss, const unsigned* __restrict__ wmax,
+                        const float* __restrict__ dloss, const unsigned* wmax,
                         float* loss, float* lse, RowInfo* info, float* q, float* alpha) {
   __shared__ float slots[5][4];
   const int64_t r = blockIdx.x;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kRowThreads)
   float m = -INFINITY, s = 0.0f;
 #pragma unroll 4
   for (int t = tid; t < tiles; t += kRowThreads) {
-    const float2 v = stats[r * tiles + t];
+    const float2 v = __ldcg(stats + r * tiles + t);
     const float m1 = fmaxf(m, v.x);
     if (m1 == -INFINITY) {
       s += v.y;  // zero or NaN
@@ -304,9 +304,8 @@ __device__ __forceinline__ float grad_value(float z, float c, float lse2, float 
 // X's rows (16-byte aligned, of `width`) twice over, for the product with both parts.
 template <bool FINE>
 __global__ void __launch_bounds__(256)
-    tg_head_grad_kernel(const float* __restrict__ z, int64_t ldz, float c,
-                        const RowInfo* __restrict__ info, int64_t rows, int64_t vocab,
-                        uint16_t* __restrict__ g, int64_t ldg, int64_t lo,
+    tg_head_grad_kernel(const float* z, int64_t ldz, float c, const RowInfo* info, int64_t rows,
+                        int64_t vocab, uint16_t* __restrict__ g, int64_t ldg, int64_t lo,
                         const uint16_t* __restrict__ x, int64_t ldx, uint16_t* __restrict__ x2,
                         int64_t ldx2, int width) {
   const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
@@ -354,10 +353,9 @@ __global__ void __launch_bounds__(256)
 // block's way: 4096 x 65537 with 64 entries took 325 to 380 us so, 235 and 17 apart.
 __global__ void __launch_bounds__(128)
     tg_head_teacher_grad_kernel(const int64_t* __restrict__ index, int64_t ldt, int top,
-                                const float* __restrict__ q, const float* __restrict__ z,
-                                int64_t ldz, float c, const RowInfo* __restrict__ info,
-                                int64_t rows, int64_t vocab, __half* __restrict__ g, int64_t ldg,
-                                int64_t lo) {
+                                const float* q, const float* z, int64_t ldz, float c,
+                                const RowInfo* info, int64_t rows, int64_t vocab,
+                                __half* __restrict__ g, int64_t ldg, int64_t lo) {
   const int64_t r = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) >> 5;
   if (r >= rows) return;
   tg::chain_wait();

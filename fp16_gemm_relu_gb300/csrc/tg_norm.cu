@@ -1131,11 +1131,11 @@ __global__ void __launch_bounds__(kLongDxThreads)
 // dgamma (blockIdx.y 0) or dbeta (1) from the blocks' partial rows, in a fixed order: 32 columns a
 // block, four a thread; each of the 32 thread rows adds every 32nd partial row, eight loads in
 // flight, then the thread rows are added in order.  The partial rows (304 of 4096 columns: 10 MB)
-// are in L2; the latency of the few loads bounds it.
+// are in L2; the latency of the few loads bounds it.  Chained to the kernel that writes them.
 constexpr int kPartRows = 32;
 template <typename P>
 __global__ void __launch_bounds__(8 * kPartRows)
-    tg_layernorm_params_kernel(const float* __restrict__ part, int parts, int64_t np, int n,
+    tg_layernorm_params_kernel(const float* part, int parts, int64_t np, int n,
                                P* dgamma, P* dbeta) {
   __shared__ float4 sum[kPartRows][8];
   P* out = blockIdx.y == 0 ? dgamma : dbeta;
@@ -1148,7 +1148,7 @@ __global__ void __launch_bounds__(8 * kPartRows)
     const float* src = part + int64_t(blockIdx.y) * parts * np + j;
 #pragma unroll 8
     for (int p = row; p < parts; p += kPartRows) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(src + p * np));
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + p * np));
       acc.x += v.x;
       acc.y += v.y;
       acc.z += v.z;
