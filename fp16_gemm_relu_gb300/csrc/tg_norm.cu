@@ -285,7 +285,9 @@ __device__ __forceinline__ Fetch plan_fetch(const uint16_t* row, int n, const Sp
   const uintptr_t from = start > sp.lo ? start : sp.lo, to = end < sp.hi ? end : sp.hi;
   return {from, to > from ? to : from, start};
 }
-// The elements that no whole block has; before the barrier's arrive, which releases them.
+// The elements that no whole block has; before the barrier's arrive, which releases them.  Only the
+// matrix's first row (among a group's first fetches) and its last (after which its slot gets no other)
+// have any: a ring's rows are longer than a block, so every other row lies inside the span.
 template <bool VEC>
 __device__ __forceinline__ void fetch_edges(const Fetch& f, uint8_t* slot, const uint16_t* row, int n) {
   if constexpr (!VEC) {
@@ -465,6 +467,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
     for (int s = 0; s < S; ++s) tg::mbar_init(tg::smem_u32(&bars[group][s]), 1);
     tg::fence_mbar_init();
     for (int s = 0; s < S && s < count; ++s) fetch(s, s);
+    // a later row's copy may write what fetch_edges has written of the first
+    if constexpr (!VEC) tg::fence_async_smem();
   }
   const uint32_t shift = A == kRowsAlike ? row_shift(x, ldx, first) : 0u;  // of all the group's rows
   const int off = static_cast<int>(shift >> 1);
@@ -603,6 +607,8 @@ __global__ void __launch_bounds__(512)
     for (int s = 0; s < S; ++s) tg::mbar_init(tg::smem_u32(&bars[group][s]), 1);
     tg::fence_mbar_init();
     for (int s = 0; s < S && s < count; ++s) fetch(s, s);
+    // a later row's copy may write what fetch_edges has written of the first
+    if constexpr (!VEC) tg::fence_async_smem();
   }
   const uint32_t shift = A == kRowsAlike ? row_shift(x, ldx, first) : 0u;  // of all the group's rows
   const int off = static_cast<int>(shift >> 1);
