@@ -307,20 +307,33 @@ __device__ __forceinline__ void fetch_blocks(const Fetch& f, uint8_t* slot, uint
       : "memory");
 }
 
-// Waits for a slot.  A wait that runs out (2 s) is recorded as a timeout and ends all later
-// waits of the block, which then runs to its end on what is there.
-__device__ __forceinline__ void slot_wait(uint32_t bar, uint32_t parity, volatile int* late,
+// Waits for a slot: true when it is filled.  A wait that runs out (2 s) is recorded as a timeout and
+// ends all later waits of the block, which then runs to its end on what is there.
+__device__ __forceinline__ bool slot_wait(uint32_t bar, uint32_t parity, volatile int* late,
                                           unsigned* err) {
-  if (tg::mbar_try_wait(bar, parity)) return;
+  if (tg::mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = tg::global_timer_ns();
   for (uint32_t it = 1; !tg::mbar_try_wait(bar, parity); ++it) {
     if ((it & 63u) != 0) continue;
-    if (*late) return;
+    if (*late) return false;
     if (tg::global_timer_ns() - t0 > 2000000000ull) {
       *late = 1;
       atomicOr(err, 1u | (tg::kRoleProducer << 8));
-      return;
+      return false;
     }
+  }
+  return true;
+}
+// After a wait that ran out, by the thread that fetches, which then fetches nothing more: copies may
+// still be on their way, and shared memory may be another block's once this one is gone.  So it waits
+// for the last of its `fetched` fetches in each slot, with the same limit.
+template <int S>
+__device__ __forceinline__ void slots_drain(uint64_t* bars, int fetched) {
+  const unsigned long long t0 = tg::global_timer_ns();
+  for (int s = 0; s < S && s < fetched; ++s) {
+    const uint32_t parity = static_cast<uint32_t>((fetched - 1 - s) / S) & 1u;
+    while (!tg::mbar_try_wait(tg::smem_u32(&bars[s]), parity))
+      if (tg::global_timer_ns() - t0 > 2000000000ull) return;
   }
 }
 
@@ -477,10 +490,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
   if constexpr (!VEC) set_edges(&edges, off, n);
   __syncthreads();
   const float inv_n = 1.0f / static_cast<float>(n);
+  bool fetcher = t == 0;
   for (int k = 0; k < count; ++k) {
     const int s = k & 1;
     const int64_t r = first + int64_t(k) * step;
-    slot_wait(tg::smem_u32(&bars[group][s]), (k >> 1) & 1, &late, err);
+    if (!slot_wait(tg::smem_u32(&bars[group][s]), (k >> 1) & 1, &late, err) && fetcher) {
+      slots_drain<S>(bars[group], min(count, k + S));
+      fetcher = false;
+    }
     const uint32_t b = A == kRowsAny ? row_shift(x, ldx, r) : shift;
     f32x2 v[CH][4], acc = pair(0.0f, 0.0f);
 #pragma unroll
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
       acc = add2(acc, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
     }
     const float mu = group_sum(sum2(acc), tpr, group, sums[group][0]) * inv_n;
-    if (t == 0 && k + S < count) fetch(k + S, s);  // everyone has read this slot
+    if (fetcher && k + S < count) fetch(k + S, s);  // everyone has read this slot
     const f32x2 less = pair(-mu, -mu);
     f32x2 q = pair(0.0f, 0.0f);
 #pragma unroll
@@ -697,8 +714,15 @@ __global__ void __launch_bounds__(512)
   const int first_warp = lane % kLanes;
   const float* mine = &sums[0][0][0] + lane / kLanes * 16 + group * wpr + first_warp;
   Stats now = stats_of(0), next = stats_of(1);
+  bool fetcher = t == 0;
+  auto wait = [&](int k, int s, uint32_t phase) {
+    if (!slot_wait(tg::smem_u32(&bars[group][s]), phase, &late, err) && fetcher) {
+      slots_drain<S>(bars[group], min(count, max(k - 1, 0) + S));
+      fetcher = false;
+    }
+  };
   if (count > 0) {
-    slot_wait(tg::smem_u32(&bars[group][0]), 0, &late, err);
+    wait(0, 0, 0);
     sum_rows(0, 0, now);
   }
   carry();
@@ -708,7 +732,7 @@ __global__ void __launch_bounds__(512)
   for (int k = 0; k < count; ++k) {
     const Stats ahead = stats_of(k + 2);
     if (k + 1 < count) {
-      slot_wait(tg::smem_u32(&bars[group][s1]), phase1, &late, err);
+      wait(k + 1, s1, phase1);
       sum_rows(k + 1, s1, next);
     }
     if (dx != nullptr) {
@@ -755,7 +779,7 @@ __global__ void __launch_bounds__(512)
     next = ahead;
     carry();
     group_sync(tpr, group);  // stage s and sums[k & 1] are free, sums[(k + 1) & 1] is written
-    if (t == 0 && k + S < count) fetch(k + S, s);
+    if (fetcher && k + S < count) fetch(k + S, s);
     s = s1;
     if (++s1 == S) {
       s1 = 0;

@@ -46,3 +46,22 @@ def test_generic_writes_of_a_slot_come_before_later_copies():
     for text in ring_kernels():
         assert re.search(r"s < S && s < count; \+\+s\) fetch\(s, s\);\s*//[^\n]*\s*"
                          r"if constexpr \(!VEC\) tg::fence_async_smem\(\);", text)
+
+
+def test_the_drain_waits_for_the_last_fetch_of_each_slot():
+    # fetch k goes to slot k mod S and is that slot's phase k / S, whose parity is waited for
+    for S in (2, 3):
+        for fetched in range(1, 40):
+            for s in range(min(S, fetched)):
+                last = max(k for k in range(fetched) if k % S == s)
+                assert last // S & 1 == (fetched - 1 - s) // S & 1
+
+
+def test_after_a_timeout_nothing_more_is_fetched_and_copies_are_waited_for():
+    assert "(fetched - 1 - s) / S) & 1u" in source()
+    for text in ring_kernels():
+        assert "if (fetcher && k + S < count) fetch(k + S, s);" in text
+        assert text.count("fetch(") == 2  # the first fetches, and that one
+        waits = re.findall(r"if \(!slot_wait\([^;]*fetcher\) \{\s*slots_drain<S>\([^;]*;\s*"
+                           r"fetcher = false;", text)
+        assert len(waits) == 1 == text.count("slot_wait(")
