@@ -736,22 +736,23 @@ __global__ void __launch_bounds__(512)
       sum_rows(k + 1, s1, next);
     }
     if (dx != nullptr) {
-      // dx = rstd (g - mean(g) - h mean(g h)) = d (gamma rstd) + x c1 + c0 with
-      // c1 = -rstd^3 mean(g u) and c0 = -rstd mean(g) - mean c1.  (Left uncentred, x c1 + c0 is off
-      // by 2^-24 |mean| / spread of its size, far below dx's rounding to fp16.)
+      // dx = rstd (g - mean(g) - h mean(g h)) = d (gamma rstd) + u c1 + c0 with
+      // c1 = -rstd^3 mean(g u) and c0 = -rstd mean(g).  Centred: with x for u, and mean c1 taken off
+      // c0, a row is off by 2^-24 |mean| / spread of h mean(g h), which dx may cancel to far less
+      // (x = 1000 +- 0.5 and dy = h: dx off by a quarter).
       const float* from = mine + (k & 1) * (V * 16);
       float v = first_warp < wpr ? from[0] : 0.0f;
       if (R == 2 && first_warp + 8 < wpr) v += from[8];
 #pragma unroll
       for (int d = kLanes / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-      f32x2 of_x[R], plus[R], times[R];
+      f32x2 less[R], of_u[R], plus[R], times[R];
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const float a = __shfl_sync(0xffffffffu, v, j * kLanes);
         const float b = __shfl_sync(0xffffffffu, v, 16 + j * kLanes);
-        const float rs = now.rs[j], c1 = -rs * rs * rs * (b * inv_n);
-        const float c0 = fmaf(-now.mu[j], c1, -rs * (a * inv_n));
-        of_x[j] = pair(c1, c1);
+        const float rs = now.rs[j], c1 = -rs * rs * rs * (b * inv_n), c0 = -rs * (a * inv_n);
+        less[j] = pair(-now.mu[j], -now.mu[j]);
+        of_u[j] = pair(c1, c1);
         plus[j] = pair(c0, c0);
         times[j] = pair(rs, rs);
       }
@@ -770,7 +771,7 @@ __global__ void __launch_bounds__(512)
           unpack8(cd[j][h], d);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            o[e] = fma2(d[e], mul2(g[e], times[j]), fma2(w[e], of_x[j], plus[j]));
+            o[e] = fma2(d[e], mul2(g[e], times[j]), fma2(add2(w[e], less[j]), of_u[j], plus[j]));
           store_row_chunk<A>(dx + row * lddx, i * tpr + t, off, n, pack8(o), lane);
         }
       }
@@ -1142,9 +1143,9 @@ __global__ void __launch_bounds__(kLongDxThreads)
     }
     const float a = group_sum(sum2(a2), T, 0, slots[turn][0]);
     const float b = group_sum(sum2(b2), T, 0, slots[turn][1]);
-    // as in the ring's kernel: dx = d (gamma rstd) + x c1 + c0
-    const float c1 = -rs * rs * rs * (b * inv_n), c0 = fmaf(-mu, c1, -rs * (a * inv_n));
-    const f32x2 of_x = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
+    // as in the ring's kernel: dx = d (gamma rstd) + u c1 + c0
+    const float c1 = -rs * rs * rs * (b * inv_n), c0 = -rs * (a * inv_n);
+    const f32x2 of_u = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       f32x2 w[4], d[4], g[4];
@@ -1152,7 +1153,7 @@ __global__ void __launch_bounds__(kLongDxThreads)
       unpack8(xv[i], w);
       unpack8(dv[i], d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = fma2(d[j], mul2(g[j], times), fma2(w[j], of_x, plus));
+      for (int j = 0; j < 4; ++j) w[j] = fma2(d[j], mul2(g[j], times), fma2(add2(w[j], less), of_u, plus));
       long_store<VEC, T>(dx + r * lddx, i, n, pack8(w));
     }
   }
