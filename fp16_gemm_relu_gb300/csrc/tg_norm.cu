@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(512)
       for (int j = 0; j < R; ++j) {
         const float a = __shfl_sync(0xffffffffu, v, j * kLanes);
         const float b = __shfl_sync(0xffffffffu, v, 16 + j * kLanes);
-        const float rs = now.rs[j], c1 = -rs * rs * rs * (b * inv_n), c0 = -rs * (a * inv_n);
+        const float rs = now.rs[j], c1 = -rs * (rs * (rs * (b * inv_n))), c0 = -rs * (a * inv_n);
         less[j] = pair(-now.mu[j], -now.mu[j]);
         of_u[j] = pair(c1, c1);
         plus[j] = pair(c0, c0);
@@ -1144,7 +1144,7 @@ __global__ void __launch_bounds__(kLongDxThreads)
     const float a = group_sum(sum2(a2), T, 0, slots[turn][0]);
     const float b = group_sum(sum2(b2), T, 0, slots[turn][1]);
     // as in the ring's kernel: dx = d (gamma rstd) + u c1 + c0
-    const float c1 = -rs * rs * rs * (b * inv_n), c0 = -rs * (a * inv_n);
+    const float c1 = -rs * (rs * (rs * (b * inv_n))), c0 = -rs * (a * inv_n);
     const f32x2 of_u = pair(c1, c1), plus = pair(c0, c0), times = pair(rs, rs);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {

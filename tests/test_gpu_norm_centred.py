@@ -30,3 +30,13 @@ def test_far_from_zero(M, N, shift, spread, along, noise):
     h = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
     dy = (along * h + noise * make(M, N, seed=81).double()).half()
     check_backward(dy, x, gamma, mean, rstd, *tg.layer_norm_backward(dy, x, mean, rstd, gamma))
+
+
+@pytest.mark.parametrize("N", [512, 1000, 4096, 9000, 20000])
+def test_constant_rows_and_a_tiny_eps(N):
+    """rstd = 1 / sqrt(eps) of a row without spread: 1e15 here, whose cube is no float32."""
+    x = torch.full((5, N), 2.0, dtype=torch.float16, device="cuda")  # its mean is exact
+    _, mean, rstd = tg.layer_norm(x, eps=1e-30, stats=True)
+    assert (mean == 2).all()
+    dx, dgamma, dbeta = tg.layer_norm_backward(torch.zeros_like(x), x, mean, rstd)
+    assert (dx == 0).all() and (dgamma == 0).all() and (dbeta == 0).all()
