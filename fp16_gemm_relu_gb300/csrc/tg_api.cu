@@ -199,9 +199,10 @@ double kblock_cycles(int bn) {
 // (a tail-split last wave counts half); memory time = the algorithmic bytes at 6.8 TB/s,
 // inflated when a wave keeps fewer than 60% of the SMs busy; plus the float32 workspace
 // traffic of split-K and its extra launch, and the operand copies of unaligned operands.
+// max_k: 0, or the K columns that a split may have at most (where the options leave the splits open).
 tg_status make_plan(uintptr_t a, uintptr_t b, uintptr_t c, int64_t M, int64_t N, int64_t K,
                     int64_t lda, int64_t ldb, int64_t ldc, int num_sms, int pair_clusters,
-                    const tg_options* opt, Plan* out, int ta = 0, int tb = 0) {
+                    const tg_options* opt, Plan* out, int ta = 0, int tb = 0, int64_t max_k = 0) {
   tg_options o;
   std::memset(&o, 0, sizeof(o));
   if (opt) o = *opt;
@@ -233,6 +234,7 @@ tg_status make_plan(uintptr_t a, uintptr_t b, uintptr_t c, int64_t M, int64_t N,
     *out = pl;
     return TG_OK;
   }
+  const int64_t least_s = max_k > 0 ? cdiv(P.kblocks, std::max<int64_t>(max_k / tg::kBK, 1)) : 1;
   const int grid_cap = o.max_ctas > 0 ? std::min(o.max_ctas, num_sms) : num_sms;
   const double clk = 1.9e9, hbm = 6.8e12;
   const double alg_bytes = 2.0 * (double(M) * K + double(K) * N + double(M) * N);
@@ -263,12 +265,12 @@ tg_status make_plan(uintptr_t a, uintptr_t b, uintptr_t c, int64_t M, int64_t N,
     const int bm = pair ? 2 * tg::kBM : tg::kBM;
     const int64_t tiles = cdiv(M, bm) * cdiv(N, bn);
     const int64_t s_max = o.split_k ? std::min<int64_t>(o.split_k, P.kblocks)
-                                    : std::min<int64_t>(P.kblocks, 32);
-    const int64_t s_min = o.split_k ? s_max : 1;
+                                    : std::min<int64_t>(P.kblocks, std::max<int64_t>(least_s, 32));
+    const int64_t s_min = o.split_k ? s_max : least_s;
     for (int64_t s = s_min; s <= s_max; ++s) {
       const int64_t kbps = cdiv(P.kblocks, s);
       const int64_t s_eff = cdiv(P.kblocks, kbps);
-      if (!o.split_k && s_eff != s) continue;  // same plan as a smaller s
+      if (s != s_min && s_eff != s) continue;  // same plan as a smaller s
       const int64_t units = tiles * s_eff;
       // a pair unit occupies two SMs; the per-SM k-block cost of the pair tile is the MMA
       // time alone (each SM loads 32 KB per k-block, well under the L2 budget)
@@ -903,7 +905,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   Plan pl;
   st = make_plan(reinterpret_cast<uintptr_t>(A), reinterpret_cast<uintptr_t>(B),
                  reinterpret_cast<uintptr_t>(C), M, N, K, lda, ldb, ldc, ds->sm_count,
-                 ds->pair_clusters, opt, &pl, ta, tb);
+                 ds->pair_clusters, opt, &pl, ta, tb, extra ? extra->max_k : 0);
   if (st != TG_OK) return st;
   if (f32) {  // the workspace is the caller's, or there is none
     pl.ldw = logits ? logits->ldz : extra->ld32;

@@ -397,6 +397,11 @@ constexpr int64_t kLeastRows = 8;
 // their own rounding to fp16; more tokens average to 0.0003).  It costs 1 to 3% of a step (64 tokens,
 // 28672 classes of 4096: 155 against 152 us).
 constexpr int64_t kFineTokens = 64;
+// Columns of V that one accumulator sums for dX, tokens for dW.  The tensor core cuts off where it adds
+// (tg_head_kernel.cuh), so a long sum shrinks: dX over 65536 columns in one accumulator by 1.2e-4 of
+// itself, over 120000 by 2.2e-4, as much as its rounding to fp16.  More splits (or, for dW, pieces) are
+// added in float32.
+constexpr int64_t kSumLength = 16384;
 // Without logits a token's scratch is its statistics: 1 GiB of them.
 constexpr int64_t kPieceStats = int64_t{1} << 27;
 
@@ -519,6 +524,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     const int64_t most = std::max<int64_t>(budget / per_row / 256 * 256, 256);
     piece = std::min(h.T, round_up(cdiv(h.T, cdiv(h.T, most)), 256));
   }
+  if (h.dW && piece < h.T) piece = std::min(piece, kSumLength);
   const bool sum_w = h.dW && piece < h.T;  // dW is summed over pieces in float32
   const bool fine = grad && h.T <= kFineTokens && piece == h.T;
   const int64_t parts = fine ? 2 : 1;  // of G
@@ -670,6 +676,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       std::memset(&ex, 0, sizeof(ex));
       ex.alpha = alpha;
       ex.chained = !both;
+      ex.max_k = kSumLength;
       if (sum_w) {  // the first piece writes the sums, the last takes them into its epilogue
         ex.ld32 = ldw32;
         if (t0 + piece < h.T) {
@@ -699,6 +706,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       ex.chained = !both;
       ex.a_rows = std::max(parts * n, kLeastRows);
       ex.fold = fine;
+      ex.max_k = kSumLength;
       // One row of tiles reads W once at the memory's rate, if the splits of V make one wave of
       // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
       // products' costs and for 128 tokens 20.4 against 20.7, 131072 x 4096 166 against 203, 28672 x
@@ -707,7 +715,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       tg_options opt = gemm_opt;
       const int64_t width = h.D <= 2048 ? 128 : 256;
       const int64_t splits =
-          std::min({sms_x / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)});
+          std::max(std::min({sms_x / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)}),
+                   cdiv(h.V, kSumLength));
       if (n <= 128 && splits > 1) {
         opt.pair = -1;
         opt.block_n = static_cast<int>(width);

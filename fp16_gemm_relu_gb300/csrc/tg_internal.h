@@ -105,6 +105,7 @@ struct GemmExtra {
   bool add;             // add to out32 (A stored K x M, B stored K x N) instead of writing it
   bool chained;         // logits or alpha: see GemmLaunch
   bool fold;            // fp16 output: M even, C has M / 2 rows, row r the sum of rows r and r + M / 2
+  int64_t max_k;        // 0, or the K columns that one split may have (without logits and out32)
   int64_t a_rows;       // 0, or the rows (>= M) that A, stored M x K and not copied, has in memory
 };
 tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
