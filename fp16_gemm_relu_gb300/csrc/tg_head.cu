@@ -150,7 +150,8 @@ __device__ __forceinline__ float teacher_at(const void* t, int64_t at, int is_f3
 // Distillation (top > 0): entries with a negative index are not there; q is the softmax of the
 // others (one at -inf has q = 0), kept for the gradient when `q` is given (0 for what is not
 // there).  A row without entries, or whose entries are all at -inf, has no teacher: loss 0 and no
-// gradient.  alpha (one float): s max|w| / 2^15, written by the first block.  Bound by latency: 4096
+// gradient.  Logits are scaled after the row's largest is taken off, so that those at the type's lowest
+// value stay finite: a row of nothing else has a flat teacher.  alpha (one float): s max|w| / 2^15, written by the first block.  Bound by latency: 4096
 // rows of 65537 classes (2 KB of statistics each) and 64 entries 18 us, one row 5 us.
 __global__ void __launch_bounds__(kRowThreads)
     tg_head_rows_kernel(const float2* stats, int tiles, Logits lg, float scale,
@@ -214,21 +215,21 @@ __global__ void __launch_bounds__(kRowThreads)
       if (i < 0) continue;
       const float u = e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32);
       bad |= i >= vocab || !(u < INFINITY);  // NaN or +inf
-      mt = fmaxf(mt, u * c);
+      mt = fmaxf(mt, u);
     }
     mt = block_max(mt, slots[2]);
     bad = __syncthreads_or(bad);
     float st = 0.0f;
     for (int e = tid; e < top && mt > -INFINITY; e += kRowThreads)
       if ((e == tid ? i0 : index[r * ldt + e]) >= 0)
-        st += exp2f(fmaf(e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32), c, -mt));
-    const float lq = mt + log2f(block_sum(st, slots[3]));
+        st += exp2f(((e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32)) - mt) * c);
+    const float lq = log2f(block_sum(st, slots[3]));
     for (int e = tid; e < top; e += kRowThreads) {
       float qe = 0.0f;
       const int64_t i = e == tid ? i0 : index[r * ldt + e];
       if (i >= 0 && mt > -INFINITY) {
         const float u = e == tid ? u0 : teacher_at(teacher, r * ldt + e, teacher_f32);
-        const float t2 = fmaf(u, c, -lq);
+        const float t2 = fmaf(u - mt, c, -lq);
         qe = exp2f(t2);
         if (qe > 0.0f && i < vocab) {
           const float z = e == tid ? z0 : lg.z ? lg.z[r * lg.ldz + i] : lg.picked[r * top + e];
