@@ -75,7 +75,9 @@ __device__ __forceinline__ void load8(const uint16_t* row, int k, int n, float (
   }
 }
 
-// max |w_t| over the rows that count, as the bits of a non-negative float.  top == 0: cross
+// max |w_t| over the rows that count and have a finite w_t, as the bits of a non-negative float (an
+// infinite one as the common factor would turn every row's 0 times it into NaN; so only its own row of
+// G is not finite).  top == 0: cross
 // entropy; else a row counts when one of its `top` entries does.  One block writes the maximum; with
 // several it is zero before and the largest of theirs wins (the order of the atomics does not
 // matter).
@@ -89,7 +91,8 @@ __global__ void __launch_bounds__(1024)
        r += int64_t(gridDim.x) * blockDim.x) {
     bool live = top == 0 && index[r] != ignore;
     for (int j = 0; j < top && !live; ++j) live = index[r * ld + j] >= 0;
-    if (live) m = fmaxf(m, fabsf(dloss[r]));
+    const float w = live ? fabsf(dloss[r]) : 0.0f;
+    if (w < INFINITY) m = fmaxf(m, w);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
