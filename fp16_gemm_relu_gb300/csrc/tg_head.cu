@@ -657,13 +657,16 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     // Few tokens: dX reads W and dW writes as much, each bound by HBM, where writes alone run at 3.9 TB/s
     // and reads and writes together at up to 6.8.  So the two run side by side, dX on a third of the
-    // SMs (28672 x 4096, 16 tokens: the step 149 us, one after the other 160; dX on 64 SMs 159, on 80
-    // 179), where the work is worth a second stream (32000 x 512 47 against 53 us, 33000 x 256 43.4
-    // against 42.7).  Not into a graph that is being captured: the stream would belong to it until its
-    // end.  (Other shares are other splits of V, so dX may differ from that in its last bit.)
-    const bool both = h.dX && h.dW && n == h.T && n <= 128 && h.V * h.D >= kSideWork &&
-                      !capturing(stream);
-    const int sms_x = both ? sms / 3 : sms;
+    // SMs, where the work is worth a second stream.  dX's splits of V are then whole waves both on that
+    // third and on all SMs, and the same in a graph that is being captured, where the two run one after
+    // the other (the stream would belong to the graph until its end).  28672 x 4096: one token 157 us, one
+    // after the other 175, 16 tokens 153 and 160, 64 tokens 160 and 169; 32 tokens of 28672 x 8192 287 and
+    // 285, 128 of 131072 x 2048 367 and 358, with one wave of splits over the third 322 and 388.
+    const int64_t width = h.D <= 2048 ? 128 : 256;  // narrow W: narrow tiles
+    const int sms_x = sms / 3;
+    const bool beside = h.dX && h.dW && n == h.T && n <= 128 && h.V * h.D >= kSideWork &&
+                        2 * cdiv(h.D, width) <= 3 * sms_x;
+    const bool both = beside && !capturing(stream);
     Side* side = nullptr;
     std::unique_lock<std::mutex> lock;
     cudaStream_t stream_w = stream;
@@ -697,6 +700,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       const uint16_t* xs = fine ? x2 : x;
       const int64_t ldxs = fine ? ldxp : ldx;
       if (n <= 256 && !(ex.out32 && ex.add)) opt.pair = -1;
+      if (beside) opt.split_k = 1;  // of two k-blocks at most: the same sums on any number of SMs
       if (both) opt.max_ctas = sms - sms_x;
       st = by_vocab
                ? tg::gemm_extra(1, 0, g, xs, h.dW, h.V, h.D, parts * n, ldg, ldxs, h.lddw, ex, &opt,
@@ -715,12 +719,11 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       // blocks over the SMs (28672 x 1024 for one token 17 against 25 us as planned from the
       // products' costs and for 128 tokens 20.4 against 20.7, 131072 x 4096 166 against 203, 28672 x
       // 8192 for one token 77 against 119; two rows of tiles gain at some widths and lose at others).
-      // Narrow W: narrow tiles.
+      // Beside dW they make three waves over a third of the SMs.
       tg_options opt = gemm_opt;
-      const int64_t width = h.D <= 2048 ? 128 : 256;
-      const int64_t splits =
-          std::max(std::min({sms_x / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)}),
-                   cdiv(h.V, kSumLength));
+      const int64_t splits = std::max(
+          std::min({(beside ? 3 * sms_x : sms) / cdiv(h.D, width), cdiv(h.V, 128), int64_t(32)}),
+          cdiv(h.V, kSumLength));
       if (n <= 128 && splits > 1) {
         opt.pair = -1;
         opt.block_n = static_cast<int>(width);

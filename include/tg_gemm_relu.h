@@ -393,8 +393,7 @@ typedef struct {
  * or 256 tokens' by default; with several pieces, dW in float32; copies of X and W when they are not
  * 16-byte aligned with leading dimensions that are multiples of 8.
  * Up to 128 tokens, with both gradients of a large head, dW runs on a library stream beside dX and
- * joins `stream`; a call made under stream capture runs one after the other (dX may differ in its
- * last bit: its sum over V is split another way).
+ * joins `stream`; in a call made under stream capture they run one after the other, to the same bits.
  * The gradient of the logits is rounded to fp16 relative to the largest |dloss|: a row whose
  * |dloss| is below 2^-15 of that keeps fewer than 11 bits of its small probabilities.  Up to 64
  * tokens in one piece it is kept in two fp16 parts, with twice the bits.
