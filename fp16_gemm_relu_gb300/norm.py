@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import binding
-from .tensors import check, here, library, on, param_type, ptr, rows, stream_handle, vector
+from .tensors import check, here, library, on, param_type, ptr, rows, stream_handle, vector, written
 
 
 def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False, out=None,
@@ -21,7 +21,8 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False,
     column stride; ``gamma`` and ``beta`` are (N,) fp16 or float32, or None for 1 and 0.
 
     Returns y, or with ``stats`` (y, mean, rstd), mean and rstd float32 (M,) as
-    :func:`layer_norm_backward` takes them.  ``out`` may be a row-major (M, N) view, or x itself.
+    :func:`layer_norm_backward` takes them.  ``out`` may be a row-major (M, N) view, or x itself; autograd
+    sees that it was written, and refuses a backward pass that needs what it held before.
     Runs on ``stream`` (default: torch's current stream) and returns without synchronising.
     """
     ldx = rows(x, "x")
@@ -46,6 +47,7 @@ def layer_norm(x, gamma=None, beta=None, eps: float = 1e-5, stats: bool = False,
         if out.shape != x.shape or out.get_device() != dev:
             raise ValueError("out must be an (M, N) tensor on x's device")
         ldy = rows(out, "out")
+        written(out)
     mean = rstd = None
     if stats:
         mean = torch.empty(M, dtype=torch.float32, device=x.device)

@@ -48,6 +48,15 @@ def vector(t: torch.Tensor, n: int, index: int, name: str) -> None:
         raise ValueError(f"{name} must be a contiguous ({n},) tensor on x's device")
 
 
+def written(t: torch.Tensor) -> None:
+    """Tells autograd that a kernel writes to ``t``, as an in-place torch operation would.  A leaf that
+    wants its gradient is refused, as there."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out must not require a gradient: this call is not differentiable")
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def here(index: int, stream) -> bool:
     """Whether a call goes to torch's current stream of the current device."""
     return stream is None and index == _current_device()

@@ -1,0 +1,47 @@
+"""What autograd has to be told or has to refuse around the operators' kernels, which write tensors
+without torch knowing."""
+
+import pytest
+
+from fp16_gemm_relu_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import fp16_gemm_relu_gb300 as tg  # noqa: E402
+from fp16_gemm_relu_gb300 import autograd  # noqa: E402
+from tests.test_gpu_head_autograd import _built, leaf  # noqa: E402,F401
+
+
+def test_a_norm_over_a_saved_tensor_is_noticed():
+    # relu_matmul keeps its output for the mask of its backward pass
+    a, b = leaf(16, 32, seed=20), leaf(32, 64, seed=21)
+    c = autograd.relu_matmul(a, b)
+    with torch.no_grad():
+        tg.layer_norm(c, out=c)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        c.sum().backward()
+    # through a view of it too, and on another stream
+    for stream in (None, torch.cuda.Stream()):
+        c = autograd.relu_matmul(a, b)
+        tg.layer_norm(c.detach()[:8], out=c.detach()[:8], stream=stream)
+        torch.cuda.synchronize()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            c.sum().backward()
+    # and in grad mode it is refused, as torch refuses out= of a tensor that requires a gradient
+    c = autograd.relu_matmul(a, b)
+    with pytest.raises(ValueError):
+        tg.layer_norm(c, out=c)
+    c.sum().backward()
+    assert torch.isfinite(a.grad).all()
+
+
+def test_other_outputs_are_as_before():
+    x = leaf(4, 64, seed=22).detach()
+    want = tg.layer_norm(x)
+    out = torch.empty_like(x)
+    before = out._version
+    assert tg.layer_norm(x, out=out) is out and torch.equal(out, want) and out._version == before + 1
+    with torch.inference_mode():
+        out = torch.empty_like(x)
+        assert torch.equal(tg.layer_norm(x, out=out), want)
