@@ -11,10 +11,13 @@ Likewise layer normalisation and the losses of a linear head: layer_norm, linear
 linear_distillation.  The losses' forward pass is the loss alone and their backward pass the whole
 step (the logits are computed again, not kept); head.linear_cross_entropy_step and
 head.linear_distillation_step give loss and gradients in one call where the upstream gradient is
-known beforehand, a quarter of the products fewer.
+known beforehand, a quarter of the products fewer.  Their gradients cannot be differentiated again
+(that raises).
 """
 
 from __future__ import annotations
+
+import functools
 
 import torch
 
@@ -75,6 +78,33 @@ def relu_matmul(A: torch.Tensor, B: torch.Tensor) -> torch.Tensor:
     return ReluMatmul.apply(A, B)
 
 
+class _Refusal(torch.autograd.Function):
+    """Passes a gradient on; its own derivative raises."""
+
+    @staticmethod
+    def forward(ctx, marker, grad):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the gradients of this operator cannot be differentiated again")
+
+
+def _once(backward):
+    """For backward passes of kernels alone: under create_graph=True their results are marked, or a
+    second derivative would take them for constants.  (torch's once_differentiable marks them only when
+    the upstream gradient requires one, which a loss's does not.)"""
+    @functools.wraps(backward)
+    def run(ctx, *upstream):
+        with torch.no_grad():
+            grads = backward(ctx, *upstream)
+        if not torch.is_grad_enabled():
+            return grads
+        marker = torch.empty(0, requires_grad=True)
+        return tuple(None if g is None else _Refusal.apply(marker, g) for g in grads)
+    return run
+
+
 class LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gamma, beta, eps):
@@ -84,6 +114,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         x, gamma, mean, rstd = ctx.saved_tensors
         want = ctx.needs_input_grad
@@ -108,6 +139,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return head.linear_cross_entropy(x, weight, target, ignore_index, logit_scale, layout)
 
     @staticmethod
+    @_once
     def backward(ctx, dloss):
         x, weight, target = ctx.saved_tensors
         want = ctx.needs_input_grad
@@ -125,6 +157,7 @@ class LinearDistillation(torch.autograd.Function):
                                         layout)
 
     @staticmethod
+    @_once
     def backward(ctx, dloss):
         x, weight, teacher_index, teacher_logits = ctx.saved_tensors
         want = ctx.needs_input_grad

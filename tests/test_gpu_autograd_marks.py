@@ -45,3 +45,20 @@ def test_other_outputs_are_as_before():
     with torch.inference_mode():
         out = torch.empty_like(x)
         assert torch.equal(tg.layer_norm(x, out=out), want)
+
+
+@pytest.mark.parametrize("which", ["layer_norm", "linear_cross_entropy", "linear_distillation"])
+def test_second_derivatives_are_refused(which):
+    """Their backward kernels have no derivative: it must not come out as zero."""
+    x, w = leaf(6, 16, seed=23), leaf(40, 16, seed=24)
+    if which == "layer_norm":
+        total = autograd.layer_norm(x, leaf(16, seed=25)).float().square().sum()
+    elif which == "linear_cross_entropy":
+        total = autograd.linear_cross_entropy(x, w, torch.arange(6, device="cuda"))
+    else:
+        index = torch.arange(24, device="cuda").view(6, 4)
+        total = autograd.linear_distillation(x, w, index, leaf(6, 4, seed=26).detach())
+    (dx,) = torch.autograd.grad(total, x, create_graph=True)
+    assert torch.isfinite(dx).all()
+    with pytest.raises(RuntimeError):  # a gradient penalty beside the loss
+        (total + dx.float().square().sum()).backward()
