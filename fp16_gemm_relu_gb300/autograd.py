@@ -192,6 +192,9 @@ def linear_distillation(x: torch.Tensor, weight: torch.Tensor, teacher_index: to
                         reduction: str = "mean",
                         layout: int = TG_HEAD_VOCAB_MAJOR) -> torch.Tensor:
     """Differentiable distillation from a teacher's top logits (see head.linear_distillation); "mean" is
-    over the rows that have an entry.  Not multiplied by temperature squared."""
+    over the rows that have an entry.  Not multiplied by temperature squared.  The teacher gets no
+    gradient: ``teacher_logits`` that require one are refused (detach them)."""
+    if teacher_logits.requires_grad and torch.is_grad_enabled():
+        raise ValueError("teacher_logits must not require a gradient: there is none (detach them)")
     loss = LinearDistillation.apply(x, weight, teacher_index, teacher_logits, temperature, layout)
     return _reduce(loss, lambda: (teacher_index >= 0).any(1).sum(), reduction)

@@ -62,3 +62,14 @@ def test_second_derivatives_are_refused(which):
     assert torch.isfinite(dx).all()
     with pytest.raises(RuntimeError):  # a gradient penalty beside the loss
         (total + dx.float().square().sum()).backward()
+
+
+def test_a_teacher_that_wants_a_gradient_is_refused():
+    x, w, logits = leaf(6, 16, seed=27), leaf(40, 16, seed=28), leaf(6, 4, seed=29)
+    index = torch.arange(24, device="cuda").view(6, 4)
+    with pytest.raises(ValueError, match="detach"):
+        autograd.linear_distillation(x, w, index, logits)
+    autograd.linear_distillation(x, w, index, logits.detach()).backward()
+    assert torch.isfinite(x.grad).all() and logits.grad is None
+    with torch.no_grad():
+        assert torch.isfinite(autograd.linear_distillation(x, w, index, logits))
