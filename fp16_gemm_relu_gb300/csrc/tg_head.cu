@@ -398,13 +398,14 @@ constexpr int64_t kLeastRows = 8;
 // Up to so many tokens the products are bound by W's and dW's bytes, not by the tensor cores, and G is
 // kept in two fp16 parts (22 bits), as twice the rows of one product: with few rows its largest entries
 // may all round badly (the gradients' error 0.00032 of their size, with two parts 0.00021, which is
-// their own rounding to fp16; more tokens average to 0.0003).  It costs 1 to 3% of a step (64 tokens,
-// 28672 classes of 4096: 155 against 152 us).
+// their own rounding to fp16; more tokens average to 0.0003).  It costs up to 3% of a step (64 tokens,
+// 28672 classes of 4096: 160 against 155 us).
 constexpr int64_t kFineTokens = 64;
 // Columns of V that one accumulator sums for dX, tokens for dW.  The tensor core cuts off where it adds
 // (tg_head_kernel.cuh), so a long sum shrinks: dX over 65536 columns in one accumulator by 1.2e-4 of
-// itself, over 120000 by 2.2e-4, as much as its rounding to fp16.  More splits (or, for dW, pieces) are
-// added in float32.
+// itself, over 120000 by 2.2e-4, as much as its rounding to fp16, and by 2e-5 in accumulators of this
+// length.  More splits (or, for dW, pieces) are added in float32: 1 to 2% of a step (2048 tokens of 28672 x
+// 8192 in two splits 1862 us, in one 1830).
 constexpr int64_t kSumLength = 16384;
 // Without logits a token's scratch is its statistics: 1 GiB of them.
 constexpr int64_t kPieceStats = int64_t{1} << 27;

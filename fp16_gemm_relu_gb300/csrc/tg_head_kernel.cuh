@@ -6,9 +6,9 @@
 //
 //  - A tile's sum over the width is cut into segments of kSegK k-blocks (1024 columns).  The tensor
 //    core adds each instruction's 16 products to the float32 accumulator by cutting off, not by
-//    rounding, so a sum's error grows with its length and always towards zero: 8192 columns put
-//    4.5e-6 on a loss, in segments of 512 or 1024 columns 2e-7 (float32 sums by other means are off
-//    by about 1e-7, the loss's own arithmetic included).  So each segment starts
+//    rounding, so a sum's error grows with its length and always towards zero: 8192 columns in one
+//    piece put 4.5e-6 on a loss, in segments of 1024 columns 4e-7, which is also the error at 1024 or
+//    2048 columns in all (float32 sums by other means are off by about 1e-7).  So each segment starts
 //    from zero in one of the two TMEM accumulators, and the epilogue warps add it to running sums
 //    in registers, rounding to nearest, while the next segment runs in the other.  Segments of 512
 //    cost 1-3% more time than of 1024, those of 2048 save nothing further.

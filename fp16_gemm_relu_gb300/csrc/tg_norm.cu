@@ -33,7 +33,7 @@ namespace {
 // apart), so a block that takes every eighth row can work on aligned 16-byte blocks, `off` elements to
 // the left of the row's own chunks of eight, and keeps the same columns for all of them: nothing is
 // shifted, and only a row's first and last block need care.  4095 x 3073 forward 20 us, shifted 32,
-// backward 39 and 47; 4096 x 12287 59 and 100, 134 and 199.
+// backward 39 and 47; 4096 x 12287 60 and 100, 133 and 199.
 enum : int { kRowsAny = 0, kRowsAlike = 1, kRowsWhole = 2 };
 
 // 16 bytes of the 32 in (lo, hi), from byte s on (even, below 16).  s is the same for a row's
@@ -344,7 +344,7 @@ __device__ __forceinline__ f32x2 there(int col, int n) {
 
 // A row's first and last chunk may have elements that are not the row's: which of the eight are, as
 // bits for them as fp16 and as factors for them as pairs.  In shared memory, the same for all rows of
-// a block (8192 x 5001 backward 98 us; worked out at each read 106).
+// a block (8192 x 5001 backward 99 us; worked out at each read 106).
 struct Edges {
   uint4 bits[2];
   f32x2 in[2][4];
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(kLongThreads)
 }
 
 // Backward: a thread's part of dgamma and dbeta beside its elements does not fit its registers
-// (4096 x 20000 took 630 us so, spilling, against 190), and so these two have a pass of their own.
+// (4096 x 20000 took 630 us so, spilling, against 187), and so these two have a pass of their own.
 // A chunk of eight columns a thread (shifted where rows are not whole: element by element 315 us
 // against 106 for 4096 x 20001), a split of the rows a block; each split writes one partial row of
 // both.  It reads what the pass for dx also reads: 10 bytes an element in all, not 6.

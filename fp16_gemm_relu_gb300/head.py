@@ -1,5 +1,7 @@
 """Losses of a linear head over a large vocabulary, with their gradients, over the C ABI
-(tg_linear_cross_entropy_f16, tg_linear_distill_f16): the logits are never kept whole.
+(tg_linear_cross_entropy_f16, tg_linear_distill_f16).  A cross entropy alone keeps no logits.  A step,
+and distillation from a (D, V) weight, keep those of a piece of the tokens in the library's scratch: all
+of them up to 2^29 (float32, and with a gradient half as much again: 3 GB) unless ``piece_rows`` is less.
 
 ``x`` is (T, D) fp16; ``weight`` is (V, D) fp16, or (D, V) with ``layout=TG_HEAD_WIDTH_MAJOR``;
 losses and the log of the softmax's sum are float32 (T,).  The ``*_step`` functions compute the loss

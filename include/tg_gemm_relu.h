@@ -332,8 +332,8 @@ tg_status tg_gemm_relu_f16_splitk_noalloc(const void* A, const void* B, void* C,
  *  - Outputs must not overlap inputs, except where said.
  *  - Invalid arguments are found before anything is launched; TG_ERR_NO_WORKSPACE and TG_ERR_CUDA
  *    of the head's losses may come after part of a call is queued (its outputs are then undefined).
- *  - Rows are independent: a NaN or an infinity in a row of activations shows in that row's results
- *    (and in sums over the rows), not in another's.  A logit of +inf makes its row's lse, loss and
+ *  - Rows are independent: a NaN or an infinity in a row of activations, or as a row's dloss, shows in
+ *    that row's results (and in sums over the rows), not in another's.  A logit of +inf makes its row's lse, loss and
  *    gradient NaN.
  * ---------------------------------------------------------------------------------------
  */
@@ -389,14 +389,17 @@ typedef struct {
  * target: int64[T].  A row whose target is ignore_index has loss 0 and no gradient; any other
  * target outside [0, V) makes the row's loss and the gradients NaN.  dloss: float32[T], needed for
  * a gradient.  V, D >= 1; T == 0 writes only dW = 0.  logit_scale > 0.
- * Scratch: the logits (float32) and their gradient (fp16) of a piece of the tokens, 2^29 of them
- * or 256 tokens' by default; with several pieces, dW in float32; copies of X and W when they are not
+ * Scratch: without a gradient 8 bytes for each token and 64 to 128 columns of V.  With one, the
+ * logits (float32) and their gradient (fp16) of a piece of the tokens, all of them up to 2^29 logits
+ * (3 GB), else pieces of that or of 256 tokens by default; with several pieces (of at most 16384 tokens),
+ * dW in float32; the parts of dX's (and dW's) sums that are longer than 16384, in float32; copies of X and W when they are not
  * 16-byte aligned with leading dimensions that are multiples of 8.
  * Up to 128 tokens, with both gradients of a large head, dW runs on a library stream beside dX and
  * joins `stream`; in a call made under stream capture they run one after the other, to the same bits.
- * The gradient of the logits is rounded to fp16 relative to the largest |dloss|: a row whose
- * |dloss| is below 2^-15 of that keeps fewer than 11 bits of its small probabilities.  Up to 64
- * tokens in one piece it is kept in two fp16 parts, with twice the bits.
+ * The gradient of the logits is rounded to fp16 with the largest finite |dloss| as common factor: row t
+ * keeps 11 bits of the probabilities from 2^-29 max|dloss| / |dloss[t]| on, and below that a spacing of
+ * 2^-39 max|dloss|.  Up to 64 tokens in one piece it is kept in two fp16 parts: 22 bits of the large
+ * values, down to the same spacing.
  */
 tg_status tg_linear_cross_entropy_f16(const void* X, const void* W, const int64_t* target,
                                       int64_t ignore_index, float logit_scale, const float* dloss,
@@ -411,7 +414,8 @@ tg_status tg_linear_cross_entropy_f16(const void* X, const void* W, const int64_
  *     z = X W^T / temperature,   lse[t] = log sum_v exp z[t][v]
  *     loss[t] = sum_e q_e (log q_e - (z[t][teacher_index[t][e]] - lse[t]))
  * (the divergence of the student from the teacher's distribution over its kept tokens; 0 log 0 is
- * 0).  teacher_index: int64, teacher_logits: teacher_type, rows of ldt >= top entries each.  An
+ * 0).  Without a gradient the logits are stored too, by pieces, where W is D x V or top D > 2 V; else the
+ * entries' logits are dot products of their own.  teacher_index: int64, teacher_logits: teacher_type, rows of ldt >= top entries each.  An
  * entry with a negative index is not there; entries may be in any order, and entries of the same
  * token add up.  A row with no entry, or with all of them at -inf, has loss 0 and no gradient.  An
  * index >= V, or a teacher's logit of NaN or +inf, makes the row's loss and the gradients NaN.
