@@ -16,7 +16,7 @@
 // them); dX and dW through the ordinary GEMMs on G.  Tokens go in pieces that bound the logits'
 // scratch; dW is summed over the pieces in float32.
 //
-// G is rounded to fp16 once, the operand type of the products (kFineTokens: twice as fine).  So that the many small
+// G is rounded to fp16 once, the operand type of the products (kFineTokens: in two parts).  So that the many small
 // probabilities stay normal fp16 numbers, G carries the factor 2^15 / max|w| (|p - q| <= 1, so
 // nothing overflows) and alpha = s max|w| / 2^15 is applied to the float32 sums: a row of the
 // largest weight keeps 11 bits of every p above 2^-29.
