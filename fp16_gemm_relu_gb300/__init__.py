@@ -8,6 +8,11 @@ raises if the compiled library is missing.
 """
 
 from .binding import (  # noqa: F401
+    TG_ACT_GELU,
+    TG_ACT_GELU_TANH,
+    TG_ACT_NONE,
+    TG_ACT_RELU,
+    TG_ACT_SILU,
     TG_EPILOGUE_NONE,
     TG_EPILOGUE_RELU,
     TG_HEAD_VOCAB_MAJOR,
@@ -25,10 +30,16 @@ from .binding import (  # noqa: F401
     tg_release_workspace,
     tg_status_string,
 )
+from .clip import clip_gradients, gradient_norm  # noqa: F401
+from .gated import gated_linear, gated_linear_backward  # noqa: F401
 from .head import (  # noqa: F401
     linear_cross_entropy,
     linear_cross_entropy_step,
     linear_distillation,
     linear_distillation_step,
+    linear_policy,
+    linear_policy_step,
+    linear_preference,
+    linear_preference_step,
 )
 from .norm import layer_norm, layer_norm_backward  # noqa: F401

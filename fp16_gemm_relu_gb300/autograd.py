@@ -7,10 +7,11 @@ Backward: dZ = C > 0 ? dC : +0                        tg_relu_backward_f16
           dA = dZ·B^T  (fp32 accumulate, fp16 out)    tg_gemm_f16_t(trans_b = 1)
           dB = A^T·dZ                                  tg_gemm_f16_t(trans_a = 1)
 
-Likewise layer normalisation and the losses of a linear head: layer_norm, linear_cross_entropy and
-linear_distillation.  The losses' forward pass is the loss alone and their backward pass the whole
-step (the logits are computed again, not kept); head.linear_cross_entropy_step and
-head.linear_distillation_step give loss and gradients in one call where the upstream gradient is
+Likewise layer normalisation, the gated feed-forward product and the losses of a linear head: layer_norm,
+gated_linear, linear_cross_entropy, linear_distillation, linear_preference and linear_policy.  The
+losses' forward pass is the loss alone and their backward pass the whole
+step (the logits are computed again, not kept); head.linear_cross_entropy_step and the others' steps
+give loss and gradients in one call where the upstream gradient is
 known beforehand, a quarter of the products fewer.  Their gradients cannot be differentiated again
 (that raises).
 """
@@ -21,8 +22,8 @@ import functools
 
 import torch
 
-from . import binding, head, norm
-from .binding import TG_HEAD_VOCAB_MAJOR
+from . import binding, gated, head, norm
+from .binding import TG_ACT_SILU, TG_HEAD_VOCAB_MAJOR
 
 
 def _ld(t: torch.Tensor) -> int:
@@ -198,3 +199,104 @@ def linear_distillation(x: torch.Tensor, weight: torch.Tensor, teacher_index: to
         raise ValueError("teacher_logits must not require a gradient: there is none (detach them)")
     loss = LinearDistillation.apply(x, weight, teacher_index, teacher_logits, temperature, layout)
     return _reduce(loss, lambda: (teacher_index >= 0).any(1).sum(), reduction)
+
+
+class GatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, activation, trans_w):
+        if not any(ctx.needs_input_grad):
+            return gated.gated_linear(x, w_gate, w_up, activation, trans_w)
+        h, gate, up = gated.gated_linear(x, w_gate, w_up, activation, trans_w, keep=True)
+        ctx.save_for_backward(x, w_gate, w_up, gate, up)
+        ctx.args = (activation, trans_w)
+        return h
+
+    @staticmethod
+    @_once
+    def backward(ctx, dh):
+        x, w_gate, w_up, gate, up = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        dx, dwg, dwu = gated.gated_linear_backward(
+            dh.to(torch.float16).contiguous(), x, w_gate, w_up, gate, up, *ctx.args,
+            input_grad=want[0], weight_grads=want[1] or want[2])
+        return dx, dwg if want[1] else None, dwu if want[2] else None, None, None
+
+
+def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                 activation: int = TG_ACT_SILU, trans_w: bool = False) -> torch.Tensor:
+    """Differentiable act(x @ w_gate) * (x @ w_up) (see gated.gated_linear); keeps both pre-activations
+    in fp16 for the backward pass."""
+    return GatedLinear.apply(x, w_gate, w_up, activation, trans_w)
+
+
+def _constant(**tensors):
+    """Inputs that get no gradient must not ask for one."""
+    for name, t in tensors.items():
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} must not require a gradient: there is none (detach it)")
+
+
+class LinearPreference(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, target, offsets, reference, *args):
+        ctx.save_for_backward(x, weight, target, offsets, reference)
+        ctx.args = args
+        loss, ratios = head._preference(x, weight, target, offsets, None, False, False, reference,
+                                        *args, 0, None)[:2]
+        ctx.mark_non_differentiable(ratios)
+        return loss, ratios
+
+    @staticmethod
+    @_once
+    def backward(ctx, dloss, _):
+        x, weight, target, offsets, reference = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        _, _, dx, dw = head._preference(x, weight, target, offsets, dloss.contiguous(), want[0], want[1],
+                                        reference, *ctx.args, 0, None)
+        return (dx, dw) + (None,) * (3 + len(ctx.args))
+
+
+class LinearPolicy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, target, old, advantage, reference, *args):
+        ctx.save_for_backward(x, weight, target, old, advantage, reference)
+        ctx.args = args
+        loss, logp = head._policy(x, weight, target, old, advantage, None, False, False, reference,
+                                  *args, 0, None)[:2]
+        ctx.mark_non_differentiable(logp)
+        return loss, logp
+
+    @staticmethod
+    @_once
+    def backward(ctx, dloss, _):
+        x, weight, target, old, advantage, reference = ctx.saved_tensors
+        want = ctx.needs_input_grad
+        _, _, dx, dw = head._policy(x, weight, target, old, advantage, dloss.contiguous(), want[0],
+                                    want[1], reference, *ctx.args, 0, None)
+        return (dx, dw) + (None,) * (4 + len(ctx.args))
+
+
+def linear_preference(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
+                      offsets: torch.Tensor, reference=None, beta: float = 0.1,
+                      label_smoothing: float = 0.0, average: bool = False, ignore_index: int = -100,
+                      reduction: str = "mean", logit_scale: float = 1.0,
+                      layout: int = TG_HEAD_VOCAB_MAJOR):
+    """Differentiable (loss, ratios) of pairs of sequences (see head.linear_preference); "mean" is over the
+    pairs.  The ratios are for looking at: they have no gradient."""
+    _constant(reference=reference)
+    loss, ratios = LinearPreference.apply(x, weight, target, offsets, reference, beta, label_smoothing,
+                                          average, ignore_index, logit_scale, layout)
+    return _reduce(loss, lambda: torch.ones_like(loss).sum(), reduction), ratios
+
+
+def linear_policy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, old: torch.Tensor,
+                  advantage: torch.Tensor, reference=None, clip_low: float = 0.2,
+                  clip_high: float = 0.2, kl_weight: float = 0.0, ignore_index: int = -100,
+                  reduction: str = "mean", logit_scale: float = 1.0,
+                  layout: int = TG_HEAD_VOCAB_MAJOR):
+    """Differentiable (loss, logp) of a clipped policy (see head.linear_policy); "mean" is over the rows
+    whose target is not ignore_index.  logp has no gradient."""
+    _constant(old=old, advantage=advantage, reference=reference)
+    loss, logp = LinearPolicy.apply(x, weight, target, old, advantage, reference, clip_low, clip_high,
+                                    kl_weight, ignore_index, logit_scale, layout)
+    return _reduce(loss, lambda: (target != ignore_index).sum(), reduction), logp

@@ -40,6 +40,7 @@ class tg_epilogue(ctypes.Structure):
 
 
 TG_ACT_NONE, TG_ACT_RELU, TG_ACT_GELU, TG_ACT_GELU_TANH = 0, 1, 2, 3
+TG_ACT_SILU = 4  # the gated product's alone
 
 TG_TYPE_F16, TG_TYPE_F32 = 0, 1
 TG_NORM_MAX_WIDTH = 32768
@@ -51,6 +52,11 @@ class tg_head_options(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int), ("debug_flags", ctypes.c_int),
                 ("timeout_ms", ctypes.c_int), ("reserved", ctypes.c_int),
                 ("piece_rows", ctypes.c_int64)]
+
+
+class tg_gradient(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("type", ctypes.c_int), ("out_type", ctypes.c_int)]
 
 
 class tg_plan(ctypes.Structure):
@@ -120,6 +126,15 @@ def load_library() -> ctypes.CDLL:
                                                   [hp, vp])
         L.tg_linear_distill_f16.argtypes = ([vp] * 4 + [ci, ci, i64, cf] + [vp] * 5 + [i64] * 7 +
                                             [hp, vp])
+        L.tg_gated_f16.argtypes = ([vp] * 6 + [ci, ci] + [i64] * 9 +
+                                   [ctypes.POINTER(tg_options), vp])
+        L.tg_gated_backward_f16.argtypes = ([vp] * 9 + [ci, ci] + [i64] * 12 +
+                                            [ctypes.POINTER(tg_options), vp])
+        L.tg_linear_preference_f16.argtypes = ([vp, vp, vp, i64, cf, vp, i64, vp, cf, cf, ci] +
+                                               [vp] * 5 + [i64] * 7 + [hp, vp])
+        L.tg_linear_policy_f16.argtypes = ([vp, vp, vp, i64, cf, vp, vp, vp, cf, cf, cf] +
+                                           [vp] * 5 + [i64] * 7 + [hp, vp])
+        L.tg_clip_gradients.argtypes = [vp, i64, cf, cf, vp, vp]
         L.tg_plan_query.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i64, ci,
                                     ctypes.POINTER(tg_options), ctypes.POINTER(tg_plan)]
         L.tg_device_error_check.argtypes = [ctypes.POINTER(ctypes.c_uint), ci]
@@ -132,7 +147,9 @@ def load_library() -> ctypes.CDLL:
                      "tg_gemm_relu_f16_splitk_noalloc", "tg_gemm_f16_epilogue",
                      "tg_gemm_f16_t", "tg_relu_backward_f16", "tg_gemm_w4a16_f16",
                      "tg_gemm_nf4a16_f16", "tg_layernorm_f16", "tg_layernorm_backward_f16",
-                     "tg_linear_cross_entropy_f16", "tg_linear_distill_f16",
+                     "tg_linear_cross_entropy_f16", "tg_linear_distill_f16", "tg_gated_f16",
+                     "tg_gated_backward_f16", "tg_linear_preference_f16", "tg_linear_policy_f16",
+                     "tg_clip_gradients",
                      "tg_plan_query", "tg_device_error_check", "tg_last_cuda_error",
                      "tg_release_workspace", "tg_version"):
             getattr(L, name).restype = ci
@@ -259,6 +276,52 @@ def tg_linear_distill_f16(X: int, W: int, teacher_index: int, teacher_logits: in
         X, W, teacher_index, teacher_logits, teacher_type, top, ldt, temperature, dloss or None,
         loss or None, lse or None, dX or None, dW or None, T, V, D, ldx, ldw, lddx, lddw,
         _head_opts(options), stream or None)
+
+
+def tg_gated_f16(X: int, Wg: int, Wu: int, H: int, gate: int, up: int, activation: int, trans_w: int,
+                 M: int, N: int, K: int, ldx: int, ldwg: int, ldwu: int, ldh: int, ldgate: int = 0,
+                 ldup: int = 0, options=None, stream: int = 0) -> int:
+    return load_library().tg_gated_f16(X, Wg, Wu, H, gate or None, up or None, activation, trans_w, M,
+                                       N, K, ldx, ldwg, ldwu, ldh, ldgate, ldup, _opts(options),
+                                       stream or None)
+
+
+def tg_gated_backward_f16(dH: int, X: int, Wg: int, Wu: int, gate: int, up: int, dX: int, dWg: int,
+                          dWu: int, activation: int, trans_w: int, M: int, N: int, K: int, lddh: int,
+                          ldx: int, ldwg: int, ldwu: int, ldgate: int, ldup: int, lddx: int = 0,
+                          lddwg: int = 0, lddwu: int = 0, options=None, stream: int = 0) -> int:
+    return load_library().tg_gated_backward_f16(
+        dH, X, Wg, Wu, gate, up, dX or None, dWg or None, dWu or None, activation, trans_w, M, N, K,
+        lddh, ldx, ldwg, ldwu, ldgate, ldup, lddx, lddwg, lddwu, _opts(options), stream or None)
+
+
+def tg_linear_preference_f16(X: int, W: int, target: int, ignore_index: int, logit_scale: float,
+                             offsets: int, pairs: int, reference: int, beta: float,
+                             label_smoothing: float, average: int, dloss: int, loss: int, ratios: int,
+                             dX: int, dW: int, T: int, V: int, D: int, ldx: int, ldw: int,
+                             lddx: int = 0, lddw: int = 0, options=None, stream: int = 0) -> int:
+    return load_library().tg_linear_preference_f16(
+        X, W, target, ignore_index, logit_scale, offsets, pairs, reference or None, beta,
+        label_smoothing, average, dloss or None, loss or None, ratios or None, dX or None, dW or None,
+        T, V, D, ldx, ldw, lddx, lddw, _head_opts(options), stream or None)
+
+
+def tg_linear_policy_f16(X: int, W: int, target: int, ignore_index: int, logit_scale: float,
+                         old_logp: int, advantage: int, reference: int, clip_low: float,
+                         clip_high: float, kl_weight: float, dloss: int, loss: int, logp: int, dX: int,
+                         dW: int, T: int, V: int, D: int, ldx: int, ldw: int, lddx: int = 0,
+                         lddw: int = 0, options=None, stream: int = 0) -> int:
+    return load_library().tg_linear_policy_f16(
+        X, W, target, ignore_index, logit_scale, old_logp, advantage, reference or None, clip_low,
+        clip_high, kl_weight, dloss or None, loss or None, logp or None, dX or None, dW or None, T, V, D,
+        ldx, ldw, lddx, lddw, _head_opts(options), stream or None)
+
+
+def tg_clip_gradients(gradients, loss_scale: float, max_norm: float, norm: int, stream: int = 0) -> int:
+    """``gradients``: a sequence of :class:`tg_gradient`."""
+    n = len(gradients)
+    return load_library().tg_clip_gradients((tg_gradient * max(n, 1))(*gradients), n, loss_scale,
+                                            max_norm, norm, stream or None)
 
 
 def tg_gemm_relu_f16_host(hA: int, hB: int, hC: int, M: int, N: int, K: int, lda: int,

@@ -1,0 +1,253 @@
+// tg_gated.cu — the gated feed-forward product and its backward pass.
+//
+//   gate = X Wg,  up = X Wu  (M x N, float32),   H = act(gate) * up
+//   dG = dH * up * act'(gate),  dU = dH * act(gate)
+//   dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "tg_gated_kernel.cuh"
+#include "tg_gemm_relu.h"
+#include "tg_internal.h"
+
+namespace {
+
+using tg::gated_activation;
+using tg::gated_slope;
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+bool misaligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
+
+constexpr int64_t kMaxSize = (int64_t{1} << 30);
+constexpr int64_t kMaxLd = int64_t{1} << 36;
+
+// fp16 values of 8 columns from `col` on to a row, 16 bytes at once where the row allows it.
+__device__ __forceinline__ void store8(__half* row, int64_t col, int64_t n, const float (&v)[8]) {
+  __half* d = row + col;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  if (col + 8 <= n && (reinterpret_cast<uintptr_t>(d) & 15u) == 0) {
+    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < n)
+        reinterpret_cast<unsigned short*>(d)[i] = static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void load8(const __half* row, int64_t col, int64_t n, float (&v)[8]) {
+  const __half* s = row + col;
+  if (col + 8 <= n && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(s));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = col + i < n ? __half2float(s[i]) : 0.0f;
+  }
+}
+
+// H (and gate, up) from the float32 products, eight columns a thread.
+__global__ void __launch_bounds__(256)
+    tg_gated_combine_kernel(const float* gate32, const float* up32, int64_t ld32, int act,
+                            __half* h, int64_t ldh, __half* gate, int64_t ldg, __half* up,
+                            int64_t ldu, int64_t M, int64_t N) {
+  const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
+  if (c >= N) return;
+  for (int64_t r = blockIdx.y; r < M; r += gridDim.y) {
+    float g[8], u[8], v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {  // ld32 is a multiple of 32
+      const float4 a = *reinterpret_cast<const float4*>(gate32 + r * ld32 + c + i);
+      const float4 b = *reinterpret_cast<const float4*>(up32 + r * ld32 + c + i);
+      g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
+      u[i] = b.x, u[i + 1] = b.y, u[i + 2] = b.z, u[i + 3] = b.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = gated_activation(g[i], act) * u[i];
+    store8(h + r * ldh, c, N, v);
+    if (gate) store8(gate + r * ldg, c, N, g);
+    if (up) store8(up + r * ldu, c, N, u);
+  }
+}
+
+// dG and dU (fp16, M x np each, rows of ld; zeros from column N on), eight columns a thread.
+__global__ void __launch_bounds__(256)
+    tg_gated_grad_kernel(const __half* __restrict__ dh, int64_t lddh, const __half* __restrict__ gate,
+                         int64_t ldg, const __half* __restrict__ up, int64_t ldu, int act,
+                         __half* out, int64_t ld, int64_t np, int64_t M, int64_t N, float* one) {
+  if (one && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *one = 1.0f;
+  const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
+  if (c >= np) return;
+  for (int64_t r = blockIdx.y; r < M; r += gridDim.y) {
+    float d[8], g[8], u[8], dg[8], du[8];
+    load8(dh + r * lddh, c, N, d);
+    load8(gate + r * ldg, c, N, g);
+    load8(up + r * ldu, c, N, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dg[i] = d[i] * (u[i] * gated_slope(g[i], act));
+      du[i] = d[i] * gated_activation(g[i], act);
+    }
+    store8(out + r * ld, c, np, dg);
+    store8(out + r * ld + np, c, np, du);
+  }
+}
+
+dim3 row_grid(int64_t cols, int64_t rows) {
+  return dim3(static_cast<unsigned>(cdiv(cols, 2048)),
+              static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(rows, 1), 65535)));
+}
+
+struct Gated {
+  const void *X, *Wg, *Wu;
+  int act, trans;
+  int64_t M, N, K, ldx, ldwg, ldwu;
+};
+
+bool bad_ld(int64_t ld, int64_t n) { return ld < n || ld > kMaxLd; }
+
+tg_status check(const Gated& a) {
+  if (a.M < 0 || a.N < 1 || a.K < 1 || a.M > kMaxSize || a.N > kMaxSize || a.K > kMaxSize)
+    return TG_ERR_INVALID_ARG;
+  if (a.act < TG_ACT_NONE || a.act > TG_ACT_SILU || (a.trans != 0 && a.trans != 1))
+    return TG_ERR_INVALID_ARG;
+  const int64_t row = a.trans ? a.K : a.N;
+  if (bad_ld(a.ldx, a.K) || bad_ld(a.ldwg, row) || bad_ld(a.ldwu, row)) return TG_ERR_INVALID_ARG;
+  if (a.M > 0 && (!a.X || !a.Wg || !a.Wu)) return TG_ERR_INVALID_ARG;
+  if (misaligned(a.X, 2) || misaligned(a.Wg, 2) || misaligned(a.Wu, 2)) return TG_ERR_MISALIGNED;
+  return TG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, void* gate, void* up,
+                       int activation, int trans_w, int64_t M, int64_t N, int64_t K, int64_t ldx,
+                       int64_t ldwg, int64_t ldwu, int64_t ldh, int64_t ldgate, int64_t ldup,
+                       const tg_options* opt, tg_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const Gated a{X, Wg, Wu, activation, trans_w, M, N, K, ldx, ldwg, ldwu};
+  tg_status st = check(a);
+  if (st != TG_OK) return st;
+  if (bad_ld(ldh, N) || (gate && bad_ld(ldgate, N)) || (up && bad_ld(ldup, N)))
+    return TG_ERR_INVALID_ARG;
+  if (M == 0) return TG_OK;
+  if (!H) return TG_ERR_INVALID_ARG;
+  if (misaligned(H, 2) || misaligned(gate, 2) || misaligned(up, 2)) return TG_ERR_MISALIGNED;
+  const int64_t ld32 = round_up(N, 32);
+  float* mem = nullptr;
+  if ((st = tg::scratch_alloc(size_t(2 * M * ld32 * 4), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
+    return st;
+  tg::GemmExtra ex;
+  std::memset(&ex, 0, sizeof(ex));
+  ex.ld32 = ld32;
+  for (int i = 0; i < 2 && st == TG_OK; ++i) {
+    ex.out32 = mem + i * M * ld32;
+    st = tg::gemm_extra(0, trans_w, X, i ? Wu : Wg, nullptr, M, N, K, ldx, i ? ldwu : ldwg, N, ex, opt,
+                        stream);
+  }
+  if (st == TG_OK) {
+    tg_gated_combine_kernel<<<row_grid(N, M), 256, 0, stream>>>(
+        mem, mem + M * ld32, ld32, activation, static_cast<__half*>(H), ldh,
+        static_cast<__half*>(gate), ldgate, static_cast<__half*>(up), ldup, M, N);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) st = tg::record_cuda_error(e);
+  }
+  const cudaError_t fe = cudaFreeAsync(mem, stream);
+  return st == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : st;
+}
+
+tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, const void* Wu,
+                                const void* gate, const void* up, void* dX, void* dWg, void* dWu,
+                                int activation, int trans_w, int64_t M, int64_t N, int64_t K,
+                                int64_t lddh, int64_t ldx, int64_t ldwg, int64_t ldwu, int64_t ldgate,
+                                int64_t ldup, int64_t lddx, int64_t lddwg, int64_t lddwu,
+                                const tg_options* opt, tg_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const Gated a{X, Wg, Wu, activation, trans_w, M, N, K, ldx, ldwg, ldwu};
+  tg_status st = check(a);
+  if (st != TG_OK) return st;
+  const int64_t w_rows = trans_w ? N : K, w_cols = trans_w ? K : N;
+  if (bad_ld(lddh, N) || bad_ld(ldgate, N) || bad_ld(ldup, N) || (dX && bad_ld(lddx, K)) ||
+      (dWg && bad_ld(lddwg, w_cols)) || (dWu && bad_ld(lddwu, w_cols)))
+    return TG_ERR_INVALID_ARG;
+  if (M > 0 && (!dH || !gate || !up)) return TG_ERR_INVALID_ARG;
+  if (misaligned(dH, 2) || misaligned(gate, 2) || misaligned(up, 2) || misaligned(dX, 2) ||
+      misaligned(dWg, 2) || misaligned(dWu, 2))
+    return TG_ERR_MISALIGNED;
+  if (!dX && !dWg && !dWu) return TG_OK;
+  cudaError_t e;
+  if (M == 0) {  // the sum over no rows
+    int sms = 0;
+    unsigned* err = nullptr;
+    if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
+    for (int i = 0; i < 2; ++i) {
+      void* d = i ? dWu : dWg;
+      if (!d) continue;
+      e = cudaMemset2DAsync(d, size_t(i ? lddwu : lddwg) * 2, 0, size_t(w_cols) * 2, size_t(w_rows), stream);
+      if (e != cudaSuccess) return tg::record_cuda_error(e);
+    }
+    return TG_OK;
+  }
+  const int64_t np = round_up(N, 128), ld = 2 * np, ld32 = round_up(K, 32);
+  const int64_t at_32 = round_up(M * ld * 2, 256), at_one = at_32 + (dX ? M * ld32 * 4 : 0);
+  uint8_t* mem = nullptr;
+  if ((st = tg::scratch_alloc(size_t(at_one + 256), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
+    return st;
+  auto done = [&](tg_status s) {
+    const cudaError_t fe = cudaFreeAsync(mem, stream);
+    return s == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : s;
+  };
+  __half* g = reinterpret_cast<__half*>(mem);
+  float* sum = reinterpret_cast<float*>(mem + at_32);
+  float* one = reinterpret_cast<float*>(mem + at_one);
+  tg_gated_grad_kernel<<<row_grid(np, M), 256, 0, stream>>>(
+      static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
+      static_cast<const __half*>(up), ldup, activation, g, ld, np, M, N, one);
+  if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
+  tg::GemmExtra ex;
+  for (int i = 0; i < 2; ++i) {
+    void* d = i ? dWu : dWg;
+    if (!d) continue;
+    const void* gi = g + i * np;
+    const int64_t ldd = i ? lddwu : lddwg;
+    std::memset(&ex, 0, sizeof(ex));
+    st = trans_w ? tg::gemm_extra(1, 0, gi, X, d, N, K, M, ld, ldx, ldd, ex, opt, stream)
+                 : tg::gemm_extra(1, 0, X, gi, d, K, N, M, ldx, ld, ldd, ex, opt, stream);
+    if (st != TG_OK) return done(st);
+  }
+  if (dX) {
+    std::memset(&ex, 0, sizeof(ex));
+    ex.out32 = sum;
+    ex.ld32 = ld32;
+    st = tg::gemm_extra(0, !trans_w, g, Wg, nullptr, M, K, N, ld, ldwg, K, ex, opt, stream);
+    if (st != TG_OK) return done(st);
+    std::memset(&ex, 0, sizeof(ex));
+    ex.alpha = one;
+    ex.addend = sum;
+    ex.ld32 = ld32;
+    st = tg::gemm_extra(0, !trans_w, g + np, Wu, dX, M, K, N, ld, ldwu, lddx, ex, opt, stream);
+    if (st != TG_OK) return done(st);
+  }
+  return done(TG_OK);
+}
+
+}  // extern "C"

@@ -378,6 +378,175 @@ __global__ void __launch_bounds__(128)
   }
 }
 
+// A preference's or a policy's loss is a function of the targets' log probabilities logp_t = -nll_t, nll
+// the cross entropy of tg_head_rows_kernel: the kernels below take those to the losses and to each row's
+// weight w_t = d total / d nll_t, from which G follows as for cross entropy.
+struct Objective {
+  int kind;                  // 0: none, else kPreference or kPolicy
+  const float* dloss;        // [pairs] or [T]: d total / d loss (NULL: no gradient)
+  float* loss;               // [pairs] or [T], NULL: not wanted
+  const float* reference;    // [T] log probabilities; NULL: 0 (preference), no penalty (policy)
+  // preference: pair p is the rows [offsets[2p], offsets[2p + 1]) and from there to offsets[2p + 2]
+  const int64_t* offsets;
+  int64_t pairs;
+  float beta, smooth;
+  int average;
+  float* ratios;             // [pairs][2], NULL: not wanted
+  // policy
+  const float *old, *advantage;
+  float low, high, kl;       // the ratio's borders, and the penalty's weight
+  float* logp;               // [T], NULL: not wanted
+};
+enum : int { kPreference = 1, kPolicy = 2 };
+
+// What the kernels of an objective share: max|w| over the rows as for cross entropy, whether any pair's
+// offsets are wrong, and (preference) the weight of a counted row of each sequence.
+struct Shared {
+  unsigned* wmax;
+  int* bad;
+  float* coef;  // [2 pairs]
+};
+
+// Bits of |w| where it is finite, else 0: see tg_head_weight_kernel.
+__device__ __forceinline__ unsigned weight_bits(float w) {
+  return fabsf(w) < INFINITY ? __float_as_uint(fabsf(w)) : 0u;
+}
+
+constexpr int kPairThreads = 256;
+__device__ __forceinline__ double block_sum(double v, double* slots) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+  for (int i = 0; i < kPairThreads / 32; ++i) v += slots[i];
+  return v;
+}
+
+// A block a pair (Rafailov et al., 2023, with smoothed labels):
+//   r_s = sum over a sequence's counted rows of logp - reference (average: their mean; none: 0)
+//   m = beta (r_chosen - r_rejected),   loss = -(1 - e) log sigma(m) - e log sigma(-m)
+// The sums are float64: those of a long answer are large and nearly the same in both.
+__global__ void __launch_bounds__(kPairThreads)
+    tg_head_pairs_kernel(Objective ob, const float* nll, const int64_t* __restrict__ target,
+                         int64_t ignore, int64_t rows, Shared sh) {
+  __shared__ double slots[4][kPairThreads / 32];
+  const int64_t p = blockIdx.x;
+  tg::chain_wait();
+  tg::chain_release();
+  const int64_t o[3] = {ob.offsets[2 * p], ob.offsets[2 * p + 1], ob.offsets[2 * p + 2]};
+  const bool fits = o[0] >= 0 && o[0] <= o[1] && o[1] <= o[2] && o[2] <= rows;
+  double r[2], n[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    double sum = 0.0, count = 0.0;
+    for (int64_t t = o[s] + threadIdx.x; fits && t < o[s + 1]; t += kPairThreads) {
+      if (target[t] == ignore) continue;
+      sum -= nll[t];
+      if (ob.reference) sum -= ob.reference[t];
+      count += 1.0;
+    }
+    sum = block_sum(sum, slots[2 * s]);
+    n[s] = block_sum(count, slots[2 * s + 1]);
+    if (!ob.average || n[s] < 1.0) n[s] = 1.0;
+    r[s] = sum / n[s];
+  }
+  if (threadIdx.x != 0) return;
+  const float m = static_cast<float>(ob.beta * (r[0] - r[1]));
+  const float away = expf(-fabsf(m)), soft = log1pf(away);       // log(1 + e^-|m|)
+  const float sigma = (m > 0.0f ? away : 1.0f) / (1.0f + away);  // sigma(-m)
+  float loss = (1.0f - ob.smooth) * (soft + fmaxf(-m, 0.0f)) + ob.smooth * (soft + fmaxf(m, 0.0f));
+  if (!fits || m != m) loss = NAN;
+  if (ob.loss) ob.loss[p] = loss;
+  if (ob.ratios) {
+    ob.ratios[2 * p] = fits ? static_cast<float>(r[0]) : NAN;
+    ob.ratios[2 * p + 1] = fits ? static_cast<float>(r[1]) : NAN;
+  }
+  if (!ob.dloss) return;
+  if (!fits) *sh.bad = 1;
+  // d loss / d m = e - sigma(-m), and w is the slope along nll
+  const float slope = ob.beta * (sigma - ob.smooth) * ob.dloss[p];
+  const float w[2] = {static_cast<float>(slope / n[0]), static_cast<float>(-slope / n[1])};
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    sh.coef[2 * p + s] = w[s];
+    if (fits && o[s + 1] > o[s]) atomicMax(sh.wmax, weight_bits(w[s]));
+  }
+}
+
+// A thread a row (Schulman et al., 2017; the penalty's unbiased, never negative estimate is Schulman's
+// of 2020):
+//   r = exp(logp - old),   loss = -min(r A, clip(r, low, high) A) + kl (e^d - d - 1),  d = reference - logp
+// The slope along logp is -r A where the first is the smaller, else 0, and kl (1 - e^d).  Comparisons
+// are such that a NaN goes through.
+__global__ void __launch_bounds__(256)
+    tg_head_policy_kernel(Objective ob, const float* nll, const int64_t* __restrict__ target,
+                          int64_t ignore, int64_t rows, float* w, Shared sh) {
+  const int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+  tg::chain_wait();
+  tg::chain_release();
+  unsigned most = 0;
+  if (r < rows) {
+    float loss = 0.0f, logp = 0.0f, slope = 0.0f;
+    if (target[r] != ignore) {
+      logp = -nll[r];
+      const float ratio = expf(logp - ob.old[r]), adv = ob.advantage[r];
+      const float kept = ratio < ob.low ? ob.low : ratio > ob.high ? ob.high : ratio;
+      const float a = ratio * adv, b = kept * adv;
+      const bool clipped = a > b;
+      loss = clipped ? -b : -a;
+      slope = clipped ? 0.0f : -a;
+      if (ob.kl > 0.0f) {
+        const float d = ob.reference[r] - logp, e = expm1f(d);
+        loss += ob.kl * (e - d);
+        slope -= ob.kl * e;
+      }
+    }
+    if (ob.loss) ob.loss[r] = loss;
+    if (ob.logp) ob.logp[r] = logp;
+    if (ob.dloss) {
+      w[r] = target[r] != ignore ? -slope * ob.dloss[r] : 0.0f;
+      most = weight_bits(w[r]);
+    }
+  }
+  if (!ob.dloss) return;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((threadIdx.x & 31) == 0 && most) atomicMax(sh.wmax, most);
+}
+
+// The rows' weights: from `w` (policy), or from their sequence's (preference; 0 outside of all of them).
+// With info: the factor of each counted row of G and alpha, as tg_head_rows_kernel gives them.  Without:
+// the weights themselves into w_out.
+__global__ void __launch_bounds__(256)
+    tg_head_factor_kernel(Objective ob, const int64_t* __restrict__ target, int64_t ignore,
+                          int64_t rows, const float* w, Shared sh, float scale, RowInfo* info,
+                          float* alpha, float* w_out) {
+  const int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
+  tg::chain_wait();
+  tg::chain_release();
+  const float most = __uint_as_float(*sh.wmax);
+  if (alpha && r == 0) *alpha = scale * most / kGScale;
+  if (r >= rows) return;
+  float v = 0.0f;
+  if (w) {
+    v = w[r];
+  } else if (*sh.bad) {
+    v = NAN;
+  } else if (target[r] != ignore && ob.pairs > 0 && r >= ob.offsets[0] && r < ob.offsets[2 * ob.pairs]) {
+    int64_t lo = 0, hi = 2 * ob.pairs - 1;  // the last sequence that begins at or before r
+    while (lo < hi) {
+      const int64_t mid = (lo + hi + 1) >> 1;
+      if (ob.offsets[mid] <= r)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    v = sh.coef[lo];
+  }
+  if (w_out) w_out[r] = v;
+  if (info && info[r].target >= 0) info[r].gs = row_factor(v, most);
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 bool misaligned(const void* p, unsigned bytes) {
@@ -460,6 +629,7 @@ struct Head {
   int64_t T, V, D, ldx, ldw, lddx, lddw;
   float scale;
   tg_head_options o;
+  Objective ob;          // kind 0: the losses themselves
 };
 
 // Parts of one scratch block, each 256-byte aligned.
@@ -489,13 +659,34 @@ tg_status check(const Head& h) {
     return TG_ERR_INVALID_ARG;
   if (h.T > 0) {
     if (!h.X || !h.W || !h.index || (h.top > 0 && !h.teacher)) return TG_ERR_INVALID_ARG;
-    if ((h.dX || h.dW) && !h.dloss) return TG_ERR_INVALID_ARG;
+    if ((h.dX || h.dW) && h.ob.kind == 0 && !h.dloss) return TG_ERR_INVALID_ARG;
   }
   if (misaligned(h.X, 2) || misaligned(h.W, 2) || misaligned(h.dX, 2) || misaligned(h.dW, 2) ||
       misaligned(h.index, 8) || misaligned(h.teacher, h.teacher_f32 ? 4 : 2) ||
       misaligned(h.dloss, 4) || misaligned(h.loss, 4) || misaligned(h.lse, 4))
     return TG_ERR_MISALIGNED;
   return TG_OK;
+}
+
+// Tokens whose logits (or statistics, per_row of either) are in scratch at a time.
+int64_t piece_of(const Head& h, int64_t per_row, int64_t budget) {
+  if (h.o.piece_rows)
+    return std::min({h.o.piece_rows, h.T, std::max<int64_t>(kMaxElements / per_row, 1)});
+  if (h.T <= budget / per_row) return h.T;
+  const int64_t most = std::max<int64_t>(budget / per_row / 256 * 256, 256);
+  return std::min(h.T, round_up(cdiv(h.T, cdiv(h.T, most)), 256));
+}
+
+// An objective's losses and weights from nll (chained: the launch before it is a kernel).
+cudaError_t launch_objective(const Head& h, const float* nll, float* w, const Shared& sh, bool chained,
+                             cudaStream_t stream) {
+  const Objective& ob = h.ob;
+  if (ob.kind == kPolicy)
+    return tg::launch_chained(tg_head_policy_kernel, chained, dim3(static_cast<unsigned>(cdiv(h.T, 256))),
+                              256, 0, stream, ob, nll, h.index, h.ignore, h.T, w, sh);
+  if (ob.pairs == 0) return cudaSuccess;
+  return tg::launch_chained(tg_head_pairs_kernel, chained, dim3(static_cast<unsigned>(ob.pairs)),
+                            kPairThreads, 0, stream, ob, nll, h.index, h.ignore, h.T, sh);
 }
 
 tg_status run_head(const Head& h, cudaStream_t stream) {
@@ -521,17 +712,11 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const bool store = grad || (h.top > 0 && !pick);
   const int64_t ldz = round_up(h.V, 32), ldg = round_up(h.V, 64);
   const int64_t tiles = 2 * cdiv(h.V, 128);  // statistics of a row, at most
-  const int64_t per_row = store ? ldz : tiles, budget = store ? kPieceLogits : kPieceStats;
-  int64_t piece = h.T;
-  if (h.o.piece_rows) {
-    piece = std::min({h.o.piece_rows, h.T, std::max<int64_t>(kMaxElements / per_row, 1)});
-  } else if (h.T > budget / per_row) {
-    const int64_t most = std::max<int64_t>(budget / per_row / 256 * 256, 256);
-    piece = std::min(h.T, round_up(cdiv(h.T, cdiv(h.T, most)), 256));
-  }
+  int64_t piece = piece_of(h, store ? ldz : tiles, store ? kPieceLogits : kPieceStats);
   if (h.dW && piece < h.T) piece = std::min(piece, kSumLength);
   const bool sum_w = h.dW && piece < h.T;  // dW is summed over pieces in float32
   const bool fine = grad && h.T <= kFineTokens && piece == h.T;
+  const bool objective = h.ob.kind != 0;  // with a gradient and in one piece (run_objective)
   const int64_t parts = fine ? 2 : 1;  // of G
 
   Layout lay;
@@ -544,7 +729,9 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const int64_t at_stats = lay.add(tiles * piece * int64_t(sizeof(float2)));
   const int64_t at_picked = lay.add(store ? 0 : piece * std::max(h.top, 1) * 4);
   const int64_t at_info = lay.add(piece * int64_t(sizeof(RowInfo)));
-  const int64_t at_small = lay.add(2 * 4);
+  const int64_t at_small = lay.add(3 * 4);
+  const int64_t at_nll = lay.add(objective ? h.T * 4 : 0);
+  const int64_t at_weights = lay.add(objective ? std::max(h.T, 2 * h.ob.pairs) * 4 : 0);
   const int64_t at_g = lay.add(grad ? std::max(parts * piece, kLeastRows) * ldg * 2 : 0);
   const int64_t at_x2 = lay.add(fine && h.dW ? 2 * h.T * ldxp * 2 : 0);
   const int64_t at_q = lay.add(grad && h.top ? piece * h.top * 4 : 0);
@@ -585,7 +772,10 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     W = mem + at_w;
     ldw = ldwp;
   }
-  if (grad) {
+  if (objective) {
+    if ((e = cudaMemsetAsync(wmax, 0, 3 * 4, stream)) != cudaSuccess)
+      return done(tg::record_cuda_error(e));
+  } else if (grad) {
     // one block for what it can read in a few microseconds, else several on a zeroed maximum
     const int64_t reads = h.T * std::max(h.top, 1);
     const int blocks = reads <= 4096 ? 1 : static_cast<int>(std::min<int64_t>(cdiv(h.T, 256), sms));
@@ -615,8 +805,9 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     const void* teacher = h.teacher == nullptr ? nullptr
                                                : static_cast<const uint8_t*>(h.teacher) +
                                                      t0 * h.ldt * (h.teacher_f32 ? 4 : 2);
-    const float* dloss = grad ? h.dloss + t0 : nullptr;
-    float* loss = h.loss ? h.loss + t0 : nullptr;
+    const float* dloss = grad && !objective ? h.dloss + t0 : nullptr;
+    float* nll = reinterpret_cast<float*>(mem + at_nll);
+    float* loss = objective ? nll : h.loss ? h.loss + t0 : nullptr;
     tg::GemmExtra ex;
     int block_n = 0;
     tg::LogitsExtra lx;
@@ -630,7 +821,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
     if (h.T < kLeastRows) ex.a_rows = kLeastRows - t0;
-    ex.chained = grad || copy_x || copy_w || t0 > 0;
+    ex.chained = !objective && (grad || copy_x || copy_w || t0 > 0);  // objective: a memset is before it
     st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &gemm_opt,
                         stream);
     if (st != TG_OK) return done(st);
@@ -642,9 +833,19 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
             static_cast<int>(h.D), picked);
     chain(tg_head_rows_kernel, dim3(static_cast<unsigned>(n)), kRowThreads,
         stats, static_cast<int>(2 * cdiv(h.V, block_n)), Logits{z, ldz, picked}, h.scale, h.V, index, h.ignore,
-        teacher, h.teacher_f32, h.ldt, h.top, dloss, wmax, loss, h.lse ? h.lse + t0 : nullptr, info,
-        q, alpha);
+        teacher, h.teacher_f32, h.ldt, h.top, dloss, objective ? nullptr : wmax, loss,
+        h.lse ? h.lse + t0 : nullptr, info, q, objective ? nullptr : alpha);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
+    if (objective) {
+      float* weights = reinterpret_cast<float*>(mem + at_weights);
+      const Shared sh{wmax, reinterpret_cast<int*>(wmax) + 2, weights};
+      const bool policy = h.ob.kind == kPolicy;
+      if ((e = launch_objective(h, nll, weights, sh, true, stream)) != cudaSuccess)
+        return done(tg::record_cuda_error(e));
+      chain(tg_head_factor_kernel, dim3(static_cast<unsigned>(cdiv(h.T, 256))), 256, h.ob, h.index,
+            h.ignore, h.T, policy ? weights : nullptr, sh, h.scale, info, alpha, nullptr);
+      if (e != cudaSuccess) return done(tg::record_cuda_error(e));
+    }
     if (!grad) continue;
     const int64_t lo = fine ? n * ldg : 0;
     uint16_t* x2 = fine && h.dW ? reinterpret_cast<uint16_t*>(mem + at_x2) : nullptr;
@@ -748,6 +949,72 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   return done(TG_OK);
 }
 
+// A preference or policy loss.  The logits of all tokens fit into one piece: one product, the losses,
+// and the gradient from the kept logits.  Else (and without a gradient) the log probabilities first,
+// which keep no logits, then the losses, then cross entropy's gradient with the weights found: one
+// product more.
+tg_status run_objective(const Head& h, cudaStream_t stream) {
+  tg_status st = check(h);
+  if (st != TG_OK) return st;
+  const Objective& ob = h.ob;
+  const bool grad = h.dX || h.dW;
+  if (ob.kind == kPreference) {
+    if (ob.pairs < 0 || ob.pairs > kMaxRows / 2 || (ob.pairs > 0 && !ob.offsets)) return TG_ERR_INVALID_ARG;
+    if (!(ob.beta > 0.0f) || !(ob.beta <= 3.0e38f) || !(ob.smooth >= 0.0f) || !(ob.smooth < 1.0f))
+      return TG_ERR_INVALID_ARG;
+    if (ob.pairs > 0 && grad && !ob.dloss) return TG_ERR_INVALID_ARG;
+  } else {
+    if (!(ob.low >= 0.0f) || !(ob.low <= 1.0f) || !(ob.high >= 1.0f) || !(ob.high <= 3.0e38f) ||
+        !(ob.kl >= 0.0f) || !(ob.kl <= 3.0e38f))
+      return TG_ERR_INVALID_ARG;
+    if (h.T > 0 && (!ob.old || !ob.advantage || (ob.kl > 0.0f && !ob.reference) || (grad && !ob.dloss)))
+      return TG_ERR_INVALID_ARG;
+  }
+  if (misaligned(ob.dloss, 4) || misaligned(ob.loss, 4) || misaligned(ob.reference, 4) ||
+      misaligned(ob.offsets, 8) || misaligned(ob.ratios, 4) || misaligned(ob.old, 4) ||
+      misaligned(ob.advantage, 4) || misaligned(ob.logp, 4))
+    return TG_ERR_MISALIGNED;
+  if (grad && h.T > 0 && piece_of(h, round_up(h.V, 32), kPieceLogits) == h.T) return run_head(h, stream);
+  if (h.T == 0 && ob.kind == kPolicy) return run_head(h, stream);
+  int sms = 0;
+  unsigned* err = nullptr;
+  if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
+  Layout lay;
+  const int64_t at_nll = lay.add(h.T * 4), at_w = lay.add(grad ? h.T * 4 : 0);
+  const int64_t at_coef = lay.add(grad ? 2 * ob.pairs * 4 : 0), at_small = lay.add(3 * 4);
+  uint8_t* mem = nullptr;
+  if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
+    return st;
+  float* nll = reinterpret_cast<float*>(mem + at_nll);
+  float* w = reinterpret_cast<float*>(mem + at_w);
+  const Shared sh{reinterpret_cast<unsigned*>(mem + at_small), reinterpret_cast<int*>(mem + at_small) + 2,
+                  reinterpret_cast<float*>(mem + at_coef)};
+  cudaError_t e = cudaMemsetAsync(sh.wmax, 0, 3 * 4, stream);
+  if (e != cudaSuccess) st = tg::record_cuda_error(e);
+  Head inner = h;
+  inner.ob.kind = 0;
+  inner.loss = nll;
+  inner.dX = inner.dW = nullptr;
+  if (st == TG_OK) st = run_head(inner, stream);
+  if (st == TG_OK) {
+    e = launch_objective(h, nll, w, sh, false, stream);
+    if (e == cudaSuccess && grad && ob.kind == kPreference && h.T > 0)
+      e = tg::launch_chained(tg_head_factor_kernel, ob.pairs > 0, dim3(static_cast<unsigned>(cdiv(h.T, 256))), 256,
+                             0, stream, ob, h.index, h.ignore, h.T, nullptr, sh, h.scale, nullptr,
+                             nullptr, w);
+    if (e != cudaSuccess) st = tg::record_cuda_error(e);
+  }
+  if (st == TG_OK && grad) {
+    inner = h;
+    inner.ob.kind = 0;
+    inner.loss = nullptr;
+    inner.dloss = w;
+    st = run_head(inner, stream);
+  }
+  e = cudaFreeAsync(mem, stream);
+  return st == TG_OK && e != cudaSuccess ? tg::record_cuda_error(e) : st;
+}
+
 tg_head_options options_or_default(const tg_head_options* opt) {
   tg_head_options o;
   std::memset(&o, 0, sizeof(o));
@@ -810,6 +1077,70 @@ tg_status tg_linear_distill_f16(const void* X, const void* W, const int64_t* tea
   h.scale = 1.0f / temperature;
   h.o = options_or_default(opt);
   return run_head(h, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tg_status tg_linear_preference_f16(const void* X, const void* W, const int64_t* target,
+                                   int64_t ignore_index, float logit_scale, const int64_t* offsets,
+                                   int64_t pairs, const float* reference, float beta,
+                                   float label_smoothing, int average, const float* dloss, float* loss,
+                                   float* ratios, void* dX, void* dW, int64_t T, int64_t V, int64_t D,
+                                   int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                                   const tg_head_options* opt, tg_stream_t stream) {
+  Head h;
+  std::memset(&h, 0, sizeof(h));
+  h.X = X;
+  h.W = W;
+  h.index = target;
+  h.ignore = ignore_index;
+  h.dX = dX;
+  h.dW = dW;
+  h.T = T, h.V = V, h.D = D;
+  h.ldx = ldx, h.ldw = ldw, h.lddx = lddx, h.lddw = lddw;
+  h.scale = logit_scale;
+  h.o = options_or_default(opt);
+  h.ob.kind = kPreference;
+  h.ob.dloss = dX || dW ? dloss : nullptr;
+  h.ob.loss = loss;
+  h.ob.reference = reference;
+  h.ob.offsets = offsets;
+  h.ob.pairs = pairs;
+  h.ob.beta = beta;
+  h.ob.smooth = label_smoothing;
+  h.ob.average = average != 0;
+  h.ob.ratios = ratios;
+  return run_objective(h, reinterpret_cast<cudaStream_t>(stream));
+}
+
+tg_status tg_linear_policy_f16(const void* X, const void* W, const int64_t* target,
+                               int64_t ignore_index, float logit_scale, const float* old_logp,
+                               const float* advantage, const float* reference, float clip_low,
+                               float clip_high, float kl_weight, const float* dloss, float* loss,
+                               float* logp, void* dX, void* dW, int64_t T, int64_t V, int64_t D,
+                               int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                               const tg_head_options* opt, tg_stream_t stream) {
+  Head h;
+  std::memset(&h, 0, sizeof(h));
+  h.X = X;
+  h.W = W;
+  h.index = target;
+  h.ignore = ignore_index;
+  h.dX = dX;
+  h.dW = dW;
+  h.T = T, h.V = V, h.D = D;
+  h.ldx = ldx, h.ldw = ldw, h.lddx = lddx, h.lddw = lddw;
+  h.scale = logit_scale;
+  h.o = options_or_default(opt);
+  h.ob.kind = kPolicy;
+  h.ob.dloss = dX || dW ? dloss : nullptr;
+  h.ob.loss = loss;
+  h.ob.reference = kl_weight > 0.0f ? reference : nullptr;
+  h.ob.old = old_logp;
+  h.ob.advantage = advantage;
+  h.ob.low = 1.0f - clip_low;
+  h.ob.high = 1.0f + clip_high;
+  h.ob.kl = kl_weight;
+  h.ob.logp = logp;
+  return run_objective(h, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

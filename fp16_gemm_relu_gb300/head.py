@@ -165,3 +165,127 @@ def linear_distillation_step(x, weight, teacher_index, teacher_logits, dloss,
     loss, _, dx, dw = _distillation(x, weight, teacher_index, teacher_logits, dloss, True, True,
                                     False, temperature, layout, piece_rows, stream)
     return loss, dx, dw
+
+
+def _token_values(T, dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            if t.dtype is not torch.float32:
+                raise TypeError(f"{name} must be torch.float32")
+            vector(t, T, dev, name)
+
+
+def _preference(x, weight, target, offsets, dloss, need_dx, need_dw, reference, beta, label_smoothing,
+                average, ignore_index, logit_scale, layout, piece_rows, stream):
+    """(loss, ratios, dx, dweight), None for what is not wanted."""
+    T, V, D, ldx, ldw = _sizes(x, weight, layout)
+    dev = x.get_device()
+    if not here(dev, stream):
+        with on(x.device, stream, x, weight, target, offsets, dloss, reference):
+            return _preference(x, weight, target, offsets, dloss, need_dx, need_dw, reference, beta,
+                               label_smoothing, average, ignore_index, logit_scale, layout, piece_rows,
+                               None)
+    if target.dtype is not torch.int64 or offsets.dtype is not torch.int64:
+        raise TypeError("target and offsets must be torch.int64")
+    vector(target, T, dev, "target")
+    if offsets.dim() != 1 or offsets.shape[0] % 2 == 0:
+        raise ValueError("offsets must be a (2 * pairs + 1,) tensor")
+    vector(offsets, offsets.shape[0], dev, "offsets")
+    pairs = offsets.shape[0] // 2
+    _token_values(T, dev, reference=reference)
+    _weights(dloss, pairs, dev)
+    loss = torch.empty(pairs, dtype=torch.float32, device=x.device)
+    ratios = torch.empty((pairs, 2), dtype=torch.float32, device=x.device)
+    _, _, dx, dw = _outputs(x, weight, 0, D, False, need_dw, False)
+    if need_dx:
+        dx = torch.empty((T, D), dtype=torch.float16, device=x.device)
+    check(library().tg_linear_preference_f16(
+        x.data_ptr(), weight.data_ptr(), target.data_ptr(), ignore_index, logit_scale,
+        offsets.data_ptr(), pairs, ptr(reference), beta, label_smoothing, 1 if average else 0,
+        ptr(dloss), loss.data_ptr(), ratios.data_ptr(), ptr(dx), ptr(dw), T, V, D, ldx, ldw, D,
+        weight.shape[1], _options(layout, piece_rows), stream_handle(dev)), "tg_linear_preference_f16")
+    return loss, ratios, dx, dw
+
+
+def linear_preference(x, weight, target, offsets, reference=None, beta: float = 0.1,
+                      label_smoothing: float = 0.0, average: bool = False, ignore_index: int = -100,
+                      logit_scale: float = 1.0, layout: int = TG_HEAD_VOCAB_MAJOR,
+                      piece_rows: int = 0, stream=None):
+    """(loss, ratios) of pairs of sequences.  With logp[t] the log probability of target[t] under the
+    softmax of logit_scale * x @ weight.T,
+
+        ratios[p, s] = sum over a sequence's rows t of logp[t] - reference[t]
+        loss[p] = -(1 - label_smoothing) log sigma(m) - label_smoothing log sigma(-m),
+        m = beta * (ratios[p, 0] - ratios[p, 1])
+
+    ``offsets`` is int64 (2 * pairs + 1,): the chosen sequence of pair p is the rows offsets[2p] to
+    offsets[2p + 1], the rejected one those from there to offsets[2p + 2]; offsets that decrease or leave
+    the rows make the pair's results NaN.  Rows whose target is ``ignore_index`` (a prompt's) do not
+    count.  ``reference`` is float32 (T,), as minus :func:`linear_cross_entropy` of the model that is
+    compared with, or None for 0; ``average`` takes means for the sums.
+    """
+    return _preference(x, weight, target, offsets, None, False, False, reference, beta, label_smoothing,
+                       average, ignore_index, logit_scale, layout, piece_rows, stream)[:2]
+
+
+def linear_preference_step(x, weight, target, offsets, dloss, reference=None, beta: float = 0.1,
+                           label_smoothing: float = 0.0, average: bool = False,
+                           ignore_index: int = -100, logit_scale: float = 1.0,
+                           layout: int = TG_HEAD_VOCAB_MAJOR, piece_rows: int = 0, stream=None):
+    """(loss, ratios, dx, dweight) of :func:`linear_preference` for the upstream gradient ``dloss``
+    (float32 (pairs,)).  Rows outside of all sequences get a dx of 0."""
+    return _preference(x, weight, target, offsets, dloss, True, True, reference, beta, label_smoothing,
+                       average, ignore_index, logit_scale, layout, piece_rows, stream)
+
+
+def _policy(x, weight, target, old, advantage, dloss, need_dx, need_dw, reference, clip_low, clip_high,
+            kl_weight, ignore_index, logit_scale, layout, piece_rows, stream):
+    """(loss, logp, dx, dweight), None for what is not wanted."""
+    T, V, D, ldx, ldw = _sizes(x, weight, layout)
+    dev = x.get_device()
+    if not here(dev, stream):
+        with on(x.device, stream, x, weight, target, old, advantage, dloss, reference):
+            return _policy(x, weight, target, old, advantage, dloss, need_dx, need_dw, reference,
+                           clip_low, clip_high, kl_weight, ignore_index, logit_scale, layout,
+                           piece_rows, None)
+    if target.dtype is not torch.int64:
+        raise TypeError("target must be torch.int64")
+    vector(target, T, dev, "target")
+    if kl_weight != 0.0 and reference is None:
+        raise ValueError("kl_weight needs reference")
+    _token_values(T, dev, old=old, advantage=advantage, reference=reference)
+    _weights(dloss, T, dev)
+    out = _outputs(x, weight, T, D, need_dx, need_dw, True)
+    loss, logp, dx, dw = out
+    check(library().tg_linear_policy_f16(
+        x.data_ptr(), weight.data_ptr(), target.data_ptr(), ignore_index, logit_scale, old.data_ptr(),
+        advantage.data_ptr(), ptr(reference), clip_low, clip_high, kl_weight, ptr(dloss),
+        loss.data_ptr(), logp.data_ptr(), ptr(dx), ptr(dw), T, V, D, ldx, ldw, D, weight.shape[1],
+        _options(layout, piece_rows), stream_handle(dev)), "tg_linear_policy_f16")
+    return out
+
+
+def linear_policy(x, weight, target, old, advantage, reference=None, clip_low: float = 0.2,
+                  clip_high: float = 0.2, kl_weight: float = 0.0, ignore_index: int = -100,
+                  logit_scale: float = 1.0, layout: int = TG_HEAD_VOCAB_MAJOR, piece_rows: int = 0,
+                  stream=None):
+    """(loss, logp) of each row: with logp[t] the log probability of target[t] under the softmax of
+    logit_scale * x @ weight.T and r = exp(logp - old), d = reference - logp,
+
+        loss = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_weight (exp(d) - d - 1)
+
+    ``old``, ``advantage`` (A) and ``reference`` (needed where kl_weight is not 0) are float32 (T,).
+    Rows whose target is ``ignore_index`` have loss and logp 0.
+    """
+    return _policy(x, weight, target, old, advantage, None, False, False, reference, clip_low, clip_high,
+                   kl_weight, ignore_index, logit_scale, layout, piece_rows, stream)[:2]
+
+
+def linear_policy_step(x, weight, target, old, advantage, dloss, reference=None, clip_low: float = 0.2,
+                       clip_high: float = 0.2, kl_weight: float = 0.0, ignore_index: int = -100,
+                       logit_scale: float = 1.0, layout: int = TG_HEAD_VOCAB_MAJOR,
+                       piece_rows: int = 0, stream=None):
+    """(loss, logp, dx, dweight) of :func:`linear_policy` for the upstream gradient ``dloss``
+    (float32 (T,))."""
+    return _policy(x, weight, target, old, advantage, dloss, True, True, reference, clip_low, clip_high,
+                   kl_weight, ignore_index, logit_scale, layout, piece_rows, stream)

@@ -428,6 +428,110 @@ tg_status tg_linear_distill_f16(const void* X, const void* W, const int64_t* tea
                                 int64_t ldw, int64_t lddx, int64_t lddw,
                                 const tg_head_options* opt, tg_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------------------
+ * A fine-tuning step: the gated feed-forward product, preference and policy losses of a linear head,
+ * and the gradients unscaled and clipped.  Conventions as for the end of a language model, above.
+ * ---------------------------------------------------------------------------------------
+ */
+
+/* An activation of the gated product alone, beside TG_ACT_NONE to TG_ACT_GELU_TANH:
+ * SILU is x / (1 + e^-x). */
+enum { TG_ACT_SILU = 4 };
+
+/*
+ * Gated feed-forward product of X (M x K) with two weights:
+ *     G = X Wg,  U = X Wu  (M x N, float32 sums),   H = fp16( act(G) * U )
+ *     trans_w = 0: Wg and Wu are stored K x N;  1: N x K
+ * gate, up: NULL, or fp16 M x N that get G and U, rounded once (the backward pass takes them).  H comes
+ * from the float32 sums either way.  H, gate and up are different buffers.  M >= 0, N, K >= 1.
+ * opt may be NULL, or set block_n (128 or 256), split_k, panel_m, max_ctas, pair, timeout_ms, debug_flags.
+ */
+tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, void* gate, void* up,
+                       int activation, int trans_w, int64_t M, int64_t N, int64_t K, int64_t ldx,
+                       int64_t ldwg, int64_t ldwu, int64_t ldh, int64_t ldgate, int64_t ldup,
+                       const tg_options* opt, tg_stream_t stream);
+
+/*
+ * Backward of tg_gated_f16 for the upstream gradient dH (M x N), from the kept gate and up:
+ *     dG = dH * up * act'(gate),   dU = dH * act(gate)
+ *     dX = dG Wg^T + dU Wu^T  (M x K),   dWg = X^T dG,  dWu = X^T dU  (stored as the weights are)
+ * dX, dWg, dWu: each may be NULL (not computed).  M == 0 writes zeros to dWg and dWu.  dG and dU are
+ * rounded to fp16, the type of the products' operands: what leaves fp16's range there is infinite in the
+ * gradients, and what is below its smallest normal number keeps fewer bits, as for any fp16 gradient
+ * under a loss scale.  The derivative of relu at 0 is 0.
+ * Scratch: dG and dU, and copies of operands that are not 16-byte aligned with leading dimensions that
+ * are multiples of 8.
+ */
+tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, const void* Wu,
+                                const void* gate, const void* up, void* dX, void* dWg, void* dWu,
+                                int activation, int trans_w, int64_t M, int64_t N, int64_t K,
+                                int64_t lddh, int64_t ldx, int64_t ldwg, int64_t ldwu, int64_t ldgate,
+                                int64_t ldup, int64_t lddx, int64_t lddwg, int64_t lddwu,
+                                const tg_options* opt, tg_stream_t stream);
+
+/*
+ * Preference loss of pairs of sequences (Rafailov et al., 2023), through the linear head of
+ * tg_linear_cross_entropy_f16: with logp[t] the log probability of target[t], over the rows of a sequence
+ * whose target is not ignore_index,
+ *     ratio_s = sum_t (logp[t] - reference[t])       (average != 0: their mean; no such row: 0)
+ *     m = beta (ratio of the chosen - ratio of the rejected)
+ *     loss = -(1 - label_smoothing) log sigma(m) - label_smoothing log sigma(-m)
+ * offsets: int64[2 pairs + 1]: the chosen sequence of pair p is the rows [offsets[2p], offsets[2p + 1]), the
+ * rejected one the rows from there to offsets[2p + 2].  Rows outside of all of them get no gradient.  A pair
+ * whose offsets decrease or leave [0, T] has a loss of NaN and makes the gradients NaN; nothing outside of
+ * the arrays is read.  reference: float32[T], the log probabilities of the model that is compared with, or
+ * NULL for 0.  loss: float32[pairs]; ratios: float32[pairs][2], chosen first; dloss: float32[pairs]; loss and ratios may be NULL.
+ * beta > 0, 0 <= label_smoothing < 1.  The ratios' sums are float64.  dX, dW, targets, scratch, accuracy and
+ * options as tg_linear_cross_entropy_f16; where the tokens' logits do not fit into one piece, the logits
+ * are computed twice, the first time without being kept.
+ */
+tg_status tg_linear_preference_f16(const void* X, const void* W, const int64_t* target,
+                                   int64_t ignore_index, float logit_scale, const int64_t* offsets,
+                                   int64_t pairs, const float* reference, float beta,
+                                   float label_smoothing, int average, const float* dloss, float* loss,
+                                   float* ratios, void* dX, void* dW, int64_t T, int64_t V, int64_t D,
+                                   int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                                   const tg_head_options* opt, tg_stream_t stream);
+
+/*
+ * Clipped policy loss of each row (Schulman et al., 2017) through the same head, with a penalty against a
+ * reference model (kl_weight > 0):
+ *     r = exp(logp - old_logp),   d = reference - logp
+ *     loss = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_weight (exp(d) - d - 1)
+ * with the row's advantage A.  old_logp, advantage, reference (NULL only with kl_weight == 0), loss, logp
+ * and dloss: float32[T]; loss and logp may be NULL.  Rows at ignore_index have loss and logp 0 and no
+ * gradient.  0 <= clip_low <= 1, clip_high >= 0, kl_weight >= 0.  Where both terms of the minimum are the
+ * same the gradient is the first one's.  Everything else as tg_linear_preference_f16.
+ */
+tg_status tg_linear_policy_f16(const void* X, const void* W, const int64_t* target,
+                               int64_t ignore_index, float logit_scale, const float* old_logp,
+                               const float* advantage, const float* reference, float clip_low,
+                               float clip_high, float kl_weight, const float* dloss, float* loss,
+                               float* logp, void* dX, void* dW, int64_t T, int64_t V, int64_t D,
+                               int64_t ldx, int64_t ldw, int64_t lddx, int64_t lddw,
+                               const tg_head_options* opt, tg_stream_t stream);
+
+/* A gradient of any shape as `count` values without gaps, and where its scaled values go. */
+typedef struct {
+  const void* data;
+  void* out;        /* count values of out_type; it may be data itself, of the same type */
+  int64_t count;
+  int type, out_type; /* TG_TYPE_* */
+} tg_gradient;
+
+/*
+ * Gradients under a loss scale, unscaled and clipped by the norm of all of them together:
+ *     *norm = sqrt( sum of all squares ) / loss_scale
+ *     out = data * min(1, max_norm / *norm) / loss_scale       (*norm not finite: data / loss_scale)
+ * norm: device float32.  list: host memory, read before the call returns; with every `out` NULL only the norm
+ * is computed, else every gradient with count > 0 has one.  Outputs do not overlap each other, nor any
+ * gradient but the one they replace (TG_ERR_INVALID_ARG).  loss_scale > 0, max_norm >= 0 (infinity: no
+ * clipping).  Squares are float32: a gradient beyond 1.8e19 counts as infinite, below 1e-23 as 0.
+ */
+tg_status tg_clip_gradients(const tg_gradient* list, int64_t n, float loss_scale, float max_norm,
+                            float* norm, tg_stream_t stream);
+
 /* Library version as major*10000 + minor*100 + patch.  300: tg_options gained dequant_first
  * (callers must be built against this header). */
 int tg_version(void);
