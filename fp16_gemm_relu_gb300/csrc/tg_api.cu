@@ -200,9 +200,11 @@ double kblock_cycles(int bn) {
 // inflated when a wave keeps fewer than 60% of the SMs busy; plus the float32 workspace
 // traffic of split-K and its extra launch, and the operand copies of unaligned operands.
 // max_k: 0, or the K columns that a split may have at most (where the options leave the splits open).
+// halves: only tiles whose halves are whole 64-column boxes (not 192).
 tg_status make_plan(uintptr_t a, uintptr_t b, uintptr_t c, int64_t M, int64_t N, int64_t K,
                     int64_t lda, int64_t ldb, int64_t ldc, int num_sms, int pair_clusters,
-                    const tg_options* opt, Plan* out, int ta = 0, int tb = 0, int64_t max_k = 0) {
+                    const tg_options* opt, Plan* out, int ta = 0, int tb = 0, int64_t max_k = 0,
+                    bool halves = false) {
   tg_options o;
   std::memset(&o, 0, sizeof(o));
   if (opt) o = *opt;
@@ -261,7 +263,7 @@ tg_status make_plan(uintptr_t a, uintptr_t b, uintptr_t c, int64_t M, int64_t N,
     const int bn = pair ? 256 : kBlockNs[kind - 1];
     if (pair && (o.pair < 0 || pair_cap < 1)) continue;
     if (!pair && o.pair > 0) continue;
-    if (o.block_n && bn != o.block_n) continue;
+    if ((o.block_n && bn != o.block_n) || (halves && bn == 192)) continue;
     const int bm = pair ? 2 * tg::kBM : tg::kBM;
     const int64_t tiles = cdiv(M, bm) * cdiv(N, bn);
     const int64_t s_max = o.split_k ? std::min<int64_t>(o.split_k, P.kblocks)
@@ -1260,6 +1262,45 @@ cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t
   launch_pack(static_cast<const uint16_t*>(src), ld_src, static_cast<uint16_t*>(dst), ld_dst, rows,
               cols, num_sms, 8, true, stream);
   return cudaGetLastError();
+}
+
+tg_status plan_tiles(int64_t M, int64_t N, int64_t K, const tg_options* opt, TilePlan* out) {
+  DeviceState* ds = nullptr;
+  tg_status st = current_device(&ds);
+  if (st != TG_OK) return st;
+  tg_options o;
+  std::memset(&o, 0, sizeof(o));
+  if (opt) o = *opt;
+  if (o.force_repack || o.force_workspace || o.swap_ab || o.a_in_place || o.tmem_decode || o.dequant_first)
+    return TG_ERR_INVALID_ARG;
+  o.tail = -1;
+  Plan pl;
+  st = make_plan(256, 256, 256, M, N, K, round_up(K, 8), round_up(N, 8), round_up(N, 8), ds->sm_count,
+                 ds->pair_clusters, &o, &pl, 0, 0, 0, true);
+  if (st != TG_OK) return st;
+  const tg_plan& P = pl.pub;
+  const int cap = o.max_ctas > 0 ? std::min(o.max_ctas, ds->sm_count) : ds->sm_count;
+  out->pair = P.cta_pair;
+  out->block_n = P.block_n;
+  out->splits = P.split_k;
+  out->num_kb = static_cast<int>(P.kblocks);
+  out->kb_per_split = static_cast<int>(P.kblocks_per_split);
+  out->units_cap = P.cta_pair ? std::max(std::min(cap / 2, ds->pair_clusters), 1) : cap;
+  return TG_OK;
+}
+
+bool half_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
+              int box_outer) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  return encode_fn(&enc) == TG_OK &&
+         encode_2d(enc, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, uint64_t(inner), uint64_t(outer),
+                   uint64_t(ld) * 2, uint32_t(box_inner), uint32_t(box_outer)) == CUDA_SUCCESS;
+}
+
+bool partial_map(CUtensorMap* m, const void* base, int64_t n, int64_t rows, int64_t splits, int64_t ldw) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  return encode_fn(&enc) == TG_OK && encode_ws_3d(enc, m, base, uint64_t(n), uint64_t(rows),
+                                                  uint64_t(splits), uint64_t(ldw)) == CUDA_SUCCESS;
 }
 
 bool tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) { return encode_fn(fn) == TG_OK; }

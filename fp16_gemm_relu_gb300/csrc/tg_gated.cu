@@ -10,7 +10,6 @@
 #include <cstdint>
 #include <cstring>
 
-#include "tg_gated_kernel.cuh"
 #include "tg_gemm_relu.h"
 #include "tg_internal.h"
 
@@ -63,27 +62,51 @@ __device__ __forceinline__ void load8(const __half* row, int64_t col, int64_t n,
   }
 }
 
-// H (and gate, up) from the float32 products, eight columns a thread.
-__global__ void __launch_bounds__(256)
-    tg_gated_combine_kernel(const float* gate32, const float* up32, int64_t ld32, int act,
-                            __half* h, int64_t ldh, __half* gate, int64_t ldg, __half* up,
-                            int64_t ldu, int64_t M, int64_t N) {
-  const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
-  if (c >= N) return;
-  for (int64_t r = blockIdx.y; r < M; r += gridDim.y) {
-    float g[8], u[8], v[8];
+// H (and gate, up) from the K splits' float32 partial sums, added in order; four columns a thread and the
+// loads of kAhead splits in flight.  A split's rows hold the gates and, nw columns further, the ups.
+constexpr int kAhead = 4;
+__device__ __forceinline__ void store4(__half* row, int64_t col, int64_t n, const float (&v)[4]) {
+  __half* d = row + col;
+  if (col + 4 <= n && (reinterpret_cast<uintptr_t>(d) & 7u) == 0) {
+    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(d) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; i += 4) {  // ld32 is a multiple of 32
-      const float4 a = *reinterpret_cast<const float4*>(gate32 + r * ld32 + c + i);
-      const float4 b = *reinterpret_cast<const float4*>(up32 + r * ld32 + c + i);
-      g[i] = a.x, g[i + 1] = a.y, g[i + 2] = a.z, g[i + 3] = a.w;
-      u[i] = b.x, u[i + 1] = b.y, u[i + 2] = b.z, u[i + 3] = b.w;
+    for (int i = 0; i < 4; ++i)
+      if (col + i < n) d[i] = __float2half_rn(v[i]);
+  }
+}
+__global__ void __launch_bounds__(128)
+    tg_gated_reduce_kernel(const float* ws, int64_t nw, int64_t stride, int splits, int act,
+                           __half* h, int64_t ldh, __half* gate, int64_t ldg, __half* up, int64_t ldu,
+                           int64_t M, int64_t N) {
+  const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 2;
+  if (c >= N) return;
+  tg::chain_wait();
+  for (int64_t r = blockIdx.y; r < M; r += gridDim.y) {
+    const float* w = ws + r * 2 * nw + c;
+    float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4];
+    for (int s0 = 0; s0 < splits; s0 += kAhead) {
+      float4 a[kAhead], b[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s0 + i >= splits) break;
+        a[i] = __ldcg(reinterpret_cast<const float4*>(w + (s0 + i) * stride));
+        b[i] = __ldcg(reinterpret_cast<const float4*>(w + (s0 + i) * stride + nw));
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (s0 + i >= splits) break;
+        g[0] += a[i].x, g[1] += a[i].y, g[2] += a[i].z, g[3] += a[i].w;
+        u[0] += b[i].x, u[1] += b[i].y, u[2] += b[i].z, u[3] += b[i].w;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = gated_activation(g[i], act) * u[i];
-    store8(h + r * ldh, c, N, v);
-    if (gate) store8(gate + r * ldg, c, N, g);
-    if (up) store8(up + r * ldu, c, N, u);
+    for (int i = 0; i < 4; ++i) v[i] = gated_activation(g[i], act) * u[i];
+    store4(h + r * ldh, c, N, v);
+    if (gate) store4(gate + r * ldg, c, N, g);
+    if (up) store4(up + r * ldu, c, N, u);
   }
 }
 
@@ -135,6 +158,51 @@ tg_status check(const Gated& a) {
   return TG_OK;
 }
 
+// Parts of one scratch block, each 256-byte aligned.
+struct Layout {
+  int64_t bytes = 0;
+  int64_t add(int64_t n) {
+    const int64_t at = bytes;
+    bytes += round_up(n, 256);
+    return at;
+  }
+};
+
+// X and the weights as TMA reads them: in place, or as copies with rows of whole 128-byte lines where
+// the caller's are not 16-byte aligned with leading dimensions that are multiples of 8.
+struct Operands {
+  const void *x, *wg, *wu;
+  int64_t ldx, ldwg, ldwu;
+  int64_t at[3];  // of the copies in scratch, or -1
+
+  void plan(const Gated& a, Layout* lay) {
+    auto one = [&](const void* p, int64_t ld, int64_t rows, int64_t cols) -> int64_t {
+      return misaligned(p, 16) || ld % 8 != 0 ? lay->add(rows * round_up(cols, 64) * 2) : -1;
+    };
+    const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
+    at[0] = one(a.X, a.ldx, a.M, a.K);
+    at[1] = one(a.Wg, a.ldwg, w_rows, w_cols);
+    at[2] = one(a.Wu, a.ldwu, w_rows, w_cols);
+  }
+  cudaError_t copy(const Gated& a, uint8_t* mem, int sms, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    auto one = [&](int i, const void* p, int64_t ld, int64_t rows, int64_t cols, const void** out,
+                   int64_t* ldo) {
+      *out = p;
+      *ldo = ld;
+      if (at[i] < 0 || e != cudaSuccess) return;
+      *out = mem + at[i];
+      *ldo = round_up(cols, 64);
+      e = tg::launch_pack_rows(p, ld, mem + at[i], *ldo, rows, cols, sms, stream);
+    };
+    const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
+    one(0, a.X, a.ldx, a.M, a.K, &x, &ldx);
+    one(1, a.Wg, a.ldwg, w_rows, w_cols, &wg, &ldwg);
+    one(2, a.Wu, a.ldwu, w_rows, w_cols, &wu, &ldwu);
+    return e;
+  }
+};
+
 }  // namespace
 
 extern "C" {
@@ -152,27 +220,86 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   if (M == 0) return TG_OK;
   if (!H) return TG_ERR_INVALID_ARG;
   if (misaligned(H, 2) || misaligned(gate, 2) || misaligned(up, 2)) return TG_ERR_MISALIGNED;
-  const int64_t ld32 = round_up(N, 32);
-  float* mem = nullptr;
-  if ((st = tg::scratch_alloc(size_t(2 * M * ld32 * 4), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
+  tg::TilePlan plan;
+  // a row of tiles of BN columns covers BN / 2 of each weight
+  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, opt, &plan)) != TG_OK) return st;
+  int sms = 0;
+  unsigned* err = nullptr;
+  if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
+  Operands ops;
+  const int64_t nw = round_up(N, 32), stride = M * 2 * nw;
+  Layout lay;
+  ops.plan(a, &lay);
+  const bool f32 = plan.splits > 1;
+  const int64_t at_ws = lay.add(f32 ? plan.splits * stride * 4 : 0);
+  uint8_t* mem = nullptr;
+  if (lay.bytes > 0 &&
+      (st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
-  tg::GemmExtra ex;
-  std::memset(&ex, 0, sizeof(ex));
-  ex.ld32 = ld32;
-  for (int i = 0; i < 2 && st == TG_OK; ++i) {
-    ex.out32 = mem + i * M * ld32;
-    st = tg::gemm_extra(0, trans_w, X, i ? Wu : Wg, nullptr, M, N, K, ldx, i ? ldwu : ldwg, N, ex, opt,
-                        stream);
+  auto done = [&](tg_status s) {
+    const cudaError_t fe = mem ? cudaFreeAsync(mem, stream) : cudaSuccess;
+    return s == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : s;
+  };
+  cudaError_t e = ops.copy(a, mem, sms, stream);
+  if (e != cudaSuccess) return done(tg::record_cuda_error(e));
+
+  const int hn = plan.pair ? 128 : plan.block_n / 2, bm = plan.pair ? 256 : 128;
+  tg::GatedLaunch l;
+  std::memset(&l, 0, sizeof(l));
+  tg::GemmParams& p = l.p.g;
+  p.tiles_m = static_cast<int>(cdiv(M, bm));
+  p.tiles_n = static_cast<int>(cdiv(N, hn));
+  p.num_kb = plan.num_kb;
+  p.kb_per_split = plan.kb_per_split;
+  p.splits = plan.splits;
+  const int64_t units = int64_t(p.tiles_m) * p.tiles_n * p.splits;
+  if (units >= (int64_t{1} << 31)) return done(TG_ERR_INVALID_ARG);
+  p.units = static_cast<int>(units);
+  p.panel_m = std::min(opt && opt->panel_m ? opt->panel_m : 8, p.tiles_m);
+  p.act = activation;
+  p.b_k = trans_w;
+  p.debug_flags = opt ? opt->debug_flags : 0;
+  p.timeout_ns = 1000000ull * static_cast<unsigned long long>(opt && opt->timeout_ms > 0 ? opt->timeout_ms : 2000);
+  p.err = err;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  l.p.h = static_cast<__half*>(H), l.p.ldh = ldh;
+  l.p.gate = static_cast<__half*>(gate), l.p.ldgate = ldgate;
+  l.p.up = static_cast<__half*>(up), l.p.ldup = ldup;
+  l.p.a_rows = static_cast<int>(M < 128 && !plan.pair ? round_up(M, 8) : 128);
+  l.p.nw = static_cast<int>(nw);
+  l.p.rotate = p.tiles_m == 1;
+  auto rows16 = [](const void* q, int64_t ld) { return !misaligned(q, 16) && ld % 8 == 0; };
+  l.p.tma = N % 8 == 0 && rows16(H, ldh) && (!gate || rows16(gate, ldgate)) && (!up || rows16(up, ldup));
+  l.grid = static_cast<int>(std::min<int64_t>(units, plan.units_cap)) * (plan.pair ? 2 : 1);
+  l.block_n = plan.pair ? 0 : plan.block_n;
+  l.out_f32 = f32;
+  l.chained = false;
+  l.stream = stream;
+  bool ok = tg::half_map(&l.x, ops.x, K, M, ops.ldx, 64, l.p.a_rows);
+  const int kbox = plan.pair ? 128 : 64;
+  if (trans_w)
+    ok = ok && tg::half_map(&l.g, ops.wg, K, N, ops.ldwg, 64, plan.pair ? 128 : hn) &&
+         tg::half_map(&l.u, ops.wu, K, N, ops.ldwu, 64, plan.pair ? 128 : hn);
+  else
+    ok = ok && tg::half_map(&l.g, ops.wg, N, K, ops.ldwg, 64, kbox) &&
+         tg::half_map(&l.u, ops.wu, N, K, ops.ldwu, 64, kbox);
+  float* ws = reinterpret_cast<float*>(mem + at_ws);
+  if (f32)
+    ok = ok && tg::partial_map(&l.h, ws, 2 * nw, M, p.splits, 2 * nw);
+  else if (l.p.tma)
+    ok = ok && tg::half_map(&l.h, H, N, M, ldh, 64, 32) &&
+         (!gate || tg::half_map(&l.gate, gate, N, M, ldgate, 64, 32)) &&
+         (!up || tg::half_map(&l.up, up, N, M, ldup, 64, 32));
+  if (!ok) return done(tg::record_cuda_error(cudaErrorInvalidValue));
+  if ((e = tg::launch_gated(l)) != cudaSuccess) return done(tg::record_cuda_error(e));
+  if (f32) {
+    const dim3 grid(static_cast<unsigned>(cdiv(N, 512)), static_cast<unsigned>(std::min<int64_t>(M, 65535)));
+    e = tg::launch_chained(tg_gated_reduce_kernel, true, grid, 128, 0, stream, ws, nw, stride, p.splits,
+                           activation, l.p.h, ldh, l.p.gate, ldgate, l.p.up, ldup, M, N);
+    if (e != cudaSuccess) return done(tg::record_cuda_error(e));
   }
-  if (st == TG_OK) {
-    tg_gated_combine_kernel<<<row_grid(N, M), 256, 0, stream>>>(
-        mem, mem + M * ld32, ld32, activation, static_cast<__half*>(H), ldh,
-        static_cast<__half*>(gate), ldgate, static_cast<__half*>(up), ldup, M, N);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) st = tg::record_cuda_error(e);
-  }
-  const cudaError_t fe = cudaFreeAsync(mem, stream);
-  return st == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : st;
+  return done(TG_OK);
 }
 
 tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, const void* Wu,

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tg_gated_kernel.cuh"
 #include "tg_gemm_kernel.cuh"
 #include "tg_gemm_relu.h"
 
@@ -111,6 +112,30 @@ struct GemmExtra {
 tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
                      int64_t K, int64_t lda, int64_t ldb, int64_t ldc, const GemmExtra& x,
                      const tg_options* opt, cudaStream_t stream);
+
+// The gated product's kernels (tg_gated_kernel.cuh says which map holds what).
+struct GatedLaunch {
+  CUtensorMap x, g, u, h, gate, up;
+  GatedParams p;
+  int grid, block_n;  // block_n 0: CTA pairs
+  bool out_f32;       // float32 partial sums
+  bool chained;       // see GemmLaunch
+  cudaStream_t stream;
+};
+cudaError_t launch_gated(const GatedLaunch& l);
+
+// How the GEMM's planner would run an M x N x K product on aligned operands, with or without K splits,
+// in tiles of 256 x 256 on CTA pairs, or 128 x 256 or 128 x 128.
+struct TilePlan {
+  int pair, block_n, splits, num_kb, kb_per_split, units_cap;  // units_cap: CTAs or pairs at a time
+};
+tg_status plan_tiles(int64_t M, int64_t N, int64_t K, const tg_options* opt, TilePlan* out);
+
+// One 2-D fp16 tensor map, 128B swizzle; false if the driver refuses it.
+bool half_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
+              int box_inner, int box_outer);
+// Float32 partial sums: dims {n, rows, splits}, rows of ldw floats, box {32, 32, 1}.
+bool partial_map(CUtensorMap* m, const void* base, int64_t n, int64_t rows, int64_t splits, int64_t ldw);
 
 // dst (rows x ld_dst, 16-byte aligned rows, columns up to a multiple of 8 written as zero) <- src.
 cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst,
