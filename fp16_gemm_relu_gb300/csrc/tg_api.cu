@@ -869,10 +869,16 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     C = const_cast<void*>(A);  // only its presence and alignment are looked at
     ldc = N;
   }
-  tg_status st = validate(A, B, C, M, N, K, lda, ldb, ldc, TG_EPILOGUE_NONE, ta, tb);
+  const bool dual = extra && extra->B2;
+  // two right operands: each has rows of its own part of K alone
+  const int64_t ldb_v = dual && tb ? std::max(ldb, K) : ldb;
+  tg_status st = validate(A, B, C, M, N, K, lda, ldb_v, ldc, TG_EPILOGUE_NONE, ta, tb);
   if (st != TG_OK) return st;
   if ((st = validate_epilogue(epi, C, N, ldc)) != TG_OK) return st;
   if (M == 0 || N == 0) return TG_OK;
+  if (dual && (ta || f32 || K % 256 != 0 || ldb % 8 != 0 || extra->ldb2 % 8 != 0 ||
+               (reinterpret_cast<uintptr_t>(B) | reinterpret_cast<uintptr_t>(extra->B2)) % 16 != 0))
+    return TG_ERR_INVALID_ARG;
   DeviceState* ds = nullptr;
   if ((st = current_device(&ds)) != TG_OK) return st;
   cudaError_t e;
@@ -909,6 +915,15 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
                  reinterpret_cast<uintptr_t>(C), M, N, K, lda, ldb, ldc, ds->sm_count,
                  ds->pair_clusters, opt, &pl, ta, tb, extra ? extra->max_k : 0);
   if (st != TG_OK) return st;
+  if (dual && pl.pub.kblocks_per_split % 2 != 0) {
+    // splits of an even number of k-blocks (a stage of a pair takes two): there may be fewer, never more
+    tg_plan& P = pl.pub;
+    const int64_t tiles = P.units / P.split_k;
+    P.kblocks_per_split += 1;
+    P.split_k = static_cast<int>(cdiv(P.kblocks, P.kblocks_per_split));
+    P.units = tiles * P.split_k;
+    P.grid = static_cast<int>(std::min<int64_t>(P.grid, P.units * (P.cta_pair ? 2 : 1)));
+  }
   if (f32) {  // the workspace is the caller's, or there is none
     pl.ldw = logits ? logits->ldz : extra->ld32;
     pl.pub.workspace_bytes = pl.off_w;
@@ -1021,11 +1036,15 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
                                  uint64_t(K), uint64_t(lda_e) * 2, 64, mn_box_k)
                      : encode_2d(enc, &L.a, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Ae, uint64_t(K),
                                  uint64_t(a_rows), uint64_t(lda_e) * 2, tg::kBK, tg::kBM);
-  if (cr == CUDA_SUCCESS)
-    cr = tb ? encode_2d(enc, &L.b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Be, uint64_t(K), uint64_t(N),
-                        uint64_t(ldb_e) * 2, tg::kBK, P.cta_pair ? 128u : uint32_t(P.block_n))
-            : encode_2d(enc, &L.b, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, Be, uint64_t(N), uint64_t(K),
-                        uint64_t(ldb_e) * 2, 64, mn_box_k);
+  const int64_t b_k = dual ? extra->b_k : K;
+  auto right = [&](CUtensorMap* m, const void* base, int64_t ld) {
+    return tb ? encode_2d(enc, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, uint64_t(b_k), uint64_t(N),
+                          uint64_t(ld) * 2, tg::kBK, P.cta_pair ? 128u : uint32_t(P.block_n))
+              : encode_2d(enc, m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, uint64_t(N), uint64_t(b_k),
+                          uint64_t(ld) * 2, 64, mn_box_k);
+  };
+  if (cr == CUDA_SUCCESS) cr = right(&L.b, Be, ldb_e);
+  if (cr == CUDA_SUCCESS && dual) cr = right(&L.b2, extra->B2, extra->ldb2);
   float* ws = f32                    ? out32
               : P.workspace_epilogue ? reinterpret_cast<float*>(scratch + pl.off_w)
                                      : nullptr;
@@ -1060,6 +1079,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     gp.alpha = extra->alpha;
     gp.addend = extra->addend;
     gp.ld_addend = extra->ld32;
+    gp.kb_switch = dual ? static_cast<int>(K / 2 / tg::kBK) : 0;
   }
   gp.a_mn = ta;
   gp.b_k = tb;
@@ -1091,6 +1111,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   auto launch = [&](const tg::GemmLaunch& l) -> cudaError_t {
     if (logits) return tg::launch_head_logits(l, *logits, P.cta_pair ? 0 : P.block_n);
     if (out32 && extra->add) return tg::launch_head_add(l);
+    if (dual) return tg::launch_gemm_dual(l, ws != nullptr, P.cta_pair ? 0 : P.block_n);
     if (l.p.alpha && !ws) return tg::launch_gemm_scaled(l, P.cta_pair ? 0 : P.block_n);
     if (P.a_row_classes) return tg::launch_gemm_pair_cls(cls, l);
     if (P.cta_pair) return tg::launch_gemm_pair(l, ws != nullptr);
@@ -1264,7 +1285,7 @@ cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t
   return cudaGetLastError();
 }
 
-tg_status plan_tiles(int64_t M, int64_t N, int64_t K, const tg_options* opt, TilePlan* out) {
+tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, const tg_options* opt, TilePlan* out) {
   DeviceState* ds = nullptr;
   tg_status st = current_device(&ds);
   if (st != TG_OK) return st;
@@ -1276,7 +1297,7 @@ tg_status plan_tiles(int64_t M, int64_t N, int64_t K, const tg_options* opt, Til
   o.tail = -1;
   Plan pl;
   st = make_plan(256, 256, 256, M, N, K, round_up(K, 8), round_up(N, 8), round_up(N, 8), ds->sm_count,
-                 ds->pair_clusters, &o, &pl, 0, 0, 0, true);
+                 ds->pair_clusters, &o, &pl, 0, 0, max_k, true);
   if (st != TG_OK) return st;
   const tg_plan& P = pl.pub;
   const int cap = o.max_ctas > 0 ? std::min(o.max_ctas, ds->sm_count) : ds->sm_count;

@@ -26,6 +26,10 @@ bool misaligned(const void* p, unsigned bytes) {
 
 constexpr int64_t kMaxSize = (int64_t{1} << 30);
 constexpr int64_t kMaxLd = int64_t{1} << 36;
+// Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
+// 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
+// Longer sums are taken in splits that are added in float32.
+constexpr int64_t kSumLength = 32768;
 
 // fp16 values of 8 columns from `col` on to a row, 16 bytes at once where the row allows it.
 __device__ __forceinline__ void store8(__half* row, int64_t col, int64_t n, const float (&v)[8]) {
@@ -114,8 +118,7 @@ __global__ void __launch_bounds__(128)
 __global__ void __launch_bounds__(256)
     tg_gated_grad_kernel(const __half* __restrict__ dh, int64_t lddh, const __half* __restrict__ gate,
                          int64_t ldg, const __half* __restrict__ up, int64_t ldu, int act,
-                         __half* out, int64_t ld, int64_t np, int64_t M, int64_t N, float* one) {
-  if (one && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *one = 1.0f;
+                         __half* out, int64_t ld, int64_t np, int64_t M, int64_t N) {
   const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   if (c >= np) return;
   for (int64_t r = blockIdx.y; r < M; r += gridDim.y) {
@@ -175,14 +178,15 @@ struct Operands {
   int64_t ldx, ldwg, ldwu;
   int64_t at[3];  // of the copies in scratch, or -1
 
-  void plan(const Gated& a, Layout* lay) {
+  // Of what is read: x, both weights.
+  void plan(const Gated& a, bool need_x, bool need_w, Layout* lay) {
     auto one = [&](const void* p, int64_t ld, int64_t rows, int64_t cols) -> int64_t {
       return misaligned(p, 16) || ld % 8 != 0 ? lay->add(rows * round_up(cols, 64) * 2) : -1;
     };
     const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
-    at[0] = one(a.X, a.ldx, a.M, a.K);
-    at[1] = one(a.Wg, a.ldwg, w_rows, w_cols);
-    at[2] = one(a.Wu, a.ldwu, w_rows, w_cols);
+    at[0] = need_x ? one(a.X, a.ldx, a.M, a.K) : -1;
+    at[1] = need_w ? one(a.Wg, a.ldwg, w_rows, w_cols) : -1;
+    at[2] = need_w ? one(a.Wu, a.ldwu, w_rows, w_cols) : -1;
   }
   cudaError_t copy(const Gated& a, uint8_t* mem, int sms, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
@@ -222,14 +226,14 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   if (misaligned(H, 2) || misaligned(gate, 2) || misaligned(up, 2)) return TG_ERR_MISALIGNED;
   tg::TilePlan plan;
   // a row of tiles of BN columns covers BN / 2 of each weight
-  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, opt, &plan)) != TG_OK) return st;
+  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, opt, &plan)) != TG_OK) return st;
   int sms = 0;
   unsigned* err = nullptr;
   if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
   Operands ops;
   const int64_t nw = round_up(N, 32), stride = M * 2 * nw;
   Layout lay;
-  ops.plan(a, &lay);
+  ops.plan(a, true, true, &lay);
   const bool f32 = plan.splits > 1;
   const int64_t at_ws = lay.add(f32 ? plan.splits * stride * 4 : 0);
   uint8_t* mem = nullptr;
@@ -334,44 +338,44 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
     }
     return TG_OK;
   }
-  const int64_t np = round_up(N, 128), ld = 2 * np, ld32 = round_up(K, 32);
-  const int64_t at_32 = round_up(M * ld * 2, 256), at_one = at_32 + (dX ? M * ld32 * 4 : 0);
+  int sms = 0;
+  unsigned* err = nullptr;
+  if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
+  const int64_t np = round_up(N, 128), ld = 2 * np;
+  Layout lay;
+  Operands ops;
+  const int64_t at_g = lay.add(M * ld * 2);
+  ops.plan(a, dWg || dWu, dX, &lay);
   uint8_t* mem = nullptr;
-  if ((st = tg::scratch_alloc(size_t(at_one + 256), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
+  if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
   auto done = [&](tg_status s) {
     const cudaError_t fe = cudaFreeAsync(mem, stream);
     return s == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : s;
   };
-  __half* g = reinterpret_cast<__half*>(mem);
-  float* sum = reinterpret_cast<float*>(mem + at_32);
-  float* one = reinterpret_cast<float*>(mem + at_one);
+  __half* g = reinterpret_cast<__half*>(mem + at_g);
   tg_gated_grad_kernel<<<row_grid(np, M), 256, 0, stream>>>(
       static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
-      static_cast<const __half*>(up), ldup, activation, g, ld, np, M, N, one);
+      static_cast<const __half*>(up), ldup, activation, g, ld, np, M, N);
   if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
+  if ((e = ops.copy(a, mem, sms, stream)) != cudaSuccess) return done(tg::record_cuda_error(e));
   tg::GemmExtra ex;
+  std::memset(&ex, 0, sizeof(ex));
+  ex.max_k = kSumLength;
   for (int i = 0; i < 2; ++i) {
     void* d = i ? dWu : dWg;
     if (!d) continue;
     const void* gi = g + i * np;
     const int64_t ldd = i ? lddwu : lddwg;
-    std::memset(&ex, 0, sizeof(ex));
-    st = trans_w ? tg::gemm_extra(1, 0, gi, X, d, N, K, M, ld, ldx, ldd, ex, opt, stream)
-                 : tg::gemm_extra(1, 0, X, gi, d, K, N, M, ldx, ld, ldd, ex, opt, stream);
+    st = trans_w ? tg::gemm_extra(1, 0, gi, ops.x, d, N, K, M, ld, ops.ldx, ldd, ex, opt, stream)
+                 : tg::gemm_extra(1, 0, ops.x, gi, d, K, N, M, ops.ldx, ld, ldd, ex, opt, stream);
     if (st != TG_OK) return done(st);
   }
-  if (dX) {
-    std::memset(&ex, 0, sizeof(ex));
-    ex.out32 = sum;
-    ex.ld32 = ld32;
-    st = tg::gemm_extra(0, !trans_w, g, Wg, nullptr, M, K, N, ld, ldwg, K, ex, opt, stream);
-    if (st != TG_OK) return done(st);
-    std::memset(&ex, 0, sizeof(ex));
-    ex.alpha = one;
-    ex.addend = sum;
-    ex.ld32 = ld32;
-    st = tg::gemm_extra(0, !trans_w, g + np, Wu, dX, M, K, N, ld, ldwu, lddx, ex, opt, stream);
+  if (dX) {  // one sum over dG's columns with Wg, then dU's with Wu
+    ex.B2 = ops.wu;
+    ex.ldb2 = ops.ldwu;
+    ex.b_k = N;
+    st = tg::gemm_extra(0, !trans_w, g, ops.wg, dX, M, K, ld, ld, ops.ldwg, lddx, ex, opt, stream);
     if (st != TG_OK) return done(st);
   }
   return done(TG_OK);

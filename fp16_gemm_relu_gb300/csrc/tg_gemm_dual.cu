@@ -1,0 +1,34 @@
+// Instantiations of the tensor-core kernels whose right operand is two matrices (kModeDual).
+#include "tg_internal.h"
+
+namespace tg {
+
+namespace {
+template <typename K>
+cudaError_t launch(K kern, int smem, const GemmLaunch& l) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.b2, l.out, l.p);
+  return cudaGetLastError();
+}
+
+template <bool OUT_F32>
+cudaError_t launch_tile(const GemmLaunch& l, int block_n) {
+  switch (block_n) {
+    case 256: return launch(tg_gemm_tc_dual_kernel<256, OUT_F32>, TileCfg<256>::kSmemBytes, l);
+    case 192: return launch(tg_gemm_tc_dual_kernel<192, OUT_F32>, TileCfg<192>::kSmemBytes, l);
+    case 128: return launch(tg_gemm_tc_dual_kernel<128, OUT_F32>, TileCfg<128>::kSmemBytes, l);
+    default: break;
+  }
+  if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
+  return l.p.b_k ? launch(tg_gemm_pair_dual_kernel<OUT_F32, true>, PairCfgFwd::kSmemBytes, l)
+                 : launch(tg_gemm_pair_dual_kernel<OUT_F32, false>, PairCfgFwd::kSmemBytes, l);
+}
+}  // namespace
+
+cudaError_t launch_gemm_dual(const GemmLaunch& l, bool out_f32, int block_n) {
+  return out_f32 ? launch_tile<true>(l, block_n) : launch_tile<false>(l, block_n);
+}
+
+}  // namespace tg

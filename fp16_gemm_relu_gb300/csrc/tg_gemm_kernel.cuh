@@ -93,13 +93,16 @@ struct GemmParams {
   // rows) start that many elements before each multiple of 64
   int cls_tiles;
   unsigned char cls_shift[kARowClasses];
+  int kb_switch;  // kModeDual: k-blocks from here on are the second right operand's (even)
 };
 
 // What the epilogue does with a tile.  Plain: the fused epilogue (fp16 output) or a store
 // (float32).  Add: a float32 tile is added to the output (each element is added to once a
 // launch, so the result does not depend on order).  Scaled: fp16(alpha (sum + addend)).  A mode
 // of the kernel and not a branch in it, so that the plain kernels carry none of the others.
-enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2 };
+// Dual: plain, but the right operand's k-blocks are two matrices', one after the other (p.kb_switch).
+enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2, kModeDual = 3 };
+constexpr int epilogue_mode(int mode) { return mode == kModeDual ? kModePlain : mode; }
 
 // Kernels that are launched chained.  chain_wait: nothing that the kernel before has written is read,
 // and nothing that it reads is written, before this.  chain_release, after it: the next kernel's
@@ -850,11 +853,11 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
 // 0); the single producer and MMA threads then build descriptors and TMA boxes from constants,
 // which keeps their per-k-block instruction count inside the MMA time.  GENERAL == true reads
 // the layouts from p.a_mn and p.b_k (the transposed-operand GEMMs of the backward pass).
-template <int BN, bool OUT_F32, bool GENERAL, int MODE = kModePlain>
-__global__ void __launch_bounds__(kThreads, 1)
-    tg_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmOut, const GemmParams p) {
+// kModeDual: tmB2 is the second right operand, of the layout of tmB.
+template <int BN, bool OUT_F32, bool GENERAL, int MODE>
+__device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                             const CUtensorMap& tmOut, const GemmParams& p,
+                                             const CUtensorMap* tmB2) {
   using Cfg = TileCfg<BN>;
   constexpr int S = Cfg::kStages;
   const int a_mn = GENERAL ? p.a_mn : 0;
@@ -935,12 +938,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < kBM / 64; ++j)
                 tma_load_2d(a_dst + j * 8192, &tmA, fb, w.m_blk * kBM + j * 64, kb * kBK);
             }
+            const CUtensorMap* mb = &tmB;
+            int kbb = kb;
+            if constexpr (MODE == kModeDual) {
+              if (kb >= p.kb_switch) {
+                mb = tmB2;
+                kbb = kb - p.kb_switch;
+              }
+            }
             if (!b_k) {
 #pragma unroll
               for (int j = 0; j < BN / 64; ++j)
-                tma_load_2d(b_dst + j * Cfg::kBBox, &tmB, fb, w.n_blk * BN + j * 64, kb * kBK);
+                tma_load_2d(b_dst + j * Cfg::kBBox, mb, fb, w.n_blk * BN + j * 64, kbb * kBK);
             } else {
-              tma_load_2d(b_dst, &tmB, fb, kb * kBK, w.n_blk * BN);
+              tma_load_2d(b_dst, mb, fb, kbb * kBK, w.n_blk * BN);
             }
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -1015,9 +1026,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
-      epilogue_tile<BN, OUT_F32, false, MODE>(&tmOut, p, tl, w.m_blk * kBM + q * 32, w.n_blk * BN,
-                                              w.split, stg, sb, smem_u32(&tempty[buf]), false,
-                                              lane);
+      epilogue_tile<BN, OUT_F32, false, epilogue_mode(MODE)>(&tmOut, p, tl, w.m_blk * kBM + q * 32,
+                                                             w.n_blk * BN, w.split, stg, sb,
+                                                             smem_u32(&tempty[buf]), false, lane);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
@@ -1030,6 +1041,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, Cfg::kTmemCols);
   }
+}
+
+template <int BN, bool OUT_F32, bool GENERAL, int MODE = kModePlain>
+__global__ void __launch_bounds__(kThreads, 1)
+    tg_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmOut, const GemmParams p) {
+  tc_gemm_body<BN, OUT_F32, GENERAL, MODE>(tmA, tmB, tmOut, p, nullptr);
+}
+template <int BN, bool OUT_F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    tg_gemm_tc_dual_kernel(const __grid_constant__ CUtensorMap tmA,
+                           const __grid_constant__ CUtensorMap tmB,
+                           const __grid_constant__ CUtensorMap tmB2,
+                           const __grid_constant__ CUtensorMap tmOut,
+                           const __grid_constant__ GemmParams p) {
+  tc_gemm_body<BN, OUT_F32, true, kModeDual>(tmA, tmB, tmOut, p, &tmB2);
 }
 
 // Epilogue of one K half of a tail-split tile (fp16 output), for one warp of the pair kernel:
@@ -1149,7 +1177,8 @@ struct AClassMaps {
 template <bool OUT_F32, bool A_MN, bool B_K, bool A_CLS, int MODE = kModePlain>
 __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                const CUtensorMap& tmOut, const GemmParams& p,
-                                               const AClassMaps* cls) {
+                                               const AClassMaps* cls,
+                                               const CUtensorMap* tmB2 = nullptr) {
   static_assert(!A_CLS || (OUT_F32 && !A_MN && !B_K), "row classes: float32 output, forward layout");
   using Cfg = PairCfgFwd;
   constexpr int S = Cfg::kStages;
@@ -1263,15 +1292,23 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
               for (int j = 0; j < kBM / 64; ++j)
                 tma_load_2d_pair(a_dst + j * Cfg::kMNBox, &tmA, fb, arow + j * 64, kb * kBK);
             }
+            const CUtensorMap* mb = &tmB;
+            int kbb = kb;
+            if constexpr (MODE == kModeDual) {  // units begin at even k-blocks: no stage has both
+              if (kb >= p.kb_switch) {
+                mb = tmB2;
+                kbb = kb - p.kb_switch;
+              }
+            }
             if constexpr (!B_K) {
 #pragma unroll
               for (int j = 0; j < Cfg::kHalfN / 64; ++j)
-                tma_load_2d_pair(b_dst + j * Cfg::kMNBox, &tmB, fb, bcol + j * 64,
-                                 kb * kBK - k_shift);
+                tma_load_2d_pair(b_dst + j * Cfg::kMNBox, mb, fb, bcol + j * 64,
+                                 kbb * kBK - k_shift);
             } else {
 #pragma unroll
               for (int h = 0; h < KB; ++h)
-                tma_load_2d_pair(b_dst + h * Cfg::kAAtom, &tmB, fb, (kb + h) * kBK, bcol);
+                tma_load_2d_pair(b_dst + h * Cfg::kAAtom, mb, fb, (kbb + h) * kBK, bcol);
             }
           }
           if (++stage == S) {
@@ -1356,12 +1393,12 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
       const int row0 = w.m_blk * 2 * kBM + static_cast<int>(rank) * kBM + q * 32;
       const uint32_t release_bar = mapa_shared(smem_u32(&tempty[buf]), 0);
       if (!OUT_F32 && w.tail_slot >= 0)
-        epilogue_tail<Cfg::kBN, MODE>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot,
+        epilogue_tail<Cfg::kBN, epilogue_mode(MODE)>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot,
                                       w.split, static_cast<int>(rank) * 4 + q, stg, sb,
                                       release_bar, lane);
       else
-        epilogue_tile<Cfg::kBN, OUT_F32, false, MODE>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN,
-                                                      w.split, stg, sb, release_bar, true, lane);
+        epilogue_tile<Cfg::kBN, OUT_F32, false, epilogue_mode(MODE)>(
+            &tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.split, stg, sb, release_bar, true, lane);
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
@@ -1387,6 +1424,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tmOut,
                         const __grid_constant__ GemmParams p) {
   pair_gemm_body<OUT_F32, A_MN, B_K, false, MODE>(tmA, tmB, tmOut, p, nullptr);
+}
+
+template <bool OUT_F32, bool B_K>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tg_gemm_pair_dual_kernel(const __grid_constant__ CUtensorMap tmA,
+                             const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmB2,
+                             const __grid_constant__ CUtensorMap tmOut,
+                             const __grid_constant__ GemmParams p) {
+  pair_gemm_body<OUT_F32, false, B_K, false, kModeDual>(tmA, tmB, tmOut, p, nullptr, &tmB2);
 }
 
 // The CTA-pair kernel with A read through row classes (float32 partials, forward layout).

@@ -14,6 +14,7 @@ namespace tg {
 
 struct GemmLaunch {
   CUtensorMap a, b, out;  // see tg_gemm_tc_kernel for the layouts each map describes
+  CUtensorMap b2;         // launch_gemm_dual: the second right operand
   GemmParams p;
   int grid;
   cudaStream_t stream;
@@ -71,6 +72,8 @@ cudaError_t launch_head_add(const GemmLaunch& l);
 // The fp16-output kernels whose epilogue is the scaled sum (kModeScaled; block_n 0: CTA pairs).
 // A^T B^T is not among the head's products and not a launch.
 cudaError_t launch_gemm_scaled(const GemmLaunch& l, int block_n);
+// The kernels with two right operands (kModeDual; block_n 0: CTA pairs).  A is stored M x K.
+cudaError_t launch_gemm_dual(const GemmLaunch& l, bool out_f32, int block_n);
 // Clusters of two that can be resident at once on the current device.
 cudaError_t gemm_pair_max_clusters(int* out);
 
@@ -107,6 +110,9 @@ struct GemmExtra {
   bool chained;         // logits or alpha: see GemmLaunch
   bool fold;            // fp16 output: M even, C has M / 2 rows, row r the sum of rows r and r + M / 2
   int64_t max_k;        // 0, or the K columns that one split may have (without logits and out32)
+  const void* B2;       // NULL, or a second right operand of B's layout, 16-byte aligned as B is: the
+  int64_t ldb2, b_k;    // product's K is twice k, k a multiple of 128; B and B2 have rows (or columns)
+                        // [0, b_k) of their k each, zeros from there on
   int64_t a_rows;       // 0, or the rows (>= M) that A, stored M x K and not copied, has in memory
 };
 tg_status gemm_extra(int ta, int tb, const void* A, const void* B, void* C, int64_t M, int64_t N,
@@ -129,7 +135,7 @@ cudaError_t launch_gated(const GatedLaunch& l);
 struct TilePlan {
   int pair, block_n, splits, num_kb, kb_per_split, units_cap;  // units_cap: CTAs or pairs at a time
 };
-tg_status plan_tiles(int64_t M, int64_t N, int64_t K, const tg_options* opt, TilePlan* out);
+tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, const tg_options* opt, TilePlan* out);
 
 // One 2-D fp16 tensor map, 128B swizzle; false if the driver refuses it.
 bool half_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
