@@ -11,13 +11,14 @@ import array
 
 import torch
 
+from . import binding
 from .tensors import check, here, library, on, param_type, stream_handle, written
+
+_KINDS = {torch.float16: binding.TG_TYPE_F16, torch.float32: binding.TG_TYPE_F32}
 
 
 def _dense(t, name):
     """Whether t's values fill its memory without gaps, in any order of dimensions."""
-    if t.is_contiguous():
-        return
     n = 1
     for stride, size in sorted((s, d) for s, d in zip(t.stride(), t.shape) if d != 1):
         if stride != n:
@@ -25,42 +26,45 @@ def _dense(t, name):
         n *= size
 
 
-def _clip(grads, outs, loss_scale, max_norm, stream):
-    dev = grads[0].get_device()
-    norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
-    words = []
-    for i, g in enumerate(grads):
-        kind = param_type(g, f"grads[{i}]")
-        if g.get_device() != dev:
-            raise ValueError("the gradients must be on one CUDA device")
-        _dense(g, f"grads[{i}]")
-        out = 0
-        out_kind = 0
-        if outs is not None:
-            out, out_kind = outs[i].data_ptr(), param_type(outs[i], f"out[{i}]")
-        words += (g.data_ptr(), out, g.numel(), kind | out_kind << 32)
-    table = array.array("Q", words)
-    check(library().tg_clip_gradients(table.buffer_info()[0], len(grads), loss_scale, max_norm,
+def _call(words, n, loss_scale, max_norm, device, dev):
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    table = array.array("Q", words)  # tg_gradient, four words each
+    check(library().tg_clip_gradients(table.buffer_info()[0], n, loss_scale, max_norm,
                                       norm.data_ptr(), stream_handle(dev)), "tg_clip_gradients")
     return norm
 
 
-def _gradients(grads):
-    grads = list(grads)
+def _kind(g, dev, i):
+    """The type of the i-th gradient, which is a dense tensor on device ``dev``.  Calls on few small
+    gradients are bound by this loop: what a good tensor needs is asked in one line."""
+    kind = _KINDS.get(g.dtype)
+    if kind is None or g.get_device() != dev or not g.is_contiguous():
+        param_type(g, f"grads[{i}]")
+        if g.get_device() != dev:
+            raise ValueError("the gradients must be on one CUDA device")
+        _dense(g, f"grads[{i}]")
+    return kind
+
+
+def _device(grads):
     if not grads:
         raise ValueError("no gradients")
-    if not all(g.is_cuda for g in grads):
+    if not grads[0].is_cuda:
         raise ValueError("the gradients must be CUDA tensors")
-    return grads
+    return grads[0].get_device()
 
 
 def gradient_norm(grads, loss_scale: float = 1.0, stream=None):
     """The norm of all of ``grads`` together over ``loss_scale``, a float32 scalar on their device."""
-    grads = _gradients(grads)
-    if not here(grads[0].get_device(), stream):
+    grads = list(grads)
+    dev = _device(grads)
+    if not here(dev, stream):
         with on(grads[0].device, stream, *grads):
-            return _clip(grads, None, loss_scale, float("inf"), None)
-    return _clip(grads, None, loss_scale, float("inf"), None)
+            return gradient_norm(grads, loss_scale)
+    words = []
+    for i, g in enumerate(grads):
+        words += (g.data_ptr(), 0, g.numel(), _kind(g, dev, i))
+    return _call(words, len(grads), loss_scale, float("inf"), grads[0].device, dev)
 
 
 def clip_gradients(grads, max_norm: float, loss_scale: float = 1.0, out=None, stream=None):
@@ -71,19 +75,28 @@ def clip_gradients(grads, max_norm: float, loss_scale: float = 1.0, out=None, st
     float32 tensors) is a list of fp16 or float32 tensors with their shapes and strides; it may be
     ``grads`` itself.  A norm that is not finite clips nothing, so that what overflowed stays to be seen.
     """
-    grads = _gradients(grads)
-    if not here(grads[0].get_device(), stream):
+    grads = list(grads)
+    dev = _device(grads)
+    if not here(dev, stream):
         with on(grads[0].device, stream, *grads, *(out or ())):
             return clip_gradients(grads, max_norm, loss_scale, out)
+    words = []
     if out is None:
-        out = [torch.empty_like(g, dtype=torch.float32, requires_grad=False) for g in grads]
+        out, like, kind32 = [], torch.empty_like, binding.TG_TYPE_F32 << 32
+        for i, g in enumerate(grads):
+            kind = _kind(g, dev, i)
+            o = like(g, dtype=torch.float32)
+            out.append(o)
+            words += (g.data_ptr(), o.data_ptr(), g.numel(), kind | kind32)
     else:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must have a tensor for each gradient")
-        for i, (o, g) in enumerate(zip(out, grads)):
-            if o.shape != g.shape or o.stride() != g.stride() or o.get_device() != g.get_device():
+        for i, (g, o) in enumerate(zip(grads, out)):
+            kind = _kind(g, dev, i)
+            if o.shape != g.shape or o.stride() != g.stride() or o.get_device() != dev:
                 raise ValueError(f"out[{i}] must have the shape, strides and device of grads[{i}]")
+            words += (g.data_ptr(), o.data_ptr(), g.numel(), kind | param_type(o, f"out[{i}]") << 32)
         for o in out:
             written(o)
-    return _clip(grads, out, loss_scale, max_norm, None), out
+    return _call(words, len(grads), loss_scale, max_norm, grads[0].device, dev), out

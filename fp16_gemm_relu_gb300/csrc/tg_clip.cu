@@ -20,17 +20,16 @@
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVec = 8;                                 // elements a thread takes at a time
-constexpr int kChunk = kThreads * kVec * 4;             // elements of a chunk
+constexpr int kChunk = kThreads * 32;                   // elements of a chunk, 32 of them a thread's
 constexpr int kTensors = 256;                           // tensors of a launch
-constexpr int kBlocksPerSm = 8;
+constexpr int kBlocksPerSm = 4;
 
 struct Tensor {
   const void* data;
   void* out;
   int64_t count;
   unsigned first;  // number of its first chunk in the launch
-  int kind;        // bit 0: float32 input, bit 1: float32 output, bit 2: vectors of kVec
+  int kind;        // bit 0: float32 input, bit 1: float32 output, bit 2: 16-byte vectors
 };
 struct Table {
   Tensor t[kTensors];
@@ -38,8 +37,9 @@ struct Table {
   unsigned chunks;
 };
 
-// The tensor that chunk c is of.
-__device__ __forceinline__ int tensor_of(const Table& tb, unsigned c) {
+// The tensor that chunk c is of: `at`, if it is still that one.
+__device__ __forceinline__ int tensor_of(const Table& tb, unsigned c, int at) {
+  if (tb.t[at].first <= c && (at + 1 == tb.n || c < tb.t[at + 1].first)) return at;
   int lo = 0, hi = tb.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -51,27 +51,59 @@ __device__ __forceinline__ int tensor_of(const Table& tb, unsigned c) {
   return lo;
 }
 
-template <bool F32>
-__device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&v)[kVec]) {
-  if constexpr (F32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p) + i);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      v[2 * j] = f.x;
-      v[2 * j + 1] = f.y;
-    }
+// E elements of one access: 8 fp16 or 4 float32 in 16 bytes, 4 fp16 in 8.
+template <bool F32, int E>
+struct Vec;
+template <>
+struct Vec<true, 4> {
+  float4 v;
+  __device__ __forceinline__ void load(const void* p) { v = *static_cast<const float4*>(p); }
+  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
+  __device__ __forceinline__ static void store(void* p, const float (&f)[4]) {
+    __stcs(static_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
   }
+};
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float load_one(const void* p, int64_t i, int kind) {
+__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+template <>
+struct Vec<false, 4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const void* p) { v = *static_cast<const uint2*>(p); }
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    unpack2(v.x, f[0], f[1]);
+    unpack2(v.y, f[2], f[3]);
+  }
+  __device__ __forceinline__ static void store(void* p, const float (&f)[4]) {
+    __stcs(static_cast<uint2*>(p), make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3])));
+  }
+};
+template <>
+struct Vec<false, 8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* p) { v = *static_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    unpack2(v.x, f[0], f[1]);
+    unpack2(v.y, f[2], f[3]);
+    unpack2(v.z, f[4], f[5]);
+    unpack2(v.w, f[6], f[7]);
+  }
+  __device__ __forceinline__ static void store(void* p, const float (&f)[8]) {
+    __stcs(static_cast<uint4*>(p), make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]),
+                                              pack2(f[6], f[7])));
+  }
+};
+
+__device__ __forceinline__ float load_one(const void* p, int i, int kind) {
   return kind & 1 ? static_cast<const float*>(p)[i] : __half2float(static_cast<const __half*>(p)[i]);
 }
-__device__ __forceinline__ void store_one(void* p, int64_t i, int kind, float v) {
+__device__ __forceinline__ void store_one(void* p, int i, int kind, float v) {
   if (kind & 2)
     static_cast<float*>(p)[i] = v;
   else
@@ -84,41 +116,68 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-template <bool F32>
-__device__ __forceinline__ void squares(const void* p, int64_t i0, int64_t n, float (&s)[4]) {
+// A thread's accesses of a chunk of n elements, E elements each and kThreads E apart: load(v, k) and then
+// use(v) of each.  Those of a whole chunk are all in flight together.
+template <int E, typename V, typename L, typename U>
+__device__ __forceinline__ void accesses(int n, L load, U use) {
+  if (n == kChunk) {
+    V v[32 / E];
 #pragma unroll
-  for (int k = 0; k < kChunk / (kThreads * kVec); ++k) {
-    const int64_t i = i0 + (int64_t(k) * kThreads + threadIdx.x) * kVec;
-    if (i + kVec <= n) {
-      float v[kVec];
-      load_vec<F32>(p, i, v);
+    for (int k = 0; k < 32 / E; ++k) load(v[k], k);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) s[j & 3] = fmaf(v[j], v[j], s[j & 3]);
-    } else {
-      for (int64_t j = i; j < n; ++j) {
-        const float v = load_one(p, j, F32 ? 1 : 0);
-        s[0] = fmaf(v, v, s[0]);
-      }
+    for (int k = 0; k < 32 / E; ++k) use(v[k], k);
+  } else {
+    const int left = n / E - static_cast<int>(threadIdx.x);
+#pragma unroll 1
+    for (int k = 0; k * kThreads < left; ++k) {
+      V v;
+      load(v, k);
+      use(v, k);
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
+// Squares of n elements, n <= kChunk.
+template <bool F32>
+__device__ __forceinline__ void squares(const void* p, int n, float (&s)[4]) {
+  constexpr int E = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
+  const uint8_t* base = static_cast<const uint8_t*>(p) + threadIdx.x * (E * kSize);
+  using V = Vec<F32, E>;
+  accesses<E, V>(n, [&](V& v, int k) { v.load(base + k * (kThreads * E * kSize)); }, [&](const V& v, int) {
+    float f[E];
+    v.get(f);
+#pragma unroll
+    for (int j = 0; j < E; ++j) s[j & 3] = fmaf(f[j], f[j], s[j & 3]);
+  });
+  const int i = n / E * E + static_cast<int>(threadIdx.x);
+  if (i < n) {
+    const float f = load_one(p, i, F32 ? 1 : 0);
+    s[0] = fmaf(f, f, s[0]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     tg_grad_squares_kernel(const __grid_constant__ Table tb, float* part) {
   __shared__ float slots[kThreads / 32];
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  tg::chain_wait();
+  tg::chain_release();
+  int at = 0;
   for (unsigned c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
-    const Tensor& t = tb.t[tensor_of(tb, c)];
-    const int64_t i0 = int64_t(c - t.first) * kChunk, n = min(t.count, i0 + kChunk);
+    at = tensor_of(tb, c, at);
+    const Tensor& t = tb.t[at];
+    const int64_t i0 = int64_t(c - t.first) * kChunk;
+    const int n = static_cast<int>(min(t.count - i0, int64_t(kChunk)));
+    const void* p = static_cast<const uint8_t*>(t.data) + i0 * (t.kind & 1 ? 4 : 2);
     if (!(t.kind & 4)) {
-      for (int64_t i = i0 + threadIdx.x; i < n; i += kThreads) {
-        const float v = load_one(t.data, i, t.kind);
+      for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float v = load_one(p, i, t.kind);
         s[0] = fmaf(v, v, s[0]);
       }
     } else if (t.kind & 1) {
-      squares<true>(t.data, i0, n, s);
+      squares<true>(p, n, s);
     } else {
-      squares<false>(t.data, i0, n, s);
+      squares<false>(p, n, s);
     }
   }
   const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
@@ -130,77 +189,78 @@ __global__ void __launch_bounds__(kThreads)
   part[blockIdx.x] = sum;
 }
 
-// The norm from the blocks' sums, added in float64, and the gradients' factor: by every block alike.
-// A norm that is not finite clips nothing.
+// The norm from the blocks' sums, added in float64, and the gradients' factor: by every block alike, in one
+// warp of it (float64 is slow here: in every thread it took 16 us).  A norm that is not finite clips nothing.
 __device__ __forceinline__ float factor_of(const float* part, int parts, float scale, float max_norm,
                                            float* norm) {
-  __shared__ double slots[kThreads / 32];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
+  __shared__ float factor;
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < parts; i += 32) s += __ldcg(part + i);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = s;
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (threadIdx.x == 0) {
+      const double r = sqrt(s) / scale;
+      if (norm && blockIdx.x == 0) *norm = static_cast<float>(r);
+      const double c = r > max_norm && r < INFINITY ? max_norm / r : 1.0;
+      factor = static_cast<float>(c / scale);
+    }
+  }
   __syncthreads();
-  s = 0.0;
-  for (int i = 0; i < kThreads / 32; ++i) s += slots[i];
-  const double r = sqrt(s) / scale;
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(r);
-  const double c = r > max_norm && r < INFINITY ? max_norm / r : 1.0;
-  return static_cast<float>(c / scale);
+  return factor;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     tg_grad_norm_kernel(const float* part, int parts, float scale, float* norm) {
+  tg::chain_wait();
   factor_of(part, parts, scale, INFINITY, norm);
 }
 
+// n elements times f, n <= kChunk.  An access is as wide as lets the lanes of a warp write one contiguous
+// piece: 8-byte loads of fp16 for 16-byte stores of float32 (with 16-byte loads, whose 32 bytes of output a
+// lane writes in two stores, 1.3 billion values took 1717 us, so 1300).
 template <bool F32, bool OUT32>
-__device__ __forceinline__ void scaled(const Tensor& t, int64_t i0, int64_t n, float f) {
-  float v[kChunk / (kThreads * kVec)][kVec];
+__device__ __forceinline__ void scaled(const void* p, void* o, int n, float f) {
+  constexpr int E = F32 || OUT32 ? 4 : 8, kSize = F32 ? 4 : 2, kOutSize = OUT32 ? 4 : 2;
+  const uint8_t* base = static_cast<const uint8_t*>(p) + threadIdx.x * (E * kSize);
+  uint8_t* out = static_cast<uint8_t*>(o) + threadIdx.x * (E * kOutSize);
+  using V = Vec<F32, E>;
+  accesses<E, V>(n, [&](V& v, int k) { v.load(base + k * (kThreads * E * kSize)); }, [&](const V& v, int k) {
+    float x[E];
+    v.get(x);
 #pragma unroll
-  for (int k = 0; k < kChunk / (kThreads * kVec); ++k) {
-    const int64_t i = i0 + (int64_t(k) * kThreads + threadIdx.x) * kVec;
-    if (i + kVec <= n) load_vec<F32>(t.data, i, v[k]);
-  }
-#pragma unroll
-  for (int k = 0; k < kChunk / (kThreads * kVec); ++k) {
-    const int64_t i = i0 + (int64_t(k) * kThreads + threadIdx.x) * kVec;
-    if (i + kVec <= n) {
-      if constexpr (OUT32) {
-        float4* d = reinterpret_cast<float4*>(static_cast<float*>(t.out) + i);
-        d[0] = make_float4(v[k][0] * f, v[k][1] * f, v[k][2] * f, v[k][3] * f);
-        d[1] = make_float4(v[k][4] * f, v[k][5] * f, v[k][6] * f, v[k][7] * f);
-      } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __half2 h = __floats2half2_rn(v[k][2 * j] * f, v[k][2 * j + 1] * f);
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(static_cast<__half*>(t.out) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-      for (int64_t j = i; j < n; ++j)
-        store_one(t.out, j, OUT32 ? 2 : 0, load_one(t.data, j, F32 ? 1 : 0) * f);
-    }
-  }
+    for (int j = 0; j < E; ++j) x[j] *= f;
+    Vec<OUT32, E>::store(out + k * (kThreads * E * kOutSize), x);
+  });
+  const int i = n / E * E + static_cast<int>(threadIdx.x);
+  if (i < n) store_one(o, i, OUT32 ? 2 : 0, load_one(p, i, F32 ? 1 : 0) * f);
 }
 
-__global__ void __launch_bounds__(kThreads)
+// The chunks are taken from the last one back: what the pass before read last is still in L2.
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     tg_grad_clip_kernel(const __grid_constant__ Table tb, const float* part, int parts, float scale,
                         float max_norm, float* norm) {
+  tg::chain_wait();
+  tg::chain_release();
   const float f = factor_of(part, parts, scale, max_norm, norm);
-  for (unsigned c = blockIdx.x; c < tb.chunks; c += gridDim.x) {
-    const Tensor& t = tb.t[tensor_of(tb, c)];
-    const int64_t i0 = int64_t(c - t.first) * kChunk, n = min(t.count, i0 + kChunk);
+  int at = tb.n - 1;
+  for (unsigned b = blockIdx.x; b < tb.chunks; b += gridDim.x) {
+    const unsigned c = tb.chunks - 1 - b;
+    at = tensor_of(tb, c, at);
+    const Tensor& t = tb.t[at];
+    const int64_t i0 = int64_t(c - t.first) * kChunk;
+    const int n = static_cast<int>(min(t.count - i0, int64_t(kChunk)));
+    const void* p = static_cast<const uint8_t*>(t.data) + i0 * (t.kind & 1 ? 4 : 2);
+    void* o = static_cast<uint8_t*>(t.out) + i0 * (t.kind & 2 ? 4 : 2);
     switch (t.kind) {
-      case 4: scaled<false, false>(t, i0, n, f); break;
-      case 5: scaled<true, false>(t, i0, n, f); break;
-      case 6: scaled<false, true>(t, i0, n, f); break;
-      case 7: scaled<true, true>(t, i0, n, f); break;
+      case 4: scaled<false, false>(p, o, n, f); break;
+      case 5: scaled<true, false>(p, o, n, f); break;
+      case 6: scaled<false, true>(p, o, n, f); break;
+      case 7: scaled<true, true>(p, o, n, f); break;
       default:
-        for (int64_t i = i0 + threadIdx.x; i < n; i += kThreads)
-          store_one(t.out, i, t.kind, load_one(t.data, i, t.kind) * f);
+        for (int i = threadIdx.x; i < n; i += kThreads)
+          store_one(o, i, t.kind, load_one(p, i, t.kind) * f);
     }
   }
 }
@@ -243,7 +303,7 @@ tg_status check(const tg_gradient* list, int64_t n, bool outs) {
     if (it != written.end() && it->first < b) return TG_ERR_INVALID_ARG;
     if (it == written.begin()) continue;
     --it;
-    if (it->second > a && !(g.out == g.data)) return TG_ERR_INVALID_ARG;
+    if (it->second > a && g.out != g.data) return TG_ERR_INVALID_ARG;
   }
   return TG_OK;
 }
@@ -301,15 +361,14 @@ extern "C" tg_status tg_clip_gradients(const tg_gradient* list, int64_t n, float
       at += grid;
     }
     if (e == cudaSuccess && !outs) {
-      tg_grad_norm_kernel<<<1, kThreads, 0, stream>>>(part, static_cast<int>(parts), scale, norm);
-      e = cudaGetLastError();
+      e = tg::launch_chained(tg_grad_norm_kernel, true, dim3(1), kThreads, 0, stream, part,
+                             static_cast<int>(parts), scale, norm);
     }
     for (const Table& tb : tables) {
       if (e != cudaSuccess || !outs) break;
       const int grid = static_cast<int>(std::min<int64_t>(std::max(tb.chunks, 1u), most));
-      tg_grad_clip_kernel<<<grid, kThreads, 0, stream>>>(tb, part, static_cast<int>(parts), scale,
-                                                         max_norm, norm);
-      e = cudaGetLastError();
+      e = tg::launch_chained(tg_grad_clip_kernel, true, dim3(grid), kThreads, 0, stream, tb, part,
+                             static_cast<int>(parts), scale, max_norm, norm);
     }
     const cudaError_t fe = cudaFreeAsync(part, stream);
     if (e == cudaSuccess) e = fe;

@@ -31,41 +31,6 @@ constexpr int64_t kMaxLd = int64_t{1} << 36;
 // Longer sums are taken in splits that are added in float32.
 constexpr int64_t kSumLength = 32768;
 
-// fp16 values of 8 columns from `col` on to a row, 16 bytes at once where the row allows it.
-__device__ __forceinline__ void store8(__half* row, int64_t col, int64_t n, const float (&v)[8]) {
-  __half* d = row + col;
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  if (col + 8 <= n && (reinterpret_cast<uintptr_t>(d) & 15u) == 0) {
-    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < n)
-        reinterpret_cast<unsigned short*>(d)[i] = static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
-  }
-}
-__device__ __forceinline__ void load8(const __half* row, int64_t col, int64_t n, float (&v)[8]) {
-  const __half* s = row + col;
-  if (col + 8 <= n && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(s));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < n ? __half2float(s[i]) : 0.0f;
-  }
-}
-
 // H (and gate, up) from the K splits' float32 partial sums, added in order; four columns a thread and the
 // loads of kAhead splits in flight.  A split's rows hold the gates and, nw columns further, the ups.
 constexpr int kAhead = 4;
@@ -114,31 +79,78 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-// dG and dU (fp16, M x np each, rows of ld; zeros from column N on), eight columns a thread.
-__global__ void __launch_bounds__(256)
+// Eight packed values of a row from column `col` on, zeros past n; 16 bytes at once where the row allows it.
+__device__ __forceinline__ uint4 load8(const __half* row, int64_t col, int64_t n) {
+  const __half* s = row + col;
+  if (col + 8 <= n && (reinterpret_cast<uintptr_t>(s) & 15u) == 0)
+    return __ldcs(reinterpret_cast<const uint4*>(s));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col + i < n) w[i >> 1] |= static_cast<uint32_t>(__half_as_ushort(s[i])) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float2 half2_of(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// dG and dU (fp16, M x np each, rows of ld; zeros from column N on), eight columns of kGradRows rows a
+// thread, whose loads go out together.
+constexpr int kGradRows = 2;
+template <int ACT>
+__global__ void __launch_bounds__(256, 4)
     tg_gated_grad_kernel(const __half* __restrict__ dh, int64_t lddh, const __half* __restrict__ gate,
-                         int64_t ldg, const __half* __restrict__ up, int64_t ldu, int act,
-                         __half* out, int64_t ld, int64_t np, int64_t M, int64_t N) {
+                         int64_t ldg, const __half* __restrict__ up, int64_t ldu, __half* out, int64_t ld,
+                         int64_t np, int64_t M, int64_t N) {
   const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   if (c >= np) return;
-  for (int64_t r = blockIdx.y; r < M; r += gridDim.y) {
-    float d[8], g[8], u[8], dg[8], du[8];
-    load8(dh + r * lddh, c, N, d);
-    load8(gate + r * ldg, c, N, g);
-    load8(up + r * ldu, c, N, u);
+  for (int64_t r0 = int64_t(blockIdx.y) * kGradRows; r0 < M; r0 += int64_t(gridDim.y) * kGradRows) {
+    uint4 d[kGradRows], g[kGradRows], u[kGradRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dg[i] = d[i] * (u[i] * gated_slope(g[i], act));
-      du[i] = d[i] * gated_activation(g[i], act);
+    for (int i = 0; i < kGradRows; ++i) {
+      if (r0 + i >= M) break;
+      d[i] = load8(dh + (r0 + i) * lddh, c, N);
+      g[i] = load8(gate + (r0 + i) * ldg, c, N);
+      u[i] = load8(up + (r0 + i) * ldu, c, N);
     }
-    store8(out + r * ld, c, np, dg);
-    store8(out + r * ld + np, c, np, du);
+#pragma unroll
+    for (int i = 0; i < kGradRows; ++i) {
+      if (r0 + i >= M) break;
+      const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w}, gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w},
+                     uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 dv = half2_of(dw[j]), gv = half2_of(gw[j]), uv = half2_of(uw[j]);
+        a[j] = pack2(dv.x * (uv.x * gated_slope(gv.x, ACT)), dv.y * (uv.y * gated_slope(gv.y, ACT)));
+        b[j] = pack2(dv.x * gated_activation(gv.x, ACT), dv.y * gated_activation(gv.y, ACT));
+      }
+      *reinterpret_cast<uint4*>(out + (r0 + i) * ld + c) = make_uint4(a[0], a[1], a[2], a[3]);
+      *reinterpret_cast<uint4*>(out + (r0 + i) * ld + np + c) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
   }
 }
 
-dim3 row_grid(int64_t cols, int64_t rows) {
-  return dim3(static_cast<unsigned>(cdiv(cols, 2048)),
-              static_cast<unsigned>(std::min<int64_t>(std::max<int64_t>(rows, 1), 65535)));
+cudaError_t launch_grad(int act, const __half* dh, int64_t lddh, const __half* gate, int64_t ldg,
+                        const __half* up, int64_t ldu, __half* out, int64_t ld, int64_t np, int64_t M,
+                        int64_t N, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(cdiv(np, 2048)),
+                  static_cast<unsigned>(std::min<int64_t>(cdiv(M, kGradRows), 65535)));
+  auto go = [&](auto kern) {
+    kern<<<grid, 256, 0, stream>>>(dh, lddh, gate, ldg, up, ldu, out, ld, np, M, N);
+    return cudaGetLastError();
+  };
+  switch (act) {
+    case TG_ACT_SILU: return go(tg_gated_grad_kernel<TG_ACT_SILU>);
+    case TG_ACT_RELU: return go(tg_gated_grad_kernel<TG_ACT_RELU>);
+    case TG_ACT_GELU: return go(tg_gated_grad_kernel<TG_ACT_GELU>);
+    case TG_ACT_GELU_TANH: return go(tg_gated_grad_kernel<TG_ACT_GELU_TANH>);
+    default: return go(tg_gated_grad_kernel<TG_ACT_NONE>);
+  }
 }
 
 struct Gated {
@@ -354,10 +366,9 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
     return s == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : s;
   };
   __half* g = reinterpret_cast<__half*>(mem + at_g);
-  tg_gated_grad_kernel<<<row_grid(np, M), 256, 0, stream>>>(
-      static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
-      static_cast<const __half*>(up), ldup, activation, g, ld, np, M, N);
-  if ((e = cudaGetLastError()) != cudaSuccess) return done(tg::record_cuda_error(e));
+  e = launch_grad(activation, static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
+                  static_cast<const __half*>(up), ldup, g, ld, np, M, N, stream);
+  if (e != cudaSuccess) return done(tg::record_cuda_error(e));
   if ((e = ops.copy(a, mem, sms, stream)) != cudaSuccess) return done(tg::record_cuda_error(e));
   tg::GemmExtra ex;
   std::memset(&ex, 0, sizeof(ex));

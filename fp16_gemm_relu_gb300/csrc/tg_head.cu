@@ -306,15 +306,19 @@ __device__ __forceinline__ float grad_value(float z, float c, float lse2, float 
 // it.  Bound by HBM: 6 bytes an element, 4096 x 131072 in 456 us, 7.0 TB/s.
 // FINE (few tokens): each value in two parts, G and `lo` elements further what its rounding left; and
 // X's rows (16-byte aligned, of `width`) twice over, for the product with both parts.
-template <bool FINE>
+// RAW: the rows hold their weights, whose largest is *wmax; alpha is written here (s: its scale).
+template <bool FINE, bool RAW>
 __global__ void __launch_bounds__(256)
     tg_head_grad_kernel(const float* z, int64_t ldz, float c, const RowInfo* info, int64_t rows,
                         int64_t vocab, uint16_t* __restrict__ g, int64_t ldg, int64_t lo,
                         const uint16_t* __restrict__ x, int64_t ldx, uint16_t* __restrict__ x2,
-                        int64_t ldx2, int width) {
+                        int64_t ldx2, int width, const unsigned* wmax, float s, float* alpha) {
   const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   tg::chain_wait();
   tg::chain_release();
+  const float most = RAW ? __uint_as_float(*wmax) : 0.0f;
+  if (RAW && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    *alpha = s * (most == most ? most : 1.0f) / kGScale;  // rows that do not count stay 0
   if (FINE && x2 != nullptr && blockIdx.x == 0) {
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
       const uint16_t* from = x + r * ldx;
@@ -328,7 +332,8 @@ __global__ void __launch_bounds__(256)
   }
   if (v0 >= vocab) return;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    const RowInfo ri = info[r];
+    RowInfo ri = info[r];
+    if (RAW && ri.target >= 0) ri.gs = most != most ? most : row_factor(ri.gs, most);
     const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
     const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
     const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -399,13 +404,21 @@ struct Objective {
 };
 enum : int { kPreference = 1, kPolicy = 2 };
 
-// What the kernels of an objective share: max|w| over the rows as for cross entropy, whether any pair's
-// offsets are wrong, and (preference) the weight of a counted row of each sequence.
-struct Shared {
+// Where an objective's weights go: max|w| over the rows as for cross entropy, NaN if any pair's offsets are
+// wrong; and each row's, into its RowInfo::gs (the factor 2^15 / max|w| is taken in the pass over the logits) or
+// into w, which is zero before.
+struct Weights {
   unsigned* wmax;
-  int* bad;
-  float* coef;  // [2 pairs]
+  RowInfo* info;
+  float* w;
+  __device__ __forceinline__ void put(int64_t row, float v) const {
+    if (info)
+      info[row].gs = v;
+    else
+      w[row] = v;
+  }
 };
+constexpr unsigned kNanBits = 0x7fc00000u;  // above all finite numbers' bits
 
 // Bits of |w| where it is finite, else 0: see tg_head_weight_kernel.
 __device__ __forceinline__ unsigned weight_bits(float w) {
@@ -413,65 +426,83 @@ __device__ __forceinline__ unsigned weight_bits(float w) {
 }
 
 constexpr int kPairThreads = 256;
-__device__ __forceinline__ double block_sum(double v, double* slots) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int i = 0; i < kPairThreads / 32; ++i) v += slots[i];
-  return v;
-}
 
 // A block a pair (Rafailov et al., 2023, with smoothed labels):
 //   r_s = sum over a sequence's counted rows of logp - reference (average: their mean; none: 0)
 //   m = beta (r_chosen - r_rejected),   loss = -(1 - e) log sigma(m) - e log sigma(-m)
-// The sums are float64: those of a long answer are large and nearly the same in both.
+// The sums are float64: those of a long answer are large and nearly the same in both.  Bound by latency:
+// one pass over the rows of both sequences and one meeting of the block.
 __global__ void __launch_bounds__(kPairThreads)
     tg_head_pairs_kernel(Objective ob, const float* nll, const int64_t* __restrict__ target,
-                         int64_t ignore, int64_t rows, Shared sh) {
-  __shared__ double slots[4][kPairThreads / 32];
+                         int64_t ignore, int64_t rows, Weights wt) {
+  __shared__ double sums[2][kPairThreads / 32];
+  __shared__ int counts[2][kPairThreads / 32];
   const int64_t p = blockIdx.x;
-  tg::chain_wait();
-  tg::chain_release();
   const int64_t o[3] = {ob.offsets[2 * p], ob.offsets[2 * p + 1], ob.offsets[2 * p + 2]};
   const bool fits = o[0] >= 0 && o[0] <= o[1] && o[1] <= o[2] && o[2] <= rows;
-  double r[2], n[2];
+  tg::chain_wait();
+  tg::chain_release();
+  double r[2] = {0.0, 0.0}, n[2];
+  int count[2] = {0, 0};
+  for (int64_t t = o[0] + threadIdx.x; fits && t < o[2]; t += kPairThreads) {
+    if (target[t] == ignore) continue;
+    const double d = -static_cast<double>(nll[t]) - (ob.reference ? ob.reference[t] : 0.0f);
+    if (t < o[1]) {
+      r[0] += d;
+      ++count[0];
+    } else {
+      r[1] += d;
+      ++count[1];
+    }
+  }
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    double sum = 0.0, count = 0.0;
-    for (int64_t t = o[s] + threadIdx.x; fits && t < o[s + 1]; t += kPairThreads) {
-      if (target[t] == ignore) continue;
-      sum -= nll[t];
-      if (ob.reference) sum -= ob.reference[t];
-      count += 1.0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) r[s] += __shfl_xor_sync(0xffffffffu, r[s], d);
+    count[s] = __reduce_add_sync(0xffffffffu, count[s]);
+    if ((threadIdx.x & 31) == 0) {
+      sums[s][threadIdx.x >> 5] = r[s];
+      counts[s][threadIdx.x >> 5] = count[s];
     }
-    sum = block_sum(sum, slots[2 * s]);
-    n[s] = block_sum(count, slots[2 * s + 1]);
-    if (!ob.average || n[s] < 1.0) n[s] = 1.0;
-    r[s] = sum / n[s];
   }
-  if (threadIdx.x != 0) return;
-  const float m = static_cast<float>(ob.beta * (r[0] - r[1]));
-  const float away = expf(-fabsf(m)), soft = log1pf(away);       // log(1 + e^-|m|)
-  const float sigma = (m > 0.0f ? away : 1.0f) / (1.0f + away);  // sigma(-m)
-  float loss = (1.0f - ob.smooth) * (soft + fmaxf(-m, 0.0f)) + ob.smooth * (soft + fmaxf(m, 0.0f));
-  if (!fits || m != m) loss = NAN;
-  if (ob.loss) ob.loss[p] = loss;
-  if (ob.ratios) {
-    ob.ratios[2 * p] = fits ? static_cast<float>(r[0]) : NAN;
-    ob.ratios[2 * p + 1] = fits ? static_cast<float>(r[1]) : NAN;
+  __syncthreads();
+  __shared__ float weight[2];
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      r[s] = 0.0;
+      count[s] = 0;
+      for (int i = 0; i < kPairThreads / 32; ++i) {
+        r[s] += sums[s][i];
+        count[s] += counts[s][i];
+      }
+      n[s] = ob.average && count[s] > 0 ? count[s] : 1;
+      r[s] /= n[s];
+    }
+    const float m = static_cast<float>(ob.beta * (r[0] - r[1]));
+    const float away = expf(-fabsf(m)), soft = log1pf(away);       // log(1 + e^-|m|)
+    const float sigma = (m > 0.0f ? away : 1.0f) / (1.0f + away);  // sigma(-m)
+    float loss = (1.0f - ob.smooth) * (soft + fmaxf(-m, 0.0f)) + ob.smooth * (soft + fmaxf(m, 0.0f));
+    if (!fits || m != m) loss = NAN;
+    if (ob.loss) ob.loss[p] = loss;
+    if (ob.ratios) {
+      ob.ratios[2 * p] = fits ? static_cast<float>(r[0]) : NAN;
+      ob.ratios[2 * p + 1] = fits ? static_cast<float>(r[1]) : NAN;
+    }
+    if (ob.dloss) {
+      // d loss / d m = e - sigma(-m), and w is the slope along nll
+      const float slope = ob.beta * (sigma - ob.smooth) * ob.dloss[p];
+      weight[0] = static_cast<float>(slope / n[0]);
+      weight[1] = static_cast<float>(-slope / n[1]);
+      const unsigned most = max(count[0] > 0 ? weight_bits(weight[0]) : 0u,
+                                count[1] > 0 ? weight_bits(weight[1]) : 0u);
+      atomicMax(wt.wmax, fits ? most : kNanBits);
+    }
   }
   if (!ob.dloss) return;
-  if (!fits) *sh.bad = 1;
-  // d loss / d m = e - sigma(-m), and w is the slope along nll
-  const float slope = ob.beta * (sigma - ob.smooth) * ob.dloss[p];
-  const float w[2] = {static_cast<float>(slope / n[0]), static_cast<float>(-slope / n[1])};
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    sh.coef[2 * p + s] = w[s];
-    if (fits && o[s + 1] > o[s]) atomicMax(sh.wmax, weight_bits(w[s]));
-  }
+  __syncthreads();
+  for (int64_t t = o[0] + threadIdx.x; fits && t < o[2]; t += kPairThreads)
+    if (target[t] != ignore) wt.put(t, weight[t >= o[1]]);
 }
 
 // A thread a row (Schulman et al., 2017; the penalty's unbiased, never negative estimate is Schulman's
@@ -481,7 +512,7 @@ __global__ void __launch_bounds__(kPairThreads)
 // are such that a NaN goes through.
 __global__ void __launch_bounds__(256)
     tg_head_policy_kernel(Objective ob, const float* nll, const int64_t* __restrict__ target,
-                          int64_t ignore, int64_t rows, float* w, Shared sh) {
+                          int64_t ignore, int64_t rows, Weights wt) {
   const int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
   tg::chain_wait();
   tg::chain_release();
@@ -504,47 +535,22 @@ __global__ void __launch_bounds__(256)
     }
     if (ob.loss) ob.loss[r] = loss;
     if (ob.logp) ob.logp[r] = logp;
-    if (ob.dloss) {
-      w[r] = target[r] != ignore ? -slope * ob.dloss[r] : 0.0f;
-      most = weight_bits(w[r]);
+    if (ob.dloss && target[r] != ignore) {
+      const float w = -slope * ob.dloss[r];
+      wt.put(r, w);
+      most = weight_bits(w);
     }
   }
   if (!ob.dloss) return;
   most = __reduce_max_sync(0xffffffffu, most);
-  if ((threadIdx.x & 31) == 0 && most) atomicMax(sh.wmax, most);
+  if ((threadIdx.x & 31) == 0 && most) atomicMax(wt.wmax, most);
 }
 
-// The rows' weights: from `w` (policy), or from their sequence's (preference; 0 outside of all of them).
-// With info: the factor of each counted row of G and alpha, as tg_head_rows_kernel gives them.  Without:
-// the weights themselves into w_out.
+// Every row's weight NaN if any pair's offsets are wrong.
 __global__ void __launch_bounds__(256)
-    tg_head_factor_kernel(Objective ob, const int64_t* __restrict__ target, int64_t ignore,
-                          int64_t rows, const float* w, Shared sh, float scale, RowInfo* info,
-                          float* alpha, float* w_out) {
+    tg_head_spoil_kernel(const unsigned* wmax, float* w, int64_t rows) {
   const int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
-  tg::chain_wait();
-  tg::chain_release();
-  const float most = __uint_as_float(*sh.wmax);
-  if (alpha && r == 0) *alpha = scale * most / kGScale;
-  if (r >= rows) return;
-  float v = 0.0f;
-  if (w) {
-    v = w[r];
-  } else if (*sh.bad) {
-    v = NAN;
-  } else if (target[r] != ignore && ob.pairs > 0 && r >= ob.offsets[0] && r < ob.offsets[2 * ob.pairs]) {
-    int64_t lo = 0, hi = 2 * ob.pairs - 1;  // the last sequence that begins at or before r
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (ob.offsets[mid] <= r)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    v = sh.coef[lo];
-  }
-  if (w_out) w_out[r] = v;
-  if (info && info[r].target >= 0) info[r].gs = row_factor(v, most);
+  if (r < rows && *wmax == kNanBits) w[r] = NAN;
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -678,15 +684,15 @@ int64_t piece_of(const Head& h, int64_t per_row, int64_t budget) {
 }
 
 // An objective's losses and weights from nll (chained: the launch before it is a kernel).
-cudaError_t launch_objective(const Head& h, const float* nll, float* w, const Shared& sh, bool chained,
+cudaError_t launch_objective(const Head& h, const float* nll, const Weights& wt, bool chained,
                              cudaStream_t stream) {
   const Objective& ob = h.ob;
   if (ob.kind == kPolicy)
     return tg::launch_chained(tg_head_policy_kernel, chained, dim3(static_cast<unsigned>(cdiv(h.T, 256))),
-                              256, 0, stream, ob, nll, h.index, h.ignore, h.T, w, sh);
+                              256, 0, stream, ob, nll, h.index, h.ignore, h.T, wt);
   if (ob.pairs == 0) return cudaSuccess;
   return tg::launch_chained(tg_head_pairs_kernel, chained, dim3(static_cast<unsigned>(ob.pairs)),
-                            kPairThreads, 0, stream, ob, nll, h.index, h.ignore, h.T, sh);
+                            kPairThreads, 0, stream, ob, nll, h.index, h.ignore, h.T, wt);
 }
 
 tg_status run_head(const Head& h, cudaStream_t stream) {
@@ -729,9 +735,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
   const int64_t at_stats = lay.add(tiles * piece * int64_t(sizeof(float2)));
   const int64_t at_picked = lay.add(store ? 0 : piece * std::max(h.top, 1) * 4);
   const int64_t at_info = lay.add(piece * int64_t(sizeof(RowInfo)));
-  const int64_t at_small = lay.add(3 * 4);
+  const int64_t at_small = lay.add(2 * 4);
   const int64_t at_nll = lay.add(objective ? h.T * 4 : 0);
-  const int64_t at_weights = lay.add(objective ? std::max(h.T, 2 * h.ob.pairs) * 4 : 0);
   const int64_t at_g = lay.add(grad ? std::max(parts * piece, kLeastRows) * ldg * 2 : 0);
   const int64_t at_x2 = lay.add(fine && h.dW ? 2 * h.T * ldxp * 2 : 0);
   const int64_t at_q = lay.add(grad && h.top ? piece * h.top * 4 : 0);
@@ -773,7 +778,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     ldw = ldwp;
   }
   if (objective) {
-    if ((e = cudaMemsetAsync(wmax, 0, 3 * 4, stream)) != cudaSuccess)
+    if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess)
       return done(tg::record_cuda_error(e));
   } else if (grad) {
     // one block for what it can read in a few microseconds, else several on a zeroed maximum
@@ -837,22 +842,19 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
         h.lse ? h.lse + t0 : nullptr, info, q, objective ? nullptr : alpha);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     if (objective) {
-      float* weights = reinterpret_cast<float*>(mem + at_weights);
-      const Shared sh{wmax, reinterpret_cast<int*>(wmax) + 2, weights};
-      const bool policy = h.ob.kind == kPolicy;
-      if ((e = launch_objective(h, nll, weights, sh, true, stream)) != cudaSuccess)
-        return done(tg::record_cuda_error(e));
-      chain(tg_head_factor_kernel, dim3(static_cast<unsigned>(cdiv(h.T, 256))), 256, h.ob, h.index,
-            h.ignore, h.T, policy ? weights : nullptr, sh, h.scale, info, alpha, nullptr);
+      e = launch_objective(h, nll, Weights{wmax, info, nullptr}, true, stream);
       if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     }
     if (!grad) continue;
     const int64_t lo = fine ? n * ldg : 0;
     uint16_t* x2 = fine && h.dW ? reinterpret_cast<uint16_t*>(mem + at_x2) : nullptr;
-    chain(fine ? tg_head_grad_kernel<true> : tg_head_grad_kernel<false>,
+    auto grad_kernel = objective ? (fine ? tg_head_grad_kernel<true, true> : tg_head_grad_kernel<false, true>)
+                                 : (fine ? tg_head_grad_kernel<true, false> : tg_head_grad_kernel<false, false>);
+    chain(grad_kernel,
           dim3(static_cast<unsigned>(cdiv(h.V, 2048)),
                static_cast<unsigned>(std::min<int64_t>(n, 65535))),
-          256, z, ldz, c, info, n, h.V, g, ldg, lo, x, ldx, x2, ldxp, static_cast<int>(h.D));
+          256, z, ldz, c, info, n, h.V, g, ldg, lo, x, ldx, x2, ldxp, static_cast<int>(h.D), wmax, h.scale,
+          alpha);
     if (h.top)
       chain(tg_head_teacher_grad_kernel, dim3(static_cast<unsigned>(cdiv(n, 4))), 128, index, h.ldt,
             h.top, q, z, ldz, c, info, n, h.V, reinterpret_cast<__half*>(g), ldg, lo);
@@ -980,16 +982,15 @@ tg_status run_objective(const Head& h, cudaStream_t stream) {
   unsigned* err = nullptr;
   if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
   Layout lay;
-  const int64_t at_nll = lay.add(h.T * 4), at_w = lay.add(grad ? h.T * 4 : 0);
-  const int64_t at_coef = lay.add(grad ? 2 * ob.pairs * 4 : 0), at_small = lay.add(3 * 4);
+  // (the weights are zeroed together with their maximum)
+  const int64_t at_nll = lay.add(h.T * 4), at_small = lay.add(4), at_w = lay.add(grad ? h.T * 4 : 0);
   uint8_t* mem = nullptr;
   if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
   float* nll = reinterpret_cast<float*>(mem + at_nll);
   float* w = reinterpret_cast<float*>(mem + at_w);
-  const Shared sh{reinterpret_cast<unsigned*>(mem + at_small), reinterpret_cast<int*>(mem + at_small) + 2,
-                  reinterpret_cast<float*>(mem + at_coef)};
-  cudaError_t e = cudaMemsetAsync(sh.wmax, 0, 3 * 4, stream);
+  const Weights wt{reinterpret_cast<unsigned*>(mem + at_small), nullptr, w};
+  cudaError_t e = cudaMemsetAsync(mem + at_small, 0, size_t(lay.bytes - at_small), stream);
   if (e != cudaSuccess) st = tg::record_cuda_error(e);
   Head inner = h;
   inner.ob.kind = 0;
@@ -997,11 +998,11 @@ tg_status run_objective(const Head& h, cudaStream_t stream) {
   inner.dX = inner.dW = nullptr;
   if (st == TG_OK) st = run_head(inner, stream);
   if (st == TG_OK) {
-    e = launch_objective(h, nll, w, sh, false, stream);
-    if (e == cudaSuccess && grad && ob.kind == kPreference && h.T > 0)
-      e = tg::launch_chained(tg_head_factor_kernel, ob.pairs > 0, dim3(static_cast<unsigned>(cdiv(h.T, 256))), 256,
-                             0, stream, ob, h.index, h.ignore, h.T, nullptr, sh, h.scale, nullptr,
-                             nullptr, w);
+    e = launch_objective(h, nll, wt, false, stream);
+    if (e == cudaSuccess && grad && ob.kind == kPreference && h.T > 0) {
+      tg_head_spoil_kernel<<<static_cast<unsigned>(cdiv(h.T, 256)), 256, 0, stream>>>(wt.wmax, w, h.T);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) st = tg::record_cuda_error(e);
   }
   if (st == TG_OK && grad) {
