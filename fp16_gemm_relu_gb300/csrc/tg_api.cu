@@ -436,9 +436,9 @@ tg_status make_plan(uintptr_t a, uintptr_t b, uintptr_t c, int64_t M, int64_t N,
 // chunk c lies in blocks c and c + 1 from there: a lane loads block c, loads block c + 1 only
 // when it holds one of the chunk's elements (so no load leaves a block that holds valid data),
 // and shifts the pair by b bytes in registers.
-__global__ void tg_pack_rows_kernel(const uint16_t* __restrict__ src, int64_t ld_src,
-                                    uint16_t* __restrict__ dst, int64_t ld_dst, int64_t rows,
-                                    int64_t cols) {
+__device__ __forceinline__ void pack_rows(const uint16_t* __restrict__ src, int64_t ld_src,
+                                          uint16_t* __restrict__ dst, int64_t ld_dst, int64_t rows,
+                                          int64_t cols) {
   const int64_t cpr = (cols + 7) >> 3;
   const int64_t gpr = (cpr + 31) >> 5;  // 32-chunk groups per row
   const int64_t items = rows * gpr;
@@ -472,6 +472,24 @@ __global__ void tg_pack_rows_kernel(const uint16_t* __restrict__ src, int64_t ld
     }
     *reinterpret_cast<uint4*>(dst + r * ld_dst + (c << 3)) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+}
+
+__global__ void tg_pack_rows_kernel(const uint16_t* __restrict__ src, int64_t ld_src,
+                                    uint16_t* __restrict__ dst, int64_t ld_dst, int64_t rows,
+                                    int64_t cols) {
+  pack_rows(src, ld_src, dst, ld_dst, rows, cols);
+}
+
+// Up to three matrices in one launch, one to each of the grid's y.
+struct PackJobs {
+  tg::PackJob j[3];
+};
+__global__ void tg_pack_jobs_kernel(const __grid_constant__ PackJobs jobs) {
+  tg::chain_wait();
+  tg::chain_release();
+  const tg::PackJob& j = jobs.j[blockIdx.y];
+  pack_rows(static_cast<const uint16_t*>(j.src), j.ld_src, static_cast<uint16_t*>(j.dst), j.ld_dst,
+            j.rows, j.cols);
 }
 
 // The same copy with each lane taking kPackItems chunks (of warp items nwarps apart) per pass,
@@ -1285,7 +1303,8 @@ cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t
   return cudaGetLastError();
 }
 
-tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, const tg_options* opt, TilePlan* out) {
+tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, bool halves, const tg_options* opt,
+                     TilePlan* out) {
   DeviceState* ds = nullptr;
   tg_status st = current_device(&ds);
   if (st != TG_OK) return st;
@@ -1297,7 +1316,7 @@ tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, const tg_op
   o.tail = -1;
   Plan pl;
   st = make_plan(256, 256, 256, M, N, K, round_up(K, 8), round_up(N, 8), round_up(N, 8), ds->sm_count,
-                 ds->pair_clusters, &o, &pl, 0, 0, max_k, true);
+                 ds->pair_clusters, &o, &pl, 0, 0, max_k, halves);
   if (st != TG_OK) return st;
   const tg_plan& P = pl.pub;
   const int cap = o.max_ctas > 0 ? std::min(o.max_ctas, ds->sm_count) : ds->sm_count;
@@ -1308,6 +1327,20 @@ tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, const tg_op
   out->kb_per_split = static_cast<int>(P.kblocks_per_split);
   out->units_cap = P.cta_pair ? std::max(std::min(cap / 2, ds->pair_clusters), 1) : cap;
   return TG_OK;
+}
+
+cudaError_t launch_pack_jobs(const PackJob* jobs, int n, int num_sms, bool chained, cudaStream_t stream) {
+  if (n == 0) return cudaSuccess;
+  PackJobs all;
+  std::memset(&all, 0, sizeof(all));
+  int64_t chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    all.j[i] = jobs[i];
+    chunks = std::max(chunks, jobs[i].rows * cdiv(jobs[i].cols, 8));
+  }
+  return launch_chained(tg_pack_jobs_kernel, chained,
+                        dim3(static_cast<unsigned>(aux_grid(chunks, num_sms)), static_cast<unsigned>(n)),
+                        256, 0, stream, all);
 }
 
 bool half_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,

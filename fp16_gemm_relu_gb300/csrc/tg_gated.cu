@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(256, 4)
     tg_gated_grad_kernel(const __half* __restrict__ dh, int64_t lddh, const __half* __restrict__ gate,
                          int64_t ldg, const __half* __restrict__ up, int64_t ldu, __half* out, int64_t ld,
                          int64_t np, int64_t M, int64_t N) {
+  tg::chain_release();
   const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   if (c >= np) return;
   for (int64_t r0 = int64_t(blockIdx.y) * kGradRows; r0 < M; r0 += int64_t(gridDim.y) * kGradRows) {
@@ -200,24 +201,89 @@ struct Operands {
     at[1] = need_w ? one(a.Wg, a.ldwg, w_rows, w_cols) : -1;
     at[2] = need_w ? one(a.Wu, a.ldwu, w_rows, w_cols) : -1;
   }
-  cudaError_t copy(const Gated& a, uint8_t* mem, int sms, cudaStream_t stream) {
-    cudaError_t e = cudaSuccess;
+  // The copies, in one launch; whether there are any.
+  cudaError_t copy(const Gated& a, uint8_t* mem, int sms, bool chained, cudaStream_t stream, bool* any) {
+    tg::PackJob jobs[3];
+    int n = 0;
     auto one = [&](int i, const void* p, int64_t ld, int64_t rows, int64_t cols, const void** out,
                    int64_t* ldo) {
       *out = p;
       *ldo = ld;
-      if (at[i] < 0 || e != cudaSuccess) return;
+      if (at[i] < 0) return;
       *out = mem + at[i];
       *ldo = round_up(cols, 64);
-      e = tg::launch_pack_rows(p, ld, mem + at[i], *ldo, rows, cols, sms, stream);
+      jobs[n++] = tg::PackJob{p, mem + at[i], ld, *ldo, rows, cols};
     };
     const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
     one(0, a.X, a.ldx, a.M, a.K, &x, &ldx);
     one(1, a.Wg, a.ldwg, w_rows, w_cols, &wg, &ldwg);
     one(2, a.Wu, a.ldwu, w_rows, w_cols, &wu, &ldwu);
-    return e;
+    *any = n > 0;
+    return tg::launch_pack_jobs(jobs, n, sms, chained, stream);
   }
 };
+
+// Whether TMA can store whole rows of n fp16 columns.
+bool whole_rows(const void* p, int64_t ld, int64_t n) {
+  return !misaligned(p, 16) && ld % 8 == 0 && n % 8 == 0;
+}
+
+int timeout_of(const tg_options* opt) { return opt && opt->timeout_ms > 0 ? opt->timeout_ms : 2000; }
+
+// dWg and dWu in one launch: X^T [dG | dU] (trans 0; the second output's tiles follow the first's along N)
+// or [dG | dU]^T X (trans 1; along M), g holding dU np columns after dG.  TG_ERR_NO_WORKSPACE: the planner
+// splits the sum, or an option asks for what this launch has not; nothing is launched.
+tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int64_t np, void* dWg,
+                       int64_t lddwg, void* dWu, int64_t lddwu, const tg_options* opt, unsigned* err,
+                       cudaStream_t stream) {
+  const int64_t rows = a.trans ? a.N : a.K, cols = a.trans ? a.K : a.N;  // of each output
+  tg::TilePlan plan;
+  tg_status st = tg::plan_tiles(a.trans ? 2 * rows : rows, a.trans ? cols : 2 * cols, a.M, kSumLength, false,
+                                opt, &plan);
+  if (st != TG_OK) return st;
+  if (plan.splits > 1) return TG_ERR_NO_WORKSPACE;
+  const int bm = plan.pair ? 256 : 128, bn = plan.block_n;
+  const int64_t tm = cdiv(rows, bm), tn = cdiv(cols, bn);
+  if (2 * tm * tn >= (int64_t{1} << 31)) return TG_ERR_NO_WORKSPACE;
+  tg::GemmLaunch l;
+  std::memset(&l, 0, sizeof(l));
+  tg::GemmParams& p = l.p;
+  p.tiles_m = static_cast<int>(a.trans ? 2 * tm : tm);
+  p.tiles_n = static_cast<int>(a.trans ? tn : 2 * tn);
+  p.num_kb = p.kb_per_split = plan.num_kb;
+  p.splits = 1;
+  p.units = p.tiles_m * p.tiles_n;
+  p.panel_m = std::min(opt && opt->panel_m ? opt->panel_m : 8, p.tiles_m);
+  p.a_mn = 1;
+  p.debug_flags = opt ? opt->debug_flags : 0;
+  p.timeout_ns = 1000000ull * static_cast<unsigned long long>(timeout_of(opt));
+  p.err = err;
+  p.c = static_cast<__half*>(dWg), p.ldc = lddwg;
+  p.M = static_cast<int>(rows), p.N = static_cast<int>(cols);
+  const bool tma = whole_rows(dWg, lddwg, cols) && whole_rows(dWu, lddwu, cols);
+  p.n_tma = tma ? p.N : 0;
+  l.two.m_first = a.trans ? static_cast<int>(tm) : INT32_MAX;
+  l.two.n_first = a.trans ? INT32_MAX : static_cast<int>(tn);
+  l.two.off = static_cast<int>(np);
+  l.two.c = static_cast<__half*>(dWu), l.two.ldc = lddwu;
+  l.grid = static_cast<int>(std::min<int64_t>(p.units, plan.units_cap)) * (plan.pair ? 2 : 1);
+  l.chained = true;
+  l.stream = stream;
+  const int kbox = plan.pair ? 128 : 64;
+  bool ok;
+  if (a.trans)
+    ok = tg::half_map(&l.a, g, 2 * np, a.M, 2 * np, 64, kbox) &&
+         tg::half_map(&l.b, ops.x, a.K, a.M, ops.ldx, 64, kbox);
+  else
+    ok = tg::half_map(&l.a, ops.x, a.K, a.M, ops.ldx, 64, kbox) &&
+         tg::half_map(&l.b, g, 2 * np, a.M, 2 * np, 64, kbox);
+  if (tma)
+    ok = ok && tg::half_map(&l.out, dWg, cols, rows, lddwg, 64, 32) &&
+         tg::half_map(&l.out2, dWu, cols, rows, lddwu, 64, 32);
+  if (!ok) return tg::record_cuda_error(cudaErrorInvalidValue);
+  const cudaError_t e = tg::launch_gemm_two(l, plan.pair ? 0 : bn);
+  return e == cudaSuccess ? TG_OK : tg::record_cuda_error(e);
+}
 
 }  // namespace
 
@@ -238,7 +304,7 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   if (misaligned(H, 2) || misaligned(gate, 2) || misaligned(up, 2)) return TG_ERR_MISALIGNED;
   tg::TilePlan plan;
   // a row of tiles of BN columns covers BN / 2 of each weight
-  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, opt, &plan)) != TG_OK) return st;
+  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, true, opt, &plan)) != TG_OK) return st;
   int sms = 0;
   unsigned* err = nullptr;
   if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
@@ -256,7 +322,8 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
     const cudaError_t fe = mem ? cudaFreeAsync(mem, stream) : cudaSuccess;
     return s == TG_OK && fe != cudaSuccess ? tg::record_cuda_error(fe) : s;
   };
-  cudaError_t e = ops.copy(a, mem, sms, stream);
+  bool copied = false;
+  cudaError_t e = ops.copy(a, mem, sms, false, stream, &copied);
   if (e != cudaSuccess) return done(tg::record_cuda_error(e));
 
   const int hn = plan.pair ? 128 : plan.block_n / 2, bm = plan.pair ? 256 : 128;
@@ -275,7 +342,7 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   p.act = activation;
   p.b_k = trans_w;
   p.debug_flags = opt ? opt->debug_flags : 0;
-  p.timeout_ns = 1000000ull * static_cast<unsigned long long>(opt && opt->timeout_ms > 0 ? opt->timeout_ms : 2000);
+  p.timeout_ns = 1000000ull * static_cast<unsigned long long>(timeout_of(opt));
   p.err = err;
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
@@ -285,12 +352,11 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   l.p.a_rows = static_cast<int>(M < 128 && !plan.pair ? round_up(M, 8) : 128);
   l.p.nw = static_cast<int>(nw);
   l.p.rotate = p.tiles_m == 1;
-  auto rows16 = [](const void* q, int64_t ld) { return !misaligned(q, 16) && ld % 8 == 0; };
-  l.p.tma = N % 8 == 0 && rows16(H, ldh) && (!gate || rows16(gate, ldgate)) && (!up || rows16(up, ldup));
+  l.p.tma = whole_rows(H, ldh, N) && (!gate || whole_rows(gate, ldgate, N)) && (!up || whole_rows(up, ldup, N));
   l.grid = static_cast<int>(std::min<int64_t>(units, plan.units_cap)) * (plan.pair ? 2 : 1);
   l.block_n = plan.pair ? 0 : plan.block_n;
   l.out_f32 = f32;
-  l.chained = false;
+  l.chained = copied;
   l.stream = stream;
   bool ok = tg::half_map(&l.x, ops.x, K, M, ops.ldx, 64, l.p.a_rows);
   const int kbox = plan.pair ? 128 : 64;
@@ -369,11 +435,18 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   e = launch_grad(activation, static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
                   static_cast<const __half*>(up), ldup, g, ld, np, M, N, stream);
   if (e != cudaSuccess) return done(tg::record_cuda_error(e));
-  if ((e = ops.copy(a, mem, sms, stream)) != cudaSuccess) return done(tg::record_cuda_error(e));
+  bool copied = false;
+  if ((e = ops.copy(a, mem, sms, true, stream, &copied)) != cudaSuccess) return done(tg::record_cuda_error(e));
   tg::GemmExtra ex;
   std::memset(&ex, 0, sizeof(ex));
   ex.max_k = kSumLength;
-  for (int i = 0; i < 2; ++i) {
+  bool one_by_one = !dWg || !dWu;
+  if (!one_by_one) {
+    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, stream);
+    if (st != TG_OK && st != TG_ERR_NO_WORKSPACE) return done(st);
+    one_by_one = st == TG_ERR_NO_WORKSPACE;
+  }
+  for (int i = 0; i < 2 && one_by_one; ++i) {
     void* d = i ? dWu : dWg;
     if (!d) continue;
     const void* gi = g + i * np;
@@ -383,6 +456,7 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
     if (st != TG_OK) return done(st);
   }
   if (dX) {  // one sum over dG's columns with Wg, then dU's with Wu
+    ex.chained = true;
     ex.B2 = ops.wu;
     ex.ldb2 = ops.ldwu;
     ex.b_k = N;

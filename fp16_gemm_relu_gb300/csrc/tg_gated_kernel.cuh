@@ -19,10 +19,18 @@ enum : int { kActSilu = 4 };
 // 1 / (1 + e^-x): 0 and 1 at the infinities.
 __device__ __forceinline__ float logistic(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
+// x times this logistic is gelu's tanh form: (1 + tanh u) / 2 = 1 / (1 + e^-2u).
+__device__ __forceinline__ float gelu_logistic(float x) {
+  return logistic(1.5957691216057308f * (x + 0.044715f * x * x * x));
+}
+
 // The activation of a gate, in float32.  silu(x) = x / (1 + e^-x) (Elfwing et al., 2018); the others
-// are the fused epilogue's.
+// are the fused epilogue's (the tanh form as a logistic: half the instructions, and no cancellation far
+// below zero).
 __device__ __forceinline__ float gated_activation(float x, int act) {
-  return act == kActSilu ? x * logistic(x) : activation(x, act);
+  if (act == kActSilu) return x * logistic(x);
+  if (act == kActGeluTanh) return x * gelu_logistic(x);
+  return activation(x, act);
 }
 
 // Its derivative.  Where the derivative is 0 or 1 to float32's precision it is taken as that, so that
@@ -37,8 +45,8 @@ __device__ __forceinline__ float gated_slope(float x, int act) {
     }
     case kActGeluTanh: {
       if (fabsf(x) > 16.0f) return x > 0.0f ? 1.0f : 0.0f;
-      const float c = 0.79788456080286536f, t = tanhf(c * (x + 0.044715f * x * x * x));
-      return 0.5f * (1.0f + t) + 0.5f * x * (1.0f - t * t) * c * (1.0f + 0.134145f * x * x);
+      const float s = gelu_logistic(x);
+      return s * (1.0f + (1.0f - s) * x * 1.5957691216057308f * (1.0f + 0.134145f * x * x));
     }
     case kActSilu: {
       if (fabsf(x) > 100.0f) return x > 0.0f ? 1.0f : 0.0f;
@@ -91,7 +99,7 @@ __device__ __forceinline__ void gated_values(const uint32_t (&g)[32], uint32_t (
     case kActSilu: all([](float x) { return x * logistic(x); }); break;
     case kActRelu: all([](float x) { return activation(x, kActRelu); }); break;
     case kActGelu: all([](float x) { return activation(x, kActGelu); }); break;
-    case kActGeluTanh: all([](float x) { return activation(x, kActGeluTanh); }); break;
+    case kActGeluTanh: all([](float x) { return x * gelu_logistic(x); }); break;
     default: all([](float x) { return x; });
   }
 }
@@ -125,18 +133,7 @@ __device__ __forceinline__ void gated_store(const CUtensorMap* tm, bool tma, __h
     }
     return;
   }
-  // rows that start anywhere: 64 bytes of a row a store
-  __syncwarp();
-  const int rows = min(32, M - row0), cols = min(64, N - col0);
-  for (int r = 0; r < rows; ++r) {
-    unsigned short* dst = reinterpret_cast<unsigned short*>(out + (row0 + r) * ld + col0);
-#pragma unroll
-    for (int j = 0; j < 64; j += 32) {
-      const int c = j + lane;
-      if (c < cols)
-        dst[c] = *reinterpret_cast<const unsigned short*>(stg + r * 128 + ((((c >> 3) ^ (r & 7)) << 4) | ((c & 7) << 1)));
-    }
-  }
+  store_rows(out, ld, stg, row0, col0, M, N, lane);
 }
 
 // tmX: fp16 X, dims {K, M}, box {64, a_rows};  tmG, tmU: the weights, B_K (stored N x K): dims {K, N}, box

@@ -1,34 +1,55 @@
-// Instantiations of the tensor-core kernels whose right operand is two matrices (kModeDual).
+// Instantiations of the tensor-core kernels whose right operand is two matrices (kModeDual), and of those
+// with two outputs (kModeTwo).
 #include "tg_internal.h"
 
 namespace tg {
 
 namespace {
-template <typename K>
-cudaError_t launch(K kern, int smem, const GemmLaunch& l) {
+template <typename K, typename... Q>
+cudaError_t launch(K kern, int smem, const GemmLaunch& l, const Q&... args) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.b2, l.out, l.p);
-  return cudaGetLastError();
+  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), kThreads, smem, l.stream,
+                        args...);
+}
+
+template <typename K>
+cudaError_t launch_dual(K kern, int smem, const GemmLaunch& l) {
+  return launch(kern, smem, l, l.a, l.b, l.b2, l.out, l.p);
+}
+template <typename K>
+cudaError_t launch_two(K kern, int smem, const GemmLaunch& l) {
+  return launch(kern, smem, l, l.a, l.b, l.out, l.out2, l.p, l.two);
 }
 
 template <bool OUT_F32>
 cudaError_t launch_tile(const GemmLaunch& l, int block_n) {
   switch (block_n) {
-    case 256: return launch(tg_gemm_tc_dual_kernel<256, OUT_F32>, TileCfg<256>::kSmemBytes, l);
-    case 192: return launch(tg_gemm_tc_dual_kernel<192, OUT_F32>, TileCfg<192>::kSmemBytes, l);
-    case 128: return launch(tg_gemm_tc_dual_kernel<128, OUT_F32>, TileCfg<128>::kSmemBytes, l);
+    case 256: return launch_dual(tg_gemm_tc_dual_kernel<256, OUT_F32>, TileCfg<256>::kSmemBytes, l);
+    case 192: return launch_dual(tg_gemm_tc_dual_kernel<192, OUT_F32>, TileCfg<192>::kSmemBytes, l);
+    case 128: return launch_dual(tg_gemm_tc_dual_kernel<128, OUT_F32>, TileCfg<128>::kSmemBytes, l);
     default: break;
   }
   if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
-  return l.p.b_k ? launch(tg_gemm_pair_dual_kernel<OUT_F32, true>, PairCfgFwd::kSmemBytes, l)
-                 : launch(tg_gemm_pair_dual_kernel<OUT_F32, false>, PairCfgFwd::kSmemBytes, l);
+  return l.p.b_k ? launch_dual(tg_gemm_pair_dual_kernel<OUT_F32, true>, PairCfgFwd::kSmemBytes, l)
+                 : launch_dual(tg_gemm_pair_dual_kernel<OUT_F32, false>, PairCfgFwd::kSmemBytes, l);
 }
 }  // namespace
 
 cudaError_t launch_gemm_dual(const GemmLaunch& l, bool out_f32, int block_n) {
   return out_f32 ? launch_tile<true>(l, block_n) : launch_tile<false>(l, block_n);
+}
+
+cudaError_t launch_gemm_two(const GemmLaunch& l, int block_n) {
+  switch (block_n) {
+    case 256: return launch_two(tg_gemm_tc_two_kernel<256>, TileCfg<256>::kSmemBytes, l);
+    case 192: return launch_two(tg_gemm_tc_two_kernel<192>, TileCfg<192>::kSmemBytes, l);
+    case 128: return launch_two(tg_gemm_tc_two_kernel<128>, TileCfg<128>::kSmemBytes, l);
+    default: break;
+  }
+  if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
+  return launch_two(tg_gemm_pair_two_kernel<0>, PairCfgFwd::kSmemBytes, l);
 }
 
 }  // namespace tg

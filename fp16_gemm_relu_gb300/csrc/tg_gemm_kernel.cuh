@@ -101,8 +101,18 @@ struct GemmParams {
 // launch, so the result does not depend on order).  Scaled: fp16(alpha (sum + addend)).  A mode
 // of the kernel and not a branch in it, so that the plain kernels carry none of the others.
 // Dual: plain, but the right operand's k-blocks are two matrices', one after the other (p.kb_switch).
-enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2, kModeDual = 3 };
+// Two: two products that share an operand, as one launch (TwoOut).
+enum : int { kModePlain = 0, kModeAdd = 1, kModeScaled = 2, kModeDual = 3, kModeTwo = 4 };
 constexpr int epilogue_mode(int mode) { return mode == kModeDual ? kModePlain : mode; }
+constexpr bool chained_mode(int mode) { return mode >= kModeScaled; }
+
+// kModeTwo, fp16 output: the tiles from m_first (in M) or n_first (in N; the other is past all tiles) on are
+// of a second output, whose columns (rows) of the operand lie `off` further than the first's.
+struct TwoOut {
+  int m_first, n_first, off;
+  __half* c;      // the second output, like p.c; tiles are stored row by row (p.n_tma == 0) or by TMA
+  long long ldc;
+};
 
 // Kernels that are launched chained.  chain_wait: nothing that the kernel before has written is read,
 // and nothing that it reads is written, before this.  chain_release, after it: the next kernel's
@@ -702,6 +712,34 @@ __device__ __forceinline__ void epilogue_general_32(const uint32_t (&acc)[32], i
   }
 }
 
+// The warp's 32 rows x 64 columns of fp16 in its staging buffer (128B-swizzled rows) to rows row0 and columns
+// col0 on of a matrix whose rows start anywhere: 64 bytes of a row a store, eight rows' in flight.
+__device__ __forceinline__ void store_rows(__half* out, long long ld, const uint8_t* stg, int row0,
+                                           int col0, int M, int N, int lane) {
+  __syncwarp();
+  const int rows = min(32, M - row0);
+  const bool in0 = col0 + lane < N, in1 = col0 + 32 + lane < N;
+  unsigned short* dst = reinterpret_cast<unsigned short*>(out + static_cast<long long>(row0) * ld + col0 + lane);
+  const uint8_t* src = stg + ((lane & 7) << 1);
+  const int c0 = lane >> 3, c1 = c0 + 4;  // 16-byte chunks of the lane's two columns
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    unsigned short a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = *reinterpret_cast<const unsigned short*>(src + (r0 + i) * 128 + ((c0 ^ i) << 4));
+      b[i] = *reinterpret_cast<const unsigned short*>(src + (r0 + i) * 128 + ((c1 ^ i) << 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + i >= rows) break;
+      if (in0) dst[0] = a[i];
+      if (in1) dst[32] = b[i];
+      dst += ld;
+    }
+  }
+}
+
 // 64 columns of one row per lane (float32 bits in r0 = columns 0..31, r1 = 32..63): epilogue,
 // fp16 pack, 128B-swizzled staging and TMA store of the warp's 32 x 64 block; columns in
 // [n_tma, N) are written with plain stores.
@@ -709,7 +747,8 @@ template <int MODE = kModePlain>
 __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const GemmParams& p,
                                                 const uint32_t (&r0)[32],
                                                 const uint32_t (&r1)[32], int row0, int col0,
-                                                uint8_t* stg, int& sb, int lane) {
+                                                uint8_t* stg, int& sb, int lane, __half* c = nullptr,
+                                                long long ldc = 0) {
   uint32_t pk[32];
   if constexpr (MODE == kModeScaled) {
     epilogue_scaled_32(r0, row0 + lane, col0, p, pk);
@@ -726,7 +765,7 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
     epilogue_general_32(r0, row0 + lane, col0, p, pk);
     epilogue_general_32(r1, row0 + lane, col0 + 32, p, pk + 16);
   }
-  if (col0 < p.n_tma) {
+  if (MODE == kModeTwo || col0 < p.n_tma) {
     uint8_t* st = stg + sb * kStagingBuf;
     if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer is done
     __syncwarp();
@@ -734,6 +773,13 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
     for (int j = 0; j < 8; ++j) {
       uint4 v = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
       *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
+    }
+    if constexpr (MODE == kModeTwo) {  // whole rows by TMA, or none
+      if (p.n_tma == 0) {
+        store_rows(c, ldc, st, row0, col0, p.M, p.N, lane);
+        sb ^= 1;
+        return;
+      }
     }
     fence_async_smem();
     __syncwarp();
@@ -780,7 +826,8 @@ template <int BN, bool OUT_F32, bool PERM8 = false, int MODE = kModePlain>
 __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const GemmParams& p,
                                               uint32_t tl, int row0, int col_base, int split,
                                               uint8_t* stg, int& sb, uint32_t release_bar,
-                                              bool remote, int lane) {
+                                              bool remote, int lane, __half* c_out = nullptr,
+                                              long long ldc = 0) {
   auto release = [&]() {
     tc_fence_before();
     __syncwarp();
@@ -795,7 +842,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
     release();
     return;
   }
-  static_assert(MODE == kModePlain || (OUT_F32 ? MODE == kModeAdd : MODE == kModeScaled),
+  static_assert(MODE == kModePlain || (OUT_F32 ? MODE == kModeAdd : MODE == kModeScaled || MODE == kModeTwo),
                 "the sum is added in float32 and scaled in fp16");
   if constexpr (!OUT_F32) {
 #pragma unroll 1
@@ -810,7 +857,8 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
         unperm8(r0);
         unperm8(r1);
       }
-      store_chunk_f16<MODE>(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
+      if (MODE == kModeTwo && col_base + c * 64 >= p.N) continue;
+      store_chunk_f16<MODE>(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane, c_out, ldc);
     }
   } else {
 #pragma unroll 1
@@ -857,11 +905,12 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
 template <int BN, bool OUT_F32, bool GENERAL, int MODE>
 __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                              const CUtensorMap& tmOut, const GemmParams& p,
-                                             const CUtensorMap* tmB2) {
+                                             const CUtensorMap* tmB2, const TwoOut* two = nullptr,
+                                             const CUtensorMap* tmOut2 = nullptr) {
   using Cfg = TileCfg<BN>;
   constexpr int S = Cfg::kStages;
-  const int a_mn = GENERAL ? p.a_mn : 0;
-  const int b_k = GENERAL ? p.b_k : 0;
+  const int a_mn = MODE == kModeTwo ? 1 : GENERAL ? p.a_mn : 0;
+  const int b_k = MODE == kModeTwo ? 0 : GENERAL ? p.b_k : 0;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -907,7 +956,7 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  if constexpr (MODE == kModeScaled) {
+  if constexpr (chained_mode(MODE)) {
     chain_wait();
     chain_release();
   }
@@ -921,6 +970,11 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
       bool dropped = false;
       for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
         const Unit w = unit_of(p, u);
+        int arow = w.m_blk * kBM, bcol = w.n_blk * BN;
+        if constexpr (MODE == kModeTwo) {
+          if (w.m_blk >= two->m_first) arow += two->off - two->m_first * kBM;
+          if (w.n_blk >= two->n_first) bcol += two->off - two->n_first * BN;
+        }
         for (int kb = w.kb_begin; kb < w.kb_end; ++kb) {
           if (!wait_phase(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p, kRoleProducer))
             goto producer_done;
@@ -932,11 +986,11 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
             const uint32_t a_dst = smem_u32(sA + stage * Cfg::kAStage);
             const uint32_t b_dst = smem_u32(sB + stage * Cfg::kBStage);
             if (!a_mn) {
-              tma_load_2d(a_dst, &tmA, fb, kb * kBK, w.m_blk * kBM);
+              tma_load_2d(a_dst, &tmA, fb, kb * kBK, arow);
             } else {
 #pragma unroll
               for (int j = 0; j < kBM / 64; ++j)
-                tma_load_2d(a_dst + j * 8192, &tmA, fb, w.m_blk * kBM + j * 64, kb * kBK);
+                tma_load_2d(a_dst + j * 8192, &tmA, fb, arow + j * 64, kb * kBK);
             }
             const CUtensorMap* mb = &tmB;
             int kbb = kb;
@@ -949,9 +1003,9 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
             if (!b_k) {
 #pragma unroll
               for (int j = 0; j < BN / 64; ++j)
-                tma_load_2d(b_dst + j * Cfg::kBBox, mb, fb, w.n_blk * BN + j * 64, kbb * kBK);
+                tma_load_2d(b_dst + j * Cfg::kBBox, mb, fb, bcol + j * 64, kbb * kBK);
             } else {
-              tma_load_2d(b_dst, mb, fb, kbb * kBK, w.n_blk * BN);
+              tma_load_2d(b_dst, mb, fb, kbb * kBK, bcol);
             }
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
@@ -1026,9 +1080,17 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
-      epilogue_tile<BN, OUT_F32, false, epilogue_mode(MODE)>(&tmOut, p, tl, w.m_blk * kBM + q * 32,
-                                                             w.n_blk * BN, w.split, stg, sb,
-                                                             smem_u32(&tempty[buf]), false, lane);
+      if constexpr (MODE == kModeTwo) {
+        const bool m2 = w.m_blk >= two->m_first, n2 = w.n_blk >= two->n_first, second = m2 || n2;
+        epilogue_tile<BN, OUT_F32, false, MODE>(
+            second ? tmOut2 : &tmOut, p, tl, (w.m_blk - (m2 ? two->m_first : 0)) * kBM + q * 32,
+            (w.n_blk - (n2 ? two->n_first : 0)) * BN, w.split, stg, sb, smem_u32(&tempty[buf]), false,
+            lane, second ? two->c : p.c, second ? two->ldc : p.ldc);
+      } else {
+        epilogue_tile<BN, OUT_F32, false, epilogue_mode(MODE)>(&tmOut, p, tl, w.m_blk * kBM + q * 32,
+                                                               w.n_blk * BN, w.split, stg, sb,
+                                                               smem_u32(&tempty[buf]), false, lane);
+      }
     }
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
@@ -1058,6 +1120,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmOut,
                            const __grid_constant__ GemmParams p) {
   tc_gemm_body<BN, OUT_F32, true, kModeDual>(tmA, tmB, tmOut, p, &tmB2);
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    tg_gemm_tc_two_kernel(const __grid_constant__ CUtensorMap tmA,
+                          const __grid_constant__ CUtensorMap tmB,
+                          const __grid_constant__ CUtensorMap tmOut,
+                          const __grid_constant__ CUtensorMap tmOut2,
+                          const __grid_constant__ GemmParams p, const __grid_constant__ TwoOut two) {
+  tc_gemm_body<BN, false, true, kModeTwo>(tmA, tmB, tmOut, p, nullptr, &two, &tmOut2);
 }
 
 // Epilogue of one K half of a tail-split tile (fp16 output), for one warp of the pair kernel:
@@ -1178,7 +1250,9 @@ template <bool OUT_F32, bool A_MN, bool B_K, bool A_CLS, int MODE = kModePlain>
 __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                const CUtensorMap& tmOut, const GemmParams& p,
                                                const AClassMaps* cls,
-                                               const CUtensorMap* tmB2 = nullptr) {
+                                               const CUtensorMap* tmB2 = nullptr,
+                                               const TwoOut* two = nullptr,
+                                               const CUtensorMap* tmOut2 = nullptr) {
   static_assert(!A_CLS || (OUT_F32 && !A_MN && !B_K), "row classes: float32 output, forward layout");
   using Cfg = PairCfgFwd;
   constexpr int S = Cfg::kStages;
@@ -1235,7 +1309,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
   cluster_sync();  // barriers of both CTAs initialised, TMEM allocated in both
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  if constexpr (MODE == kModeScaled) {
+  if constexpr (chained_mode(MODE)) {
     chain_wait();
     chain_release();
   }
@@ -1249,8 +1323,12 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
       bool dropped = false;
       for (int u = cluster; u < p.units; u += nclusters) {
         const Unit w = unit_of(p, u);
-        const int arow = w.m_blk * 2 * kBM + static_cast<int>(rank) * kBM;
-        const int bcol = w.n_blk * Cfg::kBN + static_cast<int>(rank) * Cfg::kHalfN;
+        int arow = w.m_blk * 2 * kBM + static_cast<int>(rank) * kBM;
+        int bcol = w.n_blk * Cfg::kBN + static_cast<int>(rank) * Cfg::kHalfN;
+        if constexpr (MODE == kModeTwo) {
+          if (w.m_blk >= two->m_first) arow += two->off - two->m_first * 2 * kBM;
+          if (w.n_blk >= two->n_first) bcol += two->off - two->n_first * Cfg::kBN;
+        }
         int a_class = 0, a_crow = 0, k_shift = 0;  // A_CLS: the tile's class, its row in it
         if constexpr (A_CLS) {
           a_class = w.m_blk / p.cls_tiles;
@@ -1392,7 +1470,13 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
       const int row0 = w.m_blk * 2 * kBM + static_cast<int>(rank) * kBM + q * 32;
       const uint32_t release_bar = mapa_shared(smem_u32(&tempty[buf]), 0);
-      if (!OUT_F32 && w.tail_slot >= 0)
+      if constexpr (MODE == kModeTwo) {  // (no tail)
+        const bool m2 = w.m_blk >= two->m_first, n2 = w.n_blk >= two->n_first, second = m2 || n2;
+        epilogue_tile<Cfg::kBN, OUT_F32, false, MODE>(
+            second ? tmOut2 : &tmOut, p, tl, row0 - (m2 ? two->m_first * 2 * kBM : 0),
+            (w.n_blk - (n2 ? two->n_first : 0)) * Cfg::kBN, w.split, stg, sb, release_bar, true, lane,
+            second ? two->c : p.c, second ? two->ldc : p.ldc);
+      } else if (!OUT_F32 && w.tail_slot >= 0)
         epilogue_tail<Cfg::kBN, epilogue_mode(MODE)>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot,
                                       w.split, static_cast<int>(rank) * 4 + q, stg, sb,
                                       release_bar, lane);
@@ -1434,6 +1518,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap tmOut,
                              const __grid_constant__ GemmParams p) {
   pair_gemm_body<OUT_F32, false, B_K, false, kModeDual>(tmA, tmB, tmOut, p, nullptr, &tmB2);
+}
+
+template <int NONE>  // a template so that every unit including this header shares one definition
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    tg_gemm_pair_two_kernel(const __grid_constant__ CUtensorMap tmA,
+                            const __grid_constant__ CUtensorMap tmB,
+                            const __grid_constant__ CUtensorMap tmOut,
+                            const __grid_constant__ CUtensorMap tmOut2,
+                            const __grid_constant__ GemmParams p, const __grid_constant__ TwoOut two) {
+  pair_gemm_body<false, true, false, false, kModeTwo>(tmA, tmB, tmOut, p, nullptr, nullptr, &two, &tmOut2);
 }
 
 // The CTA-pair kernel with A read through row classes (float32 partials, forward layout).

@@ -15,10 +15,12 @@ namespace tg {
 struct GemmLaunch {
   CUtensorMap a, b, out;  // see tg_gemm_tc_kernel for the layouts each map describes
   CUtensorMap b2;         // launch_gemm_dual: the second right operand
+  CUtensorMap out2;       // launch_gemm_two: the second output
+  TwoOut two;
   GemmParams p;
   int grid;
   cudaStream_t stream;
-  bool chained;  // logits and scaled kernels: the launch before it on the stream is the library's
+  bool chained;  // kernels that can be chained: the launch before it on the stream is the library's
 };
 
 // A launch that may begin while the kernel before it on the stream still runs: its blocks are made
@@ -74,6 +76,8 @@ cudaError_t launch_head_add(const GemmLaunch& l);
 cudaError_t launch_gemm_scaled(const GemmLaunch& l, int block_n);
 // The kernels with two right operands (kModeDual; block_n 0: CTA pairs).  A is stored M x K.
 cudaError_t launch_gemm_dual(const GemmLaunch& l, bool out_f32, int block_n);
+// The kernels with two outputs (kModeTwo): A stored K x M, B stored K x N.
+cudaError_t launch_gemm_two(const GemmLaunch& l, int block_n);
 // Clusters of two that can be resident at once on the current device.
 cudaError_t gemm_pair_max_clusters(int* out);
 
@@ -131,11 +135,12 @@ struct GatedLaunch {
 cudaError_t launch_gated(const GatedLaunch& l);
 
 // How the GEMM's planner would run an M x N x K product on aligned operands, with or without K splits,
-// in tiles of 256 x 256 on CTA pairs, or 128 x 256 or 128 x 128.
+// in tiles of 256 x 256 on CTA pairs, or 128 x 256, 128 x 192 (not with `halves`) or 128 x 128.
 struct TilePlan {
   int pair, block_n, splits, num_kb, kb_per_split, units_cap;  // units_cap: CTAs or pairs at a time
 };
-tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, const tg_options* opt, TilePlan* out);
+tg_status plan_tiles(int64_t M, int64_t N, int64_t K, int64_t max_k, bool halves, const tg_options* opt,
+                     TilePlan* out);
 
 // One 2-D fp16 tensor map, 128B swizzle; false if the driver refuses it.
 bool half_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
@@ -146,6 +151,14 @@ bool partial_map(CUtensorMap* m, const void* base, int64_t n, int64_t rows, int6
 // dst (rows x ld_dst, 16-byte aligned rows, columns up to a multiple of 8 written as zero) <- src.
 cudaError_t launch_pack_rows(const void* src, int64_t ld_src, void* dst, int64_t ld_dst,
                              int64_t rows, int64_t cols, int num_sms, cudaStream_t stream);
+
+// Up to three such copies in one launch (chained: see GemmLaunch).
+struct PackJob {
+  const void* src;
+  void* dst;
+  int64_t ld_src, ld_dst, rows, cols;
+};
+cudaError_t launch_pack_jobs(const PackJob* jobs, int n, int num_sms, bool chained, cudaStream_t stream);
 
 // Deterministic split-K reduction: C = fp16(epi(sum_s W[s])) (see tg_splitk_reduce_kernel).
 // p supplies the epilogue (act, bias, residual, ldr) and the shape (M, N).
