@@ -228,6 +228,41 @@ bool whole_rows(const void* p, int64_t ld, int64_t n) {
   return !misaligned(p, 16) && ld % 8 == 0 && n % 8 == 0;
 }
 
+// The plan of one row of tiles, M <= 128: bound by the weights' 4 K N bytes from memory.  A row of tiles reads
+// them at 6.6 TB/s where its units fill whole waves of blocks, and a third slower at worst where they do not
+// (the blocks that are left share the bandwidth); tiles of 128 columns read K x N weights 128 bytes of a
+// row at a time, which costs 12%; splits cost a second kernel and their float32 sums through L2.  Measured
+// (us) against the alternatives: 1 x 8192 x 28672, K x N: two splits of 256 columns 149, one 155, 128 columns 165, a
+// pair's tiles 242; N x K: 128 columns 146, 256 in two splits 149; 16 x 8192 x 22016: four splits 122, one 137;
+// 1 x 4096 x 14336: one split of 256 columns 44, four 45, 128 columns 51.
+tg::TilePlan few_rows_plan(const Gated& a, int sms) {
+  tg::TilePlan best;
+  std::memset(&best, 0, sizeof(best));
+  best.num_kb = static_cast<int>(cdiv(a.K, tg::kBK));
+  best.units_cap = sms;
+  const double bytes = 4.0 * double(a.K) * double(a.N);
+  const int least = static_cast<int>(cdiv(a.K, kSumLength));
+  double best_t = 0.0;
+  for (int bn = 256; bn >= 128; bn -= 128) {
+    const int64_t tiles = cdiv(a.N, bn / 2);
+    for (int s = least; s <= std::max(least, 16); ++s) {
+      const int kbps = static_cast<int>(cdiv(best.num_kb, s));
+      if (cdiv(best.num_kb, kbps) != s || (s > least && kbps < 4)) continue;
+      const int64_t units = tiles * s;
+      const double full = double(units) / double(cdiv(units, sms) * sms);
+      double t = bytes / 6.6e12 / (0.65 + 0.35 * full);
+      if (bn == 128 && !a.trans) t *= 1.12;
+      if (s > 1) t += 4e-6 + 16.0 * s * double(a.M) * double(a.N) / 1e13;
+      if (best.block_n && t >= best_t) continue;
+      best_t = t;
+      best.block_n = bn;
+      best.splits = s;
+      best.kb_per_split = kbps;
+    }
+  }
+  return best;
+}
+
 int timeout_of(const tg_options* opt) { return opt && opt->timeout_ms > 0 ? opt->timeout_ms : 2000; }
 
 // dWg and dWu in one launch: X^T [dG | dU] (trans 0; the second output's tiles follow the first's along N)
@@ -302,12 +337,14 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   if (M == 0) return TG_OK;
   if (!H) return TG_ERR_INVALID_ARG;
   if (misaligned(H, 2) || misaligned(gate, 2) || misaligned(up, 2)) return TG_ERR_MISALIGNED;
-  tg::TilePlan plan;
-  // a row of tiles of BN columns covers BN / 2 of each weight
-  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, true, opt, &plan)) != TG_OK) return st;
   int sms = 0;
   unsigned* err = nullptr;
   if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
+  tg::TilePlan plan;
+  const bool choose = !opt || (!opt->block_n && !opt->split_k && !opt->pair && !opt->max_ctas);
+  // (a row of tiles of BN columns covers BN / 2 of each weight; the call refuses what no plan has)
+  if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, true, opt, &plan)) != TG_OK) return st;
+  if (M <= 128 && choose) plan = few_rows_plan(a, sms);
   Operands ops;
   const int64_t nw = round_up(N, 32), stride = M * 2 * nw;
   Layout lay;
