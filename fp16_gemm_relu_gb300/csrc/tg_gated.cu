@@ -375,7 +375,10 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   const int64_t units = int64_t(p.tiles_m) * p.tiles_n * p.splits;
   if (units >= (int64_t{1} << 31)) return done(TG_ERR_INVALID_ARG);
   p.units = static_cast<int>(units);
-  p.panel_m = std::min(opt && opt->panel_m ? opt->panel_m : 8, p.tiles_m);
+  // Panels of 16 rows of tiles: the weights, the larger operand, are read half as often from memory as with the
+  // GEMM's 8, and 4096 rows of X still stay in L2 (8192 x 4096 x 14336 in a power-capped loop 1186 against 1222 us;
+  // 32 rows 1227).
+  p.panel_m = std::min(opt && opt->panel_m ? opt->panel_m : 16, p.tiles_m);
   p.act = activation;
   p.b_k = trans_w;
   p.debug_flags = opt ? opt->debug_flags : 0;

@@ -123,12 +123,12 @@ __device__ __forceinline__ void stage_half(uint8_t* stg, const uint32_t (&v)[32]
 // columns col0 on of an output.
 __device__ __forceinline__ void gated_store(const CUtensorMap* tm, bool tma, __half* out, long long ld,
                                             const uint8_t* stg, int row0, int col0, int M, int N,
-                                            int lane) {
+                                            int lane, uint64_t policy) {
   if (tma) {
     fence_async_smem();
     __syncwarp();
     if (lane == 0) {
-      tma_store_2d(tm, smem_u32(stg), col0, row0);
+      tma_store_2d_hint(tm, smem_u32(stg), col0, row0, policy);
       bulk_commit();
     }
     return;
@@ -352,6 +352,8 @@ __device__ __forceinline__ void gated_body(const CUtensorMap& tmX, const CUtenso
     const int q = warp & 3;             // TMEM lane quarter this warp may access
     const int ew = warp - 2, part = ew >> 2;
     uint8_t* stg = sStg + ew * kStagingBuf;
+    // the outputs are not read here again: they need not push the operands, which other tiles read, out of L2
+    const uint64_t policy = evict_first_policy();
     int t = 0;
     for (int u = first; u < p.units; u += step, ++t) {
       const Unit w = unit_of(p, u);
@@ -421,7 +423,7 @@ __device__ __forceinline__ void gated_body(const CUtensorMap& tmX, const CUtenso
           gated_values(g, v, p.act);
           stage_half(stg, v, c, lane);
         }
-        gated_store(&tmH, gp.tma, gp.h, gp.ldh, stg, row0, col0, p.M, p.N, lane);
+        gated_store(&tmH, gp.tma, gp.h, gp.ldh, stg, row0, col0, p.M, p.N, lane, policy);
         if (gp.gate || gp.up) {
 #pragma unroll 1
           for (int o = 0; o < 2; ++o) {  // the pre-activations, read from TMEM again
@@ -436,7 +438,7 @@ __device__ __forceinline__ void gated_body(const CUtensorMap& tmX, const CUtenso
             }
             if (o ? gp.up != nullptr : gp.gate != nullptr)
               gated_store(o ? &tmUp : &tmGate, gp.tma, o ? gp.up : gp.gate, o ? gp.ldup : gp.ldgate,
-                          stg, row0, col0, p.M, p.N, lane);
+                          stg, row0, col0, p.M, p.N, lane, policy);
           }
         }
       }
