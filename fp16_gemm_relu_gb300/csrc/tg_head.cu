@@ -636,6 +636,7 @@ struct Head {
   float scale;
   tg_head_options o;
   Objective ob;          // kind 0: the losses themselves
+  bool precise;          // logits of an objective, or for one
 };
 
 // Parts of one scratch block, each 256-byte aligned.
@@ -823,6 +824,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     lx.target = store || h.top ? nullptr : reinterpret_cast<const long long*>(index);
     lx.picked = picked;
     lx.block_n = &block_n;
+    lx.precise = h.precise;
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
     if (h.T < kLeastRows) ex.a_rows = kLeastRows - t0;
@@ -1100,6 +1102,7 @@ tg_status tg_linear_preference_f16(const void* X, const void* W, const int64_t* 
   h.scale = logit_scale;
   h.o = options_or_default(opt);
   h.ob.kind = kPreference;
+  h.precise = true;
   h.ob.dloss = dX || dW ? dloss : nullptr;
   h.ob.loss = loss;
   h.ob.reference = reference;
@@ -1132,6 +1135,7 @@ tg_status tg_linear_policy_f16(const void* X, const void* W, const int64_t* targ
   h.scale = logit_scale;
   h.o = options_or_default(opt);
   h.ob.kind = kPolicy;
+  h.precise = true;
   h.ob.dloss = dX || dW ? dloss : nullptr;
   h.ob.loss = loss;
   h.ob.reference = kl_weight > 0.0f ? reference : nullptr;

@@ -17,21 +17,8 @@ cudaError_t launch(K kern, int threads, int smem, const GemmLaunch& l, const P& 
 
 template <bool B_K, bool STORE>
 cudaError_t launch_logits(const GemmLaunch& l, const HeadParams& hp, int block_n) {
-  switch (block_n) {
-    case 0:
-      if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
-      return launch(tg_head_logits_pair_kernel<B_K, STORE>, kHeadThreads,
-                    HeadCfg<2, 256>::kSmemBytes, l, hp);
-    case 256:
-      return launch(tg_head_logits_kernel<256, B_K, STORE>, kHeadThreads,
-                    HeadCfg<1, 256>::kSmemBytes, l, hp);
-    case 192:
-      return launch(tg_head_logits_kernel<192, B_K, STORE>, kHeadThreads,
-                    HeadCfg<1, 192>::kSmemBytes, l, hp);
-    default:
-      return launch(tg_head_logits_kernel<128, B_K, STORE>, kHeadThreads,
-                    HeadCfg<1, 128>::kSmemBytes, l, hp);
-  }
+  return launch_logits_tile<B_K, STORE, false>(
+      [&](auto kern, int smem) { return launch(kern, kHeadThreads, smem, l, hp); }, l.grid, block_n);
 }
 }  // namespace
 
@@ -43,6 +30,7 @@ cudaError_t launch_head_logits(const GemmLaunch& l, const LogitsExtra& x, int bl
   hp.target = x.target;
   hp.picked = x.picked;
   hp.rotate = l.p.tiles_m == 1 ? 1 : 0;
+  if (x.precise) return launch_head_logits_precise(l, hp, x.z != nullptr, block_n);
   if (l.p.b_k)
     return x.z ? launch_logits<true, true>(l, hp, block_n) : launch_logits<true, false>(l, hp, block_n);
   return x.z ? launch_logits<false, true>(l, hp, block_n) : launch_logits<false, false>(l, hp, block_n);

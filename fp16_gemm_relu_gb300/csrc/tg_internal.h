@@ -66,9 +66,13 @@ struct LogitsExtra {
   const long long* target;  // without z: [M], and the targets' logits [M]
   float* picked;
   int* block_n;             // out: the tiles' width
+  bool precise;             // see tg_head_kernel.cuh
 };
+struct HeadParams;
 // Logits kernel (block_n 0: CTA pairs), X row-major, W in either layout (l.p.b_k).
 cudaError_t launch_head_logits(const GemmLaunch& l, const LogitsExtra& x, int block_n);
+cudaError_t launch_head_logits_precise(const GemmLaunch& l, const HeadParams& hp, bool store,
+                                       int block_n);
 // The CTA-pair kernel that adds A^T B to its float32 output (kModeAdd; A stored K x M).
 cudaError_t launch_head_add(const GemmLaunch& l);
 // The fp16-output kernels whose epilogue is the scaled sum (kModeScaled; block_n 0: CTA pairs).

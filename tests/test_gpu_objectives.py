@@ -364,13 +364,19 @@ def test_against_cross_entropy():
     T, V, D = 150, 900, 128
     x, w = operands(T, V, D, VOCAB, 110)
     target = targets(T, V, 111)
+    live = target != IGNORE
     weights = torch.rand(T, generator=gen(112), device="cuda") + 0.1
-    nll, dx, dw = tg.linear_cross_entropy_step(x, w, target, weights)
     one = torch.ones(T, device="cuda")
-    loss, logp, dx2, dw2 = tg.linear_policy_step(x, w, target, -nll, weights, one)
-    assert torch.equal(logp, torch.where(target == IGNORE, torch.zeros_like(nll), -nll))
-    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
-    assert torch.equal(loss, torch.where(target == IGNORE, torch.zeros_like(nll), -weights))
+    _, logp = tg.linear_policy(x, w, target, one, weights)
+    nll = tg.linear_cross_entropy(x, w, target)
+    head = Head(x, w, target, VOCAB)
+    assert ((logp + nll).to(D64).abs() <= 2 * head.e).all()
+    loss, again, dx, dw = tg.linear_policy_step(x, w, target, logp, weights, one)
+    assert torch.equal(logp, again)
+    assert torch.equal(loss, torch.where(live, -weights, torch.zeros_like(loss)))
+    zero = torch.zeros(T, dtype=D64, device="cuda")
+    head.check_grads(weights.to(D64), zero, dx, dw)
+    head.check_grads(weights.to(D64), zero, *tg.linear_cross_entropy_step(x, w, target, weights)[1:])
 
 
 def test_autograd():
