@@ -137,12 +137,13 @@ __device__ __forceinline__ void accesses(int n, L load, U use) {
   }
 }
 
-// Squares of n elements, n <= kChunk.
+// A thread's sum of its part of n elements' squares, n <= kChunk.
 template <bool F32>
-__device__ __forceinline__ void squares(const void* p, int n, float (&s)[4]) {
+__device__ __forceinline__ float squares(const void* p, int n) {
   constexpr int E = F32 ? 4 : 8, kSize = F32 ? 4 : 2;
   const uint8_t* base = static_cast<const uint8_t*>(p) + threadIdx.x * (E * kSize);
   using V = Vec<F32, E>;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   accesses<E, V>(n, [&](V& v, int k) { v.load(base + k * (kThreads * E * kSize)); }, [&](const V& v, int) {
     float f[E];
     v.get(f);
@@ -154,12 +155,15 @@ __device__ __forceinline__ void squares(const void* p, int n, float (&s)[4]) {
     const float f = load_one(p, i, F32 ? 1 : 0);
     s[0] = fmaf(f, f, s[0]);
   }
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// A thread's sums of chunks meet with what each addition rounds off carried along (Kahan, 1965): added up one
+// by one, 2150 squares of fp16 values come out 1.5e-6 of their sum too large.
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     tg_grad_squares_kernel(const __grid_constant__ Table tb, float* part) {
   __shared__ float slots[kThreads / 32];
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float sum = 0.0f, off = 0.0f;
   tg::chain_wait();
   tg::chain_release();
   int at = 0;
@@ -169,22 +173,26 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int64_t i0 = int64_t(c - t.first) * kChunk;
     const int n = static_cast<int>(min(t.count - i0, int64_t(kChunk)));
     const void* p = static_cast<const uint8_t*>(t.data) + i0 * (t.kind & 1 ? 4 : 2);
+    float s = 0.0f;
     if (!(t.kind & 4)) {
       for (int i = threadIdx.x; i < n; i += kThreads) {
         const float v = load_one(p, i, t.kind);
-        s[0] = fmaf(v, v, s[0]);
+        s = fmaf(v, v, s);
       }
     } else if (t.kind & 1) {
-      squares<true>(p, n, s);
+      s = squares<true>(p, n);
     } else {
-      squares<false>(p, n, s);
+      s = squares<false>(p, n);
     }
+    const float y = s - off, next = sum + y;
+    off = next < INFINITY ? (next - sum) - y : 0.0f;  // an infinite sum stays one
+    sum = next;
   }
-  const float w = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+  const float w = warp_sum(sum - off);
   if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = w;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  float sum = 0.0f;
+  sum = 0.0f;
   for (int i = 0; i < kThreads / 32; ++i) sum += slots[i];
   part[blockIdx.x] = sum;
 }

@@ -154,7 +154,7 @@ __device__ __forceinline__ float teacher_at(const void* t, int64_t at, int is_f3
 // others (one at -inf has q = 0), kept for the gradient when `q` is given (0 for what is not
 // there).  A row without entries, or whose entries are all at -inf, has no teacher: loss 0 and no
 // gradient.  Logits are scaled after the row's largest is taken off, so that those at the type's lowest
-// value stay finite: a row of nothing else has a flat teacher.  alpha (one float): s max|w| / 2^15, written by the first block.  Bound by latency: 4096
+// value stay finite: a row of nothing else has a flat teacher.  alpha (one float): s max|w| / 2^15 (0 without wmax), written by the first block.  Bound by latency: 4096
 // rows of 65537 classes (2 KB of statistics each) and 64 entries 18 us, one row 5 us.
 __global__ void __launch_bounds__(kRowThreads)
     tg_head_rows_kernel(const float2* stats, int tiles, Logits lg, float scale,
@@ -778,10 +778,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     W = mem + at_w;
     ldw = ldwp;
   }
-  if (objective) {
-    if ((e = cudaMemsetAsync(wmax, 0, 4, stream)) != cudaSuccess)
-      return done(tg::record_cuda_error(e));
-  } else if (grad) {
+  if (grad && !objective) {
     // one block for what it can read in a few microseconds, else several on a zeroed maximum
     const int64_t reads = h.T * std::max(h.top, 1);
     const int blocks = reads <= 4096 ? 1 : static_cast<int>(std::min<int64_t>(cdiv(h.T, 256), sms));
@@ -828,7 +825,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
     if (h.T < kLeastRows) ex.a_rows = kLeastRows - t0;
-    ex.chained = !objective && (grad || copy_x || copy_w || t0 > 0);  // objective: a memset is before it
+    ex.chained = (grad && !objective) || copy_x || copy_w || t0 > 0;
     st = tg::gemm_extra(0, by_vocab, x, W, nullptr, n, h.V, h.D, ldx, ldw, h.V, ex, &gemm_opt,
                         stream);
     if (st != TG_OK) return done(st);
@@ -841,7 +838,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     chain(tg_head_rows_kernel, dim3(static_cast<unsigned>(n)), kRowThreads,
         stats, static_cast<int>(2 * cdiv(h.V, block_n)), Logits{z, ldz, picked}, h.scale, h.V, index, h.ignore,
         teacher, h.teacher_f32, h.ldt, h.top, dloss, objective ? nullptr : wmax, loss,
-        h.lse ? h.lse + t0 : nullptr, info, q, objective ? nullptr : alpha);
+        h.lse ? h.lse + t0 : nullptr, info, q,
+        objective ? reinterpret_cast<float*>(wmax) : alpha);  // objective: zeroes the maximum
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     if (objective) {
       e = launch_objective(h, nll, Weights{wmax, info, nullptr}, true, stream);
@@ -984,15 +982,18 @@ tg_status run_objective(const Head& h, cudaStream_t stream) {
   unsigned* err = nullptr;
   if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
   Layout lay;
-  // (the weights are zeroed together with their maximum)
-  const int64_t at_nll = lay.add(h.T * 4), at_small = lay.add(4), at_w = lay.add(grad ? h.T * 4 : 0);
+  // (the weights are zeroed together with their maximum; a policy's log probabilities are computed in place)
+  const bool own_nll = !(ob.kind == kPolicy && ob.logp);
+  const int64_t at_nll = lay.add(own_nll ? h.T * 4 : 0);
+  const int64_t at_small = lay.add(grad ? 4 : 0), at_w = lay.add(grad ? h.T * 4 : 0);
   uint8_t* mem = nullptr;
-  if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
+  if ((own_nll || grad) &&
+      (st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
-  float* nll = reinterpret_cast<float*>(mem + at_nll);
+  float* nll = own_nll ? reinterpret_cast<float*>(mem + at_nll) : ob.logp;
   float* w = reinterpret_cast<float*>(mem + at_w);
   const Weights wt{reinterpret_cast<unsigned*>(mem + at_small), nullptr, w};
-  cudaError_t e = cudaMemsetAsync(mem + at_small, 0, size_t(lay.bytes - at_small), stream);
+  cudaError_t e = grad ? cudaMemsetAsync(mem + at_small, 0, size_t(lay.bytes - at_small), stream) : cudaSuccess;
   if (e != cudaSuccess) st = tg::record_cuda_error(e);
   Head inner = h;
   inner.ob.kind = 0;
@@ -1014,7 +1015,7 @@ tg_status run_objective(const Head& h, cudaStream_t stream) {
     inner.dloss = w;
     st = run_head(inner, stream);
   }
-  e = cudaFreeAsync(mem, stream);
+  e = mem ? cudaFreeAsync(mem, stream) : cudaSuccess;
   return st == TG_OK && e != cudaSuccess ? tg::record_cuda_error(e) : st;
 }
 

@@ -17,6 +17,8 @@ from . import binding
 from .binding import TG_ACT_SILU
 from .tensors import check, here, library, on, ptr, rows, stream_handle, written
 
+_DENSE = torch.contiguous_format
+
 
 def _sizes(x, w_gate, w_up, trans_w):
     ldx, ldg, ldu = rows(x, "x"), rows(w_gate, "w_gate"), rows(w_up, "w_up")
@@ -61,10 +63,10 @@ def gated_linear(x, w_gate, w_up, activation: int = TG_ACT_SILU, trans_w: bool =
         written(out)
     gate = up = None
     if keep:
-        gate, up = torch.empty((2, M, N), dtype=torch.float16, device=x.device)
+        gate, up = torch.empty_like(out, memory_format=_DENSE), torch.empty_like(out, memory_format=_DENSE)
     check(library().tg_gated_f16(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(),
                                  ptr(gate), ptr(up), activation, 1 if trans_w else 0, M, N, K, ldx,
-                                 ldg, ldu, ldh, N, N, binding._opts(options), stream_handle(dev)),
+                                 ldg, ldu, ldh, N, N, options and binding._opts(options), stream_handle(dev)),
           "tg_gated_f16")
     return (out, gate, up) if keep else out
 
@@ -81,15 +83,17 @@ def gated_linear_backward(dh, x, w_gate, w_up, gate, up, activation: int = TG_AC
         with on(x.device, stream, dh, x, w_gate, w_up, gate, up):
             return gated_linear_backward(dh, x, w_gate, w_up, gate, up, activation, trans_w,
                                          input_grad, weight_grads, options)
-    lddh, ldgate, ldup = (_like(t, (M, N), dev, n) for t, n in ((dh, "dh"), (gate, "gate"), (up, "up")))
-    dx = torch.empty((M, K), dtype=torch.float16, device=x.device) if input_grad else None
+    shape = (M, N)
+    lddh, ldgate, ldup = _like(dh, shape, dev, "dh"), _like(gate, shape, dev, "gate"), _like(up, shape, dev, "up")
+    dx = torch.empty_like(x, memory_format=_DENSE) if input_grad else None
     dwg = dwu = None
     if weight_grads:
-        dwg, dwu = (torch.empty(w_gate.shape, dtype=torch.float16, device=x.device) for _ in range(2))
+        dwg = torch.empty_like(w_gate, memory_format=_DENSE)
+        dwu = torch.empty_like(w_up, memory_format=_DENSE)
     ldw = w_gate.shape[1]
     check(library().tg_gated_backward_f16(
         dh.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(),
         up.data_ptr(), ptr(dx), ptr(dwg), ptr(dwu), activation, 1 if trans_w else 0, M, N, K, lddh, ldx,
-        ldg, ldu, ldgate, ldup, K, ldw, ldw, binding._opts(options), stream_handle(dev)),
+        ldg, ldu, ldgate, ldup, K, ldw, ldw, options and binding._opts(options), stream_handle(dev)),
         "tg_gated_backward_f16")
     return dx, dwg, dwu

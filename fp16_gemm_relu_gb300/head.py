@@ -167,12 +167,10 @@ def linear_distillation_step(x, weight, teacher_index, teacher_logits, dloss,
     return loss, dx, dw
 
 
-def _token_values(T, dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            if t.dtype is not torch.float32:
-                raise TypeError(f"{name} must be torch.float32")
-            vector(t, T, dev, name)
+def _token_values(t, T, dev, name):
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.float32")
+    vector(t, T, dev, name)
 
 
 def _preference(x, weight, target, offsets, dloss, need_dx, need_dw, reference, beta, label_smoothing,
@@ -192,13 +190,13 @@ def _preference(x, weight, target, offsets, dloss, need_dx, need_dw, reference, 
         raise ValueError("offsets must be a (2 * pairs + 1,) tensor")
     vector(offsets, offsets.shape[0], dev, "offsets")
     pairs = offsets.shape[0] // 2
-    _token_values(T, dev, reference=reference)
+    if reference is not None:
+        _token_values(reference, T, dev, "reference")
     _weights(dloss, pairs, dev)
     loss = torch.empty(pairs, dtype=torch.float32, device=x.device)
     ratios = torch.empty((pairs, 2), dtype=torch.float32, device=x.device)
-    _, _, dx, dw = _outputs(x, weight, 0, D, False, need_dw, False)
-    if need_dx:
-        dx = torch.empty((T, D), dtype=torch.float16, device=x.device)
+    dx = torch.empty((T, D), dtype=torch.float16, device=x.device) if need_dx else None
+    dw = torch.empty(weight.shape, dtype=torch.float16, device=x.device) if need_dw else None
     check(library().tg_linear_preference_f16(
         x.data_ptr(), weight.data_ptr(), target.data_ptr(), ignore_index, logit_scale,
         offsets.data_ptr(), pairs, ptr(reference), beta, label_smoothing, 1 if average else 0,
@@ -253,7 +251,10 @@ def _policy(x, weight, target, old, advantage, dloss, need_dx, need_dw, referenc
     vector(target, T, dev, "target")
     if kl_weight != 0.0 and reference is None:
         raise ValueError("kl_weight needs reference")
-    _token_values(T, dev, old=old, advantage=advantage, reference=reference)
+    _token_values(old, T, dev, "old")
+    _token_values(advantage, T, dev, "advantage")
+    if reference is not None:
+        _token_values(reference, T, dev, "reference")
     _weights(dloss, T, dev)
     out = _outputs(x, weight, T, D, need_dx, need_dw, True)
     loss, logp, dx, dw = out
