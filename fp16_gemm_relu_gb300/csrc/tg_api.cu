@@ -490,6 +490,13 @@ __global__ void tg_pack_jobs_kernel(const __grid_constant__ PackJobs jobs) {
   const tg::PackJob& j = jobs.j[blockIdx.y];
   pack_rows(static_cast<const uint16_t*>(j.src), j.ld_src, static_cast<uint16_t*>(j.dst), j.ld_dst,
             j.rows, j.cols);
+  const int64_t cpr = (j.cols + 7) >> 3;
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < j.zeros * cpr;
+       i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t r = i / cpr;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.dst) + (j.rows + r) * j.ld_dst + ((i - r * cpr) << 3)) =
+        make_uint4(0, 0, 0, 0);
+  }
 }
 
 // The same copy with each lane taking kPackItems chunks (of warp items nwarps apart) per pass,
@@ -1336,7 +1343,7 @@ cudaError_t launch_pack_jobs(const PackJob* jobs, int n, int num_sms, bool chain
   int64_t chunks = 0;
   for (int i = 0; i < n; ++i) {
     all.j[i] = jobs[i];
-    chunks = std::max(chunks, jobs[i].rows * cdiv(jobs[i].cols, 8));
+    chunks = std::max(chunks, (jobs[i].rows + jobs[i].zeros) * cdiv(jobs[i].cols, 8));
   }
   return launch_chained(tg_pack_jobs_kernel, chained,
                         dim3(static_cast<unsigned>(aux_grid(chunks, num_sms)), static_cast<unsigned>(n)),

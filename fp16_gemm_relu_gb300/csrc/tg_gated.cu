@@ -26,6 +26,9 @@ bool misaligned(const void* p, unsigned bytes) {
 
 constexpr int64_t kMaxSize = (int64_t{1} << 30);
 constexpr int64_t kMaxLd = int64_t{1} << 36;
+// A TMA box of many rows of a matrix of fewer than eight (the rows of a swizzle atom) takes longer at some
+// addresses, so operands of the gradients' products lie in scratch of that many rows, the others zero.
+constexpr int64_t kLeastRows = 8;
 // Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
 // 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
 // Longer sums are taken in splits that are added in float32.
@@ -98,29 +101,31 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// dG and dU (fp16, M x np each, rows of ld; zeros from column N on), eight columns of kGradRows rows a
-// thread, whose loads go out together.
+// dG and dU (fp16, rows x np each, rows of ld; zeros from column N and row M on), eight columns of kGradRows
+// rows a thread, whose loads go out together.  Bound by HBM: 8192 x 14336 183 us, 6.4 TB/s (four rows a thread, at half
+// the occupancy, 253).
 constexpr int kGradRows = 2;
 template <int ACT>
 __global__ void __launch_bounds__(256, 4)
     tg_gated_grad_kernel(const __half* __restrict__ dh, int64_t lddh, const __half* __restrict__ gate,
                          int64_t ldg, const __half* __restrict__ up, int64_t ldu, __half* out, int64_t ld,
-                         int64_t np, int64_t M, int64_t N) {
+                         int64_t np, int64_t M, int64_t N, int64_t rows) {
   tg::chain_release();
   const int64_t c = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   if (c >= np) return;
-  for (int64_t r0 = int64_t(blockIdx.y) * kGradRows; r0 < M; r0 += int64_t(gridDim.y) * kGradRows) {
+  for (int64_t r0 = int64_t(blockIdx.y) * kGradRows; r0 < rows; r0 += int64_t(gridDim.y) * kGradRows) {
     uint4 d[kGradRows], g[kGradRows], u[kGradRows];
 #pragma unroll
     for (int i = 0; i < kGradRows; ++i) {
-      if (r0 + i >= M) break;
+      d[i] = g[i] = u[i] = make_uint4(0, 0, 0, 0);  // (a gate of 0 has a finite slope)
+      if (r0 + i >= M) continue;
       d[i] = load8(dh + (r0 + i) * lddh, c, N);
       g[i] = load8(gate + (r0 + i) * ldg, c, N);
       u[i] = load8(up + (r0 + i) * ldu, c, N);
     }
 #pragma unroll
     for (int i = 0; i < kGradRows; ++i) {
-      if (r0 + i >= M) break;
+      if (r0 + i >= rows) break;
       const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w}, gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w},
                      uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
       uint32_t a[4], b[4];
@@ -138,11 +143,11 @@ __global__ void __launch_bounds__(256, 4)
 
 cudaError_t launch_grad(int act, const __half* dh, int64_t lddh, const __half* gate, int64_t ldg,
                         const __half* up, int64_t ldu, __half* out, int64_t ld, int64_t np, int64_t M,
-                        int64_t N, cudaStream_t stream) {
+                        int64_t N, int64_t rows, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(cdiv(np, 2048)),
-                  static_cast<unsigned>(std::min<int64_t>(cdiv(M, kGradRows), 65535)));
+                  static_cast<unsigned>(std::min<int64_t>(cdiv(rows, kGradRows), 65535)));
   auto go = [&](auto kern) {
-    kern<<<grid, 256, 0, stream>>>(dh, lddh, gate, ldg, up, ldu, out, ld, np, M, N);
+    kern<<<grid, 256, 0, stream>>>(dh, lddh, gate, ldg, up, ldu, out, ld, np, M, N, rows);
     return cudaGetLastError();
   };
   switch (act) {
@@ -190,14 +195,16 @@ struct Operands {
   const void *x, *wg, *wu;
   int64_t ldx, ldwg, ldwu;
   int64_t at[3];  // of the copies in scratch, or -1
+  int64_t zeros;  // rows of zeros behind a copy of X
 
-  // Of what is read: x, both weights.
-  void plan(const Gated& a, bool need_x, bool need_w, Layout* lay) {
-    auto one = [&](const void* p, int64_t ld, int64_t rows, int64_t cols) -> int64_t {
-      return misaligned(p, 16) || ld % 8 != 0 ? lay->add(rows * round_up(cols, 64) * 2) : -1;
+  // Of what is read (x, both weights); X of fewer than least_rows rows is copied too, with zeros behind it.
+  void plan(const Gated& a, bool need_x, bool need_w, int64_t least_rows, Layout* lay) {
+    zeros = std::max<int64_t>(least_rows - a.M, 0);
+    auto one = [&](const void* p, int64_t ld, int64_t rows, int64_t cols, bool copy = false) -> int64_t {
+      return copy || misaligned(p, 16) || ld % 8 != 0 ? lay->add(rows * round_up(cols, 64) * 2) : -1;
     };
     const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
-    at[0] = need_x ? one(a.X, a.ldx, a.M, a.K) : -1;
+    at[0] = need_x ? one(a.X, a.ldx, a.M + zeros, a.K, zeros > 0) : -1;
     at[1] = need_w ? one(a.Wg, a.ldwg, w_rows, w_cols) : -1;
     at[2] = need_w ? one(a.Wu, a.ldwu, w_rows, w_cols) : -1;
   }
@@ -206,16 +213,16 @@ struct Operands {
     tg::PackJob jobs[3];
     int n = 0;
     auto one = [&](int i, const void* p, int64_t ld, int64_t rows, int64_t cols, const void** out,
-                   int64_t* ldo) {
+                   int64_t* ldo, int64_t more = 0) {
       *out = p;
       *ldo = ld;
       if (at[i] < 0) return;
       *out = mem + at[i];
       *ldo = round_up(cols, 64);
-      jobs[n++] = tg::PackJob{p, mem + at[i], ld, *ldo, rows, cols};
+      jobs[n++] = tg::PackJob{p, mem + at[i], ld, *ldo, rows, cols, more};
     };
     const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
-    one(0, a.X, a.ldx, a.M, a.K, &x, &ldx);
+    one(0, a.X, a.ldx, a.M, a.K, &x, &ldx, zeros);
     one(1, a.Wg, a.ldwg, w_rows, w_cols, &wg, &ldwg);
     one(2, a.Wu, a.ldwu, w_rows, w_cols, &wu, &ldwu);
     *any = n > 0;
@@ -273,8 +280,17 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
                        cudaStream_t stream) {
   const int64_t rows = a.trans ? a.N : a.K, cols = a.trans ? a.K : a.N;  // of each output
   tg::TilePlan plan;
-  tg_status st = tg::plan_tiles(a.trans ? 2 * rows : rows, a.trans ? cols : 2 * cols, a.M, kSumLength, false,
-                                opt, &plan);
+  tg_options o;
+  std::memset(&o, 0, sizeof(o));
+  if (opt) o = *opt;
+  // Few tokens: a tile is all epilogue, which one CTA with 16 epilogue warps does faster than a pair with eight
+  // each (4096 x 14336 from 64 tokens 49 against 65 us, 54 in tiles of 128 columns; from 256 tokens 86 against 79).
+  if (a.M <= 128 && !o.pair) {
+    o.pair = -1;
+    if (!o.block_n && cdiv(rows, 128) * cdiv(cols, 256) >= 76) o.block_n = 256;
+  }
+  tg_status st = tg::plan_tiles(a.trans ? 2 * rows : rows, a.trans ? cols : 2 * cols, a.M, kSumLength, true,
+                                &o, &plan);
   if (st != TG_OK) return st;
   if (plan.splits > 1) return TG_ERR_NO_WORKSPACE;
   const int bm = plan.pair ? 256 : 128, bn = plan.block_n;
@@ -306,12 +322,13 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
   l.stream = stream;
   const int kbox = plan.pair ? 128 : 64;
   bool ok;
+  const int64_t tokens = std::max(a.M, kLeastRows);  // zeros from a.M on
   if (a.trans)
-    ok = tg::half_map(&l.a, g, 2 * np, a.M, 2 * np, 64, kbox) &&
-         tg::half_map(&l.b, ops.x, a.K, a.M, ops.ldx, 64, kbox);
+    ok = tg::half_map(&l.a, g, 2 * np, tokens, 2 * np, 64, kbox) &&
+         tg::half_map(&l.b, ops.x, a.K, tokens, ops.ldx, 64, kbox);
   else
-    ok = tg::half_map(&l.a, ops.x, a.K, a.M, ops.ldx, 64, kbox) &&
-         tg::half_map(&l.b, g, 2 * np, a.M, 2 * np, 64, kbox);
+    ok = tg::half_map(&l.a, ops.x, a.K, tokens, ops.ldx, 64, kbox) &&
+         tg::half_map(&l.b, g, 2 * np, tokens, 2 * np, 64, kbox);
   if (tma)
     ok = ok && tg::half_map(&l.out, dWg, cols, rows, lddwg, 64, 32) &&
          tg::half_map(&l.out2, dWu, cols, rows, lddwu, 64, 32);
@@ -348,7 +365,7 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   Operands ops;
   const int64_t nw = round_up(N, 32), stride = M * 2 * nw;
   Layout lay;
-  ops.plan(a, true, true, &lay);
+  ops.plan(a, true, true, 0, &lay);
   const bool f32 = plan.splits > 1;
   const int64_t at_ws = lay.add(f32 ? plan.splits * stride * 4 : 0);
   uint8_t* mem = nullptr;
@@ -462,8 +479,9 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   const int64_t np = round_up(N, 128), ld = 2 * np;
   Layout lay;
   Operands ops;
-  const int64_t at_g = lay.add(M * ld * 2);
-  ops.plan(a, dWg || dWu, dX, &lay);
+  const int64_t rows = std::max(M, kLeastRows);
+  const int64_t at_g = lay.add(rows * ld * 2);
+  ops.plan(a, dWg || dWu, dX, dWg || dWu ? kLeastRows : 0, &lay);
   uint8_t* mem = nullptr;
   if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
@@ -473,7 +491,7 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   };
   __half* g = reinterpret_cast<__half*>(mem + at_g);
   e = launch_grad(activation, static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
-                  static_cast<const __half*>(up), ldup, g, ld, np, M, N, stream);
+                  static_cast<const __half*>(up), ldup, g, ld, np, M, N, rows, stream);
   if (e != cudaSuccess) return done(tg::record_cuda_error(e));
   bool copied = false;
   if ((e = ops.copy(a, mem, sms, true, stream, &copied)) != cudaSuccess) return done(tg::record_cuda_error(e));
@@ -500,7 +518,20 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
     ex.B2 = ops.wu;
     ex.ldb2 = ops.ldwu;
     ex.b_k = N;
-    st = tg::gemm_extra(0, !trans_w, g, ops.wg, dX, M, K, ld, ld, ops.ldwg, lddx, ex, opt, stream);
+    ex.a_rows = rows;
+    // Few tokens: one row of tiles reads the weights once, at the memory's rate if its splits make one wave of
+    // blocks over the SMs.
+    tg_options o;
+    std::memset(&o, 0, sizeof(o));
+    if (opt) o = *opt;
+    const int64_t width = K <= 2048 ? 128 : 256;
+    const int64_t splits = std::max(std::min({sms / cdiv(K, width), ld / 128, int64_t(32)}), cdiv(ld, kSumLength));
+    if (M <= 128 && splits > 1 && !o.pair && !o.block_n && !o.split_k) {
+      o.pair = -1;
+      o.block_n = static_cast<int>(width);
+      o.split_k = static_cast<int>(splits);
+    }
+    st = tg::gemm_extra(0, !trans_w, g, ops.wg, dX, M, K, ld, ld, ops.ldwg, lddx, ex, &o, stream);
     if (st != TG_OK) return done(st);
   }
   return done(TG_OK);

@@ -6,21 +6,23 @@ namespace tg {
 
 namespace {
 template <typename K, typename... Q>
-cudaError_t launch(K kern, int smem, const GemmLaunch& l, const Q&... args) {
+cudaError_t launch(K kern, int threads, int smem, const GemmLaunch& l, const Q&... args) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), kThreads, smem, l.stream,
+  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), threads, smem, l.stream,
                         args...);
 }
 
 template <typename K>
 cudaError_t launch_dual(K kern, int smem, const GemmLaunch& l) {
-  return launch(kern, smem, l, l.a, l.b, l.b2, l.out, l.p);
+  return launch(kern, kThreads, smem, l, l.a, l.b, l.b2, l.out, l.p);
 }
-template <typename K>
-cudaError_t launch_two(K kern, int smem, const GemmLaunch& l) {
-  return launch(kern, smem, l, l.a, l.b, l.out, l.out2, l.p, l.two);
+template <int BN>
+cudaError_t launch_two(const GemmLaunch& l) {
+  using Cfg = TileCfg<BN, BN / 64>;
+  return launch(tg_gemm_tc_two_kernel<BN>, Cfg::kThreadsEG, Cfg::kSmemBytes, l, l.a, l.b, l.out, l.out2, l.p,
+                l.two);
 }
 
 template <bool OUT_F32>
@@ -42,14 +44,10 @@ cudaError_t launch_gemm_dual(const GemmLaunch& l, bool out_f32, int block_n) {
 }
 
 cudaError_t launch_gemm_two(const GemmLaunch& l, int block_n) {
-  switch (block_n) {
-    case 256: return launch_two(tg_gemm_tc_two_kernel<256>, TileCfg<256>::kSmemBytes, l);
-    case 192: return launch_two(tg_gemm_tc_two_kernel<192>, TileCfg<192>::kSmemBytes, l);
-    case 128: return launch_two(tg_gemm_tc_two_kernel<128>, TileCfg<128>::kSmemBytes, l);
-    default: break;
-  }
+  if (block_n) return block_n == 256 ? launch_two<256>(l) : launch_two<128>(l);
   if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
-  return launch_two(tg_gemm_pair_two_kernel<0>, PairCfgFwd::kSmemBytes, l);
+  return launch(tg_gemm_pair_two_kernel<2>, 64 + 2 * 32 * kEpiWarps, PairCfgFwd::kSmemBytes, l, l.a, l.b,
+                l.out, l.out2, l.p, l.two);
 }
 
 }  // namespace tg

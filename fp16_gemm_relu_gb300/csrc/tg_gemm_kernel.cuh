@@ -156,14 +156,17 @@ __device__ __forceinline__ float epilogue_value(float x, int row, int col, const
   return x;
 }
 
-template <int BN>
+// EG: groups of four epilogue warps.  One group has the whole tile and two staging buffers a warp; with
+// several each has its share of the columns and one buffer a warp (epilogue_share).
+template <int BN, int EG = 1>
 struct TileCfg {
   static_assert(BN % 64 == 0 && BN >= 64 && BN <= 256, "BN must be 64..256 in steps of 64");
   static constexpr int kAStage = kBM * kBK * 2;                 // 16 KB
   static constexpr int kBBox = kBK * 64 * 2;                    // one 64(N) x 64(K) box, 8 KB
   static constexpr int kBStage = kBK * BN * 2;
   static constexpr int kStageBytes = kAStage + kBStage;
-  static constexpr int kStagingBytes = kEpiWarps * 2 * kStagingBuf;
+  static constexpr int kStagingBytes = kEpiWarps * (EG == 1 ? 2 : EG) * kStagingBuf;
+  static constexpr int kThreadsEG = 64 + 32 * kEpiWarps * EG;
   static constexpr int kStagesFit = (kSmemLimit - kSmemReserve - kStagingBytes) / kStageBytes;
   static constexpr int kStages = kStagesFit > 8 ? 8 : kStagesFit;
   static constexpr int kAccStride = BN <= 128 ? 128 : 256;      // TMEM columns per accumulator
@@ -756,8 +759,7 @@ template <int MODE = kModePlain>
 __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const GemmParams& p,
                                                 const uint32_t (&r0)[32],
                                                 const uint32_t (&r1)[32], int row0, int col0,
-                                                uint8_t* stg, int& sb, int lane, __half* c = nullptr,
-                                                long long ldc = 0) {
+                                                uint8_t* stg, int& sb, int lane) {
   uint32_t pk[32];
   if constexpr (MODE == kModeScaled) {
     epilogue_scaled_32(r0, row0 + lane, col0, p, pk);
@@ -774,7 +776,7 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
     epilogue_general_32(r0, row0 + lane, col0, p, pk);
     epilogue_general_32(r1, row0 + lane, col0 + 32, p, pk + 16);
   }
-  if (MODE == kModeTwo || col0 < p.n_tma) {
+  if (col0 < p.n_tma) {
     uint8_t* st = stg + sb * kStagingBuf;
     if (lane == 0) bulk_wait_read<1>();  // the store that last read this buffer is done
     __syncwarp();
@@ -782,13 +784,6 @@ __device__ __forceinline__ void store_chunk_f16(const CUtensorMap* tmOut, const 
     for (int j = 0; j < 8; ++j) {
       uint4 v = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
       *reinterpret_cast<uint4*>(st + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
-    }
-    if constexpr (MODE == kModeTwo) {  // whole rows by TMA, or none
-      if (p.n_tma == 0) {
-        store_rows(c, ldc, st, row0, col0, p.M, p.N, lane);
-        sb ^= 1;
-        return;
-      }
     }
     fence_async_smem();
     __syncwarp();
@@ -835,8 +830,7 @@ template <int BN, bool OUT_F32, bool PERM8 = false, int MODE = kModePlain>
 __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const GemmParams& p,
                                               uint32_t tl, int row0, int col_base, int split,
                                               uint8_t* stg, int& sb, uint32_t release_bar,
-                                              bool remote, int lane, __half* c_out = nullptr,
-                                              long long ldc = 0) {
+                                              bool remote, int lane) {
   auto release = [&]() {
     tc_fence_before();
     __syncwarp();
@@ -851,7 +845,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
     release();
     return;
   }
-  static_assert(MODE == kModePlain || (OUT_F32 ? MODE == kModeAdd : MODE == kModeScaled || MODE == kModeTwo),
+  static_assert(MODE == kModePlain || (OUT_F32 ? MODE == kModeAdd : MODE == kModeScaled),
                 "the sum is added in float32 and scaled in fp16");
   if constexpr (!OUT_F32) {
 #pragma unroll 1
@@ -866,8 +860,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
         unperm8(r0);
         unperm8(r1);
       }
-      if (MODE == kModeTwo && col_base + c * 64 >= p.N) continue;
-      store_chunk_f16<MODE>(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane, c_out, ldc);
+      store_chunk_f16<MODE>(tmOut, p, r0, r1, row0, col_base + c * 64, stg, sb, lane);
     }
   } else {
 #pragma unroll 1
@@ -898,6 +891,64 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
   }
 }
 
+// The share of an output tile that one of several groups of epilogue warps has: 32 rows, BNW columns, 32 columns
+// in registers at a time, through the warp's one staging buffer.  A tile of few k-blocks is all epilogue, and
+// four warps are bound by the latency of their steps: 3.7 us a tile of 256 columns, as long as 14 k-blocks.
+template <int BNW, int MODE>
+__device__ __forceinline__ void epilogue_share(const CUtensorMap* tmOut, const GemmParams& p, uint32_t tl,
+                                               int row0, int col_base, uint8_t* stg,
+                                               uint32_t release_bar, bool remote, int lane, __half* c_out,
+                                               long long ldc) {
+  auto release = [&]() {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (remote)
+        mbar_arrive_cluster(release_bar);
+      else
+        mbar_arrive(release_bar);
+    }
+  };
+  if (row0 >= p.M || col_base >= p.N) {  // nothing of this warp's is in C
+    release();
+    return;
+  }
+#pragma unroll 1
+  for (int c = 0; c < BNW / 64; ++c) {
+    const int col0 = col_base + c * 64;
+    if (lane == 0) bulk_wait_read<0>();  // the store that last read the buffer is done
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r[32], pk[16];
+      tmem_ld_x32(tl + c * 64 + h * 32, r);
+      tmem_wait_ld(r);
+      if (c == BNW / 64 - 1 && h == 1) release();
+      if constexpr (MODE == kModeScaled) {
+        epilogue_scaled_32(r, row0 + lane, col0 + h * 32, p, pk);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) pk[i] = relu_pack_h2(r[2 * i], r[2 * i + 1], 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)) =
+            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+    }
+    if (col0 >= p.N) continue;
+    if (p.n_tma == p.N) {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tmOut, smem_u32(stg), col0, row0);
+        bulk_commit();
+      }
+    } else {
+      store_rows(c_out, ldc, stg, row0, col0, p.M, p.N, lane);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------------------
@@ -911,12 +962,13 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap* tmOut, const Ge
 // which keeps their per-k-block instruction count inside the MMA time.  GENERAL == true reads
 // the layouts from p.a_mn and p.b_k (the transposed-operand GEMMs of the backward pass).
 // kModeDual: tmB2 is the second right operand, of the layout of tmB.
-template <int BN, bool OUT_F32, bool GENERAL, int MODE>
+template <int BN, bool OUT_F32, bool GENERAL, int MODE, int EG = 1>
 __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                              const CUtensorMap& tmOut, const GemmParams& p,
                                              const CUtensorMap* tmB2, const TwoOut* two = nullptr,
                                              const CUtensorMap* tmOut2 = nullptr) {
-  using Cfg = TileCfg<BN>;
+  static_assert(EG == 1 || (!OUT_F32 && BN % (64 * EG) == 0), "shares of whole 64-column chunks");
+  using Cfg = TileCfg<BN, EG>;
   constexpr int S = Cfg::kStages;
   const int a_mn = MODE == kModeTwo ? 1 : GENERAL ? p.a_mn : 0;
   const int b_k = MODE == kModeTwo ? 0 : GENERAL ? p.b_k : 0;
@@ -946,7 +998,7 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), kEpiWarps);
+      mbar_init(smem_u32(&tempty[b]), kEpiWarps * EG);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
@@ -1075,7 +1127,7 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
     // ------------------------------ epilogue ------------------------------
     const int q = warp & 3;       // TMEM lane quarter this warp may access
     const int ew = warp - 2;      // staging slot
-    uint8_t* stg = sStg + ew * 2 * kStagingBuf;
+    uint8_t* stg = sStg + ew * (EG == 1 ? 2 : 1) * kStagingBuf;
     int sb = 0;
     int t = 0;
     for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++t) {
@@ -1089,12 +1141,21 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
       tc_fence_after();
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
-      if constexpr (MODE == kModeTwo) {
-        const bool m2 = w.m_blk >= two->m_first, n2 = w.n_blk >= two->n_first, second = m2 || n2;
-        epilogue_tile<BN, OUT_F32, false, MODE>(
-            second ? tmOut2 : &tmOut, p, tl, (w.m_blk - (m2 ? two->m_first : 0)) * kBM + q * 32,
-            (w.n_blk - (n2 ? two->n_first : 0)) * BN, w.split, stg, sb, smem_u32(&tempty[buf]), false,
-            lane, second ? two->c : p.c, second ? two->ldc : p.ldc);
+      if constexpr (EG > 1) {
+        constexpr int BNW = BN / EG;
+        const int part = (ew >> 2) * BNW;
+        int m_blk = w.m_blk, n_blk = w.n_blk;
+        const CUtensorMap* out = &tmOut;
+        __half* c_out = p.c;
+        long long ldc = p.ldc;
+        if constexpr (MODE == kModeTwo) {
+          const bool m2 = m_blk >= two->m_first, n2 = n_blk >= two->n_first;
+          if (m2) m_blk -= two->m_first;
+          if (n2) n_blk -= two->n_first;
+          if (m2 || n2) out = tmOut2, c_out = two->c, ldc = two->ldc;
+        }
+        epilogue_share<BNW, MODE>(out, p, tl + part, m_blk * kBM + q * 32, n_blk * BN + part, stg,
+                                  smem_u32(&tempty[buf]), false, lane, c_out, ldc);
       } else {
         epilogue_tile<BN, OUT_F32, false, epilogue_mode(MODE)>(&tmOut, p, tl, w.m_blk * kBM + q * 32,
                                                                w.n_blk * BN, w.split, stg, sb,
@@ -1131,14 +1192,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_gemm_body<BN, OUT_F32, true, kModeDual>(tmA, tmB, tmOut, p, &tmB2);
 }
 
+// The scaled sum (GENERAL layouts), a group of epilogue warps to every 64 columns.
 template <int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TileCfg<BN, BN / 64>::kThreadsEG, 1)
+    tg_gemm_tc_scaled_kernel(const __grid_constant__ CUtensorMap tmA,
+                             const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmOut,
+                             const __grid_constant__ GemmParams p) {
+  tc_gemm_body<BN, false, true, kModeScaled, BN / 64>(tmA, tmB, tmOut, p, nullptr);
+}
+// Two outputs, likewise.
+template <int BN>
+__global__ void __launch_bounds__(TileCfg<BN, BN / 64>::kThreadsEG, 1)
     tg_gemm_tc_two_kernel(const __grid_constant__ CUtensorMap tmA,
                           const __grid_constant__ CUtensorMap tmB,
                           const __grid_constant__ CUtensorMap tmOut,
                           const __grid_constant__ CUtensorMap tmOut2,
                           const __grid_constant__ GemmParams p, const __grid_constant__ TwoOut two) {
-  tc_gemm_body<BN, false, true, kModeTwo>(tmA, tmB, tmOut, p, nullptr, &two, &tmOut2);
+  tc_gemm_body<BN, false, true, kModeTwo, BN / 64>(tmA, tmB, tmOut, p, nullptr, &two, &tmOut2);
 }
 
 // Epilogue of one K half of a tail-split tile (fp16 output), for one warp of the pair kernel:
@@ -1255,7 +1326,7 @@ struct AClassMaps {
 // K-major ones as one {64 K, 128} box per 64-k block.  tiles_m/tiles_n in p count 256 x 256
 // pair tiles.  With A_CLS (float32 output, forward layout) A comes through `cls` (tmA unused)
 // and M tiles index class-major rows.
-template <bool OUT_F32, bool A_MN, bool B_K, bool A_CLS, int MODE = kModePlain>
+template <bool OUT_F32, bool A_MN, bool B_K, bool A_CLS, int MODE = kModePlain, int EG = 1>
 __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                const CUtensorMap& tmOut, const GemmParams& p,
                                                const AClassMaps* cls,
@@ -1263,6 +1334,8 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
                                                const TwoOut* two = nullptr,
                                                const CUtensorMap* tmOut2 = nullptr) {
   static_assert(!A_CLS || (OUT_F32 && !A_MN && !B_K), "row classes: float32 output, forward layout");
+  // (two groups of epilogue warps with one staging buffer a warp take the room of one with two)
+  static_assert(EG == 1 || (EG == 2 && !OUT_F32), "one or two groups of epilogue warps");
   using Cfg = PairCfgFwd;
   constexpr int S = Cfg::kStages;
   constexpr int KB = Cfg::kKB;
@@ -1295,7 +1368,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&tfull[b]), 1);
-      mbar_init(smem_u32(&tempty[b]), 2 * kEpiWarps);
+      mbar_init(smem_u32(&tempty[b]), 2 * kEpiWarps * EG);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0u;
@@ -1463,7 +1536,7 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
     // ------------------------------ epilogue (both CTAs) ------------------------------
     const int q = warp & 3;
     const int ew = warp - 2;
-    uint8_t* stg = sStg + ew * 2 * kStagingBuf;
+    uint8_t* stg = sStg + ew * (EG == 1 ? 2 : 1) * kStagingBuf;
     int sb = 0;
     int t = 0;
     for (int u = cluster; u < p.units; u += nclusters, ++t) {
@@ -1479,12 +1552,21 @@ __device__ __forceinline__ void pair_gemm_body(const CUtensorMap& tmA, const CUt
                           static_cast<uint32_t>(buf * Cfg::kAccStride);
       const int row0 = w.m_blk * 2 * kBM + static_cast<int>(rank) * kBM + q * 32;
       const uint32_t release_bar = mapa_shared(smem_u32(&tempty[buf]), 0);
-      if constexpr (MODE == kModeTwo) {  // (no tail)
-        const bool m2 = w.m_blk >= two->m_first, n2 = w.n_blk >= two->n_first, second = m2 || n2;
-        epilogue_tile<Cfg::kBN, OUT_F32, false, MODE>(
-            second ? tmOut2 : &tmOut, p, tl, row0 - (m2 ? two->m_first * 2 * kBM : 0),
-            (w.n_blk - (n2 ? two->n_first : 0)) * Cfg::kBN, w.split, stg, sb, release_bar, true, lane,
-            second ? two->c : p.c, second ? two->ldc : p.ldc);
+      if constexpr (EG > 1) {  // (no tail)
+        constexpr int BNW = Cfg::kBN / EG;
+        const int part = (ew >> 2) * BNW;
+        int row = row0, n_blk = w.n_blk;
+        const CUtensorMap* out = &tmOut;
+        __half* c_out = p.c;
+        long long ldc = p.ldc;
+        if constexpr (MODE == kModeTwo) {
+          const bool m2 = w.m_blk >= two->m_first, n2 = n_blk >= two->n_first;
+          if (m2) row -= two->m_first * 2 * kBM;
+          if (n2) n_blk -= two->n_first;
+          if (m2 || n2) out = tmOut2, c_out = two->c, ldc = two->ldc;
+        }
+        epilogue_share<BNW, MODE>(out, p, tl + part, row, n_blk * Cfg::kBN + part, stg, release_bar, true,
+                                  lane, c_out, ldc);
       } else if (!OUT_F32 && w.tail_slot >= 0)
         epilogue_tail<Cfg::kBN, epilogue_mode(MODE)>(&tmOut, p, tl, row0, w.n_blk * Cfg::kBN, w.tail_slot,
                                       w.split, static_cast<int>(rank) * 4 + q, stg, sb,
@@ -1529,14 +1611,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pair_gemm_body<OUT_F32, false, B_K, false, kModeDual>(tmA, tmB, tmOut, p, nullptr, &tmB2);
 }
 
-template <int NONE>  // a template so that every unit including this header shares one definition
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int EG>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps * EG, 1)
     tg_gemm_pair_two_kernel(const __grid_constant__ CUtensorMap tmA,
                             const __grid_constant__ CUtensorMap tmB,
                             const __grid_constant__ CUtensorMap tmOut,
                             const __grid_constant__ CUtensorMap tmOut2,
                             const __grid_constant__ GemmParams p, const __grid_constant__ TwoOut two) {
-  pair_gemm_body<false, true, false, false, kModeTwo>(tmA, tmB, tmOut, p, nullptr, nullptr, &two, &tmOut2);
+  pair_gemm_body<false, true, false, false, kModeTwo, EG>(tmA, tmB, tmOut, p, nullptr, nullptr, &two, &tmOut2);
 }
 
 // The CTA-pair kernel with A read through row classes (float32 partials, forward layout).

@@ -5,19 +5,23 @@ namespace tg {
 
 namespace {
 template <typename K>
-cudaError_t launch(K kern, int smem, const GemmLaunch& l) {
+cudaError_t launch(K kern, int smem, const GemmLaunch& l, int threads = kThreads) {
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), kThreads, smem, l.stream,
+  return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), threads, smem, l.stream,
                         l.a, l.b, l.out, l.p);
 }
 
+// A^T B is dW of few tokens, all epilogue: the kernel with more epilogue warps (28672 x 1024 from 256 tokens
+// 20 us with four).
 template <int BN>
 cudaError_t launch_tc(const GemmLaunch& l) {
   constexpr int smem = TileCfg<BN>::kSmemBytes;
-  return l.p.a_mn || l.p.b_k ? launch(tg_gemm_tc_kernel<BN, false, true, kModeScaled>, smem, l)
-                             : launch(tg_gemm_tc_kernel<BN, false, false, kModeScaled>, smem, l);
+  using Wide = TileCfg<BN, BN / 64>;
+  if (l.p.a_mn) return launch(tg_gemm_tc_scaled_kernel<BN>, Wide::kSmemBytes, l, Wide::kThreadsEG);
+  return l.p.b_k ? launch(tg_gemm_tc_kernel<BN, false, true, kModeScaled>, smem, l)
+                 : launch(tg_gemm_tc_kernel<BN, false, false, kModeScaled>, smem, l);
 }
 }  // namespace
 

@@ -161,6 +161,7 @@ struct PackJob {
   const void* src;
   void* dst;
   int64_t ld_src, ld_dst, rows, cols;
+  int64_t zeros;  // rows of zeros (of round_up(cols, 8)) behind the copy
 };
 cudaError_t launch_pack_jobs(const PackJob* jobs, int n, int num_sms, bool chained, cudaStream_t stream);
 
