@@ -47,10 +47,10 @@ class Student:
 
     def step(self, loss_scale: float, rate: float) -> bool:
         """Moves the masters along the gradients; False (and no move) if one overflowed fp16."""
-        grads = {k: w.grad.float() / loss_scale for k, w in self.w.items()}
-        if not all(bool(torch.isfinite(g).all()) for g in grads.values()):
+        norm, grads = tg.clip_gradients([w.grad for w in self.w.values()], float("inf"), loss_scale)
+        if not bool(torch.isfinite(norm)):
             return False
-        for k, g in grads.items():
+        for k, g in zip(self.w, grads):
             self.master[k] -= rate * g
         self.refresh()
         return True

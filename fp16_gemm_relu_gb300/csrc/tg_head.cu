@@ -433,7 +433,7 @@ constexpr int kPairThreads = 256;
 // The sums are float64: those of a long answer are large and nearly the same in both.  Bound by latency:
 // one pass over the rows of both sequences and one meeting of the block.
 __global__ void __launch_bounds__(kPairThreads)
-    tg_head_pairs_kernel(Objective ob, const float* nll, const int64_t* __restrict__ target,
+    tg_head_pairs_kernel(Objective ob, const float* nll, const int64_t* __restrict__ index,
                          int64_t ignore, int64_t rows, Weights wt) {
   __shared__ double sums[2][kPairThreads / 32];
   __shared__ int counts[2][kPairThreads / 32];
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kPairThreads)
   double r[2] = {0.0, 0.0}, n[2];
   int count[2] = {0, 0};
   for (int64_t t = o[0] + threadIdx.x; fits && t < o[2]; t += kPairThreads) {
-    if (target[t] == ignore) continue;
+    if (index[t] == ignore) continue;
     const double d = -static_cast<double>(nll[t]) - (ob.reference ? ob.reference[t] : 0.0f);
     if (t < o[1]) {
       r[0] += d;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kPairThreads)
   if (!ob.dloss) return;
   __syncthreads();
   for (int64_t t = o[0] + threadIdx.x; fits && t < o[2]; t += kPairThreads)
-    if (target[t] != ignore) wt.put(t, weight[t >= o[1]]);
+    if (index[t] != ignore) wt.put(t, weight[t >= o[1]]);
 }
 
 // A thread a row (Schulman et al., 2017; the penalty's unbiased, never negative estimate is Schulman's
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kPairThreads)
 // The slope along logp is -r A where the first is the smaller, else 0, and kl (1 - e^d).  Comparisons
 // are such that a NaN goes through.
 __global__ void __launch_bounds__(256)
-    tg_head_policy_kernel(Objective ob, const float* nll, const int64_t* __restrict__ target,
+    tg_head_policy_kernel(Objective ob, const float* nll, const int64_t* __restrict__ index,
                           int64_t ignore, int64_t rows, Weights wt) {
   const int64_t r = blockIdx.x * int64_t(blockDim.x) + threadIdx.x;
   tg::chain_wait();
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(256)
   unsigned most = 0;
   if (r < rows) {
     float loss = 0.0f, logp = 0.0f, slope = 0.0f;
-    if (target[r] != ignore) {
+    if (index[r] != ignore) {
       logp = -nll[r];
       const float ratio = expf(logp - ob.old[r]), adv = ob.advantage[r];
       const float kept = ratio < ob.low ? ob.low : ratio > ob.high ? ob.high : ratio;
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(256)
     }
     if (ob.loss) ob.loss[r] = loss;
     if (ob.logp) ob.logp[r] = logp;
-    if (ob.dloss && target[r] != ignore) {
+    if (ob.dloss && index[r] != ignore) {
       const float w = -slope * ob.dloss[r];
       wt.put(r, w);
       most = weight_bits(w);
