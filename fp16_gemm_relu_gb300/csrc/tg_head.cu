@@ -316,9 +316,12 @@ __global__ void __launch_bounds__(256)
   const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   tg::chain_wait();
   tg::chain_release();
+  // RAW: the rows' common factor 2^k takes the largest weight to [2^14, 2^15)
   const float most = RAW ? __uint_as_float(*wmax) : 0.0f;
+  const int k = min(14 - (static_cast<int>(__float_as_uint(most) >> 23) - 127), 120);
+  const float up = __int_as_float((127 + (most == most ? k : 0)) << 23);
   if (RAW && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-    *alpha = s * (most == most ? most : 1.0f) / kGScale;  // rows that do not count stay 0
+    *alpha = s / up;  // (not NaN: rows that do not count stay 0)
   if (FINE && x2 != nullptr && blockIdx.x == 0) {
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
       const uint16_t* from = x + r * ldx;
@@ -333,9 +336,9 @@ __global__ void __launch_bounds__(256)
   if (v0 >= vocab) return;
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     RowInfo ri = info[r];
-    if (RAW && ri.target >= 0) ri.gs = most != most ? most : row_factor(ri.gs, most);
     const float4* src = reinterpret_cast<const float4*>(z + r * ldz + v0);
     const float4 a = __ldcs(src), b = __ldcs(src + 1);  // ldz and ldg are multiples of 8
+    if (RAW && ri.target >= 0) ri.gs = most == most ? ri.gs * up : most;
     const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t w[4], u[4];
 #pragma unroll
@@ -405,7 +408,7 @@ struct Objective {
 enum : int { kPreference = 1, kPolicy = 2 };
 
 // Where an objective's weights go: max|w| over the rows as for cross entropy, NaN if any pair's offsets are
-// wrong; and each row's, into its RowInfo::gs (the factor 2^15 / max|w| is taken in the pass over the logits) or
+// wrong; and each row's, into its RowInfo::gs (a power of two near 2^15 / max|w| is taken in the pass over the logits) or
 // into w, which is zero before.
 struct Weights {
   unsigned* wmax;

@@ -13,15 +13,16 @@ cudaError_t launch(K kern, int smem, const GemmLaunch& l, int threads = kThreads
                         l.a, l.b, l.out, l.p);
 }
 
-// A^T B is dW of few tokens, all epilogue: the kernel with more epilogue warps (28672 x 1024 from 256 tokens
-// 20 us with four).
+// A^T B is dW.  Up to two k-blocks, 128 tokens, a tile is all epilogue: the kernel with more epilogue warps.  From
+// four on the one with more stages (28672 x 1024 from 256 tokens 20 against 23 us).
 template <int BN>
 cudaError_t launch_tc(const GemmLaunch& l) {
   constexpr int smem = TileCfg<BN>::kSmemBytes;
   using Wide = TileCfg<BN, BN / 64>;
-  if (l.p.a_mn) return launch(tg_gemm_tc_scaled_kernel<BN>, Wide::kSmemBytes, l, Wide::kThreadsEG);
-  return l.p.b_k ? launch(tg_gemm_tc_kernel<BN, false, true, kModeScaled>, smem, l)
-                 : launch(tg_gemm_tc_kernel<BN, false, false, kModeScaled>, smem, l);
+  if (l.p.a_mn && l.p.num_kb <= 2)
+    return launch(tg_gemm_tc_scaled_kernel<BN>, Wide::kSmemBytes, l, Wide::kThreadsEG);
+  return l.p.a_mn || l.p.b_k ? launch(tg_gemm_tc_kernel<BN, false, true, kModeScaled>, smem, l)
+                             : launch(tg_gemm_tc_kernel<BN, false, false, kModeScaled>, smem, l);
 }
 }  // namespace
 
