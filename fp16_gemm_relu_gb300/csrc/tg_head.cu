@@ -36,6 +36,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kGScale = 32768.0f;
+// exp2f's results are 5.1e-8 of themselves too small on average (over [-24, 0], weighted by their size), and a
+// row's sum goes through it twice: what that takes from lse, for losses whose log probabilities are added up.
+constexpr float kExpLift = 1.0e-7f;
 
 // What the passes after the logits know of a row.
 struct alignas(16) RowInfo {
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kRowThreads)
                         int64_t vocab, const int64_t* __restrict__ index, int64_t ignore,
                         const void* __restrict__ teacher, int teacher_f32, int64_t ldt, int top,
                         const float* __restrict__ dloss, const unsigned* wmax,
-                        float* loss, float* lse, RowInfo* info, float* q, float* alpha) {
+                        float* loss, float* lse, RowInfo* info, float* q, float* alpha, float lift) {
   __shared__ float slots[5][4];
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x;
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kRowThreads)
   }
   const float row_m = block_max(m, slots[0]);
   if (row_m > -INFINITY) s *= exp2f(m - row_m);
-  const float lse2 = row_m + log2f(block_sum(s, slots[1])), lse_r = lse2 * kLn2;
+  const float lse2 = row_m + log2f(block_sum(s, slots[1])), lse_r = fmaf(lse2, kLn2, lift);
   RowInfo ri;
   ri.lse2 = lse2;
   ri.gs = 0.0f;
@@ -842,7 +845,8 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
         stats, static_cast<int>(2 * cdiv(h.V, block_n)), Logits{z, ldz, picked}, h.scale, h.V, index, h.ignore,
         teacher, h.teacher_f32, h.ldt, h.top, dloss, objective ? nullptr : wmax, loss,
         h.lse ? h.lse + t0 : nullptr, info, q,
-        objective ? reinterpret_cast<float*>(wmax) : alpha);  // objective: zeroes the maximum
+        objective ? reinterpret_cast<float*>(wmax) : alpha,  // objective: zeroes the maximum
+        h.precise ? kExpLift : 0.0f);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
     if (objective) {
       e = launch_objective(h, nll, Weights{wmax, info, nullptr}, true, stream);
