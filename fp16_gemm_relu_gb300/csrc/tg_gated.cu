@@ -29,6 +29,8 @@ constexpr int64_t kMaxLd = int64_t{1} << 36;
 // A TMA box of many rows of a matrix of fewer than eight (the rows of a swizzle atom) takes longer at some
 // addresses, so operands of the gradients' products lie in scratch of that many rows, the others zero.
 constexpr int64_t kLeastRows = 8;
+// Elements of each weight from which dX runs beside dW.
+constexpr int64_t kBesideWork = int64_t{4} << 20;
 // Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
 // 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
 // Longer sums are taken in splits that are added in float32.
@@ -272,12 +274,19 @@ tg::TilePlan few_rows_plan(const Gated& a, int sms) {
 
 int timeout_of(const tg_options* opt) { return opt && opt->timeout_ms > 0 ? opt->timeout_ms : 2000; }
 
+// What a launch of the gradients' products has in common.
+void common_params(tg::GemmParams* p, const tg_options* opt, unsigned* err) {
+  p->debug_flags = opt ? opt->debug_flags : 0;
+  p->timeout_ns = 1000000ull * static_cast<unsigned long long>(timeout_of(opt));
+  p->err = err;
+}
+
 // dWg and dWu in one launch: X^T [dG | dU] (trans 0; the second output's tiles follow the first's along N)
 // or [dG | dU]^T X (trans 1; along M), g holding dU np columns after dG.  TG_ERR_NO_WORKSPACE: the planner
 // splits the sum, or an option asks for what this launch has not; nothing is launched.
 tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int64_t np, void* dWg,
                        int64_t lddwg, void* dWu, int64_t lddwu, const tg_options* opt, unsigned* err,
-                       cudaStream_t stream) {
+                       cudaStream_t stream, tg::GemmLaunch* out, int* block_n) {
   const int64_t rows = a.trans ? a.N : a.K, cols = a.trans ? a.K : a.N;  // of each output
   tg::TilePlan plan;
   tg_options o;
@@ -296,7 +305,7 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
   const int bm = plan.pair ? 256 : 128, bn = plan.block_n;
   const int64_t tm = cdiv(rows, bm), tn = cdiv(cols, bn);
   if (2 * tm * tn >= (int64_t{1} << 31)) return TG_ERR_NO_WORKSPACE;
-  tg::GemmLaunch l;
+  tg::GemmLaunch& l = *out;
   std::memset(&l, 0, sizeof(l));
   tg::GemmParams& p = l.p;
   p.tiles_m = static_cast<int>(a.trans ? 2 * tm : tm);
@@ -306,9 +315,7 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
   p.units = p.tiles_m * p.tiles_n;
   p.panel_m = std::min(opt && opt->panel_m ? opt->panel_m : 8, p.tiles_m);
   p.a_mn = 1;
-  p.debug_flags = opt ? opt->debug_flags : 0;
-  p.timeout_ns = 1000000ull * static_cast<unsigned long long>(timeout_of(opt));
-  p.err = err;
+  common_params(&p, opt, err);
   p.c = static_cast<__half*>(dWg), p.ldc = lddwg;
   p.M = static_cast<int>(rows), p.N = static_cast<int>(cols);
   const bool tma = whole_rows(dWg, lddwg, cols) && whole_rows(dWu, lddwu, cols);
@@ -332,9 +339,48 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
   if (tma)
     ok = ok && tg::half_map(&l.out, dWg, cols, rows, lddwg, 64, 32) &&
          tg::half_map(&l.out2, dWu, cols, rows, lddwu, 64, 32);
-  if (!ok) return tg::record_cuda_error(cudaErrorInvalidValue);
-  const cudaError_t e = tg::launch_gemm_two(l, plan.pair ? 0 : bn);
-  return e == cudaSuccess ? TG_OK : tg::record_cuda_error(e);
+  *block_n = plan.pair ? 0 : bn;
+  return ok ? TG_OK : tg::record_cuda_error(cudaErrorInvalidValue);
+}
+
+// Few tokens: dX, which reads the weights, beside dWg and dWu, which are as many bytes to write, in one launch
+// where each has its share of the SMs: dX up to half of them, as many as its tiles of `width` columns in some number
+// of splits make, one unit a block.  The splits, or 0 where the calls go one after the other (few weights, or tiles
+// that fit no share).  64 tokens of 4096 x 14336 90 against 104 us one after the other (with two fifths of the SMs 103),
+// 37 of 1112 x 4448 24 and 30, 128 of 4096 x 14336 102 and 118; 64 of 8192 x 28672 322 and 314.
+int beside_splits(const Gated& a, int64_t ld, int64_t width, int sms) {
+  const int64_t tiles = cdiv(a.K, width), least = cdiv(ld, kSumLength);
+  const int64_t splits = std::min<int64_t>(sms / 2 / tiles, ld / 128);
+  if (a.M > 128 || a.K * a.N < kBesideWork || splits < std::max<int64_t>(least, 1) ||
+      tiles * splits * 4 < sms)
+    return 0;
+  const int64_t kbps = round_up(cdiv(ld / tg::kBK, splits), 2);  // (a stage never has both weights' k-blocks)
+  return static_cast<int>(cdiv(ld / tg::kBK, kbps));
+}
+
+// dX's launch for that, its partial sums in ws.
+bool beside_input(const Gated& a, const Operands& ops, const __half* g, int64_t ld, int64_t width, int splits,
+                  float* ws, int64_t ldw, const tg_options* opt, unsigned* err, tg::GemmLaunch* l) {
+  std::memset(l, 0, sizeof(*l));
+  tg::GemmParams& p = l->p;
+  p.tiles_m = 1;
+  p.tiles_n = static_cast<int>(cdiv(a.K, width));
+  p.num_kb = static_cast<int>(ld / tg::kBK);
+  p.kb_per_split = static_cast<int>(round_up(cdiv(p.num_kb, splits), 2));
+  p.splits = splits;
+  p.units = p.tiles_n * splits;
+  p.panel_m = 1;
+  p.b_k = !a.trans;
+  common_params(&p, opt, err);
+  p.M = static_cast<int>(a.M), p.N = static_cast<int>(a.K);
+  p.kb_switch = p.num_kb / 2;
+  l->grid = p.units;
+  auto right = [&](CUtensorMap* m, const void* w, int64_t ldwt) {
+    return a.trans ? tg::half_map(m, w, a.K, a.N, ldwt, 64, 64)
+                   : tg::half_map(m, w, a.N, a.K, ldwt, 64, static_cast<int>(width));
+  };
+  return tg::half_map(&l->a, g, ld, std::max(a.M, kLeastRows), ld, 64, tg::kBM) && right(&l->b, ops.wg, ops.ldwg) &&
+         right(&l->b2, ops.wu, ops.ldwu) && tg::partial_map(&l->out, ws, a.K, a.M, splits, ldw);
 }
 
 }  // namespace
@@ -481,6 +527,10 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   Operands ops;
   const int64_t rows = std::max(M, kLeastRows);
   const int64_t at_g = lay.add(rows * ld * 2);
+  const int64_t width = K <= 2048 ? 128 : 256;  // few tokens: dX's tiles
+  const bool choose = !opt || (!opt->block_n && !opt->split_k && !opt->pair && !opt->max_ctas && !opt->panel_m);
+  const int beside = dX && dWg && dWu && choose ? beside_splits(a, ld, width, sms) : 0;
+  const int64_t ldw = round_up(K, 32), at_ws = lay.add(beside * M * ldw * 4);
   ops.plan(a, dWg || dWu, dX, dWg || dWu ? kLeastRows : 0, &lay);
   uint8_t* mem = nullptr;
   if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
@@ -500,9 +550,23 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   ex.max_k = kSumLength;
   bool one_by_one = !dWg || !dWu;
   if (!one_by_one) {
-    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, stream);
+    tg::GemmLaunch w;
+    int block_n = 0;
+    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, stream, &w, &block_n);
     if (st != TG_OK && st != TG_ERR_NO_WORKSPACE) return done(st);
     one_by_one = st == TG_ERR_NO_WORKSPACE;
+    if (beside && !one_by_one && block_n == 256) {
+      tg::GemmLaunch x;
+      float* ws = reinterpret_cast<float*>(mem + at_ws);
+      if (!beside_input(a, ops, g, ld, width, beside, ws, ldw, opt, err, &x))
+        return done(tg::record_cuda_error(cudaErrorInvalidValue));
+      w.grid = std::min(w.p.units, sms - x.grid);
+      if ((e = tg::launch_gemm_beside(x, static_cast<int>(width), w)) == cudaSuccess)
+        e = tg::launch_splitk_reduce(ws, ldw, M * ldw, beside, dX, lddx, x.p, sms, stream);
+      return done(e == cudaSuccess ? TG_OK : tg::record_cuda_error(e));
+    }
+    if (!one_by_one && (e = tg::launch_gemm_two(w, block_n)) != cudaSuccess)
+      return done(tg::record_cuda_error(e));
   }
   for (int i = 0; i < 2 && one_by_one; ++i) {
     void* d = i ? dWu : dWg;
@@ -524,7 +588,6 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
     tg_options o;
     std::memset(&o, 0, sizeof(o));
     if (opt) o = *opt;
-    const int64_t width = K <= 2048 ? 128 : 256;
     const int64_t splits = std::max(std::min({sms / cdiv(K, width), ld / 128, int64_t(32)}), cdiv(ld, kSumLength));
     if (M <= 128 && splits > 1 && !o.pair && !o.block_n && !o.split_k) {
       o.pair = -1;

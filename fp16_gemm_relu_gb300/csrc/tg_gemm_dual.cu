@@ -50,4 +50,20 @@ cudaError_t launch_gemm_two(const GemmLaunch& l, int block_n) {
                 l.out, l.out2, l.p, l.two);
 }
 
+namespace {
+template <int BN>
+cudaError_t launch_beside(const GemmLaunch& x, const GemmLaunch& w) {
+  using W = TileCfg<256, 4>;
+  constexpr int smem = W::kSmemBytes > TileCfg<BN>::kSmemBytes ? W::kSmemBytes : TileCfg<BN>::kSmemBytes;
+  const BesideMaps m{x.a, x.b, x.b2, x.out, w.a, w.b, w.out, w.out2};
+  GemmLaunch l = w;
+  l.grid = x.grid + w.grid;
+  return launch(tg_gemm_beside_kernel<BN>, W::kThreadsEG, smem, l, m, x.p, w.p, w.two, x.grid);
+}
+}  // namespace
+
+cudaError_t launch_gemm_beside(const GemmLaunch& x, int block_n, const GemmLaunch& w) {
+  return block_n == 256 ? launch_beside<256>(x, w) : launch_beside<128>(x, w);
+}
+
 }  // namespace tg

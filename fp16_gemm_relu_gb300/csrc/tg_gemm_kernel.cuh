@@ -962,11 +962,12 @@ __device__ __forceinline__ void epilogue_share(const CUtensorMap* tmOut, const G
 // which keeps their per-k-block instruction count inside the MMA time.  GENERAL == true reads
 // the layouts from p.a_mn and p.b_k (the transposed-operand GEMMs of the backward pass).
 // kModeDual: tmB2 is the second right operand, of the layout of tmB.
-template <int BN, bool OUT_F32, bool GENERAL, int MODE, int EG = 1>
+// The grid's CTA `cta` of `ctas`; SPARE: the block has warps beyond these roles.
+template <int BN, bool OUT_F32, bool GENERAL, int MODE, int EG = 1, bool SPARE = false>
 __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                              const CUtensorMap& tmOut, const GemmParams& p,
-                                             const CUtensorMap* tmB2, const TwoOut* two = nullptr,
-                                             const CUtensorMap* tmOut2 = nullptr) {
+                                             const CUtensorMap* tmB2, const TwoOut* two,
+                                             const CUtensorMap* tmOut2, int cta, int ctas) {
   static_assert(EG == 1 || (!OUT_F32 && BN % (64 * EG) == 0), "shares of whole 64-column chunks");
   using Cfg = TileCfg<BN, EG>;
   constexpr int S = Cfg::kStages;
@@ -1029,7 +1030,7 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
       uint32_t phase = 0;
       uint32_t armed = 0, armed_parity = 0;
       bool dropped = false;
-      for (int u = blockIdx.x; u < p.units; u += gridDim.x) {
+      for (int u = cta; u < p.units; u += ctas) {
         const Unit w = unit_of(p, u);
         int arow = w.m_blk * kBM, bcol = w.n_blk * BN;
         if constexpr (MODE == kModeTwo) {
@@ -1039,7 +1040,7 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
         for (int kb = w.kb_begin; kb < w.kb_end; ++kb) {
           if (!wait_phase(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p, kRoleProducer))
             goto producer_done;
-          if ((p.debug_flags & kDebugDropFirstStage) && blockIdx.x == 0 && !dropped) {
+          if ((p.debug_flags & kDebugDropFirstStage) && cta == 0 && !dropped) {
             dropped = true;  // injected fault: this stage is never filled
           } else {
             const uint32_t fb = smem_u32(&full[stage]);
@@ -1090,7 +1091,7 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
       int stage = 0;
       uint32_t phase = 0;
       int t = 0;
-      for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++t) {
+      for (int u = cta; u < p.units; u += ctas, ++t) {
         const Unit w = unit_of(p, u);
         const int buf = t & 1;
         const uint32_t use = static_cast<uint32_t>(t >> 1) & 1u;
@@ -1123,14 +1124,14 @@ __device__ __forceinline__ void tc_gemm_body(const CUtensorMap& tmA, const CUten
       umma_commit(smem_u32(drain));
       wait_phase_drain(smem_u32(drain), 0u, p);
     }
-  } else {
+  } else if (SPARE ? warp < 2 + kEpiWarps * EG : true) {
     // ------------------------------ epilogue ------------------------------
     const int q = warp & 3;       // TMEM lane quarter this warp may access
     const int ew = warp - 2;      // staging slot
     uint8_t* stg = sStg + ew * (EG == 1 ? 2 : 1) * kStagingBuf;
     int sb = 0;
     int t = 0;
-    for (int u = blockIdx.x; u < p.units; u += gridDim.x, ++t) {
+    for (int u = cta; u < p.units; u += ctas, ++t) {
       const Unit w = unit_of(p, u);
       const int buf = t & 1;
       const uint32_t use = static_cast<uint32_t>(t >> 1) & 1u;
@@ -1180,7 +1181,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tg_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmOut, const GemmParams p) {
-  tc_gemm_body<BN, OUT_F32, GENERAL, MODE>(tmA, tmB, tmOut, p, nullptr);
+  tc_gemm_body<BN, OUT_F32, GENERAL, MODE>(tmA, tmB, tmOut, p, nullptr, nullptr, nullptr, blockIdx.x,
+                                           gridDim.x);
 }
 template <int BN, bool OUT_F32>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -1189,7 +1191,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap tmB2,
                            const __grid_constant__ CUtensorMap tmOut,
                            const __grid_constant__ GemmParams p) {
-  tc_gemm_body<BN, OUT_F32, true, kModeDual>(tmA, tmB, tmOut, p, &tmB2);
+  tc_gemm_body<BN, OUT_F32, true, kModeDual>(tmA, tmB, tmOut, p, &tmB2, nullptr, nullptr, blockIdx.x,
+                                             gridDim.x);
 }
 
 // The scaled sum (GENERAL layouts), a group of epilogue warps to every 64 columns.
@@ -1199,7 +1202,8 @@ __global__ void __launch_bounds__(TileCfg<BN, BN / 64>::kThreadsEG, 1)
                              const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmOut,
                              const __grid_constant__ GemmParams p) {
-  tc_gemm_body<BN, false, true, kModeScaled, BN / 64>(tmA, tmB, tmOut, p, nullptr);
+  tc_gemm_body<BN, false, true, kModeScaled, BN / 64>(tmA, tmB, tmOut, p, nullptr, nullptr, nullptr,
+                                                      blockIdx.x, gridDim.x);
 }
 // Two outputs, likewise.
 template <int BN>
@@ -1209,7 +1213,29 @@ __global__ void __launch_bounds__(TileCfg<BN, BN / 64>::kThreadsEG, 1)
                           const __grid_constant__ CUtensorMap tmOut,
                           const __grid_constant__ CUtensorMap tmOut2,
                           const __grid_constant__ GemmParams p, const __grid_constant__ TwoOut two) {
-  tc_gemm_body<BN, false, true, kModeTwo, BN / 64>(tmA, tmB, tmOut, p, nullptr, &two, &tmOut2);
+  tc_gemm_body<BN, false, true, kModeTwo, BN / 64>(tmA, tmB, tmOut, p, nullptr, &two, &tmOut2, blockIdx.x,
+                                                   gridDim.x);
+}
+
+// The gradients of few tokens, side by side in one launch: the first ctas_x CTAs sum dX from the weights (two right
+// operands, float32 partial sums of its splits), the others write both weights' gradients (two outputs).  The
+// one reads as much as the other writes.
+struct BesideMaps {
+  CUtensorMap a, b, b2, out;      // dX
+  CUtensorMap wa, wb, wout, wout2;  // dW
+};
+template <int BN>
+__global__ void __launch_bounds__(TileCfg<256, 4>::kThreadsEG, 1)
+    tg_gemm_beside_kernel(const __grid_constant__ BesideMaps m, const __grid_constant__ GemmParams px,
+                          const __grid_constant__ GemmParams pw, const __grid_constant__ TwoOut two,
+                          const int ctas_x) {
+  const int cta = static_cast<int>(blockIdx.x);
+  if (cta < ctas_x)
+    tc_gemm_body<BN, true, true, kModeDual, 1, true>(m.a, m.b, m.out, px, &m.b2, nullptr, nullptr, cta,
+                                                     ctas_x);
+  else
+    tc_gemm_body<256, false, true, kModeTwo, 4>(m.wa, m.wb, m.wout, pw, nullptr, &two, &m.wout2,
+                                                cta - ctas_x, static_cast<int>(gridDim.x) - ctas_x);
 }
 
 // Epilogue of one K half of a tail-split tile (fp16 output), for one warp of the pair kernel:

@@ -82,6 +82,9 @@ cudaError_t launch_gemm_scaled(const GemmLaunch& l, int block_n);
 cudaError_t launch_gemm_dual(const GemmLaunch& l, bool out_f32, int block_n);
 // The kernels with two outputs (kModeTwo): A stored K x M, B stored K x N.
 cudaError_t launch_gemm_two(const GemmLaunch& l, int block_n);
+// Both beside each other (tg_gemm_beside_kernel): x, float32 output in tiles of 128 x block_n on x.grid CTAs, and w,
+// tiles of 128 x 256 on w.grid more.
+cudaError_t launch_gemm_beside(const GemmLaunch& x, int block_n, const GemmLaunch& w);
 // Clusters of two that can be resident at once on the current device.
 cudaError_t gemm_pair_max_clusters(int* out);
 
