@@ -480,33 +480,14 @@ __global__ void tg_pack_rows_kernel(const uint16_t* __restrict__ src, int64_t ld
   pack_rows(src, ld_src, dst, ld_dst, rows, cols);
 }
 
-// Up to three matrices in one launch, one to each of the grid's y.
-struct PackJobs {
-  tg::PackJob j[3];
-};
-__global__ void tg_pack_jobs_kernel(const __grid_constant__ PackJobs jobs) {
-  tg::chain_wait();
-  tg::chain_release();
-  const tg::PackJob& j = jobs.j[blockIdx.y];
-  pack_rows(static_cast<const uint16_t*>(j.src), j.ld_src, static_cast<uint16_t*>(j.dst), j.ld_dst,
-            j.rows, j.cols);
-  const int64_t cpr = (j.cols + 7) >> 3;
-  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < j.zeros * cpr;
-       i += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t r = i / cpr;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.dst) + (j.rows + r) * j.ld_dst + ((i - r * cpr) << 3)) =
-        make_uint4(0, 0, 0, 0);
-  }
-}
-
 // The same copy with each lane taking kPackItems chunks (of warp items nwarps apart) per pass,
 // all of their loads issued before its first store: for large copies, where every warp has
 // at least that many items (launch_pack).
 constexpr int kPackItems = 4;
 
-__global__ void tg_pack_rows4_kernel(const uint16_t* __restrict__ src, int64_t ld_src,
-                                     uint16_t* __restrict__ dst, int64_t ld_dst, int64_t rows,
-                                     int64_t cols) {
+__device__ __forceinline__ void pack_rows4(const uint16_t* __restrict__ src, int64_t ld_src,
+                                           uint16_t* __restrict__ dst, int64_t ld_dst, int64_t rows,
+                                           int64_t cols) {
   const int64_t cpr = (cols + 7) >> 3;
   const int64_t gpr = (cpr + 31) >> 5;  // 32-chunk groups per row
   const int64_t items = rows * gpr;
@@ -558,6 +539,36 @@ __global__ void tg_pack_rows4_kernel(const uint16_t* __restrict__ src, int64_t l
       }
       *reinterpret_cast<uint4*>(dst + out[i]) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+  }
+}
+
+__global__ void tg_pack_rows4_kernel(const uint16_t* __restrict__ src, int64_t ld_src,
+                                     uint16_t* __restrict__ dst, int64_t ld_dst, int64_t rows,
+                                     int64_t cols) {
+  pack_rows4(src, ld_src, dst, ld_dst, rows, cols);
+}
+
+// Up to three matrices in one launch, one to each of the grid's y.
+struct PackJobs {
+  tg::PackJob j[3];
+};
+template <bool FOUR>
+__global__ void tg_pack_jobs_kernel(const __grid_constant__ PackJobs jobs) {
+  tg::chain_wait();
+  tg::chain_release();
+  const tg::PackJob& j = jobs.j[blockIdx.y];
+  const uint16_t* src = static_cast<const uint16_t*>(j.src);
+  uint16_t* dst = static_cast<uint16_t*>(j.dst);
+  if (FOUR)
+    pack_rows4(src, j.ld_src, dst, j.ld_dst, j.rows, j.cols);
+  else
+    pack_rows(src, j.ld_src, dst, j.ld_dst, j.rows, j.cols);
+  const int64_t cpr = (j.cols + 7) >> 3;
+  for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < j.zeros * cpr;
+       i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t r = i / cpr;
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.dst) + (j.rows + r) * j.ld_dst + ((i - r * cpr) << 3)) =
+        make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -1345,9 +1356,10 @@ cudaError_t launch_pack_jobs(const PackJob* jobs, int n, int num_sms, bool chain
     all.j[i] = jobs[i];
     chunks = std::max(chunks, (jobs[i].rows + jobs[i].zeros) * cdiv(jobs[i].cols, 8));
   }
-  return launch_chained(tg_pack_jobs_kernel, chained,
-                        dim3(static_cast<unsigned>(aux_grid(chunks, num_sms)), static_cast<unsigned>(n)),
-                        256, 0, stream, all);
+  const int grid = aux_grid(chunks, num_sms);
+  const bool four = chunks >= kPackItems * int64_t(grid) * 256;  // see launch_pack
+  return launch_chained(four ? tg_pack_jobs_kernel<true> : tg_pack_jobs_kernel<false>, chained,
+                        dim3(static_cast<unsigned>(grid), static_cast<unsigned>(n)), 256, 0, stream, all);
 }
 
 bool half_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
