@@ -31,6 +31,7 @@ constexpr int64_t kMaxLd = int64_t{1} << 36;
 constexpr int64_t kLeastRows = 8;
 // Elements of each weight from which dX runs beside dW.
 constexpr int64_t kBesideWork = int64_t{4} << 20;
+constexpr int64_t kBesideTokens = 256;
 // Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
 // 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
 // Longer sums are taken in splits that are added in float32.
@@ -286,7 +287,7 @@ void common_params(tg::GemmParams* p, const tg_options* opt, unsigned* err) {
 // splits the sum, or an option asks for what this launch has not; nothing is launched.
 tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int64_t np, void* dWg,
                        int64_t lddwg, void* dWu, int64_t lddwu, const tg_options* opt, unsigned* err,
-                       cudaStream_t stream, tg::GemmLaunch* out, int* block_n) {
+                       bool beside, cudaStream_t stream, tg::GemmLaunch* out, int* block_n) {
   const int64_t rows = a.trans ? a.N : a.K, cols = a.trans ? a.K : a.N;  // of each output
   tg::TilePlan plan;
   tg_options o;
@@ -294,9 +295,9 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
   if (opt) o = *opt;
   // Few tokens: a tile is all epilogue, which one CTA with 16 epilogue warps does faster than a pair with eight
   // each (4096 x 14336 from 64 tokens 49 against 65 us, 54 in tiles of 128 columns; from 256 tokens 86 against 79).
-  if (a.M <= 128 && !o.pair) {
+  if ((a.M <= 128 || beside) && !o.pair) {
     o.pair = -1;
-    if (!o.block_n && cdiv(rows, 128) * cdiv(cols, 256) >= 76) o.block_n = 256;
+    if (!o.block_n && (beside || cdiv(rows, 128) * cdiv(cols, 256) >= 76)) o.block_n = 256;
   }
   tg_status st = tg::plan_tiles(a.trans ? 2 * rows : rows, a.trans ? cols : 2 * cols, a.M, kSumLength, true,
                                 &o, &plan);
@@ -346,13 +347,14 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
 // Few tokens: dX, which reads the weights, beside dWg and dWu, which are as many bytes to write, in one launch
 // where each has its share of the SMs: dX up to half of them, as many as its tiles of `width` columns in some number
 // of splits make, one unit a block.  The splits, or 0 where the calls go one after the other (few weights, or tiles
-// that fit no share).  64 tokens of 4096 x 14336 90 against 104 us one after the other (with two fifths of the SMs 103),
-// 37 of 1112 x 4448 24 and 30, 128 of 4096 x 14336 102 and 118; 64 of 8192 x 28672 322 and 314.
+// that make less than three eighths).  64 tokens of 4096 x 14336 90 against 104 us one after the other (with two fifths
+// of the SMs 103), 37 of 1112 x 4448 24 and 30, 128 of 4096 x 14336 102 and 118, 256 of it 150 and 167; 64 of 8192 x 28672
+// 322 and 314, 512 of 4096 x 14336 231 and 201.
 int beside_splits(const Gated& a, int64_t ld, int64_t width, int sms) {
-  const int64_t tiles = cdiv(a.K, width), least = cdiv(ld, kSumLength);
+  const int64_t tiles = cdiv(a.K, width) * cdiv(a.M, tg::kBM), least = cdiv(ld, kSumLength);
   const int64_t splits = std::min<int64_t>(sms / 2 / tiles, ld / 128);
-  if (a.M > 128 || a.K * a.N < kBesideWork || splits < std::max<int64_t>(least, 1) ||
-      tiles * splits * 4 < sms)
+  if (a.M > kBesideTokens || a.K * a.N < kBesideWork || splits < std::max<int64_t>(least, 1) ||
+      tiles * splits * 8 < 3 * sms)
     return 0;
   const int64_t kbps = round_up(cdiv(ld / tg::kBK, splits), 2);  // (a stage never has both weights' k-blocks)
   return static_cast<int>(cdiv(ld / tg::kBK, kbps));
@@ -363,13 +365,13 @@ bool beside_input(const Gated& a, const Operands& ops, const __half* g, int64_t 
                   float* ws, int64_t ldw, const tg_options* opt, unsigned* err, tg::GemmLaunch* l) {
   std::memset(l, 0, sizeof(*l));
   tg::GemmParams& p = l->p;
-  p.tiles_m = 1;
+  p.tiles_m = static_cast<int>(cdiv(a.M, tg::kBM));
   p.tiles_n = static_cast<int>(cdiv(a.K, width));
   p.num_kb = static_cast<int>(ld / tg::kBK);
   p.kb_per_split = static_cast<int>(round_up(cdiv(p.num_kb, splits), 2));
   p.splits = splits;
-  p.units = p.tiles_n * splits;
-  p.panel_m = 1;
+  p.units = p.tiles_m * p.tiles_n * splits;
+  p.panel_m = p.tiles_m;
   p.b_k = !a.trans;
   common_params(&p, opt, err);
   p.M = static_cast<int>(a.M), p.N = static_cast<int>(a.K);
@@ -552,7 +554,7 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   if (!one_by_one) {
     tg::GemmLaunch w;
     int block_n = 0;
-    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, stream, &w, &block_n);
+    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, beside > 0, stream, &w, &block_n);
     if (st != TG_OK && st != TG_ERR_NO_WORKSPACE) return done(st);
     one_by_one = st == TG_ERR_NO_WORKSPACE;
     if (beside && !one_by_one && block_n == 256) {

@@ -15,7 +15,8 @@ from tests.test_gpu_gated import (  # noqa: E402,F401
 
 SIZES = [(1, 2048, 2304, 0, 0), (7, 4100, 1032, 0, 0), (8, 1031, 4500, 0, 0), (64, 8192, 1024, 0, 0),
          (65, 2500, 2100, 4, 0), (100, 1111, 4444, 3, 1), (128, 20000, 520, 0, 0), (128, 4096, 4096, 8, 8),
-         (2, 777, 9000, 1, 3), (33, 30000, 256, 0, 0)]
+         (2, 777, 9000, 1, 3), (33, 30000, 256, 0, 0), (129, 4096, 1024, 0, 0),
+         (256, 5000, 2047, 3, 0), (200, 2300, 2304, 0, 0), (257, 4100, 1100, 0, 0)]
 
 
 @pytest.mark.parametrize("trans", [False, True])
