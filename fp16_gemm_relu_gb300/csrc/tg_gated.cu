@@ -3,6 +3,13 @@
 //   gate = X Wg,  up = X Wu  (M x N, float32),   H = act(gate) * up
 //   dG = dH * up * act'(gate),  dU = dH * act(gate)
 //   dX = dG Wg^T + dU Wu^T,  dWg = X^T dG,  dWu = X^T dU
+//
+// Forward is one kernel (tg_gated_kernel.cuh), with K splits and a reduction where few tokens leave SMs idle.
+// Backward is a pass over the M x N matrices that leaves [dG | dU] in scratch, and the products: both weights'
+// gradients as one launch with two outputs, dX as one sum over both gradients with two right operands, and up
+// to 256 tokens all three as one launch (tg_gemm_kernel.cuh: kModeTwo, kModeDual, tg_gemm_beside_kernel).  At 8192 x
+// 4096 x 14336 the pass takes 183 us, the products 2100 (1.83 PFLOP/s); with dX as two products through float32
+// and the weights' one by one the step took 2749, so 2290.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -24,7 +31,8 @@ bool misaligned(const void* p, unsigned bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
 
-constexpr int64_t kMaxSize = (int64_t{1} << 30);
+constexpr int64_t kMaxSize = int64_t{1} << 29;  // twice N is a TMA coordinate
+constexpr int64_t kMaxElements = int64_t{1} << 44;
 constexpr int64_t kMaxLd = int64_t{1} << 36;
 // A TMA box of many rows of a matrix of fewer than eight (the rows of a swizzle atom) takes longer at some
 // addresses, so operands of the gradients' products lie in scratch of that many rows, the others zero.
@@ -172,6 +180,9 @@ bool bad_ld(int64_t ld, int64_t n) { return ld < n || ld > kMaxLd; }
 
 tg_status check(const Gated& a) {
   if (a.M < 0 || a.N < 1 || a.K < 1 || a.M > kMaxSize || a.N > kMaxSize || a.K > kMaxSize)
+    return TG_ERR_INVALID_ARG;
+  // sizes whose products leave 64 bits could only come with pointers to nothing
+  if (a.M > kMaxElements / a.N || a.M > kMaxElements / a.K || a.N > kMaxElements / a.K)
     return TG_ERR_INVALID_ARG;
   if (a.act < TG_ACT_NONE || a.act > TG_ACT_SILU || (a.trans != 0 && a.trans != 1))
     return TG_ERR_INVALID_ARG;

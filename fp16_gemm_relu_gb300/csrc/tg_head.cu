@@ -437,7 +437,8 @@ constexpr int kPairThreads = 256;
 //   r_s = sum over a sequence's counted rows of logp - reference (average: their mean; none: 0)
 //   m = beta (r_chosen - r_rejected),   loss = -(1 - e) log sigma(m) - e log sigma(-m)
 // The sums are float64: those of a long answer are large and nearly the same in both.  Bound by latency:
-// one pass over the rows of both sequences and one meeting of the block.
+// one pass over the rows of both sequences and one meeting of the block (16 pairs of 256 rows 6.5 us; with a meeting
+// a sum 10).
 __global__ void __launch_bounds__(kPairThreads)
     tg_head_pairs_kernel(Objective ob, const float* nll, const int64_t* __restrict__ index,
                          int64_t ignore, int64_t rows, Weights wt) {

@@ -460,8 +460,9 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
  * rounded to fp16, the type of the products' operands: what leaves fp16's range there is infinite in the
  * gradients, and what is below its smallest normal number keeps fewer bits, as for any fp16 gradient
  * under a loss scale.  The derivative of relu at 0 is 0.
- * Scratch: dG and dU, and copies of operands that are not 16-byte aligned with leading dimensions that
- * are multiples of 8.
+ * Scratch: dG and dU, copies of operands that are not 16-byte aligned with leading dimensions that are multiples
+ * of 8 (and of an X of fewer than eight rows), and float32 sums where a sum is taken in splits (dX of few tokens; sums
+ * of more than 32768 terms).
  */
 tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, const void* Wu,
                                 const void* gate, const void* up, void* dX, void* dWg, void* dWu,

@@ -55,7 +55,8 @@ def clip(*grads, loss_scale=1.0, max_norm=1.0, norm=P):
     return b.tg_clip_gradients([b.tg_gradient(*g) for g in grads], loss_scale, max_norm, norm)
 
 
-BIG = (1 << 30) + 1
+BIG = (1 << 29) + 1
+HALF = 1 << 28
 
 
 @pytest.mark.parametrize("bad", [
@@ -63,7 +64,8 @@ BIG = (1 << 30) + 1
                                                         ldup=BIG),
     dict(ldx=23), dict(ldwg=15), dict(ldwu=15), dict(trans_w=1, ldwg=23), dict(trans_w=2), dict(ldh=15),
     dict(ldgate=15), dict(ldup=15), dict(activation=5), dict(activation=-1), dict(X=0), dict(Wg=0),
-    dict(Wu=0), dict(H=0), dict(ldx=1 << 37)])
+    dict(Wu=0), dict(H=0), dict(ldx=1 << 37),
+    dict(M=HALF, N=HALF, ldwg=HALF, ldwu=HALF, ldh=HALF, ldgate=HALF, ldup=HALF)])
 def test_gated_refuses(bad):
     assert gated(**bad) == b.TG_ERR_INVALID_ARG
 
