@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -1280,6 +1281,28 @@ cudaError_t bind_thread_context(int dev) {
 }
 
 tg_status record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
+cudaError_t allow_smem(const void* kern, int bytes) {
+  constexpr int kSlots = 256;  // more than the library's kernels; a full table only sets again
+  static std::atomic<const void*> done[kMaxDevices][kSlots];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<const void*>* slots = done[dev & (kMaxDevices - 1)];
+  const unsigned first = static_cast<unsigned>(reinterpret_cast<uintptr_t>(kern) >> 4) % kSlots;
+  for (unsigned i = 0; i < kSlots; ++i) {
+    const void* seen = slots[(first + i) % kSlots].load(std::memory_order_acquire);
+    if (seen == kern) return cudaSuccess;
+    if (seen == nullptr) break;
+  }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (unsigned i = 0; e == cudaSuccess && i < kSlots; ++i) {
+    const void* none = nullptr;
+    if (slots[(first + i) % kSlots].compare_exchange_strong(none, kern, std::memory_order_acq_rel) || none == kern)
+      break;
+  }
+  return e;
+}
 
 tg_status device_info(int* sm_count, unsigned int** err) {
   DeviceState* ds = nullptr;

@@ -37,7 +37,7 @@ constexpr int64_t kMaxLd = int64_t{1} << 36;
 // A TMA box of many rows of a matrix of fewer than eight (the rows of a swizzle atom) takes longer at some
 // addresses, so operands of the gradients' products lie in scratch of that many rows, the others zero.
 constexpr int64_t kLeastRows = 8;
-// Elements of each weight from which dX runs beside dW.
+// Elements of each weight from which it counts how dX and dW share the SMs.
 constexpr int64_t kBesideWork = int64_t{4} << 20;
 constexpr int64_t kBesideTokens = 256;
 // Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
@@ -357,15 +357,16 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
 
 // Few tokens: dX, which reads the weights, beside dWg and dWu, which are as many bytes to write, in one launch
 // where each has its share of the SMs: dX up to half of them, as many as its tiles of `width` columns in some number
-// of splits make, one unit a block.  The splits, or 0 where the calls go one after the other (few weights, or tiles
-// that make less than three eighths).  64 tokens of 4096 x 14336 90 against 104 us one after the other (with two fifths
+// of splits make, one unit a block.  The splits, or 0 where the calls go one after the other (tiles of large
+// weights that make less than three eighths).  64 tokens of 4096 x 14336 90 against 104 us one after the other (with two fifths
 // of the SMs 103), 37 of 1112 x 4448 24 and 30, 128 of 4096 x 14336 102 and 118, 256 of it 150 and 167; 64 of 8192 x 28672
-// 322 and 314, 512 of 4096 x 14336 231 and 201.
+// 322 and 314, 512 of 4096 x 14336 231 and 201.  Small weights gain by the launch that is saved, 16 of 256 x 512 17 and 21,
+// with no more splits than the sum's length pays for.
 int beside_splits(const Gated& a, int64_t ld, int64_t width, int sms) {
   const int64_t tiles = cdiv(a.K, width) * cdiv(a.M, tg::kBM), least = cdiv(ld, kSumLength);
-  const int64_t splits = std::min<int64_t>(sms / 2 / tiles, ld / 128);
-  if (a.M > kBesideTokens || a.K * a.N < kBesideWork || splits < std::max<int64_t>(least, 1) ||
-      tiles * splits * 8 < 3 * sms)
+  const bool small = a.K * a.N < kBesideWork;
+  const int64_t splits = std::min({sms / 2 / tiles, ld / 128, small ? std::max<int64_t>(8, ld / 1024) : ld});
+  if (a.M > kBesideTokens || splits < std::max<int64_t>(least, 1) || (!small && tiles * splits * 8 < 3 * sms))
     return 0;
   const int64_t kbps = round_up(cdiv(ld / tg::kBK, splits), 2);  // (a stage never has both weights' k-blocks)
   return static_cast<int>(cdiv(ld / tg::kBK, kbps));

@@ -9,8 +9,7 @@ template <bool OUT_F32, bool GENERAL>
 cudaError_t launch_one(const GemmLaunch& l) {
   auto kern = tg_gemm_tc_kernel<128, OUT_F32, GENERAL>;
   constexpr int smem = TileCfg<128>::kSmemBytes;
-  // per device and per function; cheap enough to repeat on every launch
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.out, l.p);
   return cudaGetLastError();

@@ -7,8 +7,7 @@ namespace tg {
 namespace {
 template <typename K, typename... Q>
 cudaError_t launch(K kern, int threads, int smem, const GemmLaunch& l, const Q&... args) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), threads, smem, l.stream,
                         args...);

@@ -8,7 +8,7 @@ template <bool OUT_F32, bool A_MN, bool B_K>
 cudaError_t launch_one(const GemmLaunch& l) {
   auto kern = tg_gemm_pair_kernel<OUT_F32, A_MN, B_K>;
   constexpr int smem = PairCfgFwd::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.out, l.p);  // grid is a multiple of 2
   return cudaGetLastError();
@@ -30,7 +30,7 @@ cudaError_t launch_gemm_pair_cls(const AClassMaps& cls, const GemmLaunch& l) {
   if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
   auto kern = tg_gemm_pair_cls_kernel<kARowClasses>;
   constexpr int smem = PairCfgFwd::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   kern<<<l.grid, kThreads, smem, l.stream>>>(cls, l.b, l.out, l.p);
   return cudaGetLastError();
@@ -39,7 +39,7 @@ cudaError_t launch_gemm_pair_cls(const AClassMaps& cls, const GemmLaunch& l) {
 cudaError_t gemm_pair_max_clusters(int* out) {
   auto kern = tg_gemm_pair_kernel<false, false, false>;
   constexpr int smem = PairCfgFwd::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);

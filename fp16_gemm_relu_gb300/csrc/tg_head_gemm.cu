@@ -8,8 +8,7 @@ namespace tg {
 namespace {
 template <typename K, typename P>
 cudaError_t launch(K kern, int threads, int smem, const GemmLaunch& l, const P& p) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), threads, smem, l.stream,
                         l.a, l.b, l.out, p);
@@ -40,8 +39,7 @@ cudaError_t launch_head_add(const GemmLaunch& l) {
   if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
   auto kern = tg_gemm_pair_kernel<true, true, false, kModeAdd>;
   constexpr int smem = PairCfgFwd::kSmemBytes;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   kern<<<l.grid, kThreads, smem, l.stream>>>(l.a, l.b, l.out, l.p);
   return cudaGetLastError();

@@ -10,8 +10,7 @@ template <bool B_K, bool STORE>
 cudaError_t launch_logits(const GemmLaunch& l, const HeadParams& hp, int block_n) {
   return launch_logits_tile<B_K, STORE, true>(
       [&](auto kern, int smem) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
         if (e != cudaSuccess) return e;
         return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), kHeadThreads, smem,
                               l.stream, l.a, l.b, l.out, hp);

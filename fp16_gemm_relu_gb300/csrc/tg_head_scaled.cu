@@ -6,8 +6,7 @@ namespace tg {
 namespace {
 template <typename K>
 cudaError_t launch(K kern, int smem, const GemmLaunch& l, int threads = kThreads) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_chained(kern, l.chained, dim3(static_cast<unsigned>(l.grid)), threads, smem, l.stream,
                         l.a, l.b, l.out, l.p);

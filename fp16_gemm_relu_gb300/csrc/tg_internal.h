@@ -43,6 +43,10 @@ cudaError_t launch_chained(void (*kern)(P...), bool chained, dim3 grid, int thre
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
+// cudaFuncSetAttribute of a kernel's shared memory, once per device and kernel: a small call is bound by the
+// host, where each driver call costs up to a microsecond.
+cudaError_t allow_smem(const void* kern, int bytes);
+
 // Shared-memory bytes and stage count of the kernel for a tile width.
 int gemm_smem_bytes(int block_n);
 int gemm_stages(int block_n);

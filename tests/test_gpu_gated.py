@@ -148,7 +148,8 @@ def test_backward(M, N, K, trans):
     check_backward(dh, x, wg, wu, gate, up, trans, "silu", *got)
     dx, none, none_too = tg.gated_linear_backward(dh, x, wg, wu, gate, up, trans_w=trans,
                                                   weight_grads=False)
-    assert none is None and none_too is None and torch.equal(dx, got[0])
+    assert none is None and none_too is None  # (alone, dX may be summed in other splits)
+    check_backward(dh, x, wg, wu, gate, up, trans, "silu", dx, None, None)
     none, dwg, dwu = tg.gated_linear_backward(dh, x, wg, wu, gate, up, trans_w=trans, input_grad=False)
     assert none is None and torch.equal(dwg, got[1]) and torch.equal(dwu, got[2])
 
