@@ -948,10 +948,20 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
     opt = &f32_opt;
   }
   Plan pl;
+  // rows: planned like an aligned C, without the tail's halves
+  bool rows = extra && extra->rows && ta && !tb && (reinterpret_cast<uintptr_t>(C) % 16 != 0 || ldc % 8 != 0);
+  tg_options rows_opt;
+  if (rows) {
+    std::memset(&rows_opt, 0, sizeof(rows_opt));
+    if (opt) rows_opt = *opt;
+    rows_opt.tail = -1;
+    opt = &rows_opt;
+  }
   st = make_plan(reinterpret_cast<uintptr_t>(A), reinterpret_cast<uintptr_t>(B),
-                 reinterpret_cast<uintptr_t>(C), M, N, K, lda, ldb, ldc, ds->sm_count,
-                 ds->pair_clusters, opt, &pl, ta, tb, extra ? extra->max_k : 0);
+                 rows ? 256 : reinterpret_cast<uintptr_t>(C), M, N, K, lda, ldb, rows ? round_up(ldc, 8) : ldc,
+                 ds->sm_count, ds->pair_clusters, opt, &pl, ta, tb, extra ? extra->max_k : 0);
   if (st != TG_OK) return st;
+  if (pl.pub.workspace_epilogue) rows = false;  // splits: the reduction stores any C
   if (dual && pl.pub.kblocks_per_split % 2 != 0) {
     // splits of an even number of k-blocks (a stage of a pair takes two): there may be fewer, never more
     tg_plan& P = pl.pub;
@@ -1085,7 +1095,7 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   float* ws = f32                    ? out32
               : P.workspace_epilogue ? reinterpret_cast<float*>(scratch + pl.off_w)
                                      : nullptr;
-  if (cr == CUDA_SUCCESS && (ws || !f32)) {
+  if (cr == CUDA_SUCCESS && !rows && (ws || !f32)) {
     if (ws)
       cr = encode_ws_3d(enc, &L.out, ws, uint64_t(N), uint64_t(ws_rows), uint64_t(P.split_k),
                         uint64_t(pl.ldw));
@@ -1135,7 +1145,8 @@ tg_status run_gemm(const void* A, const void* B, void* C, int64_t M, int64_t N, 
   gp.ldc = ldc;
   gp.M = static_cast<int>(M);
   gp.N = static_cast<int>(N);
-  gp.n_tma = static_cast<int>(N & ~int64_t{7});
+  gp.n_tma = rows ? 0 : static_cast<int>(N & ~int64_t{7});
+  L.rows = rows;
   const tg::GemmParams reduce_params = gp;  // the reduction writes C's M rows
   if (P.a_row_classes) {
     gp.M = static_cast<int>(ws_rows);  // the GEMM writes class-major workspace rows

@@ -936,7 +936,7 @@ __device__ __forceinline__ void epilogue_share(const CUtensorMap* tmOut, const G
             make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
     }
     if (col0 >= p.N) continue;
-    if (p.n_tma == p.N) {
+    if (p.n_tma != 0 && p.n_tma == p.N) {
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -1635,6 +1635,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                              const __grid_constant__ CUtensorMap tmOut,
                              const __grid_constant__ GemmParams p) {
   pair_gemm_body<OUT_F32, false, B_K, false, kModeDual>(tmA, tmB, tmOut, p, nullptr, &tmB2);
+}
+
+template <int EG>  // the scaled sum of A^T B with EG groups of epilogue warps
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * kEpiWarps * EG, 1)
+    tg_gemm_pair_scaled_kernel(const __grid_constant__ CUtensorMap tmA,
+                               const __grid_constant__ CUtensorMap tmB,
+                               const __grid_constant__ CUtensorMap tmOut,
+                               const __grid_constant__ GemmParams p) {
+  pair_gemm_body<false, true, false, false, kModeScaled, EG>(tmA, tmB, tmOut, p, nullptr);
 }
 
 template <int EG>

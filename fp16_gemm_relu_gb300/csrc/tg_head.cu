@@ -319,12 +319,13 @@ __global__ void __launch_bounds__(256)
   const int64_t v0 = (blockIdx.x * int64_t(blockDim.x) + threadIdx.x) << 3;
   tg::chain_wait();
   tg::chain_release();
-  // RAW: the rows' common factor 2^k takes the largest weight to [2^14, 2^15)
+  // RAW: the rows' common factor takes the largest weight to 2^15 (as row_factor: the large entries of rows of that
+  // weight, near -1 times it, then lie just below a power of two, where fp16 rounds them by 2^-12 of themselves)
   const float most = RAW ? __uint_as_float(*wmax) : 0.0f;
-  const int k = min(14 - (static_cast<int>(__float_as_uint(most) >> 23) - 127), 120);
-  const float up = __int_as_float((127 + (most == most ? k : 0)) << 23);
+  const float least = fmaxf(most, 0x1p-100f);  // (a NaN gives the other)
+  const float up = kGScale / least;
   if (RAW && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-    *alpha = s / up;  // (not NaN: rows that do not count stay 0)
+    *alpha = s * least / kGScale;  // (not NaN: rows that do not count stay 0)
   if (FINE && x2 != nullptr && blockIdx.x == 0) {
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
       const uint16_t* from = x + r * ldx;
@@ -411,7 +412,7 @@ struct Objective {
 enum : int { kPreference = 1, kPolicy = 2 };
 
 // Where an objective's weights go: max|w| over the rows as for cross entropy, NaN if any pair's offsets are
-// wrong; and each row's, into its RowInfo::gs (a power of two near 2^15 / max|w| is taken in the pass over the logits) or
+// wrong; and each row's, into its RowInfo::gs (the factor 2^15 / max|w| is taken in the pass over the logits) or
 // into w, which is zero before.
 struct Weights {
   unsigned* wmax;
@@ -896,6 +897,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
       ex.alpha = alpha;
       ex.chained = !both;
       ex.max_k = kSumLength;
+      ex.rows = h.precise;
       if (sum_w) {  // the first piece writes the sums, the last takes them into its epilogue
         ex.ld32 = ldw32;
         if (t0 + piece < h.T) {

@@ -18,7 +18,7 @@ template <int BN>
 cudaError_t launch_tc(const GemmLaunch& l) {
   constexpr int smem = TileCfg<BN>::kSmemBytes;
   using Wide = TileCfg<BN, BN / 64>;
-  if (l.p.a_mn && l.p.num_kb <= 2)
+  if (l.p.a_mn && (l.rows || l.p.num_kb <= 2))
     return launch(tg_gemm_tc_scaled_kernel<BN>, Wide::kSmemBytes, l, Wide::kThreadsEG);
   return l.p.a_mn || l.p.b_k ? launch(tg_gemm_tc_kernel<BN, false, true, kModeScaled>, smem, l)
                              : launch(tg_gemm_tc_kernel<BN, false, false, kModeScaled>, smem, l);
@@ -35,6 +35,7 @@ cudaError_t launch_gemm_scaled(const GemmLaunch& l, int block_n) {
   }
   if (l.grid <= 0 || (l.grid & 1)) return cudaErrorInvalidConfiguration;
   constexpr int smem = PairCfgFwd::kSmemBytes;
+  if (l.rows) return launch(tg_gemm_pair_scaled_kernel<2>, smem, l, 64 + 2 * 32 * kEpiWarps);
   if (l.p.a_mn) return launch(tg_gemm_pair_kernel<false, true, false, kModeScaled>, smem, l);
   return l.p.b_k ? launch(tg_gemm_pair_kernel<false, false, true, kModeScaled>, smem, l)
                  : launch(tg_gemm_pair_kernel<false, false, false, kModeScaled>, smem, l);

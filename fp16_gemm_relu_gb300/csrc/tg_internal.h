@@ -20,6 +20,7 @@ struct GemmLaunch {
   GemmParams p;
   int grid;
   cudaStream_t stream;
+  bool rows;     // scaled kernels: see GemmExtra (p.n_tma is 0)
   bool chained;  // kernels that can be chained: the launch before it on the stream is the library's
 };
 
@@ -123,6 +124,8 @@ struct GemmExtra {
   int64_t ld32;
   bool add;             // add to out32 (A stored K x M, B stored K x N) instead of writing it
   bool chained;         // logits or alpha: see GemmLaunch
+  bool rows;            // alpha, A stored K x M, B stored K x N: a C that TMA cannot store whole is stored row by
+                        // row from the epilogue, not through a float32 workspace
   bool fold;            // fp16 output: M even, C has M / 2 rows, row r the sum of rows r and r + M / 2
   int64_t max_k;        // 0, or the K columns that one split may have (without logits and out32)
   const void* B2;       // NULL, or a second right operand of B's layout, 16-byte aligned as B is: the

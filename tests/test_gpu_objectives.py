@@ -207,6 +207,23 @@ def test_strides(pad, offset, layout):
     head.check_grads(slope, es, *got[2:])
 
 
+@pytest.mark.parametrize("layout", [VOCAB, WIDTH])
+@pytest.mark.parametrize("T,V,D,pad,offset", [
+    (600, 3001, 1001, 0, 0), (300, 5003, 777, 3, 1), (3, 9001, 601, 0, 0), (1500, 2501, 259, 1, 3),
+    (130, 20001, 65, 0, 0)])
+def test_rows_that_start_anywhere(T, V, D, pad, offset, layout):
+    """Gradients whose rows TMA cannot store, from few tokens to tiles of a pair, whole and summed over pieces."""
+    x, w, target, offsets, reference = batch(T, V, D, 1, layout, 150, pad, offset)
+    head = Head(x, w, target, layout)
+    advantage, old = torch.randn(T, generator=gen(151), device="cuda"), head.logp.float()
+    loss, el, weight, ew = policy_reference(head, old, advantage, reference, 0.2, 0.2, 0.0)
+    for piece_rows in (0, T // 2 + 1):
+        got = tg.linear_policy_step(x, w, target, old, advantage, torch.ones(T, device="cuda"), layout=layout,
+                                    piece_rows=piece_rows)
+        assert ((got[0].to(D64) - loss).abs() <= el).all()
+        head.check_grads(weight, ew, *got[2:])
+
+
 @pytest.mark.parametrize("piece_rows", [0, 16])
 def test_empty_and_ignored(piece_rows):
     """Empty sequences, sequences of ignored rows alone, no pairs at all, no rows at all."""
