@@ -421,7 +421,17 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   const bool choose = !opt || (!opt->block_n && !opt->split_k && !opt->pair && !opt->max_ctas);
   // (a row of tiles of BN columns covers BN / 2 of each weight; the call refuses what no plan has)
   if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, true, opt, &plan)) != TG_OK) return st;
-  if (M <= 128 && choose) plan = few_rows_plan(a, sms);
+  if (M <= 128 && choose) {
+    plan = few_rows_plan(a, sms);
+  } else if (choose && !plan.pair && plan.block_n == 128 && cdiv(M, 256) * cdiv(N, 128) >= sms / 2) {
+    // a last wave that narrow tiles fill better is no gain where they read X four times as often: 256 x 4096 x 14336
+    // 65 us, on pairs 58, 160 x 4096 x 11008 63 and 55; below a wave of pairs the planner stands
+    tg_options o;
+    std::memset(&o, 0, sizeof(o));
+    if (opt) o = *opt;
+    o.pair = 1;
+    if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, true, &o, &plan)) != TG_OK) return st;
+  }
   Operands ops;
   const int64_t nw = round_up(N, 32), stride = M * 2 * nw;
   Layout lay;
