@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(kPairThreads)
     const float m = static_cast<float>(ob.beta * (r[0] - r[1]));
     const float away = expf(-fabsf(m)), soft = log1pf(away);       // log(1 + e^-|m|)
     const float sigma = (m > 0.0f ? away : 1.0f) / (1.0f + away);  // sigma(-m)
-    float loss = (1.0f - ob.smooth) * (soft + fmaxf(-m, 0.0f)) + ob.smooth * (soft + fmaxf(m, 0.0f));
+    float loss = (1.0f - ob.smooth) * (soft + fmaxf(-m, 0.0f));
+    if (ob.smooth > 0.0f) loss += ob.smooth * (soft + fmaxf(m, 0.0f));  // (not 0 times an infinite margin)
     if (!fits || m != m) loss = NAN;
     if (ob.loss) ob.loss[p] = loss;
     if (ob.ratios) {
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(256)
       slope = clipped ? 0.0f : -a;
       if (ob.kl > 0.0f) {
         const float d = ob.reference[r] - logp, e = expm1f(d);
-        loss += ob.kl * (e - d);
+        loss += ob.kl * (d < 100.0f ? e - d : e);  // (not infinity less itself; a NaN is e's)
         slope -= ob.kl * e;
       }
     }

@@ -307,6 +307,32 @@ def test_bad_targets_and_values(piece_rows):
     assert abs(float(loss[12]) + 1.2) < 1e-6 and (dx[12] == 0).all() and dw.isnan().any()
 
 
+@pytest.mark.parametrize("piece_rows", [0, 16])
+def test_infinite_references(piece_rows):
+    """A reference that held a token impossible: the margin is infinite, and the losses and gradients are
+    their limits."""
+    T, V, D = 40, 300, 64
+    x, w, target, _, reference = batch(T, V, D, 1, VOCAB, 160)
+    target[:] = 7
+    offsets = torch.tensor([0, 10, 20, 30, 40], device="cuda")
+    reference[3] = -math.inf   # the chosen of pair 0: infinitely ahead
+    reference[25] = -math.inf  # the chosen of pair 1
+    reference[35] = -math.inf  # and its rejected: no order between them
+    loss, ratios, dx, _ = tg.linear_preference_step(x, w, target, offsets, torch.ones(2, device="cuda"),
+                                                    reference=reference, piece_rows=piece_rows)
+    assert float(loss[0]) == 0 and float(ratios[0, 0]) == math.inf and loss[1].isnan()
+    assert (dx[:20] == 0).all() and dx[20:].isnan().all()
+    loss, _, dx, _ = tg.linear_preference_step(x[:20], w, target[:20], offsets[[0, 0, 1, 1, 2]].contiguous(),
+                                               torch.ones(2, device="cuda"), reference=reference[:20].contiguous(),
+                                               piece_rows=piece_rows)
+    assert loss[0] == math.inf and loss[1].isfinite() and dx.isfinite().all()
+    one = torch.ones(T, device="cuda")
+    reference[5] = math.inf
+    loss, logp, _, _ = tg.linear_policy_step(x, w, target, one, one, one, reference=reference, kl_weight=0.1,
+                                             piece_rows=piece_rows)
+    assert loss[5] == math.inf and loss[3] == math.inf and loss[[0, 1, 2, 4]].isfinite().all()
+
+
 def test_long_answers():
     """Sums of long answers that nearly cancel keep their difference; an answer that is far behind or
     ahead."""
