@@ -547,6 +547,8 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   unsigned* err = nullptr;
   if ((st = tg::device_info(&sms, &err)) != TG_OK) return st;
   const int64_t np = round_up(N, 128), ld = 2 * np;
+  tg::TilePlan asked;  // options that no plan has are refused before anything is launched
+  if (opt && (st = tg::plan_tiles(M, K, ld, kSumLength, true, opt, &asked)) != TG_OK) return st;
   Layout lay;
   Operands ops;
   const int64_t rows = std::max(M, kLeastRows);

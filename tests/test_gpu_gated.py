@@ -329,3 +329,10 @@ def test_refusals():
     h, gate, up = tg.gated_linear(x, wg, wu, keep=True)
     with pytest.raises(ValueError):
         tg.gated_linear_backward(h, x, wg, wu, gate[:4], up)
+    for options in (dict(block_n=192), dict(block_n=100), dict(split_k=-1), dict(pair=2), dict(force_repack=1),
+                    dict(pair=1, max_ctas=1)):
+        with pytest.raises(tg.TgError):
+            tg.gated_linear(x, wg, wu, options=options)
+        for which in (dict(), dict(input_grad=False), dict(weight_grads=False)):
+            with pytest.raises(tg.TgError):
+                tg.gated_linear_backward(h, x, wg, wu, gate, up, options=options, **which)
