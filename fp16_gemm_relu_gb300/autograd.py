@@ -225,7 +225,9 @@ class GatedLinear(torch.autograd.Function):
 def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
                  activation: int = TG_ACT_SILU, trans_w: bool = False) -> torch.Tensor:
     """Differentiable act(x @ w_gate) * (x @ w_up) (see gated.gated_linear); keeps both pre-activations
-    in fp16 for the backward pass."""
+    in fp16 for the backward pass, and neither where gradients are off."""
+    if not torch.is_grad_enabled():  # (a Function's forward pass sees the inputs' requires_grad alone)
+        return gated.gated_linear(x, w_gate, w_up, activation, trans_w)
     return GatedLinear.apply(x, w_gate, w_up, activation, trans_w)
 
 

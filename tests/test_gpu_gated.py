@@ -288,6 +288,21 @@ def test_autograd(act):
         only.float().sum().backward()
 
 
+@pytest.mark.parametrize("off", [torch.no_grad, torch.inference_mode])
+def test_autograd_without_gradients(off):
+    """Parameters in a serving loop: nothing is kept, and the product is the same."""
+    M, N, K = 1024, 4096, 128
+    x, wg, wu = operands(M, N, K, False, 19)
+    want = tg.gated_linear(x, wg, wu)
+    wg, wu = torch.nn.Parameter(wg), torch.nn.Parameter(wu)
+    with off():
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        got = autograd.gated_linear(x, wg, wu)
+        used = torch.cuda.max_memory_allocated() - before
+    assert torch.equal(got, want) and not got.requires_grad and used < 2 * want.nbytes
+
+
 def test_differences():
     """The gradient against differences of the loss sum(dh h), along directions that keep fp16's grid:
     each step moves the operands by whole multiples of their spacing."""
