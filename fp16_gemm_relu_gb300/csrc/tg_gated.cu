@@ -255,7 +255,9 @@ bool whole_rows(const void* p, int64_t ld, int64_t n) {
 // row at a time, which costs 12%; splits cost a second kernel and their float32 sums through L2.  Measured
 // (us) against the alternatives: 1 x 8192 x 28672, K x N: two splits of 256 columns 149, one 155, 128 columns 165, a
 // pair's tiles 242; N x K: 128 columns 146, 256 in two splits 149; 16 x 8192 x 22016: four splits 122, one 137;
-// 1 x 4096 x 14336: one split of 256 columns 44, four 45, 128 columns 51.
+// 1 x 4096 x 14336: one split of 256 columns 44, four 45, 128 columns 51.  One block alone waits for its stages: a
+// k-block takes it 0.40 us at 256 columns and 0.27 at 128, so narrow weights are split by that: 64 x 8192 x 1000 in
+// 16 splits 19, whole 70; 1 x 28672 x 512 in 16 of 128 columns 22, whole 127; 1 x 4096 x 4096 in four 20, whole 31.
 tg::TilePlan few_rows_plan(const Gated& a, int sms) {
   tg::TilePlan best;
   std::memset(&best, 0, sizeof(best));
@@ -266,13 +268,14 @@ tg::TilePlan few_rows_plan(const Gated& a, int sms) {
   double best_t = 0.0;
   for (int bn = 256; bn >= 128; bn -= 128) {
     const int64_t tiles = cdiv(a.N, bn / 2);
-    for (int s = least; s <= std::max(least, 16); ++s) {
+    for (int s = least; s <= std::max(least, 32); ++s) {
       const int kbps = static_cast<int>(cdiv(best.num_kb, s));
       if (cdiv(best.num_kb, kbps) != s || (s > least && kbps < 4)) continue;
       const int64_t units = tiles * s;
       const double full = double(units) / double(cdiv(units, sms) * sms);
       double t = bytes / 6.6e12 / (0.65 + 0.35 * full);
       if (bn == 128 && !a.trans) t *= 1.12;
+      t = std::max(t, double(cdiv(units, sms)) * kbps * (bn == 128 ? 0.27e-6 : 0.40e-6));
       if (s > 1) t += 4e-6 + 16.0 * s * double(a.M) * double(a.N) / 1e13;
       if (best.block_n && t >= best_t) continue;
       best_t = t;

@@ -82,6 +82,16 @@ def test_long_sums(M, N, K):
                    *tg.gated_linear_backward(dh, x, wg, wu, gate, up))
 
 
+@pytest.mark.parametrize("K,N", [(8192, 64), (28672, 512), (4096, 1000), (1024, 256), (16384, 136)])
+@pytest.mark.parametrize("M", [1, 5, 64, 128])
+def test_narrow_weights(M, K, N):
+    """Few tiles of a long sum: split."""
+    for trans in (False, True):
+        x, wg, wu = operands(M, N, K, trans, 85)
+        h, gate, up = tg.gated_linear(x, wg, wu, trans_w=trans, keep=True)
+        check_forward(x, wg, wu, trans, "silu", h, gate, up)
+
+
 def test_rows_of_nan_stay_apart():
     """Few tokens' operands lie in scratch of eight rows: what is behind them does not come in, and a row of
     NaN spoils its own dx alone."""
