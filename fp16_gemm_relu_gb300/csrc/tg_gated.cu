@@ -40,6 +40,8 @@ constexpr int64_t kLeastRows = 8;
 // Elements of each weight from which it counts how dX and dW share the SMs.
 constexpr int64_t kBesideWork = int64_t{4} << 20;
 constexpr int64_t kBesideTokens = 256;
+// Tokens for which weights that TMA cannot read are not copied.
+constexpr int64_t kDirectTokens = 4;
 // Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
 // 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
 // Longer sums are taken in splits that are added in float32.
@@ -203,6 +205,8 @@ struct Layout {
   }
 };
 
+bool tma_cannot(const void* p, int64_t ld) { return misaligned(p, 16) || ld % 8 != 0; }
+
 // X and the weights as TMA reads them: in place, or as copies with rows of whole 128-byte lines where
 // the caller's are not 16-byte aligned with leading dimensions that are multiples of 8.
 struct Operands {
@@ -215,7 +219,7 @@ struct Operands {
   void plan(const Gated& a, bool need_x, bool need_w, int64_t least_rows, Layout* lay) {
     zeros = std::max<int64_t>(least_rows - a.M, 0);
     auto one = [&](const void* p, int64_t ld, int64_t rows, int64_t cols, bool copy = false) -> int64_t {
-      return copy || misaligned(p, 16) || ld % 8 != 0 ? lay->add(rows * round_up(cols, 64) * 2) : -1;
+      return copy || tma_cannot(p, ld) ? lay->add(rows * round_up(cols, 64) * 2) : -1;
     };
     const int64_t w_rows = a.trans ? a.N : a.K, w_cols = a.trans ? a.K : a.N;
     at[0] = need_x ? one(a.X, a.ldx, a.M + zeros, a.K, zeros > 0) : -1;
@@ -435,8 +439,39 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
     o.pair = 1;
     if ((st = tg::plan_tiles(M, 2 * round_up(N, 128), K, kSumLength, true, &o, &plan)) != TG_OK) return st;
   }
-  Operands ops;
   const int64_t nw = round_up(N, 32), stride = M * 2 * nw;
+  auto launch_reduce = [&](const float* sums, int splits) {
+    const dim3 grid(static_cast<unsigned>(cdiv(N, 512)), static_cast<unsigned>(std::min<int64_t>(M, 65535)));
+    return tg::launch_chained(tg_gated_reduce_kernel, true, grid, 128, 0, stream, sums, nw, stride, splits,
+                              activation, static_cast<__half*>(H), ldh, static_cast<__half*>(gate), ldgate,
+                              static_cast<__half*>(up), ldup, M, N);
+  };
+  // Up to four tokens over weights that would be copied for TMA: read where they are (1 x 4096 x 14333: K x N 57 us,
+  // with the copies 133; N x K, 4095 x 14336, 52 and 135; two tokens 63 and 59, four 77 and 82; eight would be about as
+  // long as the copies).  Weights that TMA reads are faster through it (44).
+  if (M <= kDirectTokens && choose && (tma_cannot(Wg, ldwg) || tma_cannot(Wu, ldwu))) {
+    tg::GatedRows r;
+    std::memset(&r, 0, sizeof(r));
+    r.x = static_cast<const __half*>(X), r.ldx = ldx;
+    r.wg = static_cast<const __half*>(Wg), r.ldwg = ldwg;
+    r.wu = static_cast<const __half*>(Wu), r.ldwu = ldwu;
+    r.h = static_cast<__half*>(H), r.ldh = ldh;
+    r.gate = static_cast<__half*>(gate), r.ldgate = ldgate;
+    r.up = static_cast<__half*>(up), r.ldup = ldup;
+    r.N = N, r.L = K, r.M = static_cast<int>(M), r.act = activation, r.nw = nw;
+    const int splits = tg::gated_rows_splits(M, N, K, trans_w, sms);
+    if (splits > 1 && (st = tg::scratch_alloc(size_t(splits * stride) * 4, stream,
+                                              reinterpret_cast<void**>(&r.ws))) != TG_OK)
+      return st;
+    cudaError_t e = tg::launch_gated_rows(r, trans_w, splits, sms, stream);
+    if (r.ws) {
+      if (e == cudaSuccess) e = launch_reduce(r.ws, splits);
+      const cudaError_t fe = cudaFreeAsync(r.ws, stream);
+      if (e == cudaSuccess) e = fe;
+    }
+    return e == cudaSuccess ? TG_OK : tg::record_cuda_error(e);
+  }
+  Operands ops;
   Layout lay;
   ops.plan(a, true, true, 0, &lay);
   const bool f32 = plan.splits > 1;
@@ -506,9 +541,7 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   if (!ok) return done(tg::record_cuda_error(cudaErrorInvalidValue));
   if ((e = tg::launch_gated(l)) != cudaSuccess) return done(tg::record_cuda_error(e));
   if (f32) {
-    const dim3 grid(static_cast<unsigned>(cdiv(N, 512)), static_cast<unsigned>(std::min<int64_t>(M, 65535)));
-    e = tg::launch_chained(tg_gated_reduce_kernel, true, grid, 128, 0, stream, ws, nw, stride, p.splits,
-                           activation, l.p.h, ldh, l.p.gate, ldgate, l.p.up, ldup, M, N);
+    e = launch_reduce(ws, p.splits);
     if (e != cudaSuccess) return done(tg::record_cuda_error(e));
   }
   return done(TG_OK);

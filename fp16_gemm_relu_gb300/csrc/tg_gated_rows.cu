@@ -1,0 +1,307 @@
+// tg_gated_rows.cu — the gated product of a few tokens over weights that TMA cannot read (rows that start
+// off 16-byte boundaries), straight from memory.
+//
+//   H[m, n] = act(sum_l X[m, l] Wg(l, n)) * sum_l X[m, l] Wu(l, n)
+//
+// A copy for TMA costs 4 bytes read and written for each 2 that the product needs, and few tokens need every
+// weight once: the float32 units, with a multiply for an element and token, keep up with the memory.
+// Weights are loaded in aligned words of two, 128 contiguous bytes a warp, wherever a row starts: a row that
+// starts inside a word is read from half a word before it, and its sums (or its tokens' elements) are those of one
+// column further left.  32 loads of a thread are under way at once, around the L1.  The words at the ends of a
+// row are put together from their halves, so nothing beside it is read.  Sums are float32, added in an order
+// that the sizes alone decide; the tokens' elements lie in shared memory in float32.
+//
+// One token of 4096 x 14333: K x N 57 us with the reduction (4.1 TB/s; in 2-byte loads 61, in clusters of four blocks 80, which left
+// SMs idle), 4095 x 14336 stored N x K 52 (4.5 TB/s); with the copies 133 and 135.  Bound by the loads under way
+// for one token, and by instructions from two on (two 63 and 59, four 77 and 82).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "tg_internal.h"
+
+namespace tg {
+namespace {
+
+constexpr int kWarps = 8;
+
+// A half's bits, or 0; without a branch, so that many are under way at once.
+__device__ __forceinline__ uint32_t half_bits(const __half* p, bool in) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .u16 h;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.u16 h, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}"
+      : "=r"(v)
+      : "l"(p), "r"(static_cast<int>(in)));
+  return v;
+}
+// Elements [at, at + 2) of a row of n, a word.  kInside: all are.  kRim: one or both may not be, and are zeros; the
+// word loaded is one of the row's, but may reach into the gap or the row beside it, so this is for rows with one on
+// either side.  kEdge: for all others, by halves; zeros if !in.
+enum : int { kInside, kRim, kEdge };
+template <int MODE>
+__device__ __forceinline__ uint32_t word(const __half* row, int64_t at, int64_t n, bool in) {
+  if constexpr (MODE == kEdge)
+    return half_bits(row + at, in && at >= 0 && at < n) | half_bits(row + at + 1, in && at >= -1 && at + 1 < n) << 16;
+  uint32_t w, keep = ~0u;
+  if constexpr (MODE == kRim) {
+    keep = at < 0 ? 0xffff0000u : at + 1 < n ? ~0u : at < n ? 0xffffu : 0u;
+    at = min(at, n - 1 - ((n - 1 - at) & 1));
+  }
+  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w) : "l"(row + at));
+  return w & keep;
+}
+__device__ __forceinline__ float2 floats(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <int MODE>
+using Mode = std::integral_constant<int, MODE>;
+// Whether a row starts in the middle of a word.
+__device__ __forceinline__ int odd(const __half* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+}
+
+__device__ __forceinline__ void finish(const GatedRows& p, int m, int64_t n, float g, float u) {
+  p.h[m * p.ldh + n] = __float2half_rn(gated_activation(g, p.act) * u);
+  if (p.gate) p.gate[m * p.ldgate + n] = __float2half_rn(g);
+  if (p.up) p.up[m * p.ldup + n] = __float2half_rn(u);
+}
+
+// Weights stored L x N.  A block has kColumns columns of H; the blocks along y share the rows, p.span each, and a block's warps take kTurn of them in turn.  A lane's two words of a row are columns
+// n0 - odd + 2 lane and 64 further: an odd row's lack the last column of 128 and an even one's have none before
+// n0, so a block's columns are 126.  The sums of even and odd turns stay apart until the end.
+constexpr int kColumns = 126, kTurn = 8, kChunk = 1024, kSlots = 130;
+template <int MM>
+__global__ void __launch_bounds__(kWarps * 32, MM > 2 ? 2 : 3) tg_gated_columns_kernel(const GatedRows p) {
+  __shared__ __align__(16) float mem[MM * kWarps * 2 * kSlots];  // tokens' elements; then each warp's sums
+  __shared__ float sum[MM][2 * kSlots];
+  static_assert(kWarps * 2 * kSlots >= kChunk, "the elements fit");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n0 = blockIdx.x * int64_t(kColumns);
+  const int64_t first = blockIdx.y * int64_t(p.span), last = min(p.L, first + p.span);
+  const int og[2] = {odd(p.wg), odd(p.wg + p.ldwg)}, ou[2] = {odd(p.wu), odd(p.wu + p.ldwu)};
+  float2 g[MM][2][2] = {}, u[MM][2][2] = {};  // by token, the row's parity, and 64 columns
+  const bool inside = n0 > 0 && n0 + 128 <= p.N;
+  auto turn = [&](auto mode, int64_t l, const float* x) {  // rows l to l + kTurn; l is even
+    constexpr int kMode = decltype(mode)::value;
+    uint32_t wg[kTurn][2], wu[kTurn][2];
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bool in = l + i < last;
+        const int64_t at = n0 + 64 * c + 2 * lane;
+        wg[i][c] = word<kMode>(p.wg + (l + i) * p.ldwg, at - og[i & 1], p.N, in);
+        wu[i][c] = word<kMode>(p.wu + (l + i) * p.ldwu, at - ou[i & 1], p.N, in);
+      }
+#pragma unroll
+    for (int i = 0; i < kTurn; ++i) {
+      float xs[MM];
+#pragma unroll
+      for (int m = 0; m < MM; ++m) xs[m] = x[i * MM + m];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float2 a = floats(wg[i][c]), b = floats(wu[i][c]);
+#pragma unroll
+        for (int m = 0; m < MM; ++m) {
+          float2 &s = g[m][i & 1][c], &t = u[m][i & 1][c];
+          s.x = fmaf(xs[m], a.x, s.x), s.y = fmaf(xs[m], a.y, s.y);
+          t.x = fmaf(xs[m], b.x, t.x), t.y = fmaf(xs[m], b.y, t.y);
+        }
+      }
+    }
+  };
+  for (int64_t c0 = first; c0 < last; c0 += kChunk) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kChunk * MM; i += kWarps * 32) {
+      const int m = i / kChunk, l = i % kChunk;
+      mem[l * MM + m] = m < p.M && c0 + l < last ? __half2float(__ldg(p.x + m * p.ldx + c0 + l)) : 0.0f;
+    }
+    __syncthreads();
+    const int rows = static_cast<int>(min(int64_t(kChunk), last - c0));
+    for (int l = warp * kTurn; l < rows; l += kWarps * kTurn) {
+      if (c0 + l == 0 || l + kTurn > rows || c0 + l + kTurn >= p.L)
+        turn(Mode<kEdge>{}, c0 + l, mem + l * MM);
+      else if (inside)
+        turn(Mode<kInside>{}, c0 + l, mem + l * MM);
+      else
+        turn(Mode<kRim>{}, c0 + l, mem + l * MM);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < MM; ++m) {
+    float* mine = mem + (m * kWarps + warp) * 2 * kSlots + 1;  // slot 0 is column n0 - 1
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float *s = mine + 64 * c + 2 * lane - og[q], *t = mine + kSlots + 64 * c + 2 * lane - ou[q];
+        const float2 a = g[m][q][c], b = u[m][q][c];
+        s[0] = q ? s[0] + a.x : a.x, s[1] = q ? s[1] + a.y : a.y;
+        t[0] = q ? t[0] + b.x : b.x, t[1] = q ? t[1] + b.y : b.y;
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < MM * 2 * kColumns; i += kWarps * 32) {  // over the warps, in order
+    const int m = i / (2 * kColumns), w = i / kColumns % 2, c = i % kColumns;
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) s += mem[(m * kWarps + k) * 2 * kSlots + w * kSlots + c + 1];
+    sum[m][w * kSlots + c] = s;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < MM * kColumns; i += kWarps * 32) {
+    const int m = i / kColumns, c = i % kColumns;
+    if (m >= p.M || n0 + c >= p.N) continue;
+    const float gs = sum[m][c], us = sum[m][kSlots + c];
+    if (p.ws) {  // the splits' sums, as tg_gated_reduce_kernel takes them
+      float* w = p.ws + (int64_t(blockIdx.y) * p.M + m) * 2 * p.nw + n0 + c;
+      w[0] = gs;
+      w[p.nw] = us;
+    } else {
+      finish(p, m, n0 + c, gs, us);
+    }
+  }
+}
+
+// Weights stored N x L.  A warp has four rows of each weight, and kReach words of each at once; p.parts of a
+// block's warps share their length.  A lane's word of a row that starts inside a word meets the tokens' elements one
+// further left, which it has too.
+constexpr int kRows = 4, kReach = 4, kLength = 2048;
+template <int MM>
+__global__ void __launch_bounds__(kWarps * 32, MM > 2 ? 2 : 3) tg_gated_rows_kernel(const GatedRows p) {
+  __shared__ __align__(16) float x[MM][kLength + 2];  // from element c0 - 2 on
+  __shared__ float red[kWarps][MM][2 * kRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / p.parts, part = warp % p.parts, groups = kWarps / p.parts;
+  const int64_t n0 = (blockIdx.x * int64_t(groups) + group) * kRows;
+  const __half *pg = p.wg + n0 * p.ldwg, *pu = p.wu + n0 * p.ldwu;  // (n0 is even: the parity of row 0 and row 1)
+  const int og[2] = {odd(p.wg), odd(p.wg + p.ldwg)}, ou[2] = {odd(p.wu), odd(p.wu + p.ldwu)};
+  float g[MM][kRows] = {}, u[MM][kRows] = {};
+  auto reach = [&](auto mode, int64_t l, const float* x0) {
+    constexpr int kMode = decltype(mode)::value;
+    uint32_t wg[kReach][kRows], wu[kReach][kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int j = 0; j < kReach; ++j) {
+        const bool in = n0 + r < p.N;
+        const int64_t at = l + 64 * j + 2 * lane;
+        wg[j][r] = word<kMode>(pg + r * p.ldwg, at - og[r & 1], p.L, in);
+        wu[j][r] = word<kMode>(pu + r * p.ldwu, at - ou[r & 1], p.L, in);
+      }
+#pragma unroll
+    for (int j = 0; j < kReach; ++j) {
+      float xs[MM][3];
+#pragma unroll
+      for (int m = 0; m < MM; ++m) {
+        const float* s = x0 + m * (kLength + 2) + 64 * j + 2 * lane;
+        const float2 v = *reinterpret_cast<const float2*>(s);
+        xs[m][0] = s[-1], xs[m][1] = v.x, xs[m][2] = v.y;
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float2 a = floats(wg[j][r]), b = floats(wu[j][r]);
+        const bool sg = og[r & 1], su = ou[r & 1];
+#pragma unroll
+        for (int m = 0; m < MM; ++m) {
+          g[m][r] = fmaf(sg ? xs[m][0] : xs[m][1], a.x, fmaf(sg ? xs[m][1] : xs[m][2], a.y, g[m][r]));
+          u[m][r] = fmaf(su ? xs[m][0] : xs[m][1], b.x, fmaf(su ? xs[m][1] : xs[m][2], b.y, u[m][r]));
+        }
+      }
+    }
+  };
+  const int step = 64 * kReach;
+  for (int64_t c0 = 0; c0 <= p.L; c0 += kLength) {  // (element L - 1 may be the first of the word at L)
+    __syncthreads();
+    for (int i = threadIdx.x; i < MM * (kLength + 2); i += kWarps * 32) {
+      const int m = i / (kLength + 2), l = i % (kLength + 2);
+      const int64_t at = c0 + l - 2;
+      x[m][l] = m < p.M && at >= 0 && at < p.L ? __half2float(__ldg(p.x + m * p.ldx + at)) : 0.0f;
+    }
+    __syncthreads();
+    const int64_t end = min(c0 + kLength, p.L + 1);
+    for (int64_t l = c0 + part * step; l < end; l += p.parts * step) {
+      if (l > 0 && l + step <= p.L && n0 + kRows <= p.N)
+        reach(Mode<kInside>{}, l, &x[0][2] + (l - c0));
+      else if (n0 > 0 && n0 + kRows < p.N)
+        reach(Mode<kRim>{}, l, &x[0][2] + (l - c0));
+      else
+        reach(Mode<kEdge>{}, l, &x[0][2] + (l - c0));
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MM; ++m)
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        g[m][r] += __shfl_xor_sync(~0u, g[m][r], o);
+        u[m][r] += __shfl_xor_sync(~0u, u[m][r], o);
+      }
+      if (lane == 0) {
+        red[warp][m][r] = g[m][r];
+        red[warp][m][kRows + r] = u[m][r];
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < groups * MM * kRows; i += kWarps * 32) {
+    const int r = i % kRows, gr = i / kRows % groups, m = i / (kRows * groups);
+    const int64_t n = (blockIdx.x * int64_t(groups) + gr) * kRows + r;
+    if (m >= p.M || n >= p.N) continue;
+    float gs = 0.0f, us = 0.0f;
+    for (int q = 0; q < p.parts; ++q) {
+      gs += red[gr * p.parts + q][m][r];
+      us += red[gr * p.parts + q][m][kRows + r];
+    }
+    finish(p, m, n, gs, us);
+  }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+int gated_rows_splits(int64_t M, int64_t N, int64_t L, bool trans, int sms) {
+  if (trans) return 1;
+  // The rows of the longest turn of blocks, three to an SM, or two.
+  const int64_t blocks = cdiv(N, kColumns), at_once = int64_t(sms) * (M > 2 ? 2 : 3);
+  int64_t best = 0;
+  int splits = 1;
+  for (int s = 1; s <= 32 && (s == 1 || L >= int64_t(s) * kWarps * kTurn); ++s) {
+    const int64_t t = cdiv(blocks * s, at_once) * cdiv(L, s) + 8 * s;
+    if (s > 1 && t >= best) continue;
+    best = t;
+    splits = s;
+  }
+  return splits;
+}
+
+cudaError_t launch_gated_rows(const GatedRows& q, bool trans, int splits, int sms, cudaStream_t stream) {
+  GatedRows p = q;
+  auto go = [&](auto columns, auto rows) {
+    if (trans) {
+      // the warps that SMs of two blocks hold at once, where the rows are as many
+      const int64_t sets = cdiv(p.N, kRows);
+      p.parts = 1;
+      while (p.parts < kWarps && sets * p.parts < int64_t(sms) * 16) p.parts *= 2;
+      rows<<<static_cast<unsigned>(cdiv(sets * p.parts, kWarps)), kWarps * 32, 0, stream>>>(p);
+    } else {
+      p.span = cdiv(cdiv(p.L, splits), kTurn) * kTurn;
+      const dim3 grid(static_cast<unsigned>(cdiv(p.N, kColumns)), static_cast<unsigned>(splits));
+      columns<<<grid, kWarps * 32, 0, stream>>>(p);
+    }
+    return cudaGetLastError();
+  };
+  if (p.M == 1) return go(tg_gated_columns_kernel<1>, tg_gated_rows_kernel<1>);
+  if (p.M == 2) return go(tg_gated_columns_kernel<2>, tg_gated_rows_kernel<2>);
+  return go(tg_gated_columns_kernel<4>, tg_gated_rows_kernel<4>);
+}
+
+}  // namespace tg

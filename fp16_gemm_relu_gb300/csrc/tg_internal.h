@@ -148,6 +148,19 @@ struct GatedLaunch {
 };
 cudaError_t launch_gated(const GatedLaunch& l);
 
+// Up to four tokens over weights read where they are (tg_gated_rows.cu): rows of N, or trans, of L.  Splits of
+// the sum, where there are several, go to ws, for tg_gated_reduce_kernel.
+struct GatedRows {
+  const __half *x, *wg, *wu;
+  __half *h, *gate, *up;  // gate and up may be NULL
+  float* ws;              // splits x M rows of gates and, nw further, ups
+  long long ldx, ldwg, ldwu, ldh, ldgate, ldup, nw;
+  int64_t N, L, span;     // span and parts: the launch's own
+  int M, act, parts;
+};
+int gated_rows_splits(int64_t M, int64_t N, int64_t L, bool trans, int sms);
+cudaError_t launch_gated_rows(const GatedRows& p, bool trans, int splits, int sms, cudaStream_t stream);
+
 // How the GEMM's planner would run an M x N x K product on aligned operands, with or without K splits,
 // in tiles of 256 x 256 on CTA pairs, or 128 x 256, 128 x 192 (not with `halves`) or 128 x 128.
 struct TilePlan {
