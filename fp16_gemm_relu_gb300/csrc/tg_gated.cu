@@ -40,8 +40,8 @@ constexpr int64_t kLeastRows = 8;
 // Elements of each weight from which it counts how dX and dW share the SMs.
 constexpr int64_t kBesideWork = int64_t{4} << 20;
 constexpr int64_t kBesideTokens = 256;
-// Tokens for which weights that TMA cannot read are not copied.
-constexpr int64_t kDirectTokens = 4;
+// Elements of each weight and token from which gradients are taken without copies of the weights.
+constexpr int64_t kStraightWork = int64_t{2} << 20;
 // Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
 // 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
 // Longer sums are taken in splits that are added in float32.
@@ -248,6 +248,11 @@ struct Operands {
   }
 };
 
+// Up to four tokens over weights that would be copied for TMA: read where they are (1 x 4096 x 14333: K x N 57 us,
+// with the copies 133; N x K, 4095 x 14336, 52 and 135; two tokens 63 and 59, four 77 and 82; eight would be about as
+// long as the copies).  Weights that TMA reads are faster through it (44).
+bool straight(const Gated& a) { return a.M <= 4 && (tma_cannot(a.Wg, a.ldwg) || tma_cannot(a.Wu, a.ldwu)); }
+
 // Whether TMA can store whole rows of n fp16 columns.
 bool whole_rows(const void* p, int64_t ld, int64_t n) {
   return !misaligned(p, 16) && ld % 8 == 0 && n % 8 == 0;
@@ -446,10 +451,7 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
                               activation, static_cast<__half*>(H), ldh, static_cast<__half*>(gate), ldgate,
                               static_cast<__half*>(up), ldup, M, N);
   };
-  // Up to four tokens over weights that would be copied for TMA: read where they are (1 x 4096 x 14333: K x N 57 us,
-  // with the copies 133; N x K, 4095 x 14336, 52 and 135; two tokens 63 and 59, four 77 and 82; eight would be about as
-  // long as the copies).  Weights that TMA reads are faster through it (44).
-  if (M <= kDirectTokens && choose && (tma_cannot(Wg, ldwg) || tma_cannot(Wu, ldwu))) {
+  if (choose && straight(a)) {
     tg::GatedRows r;
     std::memset(&r, 0, sizeof(r));
     r.x = static_cast<const __half*>(X), r.ldx = ldx;
@@ -459,11 +461,11 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
     r.gate = static_cast<__half*>(gate), r.ldgate = ldgate;
     r.up = static_cast<__half*>(up), r.ldup = ldup;
     r.N = N, r.L = K, r.M = static_cast<int>(M), r.act = activation, r.nw = nw;
-    const int splits = tg::gated_rows_splits(M, N, K, trans_w, sms);
+    const int splits = tg::plan_gated_rows(&r, trans_w, false, sms);
     if (splits > 1 && (st = tg::scratch_alloc(size_t(splits * stride) * 4, stream,
                                               reinterpret_cast<void**>(&r.ws))) != TG_OK)
       return st;
-    cudaError_t e = tg::launch_gated_rows(r, trans_w, splits, sms, stream);
+    cudaError_t e = tg::launch_gated_rows(r, trans_w, splits, stream);
     if (r.ws) {
       if (e == cudaSuccess) e = launch_reduce(r.ws, splits);
       const cudaError_t fe = cudaFreeAsync(r.ws, stream);
@@ -591,9 +593,16 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   const int64_t at_g = lay.add(rows * ld * 2);
   const int64_t width = K <= 2048 ? 128 : 256;  // few tokens: dX's tiles
   const bool choose = !opt || (!opt->block_n && !opt->split_k && !opt->pair && !opt->max_ctas && !opt->panel_m);
-  const int beside = dX && dWg && dWu && choose ? beside_splits(a, ld, width, sms) : 0;
-  const int64_t ldw = round_up(K, 32), at_ws = lay.add(beside * M * ldw * 4);
-  ops.plan(a, dWg || dWu, dX, dWg || dWu ? kLeastRows : 0, &lay);
+  // Its gradients: one token of 4096 x 14333 114 us, with the copies 220, two 129, four 166 and 222; smaller weights
+  // pay more for two more launches than their copies cost (four of 1023 x 4091 42 to 45 and 40, one 28 to 34 and 38).
+  const bool direct = choose && straight(a) && K * N >= M * kStraightWork;
+  const int beside = dX && dWg && dWu && choose && !direct ? beside_splits(a, ld, width, sms) : 0;
+  tg::GatedRows r;
+  std::memset(&r, 0, sizeof(r));
+  r.N = K, r.L = N, r.M = static_cast<int>(std::min<int64_t>(M, 4));
+  const int apart = direct && dX ? tg::plan_gated_rows(&r, !trans_w, true, sms) : 1;  // dX's sum
+  const int64_t ldw = round_up(K, 32), at_ws = lay.add((apart > 1 ? apart : beside) * M * ldw * 4);
+  if (!direct) ops.plan(a, dWg || dWu, dX, dWg || dWu ? kLeastRows : 0, &lay);
   uint8_t* mem = nullptr;
   if ((st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
@@ -603,8 +612,36 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   };
   __half* g = reinterpret_cast<__half*>(mem + at_g);
   e = launch_grad(activation, static_cast<const __half*>(dH), lddh, static_cast<const __half*>(gate), ldgate,
-                  static_cast<const __half*>(up), ldup, g, ld, np, M, N, rows, stream);
+                  static_cast<const __half*>(up), ldup, g, ld, np, M, N, direct ? M : rows, stream);
   if (e != cudaSuccess) return done(tg::record_cuda_error(e));
+  if (direct) {
+    const __half* x = static_cast<const __half*>(X);
+    if (dWg || dWu) {
+      tg::GatedOuter w;
+      std::memset(&w, 0, sizeof(w));
+      w.rows = trans_w ? g : x, w.rows2 = trans_w ? g + np : x, w.ld_rows = trans_w ? ld : ldx;
+      w.cols = trans_w ? x : g, w.cols2 = trans_w ? x : g + np, w.ld_cols = trans_w ? ldx : ld;
+      w.out = static_cast<__half*>(dWg), w.ld = lddwg;
+      w.out2 = static_cast<__half*>(dWu), w.ld2 = lddwu;
+      w.n_rows = w_rows, w.n_cols = w_cols, w.M = static_cast<int>(M);
+      e = tg::launch_gated_outer(w, stream);
+    }
+    if (dX && e == cudaSuccess) {
+      r.x = g, r.x2 = g + np, r.ldx = ld;
+      r.wg = static_cast<const __half*>(Wg), r.ldwg = ldwg;
+      r.wu = static_cast<const __half*>(Wu), r.ldwu = ldwu;
+      r.h = static_cast<__half*>(dX), r.ldh = lddx;
+      r.ws = apart > 1 ? reinterpret_cast<float*>(mem + at_ws) : nullptr, r.nw = ldw;
+      e = tg::launch_gated_rows(r, !trans_w, apart, stream);
+      if (r.ws && e == cudaSuccess) {
+        tg::GemmParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.M = static_cast<int>(M), p.N = static_cast<int>(K);
+        e = tg::launch_splitk_reduce(r.ws, ldw, M * ldw, apart, dX, lddx, p, sms, stream);
+      }
+    }
+    return done(e == cudaSuccess ? TG_OK : tg::record_cuda_error(e));
+  }
   bool copied = false;
   if ((e = ops.copy(a, mem, sms, true, stream, &copied)) != cudaSuccess) return done(tg::record_cuda_error(e));
   tg::GemmExtra ex;

@@ -149,17 +149,28 @@ struct GatedLaunch {
 cudaError_t launch_gated(const GatedLaunch& l);
 
 // Up to four tokens over weights read where they are (tg_gated_rows.cu): rows of N, or trans, of L.  Splits of
-// the sum, where there are several, go to ws, for tg_gated_reduce_kernel.
+// the sum, where there are several, go to ws, for tg_gated_reduce_kernel.  With x2, the gradient's sum instead:
+// h = x Wg' + x2 Wu', and splits of M rows of nw.
 struct GatedRows {
-  const __half *x, *wg, *wu;
+  const __half *x, *x2, *wg, *wu;
   __half *h, *gate, *up;  // gate and up may be NULL
   float* ws;              // splits x M rows of gates and, nw further, ups
   long long ldx, ldwg, ldwu, ldh, ldgate, ldup, nw;
-  int64_t N, L, span;     // span and parts: the launch's own
+  int64_t N, L, span;     // span and parts: the plan's
   int M, act, parts;
 };
-int gated_rows_splits(int64_t M, int64_t N, int64_t L, bool trans, int sms);
-cudaError_t launch_gated_rows(const GatedRows& p, bool trans, int splits, int sms, cudaStream_t stream);
+// The splits for M, N and L; sets span and parts.
+int plan_gated_rows(GatedRows* p, bool trans, bool dual, int sms);
+cudaError_t launch_gated_rows(const GatedRows& p, bool trans, int splits, cudaStream_t stream);
+// Two products of up to four tokens, out = rows^T cols and out2 = rows2^T cols2; either may be NULL.
+struct GatedOuter {
+  const __half *rows, *rows2, *cols, *cols2;
+  __half *out, *out2;
+  long long ld_rows, ld_cols, ld, ld2;
+  int64_t n_rows, n_cols;
+  int M;
+};
+cudaError_t launch_gated_outer(const GatedOuter& p, cudaStream_t stream);
 
 // How the GEMM's planner would run an M x N x K product on aligned operands, with or without K splits,
 // in tiles of 256 x 256 on CTA pairs, or 128 x 256, 128 x 192 (not with `halves`) or 128 x 128.

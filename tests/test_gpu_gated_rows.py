@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 import fp16_gemm_relu_gb300 as tg  # noqa: E402
-from tests.test_gpu_gated import ACTS, _built, check_forward, gen  # noqa: E402,F401
+from tests.test_gpu_gated import ACTS, _built, check_backward, check_forward, gen  # noqa: E402,F401
 
 
 def between_nan(t, pad, offset):
@@ -47,6 +47,70 @@ def test_sizes(M, N, K, trans):
         h, gate, up = tg.gated_linear(x, wg, wu, trans_w=trans, keep=True)
         check_forward(x, wg, wu, trans, "silu", h, gate, up)
         assert torch.equal(h, tg.gated_linear(x, wg, wu, trans_w=trans))
+
+
+def pre_activations(M, N, seed, pad, offset):
+    g = gen(seed)
+    return [between_nan(torch.randn(M, N, generator=g, device="cuda") * s, pad, offset) for s in (0.25, 1.5, 1.5)]
+
+
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 2051, 1031), (2, 2305, 2051), (3, 4097, 2053), (4, 2053, 4097), (4, 515, 16389),
+                                   (3, 16389, 515), (2, 5, 1000001), (2, 1000001, 5), (1, 1, 2100001), (1, 2100001, 1),
+                                   (4, 127, 66053), (4, 66053, 127), (1, 1024, 2049), (2, 2048, 2049), (1, 2049, 1024)])
+def test_gradients(M, N, K, trans):
+    for pad, offsets in ((0, (1, 0, 0)), (1, (0, 3, 1)), (0, (2, 4, 3))):
+        x, wg, wu = operands(M, N, K, trans, N + K, pad, offsets)
+        dh, gate, up = pre_activations(M, N, 86, pad, offsets[1])
+        got = tg.gated_linear_backward(dh, x, wg, wu, gate, up, trans_w=trans)
+        check_backward(dh, x, wg, wu, gate, up, trans, "silu", *got)
+        dx = tg.gated_linear_backward(dh, x, wg, wu, gate, up, trans_w=trans, weight_grads=False)[0]
+        dw = tg.gated_linear_backward(dh, x, wg, wu, gate, up, trans_w=trans, input_grad=False)[1:]
+        assert all(torch.equal(a, b) for a, b in zip(got, (dx, *dw)))
+
+
+def test_gradients_of_very_many_rows():
+    M, N, K = 1, 3, 65535 * 128 + 130
+    x, wg, wu = operands(M, N, K, False, 87, 0, (1, 0, 0))
+    dh, gate, up = pre_activations(M, N, 88, 0, 0)
+    check_backward(dh, x, wg, wu, gate, up, False, "silu", *tg.gated_linear_backward(dh, x, wg, wu, gate, up))
+
+
+def test_gradients_into_views():
+    """One weight's gradient alone, rows that start anywhere and what is beside them."""
+    from fp16_gemm_relu_gb300 import binding
+
+    M, N, K, pad = 2, 2305, 2051, 3
+    x, wg, wu = operands(M, N, K, False, 89, 1, (1, 2, 0))
+    dh, gate, up = pre_activations(M, N, 90, 0, 0)
+    want = tg.gated_linear_backward(dh, x, wg, wu, gate, up)
+    stream = torch.cuda.current_stream().cuda_stream
+    for which in ((1, 0), (0, 1), (1, 1)):
+        for offset in (0, 1):
+            bufs = [torch.full((K * (N + pad) + 8,), 9.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+            views = [b.as_strided((K, N), (N + pad, 1), offset) for b in bufs]
+            st = binding.tg_gated_backward_f16(
+                dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), gate.data_ptr(), up.data_ptr(), 0,
+                *(v.data_ptr() if w else 0 for v, w in zip(views, which)), binding.TG_ACT_SILU, 0, M, N, K, N,
+                x.stride(0), wg.stride(0), wu.stride(0), N, N, 0, N + pad, N + pad, stream=stream)
+            assert st == binding.TG_OK
+            for b, v, w, ref in zip(bufs, views, which, want[1:]):
+                if w:
+                    assert torch.equal(v, ref)
+                    v.fill_(9.0)
+                assert (b == 9).all()
+
+
+@pytest.mark.parametrize("trans", [False, True])
+def test_gradients_of_rows_of_nan(trans):
+    M, N, K = 3, 4097, 2053
+    x, wg, wu = operands(M, N, K, trans, 91, 0, (1, 0, 1))
+    dh, gate, up = pre_activations(M, N, 92, 0, 1)
+    want = tg.gated_linear_backward(dh, x, wg, wu, gate, up, trans_w=trans)
+    bad = dh.clone()
+    bad[1] = math.nan
+    dx, dwg, dwu = tg.gated_linear_backward(bad, x, wg, wu, gate, up, trans_w=trans)
+    assert dx[1].isnan().all() and torch.equal(dx[::2], want[0][::2]) and dwg.isnan().all() and dwu.isnan().all()
 
 
 @pytest.mark.parametrize("trans", [False, True])
@@ -98,15 +162,20 @@ def test_extreme_weights():
 def test_same_bits_captured_and_on_a_stream(trans):
     M, N, K = 2, 3001, 2999
     x, wg, wu = operands(M, N, K, trans, 83, 0, (0, 1, 0))
-    want = tg.gated_linear(x, wg, wu, trans_w=trans, keep=True)
+
+    def step(stream=None):
+        h, gate, up = tg.gated_linear(x, wg, wu, trans_w=trans, keep=True, stream=stream)
+        return h, gate, up, *tg.gated_linear_backward(h, x, wg, wu, gate, up, trans_w=trans, stream=stream)
+
+    want = step()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    other = tg.gated_linear(x, wg, wu, trans_w=trans, keep=True, stream=side)
+    other = step(side)
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        got = tg.gated_linear(x, wg, wu, trans_w=trans, keep=True)
+        got = step()
     for t in got:
         t.zero_()
     graph.replay()
