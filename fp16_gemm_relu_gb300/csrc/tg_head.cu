@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kRowThreads)
                         const void* __restrict__ teacher, int teacher_f32, int64_t ldt, int top,
                         const float* __restrict__ dloss, const unsigned* wmax,
                         float* loss, float* lse, RowInfo* info, float* q, float* alpha, float lift) {
-  __shared__ float slots[5][4];
+  __shared__ float slots[6][4];
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x;
   tg::chain_wait();
@@ -181,9 +181,20 @@ __global__ void __launch_bounds__(kRowThreads)
     if (i0 >= 0 && i0 < vocab) z0 = lg.z ? lg.z[r * lg.ldz + i0] : lg.picked[r * top + tid];
   }
   float m = -INFINITY, s = 0.0f;
+  const float2* parts = stats + r * tiles;
+  if (lift > 0.0f) {  // with the row's maximum before any sum, so that each of them takes one power of two
 #pragma unroll 4
-  for (int t = tid; t < tiles; t += kRowThreads) {
-    const float2 v = __ldcg(stats + r * tiles + t);
+    for (int t = tid; t < tiles; t += kRowThreads) m = fmaxf(m, __ldcg(&parts[t].x));
+    m = block_max(m, slots[5]);
+#pragma unroll 4
+    for (int t = tid; t < tiles; t += kRowThreads) {
+      const float2 v = __ldcg(parts + t);
+      s += m > -INFINITY ? v.y * exp2f(v.x - m) : v.y;
+    }
+  }
+#pragma unroll 4
+  for (int t = lift > 0.0f ? tiles : tid; t < tiles; t += kRowThreads) {
+    const float2 v = __ldcg(parts + t);
     const float m1 = fmaxf(m, v.x);
     if (m1 == -INFINITY) {
       s += v.y;  // zero or NaN
@@ -831,6 +842,7 @@ tg_status run_head(const Head& h, cudaStream_t stream) {
     lx.picked = picked;
     lx.block_n = &block_n;
     lx.precise = h.precise;
+    lx.width = h.D;
     std::memset(&ex, 0, sizeof(ex));
     ex.logits = &lx;
     if (h.T < kLeastRows) ex.a_rows = kLeastRows - t0;

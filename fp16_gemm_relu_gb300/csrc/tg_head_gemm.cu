@@ -29,6 +29,7 @@ cudaError_t launch_head_logits(const GemmLaunch& l, const LogitsExtra& x, int bl
   hp.target = x.target;
   hp.picked = x.picked;
   hp.rotate = l.p.tiles_m == 1 ? 1 : 0;
+  hp.spare = static_cast<int>((int64_t(l.p.num_kb) * kBK - x.width) / kUmmaK);
   if (x.precise) return launch_head_logits_precise(l, hp, x.z != nullptr, block_n);
   if (l.p.b_k)
     return x.z ? launch_logits<true, true>(l, hp, block_n) : launch_logits<true, false>(l, hp, block_n);

@@ -14,12 +14,14 @@
 //    cost 1-3% more time than of 1024, those of 2048 save nothing further.
 //    PRECISE, for losses of differences of log probabilities, where what every token's log probability is
 //    off in one direction adds up over a sequence: segments of 768 columns, and what the cutting off takes from a
-//    segment of n instructions on average, c(n) = (0.276 n + 0.38) 2^-24 of its sum, is put back as it is
-//    added.  Measured over 4096 tokens, 4096 classes of normal logits of spread 2, 64 to 4096 columns: a logit
-//    shrinks by 1.1e-6 of itself in segments of 1024 and 5.5e-7 in those of 512 (n = 4 to 64: c(n) within 2%,
-//    operands with a mean 10% more), which shifts a log probability by 4.4e-6 and 2.4e-6; put back, by less than
-//    1.1e-7.  Random errors are 2.6e-6 in segments of 1024, 1.1e-6 in those of 768.  4096 tokens, 65537 classes of 2048
-//    with the logits stored 700 us, 680 without any of this, 735 in segments of 512.
+//    segment's sum v on average is put back as it is added.  Each of n instructions cuts half a unit of the partial
+//    sum's last place.  Of sums that are large beside their row's, whose partial sums go there straight, that is up to
+//    0.3 n 2^-24, of others 0.27 n, whose partial sums stay below v or change sign; measured over normal logits of
+//    spread 1 to 4, n = 5 to 48, it is (0.266 n + 0.38 + n min(0.0036 (v / s)^2, 0.035)) 2^-24 of v within 1% of n, s being the
+//    row's root mean square (of a warp's first 32 columns).  An instruction past the last column cuts nothing.
+//    A log probability is then off by less than 5e-8 on average (30666 classes of 768 1e-8; with 0.276 n for all 1.4e-7, with
+//    nothing put back in segments of 1024 4.4e-6), root mean square 1.1e-6 (2.6e-6 in segments of 1024).
+//    4096 tokens, 65537 classes of 2048: the whole step 2280 us, 2230 with 0.276 n for all; segments of 512 would cost 35 more.
 //  - The running sums take 128 registers a thread, so there are eight epilogue warps, each with 32
 //    rows and half of the tile's columns.  With the whole row segment in registers they take its
 //    maximum and sum of exponentials, and then store it, or only look up the rows' targets.
@@ -63,7 +65,14 @@ struct HeadParams {
   const long long* target;  // !STORE, or NULL: [M], the column whose logit goes to picked
   float* picked;
   int rotate;               // 1: tiles start at different k-blocks (CG == 1)
+  int spare;                // instructions of the last k-block that add nothing
 };
+
+// The k-block that a tile begins with.
+template <int CG>
+__device__ __forceinline__ int first_kb(const HeadParams& hp, int u) {
+  return CG == 1 && hp.rotate ? static_cast<int>(static_cast<unsigned>(u) * 7u % static_cast<unsigned>(hp.g.num_kb)) : 0;
+}
 
 // Softmax statistics of NC columns of one row (cnt: how many of them the matrix has): m = the largest
 // of the scaled sums, s = the sum of 2^(scaled sum - m), with log2(e) in the scale c.  A row's
@@ -195,7 +204,7 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
         const int wrow = w.n_blk * BN + static_cast<int>(rank) * Cfg::kBRows;
         // Where W's rows stream from memory once (few tokens), tiles that all walk the same
         // columns at the same time meet in the same memory channels: each starts elsewhere.
-        int at = CG == 1 && hp.rotate ? static_cast<int>(static_cast<unsigned>(u) * 7u % static_cast<unsigned>(p.num_kb)) : 0;
+        int at = first_kb<CG>(hp, u);
         for (int kb = 0; kb < p.num_kb; kb += KB) {
           if (!wait_phase(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p, kRoleProducer))
             goto producer_done;
@@ -326,6 +335,7 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
       const int row0 = (w.m_blk * CG + static_cast<int>(rank)) * kBM + q * 32;
       const int col0 = w.n_blk * BN + half * NC;
       const bool live = row0 < p.M;     // a warp without rows only hands the accumulators back
+      const int last_kb = p.num_kb - 1 - first_kb<CG>(hp, u);  // when the last k-block's turn is
       float acc[NC];
 #pragma unroll
       for (int i = 0; i < NC; ++i) acc[i] = 0.0f;
@@ -344,18 +354,28 @@ __device__ __forceinline__ void head_logits_body(const CUtensorMap& tmX, const C
           const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                               static_cast<uint32_t>(buf * Cfg::kAccStride + half * NC);
           // what the segment's instructions cut off, of its sum (PRECISE); 1 + back would be rounded to 2^-23
-          const float back = (0.276f * (min(SEG, p.num_kb - k0) * (kBK / kUmmaK)) + 0.38f) * 0x1p-24f;
+          const bool tail = last_kb >= k0 && last_kb < k0 + SEG;
+          const int n = min(SEG, p.num_kb - k0) * (kBK / kUmmaK) - (tail ? hp.spare : 0);
+          const float unit = 0x1p-24f * n, back = fmaf(0.266f, unit, 0.38f * 0x1p-24f), top = back + 0.035f * unit;
+          float squares = 1e-30f, slope = 0.0f;
 #pragma unroll
           for (int c = 0; c < NC / 16; ++c) {  // 16 at a time: NC registers are taken already
             uint32_t r[16];
             tmem_ld_x16(tl + c * 16, r);
             tmem_wait_ld(r);
+            if constexpr (PRECISE)
+              if (c < 2) {  // the spread of the row's sums, from its first columns
+#pragma unroll
+                for (int i = 0; i < 16; ++i) squares = fmaf(__uint_as_float(r[i]), __uint_as_float(r[i]), squares);
+                slope = __fdividef(0.0036f * unit * (16 * c + 16), squares);
+              }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
+              const float v = __uint_as_float(r[i]);
               if constexpr (PRECISE)
-                acc[c * 16 + i] = fmaf(__uint_as_float(r[i]), back, acc[c * 16 + i] + __uint_as_float(r[i]));
+                acc[c * 16 + i] = fmaf(v, fminf(fmaf(v * v, slope, back), top), acc[c * 16 + i] + v);
               else
-                acc[c * 16 + i] += __uint_as_float(r[i]);
+                acc[c * 16 + i] += v;
             }
           }
         }

@@ -72,6 +72,7 @@ struct LogitsExtra {
   float* picked;
   int* block_n;             // out: the tiles' width
   bool precise;             // see tg_head_kernel.cuh
+  int64_t width;            // the sums' terms
 };
 struct HeadParams;
 // Logits kernel (block_n 0: CTA pairs), X row-major, W in either layout (l.p.b_k).

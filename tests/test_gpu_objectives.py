@@ -333,6 +333,24 @@ def test_infinite_references(piece_rows):
     assert loss[5] == math.inf and loss[3] == math.inf and loss[[0, 1, 2, 4]].isfinite().all()
 
 
+@pytest.mark.parametrize("V,D", [(1710, 80), (7033, 360), (30666, 768), (7033, 1596)])
+def test_log_probabilities_lean_neither_way(V, D):
+    """The mean error over many tokens, which a sum over a sequence multiplies: 5e-8 and three standard errors of 4096
+    tokens whose errors are 1.3e-6 (2^-24 of up to 8 for each of a logit's few roundings), 1.1e-7 in all."""
+    T = 4096
+    g = gen(170)
+    x = torch.randn(T, D, generator=g, device="cuda").half()
+    w = (torch.randn(V, D, generator=g, device="cuda") * (2 / math.sqrt(D))).half()
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    one = torch.zeros(T, device="cuda")
+    _, logp = tg.linear_policy(x, w, target, one, one)
+    error = torch.empty(T, dtype=D64, device="cuda")
+    for a in range(0, T, 1024):
+        z = x[a:a + 1024].to(D64) @ w.to(D64).t()
+        error[a:a + 1024] = logp[a:a + 1024] - torch.log_softmax(z, 1).gather(1, target[a:a + 1024, None])[:, 0]
+    assert abs(float(error.mean())) < 1.1e-7 and float(error.square().mean().sqrt()) < 1.6e-6
+
+
 def test_long_answers():
     """Sums of long answers that nearly cancel keep their difference; an answer that is far behind or
     ahead."""
