@@ -248,9 +248,9 @@ struct Operands {
   }
 };
 
-// Up to four tokens over weights that would be copied for TMA: read where they are (1 x 4096 x 14333: K x N 57 us,
-// with the copies 133; N x K, 4095 x 14336, 52 and 135; two tokens 63 and 59, four 77 and 82; eight would be about as
-// long as the copies).  Weights that TMA reads are faster through it (44).
+// Up to four tokens over weights that would be copied for TMA: read where they are (1 x 4096 x 14333: K x N 48 us,
+// with the copies 133; N x K, 4095 x 14336, 51 and 135; two tokens 63 and 57, four 77 and 88; eight would be about as
+// long as the copies).  Weights that TMA reads are faster through it (43).
 bool straight(const Gated& a) { return a.M <= 4 && (tma_cannot(a.Wg, a.ldwg) || tma_cannot(a.Wu, a.ldwu)); }
 
 // Whether TMA can store whole rows of n fp16 columns.
