@@ -16,9 +16,10 @@
 // left operand (DUAL: the sums are added instead), and dWg and dWu, whose rows start anywhere as well, in
 // aligned words from a kernel that only writes.
 //
-// One token of 4096 x 14333: K x N 48 us with the splits' sums joined (the kernel 44, 5.3 TB/s; in 2-byte loads 61, the splits as
-// clusters' blocks 80, which left SMs idle), 4095 x 14336 stored N x K 51; with the copies 133 and 135; 8192 x 28671 160 and 146, 480.
-// Bound by the loads under way for one token, and by instructions from two on (two 63 and 57, four 77 and 88).
+// One token of 4096 x 14333: K x N 48 us with the splits' sums joined (the kernel 44, 5.3 TB/s; in 2-byte loads 61, the
+// splits as clusters' blocks 80, which left SMs idle), 4095 x 14336 stored N x K 51; with the copies 133 and 135;
+// 8192 x 28671 160 and 146, 480.  Bound by the loads under way for one token, and by instructions from two on (two 63 and
+// 57, four 77 and 88).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -95,9 +96,10 @@ __device__ __forceinline__ void finish(const GatedRows& p, int m, int64_t n, flo
   if (p.up) p.up[m * p.ldup + n] = __float2half_rn(u);
 }
 
-// Weights stored L x N.  A block has kColumns columns of H; the blocks along y share the rows, p.span each, and a block's warps take kTurn of them in turn.  A lane's two words of a row are columns
-// n0 - odd + 2 lane and 64 further: an odd row's lack the last column of 128 and an even one's have none before
-// n0, so a block's columns are 126.  The sums of even and odd turns stay apart until the end.
+// Weights stored L x N.  A block has kColumns columns of H; the blocks along y share the rows, p.span each, and a
+// block's warps take kTurn of them in turn.  A lane's two words of a row are columns n0 - odd + 2 lane and 64 further:
+// an odd row's lack the last column of 128 and an even one's have none before n0, so a block's columns are 126.  The
+// sums of even and odd turns stay apart until the end.
 constexpr int kColumns = 126, kTurn = 8, kChunk = 1024, kSlots = 130;
 template <int MM, bool DUAL>
 __global__ void __launch_bounds__(kWarps * 32, MM > 2 ? 2 : 3) tg_gated_columns_kernel(const GatedRows p) {
