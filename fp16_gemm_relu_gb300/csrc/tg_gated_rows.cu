@@ -99,7 +99,7 @@ __device__ __forceinline__ void finish(const GatedRows& p, int m, int64_t n, flo
 // Weights stored L x N.  A block has kColumns columns of H; the blocks along y share the rows, p.span each, and a
 // block's warps take kTurn of them in turn.  A lane's two words of a row are columns n0 - odd + 2 lane and 64 further:
 // an odd row's lack the last column of 128 and an even one's have none before n0, so a block's columns are 126.  The
-// sums of even and odd turns stay apart until the end.
+// sums of even and odd rows stay apart until the end.
 constexpr int kColumns = 126, kTurn = 8, kChunk = 1024, kSlots = 130;
 template <int MM, bool DUAL>
 __global__ void __launch_bounds__(kWarps * 32, MM > 2 ? 2 : 3) tg_gated_columns_kernel(const GatedRows p) {
