@@ -203,8 +203,8 @@ def linear_distillation(x: torch.Tensor, weight: torch.Tensor, teacher_index: to
 
 class GatedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, activation, trans_w):
-        if not any(ctx.needs_input_grad):
+    def forward(ctx, x, w_gate, w_up, activation, trans_w, keep):
+        if not keep or not any(ctx.needs_input_grad):
             return gated.gated_linear(x, w_gate, w_up, activation, trans_w)
         h, gate, up = gated.gated_linear(x, w_gate, w_up, activation, trans_w, keep=True)
         ctx.save_for_backward(x, w_gate, w_up, gate, up)
@@ -219,16 +219,15 @@ class GatedLinear(torch.autograd.Function):
         dx, dwg, dwu = gated.gated_linear_backward(
             dh.to(torch.float16).contiguous(), x, w_gate, w_up, gate, up, *ctx.args,
             input_grad=want[0], weight_grads=want[1] or want[2])
-        return dx, dwg if want[1] else None, dwu if want[2] else None, None, None
+        return dx, dwg if want[1] else None, dwu if want[2] else None, None, None, None
 
 
 def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
                  activation: int = TG_ACT_SILU, trans_w: bool = False) -> torch.Tensor:
     """Differentiable act(x @ w_gate) * (x @ w_up) (see gated.gated_linear); keeps both pre-activations
     in fp16 for the backward pass, and neither where gradients are off."""
-    if not torch.is_grad_enabled():  # (a Function's forward pass sees the inputs' requires_grad alone)
-        return gated.gated_linear(x, w_gate, w_up, activation, trans_w)
-    return GatedLinear.apply(x, w_gate, w_up, activation, trans_w)
+    # (a Function's forward pass sees the inputs' requires_grad alone)
+    return GatedLinear.apply(x, w_gate, w_up, activation, trans_w, torch.is_grad_enabled())
 
 
 def _constant(**tensors):
