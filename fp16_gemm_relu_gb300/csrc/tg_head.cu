@@ -1010,7 +1010,7 @@ tg_status run_objective(const Head& h, cudaStream_t stream) {
   const int64_t at_nll = lay.add(own_nll ? h.T * 4 : 0);
   const int64_t at_small = lay.add(grad ? 4 : 0), at_w = lay.add(grad ? h.T * 4 : 0);
   uint8_t* mem = nullptr;
-  if ((own_nll || grad) &&
+  if (lay.bytes > 0 &&  // (none without rows and a gradient)
       (st = tg::scratch_alloc(size_t(lay.bytes), stream, reinterpret_cast<void**>(&mem))) != TG_OK)
     return st;
   float* nll = own_nll ? reinterpret_cast<float*>(mem + at_nll) : ob.logp;
