@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(256)
       logp = -nll[r];
       const float ratio = expf(logp - ob.old[r]), adv = ob.advantage[r];
       const float kept = ratio < ob.low ? ob.low : ratio > ob.high ? ob.high : ratio;
-      const float a = ratio * adv, b = kept * adv;
+      // (a ratio beyond float32's range times an advantage of 0 is 0; a NaN stays one)
+      const float a = adv == 0.0f && ratio == INFINITY ? 0.0f : ratio * adv, b = kept * adv;
       const bool clipped = a > b;
       loss = clipped ? -b : -a;
       slope = clipped ? 0.0f : -a;

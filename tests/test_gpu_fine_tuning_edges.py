@@ -47,3 +47,27 @@ def test_no_rows_without_a_gradient(captured):
     loss, _ = autograd.linear_preference(x.clone().requires_grad_(True), w, target, offsets)
     assert abs(float(loss.detach()) - math.log(2)) < 1e-6
     loss.backward()
+
+
+@pytest.mark.parametrize("piece_rows", [0, 2])
+def test_a_ratio_beyond_float32_without_an_advantage(piece_rows):
+    """r A is 0 for an advantage of 0, however large r is; a log probability that is NaN stays one."""
+    x, w = normal(5, 64, seed=2), normal(40, 64, seed=3)
+    target = torch.zeros(5, dtype=torch.int64, device="cuda")
+    old = torch.tensor([-200.0, -math.inf, -200.0, math.nan, -3.0], device="cuda")
+    advantage = torch.tensor([0.0, -0.0, 1.0, 0.0, 0.0], device="cuda")
+    one = torch.ones(5, device="cuda")
+    for kl in (0.0, 0.5):
+        args = dict(reference=torch.zeros(5, device="cuda"), kl_weight=kl)
+        value = tg.linear_policy(x, w, target, old, advantage, piece_rows=piece_rows, **args)
+        loss, logp, dx, dw = tg.linear_policy_step(x, w, target, old, advantage, one, piece_rows=piece_rows, **args)
+        d = -logp
+        want = kl * (torch.expm1(d) - d)
+        want[2] -= 1.2  # clipped: no gradient of its own
+        good = torch.tensor([0, 1, 2, 4], device="cuda")
+        for got in (loss, value[0]):
+            assert got[3].isnan() and torch.allclose(got[good], want[good], rtol=1e-5, atol=1e-6)
+        # (the penalty's slope is 0.5 (1 - e^d) with d up to 30 here, far beyond fp16: infinite, not NaN)
+        assert dx[3].isnan().all() and not dx[good].isnan().any() and dw.isnan().any()
+        if kl == 0:
+            assert (dx[good] == 0).all()
