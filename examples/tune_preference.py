@@ -42,6 +42,13 @@ def features(x, w):
     return autograd.layer_norm(x + Project.apply(h, w["down"]), w["gamma"], w["beta"])
 
 
+def log_probabilities(x, w, target):
+    """The targets' log probabilities as the preference loss has them, without a gradient."""
+    with torch.no_grad():
+        zero = torch.zeros(target.shape, device=target.device)  # (a policy's loss is not wanted)
+        return tg.linear_policy(features(x, w), w["head"], target, zero, zero)[1]
+
+
 def run(steps: int = 30, pairs: int = 16, length: int = 64, width: int = 512, hidden: int = 1024,
         vocab: int = 8000, beta: float = 0.1, rate: float = 0.5, max_norm: float = 1.0,
         quiet: bool = False) -> list[tuple[float, float]]:
@@ -61,8 +68,7 @@ def run(steps: int = 30, pairs: int = 16, length: int = 64, width: int = 512, hi
     offsets = torch.arange(2 * pairs + 1, device="cuda") * length
     loss_scale = 4096.0
     w = {k: v.half().requires_grad_(True) for k, v in master.items()}
-    with torch.no_grad():  # the reference's log probabilities, once
-        reference = -tg.linear_cross_entropy(features(x, w), w["head"], target)
+    reference = log_probabilities(x, w, target)  # once
     seen = []
     for i in range(steps):
         loss, ratios = autograd.linear_preference(features(x, w), w["head"], target, offsets, reference,

@@ -219,8 +219,10 @@ def linear_preference(x, weight, target, offsets, reference=None, beta: float = 
     ``offsets`` is int64 (2 * pairs + 1,): the chosen sequence of pair p is the rows offsets[2p] to
     offsets[2p + 1], the rejected one those from there to offsets[2p + 2]; offsets that decrease or leave
     the rows make the pair's results NaN.  Rows whose target is ``ignore_index`` (a prompt's) do not
-    count.  ``reference`` is float32 (T,), as minus :func:`linear_cross_entropy` of the model that is
-    compared with, or None for 0; ``average`` takes means for the sums.
+    count.  ``reference`` is float32 (T,): the ``logp`` that :func:`linear_policy` gives for the model that
+    is compared with (its ``old`` and ``advantage`` may be zeros), or None for 0.  Minus
+    :func:`linear_cross_entropy` will not do: its logits are summed less exactly, which adds about 4e-6 a
+    token to every ratio.  ``average`` takes means for the sums.
     """
     return _preference(x, weight, target, offsets, None, False, False, reference, beta, label_smoothing,
                        average, ignore_index, logit_scale, layout, piece_rows, stream)[:2]
@@ -275,8 +277,9 @@ def linear_policy(x, weight, target, old, advantage, reference=None, clip_low: f
 
         loss = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl_weight (exp(d) - d - 1)
 
-    ``old``, ``advantage`` (A) and ``reference`` (needed where kl_weight is not 0) are float32 (T,).
-    Rows whose target is ``ignore_index`` have loss and logp 0.
+    ``old``, ``advantage`` (A) and ``reference`` (needed where kl_weight is not 0) are float32 (T,); ``old``
+    and ``reference`` are the ``logp`` that this function gives for those models (see
+    :func:`linear_preference`).  Rows whose target is ``ignore_index`` have loss and logp 0.
     """
     return _policy(x, weight, target, old, advantage, None, False, False, reference, clip_low, clip_high,
                    kl_weight, ignore_index, logit_scale, layout, piece_rows, stream)[:2]

@@ -481,8 +481,9 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
  * offsets: int64[2 pairs + 1]: the chosen sequence of pair p is the rows [offsets[2p], offsets[2p + 1]), the
  * rejected one the rows from there to offsets[2p + 2].  Rows outside of all of them get no gradient.  A pair
  * whose offsets decrease or leave [0, T] has a loss of NaN and makes the gradients NaN; nothing outside of
- * the arrays is read.  reference: float32[T], the log probabilities of the model that is compared with, or
- * NULL for 0.  loss: float32[pairs]; ratios: float32[pairs][2], chosen first; dloss: float32[pairs]; loss and ratios may be NULL.
+ * the arrays is read.  reference: float32[T], the log probabilities of the model that is compared with as
+ * tg_linear_policy_f16's logp has them, or NULL for 0 (minus tg_linear_cross_entropy_f16's loss differs from them
+ * by about 4e-6 a token, always to the same side, which a sequence adds up).  loss: float32[pairs]; ratios: float32[pairs][2], chosen first; dloss: float32[pairs]; loss and ratios may be NULL.
  * beta > 0, 0 <= label_smoothing < 1.  The ratios' sums are float64.  dX, dW, targets, scratch, accuracy and
  * options as tg_linear_cross_entropy_f16; where the tokens' logits do not fit into one piece, the logits
  * are computed twice, the first time without being kept.
@@ -501,8 +502,9 @@ tg_status tg_linear_preference_f16(const void* X, const void* W, const int64_t* 
  *     r = exp(logp - old_logp),   d = reference - logp
  *     loss = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_weight (exp(d) - d - 1)
  * with the row's advantage A.  old_logp, advantage, reference (NULL only with kl_weight == 0), loss, logp
- * and dloss: float32[T]; loss and logp may be NULL.  Rows at ignore_index have loss and logp 0 and no
- * gradient.  0 <= clip_low <= 1, clip_high >= 0, kl_weight >= 0.  Where both terms of the minimum are the
+ * and dloss: float32[T]; loss and logp may be NULL; old_logp and reference are this function's logp of those
+ * models.  Rows at ignore_index have loss and logp 0 and no gradient.
+ * 0 <= clip_low <= 1, clip_high >= 0, kl_weight >= 0.  Where both terms of the minimum are the
  * same the gradient is the first one's.  Everything else as tg_linear_preference_f16.
  */
 tg_status tg_linear_policy_f16(const void* X, const void* W, const int64_t* target,

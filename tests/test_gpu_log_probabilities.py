@@ -30,6 +30,54 @@ def example():
     return mod
 
 
+@pytest.mark.parametrize("T,V,D,layout", [
+    (2048, 8192, 2048, tg.TG_HEAD_VOCAB_MAJOR), (1000, 7033, 1596, tg.TG_HEAD_VOCAB_MAJOR),
+    (1024, 2501, 1024, tg.TG_HEAD_WIDTH_MAJOR), (48, 30666, 768, tg.TG_HEAD_VOCAB_MAJOR)])
+def test_an_unmoved_model_has_no_margin(T, V, D, layout):
+    """Against its own log probabilities a model's ratios are 0 but for the roundings of a token's: of a logit below 8
+    and of the sum's logarithm below 16, 2^-22 + 2^-21 < 2^-20 at worst, which do not lean; n 2^-21 allows for half of
+    them to point in one direction.  (Minus linear_cross_entropy as the reference: 3.5e-6 to 4.6e-6, 7 to 10 times
+    that, a token at these sizes.)"""
+    g = gen(1)
+    x = torch.randn(T, D, generator=g, device="cuda").half()
+    w = (torch.randn(V, D, generator=g, device="cuda") * (2 / math.sqrt(D))).half()
+    if layout == tg.TG_HEAD_WIDTH_MAJOR:
+        w = w.t().contiguous()
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    target[::7] = -100
+    zero = torch.zeros(T, device="cuda")
+    reference = tg.linear_policy(x, w, target, zero, zero, layout=layout)[1]
+    assert (reference[::7] == 0).all()
+    offsets = torch.tensor([0, T // 8, T], device="cuda")
+    count = torch.tensor([int((target[:T // 8] >= 0).sum()), int((target[T // 8:] >= 0).sum())], device="cuda")
+    one = torch.ones(1, device="cuda")
+    for _, ratios, *_ in (tg.linear_preference(x, w, target, offsets, reference, layout=layout),
+                          tg.linear_preference_step(x, w, target, offsets, one, reference, layout=layout),
+                          tg.linear_preference_step(x, w, target, offsets, one, reference, layout=layout,
+                                                    piece_rows=T // 3)):
+        assert (ratios[0].abs() <= count * 2 ** -21).all(), ratios
+
+
+def test_the_examples_reference():
+    """tune_preference.py's reference is its own model's log probabilities: no margin before the first step, for
+    answers of any lengths."""
+    mod = example()
+    T, D, V = 1024, 1024, 4000
+    g = gen(2)
+
+    def normal(*shape, size):
+        return (torch.randn(*shape, generator=g, device="cuda") * size).half()
+
+    w = {"gate": normal(D, D, size=D ** -0.5), "up": normal(D, D, size=D ** -0.5), "down": normal(D, D, size=D ** -0.5),
+         "gamma": normal(D, size=0.1) + 1, "beta": normal(D, size=0.1), "head": normal(V, D, size=2 * D ** -0.5)}
+    x = normal(T, D, size=1.0)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    reference = mod.log_probabilities(x, w, target)
+    offsets = torch.tensor([0, 24, T], device="cuda")
+    ratios = tg.linear_preference(mod.features(x, w), w["head"], target, offsets, reference)[1][0]
+    assert (ratios.abs() <= torch.tensor([24, T - 24], device="cuda") * 2 ** -21).all(), ratios
+
+
 def rows_of(kind, T, V, D):
     g = gen(3)
 
