@@ -279,7 +279,8 @@ def linear_policy(x, weight, target, old, advantage, reference=None, clip_low: f
 
     ``old``, ``advantage`` (A) and ``reference`` (needed where kl_weight is not 0) are float32 (T,); ``old``
     and ``reference`` are the ``logp`` that this function gives for those models (see
-    :func:`linear_preference`).  Rows whose target is ``ignore_index`` have loss and logp 0.
+    :func:`linear_preference`).  ``clip_high`` is finite: one that no ratio reaches, as 1e30, clips from below
+    alone.  Rows whose target is ``ignore_index`` have loss and logp 0.
     """
     return _policy(x, weight, target, old, advantage, None, False, False, reference, clip_low, clip_high,
                    kl_weight, ignore_index, logit_scale, layout, piece_rows, stream)[:2]

@@ -503,8 +503,8 @@ tg_status tg_linear_preference_f16(const void* X, const void* W, const int64_t* 
  *     loss = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_weight (exp(d) - d - 1)
  * with the row's advantage A.  old_logp, advantage, reference (NULL only with kl_weight == 0), loss, logp
  * and dloss: float32[T]; loss and logp may be NULL; old_logp and reference are this function's logp of those
- * models.  Rows at ignore_index have loss and logp 0 and no gradient.
- * 0 <= clip_low <= 1, clip_high >= 0, kl_weight >= 0.  Where both terms of the minimum are the
+ * models.  Rows at ignore_index have loss and logp 0 and no gradient; r A is 0 where A is, however large r.
+ * 0 <= clip_low <= 1, clip_high >= 0 and at most 3e38, kl_weight >= 0.  Where both terms of the minimum are the
  * same the gradient is the first one's.  Everything else as tg_linear_preference_f16.
  */
 tg_status tg_linear_policy_f16(const void* X, const void* W, const int64_t* target,

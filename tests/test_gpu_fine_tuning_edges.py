@@ -71,3 +71,18 @@ def test_a_ratio_beyond_float32_without_an_advantage(piece_rows):
         assert dx[3].isnan().all() and not dx[good].isnan().any() and dw.isnan().any()
         if kl == 0:
             assert (dx[good] == 0).all()
+
+
+def test_a_policy_clipped_from_below_alone():
+    """A clip_high that no ratio reaches clips nothing."""
+    x, w = normal(6, 64, seed=4), normal(40, 64, seed=5)
+    target = torch.arange(6, device="cuda")
+    zero = torch.zeros(6, device="cuda")
+    logp = tg.linear_policy(x, w, target, zero, zero)[1]
+    advantage = torch.tensor([1.0, 1.0, 1.0, -1.0, -1.0, -1.0], device="cuda")
+    moved = torch.tensor([4.0, 0.0, -4.0] * 2, device="cuda")
+    ratio = torch.exp(moved)
+    loss, _ = tg.linear_policy(x, w, target, logp - moved, advantage, clip_high=1e30)
+    want = -torch.minimum(ratio * advantage, ratio.clamp_min(0.8) * advantage)
+    # old is rounded by up to 2^-20 (of values below 16), and e^m by 2^-20 of itself
+    assert ((loss - want).abs() <= 2 ** -18 * want.abs()).all()
