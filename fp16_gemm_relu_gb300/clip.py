@@ -76,6 +76,7 @@ def clip_gradients(grads, max_norm: float, loss_scale: float = 1.0, out=None, st
     ``grads`` itself.  A norm that is not finite clips nothing, so that what overflowed stays to be seen.
     """
     grads = list(grads)
+    out = None if out is None else list(out)
     dev = _device(grads)
     if not here(dev, stream):
         with on(grads[0].device, stream, *grads, *(out or ())):
@@ -89,7 +90,6 @@ def clip_gradients(grads, max_norm: float, loss_scale: float = 1.0, out=None, st
             out.append(o)
             words += (g.data_ptr(), o.data_ptr(), g.numel(), kind | kind32)
     else:
-        out = list(out)
         if len(out) != len(grads):
             raise ValueError("out must have a tensor for each gradient")
         for i, (g, o) in enumerate(zip(grads, out)):

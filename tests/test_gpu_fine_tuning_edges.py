@@ -86,3 +86,17 @@ def test_a_policy_clipped_from_below_alone():
     want = -torch.minimum(ratio * advantage, ratio.clamp_min(0.8) * advantage)
     # old is rounded by up to 2^-20 (of values below 16), and e^m by 2^-20 of itself
     assert ((loss - want).abs() <= 2 ** -18 * want.abs()).all()
+
+
+@pytest.mark.parametrize("stream", [False, True])
+def test_clip_takes_any_iterable(stream):
+    grads = [normal(33, 5, seed=6), normal(7, seed=7).float()]
+    want = tg.clip_gradients(grads, 0.5)
+    torch.cuda.synchronize()
+    out = [torch.empty_like(g, dtype=torch.float32) for g in grads]
+    s = torch.cuda.Stream() if stream else None
+    norm, got = tg.clip_gradients(iter(grads), 0.5, out=iter(out), stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(norm, want[0]) and all(a is b for a, b in zip(got, out))
+    assert all(torch.equal(a, b) for a, b in zip(got, want[1]))
+    assert torch.equal(tg.gradient_norm(iter(grads), stream=s), norm)
