@@ -26,6 +26,13 @@ def _dense(t, name):
         n *= size
 
 
+def _alike(a, b):
+    """Whether two tensors of one shape have their values in the same order in memory: their strides say so but
+    for those of dimensions of one element."""
+    return a.stride() == b.stride() or (
+        a.numel() == 0 or all(s == t for s, t, d in zip(a.stride(), b.stride(), a.shape) if d != 1))
+
+
 def _call(words, n, loss_scale, max_norm, device, dev):
     norm = torch.empty((), dtype=torch.float32, device=device)
     table = array.array("Q", words)  # tg_gradient, four words each
@@ -72,7 +79,7 @@ def clip_gradients(grads, max_norm: float, loss_scale: float = 1.0, out=None, st
     min(1, max_norm / norm) / loss_scale.
 
     ``grads`` are fp16 or float32 CUDA tensors of any shapes without gaps in memory.  ``out`` (default: new
-    float32 tensors) is a list of fp16 or float32 tensors with their shapes and strides; it may be
+    float32 tensors) holds fp16 or float32 tensors with their shapes and orders in memory; it may be
     ``grads`` itself.  A norm that is not finite clips nothing, so that what overflowed stays to be seen.
     """
     grads = list(grads)
@@ -94,8 +101,8 @@ def clip_gradients(grads, max_norm: float, loss_scale: float = 1.0, out=None, st
             raise ValueError("out must have a tensor for each gradient")
         for i, (g, o) in enumerate(zip(grads, out)):
             kind = _kind(g, dev, i)
-            if o.shape != g.shape or o.stride() != g.stride() or o.get_device() != dev:
-                raise ValueError(f"out[{i}] must have the shape, strides and device of grads[{i}]")
+            if o.shape != g.shape or o.get_device() != dev or not _alike(o, g):
+                raise ValueError(f"out[{i}] must have the shape, order in memory and device of grads[{i}]")
             words += (g.data_ptr(), o.data_ptr(), g.numel(), kind | param_type(o, f"out[{i}]") << 32)
         for o in out:
             written(o)

@@ -100,3 +100,14 @@ def test_clip_takes_any_iterable(stream):
     assert torch.equal(norm, want[0]) and all(a is b for a, b in zip(got, out))
     assert all(torch.equal(a, b) for a, b in zip(got, want[1]))
     assert torch.equal(tg.gradient_norm(iter(grads), stream=s), norm)
+
+
+def test_clip_into_the_same_memory_order_under_other_strides():
+    """The stride of a dimension of one element says nothing about where values lie."""
+    g = normal(6, 5, 1, 1, seed=8)
+    out = torch.empty(6, 5, 1, 1, device="cuda").as_strided((6, 5, 1, 1), (5, 1, 5, 5))
+    assert g.stride() != out.stride()
+    norm, (got,) = tg.clip_gradients([g], 1.0, out=[out])
+    assert got is out and torch.equal(out, tg.clip_gradients([g], 1.0)[1][0])
+    with pytest.raises(ValueError):  # another order
+        tg.clip_gradients([normal(6, 5, seed=9)], 1.0, out=[torch.empty(5, 6, device="cuda").t()])
