@@ -530,7 +530,9 @@ typedef struct {
  * norm: device float32.  list: host memory, read before the call returns; with every `out` NULL only the norm
  * is computed, else every gradient with count > 0 has one.  Outputs do not overlap each other, nor any
  * gradient but the one they replace (TG_ERR_INVALID_ARG).  loss_scale > 0, max_norm >= 0 (infinity: no
- * clipping).  Squares are float32: a gradient beyond 1.8e19 counts as infinite, below 1e-23 as 0.
+ * clipping).  Squares and a thread block's sums of them are float32: where all of them add up to more than 3.4e38
+ * (a sum's root of 1.8e19: one value, or 2^26 of 2.3e15) the norm may come out infinite, and then nothing is
+ * clipped; a value below 1e-23 counts as 0.
  */
 tg_status tg_clip_gradients(const tg_gradient* list, int64_t n, float loss_scale, float max_norm,
                             float* norm, tg_stream_t stream);

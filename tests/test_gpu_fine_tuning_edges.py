@@ -111,3 +111,19 @@ def test_clip_into_the_same_memory_order_under_other_strides():
     assert got is out and torch.equal(out, tg.clip_gradients([g], 1.0)[1][0])
     with pytest.raises(ValueError):  # another order
         tg.clip_gradients([normal(6, 5, seed=9)], 1.0, out=[torch.empty(5, 6, device="cuda").t()])
+
+
+def test_norms_up_to_the_range_of_their_squares():
+    """Squares that add up to less than float32's largest value have a finite norm, whichever tensors and blocks they
+    lie in; a value whose square is larger has an infinite one, and nothing is clipped."""
+    for n, value in ((8192, 1e17), (1 << 22, 8e15), (3, 5e18), (1 << 26, 2e15)):
+        grads = [torch.full((n,), value, device="cuda"), torch.full((5,), value, device="cuda")]
+        ref = math.sqrt(n + 5) * float(grads[0][0].double())
+        assert ref ** 2 < 3.4e38
+        norm, out = tg.clip_gradients(grads, ref / 4)
+        assert abs(float(norm) - ref) <= 2 ** -20 * ref
+        for g, o in zip(grads, out):
+            assert ((o - g / 4).abs() <= 2 ** -19 * g / 4).all()
+    grads = [torch.tensor([1.0, -1.9e19], device="cuda")]
+    norm, out = tg.clip_gradients(grads, 1.0, 2.0)
+    assert float(norm) == math.inf and torch.equal(out[0], grads[0] / 2)
