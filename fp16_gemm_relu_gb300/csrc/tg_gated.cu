@@ -42,9 +42,10 @@ constexpr int64_t kBesideWork = int64_t{4} << 20;
 constexpr int64_t kBesideTokens = 256;
 // Elements of each weight and token from which gradients are taken without copies of the weights.
 constexpr int64_t kStraightWork = int64_t{2} << 20;
-// Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: by
-// 1.2e-4 of itself over 65536 terms, half of what its rounding to fp16 may take, by 6e-5 at this length.
-// Longer sums are taken in splits that are added in float32.
+// Terms that one accumulator adds up.  The tensor core cuts off where it adds, so a long sum shrinks: terms of one
+// sign by 4.0e-4 of themselves over 65536 terms, nearly all that its rounding to fp16 may take (4.9e-4), and by 2.0e-4 at
+// this length; terms of either sign lose several times less.  Longer sums are taken in splits that are added in
+// float32.
 constexpr int64_t kSumLength = 32768;
 
 // H (and gate, up) from the K splits' float32 partial sums, added in order; four columns a thread and the
