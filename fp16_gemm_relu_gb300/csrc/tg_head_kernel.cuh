@@ -15,12 +15,17 @@
 //    PRECISE, for losses of differences of log probabilities, where what every token's log probability is
 //    off in one direction adds up over a sequence: segments of 768 columns, and what the cutting off takes from a
 //    segment's sum v on average is put back as it is added.  Each of n instructions cuts half a unit of the partial
-//    sum's last place.  Of sums that are large beside their row's, whose partial sums go there straight, that is up to
+//    sum's last place (16 products of one sign: up to 2.5 units).  Of sums that are large beside their row's, whose partial sums go there straight, that is up to
 //    0.3 n 2^-24, of others 0.27 n, whose partial sums stay below v or change sign; measured over normal logits of
 //    spread 1 to 4, n = 5 to 48, it is (0.266 n + 0.38 + n min(0.0036 (v / s)^2, 0.035)) 2^-24 of v within 1% of n, s being the
 //    row's root mean square (of a warp's first 32 columns).  An instruction past the last column cuts nothing.
 //    A log probability is then off by less than 5e-8 on average (30666 classes of 768 1e-8; with 0.276 n for all 1.4e-7, with
-//    nothing put back in segments of 1024 4.4e-6), root mean square 1.1e-6 (2.6e-6 in segments of 1024).
+//    nothing put back in segments of 1024 4.4e-6), root mean square 1.1e-6 (2.6e-6 in segments of 1024).  That is for
+//    entries of about one size and logits up to 8: normal, uniform, one-sided and quantised ones within 1e-7, targets whose
+//    weights point along x within 3e-7; logits up to 25 lean by 0.2 to 1.5e-6 (with nothing put back 14 to 26e-6).  What is
+//    put back depends on n and v alone, so it is wrong where the cut is another: with eight columns 30 times the others it
+//    takes the lean from 18 to 38e-6 down to 5 to 17e-6, with 5% of x not zero from 1.8e-6 to -1.9e-6, and sums of which nothing is cut (one-hot rows, small integers) come
+//    out up to (0.301 n + 0.38) 2^-24, 8.9e-7, of themselves too large.
 //    4096 tokens, 65537 classes of 2048: the whole step 2280 us, 2230 with 0.276 n for all; segments of 512 would cost 35 more.
 //  - The running sums take 128 registers a thread, so there are eight epilogue warps, each with 32
 //    rows and half of the tile's columns.  With the whole row segment in registers they take its

@@ -98,6 +98,27 @@ def rows_of(kind, T, V, D):
     return integers(T, D, lo=-2, hi=2), integers(V, D, lo=-1, hi=1) / 4
 
 
+@pytest.mark.parametrize("kind", ["one entry", "one entry a segment", "few entries", "small integers"])
+@pytest.mark.parametrize("T,V,D", [(3, 900, 768), (200, 1000, 1536), (600, 2049, 2000)])
+def test_exact_sums(kind, T, V, D):
+    """Sums of which nothing is cut off."""
+    x, w = rows_of(kind, T, V, D)
+    target = torch.randint(0, V, (T,), generator=gen(4), device="cuda")
+    zero = torch.zeros(T, device="cuda")
+    z = x.to(D64) @ w.to(D64).t()
+    segments = sum((x[:, a:a + 768].to(D64) @ w[:, a:a + 768].to(D64).t()).abs() for a in range(0, D, 768))
+    dz = (PUT_BACK + math.ceil(D / 768) * 2 ** -24) * segments
+    at = target[:, None]
+    lse, zt = torch.logsumexp(z, 1), z.gather(1, at)[:, 0]
+    # the softmax's sum moves by at most the largest logit's error; scaling by log2(e) and back, exp2f, log2f, the sum
+    # over the row's parts (2^-21 of it) and the subtraction
+    tol = dz.gather(1, at)[:, 0] + dz.amax(1) + 2 ** -21 * (lse.abs() + zt.abs() + 1)
+    want = zt - lse
+    for got in (tg.linear_policy(x, w, target, zero, zero)[1],
+                tg.linear_policy_step(x, w, target, zero, zero, zero)[1]):
+        assert ((got.to(D64) - want).abs() <= tol).all(), float(((got.to(D64) - want).abs() / tol).max())
+
+
 @pytest.mark.parametrize("T", [3, 200])
 @pytest.mark.parametrize("V,D", [(1, 64), (1, 2000), (500, 64), (3000, 1536)])
 def test_certain_targets(T, V, D):
