@@ -437,8 +437,10 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
   if (M <= 128 && choose) {
     plan = few_rows_plan(a, sms);
   } else if (choose && !plan.pair && plan.block_n == 128 && cdiv(M, 256) * cdiv(N, 128) >= sms / 2) {
-    // a last wave that narrow tiles fill better is no gain where they read X four times as often: 256 x 4096 x 14336
-    // 65 us, on pairs 58, 160 x 4096 x 11008 63 and 55; below a wave of pairs the planner stands
+    // a last wave that narrow tiles fill better is no gain where they read X four times as often: from 136 to 1024
+    // tokens of six weights (2048 x 8192 to 8192 x 28672) they took 1.08 to 1.7 times as long as pairs (256 x 4096 x
+    // 14336 61 us, on pairs 57, 320 of it 95 and 75, 160 x 4096 x 11008 60 and 54, 640 x 2048 x 8192 52 and 39); below a
+    // wave of pairs the planner stands
     tg_options o;
     std::memset(&o, 0, sizeof(o));
     if (opt) o = *opt;
