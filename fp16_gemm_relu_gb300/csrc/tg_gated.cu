@@ -311,7 +311,7 @@ void common_params(tg::GemmParams* p, const tg_options* opt, unsigned* err) {
 // splits the sum, or an option asks for what this launch has not; nothing is launched.
 tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int64_t np, void* dWg,
                        int64_t lddwg, void* dWu, int64_t lddwu, const tg_options* opt, unsigned* err,
-                       bool beside, cudaStream_t stream, tg::GemmLaunch* out, int* block_n) {
+                       bool beside, int sms, cudaStream_t stream, tg::GemmLaunch* out, int* block_n) {
   const int64_t rows = a.trans ? a.N : a.K, cols = a.trans ? a.K : a.N;  // of each output
   tg::TilePlan plan;
   tg_options o;
@@ -321,7 +321,7 @@ tg_status weight_grads(const Gated& a, const Operands& ops, const __half* g, int
   // each (4096 x 14336 from 64 tokens 49 against 65 us, 54 in tiles of 128 columns; from 256 tokens 86 against 79).
   if ((a.M <= 128 || beside) && !o.pair) {
     o.pair = -1;
-    if (!o.block_n && (beside || cdiv(rows, 128) * cdiv(cols, 256) >= 76)) o.block_n = 256;
+    if (!o.block_n && (beside || cdiv(rows, 128) * cdiv(cols, 256) >= sms / 2)) o.block_n = 256;
   }
   tg_status st = tg::plan_tiles(a.trans ? 2 * rows : rows, a.trans ? cols : 2 * cols, a.M, kSumLength, true,
                                 &o, &plan);
@@ -654,7 +654,7 @@ tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, c
   if (!one_by_one) {
     tg::GemmLaunch w;
     int block_n = 0;
-    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, beside > 0, stream, &w, &block_n);
+    st = weight_grads(a, ops, g, np, dWg, lddwg, dWu, lddwu, opt, err, beside > 0, sms, stream, &w, &block_n);
     if (st != TG_OK && st != TG_ERR_NO_WORKSPACE) return done(st);
     one_by_one = st == TG_ERR_NO_WORKSPACE;
     if (beside && !one_by_one && block_n == 256) {
