@@ -19,7 +19,7 @@
 // One token of 4096 x 14333: K x N 48 us with the splits' sums joined (the kernel 44, 5.3 TB/s; in 2-byte loads 61, the
 // splits as clusters' blocks 80, which left SMs idle), 4095 x 14336 stored N x K 51; with the copies 133 and 135;
 // 8192 x 28671 160 and 146, 480.  Bound by the loads under way for one token, and by instructions from two on (two 63 and
-// 57, four 77 and 88).
+// 57, with 160 bytes a thread spilled: 80 registers for three blocks an SM; four 77 and 88).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -462,7 +462,8 @@ tg_status tg_gated_f16(const void* X, const void* Wg, const void* Wu, void* H, v
  * under a loss scale.  The derivative of relu at 0 is 0.
  * Scratch: dG and dU, copies of operands that are not 16-byte aligned with leading dimensions that are multiples
  * of 8 (for up to four rows of X such weights are read where they are if each has 2^21 elements or more for each
- * row) and of an X of fewer than eight rows, and float32 sums where a sum is taken in splits (dX of few tokens; sums of more than 32768 terms).
+ * row) and of an X of fewer than eight rows, and float32 sums where a sum is taken in splits (dX of few tokens; sums
+ * of more than 32768 terms).
  */
 tg_status tg_gated_backward_f16(const void* dH, const void* X, const void* Wg, const void* Wu,
                                 const void* gate, const void* up, void* dX, void* dWg, void* dWu,
