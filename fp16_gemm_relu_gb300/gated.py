@@ -47,7 +47,7 @@ def gated_linear(x, w_gate, w_up, activation: int = TG_ACT_SILU, trans_w: bool =
     """h = act(x @ w_gate) * (x @ w_up), or with ``keep`` (h, gate, up) as
     :func:`gated_linear_backward` takes them.
 
-    ``out`` may be a row-major (M, N) view for h; autograd sees that it was written.  ``options`` may
+    ``out`` may be a row-major (M, N) view for h that overlaps no input; autograd sees that it was written.  ``options`` may
     hold plan overrides by name (block_n, split_k, pair, panel_m, max_ctas, timeout_ms).
     """
     M, N, K, ldx, ldg, ldu = _sizes(x, w_gate, w_up, trans_w)
